@@ -239,7 +239,7 @@ def prepare(case, seed):
     if own:  # the handle of the cache and the scratch memory, kept from step to step
         from w4a16_int4_weight_gemv_gb300 import binding
         s["cache_handle"] = binding.PagedCache(k_cache, v_cache, k_scale, v_scale)
-        s["workspace"] = binding.paged_attention_workspace(s["cache_handle"], n, case["q_heads"])
+        s["workspace"] = binding.paged_attention_workspace(s["cache_handle"], case["q_heads"])
     return s
 
 
