@@ -84,6 +84,9 @@ typedef enum w4a16_out_dtype {
 #define W4A16_DEVERR_RANGE 0x4u     /* an activation outside the CUDA-core kernel's
                                        input range: |x| >= 2^43 or not finite
                                        (see w4a16_gemv) */
+#define W4A16_DEVERR_SLOT 0x8u      /* a block id or slot outside the paged cache */
+#define W4A16_DEVERR_BLOCKS 0x10u   /* w4a16_paged_map ran out of free blocks, table
+                                       columns or token places, or a length was negative */
 
 /* Version of this interface; bumped on any incompatible change. */
 W4A16_API int w4a16_abi_version(void);
@@ -458,6 +461,146 @@ W4A16_API w4a16_status w3a16_moe_gemv(const uint16_t* x, int x_per_slot,
                                       const uint32_t* wq3, const uint16_t* scale,
                                       const uint8_t* zero, uint16_t* y, int M, int topk, int E,
                                       int64_t N, int64_t K, int64_t g, void* stream);
+
+/*
+ * Paged key/value cache.  A decoder layer's keys and values live in blocks of
+ * `page` tokens; a request's tokens fill the blocks its row of the block
+ * table names, in order.  Slot s is place s % page of block s / page.  The
+ * calls below are what a decode step runs between the fused QKV projection
+ * (w4a16_gemv) and the output projection:
+ *   w4a16_paged_map        lengths -> block tables, slots, positions (once a step)
+ *   w4a16_rope_append      rotary positions on q and k, k and v into the cache
+ *   w4a16_paged_attention  one new token of every request over its cache
+ * (The README has no counterpart: it describes the weight products only.)
+ * Integer arrays need 4-byte alignment; q, k, v, the cache and the outputs
+ * 16-byte alignment of the pointers and of every row (strides multiples of 8
+ * bf16 elements, or of 16 e4m3 elements).
+ */
+typedef enum w4a16_cache_dtype {
+    W4A16_CACHE_BF16 = 0,
+    W4A16_CACHE_E4M3 = 1 /* 8-bit floats: 4 exponent and 3 fraction bits, largest 448 */
+} w4a16_cache_dtype;
+
+typedef struct w4a16_kv_cache {
+    void* k;              /* k and v: device, element (block, token, head, d) at */
+    void* v;              /*   block * *_block + token * *_token + head * *_head + d */
+    const float* k_scale; /* E4M3 only: fp32 [heads], key = code * k_scale[head]; else NULL */
+    const float* v_scale; /* the same for the values */
+    int32_t dtype;        /* w4a16_cache_dtype */
+    int32_t heads;        /* key/value heads */
+    int32_t dim;          /* values of a head: a multiple of 16, 16..256 */
+    int32_t page;         /* tokens of a block, 1..65536 */
+    int64_t blocks;       /* blocks * page < 2^31 */
+    int64_t k_block, k_token, k_head; /* strides in elements */
+    int64_t v_block, v_token, v_head;
+} w4a16_kv_cache;
+
+/*
+ * w4a16_paged_map -- block tables and slot maps from the lengths of B
+ * requests (1 <= B <= 16384), of which request b has ctx_len[b] tokens cached
+ * and adds new_len[b] (0 allowed).  With before_b = ceil(ctx_len[b] / page)
+ * and after_b = ceil((ctx_len[b] + new_len[b]) / page):
+ *   block_table[b][before_b .. after_b - 1] = the next free blocks, taken in
+ *       the order of the requests from free_blocks[*free_head] on; other
+ *       entries are left as they are;
+ *   new token t of all, request after request: positions[t] = its place in
+ *       the request (ctx_len[b], ctx_len[b] + 1, ...), slots[t] =
+ *       block_table[b][positions[t] / page] * page + positions[t] % page;
+ *       both are -1 from the last new token to tokens - 1;
+ *   row_start[b] = sum of new_len before b (B + 1 entries),
+ *   kv_len[b] = ctx_len[b] + new_len[b],
+ *   *free_head_out = *free_head + the blocks taken (at most n_free).
+ * block_table: int32, rows table_stride apart, `columns` entries each.
+ * The inputs and the outputs are different buffers, but for block_table
+ * (W4A16_ERR_UNSUPPORTED where kv_len is ctx_len or new_len, or
+ * free_head_out is free_head).
+ * Where something runs out the call goes on and sets W4A16_DEVERR_BLOCKS:
+ * without a free block the table entry and its tokens' slots are -1; tokens
+ * past columns * page get slot -1; tokens past `tokens` are not written; a
+ * negative length counts as 0.  A block id outside [0, num_blocks), in the
+ * table or in the free list, gives -1 and W4A16_DEVERR_SLOT.
+ */
+W4A16_API w4a16_status w4a16_paged_map(const int32_t* ctx_len, const int32_t* new_len, int B,
+                                       int32_t* block_table, int64_t table_stride, int columns,
+                                       const int32_t* free_blocks, int64_t n_free,
+                                       const int32_t* free_head, int page, int64_t num_blocks,
+                                       int32_t* slots, int32_t* positions, int64_t tokens,
+                                       int32_t* row_start, int32_t* kv_len,
+                                       int32_t* free_head_out, void* stream);
+
+/* Flags of w4a16_rope_append. */
+#define W4A16_ROPE_INTERLEAVED 0x1u /* pair i is (2i, 2i + 1), not (i, i + rotary / 2) */
+#define W4A16_ROPE_INVERSE 0x2u     /* turn by -angle: the rotation's inverse and its gradient */
+
+/*
+ * w4a16_rope_append -- rotary positions with several axes on the queries and
+ * keys of T tokens, and the write of keys and values into the paged cache, in
+ * one launch.  The first `rotary` values of a head are turned in pairs; pair
+ * i (0 <= i < rotary / 2) of token t by the angle
+ *     a = positions[axis(i)][t] * inv_freq[i],
+ *     y1 = x1 cos a - x2 sin a,  y2 = x2 cos a + x1 sin a;
+ * the rest of the head is copied.  axis(i): sections[0] pairs go by axis 0,
+ * the next sections[1] by axis 1, and so on (host array of `axes` <= 4
+ * entries, sum rotary / 2; NULL with one axis).  The angle is reduced in
+ * more than 32 bits, so large positions turn as exactly as small ones (cosine
+ * and sine to about 2^-21).
+ *   q: bf16, head h of token t at q + t * q_token + h * q_head; q_out the same
+ *      with its own strides (may be q itself); both NULL: no queries.
+ *   k, v: bf16 like q, cache->heads heads each; rotated k and plain v go to
+ *      slot slots[t] of the cache, rounded once: to bf16, or to e4m3 of
+ *      value / scale (beyond +-448: +-448).  slots[t] == -1: not stored; a
+ *      slot outside the cache: not stored and W4A16_DEVERR_SLOT.  Slots are
+ *      to be different from one another.  k, v, slots and cache NULL: no keys.
+ *   positions: int32, axis a at positions + a * axis_stride.
+ * dim: 16..256, a multiple of 16 (cache->dim where there is a cache); rotary:
+ * a multiple of 16, 0..dim.  T = 0 is allowed.
+ */
+W4A16_API w4a16_status w4a16_rope_append(const uint16_t* q, int64_t q_token, int64_t q_head,
+                                         uint16_t* q_out, int64_t q_out_token, int64_t q_out_head,
+                                         int q_heads, const uint16_t* k, int64_t k_token,
+                                         int64_t k_head, const uint16_t* v, int64_t v_token,
+                                         int64_t v_head, const int32_t* positions,
+                                         int64_t axis_stride, const float* inv_freq,
+                                         const int32_t* sections, int axes, int rotary, int dim,
+                                         unsigned flags, const int32_t* slots,
+                                         const w4a16_kv_cache* cache, int64_t T, void* stream);
+
+/*
+ * w4a16_paged_attention_workspace_bytes -- device workspace of
+ * w4a16_paged_attention for this head layout (it does not depend on the
+ * number of requests or on their lengths).
+ */
+W4A16_API size_t w4a16_paged_attention_workspace_bytes(int q_heads, int kv_heads, int dim);
+
+/*
+ * w4a16_paged_attention -- attention of one new token of each of B requests
+ * over its paged cache.  Query head h reads key/value head h / (q_heads /
+ * cache->heads).  For the tokens j that request b sees, max(0, kv_len[b] -
+ * window) <= j < kv_len[b] (window 0: all of them):
+ *     s_j = scale * q . k_j,   p = softmax(s),   out = sum_j p_j v_j,
+ *     lse = log sum_j exp(s_j)
+ * with fp32 scores, sums and outputs, rounded once to bf16 at the end.  A
+ * request without tokens gets out = 0 and lse = -infinity.
+ *   q, out: bf16, request b's head h at b * *_request + h * *_head; lse: fp32
+ *   [B][q_heads] or NULL.
+ *   block_table: int32, rows table_stride apart, `columns` entries; entries
+ *   past a request's length are not read, nor is anything in the cache that
+ *   no request sees.  A token whose block id is outside [0, cache->blocks) is
+ *   left out and W4A16_DEVERR_SLOT set, as for a length above columns * page
+ *   (a negative one counts as 0).
+ *   workspace: >= w4a16_paged_attention_workspace_bytes(...) bytes, 16-byte
+ *   aligned, zero before its first call; each call leaves it so.  Calls that
+ *   may overlap need one each.
+ * Limits: q_heads a multiple of cache->heads, B * q_heads < 2^24.
+ */
+W4A16_API w4a16_status w4a16_paged_attention(const uint16_t* q, int64_t q_request, int64_t q_head,
+                                             const w4a16_kv_cache* cache,
+                                             const int32_t* block_table, int64_t table_stride,
+                                             int columns, const int32_t* kv_len, int B,
+                                             int q_heads, float scale, int window, uint16_t* out,
+                                             int64_t out_request, int64_t out_head, float* lse,
+                                             void* workspace, size_t workspace_bytes,
+                                             void* stream);
 
 /*
  * w4a16_swiglu -- h[r][n] = bf16(silu(gate[r][n]) * up[r][n]), computed in

@@ -1,0 +1,141 @@
+"""The paged-cache entry points check their arguments before anything is
+launched (no GPU needed), and the plain forms the GPU tests compare with agree
+with hand-worked cases."""
+import ctypes
+
+import pytest
+import torch
+
+from . import paged_reference as ref
+
+P = ctypes.c_void_p
+A16, MIS, ODD = P(0x1000), P(0x1008), P(0x1002)  # never dereferenced: validation fails first
+
+
+@pytest.fixture(scope="module")
+def w():
+    from w4a16_int4_weight_gemv_gb300 import build_ext
+    build_ext.build()
+    from w4a16_int4_weight_gemv_gb300 import binding
+    return binding
+
+
+def cache(w, **kw):
+    d = dict(k=0x1000, v=0x1000, k_scale=None, v_scale=None, dtype=0, heads=8, dim=128, page=16, blocks=64, k_block=16 * 1024,
+             k_token=1024, k_head=128, v_block=16 * 1024, v_token=1024, v_head=128)
+    d.update(kw)
+    return ctypes.byref(w._KvCache(**d))
+
+
+def test_map_checks(w):
+    S = w.Status
+    def call(ctx=A16, new=P(0x2000), B=4, table=A16, stride=8, columns=8, free=A16, n_free=9, head=A16, page=16, blocks=64,
+             slots=A16, pos=A16, tokens=5, start=A16, kv=P(0x3000), head_out=P(0x4000)):
+        return w.load_library().w4a16_paged_map(ctx, new, B, table, stride, columns, free, n_free, head, page, blocks, slots, pos,
+                                                tokens, start, kv, head_out, None)
+    for bad in (dict(ctx=None), dict(new=None), dict(table=None), dict(head=None), dict(start=None), dict(kv=None), dict(head_out=None),
+                dict(free=None), dict(slots=None), dict(pos=None)):
+        assert call(**bad) == S.ERR_NULL, bad
+    for bad in (dict(B=0), dict(columns=0), dict(stride=7), dict(n_free=-1), dict(page=0), dict(blocks=0), dict(tokens=-1)):
+        assert call(**bad) == S.ERR_SHAPE, bad
+    for bad in (dict(B=16385), dict(page=65537), dict(blocks=1 << 27), dict(tokens=1 << 31), dict(n_free=1 << 31), dict(kv=A16),
+                dict(kv=P(0x2000)), dict(head_out=A16)):
+        assert call(**bad) == S.ERR_UNSUPPORTED, bad
+    for bad in (dict(ctx=ODD), dict(slots=ODD), dict(table=ODD), dict(head_out=ODD)):
+        assert call(**bad) == S.ERR_ALIGN, bad
+    if not torch.cuda.is_available():
+        assert call() == S.ERR_CUDA
+        assert call(free=None, n_free=0, slots=None, pos=None, tokens=0) == S.ERR_CUDA  # allowed: the device is the next check
+
+
+def test_rope_append_checks(w):
+    S = w.Status
+    def call(q=A16, qt=4096, qh=128, qo=A16, qot=4096, qoh=128, hq=32, k=A16, kt=1024, kh=128, v=A16, vt=1024, vh=128, pos=A16, ax=0,
+             f=A16, sec=None, axes=1, rotary=128, dim=128, flags=0, slots=A16, c=None, T=2):
+        c = cache(w) if c is None else c
+        return w.load_library().w4a16_rope_append(q, qt, qh, qo, qot, qoh, hq, k, kt, kh, v, vt, vh, pos, ax, f, sec, axes, rotary, dim,
+                                                  flags, slots, c if c != "none" else None, T, None)
+    sections = lambda *v: (ctypes.c_int32 * len(v))(*v)
+    for bad in (dict(q=None), dict(qo=None), dict(k=None), dict(v=None), dict(slots=None), dict(c="none"), dict(pos=None), dict(f=None),
+                dict(q=None, qo=None, k=None, v=None, slots=None, c="none"), dict(axes=2), dict(c=cache(w, k=None)),
+                dict(c=cache(w, dtype=1))):
+        assert call(**bad) == S.ERR_NULL, bad
+    for bad in (dict(T=-1), dict(axes=0, sec=sections(1)), dict(rotary=24), dict(rotary=-16), dict(rotary=144), dict(dim=120, rotary=64), dict(hq=0),
+                dict(sec=sections(63)), dict(sec=sections(65)), dict(axes=2, sec=sections(-1, 65)), dict(axes=2, sec=sections(32, 31)),
+                dict(c=cache(w, dim=64)), dict(c=cache(w, heads=0)), dict(c=cache(w, page=0)), dict(c=cache(w, dim=72))):
+        assert call(**bad) == S.ERR_SHAPE, bad
+    for bad in (dict(flags=4), dict(axes=5, sec=sections(64, 0, 0, 0, 0)), dict(dim=272, rotary=64), dict(c=cache(w, dtype=2)),
+                dict(c=cache(w, blocks=1 << 27)), dict(c=cache(w, dim=512))):
+        assert call(**bad) == S.ERR_UNSUPPORTED, bad
+    for bad in (dict(q=MIS), dict(qo=MIS), dict(k=MIS), dict(v=MIS), dict(qt=4100), dict(qoh=4), dict(vh=-128), dict(pos=ODD), dict(slots=ODD),
+                dict(c=cache(w, k=0x1008)), dict(c=cache(w, v_head=132)), dict(c=cache(w, dtype=1, k_scale=0x1000, v_scale=0x1000, k_token=1032))):
+        assert call(**bad) == S.ERR_ALIGN, bad
+    assert call(T=0) == S.OK
+    if not torch.cuda.is_available():
+        assert call() == S.ERR_CUDA
+        assert call(rotary=0, pos=None, f=None) == S.ERR_CUDA
+
+
+def test_attention_checks(w):
+    S, lib = w.Status, w.load_library()
+    need = lib.w4a16_paged_attention_workspace_bytes(32, 8, 128)
+    assert need > 0
+    for bad in ((0, 8, 128), (32, 0, 128), (30, 8, 128), (32, 8, 0), (32, 8, 72), (32, 8, 272)):
+        assert lib.w4a16_paged_attention_workspace_bytes(*bad) == 0
+    def call(q=A16, qr=4096, qh=128, c=None, table=A16, stride=8, columns=8, kv=A16, B=2, hq=32, scale=0.1, window=0, out=A16, outr=4096, outh=128,
+             lse=None, ws=A16, n=need):
+        return lib.w4a16_paged_attention(q, qr, qh, cache(w) if c is None else c if c != "none" else None, table, stride, columns, kv, B, hq, scale,
+                                         window, out, outr, outh, lse, ws, n, None)
+    for bad in (dict(q=None), dict(c="none"), dict(table=None), dict(kv=None), dict(out=None), dict(c=cache(w, v=None))):
+        assert call(**bad) == S.ERR_NULL, bad
+    for bad in (dict(B=0), dict(hq=0), dict(hq=30), dict(columns=0), dict(stride=7), dict(window=-1)):
+        assert call(**bad) == S.ERR_SHAPE, bad
+    assert call(B=1 << 19) == S.ERR_UNSUPPORTED
+    for bad in (dict(q=MIS), dict(out=MIS), dict(qr=100), dict(outh=4), dict(table=ODD), dict(kv=ODD), dict(lse=ODD), dict(ws=MIS)):
+        assert call(**bad) == S.ERR_ALIGN, bad
+    for bad in (dict(ws=None), dict(n=need - 1)):
+        assert call(**bad) == S.ERR_WORKSPACE, bad
+    if not torch.cuda.is_available():
+        assert call() == S.ERR_CUDA
+
+
+def test_binding_refuses_cpu_tensors(w):
+    z = torch.zeros
+    with pytest.raises(ValueError):
+        w.PagedCache(z(2, 16, 1, 64).bfloat16(), z(2, 16, 1, 64).bfloat16())
+    with pytest.raises(ValueError):
+        w.w4a16_paged_map(z(2).int(), z(2).int(), z(2, 4).int(), z(8).int(), z(1).int(), 16, 8, 2)
+    with pytest.raises(ValueError):
+        w.w4a16_rope_append(z(2, 4, 64).bfloat16(), None, None, z(2).int(), z(32), None, None)
+
+
+def test_reference_map_by_hand():
+    # request 0 holds 5 of 4-token blocks [9, 7], adds 4: one new block; request 1 begins with 3 tokens
+    got = ref.paged_map([5, 0], [4, 3], [[9, 7, -1], [-1, -1, -1]], [50, 2, 4, 6], 1, 4, 10, 8)
+    assert got[0] == [[9, 7, 2], [4, -1, -1]]
+    assert got[1] == [7 * 4 + 1, 7 * 4 + 2, 7 * 4 + 3, 2 * 4, 16, 17, 18, -1]
+    assert got[2] == [5, 6, 7, 8, 0, 1, 2, -1]
+    assert got[3:] == ([0, 4, 7], [9, 3], 3, set())
+
+
+def test_reference_rope_by_hand():
+    x = torch.tensor([[[1.0, 2.0, 3.0, 4.0, 5.0]]], dtype=torch.float64)
+    quarter = torch.tensor([3.14159265358979 / 2, 0.0]).float()
+    y = ref.rope(x, torch.tensor([[1]]), quarter, [2], False)
+    assert torch.allclose(y, torch.tensor([[[-3.0, 2.0, 1.0, 4.0, 5.0]]], dtype=torch.float64), atol=1e-6)
+    y = ref.rope(x, torch.tensor([[1]]), quarter, [2], True)
+    assert torch.allclose(y, torch.tensor([[[-2.0, 1.0, 3.0, 4.0, 5.0]]], dtype=torch.float64), atol=1e-6)
+    z = ref.rope(y, torch.tensor([[1]]), quarter, [2], True, inverse=True)
+    assert torch.allclose(z, x, atol=1e-12)
+
+
+def test_reference_attention_against_softmax():
+    gen = torch.Generator().manual_seed(0)
+    k, v = (torch.randn(4, 2, 1, 16, generator=gen, dtype=torch.float64) for _ in range(2))
+    q = torch.randn(1, 2, 16, generator=gen, dtype=torch.float64)
+    out, lse, spread, reach = ref.attention(q, k, v, [[3, 0, 1]], [5], 0.25, 3)
+    rows = [(0, 0), (0, 1), (1, 0)]  # the last three of five tokens
+    kk, vv = torch.stack([k[i, p, 0] for i, p in rows]), torch.stack([v[i, p, 0] for i, p in rows])
+    s = 0.25 * q[0] @ kk.t()
+    assert torch.allclose(out[0], torch.softmax(s, 1) @ vv)
+    assert torch.allclose(lse[0], torch.logsumexp(s, 1))

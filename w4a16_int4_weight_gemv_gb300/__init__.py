@@ -17,7 +17,9 @@ _BINDING_NAMES = (
     "Status", "W4A16Error", "lib_path", "load_library", "status_string",
     "int4_pack", "int4_dequant", "w4a16_gemv", "w4a16_gemv_workspace_bytes",
     "w4a16_moe_gemv", "w4a16_moe_workspace_bytes", "w4a16_swiglu",
-    "w4a16_device_error", "moe_ffn", "gemv_plan",
+    "w4a16_device_error", "moe_ffn", "gemv_plan", "PagedCache", "PagedMap",
+    "paged_map_buffers", "w4a16_paged_map", "w4a16_rope_append",
+    "paged_attention_workspace", "w4a16_paged_attention",
 )
 
 __all__ = list(_BINDING_NAMES) + ["synth"]

@@ -11,6 +11,7 @@ patterns.  Packed weights are int32 (bit patterns of the uint32 words).
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import enum
 import os
@@ -34,6 +35,8 @@ class Status(enum.IntEnum):
 DEVERR_EXPERT_ID = 0x1
 DEVERR_RANGE = 0x4
 DEVERR_TIMEOUT = 0x2
+DEVERR_SLOT = 0x8
+DEVERR_BLOCKS = 0x10
 OUT_BF16 = 0
 OUT_F32 = 1
 
@@ -110,6 +113,16 @@ def load_library():
                                            I32, P, SZ, P]
     lib.w3a16_moe_gemv.restype = I32
     lib.w3a16_moe_gemv.argtypes = [P, I32, P, P, P, P, P, P, I32, I32, I32, I64, I64, I64, P]
+    lib.w4a16_paged_map.restype = I32
+    lib.w4a16_paged_map.argtypes = [P, P, I32, P, I64, I32, P, I64, P, I32, I64, P, P, I64, P, P, P, P]
+    lib.w4a16_rope_append.restype = I32
+    lib.w4a16_rope_append.argtypes = [P, I64, I64, P, I64, I64, I32, P, I64, I64, P, I64, I64, P, I64, P, P,
+                                      I32, I32, I32, ctypes.c_uint, P, P, I64, P]
+    lib.w4a16_paged_attention_workspace_bytes.restype = SZ
+    lib.w4a16_paged_attention_workspace_bytes.argtypes = [I32, I32, I32]
+    lib.w4a16_paged_attention.restype = I32
+    lib.w4a16_paged_attention.argtypes = [P, I64, I64, P, P, I64, I32, P, I32, I32, ctypes.c_float, I32, P,
+                                          I64, I64, P, P, SZ, P]
     _lib = lib
     return lib
 
@@ -519,6 +532,207 @@ def w3a16_moe_gemv(x, expert_ids, wq3, scale, zero, g: int, route_w=None, x_per_
                                          _ptr(scale), _ptr(zero), _ptr(out), M, topk, E, N, K, g,
                                          _stream(stream, x.get_device())), "w3a16_moe_gemv")
     return out
+
+
+# --------------------------------------------------------------------------
+# paged key/value cache: block map, rotary + append, one-token attention
+# --------------------------------------------------------------------------
+class _KvCache(ctypes.Structure):
+    """w4a16_kv_cache of include/w4a16.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("dtype", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("page", ctypes.c_int32), ("blocks", ctypes.c_int64),
+                ("k_block", ctypes.c_int64), ("k_token", ctypes.c_int64), ("k_head", ctypes.c_int64),
+                ("v_block", ctypes.c_int64), ("v_token", ctypes.c_int64), ("v_head", ctypes.c_int64)]
+
+
+CACHE_BF16 = 0
+CACHE_E4M3 = 1
+ROPE_INTERLEAVED = 0x1
+ROPE_INVERSE = 0x2
+_I32 = (torch.int32,)
+_F32 = (torch.float32,)
+
+
+class PagedCache:
+    """Handle of one layer's paged key/value cache.
+
+    k, v: CUDA tensors [blocks, page, heads, dim], bfloat16 or float8_e4m3fn,
+    dim contiguous, the other strides free (a cache kept as [blocks, heads,
+    page, dim] is passed as its permute(0, 2, 1, 3)); k_scale, v_scale:
+    float32 [heads], needed with float8 (key = code * k_scale[head]).  The
+    tensors stay the caller's; the handle holds references to them, so the
+    memory it points at lives as long as it does."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        for t, name in ((k, "k"), (v, "v")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError("%s must be a torch.Tensor" % name)
+            if not t.is_cuda or t.dim() != 4 or t.stride(3) != 1:
+                raise ValueError("%s must be a CUDA tensor [blocks, page, heads, dim], dim contiguous" % name)
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or v.dtype != k.dtype:
+            raise TypeError("k and v must both be bfloat16 or both float8_e4m3fn")
+        if v.shape != k.shape or v.device != k.device:
+            raise ValueError("k and v must have the same shape and device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.blocks, self.page, self.heads, self.dim = k.shape
+        e4m3 = k.dtype == torch.float8_e4m3fn
+        if e4m3:
+            _need(k_scale, "k_scale", _F32, (self.heads,))
+            _need(v_scale, "v_scale", _F32, (self.heads,))
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("a bfloat16 cache has no scales")
+        self._struct = _KvCache(_ptr(k), _ptr(v), _ptr(k_scale) if e4m3 else None,
+                                _ptr(v_scale) if e4m3 else None, CACHE_E4M3 if e4m3 else CACHE_BF16,
+                                self.heads, self.dim, self.page, self.blocks,
+                                *k.stride()[:3], *v.stride()[:3])
+        self._ref = ctypes.addressof(self._struct)
+
+
+PagedMap = collections.namedtuple("PagedMap", "slots positions row_start kv_len free_head")
+
+
+def paged_map_buffers(requests: int, tokens: int, device) -> PagedMap:
+    """Output buffers of w4a16_paged_map, to be kept from step to step."""
+    new = lambda n: torch.empty(n, dtype=torch.int32, device=device)
+    return PagedMap(new(tokens), new(tokens), new(requests + 1), new(requests), new(1))
+
+
+def w4a16_paged_map(ctx_len, new_len, block_table, free_blocks, free_head, page: int, num_blocks: int,
+                    tokens: int, out: PagedMap = None, stream=None) -> PagedMap:
+    """Block tables and slot maps from the lengths of the requests.
+
+    ctx_len, new_len int32 [B]: tokens request b has cached and adds now;
+    block_table int32 [B, columns] (a row stride is allowed): the entries of
+    the blocks the new tokens begin are filled in place from free_blocks
+    int32 [F], from entry free_head int32 [1] on; tokens: how many places the
+    slots and positions have (at least the new tokens; the rest gets -1).
+    Returns PagedMap(slots [tokens], positions [tokens], row_start [B + 1],
+    kv_len [B], free_head [1]), all int32."""
+    _need(ctx_len, "ctx_len", _I32)
+    B = ctx_len.shape[0]
+    _need(new_len, "new_len", _I32, (B,))
+    _need(free_blocks, "free_blocks", _I32)
+    _need(free_head, "free_head", _I32)
+    if (block_table.dim() != 2 or block_table.dtype != torch.int32 or not block_table.is_cuda
+            or block_table.stride(1) != 1 or block_table.shape[0] != B):
+        raise ValueError("block_table must be a CUDA int32 [%d, columns] with unit column stride" % B)
+    if out is None:
+        out = paged_map_buffers(B, tokens, ctx_len.device)
+    else:
+        for t, name, n in zip(out, PagedMap._fields, (tokens, tokens, B + 1, B, 1)):
+            _need(t, name, _I32, (n,))
+    _check(load_library().w4a16_paged_map(
+        _ptr(ctx_len), _ptr(new_len), B, _ptr(block_table), block_table.stride(0), block_table.shape[1],
+        _ptr(free_blocks), free_blocks.numel(), _ptr(free_head), page, num_blocks, _ptr(out.slots),
+        _ptr(out.positions), tokens, _ptr(out.row_start), _ptr(out.kv_len), _ptr(out.free_head),
+        _stream(stream, ctx_len.get_device())), "w4a16_paged_map")
+    return out
+
+
+def _need_rows(t, name: str, shape):
+    """bf16 heads [rows, heads, dim], dim contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda or t.dtype not in _BF16 or t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError("%s must be a CUDA bf16 tensor [rows, heads, dim], dim contiguous" % name)
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+
+
+def w4a16_rope_append(q, k, v, positions, inv_freq, slots, cache: PagedCache, sections=None,
+                      interleaved: bool = False, inverse: bool = False, q_out=None, stream=None):
+    """Rotary positions on q and k, and k and v into the paged cache.
+
+    q bf16 [T, q_heads, dim], k and v bf16 [T, heads, dim] (views with token
+    and head strides, e.g. of a fused QKV output); positions int32 [T] or
+    [axes, T]; inv_freq float32 [rotary / 2]; sections: how many pairs go by
+    each axis; slots int32 [T], -1 for a token that is not stored.
+    interleaved: pairs (2i, 2i + 1) instead of (i, i + rotary / 2); inverse
+    turns back (the gradient).  q, or k, v, slots and cache together, may be
+    None.  Returns the rotated queries (q_out, or a new tensor; q_out=q
+    rotates in place)."""
+    ref = q if q is not None else k
+    T, _, dim = ref.shape
+    if q is not None:
+        _need_rows(q, "q", q.shape)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        else:
+            _need_rows(q_out, "q_out", q.shape)
+        qa = (_ptr(q), q.stride(0), q.stride(1), _ptr(q_out), q_out.stride(0), q_out.stride(1), q.shape[1])
+    else:
+        qa = (None, 0, 0, None, 0, 0, 0)
+    if cache is not None:
+        shape = (T, cache.heads, cache.dim)
+        _need_rows(k, "k", shape)
+        _need_rows(v, "v", shape)
+        _need(slots, "slots", _I32, (T,))
+        ka = (_ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1))
+        slots_ptr, cache_ref = _ptr(slots), cache._ref
+    else:
+        if k is not None or v is not None or slots is not None:
+            raise ValueError("k, v and slots go with a cache")
+        ka, slots_ptr, cache_ref = (None, 0, 0, None, 0, 0), None, None
+    _need(inv_freq, "inv_freq", _F32)
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    _need(positions, "positions", _I32, (T,) if positions.dim() == 1 else (axes, T))
+    sec = None
+    if sections is not None:
+        if len(sections) != axes:
+            raise ValueError("%d sections for %d axes" % (len(sections), axes))
+        sec = (ctypes.c_int32 * axes)(*sections)
+    if T == 0:
+        return q_out
+    _check(load_library().w4a16_rope_append(
+        *qa, *ka, _ptr(positions), T, _ptr(inv_freq), sec, axes, 2 * inv_freq.numel(), dim,
+        (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0), slots_ptr, cache_ref,
+        T, _stream(stream, ref.get_device())), "w4a16_rope_append")
+    return q_out
+
+
+def paged_attention_workspace(cache: PagedCache, q_heads: int) -> torch.Tensor:
+    """Workspace of w4a16_paged_attention for this cache and number of query
+    heads: zeroed once here, left zero where it has to be by every call."""
+    n = int(load_library().w4a16_paged_attention_workspace_bytes(q_heads, cache.heads, cache.dim))
+    return torch.zeros(max(n, 16), dtype=torch.uint8, device=cache.k.device)
+
+
+def w4a16_paged_attention(q, cache: PagedCache, block_table, kv_len, scale: float = None, window: int = 0,
+                          out=None, lse=None, workspace=None, stream=None):
+    """Attention of one new token per request over the paged cache.
+
+    q bf16 [B, q_heads, dim] (request and head strides allowed); block_table
+    int32 [B, columns]; kv_len int32 [B], the tokens each request sees, the
+    new one among them; window > 0: only the last `window` of them.  scale
+    defaults to dim ** -0.5.  Returns (out bf16 [B, q_heads, dim], lse float32
+    [B, q_heads]); a request of length 0 gets zeros and -infinity.
+    workspace: from paged_attention_workspace, one per stream in use (None:
+    a new one for this call)."""
+    B = q.shape[0]
+    H = q.shape[1]
+    _need_rows(q, "q", (B, H, cache.dim))
+    if (block_table.dim() != 2 or block_table.dtype != torch.int32 or not block_table.is_cuda
+            or block_table.stride(1) != 1 or block_table.shape[0] != B):
+        raise ValueError("block_table must be a CUDA int32 [%d, columns] with unit column stride" % B)
+    _need(kv_len, "kv_len", _I32, (B,))
+    if out is None:
+        out = torch.empty((B, H, cache.dim), dtype=torch.bfloat16, device=q.device)
+    else:
+        _need_rows(out, "out", q.shape)
+    if lse is None:
+        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+    else:
+        _need(lse, "lse", _F32, (B, H))
+    if workspace is None:
+        workspace = paged_attention_workspace(cache, H)
+    _check(load_library().w4a16_paged_attention(
+        _ptr(q), q.stride(0), q.stride(1), cache._ref, _ptr(block_table), block_table.stride(0),
+        block_table.shape[1], _ptr(kv_len), B, H, cache.dim ** -0.5 if scale is None else scale, window,
+        _ptr(out), out.stride(0), out.stride(1), _ptr(lse), _ptr(workspace), workspace.numel(),
+        _stream(stream, q.get_device())), "w4a16_paged_attention")
+    return out, lse
 
 
 load_library()

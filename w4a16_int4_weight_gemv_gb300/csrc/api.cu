@@ -8,12 +8,14 @@
 // problems instead of trapping.
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include <cuda_runtime.h>
 
 #include "launch.h"
 #include "moe_hmma_gemv.h"
+#include "paged.h"
 #include "w4a16.h"
 
 namespace w4a16 {
@@ -681,6 +683,153 @@ w4a16_status w4a16_device_error(uint32_t* bits_out, int clear, void* stream) {
         return from_cuda(cudaErrorUnknown);
     *bits_out = v;
     return W4A16_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// strides of rows that are read and written 16 bytes at a time
+bool row_strides(int64_t a, int64_t b, int elements) {
+    return a >= 0 && b >= 0 && a % elements == 0 && b % elements == 0;
+}
+
+w4a16_status check_cache(const w4a16_kv_cache& c) {
+    if (!c.k || !c.v) return W4A16_ERR_NULL;
+    if (c.dtype != W4A16_CACHE_BF16 && c.dtype != W4A16_CACHE_E4M3) return W4A16_ERR_UNSUPPORTED;
+    if (c.dtype == W4A16_CACHE_E4M3 && (!c.k_scale || !c.v_scale)) return W4A16_ERR_NULL;
+    if (c.heads < 1 || c.page < 1 || c.blocks < 1 || c.dim < 16 || c.dim % 16 != 0) return W4A16_ERR_SHAPE;
+    if (c.dim > 256 || c.page > 65536 || c.heads > 65536) return W4A16_ERR_UNSUPPORTED;
+    if (c.blocks >= (int64_t(1) << 31) / c.page) return W4A16_ERR_UNSUPPORTED;
+    const int row = c.dtype == W4A16_CACHE_BF16 ? 8 : 16;
+    if (!aligned16(c.k) || !aligned16(c.v) || !aligned4(c.k_scale) || !aligned4(c.v_scale) ||
+        !row_strides(c.k_block, c.k_token, row) || !row_strides(c.v_block, c.v_token, row) ||
+        !row_strides(c.k_head, c.v_head, row))
+        return W4A16_ERR_ALIGN;
+    return W4A16_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+w4a16_status w4a16_paged_map(const int32_t* ctx_len, const int32_t* new_len, int B, int32_t* block_table,
+                             int64_t table_stride, int columns, const int32_t* free_blocks, int64_t n_free,
+                             const int32_t* free_head, int page, int64_t num_blocks, int32_t* slots,
+                             int32_t* positions, int64_t tokens, int32_t* row_start, int32_t* kv_len,
+                             int32_t* free_head_out, void* stream) {
+    if (!ctx_len || !new_len || !block_table || !free_head || !row_start || !kv_len || !free_head_out ||
+        (n_free > 0 && !free_blocks) || (tokens > 0 && (!slots || !positions)))
+        return W4A16_ERR_NULL;
+    if (B < 1 || columns < 1 || table_stride < columns || n_free < 0 || page < 1 || num_blocks < 1 || tokens < 0)
+        return W4A16_ERR_SHAPE;
+    if (B > kMaxMapRequests || page > 65536 || num_blocks >= (int64_t(1) << 31) / page ||
+        tokens >= (int64_t(1) << 31) || n_free >= (int64_t(1) << 31))
+        return W4A16_ERR_UNSUPPORTED;
+    if (kv_len == ctx_len || kv_len == new_len || free_head_out == free_head) return W4A16_ERR_UNSUPPORTED;
+    for (const void* p : {static_cast<const void*>(ctx_len), static_cast<const void*>(new_len),
+                          static_cast<const void*>(block_table), static_cast<const void*>(free_blocks),
+                          static_cast<const void*>(free_head), static_cast<const void*>(slots),
+                          static_cast<const void*>(positions), static_cast<const void*>(row_start),
+                          static_cast<const void*>(kv_len), static_cast<const void*>(free_head_out)})
+        if (!aligned4(p)) return W4A16_ERR_ALIGN;
+    DeviceCache* dev = nullptr;
+    w4a16_status st = current_device(&dev);
+    if (st != W4A16_OK) return st;
+    PagedMapArgs a{ctx_len, new_len, block_table, table_stride, free_blocks, free_head, slots, positions,
+                   row_start, kv_len, free_head_out, n_free, num_blocks, tokens, B, columns, page, dev->err};
+    return from_cuda(launch_paged_map(a, dev->info, static_cast<cudaStream_t>(stream)));
+}
+
+w4a16_status w4a16_rope_append(const uint16_t* q, int64_t q_token, int64_t q_head, uint16_t* q_out,
+                               int64_t q_out_token, int64_t q_out_head, int q_heads, const uint16_t* k,
+                               int64_t k_token, int64_t k_head, const uint16_t* v, int64_t v_token,
+                               int64_t v_head, const int32_t* positions, int64_t axis_stride,
+                               const float* inv_freq, const int32_t* sections, int axes, int rotary, int dim,
+                               unsigned flags, const int32_t* slots, const w4a16_kv_cache* cache, int64_t T,
+                               void* stream) {
+    if (flags & ~static_cast<unsigned>(W4A16_ROPE_INTERLEAVED | W4A16_ROPE_INVERSE)) return W4A16_ERR_UNSUPPORTED;
+    const bool has_q = q != nullptr, has_kv = cache != nullptr;
+    if (has_q != (q_out != nullptr) || has_kv != (k != nullptr) || has_kv != (v != nullptr) ||
+        has_kv != (slots != nullptr) || (!has_q && !has_kv))
+        return W4A16_ERR_NULL;
+    if (rotary > 0 && (!positions || !inv_freq)) return W4A16_ERR_NULL;
+    if (T < 0 || axes < 1 || axis_stride < 0 || rotary < 0 || rotary % 16 != 0 || dim < 16 || dim % 16 != 0 ||
+        rotary > dim || (has_q && q_heads < 1))
+        return W4A16_ERR_SHAPE;
+    if (axes > 4 || dim > 256 || q_heads > 65536) return W4A16_ERR_UNSUPPORTED;
+    RopeArgs a{};
+    if (has_kv) {
+        w4a16_status st = check_cache(*cache);
+        if (st != W4A16_OK) return st;
+        if (cache->dim != dim) return W4A16_ERR_SHAPE;
+        a.cache = *cache;
+    }
+    if (!sections && axes != 1) return W4A16_ERR_NULL;
+    int sum = 0;
+    for (int i = 0; i < 4; ++i) {
+        if (i < axes) {
+            const int n = sections ? sections[i] : rotary / 2;
+            if (n < 0 || n > rotary / 2) return W4A16_ERR_SHAPE;
+            sum += n;
+        }
+        a.axis_end[i] = sum;
+    }
+    if (sum != rotary / 2) return W4A16_ERR_SHAPE;
+    if ((has_q && (!aligned16(q) || !aligned16(q_out) || !row_strides(q_token, q_head, 8) ||
+                   !row_strides(q_out_token, q_out_head, 8))) ||
+        (has_kv && (!aligned16(k) || !aligned16(v) || !row_strides(k_token, k_head, 8) ||
+                    !row_strides(v_token, v_head, 8))) ||
+        !aligned4(positions) || !aligned4(inv_freq) || !aligned4(slots))
+        return W4A16_ERR_ALIGN;
+    if (T == 0) return W4A16_OK;
+    DeviceCache* dev = nullptr;
+    w4a16_status st = current_device(&dev);
+    if (st != W4A16_OK) return st;
+    a.q = q, a.q_token = q_token, a.q_head = q_head;
+    a.q_out = q_out, a.qo_token = q_out_token, a.qo_head = q_out_head;
+    a.q_heads = has_q ? q_heads : 0;
+    a.k = k, a.k_token = k_token, a.k_head = k_head;
+    a.v = v, a.v_token = v_token, a.v_head = v_head;
+    a.positions = positions, a.axis_stride = axis_stride, a.inv_freq = inv_freq;
+    a.slots = slots, a.rotary = rotary, a.dim = dim, a.T = T;
+    a.interleaved = (flags & W4A16_ROPE_INTERLEAVED) ? 1 : 0;
+    a.inverse = (flags & W4A16_ROPE_INVERSE) ? 1 : 0;
+    a.err = dev->err;
+    return from_cuda(launch_rope_append(a, dev->info, static_cast<cudaStream_t>(stream)));
+}
+
+size_t w4a16_paged_attention_workspace_bytes(int q_heads, int kv_heads, int dim) {
+    if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || dim < 16 || dim > 256 || dim % 16 != 0) return 0;
+    return paged_attention_workspace(q_heads, kv_heads, dim);
+}
+
+w4a16_status w4a16_paged_attention(const uint16_t* q, int64_t q_request, int64_t q_head,
+                                   const w4a16_kv_cache* cache, const int32_t* block_table,
+                                   int64_t table_stride, int columns, const int32_t* kv_len, int B, int q_heads,
+                                   float scale, int window, uint16_t* out, int64_t out_request,
+                                   int64_t out_head, float* lse, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+    if (!q || !cache || !block_table || !kv_len || !out) return W4A16_ERR_NULL;
+    w4a16_status st = check_cache(*cache);
+    if (st != W4A16_OK) return st;
+    if (B < 1 || q_heads < 1 || q_heads % cache->heads != 0 || columns < 1 || table_stride < columns || window < 0)
+        return W4A16_ERR_SHAPE;
+    if (static_cast<int64_t>(B) * q_heads >= (1 << 24)) return W4A16_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(out) || !row_strides(q_request, q_head, 8) ||
+        !row_strides(out_request, out_head, 8) || !aligned4(block_table) || !aligned4(kv_len) || !aligned4(lse))
+        return W4A16_ERR_ALIGN;
+    if (!workspace || workspace_bytes < paged_attention_workspace(q_heads, cache->heads, cache->dim))
+        return W4A16_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return W4A16_ERR_ALIGN;
+    DeviceCache* dev = nullptr;
+    st = current_device(&dev);
+    if (st != W4A16_OK) return st;
+    AttentionArgs a{q, q_request, q_head, *cache, block_table, table_stride, kv_len, columns, B, q_heads, window,
+                    scale, out, out_request, out_head, lse, workspace, dev->err};
+    return from_cuda(launch_paged_attention(a, dev->info, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
