@@ -1,0 +1,643 @@
+// Attention of one new token per request over a paged key/value cache
+// (w4a16_paged_attention): the kernel, for one cache type per translation unit.
+//
+// A row is one request, one key/value head and up to 8 * NT of the query
+// heads that share it.  For the tokens j a row sees,
+//     s_j = c q . k_j (log2 units),  m = max s_j,  p_j = 2^(s_j - m),
+//     l = sum p_j,  o = sum p_j v_j,  out = o / l,
+// in one pass: a larger m scales the running l and o by 2^(m_old - m).
+// Partial (m, l, o) of disjoint token sets join the same way, in any grouping.
+//
+// Bound by HBM: each key and value is read once, for 2 * heads operations a
+// byte at most.  So the kernel is built around the copies:
+//   - Work is dealt in tiles of 16 tokens, rows one after another, and every
+//     CTA takes an equal consecutive share of all tiles, whatever the lengths
+//     are (each forms the sum of the tile counts itself).  A row that spans
+//     several CTAs is joined by the last of them to finish, in the order of
+//     the CTAs, so the result does not depend on which one that is.
+//   - Inside a CTA each warp takes every fourth tile of a row through a ring
+//     of its own of cp.async stages that runs on across rows; warps meet only
+//     at the end of a row.
+//   - The products run on the warp MMA with the keys as the 16-row operand
+//     (tokens) and the heads as its 8 columns: one product covers 8 query
+//     heads, and the transposed second product (values^T times p^T) takes the
+//     probabilities from the accumulators by one 8x8 transpose in registers.
+//     (tcgen05 would want 64 or more query rows; here there are 1 to 16.)
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "paged.h"
+
+namespace w4a16 {
+namespace {
+
+constexpr int kTile = 16;  // tokens of a tile: the MMA's rows
+constexpr int kAttnWarps = 4;
+constexpr int kAttnThreads = kAttnWarps * 32;
+constexpr int kMinTiles = 8;  // tiles a CTA takes at least
+
+// Shared memory: rings of `stages` tiles per warp, and the (m, l, o) of the
+// four warps.  A pitch of DP + 4 floats spreads the fragments' 8 dims x 4
+// head pairs over all banks.
+template <bool E4M3, int DP, int NT>
+struct AttnShape {
+    static constexpr int kHeads = 8 * NT;
+    static constexpr int kRowBytes = DP * (E4M3 ? 1 : 2);
+    static constexpr int kChunks = kRowBytes / 16;          // 16-byte chunks of a row
+    static constexpr int kStageBytes = 2 * kTile * kRowBytes;  // keys, then values
+    static constexpr int kPitch = DP + 4;
+    static constexpr int kJoinBytes = kAttnWarps * kHeads * (kPitch + 2) * 4;
+    // two CTAs an SM with three or more stages where that fits, else one
+    static constexpr int kTwo = (113 * 1024 - kJoinBytes - 512) / (kAttnWarps * kStageBytes);
+    static constexpr int kOne = (226 * 1024 - kJoinBytes - 512) / (kAttnWarps * kStageBytes);
+    static constexpr int kPerSm = kTwo >= 3 ? 2 : 1;
+    static constexpr int kFit = kPerSm == 2 ? kTwo : kOne;
+    static constexpr int kStages = kFit > 6 ? 6 : kFit;
+    static constexpr int kSmem = kAttnWarps * kStages * kStageBytes + kJoinBytes;
+    static_assert(kStages >= 2, "ring too short");
+};
+
+__device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void* src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&d)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// 8x8 transpose of 16-bit elements across the warp
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+    return d;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// two e4m3 codes (low and high byte) as an fp16 pair, exactly
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<uint16_t>(v)));
+    return d;
+}
+template <bool E4M3>
+__device__ __forceinline__ void attn_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    if (E4M3) {
+        mma_f16_16816(d, a0, a1, a2, a3, b0, b1);
+    } else {
+        const uint32_t a[4] = {a0, a1, a2, a3};
+        mma_bf16_16816(d, a, b0, b1, d);
+    }
+}
+
+// byte offset of chunk c of row r in a tile whose rows have CH chunks: eight
+// rows reading one chunk hit eight different 16-byte bank groups
+template <int CH>
+__device__ __forceinline__ uint32_t tile_offset(int r, int c) {
+    const int f = (CH % 8 == 0) ? (r & 7) : ((r >> 1) & 3);
+    return static_cast<uint32_t>((r * CH + (c ^ f)) * 16);
+}
+
+// What one request looks like: its visible tokens [start, len), in tiles from
+// tile0 on.
+struct Request {
+    int len, start, tile0, tiles;
+};
+
+__device__ __forceinline__ Request request_of(const AttentionArgs& a, int b, bool& bad) {
+    Request q;
+    int64_t len = a.kv_len[b];
+    const int64_t most = static_cast<int64_t>(a.columns) * a.cache.page;
+    bad |= len < 0 || len > most;
+    len = len < 0 ? 0 : len > most ? most : len;
+    q.len = static_cast<int>(len);
+    q.start = a.window > 0 && q.len > a.window ? q.len - a.window : 0;
+    q.tile0 = q.start / kTile;
+    q.tiles = q.len > 0 ? (q.len - 1) / kTile + 1 - q.tile0 : 0;
+    return q;
+}
+
+// A run of tiles of one row inside a CTA's share.
+struct Segment {
+    int b, row;   // request, and row of the request
+    int t0, t1;   // tiles of the row
+    int64_t left;  // tiles of the share after this segment
+    Request q;
+};
+
+// Partials of rows that several CTAs share: two places per CTA (0: the row
+// its share begins inside of, 1: the row its share ends inside of), and a
+// counter per CTA for the row that begins in it.
+struct Workspace {
+    uint32_t* arrived;
+    float* part;  // [cta][2][heads * (DP + 2)]: o [heads][DP], then m, then l
+};
+
+template <bool E4M3, int DP, int NT>
+__global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const AttentionArgs a, const Workspace ws) {
+    using Sh = AttnShape<E4M3, DP, NT>;
+    constexpr int CH = Sh::kChunks, S = Sh::kStages, HEADS = Sh::kHeads;
+    constexpr int kPart = HEADS * (DP + 2);
+    constexpr float kBias = E4M3 ? 15.f : 0.f;  // p up to 2^15: fp16 then holds p down to 2^-39 of the largest
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint32_t tile_mask[kAttnWarps][S];
+    __shared__ int64_t scan_sum[kAttnWarps];
+    __shared__ int64_t found_before;
+    __shared__ int found_b;
+    __shared__ uint32_t arrived_before;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = lane >> 2, c = lane & 3;
+    const uint32_t ring = smem_addr(smem) + warp * S * Sh::kStageBytes;
+    float* join = reinterpret_cast<float*>(smem + kAttnWarps * S * Sh::kStageBytes);
+    float* join_m = join + kAttnWarps * HEADS * Sh::kPitch;
+    float* join_l = join_m + kAttnWarps * HEADS;
+    const int D = a.cache.dim, G = a.q_heads / a.cache.heads;
+    const int chunks_of_group = (G + HEADS - 1) / HEADS;
+    const int rows = a.cache.heads * chunks_of_group;  // of a request
+    const int real_chunks = D * (E4M3 ? 1 : 2) / 16;
+    bool bad = false;
+
+    grid_dependents_launch();
+    if (D != DP) {  // columns past dim are never copied: zero them once
+        for (int i = threadIdx.x; i < kAttnWarps * S * Sh::kStageBytes / 16; i += kAttnThreads)
+            reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
+        __syncthreads();
+    }
+    grid_dependency_wait();
+
+    // --- the share of this CTA ---------------------------------------------
+    int64_t sum = 0;
+    int mine = 0;  // tiles of request threadIdx.x
+    for (int b = threadIdx.x; b < a.B; b += kAttnThreads) {
+        const int n = request_of(a, b, bad).tiles;
+        if (b < kAttnThreads) mine = n;
+        sum += n;
+    }
+#pragma unroll
+    for (int d = 16; d; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    if (lane == 0) scan_sum[warp] = sum;
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) total += scan_sum[w];
+    total *= rows;
+    // requests without tokens
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        if (request_of(a, b, bad).tiles > 0) continue;
+        for (int i = threadIdx.x; i < a.q_heads * (D / 8); i += kAttnThreads) {
+            const int h = i / (D / 8), d = (i - h * (D / 8)) * 8;
+            *reinterpret_cast<uint4*>(a.out + b * a.out_request + h * a.out_head + d) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (a.lse)
+            for (int h = threadIdx.x; h < a.q_heads; h += kAttnThreads)
+                a.lse[static_cast<int64_t>(b) * a.q_heads + h] = -INFINITY;
+    }
+    const int64_t want = (total + kMinTiles - 1) / kMinTiles;
+    const int ctas = want < gridDim.x ? static_cast<int>(want) : static_cast<int>(gridDim.x);
+    if (static_cast<int>(blockIdx.x) >= ctas) {
+        if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
+        return;
+    }
+    const int64_t u0 = blockIdx.x * total / ctas, u1 = (blockIdx.x + 1) * total / ctas;
+    // the request that tile u0 of all belongs to, and the tiles before it
+    int64_t before = 0;
+    for (int base = 0; base < a.B; base += kAttnThreads) {
+        const int b = base + static_cast<int>(threadIdx.x);
+        const int64_t n = base == 0 ? static_cast<int64_t>(mine) * rows
+                                    : (b < a.B ? static_cast<int64_t>(request_of(a, b, bad).tiles) * rows : 0);
+        int64_t inc = n;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+            if (lane >= d) inc += v;
+        }
+        __syncthreads();
+        if (lane == 31) scan_sum[warp] = inc;
+        __syncthreads();
+        int64_t start = before, chunk = 0;
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) {
+            if (w < warp) start += scan_sum[w];
+            chunk += scan_sum[w];
+        }
+        start += inc - n;
+        if (u0 >= start && u0 < start + n) {
+            found_b = b;
+            found_before = start;
+        }
+        before += chunk;
+        if (before > u0) break;
+    }
+    __syncthreads();
+
+    // --- tiles, in order ---------------------------------------------------
+    auto open_segment = [&](Segment& s, int64_t left) {
+        s.t1 = left < s.q.tiles - s.t0 ? s.t0 + static_cast<int>(left) : s.q.tiles;
+        s.left = left - (s.t1 - s.t0);
+    };
+    auto next_segment = [&](Segment& s) -> bool {
+        if (s.left == 0) return false;
+        if (++s.row == rows) {
+            s.row = 0;
+            do {
+                ++s.b;
+                s.q = request_of(a, s.b, bad);
+            } while (s.q.tiles == 0);
+        }
+        s.t0 = 0;
+        open_segment(s, s.left);
+        return true;
+    };
+    Segment seg;
+    seg.b = found_b;
+    seg.q = request_of(a, seg.b, bad);
+    {
+        const int64_t in = u0 - found_before;
+        seg.row = static_cast<int>(in / seg.q.tiles);
+        seg.t0 = static_cast<int>(in - static_cast<int64_t>(seg.row) * seg.q.tiles);
+    }
+    open_segment(seg, u1 - u0);
+
+    // The copies run ahead of the products: `ahead` is the segment of the next
+    // tile to copy, `ahead_t` the tile, ahead_id this lane's block id for it
+    // (lane i and lane i + 16: token i), loaded one tile early.
+    Segment ahead = seg;
+    int ahead_t = seg.t0 + warp;
+    bool more = true;
+    int ahead_id = -1, ahead_place = 0;
+    auto settle = [&]() {
+        while (more && ahead_t >= ahead.t1) {
+            more = next_segment(ahead);
+            ahead_t = ahead.t0 + warp;
+        }
+        if (!more) return;
+        const int token = (ahead.q.tile0 + ahead_t) * kTile + (lane & 15);
+        const int col = static_cast<int>(static_cast<unsigned>(token) / static_cast<unsigned>(a.cache.page));
+        ahead_place = token - col * a.cache.page;
+        ahead_id = -1;
+        if (token >= ahead.q.start && token < ahead.q.len) {
+            ahead_id = a.block_table[ahead.b * a.table_stride + col];
+            if (ahead_id < 0) ahead_id = -2;
+        }
+    };
+    constexpr int kBytes = E4M3 ? 1 : 2;
+    auto copy_tile = [&](int slot) {
+        if (more) {
+            const bool valid = ahead_id >= 0 && ahead_id < a.cache.blocks;
+            bad |= ahead_id != -1 && !valid;
+            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, valid) & 0xFFFFu;
+            if (lane == 0) tile_mask[warp][slot] = mask;
+            const int64_t id = valid ? ahead_id : 0, place = valid ? ahead_place : 0;
+            const int hk = ahead.row / chunks_of_group;
+            const int64_t ko = id * a.cache.k_block + place * a.cache.k_token;
+            const int64_t vo = id * a.cache.v_block + place * a.cache.v_token;
+            const char* kp = static_cast<const char*>(a.cache.k) + hk * a.cache.k_head * kBytes;
+            const char* vp = static_cast<const char*>(a.cache.v) + hk * a.cache.v_head * kBytes;
+            const uint32_t dst = ring + slot * Sh::kStageBytes;
+#pragma unroll
+            for (int i = 0; i < kTile * CH / 32; ++i) {
+                const int row = (i * 32 + lane) / CH, ch = (i * 32 + lane) % CH;
+                const int64_t kr = __shfl_sync(0xFFFFFFFFu, ko, row);
+                const int64_t vr = __shfl_sync(0xFFFFFFFFu, vo, row);
+                const bool ok = (mask >> row) & 1u;
+                if (ch < real_chunks) {
+                    const uint32_t at = dst + tile_offset<CH>(row, ch);
+                    cp_async_16_zfill(at, kp + kr * kBytes + ch * 16, ok);
+                    cp_async_16_zfill(at + kTile * Sh::kRowBytes, vp + vr * kBytes + ch * 16, ok);
+                }
+            }
+            ahead_t += kAttnWarps;
+            settle();
+        }
+        cp_async_commit();
+    };
+
+    settle();
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) copy_tile(i);
+
+    int slot = 0;
+    while (true) {
+        // queries of the row, as B fragments (columns: heads)
+        const int hk = seg.row / chunks_of_group, chunk = seg.row - hk * chunks_of_group;
+        const int head0 = hk * G + chunk * HEADS;           // first query head of the row
+        const int heads = min(HEADS, G - chunk * HEADS);
+        uint32_t qf[NT][DP / 16][2];
+        float sl[NT][2];  // score scale of columns 2c, 2c + 1
+        float m[NT][2], l[NT][2], o[NT][DP / 16][4];
+        const float base = a.scale * 1.4426950408889634f * (E4M3 ? a.cache.k_scale[hk] : 1.f);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const uint16_t* qp = a.q + seg.b * a.q_request + (head0 + n * 8 + r) * a.q_head;
+            const bool have = n * 8 + r < heads;
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k) {
+                qf[n][k][0] = qf[n][k][1] = 0u;
+                if (have && k * 16 < D) {
+                    // bf16: dims 2c, 2c + 1 and 8 further; e4m3: the four dims whose codes one word holds
+                    const int d = k * 16 + (E4M3 ? 4 * c : 2 * c);
+                    qf[n][k][0] = *reinterpret_cast<const uint32_t*>(qp + d);
+                    qf[n][k][1] = *reinterpret_cast<const uint32_t*>(qp + d + (E4M3 ? 2 : 8));
+                }
+            }
+            sl[n][0] = sl[n][1] = base;
+            if (E4M3) {
+                // to fp16, scaled by a power of two that takes the head's largest into [2^14, 2^15)
+                uint32_t big = 0u;
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    big = __vmaxu2(big, __vmaxu2(qf[n][k][0] & 0x7FFF7FFFu, qf[n][k][1] & 0x7FFF7FFFu));
+                big = max(big & 0xFFFFu, big >> 16);
+                big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+                big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+                const int eb = min(static_cast<int>(big >> 7), 254);
+                const int sh = min(141 - eb, 126);
+                const float up = exp2i(sh), down = exp2i(-sh);
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t v = qf[n][k][e];
+                        const __half2 h = __floats2half2_rn(bf16_to_f32(v & 0xFFFFu) * up, bf16_to_f32(v >> 16) * up);
+                        qf[n][k][e] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                sl[n][0] *= __shfl_sync(0xFFFFFFFFu, down, 8 * c);
+                sl[n][1] *= __shfl_sync(0xFFFFFFFFu, down, 8 * c + 4);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[n][e] = -INFINITY;
+                l[n][e] = 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][k][e] = 0.f;
+        }
+
+        for (int t = seg.t0 + warp; t < seg.t1; t += kAttnWarps) {
+            cp_async_wait_group<S - 2>();
+            __syncwarp();
+            copy_tile(slot == 0 ? S - 1 : slot - 1);
+            const uint32_t kt = ring + slot * Sh::kStageBytes, vt = kt + kTile * Sh::kRowBytes;
+            const uint32_t mask = tile_mask[warp][slot];
+            slot = slot + 1 == S ? 0 : slot + 1;
+
+            float s[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+            if (!E4M3) {
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) {
+                    uint32_t f[4];
+                    ldmatrix_x4(f, kt + tile_offset<CH>(lane & 15, 2 * k + (lane >> 4)));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) attn_mma<E4M3>(s[n], f[0], f[1], f[2], f[3], qf[n][k][0], qf[n][k][1]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < DP / 16; k += 2) {
+                    uint32_t f[4];  // two chunks of 16 codes: rows r and r + 8 of each
+                    ldmatrix_x4(f, kt + tile_offset<CH>(lane & 15, k + (lane >> 4)));
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t a0 = e4m3x2_to_f16x2(f[2 * j]), a2 = e4m3x2_to_f16x2(f[2 * j] >> 16);
+                        const uint32_t a1 = e4m3x2_to_f16x2(f[2 * j + 1]), a3 = e4m3x2_to_f16x2(f[2 * j + 1] >> 16);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            attn_mma<E4M3>(s[n], a0, a1, a2, a3, qf[n][k + j][0], qf[n][k + j][1]);
+                    }
+                }
+            }
+            uint32_t pf[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][e] *= sl[n][e & 1];
+                if (mask != 0xFFFFu) {
+                    const bool lo = (mask >> r) & 1u, hi = (mask >> (r + 8)) & 1u;
+                    if (!lo) s[n][0] = s[n][1] = -INFINITY;
+                    if (!hi) s[n][2] = s[n][3] = -INFINITY;
+                }
+                float top[2] = {fmaxf(s[n][0], s[n][2]), fmaxf(s[n][1], s[n][3])};
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 4));
+                    top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 8));
+                    top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 16));
+                    top[e] = fmaxf(top[e], m[n][e]);
+                }
+                if (__any_sync(0xFFFFFFFFu, top[0] > m[n][0] || top[1] > m[n][1])) {
+                    float keep[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        keep[e] = m[n][e] == top[e] ? 1.f : exp2_fast(m[n][e] - top[e]);  // -inf: 0
+                        m[n][e] = top[e];
+                        l[n][e] *= keep[e];
+                    }
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[n][k][e] *= keep[e & 1];
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float from = m[n][e & 1] == -INFINITY ? 0.f : m[n][e & 1] - kBias;
+                    s[n][e] = exp2_fast(s[n][e] - from);
+                    l[n][e & 1] += s[n][e];
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    uint32_t v;
+                    if (E4M3) {
+                        const __half2 h = __floats2half2_rn(s[n][2 * e], s[n][2 * e + 1]);
+                        v = *reinterpret_cast<const uint32_t*>(&h);
+                    } else {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(s[n][2 * e], s[n][2 * e + 1]);
+                        v = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                    pf[n][e] = transpose_8x8(v);
+                }
+            }
+            if (!E4M3) {
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) {
+                    uint32_t f[4];
+                    ldmatrix_x4_trans(f, vt + tile_offset<CH>((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) attn_mma<E4M3>(o[n][k], f[0], f[1], f[2], f[3], pf[n][0], pf[n][1]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < DP / 16; k += 2) {
+                    uint32_t f[4];  // chunk k: tokens 0..7, 8..15, then chunk k + 1
+                    ldmatrix_x4_trans(f, vt + tile_offset<CH>(lane & 15, k + (lane >> 4)));
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        // word: dims 2r, 2r + 1 of token 2c, then of token 2c + 1
+                        const uint32_t x0 = e4m3x2_to_f16x2(f[2 * j]), x1 = e4m3x2_to_f16x2(f[2 * j] >> 16);
+                        const uint32_t y0 = e4m3x2_to_f16x2(f[2 * j + 1]), y1 = e4m3x2_to_f16x2(f[2 * j + 1] >> 16);
+                        const uint32_t a0 = __byte_perm(x0, x1, 0x5410), a1 = __byte_perm(x0, x1, 0x7632);
+                        const uint32_t a2 = __byte_perm(y0, y1, 0x5410), a3 = __byte_perm(y0, y1, 0x7632);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            attn_mma<E4M3>(o[n][k + j], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+                    }
+                }
+            }
+        }
+
+        // --- join the warps --------------------------------------------------
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 4);
+                l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 8);
+                l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 16);
+                const int h = warp * HEADS + n * 8 + 2 * c + e;
+                if (r == 0) {
+                    join_m[h] = m[n][e];
+                    join_l[h] = l[n][e];
+                }
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) {
+                    // e4m3: rows r and r + 8 of the product are dims 2r and 2r + 1
+                    float* p = join + h * Sh::kPitch + k * 16;
+                    p[E4M3 ? 2 * r : r] = o[n][k][e];
+                    p[E4M3 ? 2 * r + 1 : r + 8] = o[n][k][2 + e];
+                }
+            }
+        }
+        __syncthreads();
+        const bool whole = seg.t0 == 0 && seg.t1 == seg.q.tiles;
+        const int place = seg.t0 == 0 ? 1 : 0;
+        float* part = ws.part + (static_cast<int64_t>(blockIdx.x) * 2 + place) * kPart;
+        auto finish = [&](int h, int d, float4 v, float top, float all) {
+            const float f = all != 0.f ? (E4M3 ? a.cache.v_scale[hk] : 1.f) / all : 0.f;
+            const uint32_t lo = f32_to_bf16_rn(v.x * f) | (static_cast<uint32_t>(f32_to_bf16_rn(v.y * f)) << 16);
+            const uint32_t hi = f32_to_bf16_rn(v.z * f) | (static_cast<uint32_t>(f32_to_bf16_rn(v.w * f)) << 16);
+            *reinterpret_cast<uint2*>(a.out + seg.b * a.out_request + (head0 + h) * a.out_head + d) = make_uint2(lo, hi);
+            if (d == 0 && a.lse)
+                a.lse[static_cast<int64_t>(seg.b) * a.q_heads + head0 + h] =
+                    all != 0.f ? (top + (log2f(all) - kBias)) * 0.6931471805599453f : -INFINITY;
+        };
+        for (int i = threadIdx.x; i < heads * (D / 4); i += kAttnThreads) {
+            const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
+            float top = -INFINITY, all = 0.f;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, join_m[w * HEADS + h]);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) {
+                const float lw = join_l[w * HEADS + h];
+                if (lw != 0.f) {
+                    const float mw = join_m[w * HEADS + h];
+                    const float f = mw == top ? 1.f : exp2_fast(mw - top);
+                    const float4 x = *reinterpret_cast<const float4*>(join + (w * HEADS + h) * Sh::kPitch + d);
+                    all = fmaf(lw, f, all);
+                    v.x = fmaf(x.x, f, v.x), v.y = fmaf(x.y, f, v.y);
+                    v.z = fmaf(x.z, f, v.z), v.w = fmaf(x.w, f, v.w);
+                }
+            }
+            if (whole) {
+                finish(h, d, v, top, all);
+            } else {
+                __stcg(reinterpret_cast<float4*>(part + h * DP + d), v);
+                if (d == 0) {
+                    __stcg(part + HEADS * DP + h, top);
+                    __stcg(part + HEADS * (DP + 1) + h, all);
+                }
+            }
+        }
+        if (!whole) {
+            // --- join the CTAs of the row: the last one to arrive does it ----
+            const int64_t first_tile = u1 - seg.left - (seg.t1 - seg.t0) - seg.t0;  // the row's first tile of all
+            const int first = static_cast<int>(((first_tile + 1) * ctas - 1) / total);
+            const int last = static_cast<int>(((first_tile + seg.q.tiles) * ctas - 1) / total);
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) arrived_before = atomicAdd(ws.arrived + first, 1u);
+            __syncthreads();
+            if (arrived_before == static_cast<uint32_t>(last - first)) {
+                __threadfence();
+                for (int i = threadIdx.x; i < heads * (D / 4); i += kAttnThreads) {
+                    const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
+                    const float* p0 = ws.part + (static_cast<int64_t>(first) * 2 + 1) * kPart;
+                    float top = -INFINITY, all = 0.f;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int q = first; q <= last; ++q) {
+                        const float* p = q == first ? p0 : ws.part + static_cast<int64_t>(q) * 2 * kPart;
+                        const float mq = __ldcg(p + HEADS * DP + h), lq = __ldcg(p + HEADS * (DP + 1) + h);
+                        const float4 x = __ldcg(reinterpret_cast<const float4*>(p + h * DP + d));
+                        if (lq == 0.f) continue;
+                        const float t = fmaxf(top, mq);
+                        const float f0 = top == t ? 1.f : exp2_fast(top - t), f1 = mq == t ? 1.f : exp2_fast(mq - t);
+                        top = t;
+                        all = all * f0 + lq * f1;
+                        v.x = v.x * f0 + x.x * f1, v.y = v.y * f0 + x.y * f1;
+                        v.z = v.z * f0 + x.z * f1, v.w = v.w * f0 + x.w * f1;
+                    }
+                    finish(h, d, v, top, all);
+                }
+                if (threadIdx.x == 0) ws.arrived[first] = 0u;
+            }
+        }
+        __syncthreads();
+        if (!next_segment(seg)) break;
+    }
+    cp_async_wait_group<0>();
+    if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
+}
+
+template <bool E4M3, int DP, int NT>
+cudaError_t launch_attention_shape(const AttentionArgs& a, const DeviceInfo& dev, const Workspace& ws, int most,
+                                   cudaStream_t s) {
+    using Sh = AttnShape<E4M3, DP, NT>;
+    const void* kernel = reinterpret_cast<const void*>(k_paged_attention_mma<E4M3, DP, NT>);
+    cudaError_t e = ensure_dynamic_smem(kernel, Sh::kSmem);
+    if (e != cudaSuccess) return e;
+    int ctas = dev.sms * Sh::kPerSm;
+    if (ctas > most) ctas = most;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kAttnThreads);
+    cfg.dynamicSmemBytes = Sh::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, k_paged_attention_mma<E4M3, DP, NT>, a, ws);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <bool E4M3>
+cudaError_t launch_attention_type(const AttentionArgs& a, const DeviceInfo& dev, const Workspace& ws, int most,
+                                  cudaStream_t s) {
+    const bool wide = a.q_heads / a.cache.heads > 8;
+    switch ((a.cache.dim + 63) / 64) {
+        case 1: return wide ? launch_attention_shape<E4M3, 64, 2>(a, dev, ws, most, s) : launch_attention_shape<E4M3, 64, 1>(a, dev, ws, most, s);
+        case 2: return wide ? launch_attention_shape<E4M3, 128, 2>(a, dev, ws, most, s) : launch_attention_shape<E4M3, 128, 1>(a, dev, ws, most, s);
+        case 3: return wide ? launch_attention_shape<E4M3, 192, 2>(a, dev, ws, most, s) : launch_attention_shape<E4M3, 192, 1>(a, dev, ws, most, s);
+        default: return wide ? launch_attention_shape<E4M3, 256, 2>(a, dev, ws, most, s) : launch_attention_shape<E4M3, 256, 1>(a, dev, ws, most, s);
+    }
+}
+
+}  // namespace
+}  // namespace w4a16
