@@ -589,8 +589,8 @@ W4A16_API size_t w4a16_paged_attention_workspace_bytes(int q_heads, int kv_heads
  *   left out and W4A16_DEVERR_SLOT set, as for a length above columns * page
  *   (a negative one counts as 0).
  *   workspace: >= w4a16_paged_attention_workspace_bytes(...) bytes, 16-byte
- *   aligned, zero before its first call; each call leaves it so.  Calls that
- *   may overlap need one each.
+ *   aligned; its contents need no initialisation.  Calls that may overlap
+ *   need one each.
  * Limits: q_heads a multiple of cache->heads, B * q_heads < 2^24.
  */
 W4A16_API w4a16_status w4a16_paged_attention(const uint16_t* q, int64_t q_request, int64_t q_head,

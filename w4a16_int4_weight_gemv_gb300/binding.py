@@ -694,9 +694,9 @@ def w4a16_rope_append(q, k, v, positions, inv_freq, slots, cache: PagedCache, se
 
 def paged_attention_workspace(cache: PagedCache, q_heads: int) -> torch.Tensor:
     """Workspace of w4a16_paged_attention for this cache and number of query
-    heads: zeroed once here, left zero where it has to be by every call."""
+    heads (its contents need no initialisation)."""
     n = int(load_library().w4a16_paged_attention_workspace_bytes(q_heads, cache.heads, cache.dim))
-    return torch.zeros(max(n, 16), dtype=torch.uint8, device=cache.k.device)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=cache.k.device)
 
 
 def w4a16_paged_attention(q, cache: PagedCache, block_table, kv_len, scale: float = None, window: int = 0,

@@ -1,31 +1,128 @@
-// w4a16_paged_attention: workspace layout and choice of the kernel.
-#include "paged.h"
+// w4a16_paged_attention: workspace, the two launches, and the second of them,
+// which joins the rows that several CTAs of the first one share.
+//
+// Parts (m, l, o) of disjoint token sets join as
+//     M = max m_i,  L = sum l_i 2^(m_i - M),  O = sum o_i 2^(m_i - M),  out = O / L.
+// A CTA takes some heads of one row: its threads take four dims of a head
+// each, in groups that take every n-th part, so that all of a row's parts are
+// requested at once; the groups are joined in shared memory.  It is launched
+// while the first launch runs and waits for its end, so it costs the latency
+// of three dependent reads, and nothing but that where no row was split.
+#include "common.cuh"
+#include "paged_attention.h"
 
 namespace w4a16 {
-
-// paged_attention_bf16.cu, paged_attention_e4m3.cu
-cudaError_t launch_attention_bf16(const AttentionArgs& a, const DeviceInfo& dev, uint32_t* arrived, float* part, int most,
-                                  cudaStream_t s);
-cudaError_t launch_attention_e4m3(const AttentionArgs& a, const DeviceInfo& dev, uint32_t* arrived, float* part, int most,
-                                  cudaStream_t s);
-
 namespace {
-constexpr int kMostCtas = 320;  // of a launch: two on each of 152 SMs, rounded up
-constexpr size_t kCounterBytes = kMostCtas * sizeof(uint32_t);
+
+constexpr int kThreads = 512;
+constexpr int kDepth = 4;  // parts a thread requests together
+
+struct Sum {
+    float top, all;
+    float4 v;
+};
+
+// adds the part (m, l, o) to s
+__device__ __forceinline__ void add_part(Sum& s, float m, float l, const float4& o) {
+    if (l == 0.f) return;
+    const float t = fmaxf(s.top, m);
+    const float f0 = s.top == t ? 1.f : exp2f(s.top - t), f1 = m == t ? 1.f : exp2f(m - t);
+    s.top = t;
+    s.all = s.all * f0 + l * f1;
+    s.v.x = s.v.x * f0 + o.x * f1, s.v.y = s.v.y * f0 + o.y * f1;
+    s.v.z = s.v.z * f0 + o.z * f1, s.v.w = s.v.w * f0 + o.w * f1;
+}
+
+__global__ void __launch_bounds__(kThreads) k_attention_join(const AttentionArgs a, const JoinPlan j) {
+    __shared__ Sum sums[kThreads];
+    grid_dependents_launch();
+    grid_dependency_wait();
+    const int4 d = __ldcg(j.joins + blockIdx.x);
+    const int b = d.x, row = d.y, first = d.z, last = d.w;
+    if (b < 0) return;
+    const int G = a.q_heads / a.cache.heads, lanes = a.cache.dim / 4;
+    const int chunks = j.rows / a.cache.heads;
+    const int hk = row / chunks, chunk = row - hk * chunks;
+    const int head0 = hk * G + chunk * j.heads, heads = min(j.heads, G - chunk * j.heads);
+    const bool e4m3 = a.cache.dtype == W4A16_CACHE_E4M3;
+    const int each = (heads + static_cast<int>(gridDim.y) - 1) / static_cast<int>(gridDim.y);
+    const int h_begin = blockIdx.y * each, h_end = min(heads, h_begin + each);
+    const int items = (h_end - h_begin) * lanes;
+    if (items <= 0) return;
+    const int width = min(items, kThreads), groups = kThreads / width;
+    const int group = threadIdx.x / width, lane = threadIdx.x - group * width;
+    const int64_t size = static_cast<int64_t>(j.heads) * (j.padded + 2);
+    for (int base = 0; base < items; base += width) {
+        const int item = base + lane;
+        const bool mine = group < groups && item < items;
+        const int h = h_begin + item / lanes, dim = (item % lanes) * 4;
+        Sum s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        if (mine) {
+            for (int q = first + group; q <= last; q += groups * kDepth) {
+                float m[kDepth], l[kDepth];
+                float4 o[kDepth];
+#pragma unroll
+                for (int i = 0; i < kDepth; ++i) {
+                    const int p = min(q + i * groups, last);
+                    const float* part = j.part + (static_cast<int64_t>(p) * 2 + (p == first ? 1 : 0)) * size;
+                    o[i] = __ldcg(reinterpret_cast<const float4*>(part + h * j.padded + dim));
+                    m[i] = __ldcg(part + j.heads * j.padded + h);
+                    l[i] = q + i * groups <= last ? __ldcg(part + j.heads * (j.padded + 1) + h) : 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < kDepth; ++i) add_part(s, m[i], l[i], o[i]);
+            }
+        }
+        sums[threadIdx.x] = s;
+        __syncthreads();
+        if (mine && group == 0) {
+            for (int g = 1; g < groups; ++g) {
+                const Sum& x = sums[g * width + lane];
+                add_part(s, x.top, x.all, x.v);
+            }
+            const float f = s.all != 0.f ? (e4m3 ? a.cache.v_scale[hk] : 1.f) / s.all : 0.f;
+            const uint32_t lo = f32_to_bf16_rn(s.v.x * f) | (static_cast<uint32_t>(f32_to_bf16_rn(s.v.y * f)) << 16);
+            const uint32_t hi = f32_to_bf16_rn(s.v.z * f) | (static_cast<uint32_t>(f32_to_bf16_rn(s.v.w * f)) << 16);
+            *reinterpret_cast<uint2*>(a.out + b * a.out_request + (head0 + h) * a.out_head + dim) = make_uint2(lo, hi);
+            if (dim == 0 && a.lse)
+                a.lse[static_cast<int64_t>(b) * a.q_heads + head0 + h] =
+                    s.all != 0.f ? (s.top + (log2f(s.all) - (e4m3 ? kE4m3Bias : 0.f))) * 0.6931471805599453f : -INFINITY;
+        }
+        __syncthreads();
+    }
+}
+
 }  // namespace
 
-// A counter per CTA, then two partial rows per CTA: o [heads][dim], m, l.
 size_t paged_attention_workspace(int q_heads, int kv_heads, int dim) {
     const int heads = q_heads / kv_heads > 8 ? 16 : 8;
     const int padded = (dim + 63) / 64 * 64;
-    return kCounterBytes + static_cast<size_t>(kMostCtas) * 2 * heads * (padded + 2) * sizeof(float);
+    return kMostAttnCtas * sizeof(int4) +
+           static_cast<size_t>(kMostAttnCtas) * 2 * heads * (padded + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_attention(const AttentionArgs& a, const DeviceInfo& dev, cudaStream_t s) {
-    uint32_t* arrived = static_cast<uint32_t*>(a.workspace);
-    float* part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kCounterBytes);
-    return a.cache.dtype == W4A16_CACHE_BF16 ? launch_attention_bf16(a, dev, arrived, part, kMostCtas, s)
-                                             : launch_attention_e4m3(a, dev, arrived, part, kMostCtas, s);
+    JoinPlan join{};
+    join.joins = static_cast<int4*>(a.workspace);
+    join.part = reinterpret_cast<float*>(join.joins + kMostAttnCtas);
+    cudaError_t e = a.cache.dtype == W4A16_CACHE_BF16 ? launch_attention_bf16(a, dev, join, s)
+                                                      : launch_attention_e4m3(a, dev, join, s);
+    if (e != cudaSuccess) return e;
+    const int places = join.by_row ? a.B * join.rows : join.ctas;
+    int slices = 2 * dev.sms / places;  // few rows: their heads over several CTAs
+    if (slices > join.heads) slices = join.heads;
+    if (slices < 1) slices = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(places, slices);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, k_attention_join, a, join);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace w4a16

@@ -3,9 +3,8 @@
 
 namespace w4a16 {
 
-cudaError_t launch_attention_bf16(const AttentionArgs& a, const DeviceInfo& dev, uint32_t* arrived, float* part, int most,
-                                  cudaStream_t s) {
-    return launch_attention_type<false>(a, dev, Workspace{arrived, part}, most, s);
+cudaError_t launch_attention_bf16(const AttentionArgs& a, const DeviceInfo& dev, JoinPlan& join, cudaStream_t s) {
+    return launch_attention_type<false>(a, dev, join, s);
 }
 
 }  // namespace w4a16

@@ -28,7 +28,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
-#include "paged.h"
+#include "paged_attention.h"
 
 namespace w4a16 {
 namespace {
@@ -137,26 +137,17 @@ struct Segment {
     Request q;
 };
 
-// Partials of rows that several CTAs share: two places per CTA (0: the row
-// its share begins inside of, 1: the row its share ends inside of), and a
-// counter per CTA for the row that begins in it.
-struct Workspace {
-    uint32_t* arrived;
-    float* part;  // [cta][2][heads * (DP + 2)]: o [heads][DP], then m, then l
-};
-
 template <bool E4M3, int DP, int NT>
-__global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const AttentionArgs a, const Workspace ws) {
+__global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const AttentionArgs a, const JoinPlan ws) {
     using Sh = AttnShape<E4M3, DP, NT>;
     constexpr int CH = Sh::kChunks, S = Sh::kStages, HEADS = Sh::kHeads;
     constexpr int kPart = HEADS * (DP + 2);
-    constexpr float kBias = E4M3 ? 15.f : 0.f;  // p up to 2^15: fp16 then holds p down to 2^-39 of the largest
+    constexpr float kBias = E4M3 ? kE4m3Bias : 0.f;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t tile_mask[kAttnWarps][S];
     __shared__ int64_t scan_sum[kAttnWarps];
     __shared__ int64_t found_before;
     __shared__ int found_b;
-    __shared__ uint32_t arrived_before;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane >> 2, c = lane & 3;
     const uint32_t ring = smem_addr(smem) + warp * S * Sh::kStageBytes;
@@ -169,13 +160,13 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
     const int real_chunks = D * (E4M3 ? 1 : 2) / 16;
     bool bad = false;
 
-    grid_dependents_launch();
     if (D != DP) {  // columns past dim are never copied: zero them once
         for (int i = threadIdx.x; i < kAttnWarps * S * Sh::kStageBytes / 16; i += kAttnThreads)
             reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
     }
     grid_dependency_wait();
+    grid_dependents_launch();
 
     // --- the share of this CTA ---------------------------------------------
     int64_t sum = 0;
@@ -203,10 +194,13 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
         if (a.lse)
             for (int h = threadIdx.x; h < a.q_heads; h += kAttnThreads)
                 a.lse[static_cast<int64_t>(b) * a.q_heads + h] = -INFINITY;
+        if (ws.by_row)
+            for (int i = threadIdx.x; i < rows; i += kAttnThreads) ws.joins[b * rows + i] = make_int4(-1, 0, 0, 0);
     }
     const int64_t want = (total + kMinTiles - 1) / kMinTiles;
     const int ctas = want < gridDim.x ? static_cast<int>(want) : static_cast<int>(gridDim.x);
     if (static_cast<int>(blockIdx.x) >= ctas) {
+        if (!ws.by_row && threadIdx.x == 0) ws.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
         if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
         return;
     }
@@ -564,39 +558,15 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
                 }
             }
         }
-        if (!whole) {
-            // --- join the CTAs of the row: the last one to arrive does it ----
-            const int64_t first_tile = u1 - seg.left - (seg.t1 - seg.t0) - seg.t0;  // the row's first tile of all
-            const int first = static_cast<int>(((first_tile + 1) * ctas - 1) / total);
+        // a row that begins here: what the join launch has to do for it
+        if (threadIdx.x == 0 && seg.t0 == 0 && (ws.by_row || seg.left == 0)) {
+            const int64_t first_tile = u1 - seg.left - seg.t1;  // of all
             const int last = static_cast<int>(((first_tile + seg.q.tiles) * ctas - 1) / total);
-            __threadfence();
-            __syncthreads();
-            if (threadIdx.x == 0) arrived_before = atomicAdd(ws.arrived + first, 1u);
-            __syncthreads();
-            if (arrived_before == static_cast<uint32_t>(last - first)) {
-                __threadfence();
-                for (int i = threadIdx.x; i < heads * (D / 4); i += kAttnThreads) {
-                    const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
-                    const float* p0 = ws.part + (static_cast<int64_t>(first) * 2 + 1) * kPart;
-                    float top = -INFINITY, all = 0.f;
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int q = first; q <= last; ++q) {
-                        const float* p = q == first ? p0 : ws.part + static_cast<int64_t>(q) * 2 * kPart;
-                        const float mq = __ldcg(p + HEADS * DP + h), lq = __ldcg(p + HEADS * (DP + 1) + h);
-                        const float4 x = __ldcg(reinterpret_cast<const float4*>(p + h * DP + d));
-                        if (lq == 0.f) continue;
-                        const float t = fmaxf(top, mq);
-                        const float f0 = top == t ? 1.f : exp2_fast(top - t), f1 = mq == t ? 1.f : exp2_fast(mq - t);
-                        top = t;
-                        all = all * f0 + lq * f1;
-                        v.x = v.x * f0 + x.x * f1, v.y = v.y * f0 + x.y * f1;
-                        v.z = v.z * f0 + x.z * f1, v.w = v.w * f0 + x.w * f1;
-                    }
-                    finish(h, d, v, top, all);
-                }
-                if (threadIdx.x == 0) ws.arrived[first] = 0u;
-            }
+            ws.joins[ws.by_row ? seg.b * rows + seg.row : static_cast<int>(blockIdx.x)] =
+                make_int4(whole ? -1 : seg.b, seg.row, static_cast<int>(blockIdx.x), last);
         }
+        if (threadIdx.x == 0 && seg.t0 != 0 && !ws.by_row && seg.left == 0)
+            ws.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
         __syncthreads();
         if (!next_segment(seg)) break;
     }
@@ -605,14 +575,19 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
 }
 
 template <bool E4M3, int DP, int NT>
-cudaError_t launch_attention_shape(const AttentionArgs& a, const DeviceInfo& dev, const Workspace& ws, int most,
+cudaError_t launch_attention_shape(const AttentionArgs& a, const DeviceInfo& dev, JoinPlan& ws,
                                    cudaStream_t s) {
     using Sh = AttnShape<E4M3, DP, NT>;
     const void* kernel = reinterpret_cast<const void*>(k_paged_attention_mma<E4M3, DP, NT>);
     cudaError_t e = ensure_dynamic_smem(kernel, Sh::kSmem);
     if (e != cudaSuccess) return e;
     int ctas = dev.sms * Sh::kPerSm;
-    if (ctas > most) ctas = most;
+    if (ctas > kMostAttnCtas) ctas = kMostAttnCtas;
+    ws.heads = Sh::kHeads;
+    ws.padded = DP;
+    ws.rows = a.cache.heads * ((a.q_heads / a.cache.heads + Sh::kHeads - 1) / Sh::kHeads);
+    ws.by_row = static_cast<int64_t>(a.B) * ws.rows <= ctas;
+    ws.ctas = ctas;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kAttnThreads);
@@ -628,14 +603,14 @@ cudaError_t launch_attention_shape(const AttentionArgs& a, const DeviceInfo& dev
 }
 
 template <bool E4M3>
-cudaError_t launch_attention_type(const AttentionArgs& a, const DeviceInfo& dev, const Workspace& ws, int most,
+cudaError_t launch_attention_type(const AttentionArgs& a, const DeviceInfo& dev, JoinPlan& ws,
                                   cudaStream_t s) {
     const bool wide = a.q_heads / a.cache.heads > 8;
     switch ((a.cache.dim + 63) / 64) {
-        case 1: return wide ? launch_attention_shape<E4M3, 64, 2>(a, dev, ws, most, s) : launch_attention_shape<E4M3, 64, 1>(a, dev, ws, most, s);
-        case 2: return wide ? launch_attention_shape<E4M3, 128, 2>(a, dev, ws, most, s) : launch_attention_shape<E4M3, 128, 1>(a, dev, ws, most, s);
-        case 3: return wide ? launch_attention_shape<E4M3, 192, 2>(a, dev, ws, most, s) : launch_attention_shape<E4M3, 192, 1>(a, dev, ws, most, s);
-        default: return wide ? launch_attention_shape<E4M3, 256, 2>(a, dev, ws, most, s) : launch_attention_shape<E4M3, 256, 1>(a, dev, ws, most, s);
+        case 1: return wide ? launch_attention_shape<E4M3, 64, 2>(a, dev, ws, s) : launch_attention_shape<E4M3, 64, 1>(a, dev, ws, s);
+        case 2: return wide ? launch_attention_shape<E4M3, 128, 2>(a, dev, ws, s) : launch_attention_shape<E4M3, 128, 1>(a, dev, ws, s);
+        case 3: return wide ? launch_attention_shape<E4M3, 192, 2>(a, dev, ws, s) : launch_attention_shape<E4M3, 192, 1>(a, dev, ws, s);
+        default: return wide ? launch_attention_shape<E4M3, 256, 2>(a, dev, ws, s) : launch_attention_shape<E4M3, 256, 1>(a, dev, ws, s);
     }
 }
 
