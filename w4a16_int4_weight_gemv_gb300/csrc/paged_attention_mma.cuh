@@ -11,13 +11,15 @@
 // Bound by HBM: each key and value is read once, for 2 * heads operations a
 // byte at most.  So the kernel is built around the copies:
 //   - Work is dealt in tiles of 16 tokens, rows one after another, and every
-//     CTA takes an equal consecutive share of all tiles, whatever the lengths
-//     are (each forms the sum of the tile counts itself).  A row that spans
-//     several CTAs is joined by the last of them to finish, in the order of
-//     the CTAs, so the result does not depend on which one that is.
-//   - Inside a CTA each warp takes every fourth tile of a row through a ring
-//     of its own of cp.async stages that runs on across rows; warps meet only
-//     at the end of a row.
+//     warp takes an equal consecutive share of all tiles, whatever the lengths
+//     are (each CTA forms the sum of the tile counts itself; a row counts a
+//     tile more than it has, for its queries and its result).
+//   - A warp works alone, through a ring of its own of cp.async stages that
+//     runs on across rows; a row inside its share it finishes alone.  Only the
+//     two rows at the ends of its share may be others' too: their parts meet
+//     in shared memory once the CTA's warps are done, and what the CTA does
+//     not hold whole goes to the workspace, for a second launch to join
+//     (paged_attention.cu), always in the order of the tokens.
 //   - The products run on the warp MMA with the keys as the 16-row operand
 //     (tokens) and the heads as its 8 columns: one product covers 8 query
 //     heads, and the transposed second product (values^T times p^T) takes the
@@ -36,27 +38,29 @@ namespace {
 constexpr int kTile = 16;  // tokens of a tile: the MMA's rows
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
-constexpr int kMinTiles = 8;  // tiles a CTA takes at least
+constexpr int kRowCost = 1;   // a row's queries and result, in tiles
+constexpr int kMinCost = 4;   // a warp's share at least
 
-// Shared memory: rings of `stages` tiles per warp, and the (m, l, o) of the
-// four warps.  A pitch of DP + 4 floats spreads the fragments' 8 dims x 4
-// head pairs over all banks.
+// Shared memory: a ring of kStages tiles per warp, and a place for the (o) of
+// the row a warp's share begins inside of (the row it ends inside of goes
+// where its ring was).
 template <bool E4M3, int DP, int NT>
 struct AttnShape {
     static constexpr int kHeads = 8 * NT;
     static constexpr int kRowBytes = DP * (E4M3 ? 1 : 2);
-    static constexpr int kChunks = kRowBytes / 16;          // 16-byte chunks of a row
+    static constexpr int kChunks = kRowBytes / 16;             // 16-byte chunks of a row
     static constexpr int kStageBytes = 2 * kTile * kRowBytes;  // keys, then values
-    static constexpr int kPitch = DP + 4;
-    static constexpr int kJoinBytes = kAttnWarps * kHeads * (kPitch + 2) * 4;
+    static constexpr int kPartBytes = kHeads * DP * 4;
+    static constexpr int kJoinBytes = kAttnWarps * kPartBytes;
     // two CTAs an SM with three or more stages where that fits, else one
-    static constexpr int kTwo = (113 * 1024 - kJoinBytes - 512) / (kAttnWarps * kStageBytes);
-    static constexpr int kOne = (226 * 1024 - kJoinBytes - 512) / (kAttnWarps * kStageBytes);
+    static constexpr int kTwo = (112 * 1024 + 512 - kJoinBytes) / (kAttnWarps * kStageBytes);
+    static constexpr int kOne = (225 * 1024 - kJoinBytes) / (kAttnWarps * kStageBytes);
     static constexpr int kPerSm = kTwo >= 3 ? 2 : 1;
     static constexpr int kFit = kPerSm == 2 ? kTwo : kOne;
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
-    static constexpr int kSmem = kAttnWarps * kStages * kStageBytes + kJoinBytes;
-    static_assert(kStages >= 2, "ring too short");
+    static constexpr int kRingBytes = kStages * kStageBytes;  // of a warp
+    static constexpr int kSmem = kAttnWarps * kRingBytes + kJoinBytes;
+    static_assert(kStages >= 2 && kRingBytes >= kPartBytes, "ring too short");
 };
 
 __device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void* src, bool valid) {
@@ -129,50 +133,64 @@ __device__ __forceinline__ Request request_of(const AttentionArgs& a, int b, boo
     return q;
 }
 
-// A run of tiles of one row inside a CTA's share.
+// The tiles [t0, t1) of one row, and where the row begins among all costs.
 struct Segment {
-    int b, row;   // request, and row of the request
-    int t0, t1;   // tiles of the row
-    int64_t left;  // tiles of the share after this segment
+    int64_t at;
+    int b, row, t0, t1;
     Request q;
 };
 
+// float index of (head h, dim d) in a part in shared memory: swizzled so that a
+// fragment's 8 dims x 4 head pairs lie in different banks, four dims together
+template <bool E4M3, int DP>
+__device__ __forceinline__ int part_index(int h, int d) {
+    return h * DP + (d ^ (((h >> 1) & 3) * (E4M3 ? 16 : 8)));
+}
+
 template <bool E4M3, int DP, int NT>
-__global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const AttentionArgs a, const JoinPlan ws) {
+__global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const AttentionArgs a, const JoinPlan jp) {
     using Sh = AttnShape<E4M3, DP, NT>;
-    constexpr int CH = Sh::kChunks, S = Sh::kStages, HEADS = Sh::kHeads;
-    constexpr int kPart = HEADS * (DP + 2);
+    constexpr int CH = Sh::kChunks, S = Sh::kStages, HEADS = Sh::kHeads, KS = DP / 16;
+    constexpr int kBytes = E4M3 ? 1 : 2;
     constexpr float kBias = E4M3 ? kE4m3Bias : 0.f;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint32_t tile_mask[kAttnWarps][S];
     __shared__ int64_t scan_sum[kAttnWarps];
-    __shared__ int64_t found_before;
-    __shared__ int found_b;
+    __shared__ int64_t found_at[kAttnWarps];  // costs before the request of a warp's first tile
+    __shared__ int found_b[kAttnWarps];
+    __shared__ uint32_t tile_mask[kAttnWarps][S];
+    // parts of a warp: 0 of the row its share begins inside of, 1 of the one it ends inside of
+    __shared__ int64_t part_at[kAttnWarps * 2];
+    __shared__ int part_b[kAttnWarps * 2], part_row[kAttnWarps * 2], part_ends[kAttnWarps * 2], part_tiles[kAttnWarps * 2];
+    __shared__ float part_m[kAttnWarps * 2][HEADS], part_l[kAttnWarps * 2][HEADS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane >> 2, c = lane & 3;
-    const uint32_t ring = smem_addr(smem) + warp * S * Sh::kStageBytes;
-    float* join = reinterpret_cast<float*>(smem + kAttnWarps * S * Sh::kStageBytes);
-    float* join_m = join + kAttnWarps * HEADS * Sh::kPitch;
-    float* join_l = join_m + kAttnWarps * HEADS;
+    const uint32_t ring = smem_addr(smem) + warp * Sh::kRingBytes;
+    auto part_of = [&](int i) -> float* {
+        return reinterpret_cast<float*>(smem + ((i & 1) ? (i >> 1) * Sh::kRingBytes
+                                                        : kAttnWarps * Sh::kRingBytes + (i >> 1) * Sh::kPartBytes));
+    };
     const int D = a.cache.dim, G = a.q_heads / a.cache.heads;
     const int chunks_of_group = (G + HEADS - 1) / HEADS;
-    const int rows = a.cache.heads * chunks_of_group;  // of a request
-    const int real_chunks = D * (E4M3 ? 1 : 2) / 16;
+    const int rows = jp.rows;  // of a request
+    const int real_chunks = D * kBytes / 16;
     bool bad = false;
 
     if (D != DP) {  // columns past dim are never copied: zero them once
-        for (int i = threadIdx.x; i < kAttnWarps * S * Sh::kStageBytes / 16; i += kAttnThreads)
+        for (int i = threadIdx.x; i < kAttnWarps * Sh::kRingBytes / 16; i += kAttnThreads)
             reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
-        __syncthreads();
     }
+    if (threadIdx.x < kAttnWarps * 2) part_b[threadIdx.x] = -1;
     grid_dependency_wait();
     grid_dependents_launch();
 
-    // --- the share of this CTA ---------------------------------------------
-    int64_t sum = 0;
-    int mine = 0;  // tiles of request threadIdx.x
-    for (int b = threadIdx.x; b < a.B; b += kAttnThreads) {
+    // --- the share of each warp ---------------------------------------------
+    auto cost_of = [&](int b) -> int64_t {
         const int n = request_of(a, b, bad).tiles;
+        return n ? static_cast<int64_t>(n + kRowCost) * rows : 0;
+    };
+    int64_t sum = 0, mine = 0;  // mine: of request threadIdx.x
+    for (int b = threadIdx.x; b < a.B; b += kAttnThreads) {
+        const int64_t n = cost_of(b);
         if (b < kAttnThreads) mine = n;
         sum += n;
     }
@@ -183,7 +201,6 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
     int64_t total = 0;
 #pragma unroll
     for (int w = 0; w < kAttnWarps; ++w) total += scan_sum[w];
-    total *= rows;
     // requests without tokens
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         if (request_of(a, b, bad).tiles > 0) continue;
@@ -194,23 +211,27 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
         if (a.lse)
             for (int h = threadIdx.x; h < a.q_heads; h += kAttnThreads)
                 a.lse[static_cast<int64_t>(b) * a.q_heads + h] = -INFINITY;
-        if (ws.by_row)
-            for (int i = threadIdx.x; i < rows; i += kAttnThreads) ws.joins[b * rows + i] = make_int4(-1, 0, 0, 0);
+        if (jp.by_row)
+            for (int i = threadIdx.x; i < rows; i += kAttnThreads) jp.joins[b * rows + i] = make_int4(-1, 0, 0, 0);
     }
-    const int64_t want = (total + kMinTiles - 1) / kMinTiles;
-    const int ctas = want < gridDim.x ? static_cast<int>(want) : static_cast<int>(gridDim.x);
+    const int64_t want = (total + kMinCost * kAttnWarps - 1) / (kMinCost * kAttnWarps);
+    int ctas = want < gridDim.x ? static_cast<int>(want) : static_cast<int>(gridDim.x);
+    // one request: rows of one length, so a multiple of them splits none unevenly
+    if (a.B == 1 && ctas > rows) ctas -= ctas % rows;
     if (static_cast<int>(blockIdx.x) >= ctas) {
-        if (!ws.by_row && threadIdx.x == 0) ws.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        if (!jp.by_row && threadIdx.x == 0) jp.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
         if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
         return;
     }
-    const int64_t u0 = blockIdx.x * total / ctas, u1 = (blockIdx.x + 1) * total / ctas;
-    // the request that tile u0 of all belongs to, and the tiles before it
+    const int64_t workers = static_cast<int64_t>(ctas) * kAttnWarps, worker0 = static_cast<int64_t>(blockIdx.x) * kAttnWarps;
+    const int64_t u0 = (worker0 + warp) * total / workers, u1 = (worker0 + warp + 1) * total / workers;
+    auto cta_of = [&](int64_t u) { return static_cast<int>(((u + 1) * workers - 1) / total / kAttnWarps); };
+    // the requests that the warps' first costs belong to
     int64_t before = 0;
+    const int64_t last_u0 = (worker0 + kAttnWarps - 1) * total / workers;
     for (int base = 0; base < a.B; base += kAttnThreads) {
         const int b = base + static_cast<int>(threadIdx.x);
-        const int64_t n = base == 0 ? static_cast<int64_t>(mine) * rows
-                                    : (b < a.B ? static_cast<int64_t>(request_of(a, b, bad).tiles) * rows : 0);
+        const int64_t n = base == 0 ? mine : (b < a.B ? cost_of(b) : 0);
         int64_t inc = n;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -227,22 +248,27 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
             chunk += scan_sum[w];
         }
         start += inc - n;
-        if (u0 >= start && u0 < start + n) {
-            found_b = b;
-            found_before = start;
+        for (int w = 0; w < kAttnWarps; ++w) {
+            const int64_t u = (worker0 + w) * total / workers;
+            if (u >= start && u < start + n) {
+                found_b[w] = b;
+                found_at[w] = start;
+            }
         }
         before += chunk;
-        if (before > u0) break;
+        if (before > last_u0) break;
     }
     __syncthreads();
 
-    // --- tiles, in order ---------------------------------------------------
-    auto open_segment = [&](Segment& s, int64_t left) {
-        s.t1 = left < s.q.tiles - s.t0 ? s.t0 + static_cast<int>(left) : s.q.tiles;
-        s.left = left - (s.t1 - s.t0);
+    // --- the rows of a share, in order ---------------------------------------
+    auto open_segment = [&](Segment& s) {
+        const int64_t first = s.at + kRowCost;  // of the row's tiles
+        s.t0 = u0 > first ? static_cast<int>(u0 - first) : 0;
+        s.t1 = u1 - first < s.q.tiles ? static_cast<int>(u1 - first) : s.q.tiles;  // at most t0: nothing
     };
     auto next_segment = [&](Segment& s) -> bool {
-        if (s.left == 0) return false;
+        s.at += s.q.tiles + kRowCost;
+        if (s.at + kRowCost >= u1) return false;
         if (++s.row == rows) {
             s.row = 0;
             do {
@@ -250,31 +276,29 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
                 s.q = request_of(a, s.b, bad);
             } while (s.q.tiles == 0);
         }
-        s.t0 = 0;
-        open_segment(s, s.left);
+        open_segment(s);
         return true;
     };
     Segment seg;
-    seg.b = found_b;
+    seg.b = found_b[warp];
     seg.q = request_of(a, seg.b, bad);
-    {
-        const int64_t in = u0 - found_before;
-        seg.row = static_cast<int>(in / seg.q.tiles);
-        seg.t0 = static_cast<int>(in - static_cast<int64_t>(seg.row) * seg.q.tiles);
-    }
-    open_segment(seg, u1 - u0);
+    seg.row = static_cast<int>((u0 - found_at[warp]) / (seg.q.tiles + kRowCost));
+    seg.at = found_at[warp] + static_cast<int64_t>(seg.row) * (seg.q.tiles + kRowCost);
+    open_segment(seg);
+    bool live = seg.t1 > seg.t0;
 
     // The copies run ahead of the products: `ahead` is the segment of the next
-    // tile to copy, `ahead_t` the tile, ahead_id this lane's block id for it
+    // tile to copy, ahead_t the tile, ahead_id this lane's block id for it
     // (lane i and lane i + 16: token i), loaded one tile early.
     Segment ahead = seg;
-    int ahead_t = seg.t0 + warp;
-    bool more = true;
+    int ahead_t = seg.t0;
+    bool more = live;
     int ahead_id = -1, ahead_place = 0;
+    const bool aligned_pages = a.cache.page % kTile == 0;  // a tile lies in one block
     auto settle = [&]() {
-        while (more && ahead_t >= ahead.t1) {
+        if (more && ahead_t >= ahead.t1) {
             more = next_segment(ahead);
-            ahead_t = ahead.t0 + warp;
+            ahead_t = ahead.t0;
         }
         if (!more) return;
         const int token = (ahead.q.tile0 + ahead_t) * kTile + (lane & 15);
@@ -286,33 +310,52 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
             if (ahead_id < 0) ahead_id = -2;
         }
     };
-    constexpr int kBytes = E4M3 ? 1 : 2;
     auto copy_tile = [&](int slot) {
         if (more) {
             const bool valid = ahead_id >= 0 && ahead_id < a.cache.blocks;
             bad |= ahead_id != -1 && !valid;
             const uint32_t mask = __ballot_sync(0xFFFFFFFFu, valid) & 0xFFFFu;
             if (lane == 0) tile_mask[warp][slot] = mask;
-            const int64_t id = valid ? ahead_id : 0, place = valid ? ahead_place : 0;
             const int hk = ahead.row / chunks_of_group;
-            const int64_t ko = id * a.cache.k_block + place * a.cache.k_token;
-            const int64_t vo = id * a.cache.v_block + place * a.cache.v_token;
             const char* kp = static_cast<const char*>(a.cache.k) + hk * a.cache.k_head * kBytes;
             const char* vp = static_cast<const char*>(a.cache.v) + hk * a.cache.v_head * kBytes;
             const uint32_t dst = ring + slot * Sh::kStageBytes;
+            if (aligned_pages) {
+                // one block for all sixteen tokens: any valid lane has its id and the first place
+                const int from = mask ? __ffs(mask) - 1 : 0;
+                const int64_t id = mask ? __shfl_sync(0xFFFFFFFFu, ahead_id, from) : 0;
+                const int place = __shfl_sync(0xFFFFFFFFu, ahead_place, 0);
+                kp += (id * a.cache.k_block + place * a.cache.k_token) * kBytes;
+                vp += (id * a.cache.v_block + place * a.cache.v_token) * kBytes;
+                const int64_t kt = a.cache.k_token * kBytes, vt = a.cache.v_token * kBytes;
 #pragma unroll
-            for (int i = 0; i < kTile * CH / 32; ++i) {
-                const int row = (i * 32 + lane) / CH, ch = (i * 32 + lane) % CH;
-                const int64_t kr = __shfl_sync(0xFFFFFFFFu, ko, row);
-                const int64_t vr = __shfl_sync(0xFFFFFFFFu, vo, row);
-                const bool ok = (mask >> row) & 1u;
-                if (ch < real_chunks) {
-                    const uint32_t at = dst + tile_offset<CH>(row, ch);
-                    cp_async_16_zfill(at, kp + kr * kBytes + ch * 16, ok);
-                    cp_async_16_zfill(at + kTile * Sh::kRowBytes, vp + vr * kBytes + ch * 16, ok);
+                for (int i = 0; i < kTile * CH / 32; ++i) {
+                    const int row = (i * 32 + lane) / CH, ch = (i * 32 + lane) % CH;
+                    const bool ok = (mask >> row) & 1u;
+                    if (ch < real_chunks) {
+                        const uint32_t at = dst + tile_offset<CH>(row, ch);
+                        cp_async_16_zfill(at, kp + row * kt + ch * 16, ok);
+                        cp_async_16_zfill(at + kTile * Sh::kRowBytes, vp + row * vt + ch * 16, ok);
+                    }
+                }
+            } else {
+                const int64_t id = valid ? ahead_id : 0, place = valid ? ahead_place : 0;
+                const int64_t ko = (id * a.cache.k_block + place * a.cache.k_token) * kBytes;
+                const int64_t vo = (id * a.cache.v_block + place * a.cache.v_token) * kBytes;
+#pragma unroll
+                for (int i = 0; i < kTile * CH / 32; ++i) {
+                    const int row = (i * 32 + lane) / CH, ch = (i * 32 + lane) % CH;
+                    const int64_t kr = __shfl_sync(0xFFFFFFFFu, ko, row);
+                    const int64_t vr = __shfl_sync(0xFFFFFFFFu, vo, row);
+                    const bool ok = (mask >> row) & 1u;
+                    if (ch < real_chunks) {
+                        const uint32_t at = dst + tile_offset<CH>(row, ch);
+                        cp_async_16_zfill(at, kp + kr + ch * 16, ok);
+                        cp_async_16_zfill(at + kTile * Sh::kRowBytes, vp + vr + ch * 16, ok);
+                    }
                 }
             }
-            ahead_t += kAttnWarps;
+            ++ahead_t;
             settle();
         }
         cp_async_commit();
@@ -323,21 +366,21 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
     for (int i = 0; i < S - 1; ++i) copy_tile(i);
 
     int slot = 0;
-    while (true) {
+    while (live) {
         // queries of the row, as B fragments (columns: heads)
         const int hk = seg.row / chunks_of_group, chunk = seg.row - hk * chunks_of_group;
-        const int head0 = hk * G + chunk * HEADS;           // first query head of the row
+        const int head0 = hk * G + chunk * HEADS;  // first query head of the row
         const int heads = min(HEADS, G - chunk * HEADS);
-        uint32_t qf[NT][DP / 16][2];
+        uint32_t qf[NT][KS][2];
         float sl[NT][2];  // score scale of columns 2c, 2c + 1
-        float m[NT][2], l[NT][2], o[NT][DP / 16][4];
+        float m[NT][2], l[NT][2], o[NT][KS][4];
         const float base = a.scale * 1.4426950408889634f * (E4M3 ? a.cache.k_scale[hk] : 1.f);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const uint16_t* qp = a.q + seg.b * a.q_request + (head0 + n * 8 + r) * a.q_head;
             const bool have = n * 8 + r < heads;
 #pragma unroll
-            for (int k = 0; k < DP / 16; ++k) {
+            for (int k = 0; k < KS; ++k) {
                 qf[n][k][0] = qf[n][k][1] = 0u;
                 if (have && k * 16 < D) {
                     // bf16: dims 2c, 2c + 1 and 8 further; e4m3: the four dims whose codes one word holds
@@ -351,7 +394,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
                 // to fp16, scaled by a power of two that takes the head's largest into [2^14, 2^15)
                 uint32_t big = 0u;
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
+                for (int k = 0; k < KS; ++k)
                     big = __vmaxu2(big, __vmaxu2(qf[n][k][0] & 0x7FFF7FFFu, qf[n][k][1] & 0x7FFF7FFFu));
                 big = max(big & 0xFFFFu, big >> 16);
                 big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
@@ -360,7 +403,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
                 const int sh = min(141 - eb, 126);
                 const float up = exp2i(sh), down = exp2i(-sh);
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
+                for (int k = 0; k < KS; ++k)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const uint32_t v = qf[n][k][e];
@@ -376,12 +419,12 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
                 l[n][e] = 0.f;
             }
 #pragma unroll
-            for (int k = 0; k < DP / 16; ++k)
+            for (int k = 0; k < KS; ++k)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[n][k][e] = 0.f;
         }
 
-        for (int t = seg.t0 + warp; t < seg.t1; t += kAttnWarps) {
+        for (int t = seg.t0; t < seg.t1; ++t) {
             cp_async_wait_group<S - 2>();
             __syncwarp();
             copy_tile(slot == 0 ? S - 1 : slot - 1);
@@ -396,7 +439,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
                 for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
             if (!E4M3) {
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k) {
+                for (int k = 0; k < KS; ++k) {
                     uint32_t f[4];
                     ldmatrix_x4(f, kt + tile_offset<CH>(lane & 15, 2 * k + (lane >> 4)));
 #pragma unroll
@@ -404,7 +447,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
                 }
             } else {
 #pragma unroll
-                for (int k = 0; k < DP / 16; k += 2) {
+                for (int k = 0; k < KS; k += 2) {
                     uint32_t f[4];  // two chunks of 16 codes: rows r and r + 8 of each
                     ldmatrix_x4(f, kt + tile_offset<CH>(lane & 15, k + (lane >> 4)));
 #pragma unroll
@@ -444,7 +487,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
                         l[n][e] *= keep[e];
                     }
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k)
+                    for (int k = 0; k < KS; ++k)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[n][k][e] *= keep[e & 1];
                 }
@@ -469,7 +512,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
             }
             if (!E4M3) {
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k) {
+                for (int k = 0; k < KS; ++k) {
                     uint32_t f[4];
                     ldmatrix_x4_trans(f, vt + tile_offset<CH>((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
 #pragma unroll
@@ -477,7 +520,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
                 }
             } else {
 #pragma unroll
-                for (int k = 0; k < DP / 16; k += 2) {
+                for (int k = 0; k < KS; k += 2) {
                     uint32_t f[4];  // chunk k: tokens 0..7, 8..15, then chunk k + 1
                     ldmatrix_x4_trans(f, vt + tile_offset<CH>(lane & 15, k + (lane >> 4)));
 #pragma unroll
@@ -495,82 +538,142 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
             }
         }
 
-        // --- join the warps --------------------------------------------------
+        // --- the result of the segment ---------------------------------------
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 4);
                 l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 8);
                 l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 16);
-                const int h = warp * HEADS + n * 8 + 2 * c + e;
-                if (r == 0) {
-                    join_m[h] = m[n][e];
-                    join_l[h] = l[n][e];
-                }
+            }
+        const bool begins = seg.t0 == 0, ends = seg.t1 == seg.q.tiles;
+        if (begins && ends) {
+            const float vs = E4M3 ? a.cache.v_scale[hk] : 1.f;
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k) {
-                    // e4m3: rows r and r + 8 of the product are dims 2r and 2r + 1
-                    float* p = join + h * Sh::kPitch + k * 16;
-                    p[E4M3 ? 2 * r : r] = o[n][k][e];
-                    p[E4M3 ? 2 * r + 1 : r + 8] = o[n][k][2 + e];
+            for (int n = 0; n < NT; ++n) {
+                float f[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    f[e] = l[n][e] != 0.f ? vs / l[n][e] : 0.f;
+                    const int h = n * 8 + 2 * c + e;
+                    if (a.lse && r == 0 && h < heads)
+                        a.lse[static_cast<int64_t>(seg.b) * a.q_heads + head0 + h] =
+                            l[n][e] != 0.f ? (m[n][e] + (log2f(l[n][e]) - kBias)) * 0.6931471805599453f : -INFINITY;
                 }
+                // transposed to dims along the lanes of a head
+                uint16_t* out = a.out + seg.b * a.out_request + (head0 + n * 8 + r) * a.out_head;
+                const bool have = n * 8 + r < heads;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    uint32_t v[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const __nv_bfloat162 p = __floats2bfloat162_rn(o[n][k][2 * e] * f[0], o[n][k][2 * e + 1] * f[1]);
+                        v[e] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&p));
+                    }
+                    if (have && k * 16 < D) {
+                        if (E4M3) {  // rows of the product: even dims, then odd ones
+                            *reinterpret_cast<uint2*>(out + k * 16 + 4 * c) =
+                                make_uint2(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[0], v[1], 0x7632));
+                        } else {
+                            *reinterpret_cast<uint32_t*>(out + k * 16 + 2 * c) = v[0];
+                            *reinterpret_cast<uint32_t*>(out + k * 16 + 8 + 2 * c) = v[1];
+                        }
+                    }
+                }
+            }
+            if (jp.by_row && lane == 0) jp.joins[seg.b * rows + seg.row] = make_int4(-1, 0, 0, 0);
+        } else {
+            const int i = warp * 2 + (begins ? 1 : 0);
+            if (begins) {  // the last tiles of the share: the ring is free
+                cp_async_wait_group<0>();
+                __syncwarp();
+            }
+            float* part = part_of(i);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int h = n * 8 + 2 * c + e;
+                    if (r == 0) {
+                        part_m[i][h] = m[n][e];
+                        part_l[i][h] = l[n][e];
+                    }
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) {
+                        if (E4M3) {
+                            *reinterpret_cast<float2*>(part + part_index<E4M3, DP>(h, k * 16 + 2 * r)) =
+                                make_float2(o[n][k][e], o[n][k][2 + e]);
+                        } else {
+                            part[part_index<E4M3, DP>(h, k * 16 + r)] = o[n][k][e];
+                            part[part_index<E4M3, DP>(h, k * 16 + r + 8)] = o[n][k][2 + e];
+                        }
+                    }
+                }
+            if (lane == 0) {
+                part_b[i] = seg.b;
+                part_row[i] = seg.row;
+                part_ends[i] = (begins ? 1 : 0) | (ends ? 2 : 0);
+                part_at[i] = seg.at + kRowCost;
+                part_tiles[i] = seg.q.tiles;
             }
         }
-        __syncthreads();
-        const bool whole = seg.t0 == 0 && seg.t1 == seg.q.tiles;
-        const int place = seg.t0 == 0 ? 1 : 0;
-        float* part = ws.part + (static_cast<int64_t>(blockIdx.x) * 2 + place) * kPart;
-        auto finish = [&](int h, int d, float4 v, float top, float all) {
-            const float f = all != 0.f ? (E4M3 ? a.cache.v_scale[hk] : 1.f) / all : 0.f;
-            const uint32_t lo = f32_to_bf16_rn(v.x * f) | (static_cast<uint32_t>(f32_to_bf16_rn(v.y * f)) << 16);
-            const uint32_t hi = f32_to_bf16_rn(v.z * f) | (static_cast<uint32_t>(f32_to_bf16_rn(v.w * f)) << 16);
-            *reinterpret_cast<uint2*>(a.out + seg.b * a.out_request + (head0 + h) * a.out_head + d) = make_uint2(lo, hi);
-            if (d == 0 && a.lse)
-                a.lse[static_cast<int64_t>(seg.b) * a.q_heads + head0 + h] =
-                    all != 0.f ? (top + (log2f(all) - kBias)) * 0.6931471805599453f : -INFINITY;
-        };
-        for (int i = threadIdx.x; i < heads * (D / 4); i += kAttnThreads) {
-            const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
+        live = next_segment(seg);
+    }
+    cp_async_wait_group<0>();
+    __syncthreads();
+
+    // --- parts of one row, next to one another, become one -------------------
+    if (!jp.by_row && threadIdx.x == 0) jp.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    for (int i = 0; i < kAttnWarps * 2;) {
+        if (part_b[i] < 0) {
+            ++i;
+            continue;
+        }
+        const int b = part_b[i], row = part_row[i], from = i;
+        int flags = 0;
+        for (; i < kAttnWarps * 2 && (part_b[i] < 0 || (part_b[i] == b && part_row[i] == row)); ++i)
+            if (part_b[i] >= 0) flags |= part_ends[i];
+        const int hk = row / chunks_of_group, chunk = row - hk * chunks_of_group;
+        const int head0 = hk * G + chunk * HEADS, heads = min(HEADS, G - chunk * HEADS);
+        const bool whole = flags == 3;
+        float* const to = jp.part + (static_cast<int64_t>(blockIdx.x) * 2 + (flags & 1)) * (HEADS * (DP + 2));
+        for (int item = threadIdx.x; item < heads * (D / 4); item += kAttnThreads) {
+            const int h = item / (D / 4), d = (item - h * (D / 4)) * 4;
             float top = -INFINITY, all = 0.f;
-#pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, join_m[w * HEADS + h]);
+            for (int j = from; j < i; ++j)
+                if (part_b[j] >= 0) top = fmaxf(top, part_m[j][h]);
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) {
-                const float lw = join_l[w * HEADS + h];
-                if (lw != 0.f) {
-                    const float mw = join_m[w * HEADS + h];
-                    const float f = mw == top ? 1.f : exp2_fast(mw - top);
-                    const float4 x = *reinterpret_cast<const float4*>(join + (w * HEADS + h) * Sh::kPitch + d);
-                    all = fmaf(lw, f, all);
-                    v.x = fmaf(x.x, f, v.x), v.y = fmaf(x.y, f, v.y);
-                    v.z = fmaf(x.z, f, v.z), v.w = fmaf(x.w, f, v.w);
-                }
+            for (int j = from; j < i; ++j) {
+                if (part_b[j] < 0 || part_l[j][h] == 0.f) continue;
+                const float mj = part_m[j][h], f = mj == top ? 1.f : exp2_fast(mj - top);
+                const float4 x = *reinterpret_cast<const float4*>(part_of(j) + part_index<E4M3, DP>(h, d));
+                all = fmaf(part_l[j][h], f, all);
+                v.x = fmaf(x.x, f, v.x), v.y = fmaf(x.y, f, v.y);
+                v.z = fmaf(x.z, f, v.z), v.w = fmaf(x.w, f, v.w);
             }
             if (whole) {
-                finish(h, d, v, top, all);
+                const float f = all != 0.f ? (E4M3 ? a.cache.v_scale[hk] : 1.f) / all : 0.f;
+                const uint32_t lo = f32_to_bf16_rn(v.x * f) | (static_cast<uint32_t>(f32_to_bf16_rn(v.y * f)) << 16);
+                const uint32_t hi = f32_to_bf16_rn(v.z * f) | (static_cast<uint32_t>(f32_to_bf16_rn(v.w * f)) << 16);
+                *reinterpret_cast<uint2*>(a.out + b * a.out_request + (head0 + h) * a.out_head + d) = make_uint2(lo, hi);
+                if (d == 0 && a.lse)
+                    a.lse[static_cast<int64_t>(b) * a.q_heads + head0 + h] =
+                        all != 0.f ? (top + (log2f(all) - kBias)) * 0.6931471805599453f : -INFINITY;
             } else {
-                __stcg(reinterpret_cast<float4*>(part + h * DP + d), v);
+                *reinterpret_cast<float4*>(to + h * DP + d) = v;
                 if (d == 0) {
-                    __stcg(part + HEADS * DP + h, top);
-                    __stcg(part + HEADS * (DP + 1) + h, all);
+                    to[HEADS * DP + h] = top;
+                    to[HEADS * (DP + 1) + h] = all;
                 }
             }
         }
         // a row that begins here: what the join launch has to do for it
-        if (threadIdx.x == 0 && seg.t0 == 0 && (ws.by_row || seg.left == 0)) {
-            const int64_t first_tile = u1 - seg.left - seg.t1;  // of all
-            const int last = static_cast<int>(((first_tile + seg.q.tiles) * ctas - 1) / total);
-            ws.joins[ws.by_row ? seg.b * rows + seg.row : static_cast<int>(blockIdx.x)] =
-                make_int4(whole ? -1 : seg.b, seg.row, static_cast<int>(blockIdx.x), last);
-        }
-        if (threadIdx.x == 0 && seg.t0 != 0 && !ws.by_row && seg.left == 0)
-            ws.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
-        __syncthreads();
-        if (!next_segment(seg)) break;
+        if (threadIdx.x == 0 && (flags & 1) && (jp.by_row || !whole))
+            jp.joins[jp.by_row ? b * rows + row : static_cast<int>(blockIdx.x)] =
+                make_int4(whole ? -1 : b, row, static_cast<int>(blockIdx.x), cta_of(part_at[from] + part_tiles[from] - 1));
     }
-    cp_async_wait_group<0>();
     if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
 }
 
