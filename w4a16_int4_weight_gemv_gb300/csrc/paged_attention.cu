@@ -107,7 +107,7 @@ cudaError_t launch_paged_attention(const AttentionArgs& a, const DeviceInfo& dev
     join.part = reinterpret_cast<float*>(join.joins + kMostAttnCtas);
     cudaError_t e = a.cache.dtype == W4A16_CACHE_BF16 ? launch_attention_bf16(a, dev, join, s)
                                                       : launch_attention_e4m3(a, dev, join, s);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || !join.split) return e;
     const int places = join.by_row ? a.B * join.rows : join.ctas;
     int slices = 2 * dev.sms / places;  // few rows: their heads over several CTAs
     if (slices > join.heads) slices = join.heads;

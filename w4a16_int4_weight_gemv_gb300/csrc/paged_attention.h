@@ -22,6 +22,7 @@ struct JoinPlan {
     // place 0: the row that the CTA's share begins inside of, 1: the row it ends inside of
     float* part;
     int by_row;
+    int split;   // rows may span CTAs: the second launch is needed
     int rows;    // of a request: key/value heads times chunks of the query heads sharing one
     int heads;   // query heads of a chunk: 8 or 16
     int padded;  // dim rounded up to 64

@@ -40,6 +40,7 @@ constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
 constexpr int kRowCost = 1;   // a row's queries and result, in tiles
 constexpr int kMinCost = 4;   // a warp's share at least
+constexpr int kWholeTiles = 32;  // rows that cannot be longer are not split over CTAs
 
 // Shared memory: a ring of kStages tiles per warp, and a place for the (o) of
 // the row a warp's share begins inside of (the row it ends inside of goes
@@ -53,14 +54,14 @@ struct AttnShape {
     static constexpr int kPartBytes = kHeads * DP * 4;
     static constexpr int kJoinBytes = kAttnWarps * kPartBytes;
     // two CTAs an SM with three or more stages where that fits, else one
-    static constexpr int kTwo = (112 * 1024 + 512 - kJoinBytes) / (kAttnWarps * kStageBytes);
+    static constexpr int kTwo = (112 * 1024 - kJoinBytes) / (kAttnWarps * kStageBytes);
     static constexpr int kOne = (225 * 1024 - kJoinBytes) / (kAttnWarps * kStageBytes);
     static constexpr int kPerSm = kTwo >= 3 ? 2 : 1;
     static constexpr int kFit = kPerSm == 2 ? kTwo : kOne;
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
     static constexpr int kRingBytes = kStages * kStageBytes;  // of a warp
     static constexpr int kSmem = kAttnWarps * kRingBytes + kJoinBytes;
-    static_assert(kStages >= 2 && kRingBytes >= kPartBytes, "ring too short");
+    static_assert(kStages >= 2 && kRingBytes >= kPartBytes + 3 * 2 * kAttnWarps * kHeads * 4, "ring too short");
 };
 
 __device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void* src, bool valid) {
@@ -94,6 +95,9 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
     uint32_t d;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<uint16_t>(v)));
     return d;
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 template <bool E4M3>
 __device__ __forceinline__ void attn_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -133,6 +137,13 @@ __device__ __forceinline__ Request request_of(const AttentionArgs& a, int b, boo
     return q;
 }
 
+// n / d for n >= 0, d > 0: in 32 bits where both fit, as they do in all but
+// the largest calls (a 64-bit division takes about 200 ns here)
+__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
+    if (((n | d) >> 32) == 0) return static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
+    return n / d;
+}
+
 // The tiles [t0, t1) of one row, and where the row begins among all costs.
 struct Segment {
     int64_t at;
@@ -162,6 +173,11 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
     __shared__ int64_t part_at[kAttnWarps * 2];
     __shared__ int part_b[kAttnWarps * 2], part_row[kAttnWarps * 2], part_ends[kAttnWarps * 2], part_tiles[kAttnWarps * 2];
     __shared__ float part_m[kAttnWarps * 2][HEADS], part_l[kAttnWarps * 2][HEADS];
+    __shared__ uint32_t part_members[kAttnWarps * 2];
+    // once the rings are done, behind the first one's part: a part's factor, and the maximum and sum of its row
+    using PartFloats = float[HEADS];
+    PartFloats* const part_f = reinterpret_cast<PartFloats*>(smem + Sh::kPartBytes);
+    PartFloats *const part_top = part_f + kAttnWarps * 2, *const part_all = part_top + kAttnWarps * 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane >> 2, c = lane & 3;
     const uint32_t ring = smem_addr(smem) + warp * Sh::kRingBytes;
@@ -211,54 +227,78 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
         if (a.lse)
             for (int h = threadIdx.x; h < a.q_heads; h += kAttnThreads)
                 a.lse[static_cast<int64_t>(b) * a.q_heads + h] = -INFINITY;
-        if (jp.by_row)
+        if (jp.split && jp.by_row)
             for (int i = threadIdx.x; i < rows; i += kAttnThreads) jp.joins[b * rows + i] = make_int4(-1, 0, 0, 0);
     }
-    const int64_t want = (total + kMinCost * kAttnWarps - 1) / (kMinCost * kAttnWarps);
+    const int64_t want = quotient(total + kMinCost * kAttnWarps - 1, kMinCost * kAttnWarps);
     int ctas = want < gridDim.x ? static_cast<int>(want) : static_cast<int>(gridDim.x);
     // one request: rows of one length, so a multiple of them splits none unevenly
     if (a.B == 1 && ctas > rows) ctas -= ctas % rows;
     if (static_cast<int>(blockIdx.x) >= ctas) {
-        if (!jp.by_row && threadIdx.x == 0) jp.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        if (jp.split && !jp.by_row && threadIdx.x == 0) jp.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
         if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
         return;
     }
-    const int64_t workers = static_cast<int64_t>(ctas) * kAttnWarps, worker0 = static_cast<int64_t>(blockIdx.x) * kAttnWarps;
-    const int64_t u0 = (worker0 + warp) * total / workers, u1 = (worker0 + warp + 1) * total / workers;
-    auto cta_of = [&](int64_t u) { return static_cast<int>(((u + 1) * workers - 1) / total / kAttnWarps); };
-    // the requests that the warps' first costs belong to
-    int64_t before = 0;
-    const int64_t last_u0 = (worker0 + kAttnWarps - 1) * total / workers;
-    for (int base = 0; base < a.B; base += kAttnThreads) {
-        const int b = base + static_cast<int>(threadIdx.x);
-        const int64_t n = base == 0 ? mine : (b < a.B ? cost_of(b) : 0);
-        int64_t inc = n;
+    // costs before CTA i: equal shares, the remainder to the first ones
+    const int64_t share = quotient(total, ctas), extra = total - share * ctas;
+    auto cta_begin = [&](int i) { return i * share + (i < extra ? i : extra); };
+    auto cta_of = [&](int64_t u) {
+        const int64_t big = extra * (share + 1);
+        return static_cast<int>(u < big ? quotient(u, share + 1) : extra + quotient(u - big, share));
+    };
+    // for each of n places: the request that holds it, and the costs before that
+    auto locate = [&](const int64_t* place, int n) {
+        int64_t before = 0, last = 0;
+        for (int i = 0; i < n; ++i) last = place[i] > last ? place[i] : last;
+        for (int base = 0; base < a.B; base += kAttnThreads) {
+            const int b = base + static_cast<int>(threadIdx.x);
+            const int64_t cost = base == 0 ? mine : (b < a.B ? cost_of(b) : 0);
+            int64_t inc = cost;
 #pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
-            if (lane >= d) inc += v;
-        }
-        __syncthreads();
-        if (lane == 31) scan_sum[warp] = inc;
-        __syncthreads();
-        int64_t start = before, chunk = 0;
-#pragma unroll
-        for (int w = 0; w < kAttnWarps; ++w) {
-            if (w < warp) start += scan_sum[w];
-            chunk += scan_sum[w];
-        }
-        start += inc - n;
-        for (int w = 0; w < kAttnWarps; ++w) {
-            const int64_t u = (worker0 + w) * total / workers;
-            if (u >= start && u < start + n) {
-                found_b[w] = b;
-                found_at[w] = start;
+            for (int d = 1; d < 32; d *= 2) {
+                const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+                if (lane >= d) inc += v;
             }
+            __syncthreads();
+            if (lane == 31) scan_sum[warp] = inc;
+            __syncthreads();
+            int64_t start = before, chunk = 0;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) {
+                if (w < warp) start += scan_sum[w];
+                chunk += scan_sum[w];
+            }
+            start += inc - cost;
+            for (int i = 0; i < n; ++i) {
+                if (place[i] >= start && place[i] < start + cost) {
+                    found_b[i] = b;
+                    found_at[i] = start;
+                }
+            }
+            before += chunk;
+            if (before > last) break;
         }
-        before += chunk;
-        if (before > last_u0) break;
+        __syncthreads();
+    };
+    int64_t begin = cta_begin(blockIdx.x), end = cta_begin(blockIdx.x + 1);
+    if (!jp.split) {
+        // whole rows: from the first that begins in the share to the last that does
+        const int64_t ends[2] = {begin, end};
+        if (threadIdx.x < 2) found_b[threadIdx.x] = -1;
+        locate(ends, 2);
+        auto row_from = [&](int64_t u, int i) -> int64_t {
+            if (found_b[i] < 0) return u;  // past the last request
+            const int n = request_of(a, found_b[i], bad).tiles + kRowCost;
+            return found_at[i] + quotient(u - found_at[i] + n - 1, n) * n;
+        };
+        begin = row_from(begin, 0), end = row_from(end, 1);
+        __syncthreads();
     }
-    __syncthreads();
+    const int64_t places[kAttnWarps] = {begin, begin + (end - begin) / 4, begin + (end - begin) / 2,
+                                        begin + (end - begin) * 3 / 4};
+    static_assert(kAttnWarps == 4, "shares of four warps");
+    locate(places, kAttnWarps);
+    const int64_t u0 = places[warp], u1 = warp + 1 < kAttnWarps ? places[(warp + 1) % kAttnWarps] : end;
 
     // --- the rows of a share, in order ---------------------------------------
     auto open_segment = [&](Segment& s) {
@@ -279,52 +319,62 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
         open_segment(s);
         return true;
     };
-    Segment seg;
-    seg.b = found_b[warp];
-    seg.q = request_of(a, seg.b, bad);
-    seg.row = static_cast<int>((u0 - found_at[warp]) / (seg.q.tiles + kRowCost));
-    seg.at = found_at[warp] + static_cast<int64_t>(seg.row) * (seg.q.tiles + kRowCost);
-    open_segment(seg);
-    bool live = seg.t1 > seg.t0;
+    Segment seg{};
+    bool live = u1 > u0;
+    if (live) {
+        seg.b = found_b[warp];
+        seg.q = request_of(a, seg.b, bad);
+        seg.row = static_cast<int>(quotient(u0 - found_at[warp], seg.q.tiles + kRowCost));
+        seg.at = found_at[warp] + static_cast<int64_t>(seg.row) * (seg.q.tiles + kRowCost);
+        open_segment(seg);
+        live = seg.t1 > seg.t0;
+    }
 
     // The copies run ahead of the products: `ahead` is the segment of the next
-    // tile to copy, ahead_t the tile, ahead_id this lane's block id for it
-    // (lane i and lane i + 16: token i), loaded one tile early.
+    // tile to copy, ahead_t the tile.  Block ids are loaded early: where a tile
+    // lies in one block, those of 32 tiles at once (lane i: tile win_t + i),
+    // else those of the next tile's tokens (lanes i and i + 16: token i).
     Segment ahead = seg;
-    int ahead_t = seg.t0;
+    int ahead_t = seg.t0, win_t = seg.t0 - 32;
     bool more = live;
     int ahead_id = -1, ahead_place = 0;
-    const bool aligned_pages = a.cache.page % kTile == 0;  // a tile lies in one block
+    const bool aligned_pages = a.cache.page % kTile == 0;
     auto settle = [&]() {
         if (more && ahead_t >= ahead.t1) {
             more = next_segment(ahead);
             ahead_t = ahead.t0;
+            win_t = ahead_t - 32;
         }
-        if (!more) return;
-        const int token = (ahead.q.tile0 + ahead_t) * kTile + (lane & 15);
+        if (!more || (aligned_pages && ahead_t < win_t + 32)) return;
+        win_t = ahead_t;
+        const int token = aligned_pages ? (ahead.q.tile0 + ahead_t + lane) * kTile
+                                        : (ahead.q.tile0 + ahead_t) * kTile + (lane & 15);
         const int col = static_cast<int>(static_cast<unsigned>(token) / static_cast<unsigned>(a.cache.page));
         ahead_place = token - col * a.cache.page;
         ahead_id = -1;
-        if (token >= ahead.q.start && token < ahead.q.len) {
+        if (aligned_pages ? ahead_t + lane < ahead.t1 : token >= ahead.q.start && token < ahead.q.len) {
             ahead_id = a.block_table[ahead.b * a.table_stride + col];
             if (ahead_id < 0) ahead_id = -2;
         }
     };
     auto copy_tile = [&](int slot) {
         if (more) {
-            const bool valid = ahead_id >= 0 && ahead_id < a.cache.blocks;
-            bad |= ahead_id != -1 && !valid;
-            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, valid) & 0xFFFFu;
-            if (lane == 0) tile_mask[warp][slot] = mask;
             const int hk = ahead.row / chunks_of_group;
             const char* kp = static_cast<const char*>(a.cache.k) + hk * a.cache.k_head * kBytes;
             const char* vp = static_cast<const char*>(a.cache.v) + hk * a.cache.v_head * kBytes;
             const uint32_t dst = ring + slot * Sh::kStageBytes;
+            uint32_t mask;  // the tokens of the tile that the row sees
             if (aligned_pages) {
-                // one block for all sixteen tokens: any valid lane has its id and the first place
-                const int from = mask ? __ffs(mask) - 1 : 0;
-                const int64_t id = mask ? __shfl_sync(0xFFFFFFFFu, ahead_id, from) : 0;
-                const int place = __shfl_sync(0xFFFFFFFFu, ahead_place, 0);
+                int64_t id = __shfl_sync(0xFFFFFFFFu, ahead_id, ahead_t - win_t);
+                const int place = __shfl_sync(0xFFFFFFFFu, ahead_place, ahead_t - win_t);
+                const int token = (ahead.q.tile0 + ahead_t) * kTile;
+                mask = ahead.q.len - token < kTile ? (1u << (ahead.q.len - token)) - 1u : 0xFFFFu;
+                if (ahead.q.start > token) mask &= 0xFFFFu << (ahead.q.start - token);
+                if (id < 0 || id >= a.cache.blocks) {
+                    bad = true;
+                    mask = 0u;
+                    id = 0;
+                }
                 kp += (id * a.cache.k_block + place * a.cache.k_token) * kBytes;
                 vp += (id * a.cache.v_block + place * a.cache.v_token) * kBytes;
                 const int64_t kt = a.cache.k_token * kBytes, vt = a.cache.v_token * kBytes;
@@ -339,6 +389,9 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
                     }
                 }
             } else {
+                const bool valid = ahead_id >= 0 && ahead_id < a.cache.blocks;
+                bad |= ahead_id != -1 && !valid;
+                mask = __ballot_sync(0xFFFFFFFFu, valid) & 0xFFFFu;
                 const int64_t id = valid ? ahead_id : 0, place = valid ? ahead_place : 0;
                 const int64_t ko = (id * a.cache.k_block + place * a.cache.k_token) * kBytes;
                 const int64_t vo = (id * a.cache.v_block + place * a.cache.v_token) * kBytes;
@@ -355,6 +408,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
                     }
                 }
             }
+            if (lane == 0) tile_mask[warp][slot] = mask;
             ++ahead_t;
             settle();
         }
@@ -362,72 +416,94 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
     };
 
     settle();
-#pragma unroll
-    for (int i = 0; i < S - 1; ++i) copy_tile(i);
-
-    int slot = 0;
+    // One step of the loop copies a tile and, once the ring is full, works on
+    // the oldest one.
+    int t = seg.t0, put = 0, slot = 0, primed = 0;
+    bool fresh = true;  // the next tile is the first of its row here
+    int hk = 0, head0 = 0, heads = 0;  // key/value head, first query head and their number
+    uint32_t qf[NT][KS][2];            // queries as B fragments (columns: heads)
+    float sl[NT][2];                   // score scale of columns 2c, 2c + 1
+    float m[NT][2], l[NT][2], o[NT][KS][4];
     while (live) {
-        // queries of the row, as B fragments (columns: heads)
-        const int hk = seg.row / chunks_of_group, chunk = seg.row - hk * chunks_of_group;
-        const int head0 = hk * G + chunk * HEADS;  // first query head of the row
-        const int heads = min(HEADS, G - chunk * HEADS);
-        uint32_t qf[NT][KS][2];
-        float sl[NT][2];  // score scale of columns 2c, 2c + 1
-        float m[NT][2], l[NT][2], o[NT][KS][4];
-        const float base = a.scale * 1.4426950408889634f * (E4M3 ? a.cache.k_scale[hk] : 1.f);
+        if (fresh) {
+            // the queries are requested before the tiles, which they would queue behind
+            fresh = false;
+            hk = seg.row / chunks_of_group;
+            const int chunk = seg.row - hk * chunks_of_group;
+            head0 = hk * G + chunk * HEADS;
+            heads = min(HEADS, G - chunk * HEADS);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const uint16_t* qp = a.q + seg.b * a.q_request + (head0 + n * 8 + r) * a.q_head;
-            const bool have = n * 8 + r < heads;
+            for (int n = 0; n < NT; ++n) {
+                const uint16_t* qp = a.q + seg.b * a.q_request + (head0 + n * 8 + r) * a.q_head;
+                const bool have = n * 8 + r < heads;
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                qf[n][k][0] = qf[n][k][1] = 0u;
-                if (have && k * 16 < D) {
-                    // bf16: dims 2c, 2c + 1 and 8 further; e4m3: the four dims whose codes one word holds
-                    const int d = k * 16 + (E4M3 ? 4 * c : 2 * c);
-                    qf[n][k][0] = *reinterpret_cast<const uint32_t*>(qp + d);
-                    qf[n][k][1] = *reinterpret_cast<const uint32_t*>(qp + d + (E4M3 ? 2 : 8));
+                for (int k = 0; k < KS; ++k) {
+                    qf[n][k][0] = qf[n][k][1] = 0u;
+                    if (have && k * 16 < D) {
+                        // bf16: dims 2c, 2c + 1 and 8 further; e4m3: the four dims whose codes one word holds
+                        const int d = k * 16 + (E4M3 ? 4 * c : 2 * c);
+                        qf[n][k][0] = *reinterpret_cast<const uint32_t*>(qp + d);
+                        qf[n][k][1] = *reinterpret_cast<const uint32_t*>(qp + d + (E4M3 ? 2 : 8));
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    m[n][e] = -INFINITY;
+                    l[n][e] = 0.f;
+                }
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[n][k][e] = 0.f;
+            }
+            // and those of the row after this one brought to L2
+            const int after_b = seg.row + 1 < rows ? seg.b : seg.b + 1, after_row = seg.row + 1 < rows ? seg.row + 1 : 0;
+            if (after_b < a.B) {
+                const int g = after_row / chunks_of_group, h = (after_row - g * chunks_of_group) * HEADS;
+                for (int i = lane; i < min(HEADS, G - h) * KS / 4; i += 32)
+                    if ((i % (KS / 4)) * 64 < D)
+                        prefetch_l2(a.q + after_b * a.q_request + (g * G + h + i / (KS / 4)) * a.q_head + (i % (KS / 4)) * 64);
+            }
+        }
+        const bool full = primed == S - 1;
+        if (full) cp_async_wait_group<S - 2>();
+        __syncwarp();
+        copy_tile(put);
+        put = put + 1 == S ? 0 : put + 1;
+        if (!full) {
+            ++primed;
+            continue;
+        }
+        if (t == seg.t0) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                sl[n][0] = sl[n][1] = a.scale * 1.4426950408889634f * (E4M3 ? a.cache.k_scale[hk] : 1.f);
+                if (E4M3) {
+                    // to fp16, scaled by a power of two that takes the head's largest into [2^14, 2^15)
+                    uint32_t big = 0u;
+#pragma unroll
+                    for (int k = 0; k < KS; ++k)
+                        big = __vmaxu2(big, __vmaxu2(qf[n][k][0] & 0x7FFF7FFFu, qf[n][k][1] & 0x7FFF7FFFu));
+                    big = max(big & 0xFFFFu, big >> 16);
+                    big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+                    big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+                    const int eb = min(static_cast<int>(big >> 7), 254);
+                    const int sh = min(141 - eb, 126);
+                    const float up = exp2i(sh), down = exp2i(-sh);
+#pragma unroll
+                    for (int k = 0; k < KS; ++k)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t v = qf[n][k][e];
+                            const __half2 h = __floats2half2_rn(bf16_to_f32(v & 0xFFFFu) * up, bf16_to_f32(v >> 16) * up);
+                            qf[n][k][e] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                    sl[n][0] *= __shfl_sync(0xFFFFFFFFu, down, 8 * c);
+                    sl[n][1] *= __shfl_sync(0xFFFFFFFFu, down, 8 * c + 4);
                 }
             }
-            sl[n][0] = sl[n][1] = base;
-            if (E4M3) {
-                // to fp16, scaled by a power of two that takes the head's largest into [2^14, 2^15)
-                uint32_t big = 0u;
-#pragma unroll
-                for (int k = 0; k < KS; ++k)
-                    big = __vmaxu2(big, __vmaxu2(qf[n][k][0] & 0x7FFF7FFFu, qf[n][k][1] & 0x7FFF7FFFu));
-                big = max(big & 0xFFFFu, big >> 16);
-                big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
-                big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
-                const int eb = min(static_cast<int>(big >> 7), 254);
-                const int sh = min(141 - eb, 126);
-                const float up = exp2i(sh), down = exp2i(-sh);
-#pragma unroll
-                for (int k = 0; k < KS; ++k)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t v = qf[n][k][e];
-                        const __half2 h = __floats2half2_rn(bf16_to_f32(v & 0xFFFFu) * up, bf16_to_f32(v >> 16) * up);
-                        qf[n][k][e] = *reinterpret_cast<const uint32_t*>(&h);
-                    }
-                sl[n][0] *= __shfl_sync(0xFFFFFFFFu, down, 8 * c);
-                sl[n][1] *= __shfl_sync(0xFFFFFFFFu, down, 8 * c + 4);
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                m[n][e] = -INFINITY;
-                l[n][e] = 0.f;
-            }
-#pragma unroll
-            for (int k = 0; k < KS; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[n][k][e] = 0.f;
         }
-
-        for (int t = seg.t0; t < seg.t1; ++t) {
-            cp_async_wait_group<S - 2>();
-            __syncwarp();
-            copy_tile(slot == 0 ? S - 1 : slot - 1);
+        {
             const uint32_t kt = ring + slot * Sh::kStageBytes, vt = kt + kTile * Sh::kRowBytes;
             const uint32_t mask = tile_mask[warp][slot];
             slot = slot + 1 == S ? 0 : slot + 1;
@@ -538,6 +614,8 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
             }
         }
 
+        if (++t < seg.t1) continue;
+
         // --- the result of the segment ---------------------------------------
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -583,7 +661,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
                     }
                 }
             }
-            if (jp.by_row && lane == 0) jp.joins[seg.b * rows + seg.row] = make_int4(-1, 0, 0, 0);
+            if (jp.split && jp.by_row && lane == 0) jp.joins[seg.b * rows + seg.row] = make_int4(-1, 0, 0, 0);
         } else {
             const int i = warp * 2 + (begins ? 1 : 0);
             if (begins) {  // the last tiles of the share: the ring is free
@@ -620,59 +698,81 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
             }
         }
         live = next_segment(seg);
+        t = seg.t0;
+        fresh = true;
     }
     cp_async_wait_group<0>();
     __syncthreads();
 
-    // --- parts of one row, next to one another, become one -------------------
-    if (!jp.by_row && threadIdx.x == 0) jp.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    for (int i = 0; i < kAttnWarps * 2;) {
-        if (part_b[i] < 0) {
-            ++i;
-            continue;
-        }
-        const int b = part_b[i], row = part_row[i], from = i;
-        int flags = 0;
-        for (; i < kAttnWarps * 2 && (part_b[i] < 0 || (part_b[i] == b && part_row[i] == row)); ++i)
-            if (part_b[i] >= 0) flags |= part_ends[i];
-        const int hk = row / chunks_of_group, chunk = row - hk * chunks_of_group;
-        const int head0 = hk * G + chunk * HEADS, heads = min(HEADS, G - chunk * HEADS);
+    // --- parts of one row become one -----------------------------------------
+    // thread (i, h): the factor of part i's head h, and what part i leads
+    for (int x = threadIdx.x; x < kAttnWarps * 2 * HEADS; x += kAttnThreads) {
+        const int i = x / HEADS, h = x - i * HEADS;
+        if (part_b[i] < 0) continue;
+        float top = -INFINITY, all = 0.f;
+        uint32_t members = 0u;
+#pragma unroll
+        for (int j = 0; j < kAttnWarps * 2; ++j)
+            if (part_b[j] == part_b[i] && part_row[j] == part_row[i]) {
+                members |= 1u << j;
+                top = fmaxf(top, part_m[j][h]);
+            }
+#pragma unroll
+        for (int j = 0; j < kAttnWarps * 2; ++j)
+            if ((members >> j) & 1u)
+                if (part_l[j][h] != 0.f) all += part_l[j][h] * (part_m[j][h] == top ? 1.f : exp2_fast(part_m[j][h] - top));
+        part_f[i][h] = part_l[i][h] != 0.f ? (part_m[i][h] == top ? 1.f : exp2_fast(part_m[i][h] - top)) : 0.f;
+        part_top[i][h] = top;
+        part_all[i][h] = all;
+        if (h == 0) part_members[i] = members;
+    }
+    if (jp.split && !jp.by_row && threadIdx.x == 0) jp.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    __syncthreads();
+    for (int i = 0; i < kAttnWarps * 2; ++i) {
+        if (part_b[i] < 0) continue;
+        const uint32_t members = part_members[i];
+        if (members & ((1u << i) - 1u)) continue;  // an earlier part leads
+        const int b = part_b[i], row = part_row[i], final_part = 31 - __clz(members);
+        const int flags = part_ends[i] | part_ends[final_part];
+        const int hk_i = row / chunks_of_group, chunk = row - hk_i * chunks_of_group;
+        const int head_i = hk_i * G + chunk * HEADS, n = min(HEADS, G - chunk * HEADS);
         const bool whole = flags == 3;
+        const float vs = E4M3 ? a.cache.v_scale[hk_i] : 1.f;
         float* const to = jp.part + (static_cast<int64_t>(blockIdx.x) * 2 + (flags & 1)) * (HEADS * (DP + 2));
-        for (int item = threadIdx.x; item < heads * (D / 4); item += kAttnThreads) {
-            const int h = item / (D / 4), d = (item - h * (D / 4)) * 4;
-            float top = -INFINITY, all = 0.f;
-            for (int j = from; j < i; ++j)
-                if (part_b[j] >= 0) top = fmaxf(top, part_m[j][h]);
+        for (int item = threadIdx.x; item < n * (DP / 4); item += kAttnThreads) {
+            const int h = item / (DP / 4), d = (item % (DP / 4)) * 4;
+            if (d >= D) continue;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int j = from; j < i; ++j) {
-                if (part_b[j] < 0 || part_l[j][h] == 0.f) continue;
-                const float mj = part_m[j][h], f = mj == top ? 1.f : exp2_fast(mj - top);
+#pragma unroll
+            for (int j = 0; j < kAttnWarps * 2; ++j) {
+                if (!((members >> j) & 1u)) continue;
+                const float f = part_f[j][h];
+                if (f == 0.f) continue;  // nothing there: the part may hold anything
                 const float4 x = *reinterpret_cast<const float4*>(part_of(j) + part_index<E4M3, DP>(h, d));
-                all = fmaf(part_l[j][h], f, all);
                 v.x = fmaf(x.x, f, v.x), v.y = fmaf(x.y, f, v.y);
                 v.z = fmaf(x.z, f, v.z), v.w = fmaf(x.w, f, v.w);
             }
+            const float all = part_all[i][h];
             if (whole) {
-                const float f = all != 0.f ? (E4M3 ? a.cache.v_scale[hk] : 1.f) / all : 0.f;
+                const float f = all != 0.f ? vs / all : 0.f;
                 const uint32_t lo = f32_to_bf16_rn(v.x * f) | (static_cast<uint32_t>(f32_to_bf16_rn(v.y * f)) << 16);
                 const uint32_t hi = f32_to_bf16_rn(v.z * f) | (static_cast<uint32_t>(f32_to_bf16_rn(v.w * f)) << 16);
-                *reinterpret_cast<uint2*>(a.out + b * a.out_request + (head0 + h) * a.out_head + d) = make_uint2(lo, hi);
+                *reinterpret_cast<uint2*>(a.out + b * a.out_request + (head_i + h) * a.out_head + d) = make_uint2(lo, hi);
                 if (d == 0 && a.lse)
-                    a.lse[static_cast<int64_t>(b) * a.q_heads + head0 + h] =
-                        all != 0.f ? (top + (log2f(all) - kBias)) * 0.6931471805599453f : -INFINITY;
+                    a.lse[static_cast<int64_t>(b) * a.q_heads + head_i + h] =
+                        all != 0.f ? (part_top[i][h] + (log2f(all) - kBias)) * 0.6931471805599453f : -INFINITY;
             } else {
                 *reinterpret_cast<float4*>(to + h * DP + d) = v;
                 if (d == 0) {
-                    to[HEADS * DP + h] = top;
+                    to[HEADS * DP + h] = part_top[i][h];
                     to[HEADS * (DP + 1) + h] = all;
                 }
             }
         }
         // a row that begins here: what the join launch has to do for it
-        if (threadIdx.x == 0 && (flags & 1) && (jp.by_row || !whole))
+        if (jp.split && threadIdx.x == 0 && (flags & 1) && (jp.by_row || !whole))
             jp.joins[jp.by_row ? b * rows + row : static_cast<int>(blockIdx.x)] =
-                make_int4(whole ? -1 : b, row, static_cast<int>(blockIdx.x), cta_of(part_at[from] + part_tiles[from] - 1));
+                make_int4(whole ? -1 : b, row, static_cast<int>(blockIdx.x), cta_of(part_at[i] + part_tiles[i] - 1));
     }
     if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
 }
@@ -691,6 +791,8 @@ cudaError_t launch_attention_shape(const AttentionArgs& a, const DeviceInfo& dev
     ws.rows = a.cache.heads * ((a.q_heads / a.cache.heads + Sh::kHeads - 1) / Sh::kHeads);
     ws.by_row = static_cast<int64_t>(a.B) * ws.rows <= ctas;
     ws.ctas = ctas;
+    // rows of few tiles: not worth a second launch, so CTAs take them whole
+    ws.split = static_cast<int64_t>(a.columns) * a.cache.page > kWholeTiles * kTile;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kAttnThreads);
