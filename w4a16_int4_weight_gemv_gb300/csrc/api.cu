@@ -827,7 +827,9 @@ w4a16_status w4a16_paged_attention(const uint16_t* q, int64_t q_request, int64_t
     DeviceCache* dev = nullptr;
     st = current_device(&dev);
     if (st != W4A16_OK) return st;
-    AttentionArgs a{q, q_request, q_head, *cache, block_table, table_stride, kv_len, columns, B, q_heads, window,
+    int64_t most = static_cast<int64_t>(columns) * cache->page;
+    if (most > 0x7FFFFFFF - 1024) most = 0x7FFFFFFF - 1024;  // token numbers stay in 32 bits
+    AttentionArgs a{q, q_request, q_head, *cache, block_table, table_stride, kv_len, static_cast<int>(most), B, q_heads, window,
                     scale, out, out_request, out_head, lse, workspace, dev->err};
     return from_cuda(launch_paged_attention(a, dev->info, static_cast<cudaStream_t>(stream)));
 }

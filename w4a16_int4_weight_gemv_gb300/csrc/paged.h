@@ -66,7 +66,7 @@ struct AttentionArgs {
     const int32_t* block_table;
     int64_t table_stride;
     const int32_t* kv_len;
-    int columns;
+    int most;  // tokens a row of the table holds
     int B;
     int q_heads;
     int window;

@@ -7,7 +7,7 @@
 // each, in groups that take every n-th part, so that all of a row's parts are
 // requested at once; the groups are joined in shared memory.  It is launched
 // while the first launch runs and waits for its end, so it costs the latency
-// of three dependent reads, and nothing but that where no row was split.
+// of two dependent reads, and nothing but that where no row was split.
 #include "common.cuh"
 #include "paged_attention.h"
 
@@ -33,63 +33,52 @@ __device__ __forceinline__ void add_part(Sum& s, float m, float l, const float4&
     s.v.z = s.v.z * f0 + o.z * f1, s.v.w = s.v.w * f0 + o.w * f1;
 }
 
-__global__ void __launch_bounds__(kThreads) k_attention_join(const AttentionArgs a, const JoinPlan j) {
+// Threads (x: four dims, y: head and group of parts); grid (row, slice of its heads).
+__global__ void __launch_bounds__(kThreads) k_attention_join(const AttentionArgs a, const JoinPlan j, const int log_heads) {
     __shared__ Sum sums[kThreads];
     grid_dependents_launch();
     grid_dependency_wait();
     const int4 d = __ldcg(j.joins + blockIdx.x);
     const int b = d.x, row = d.y, first = d.z, last = d.w;
     if (b < 0) return;
-    const int G = a.q_heads / a.cache.heads, lanes = a.cache.dim / 4;
-    const int chunks = j.rows / a.cache.heads;
-    const int hk = row / chunks, chunk = row - hk * chunks;
-    const int head0 = hk * G + chunk * j.heads, heads = min(j.heads, G - chunk * j.heads);
-    const bool e4m3 = a.cache.dtype == W4A16_CACHE_E4M3;
-    const int each = (heads + static_cast<int>(gridDim.y) - 1) / static_cast<int>(gridDim.y);
-    const int h_begin = blockIdx.y * each, h_end = min(heads, h_begin + each);
-    const int items = (h_end - h_begin) * lanes;
-    if (items <= 0) return;
-    const int width = min(items, kThreads), groups = kThreads / width;
-    const int group = threadIdx.x / width, lane = threadIdx.x - group * width;
+    const int lanes = blockDim.x, groups = blockDim.y >> log_heads, group = threadIdx.y >> log_heads;
+    const int h = (blockIdx.y << log_heads) + (threadIdx.y & ((1 << log_heads) - 1)), dim = threadIdx.x * 4;
     const int64_t size = static_cast<int64_t>(j.heads) * (j.padded + 2);
-    for (int base = 0; base < items; base += width) {
-        const int item = base + lane;
-        const bool mine = group < groups && item < items;
-        const int h = h_begin + item / lanes, dim = (item % lanes) * 4;
-        Sum s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-        if (mine) {
-            for (int q = first + group; q <= last; q += groups * kDepth) {
-                float m[kDepth], l[kDepth];
-                float4 o[kDepth];
+    Sum s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 1
+    for (int q = first + group; q <= last; q += groups * kDepth) {
+        float m[kDepth], l[kDepth];
+        float4 o[kDepth];
 #pragma unroll
-                for (int i = 0; i < kDepth; ++i) {
-                    const int p = min(q + i * groups, last);
-                    const float* part = j.part + (static_cast<int64_t>(p) * 2 + (p == first ? 1 : 0)) * size;
-                    o[i] = __ldcg(reinterpret_cast<const float4*>(part + h * j.padded + dim));
-                    m[i] = __ldcg(part + j.heads * j.padded + h);
-                    l[i] = q + i * groups <= last ? __ldcg(part + j.heads * (j.padded + 1) + h) : 0.f;
-                }
+        for (int i = 0; i < kDepth; ++i) {
+            const int p = min(q + i * groups, last);
+            const float* part = j.part + (static_cast<int64_t>(p) * 2 + (p == first ? 1 : 0)) * size;
+            o[i] = __ldcg(reinterpret_cast<const float4*>(part + h * j.padded + dim));
+            m[i] = __ldcg(part + j.heads * j.padded + h);
+            l[i] = q + i * groups <= last ? __ldcg(part + j.heads * (j.padded + 1) + h) : 0.f;
+        }
 #pragma unroll
-                for (int i = 0; i < kDepth; ++i) add_part(s, m[i], l[i], o[i]);
-            }
-        }
-        sums[threadIdx.x] = s;
-        __syncthreads();
-        if (mine && group == 0) {
-            for (int g = 1; g < groups; ++g) {
-                const Sum& x = sums[g * width + lane];
-                add_part(s, x.top, x.all, x.v);
-            }
-            const float f = s.all != 0.f ? (e4m3 ? a.cache.v_scale[hk] : 1.f) / s.all : 0.f;
-            const uint32_t lo = f32_to_bf16_rn(s.v.x * f) | (static_cast<uint32_t>(f32_to_bf16_rn(s.v.y * f)) << 16);
-            const uint32_t hi = f32_to_bf16_rn(s.v.z * f) | (static_cast<uint32_t>(f32_to_bf16_rn(s.v.w * f)) << 16);
-            *reinterpret_cast<uint2*>(a.out + b * a.out_request + (head0 + h) * a.out_head + dim) = make_uint2(lo, hi);
-            if (dim == 0 && a.lse)
-                a.lse[static_cast<int64_t>(b) * a.q_heads + head0 + h] =
-                    s.all != 0.f ? (s.top + (log2f(s.all) - (e4m3 ? kE4m3Bias : 0.f))) * 0.6931471805599453f : -INFINITY;
-        }
-        __syncthreads();
+        for (int i = 0; i < kDepth; ++i) add_part(s, m[i], l[i], o[i]);
     }
+    const int me = threadIdx.y * lanes + threadIdx.x, step = lanes << log_heads;
+    sums[me] = s;
+    __syncthreads();
+    const int G = a.q_heads / a.cache.heads, chunks = j.rows / a.cache.heads;
+    const int hk = row / chunks, head = (row - hk * chunks) * j.heads + h;  // of the group
+    if (group > 0 || head >= G || dim >= a.cache.dim) return;
+#pragma unroll 1
+    for (int g = 1; g < groups; ++g) {
+        const Sum& x = sums[me + g * step];
+        add_part(s, x.top, x.all, x.v);
+    }
+    const bool e4m3 = a.cache.dtype == W4A16_CACHE_E4M3;
+    const float f = s.all != 0.f ? (e4m3 ? a.cache.v_scale[hk] : 1.f) / s.all : 0.f;
+    const uint32_t lo = f32_to_bf16_rn(s.v.x * f) | (static_cast<uint32_t>(f32_to_bf16_rn(s.v.y * f)) << 16);
+    const uint32_t hi = f32_to_bf16_rn(s.v.z * f) | (static_cast<uint32_t>(f32_to_bf16_rn(s.v.w * f)) << 16);
+    *reinterpret_cast<uint2*>(a.out + b * a.out_request + (hk * G + head) * a.out_head + dim) = make_uint2(lo, hi);
+    if (dim == 0 && a.lse)
+        a.lse[static_cast<int64_t>(b) * a.q_heads + hk * G + head] =
+            s.all != 0.f ? (s.top + (log2f(s.all) - (e4m3 ? kE4m3Bias : 0.f))) * 0.6931471805599453f : -INFINITY;
 }
 
 }  // namespace
@@ -109,19 +98,21 @@ cudaError_t launch_paged_attention(const AttentionArgs& a, const DeviceInfo& dev
                                                       : launch_attention_e4m3(a, dev, join, s);
     if (e != cudaSuccess || !join.split) return e;
     const int places = join.by_row ? a.B * join.rows : join.ctas;
-    int slices = 2 * dev.sms / places;  // few rows: their heads over several CTAs
-    if (slices > join.heads) slices = join.heads;
-    if (slices < 1) slices = 1;
+    // few rows: their heads over several CTAs, down to one head each
+    const int lanes = join.padded / 4;
+    int log_heads = join.heads == 16 ? 4 : 3;
+    while (log_heads > 0 && ((lanes << log_heads) > kThreads || places * (join.heads >> log_heads) < dev.sms)) --log_heads;
+    const int groups = kThreads / (lanes << log_heads);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(places, slices);
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(places, join.heads >> log_heads);
+    cfg.blockDim = dim3(lanes, groups << log_heads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_attention_join, a, join);
+    e = cudaLaunchKernelEx(&cfg, k_attention_join, a, join, log_heads);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

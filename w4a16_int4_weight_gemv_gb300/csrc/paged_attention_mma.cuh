@@ -126,12 +126,10 @@ struct Request {
 
 __device__ __forceinline__ Request request_of(const AttentionArgs& a, int b, bool& bad) {
     Request q;
-    int64_t len = a.kv_len[b];
-    const int64_t most = static_cast<int64_t>(a.columns) * a.cache.page;
-    bad |= len < 0 || len > most;
-    len = len < 0 ? 0 : len > most ? most : len;
-    q.len = static_cast<int>(len);
-    q.start = a.window > 0 && q.len > a.window ? q.len - a.window : 0;
+    const int len = a.kv_len[b];
+    bad |= len < 0 || len > a.most;
+    q.len = min(max(len, 0), a.most);
+    q.start = a.window > 0 ? max(q.len - a.window, 0) : 0;
     q.tile0 = q.start / kTile;
     q.tiles = q.len > 0 ? (q.len - 1) / kTile + 1 - q.tile0 : 0;
     return q;
@@ -165,9 +163,6 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
     constexpr int kBytes = E4M3 ? 1 : 2;
     constexpr float kBias = E4M3 ? kE4m3Bias : 0.f;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t scan_sum[kAttnWarps];
-    __shared__ int64_t found_at[kAttnWarps];  // costs before the request of a warp's first tile
-    __shared__ int found_b[kAttnWarps];
     __shared__ uint32_t tile_mask[kAttnWarps][S];
     // parts of a warp: 0 of the row its share begins inside of, 1 of the one it ends inside of
     __shared__ int64_t part_at[kAttnWarps * 2];
@@ -196,27 +191,41 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
             reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
     }
     if (threadIdx.x < kAttnWarps * 2) part_b[threadIdx.x] = -1;
+    __syncthreads();
     grid_dependency_wait();
     grid_dependents_launch();
 
     // --- the share of each warp ---------------------------------------------
-    auto cost_of = [&](int b) -> int64_t {
-        const int n = request_of(a, b, bad).tiles;
-        return n ? static_cast<int64_t>(n + kRowCost) * rows : 0;
+    // Every warp forms the costs of all requests itself, kScan of them at a
+    // time (lane i: kPer in a row from kPer * i on): no barrier is needed.
+    constexpr int kPer = 4, kScan = 32 * kPer;
+    int64_t cost[kPer];  // of this lane's requests
+    // the costs of requests base .. base + kScan - 1; returns those before this lane's, `sum`: all
+    auto scan = [&](int base, int64_t& sum) -> int64_t {
+        int64_t own = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int b = base + lane * kPer + i;
+            const int n = b < a.B ? request_of(a, b, bad).tiles : 0;
+            cost[i] = n ? static_cast<int64_t>(n + kRowCost) * rows : 0;
+            own += cost[i];
+        }
+        int64_t inc = own;
+#pragma unroll 1
+        for (int d = 1; d < 32; d *= 2) {
+            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+            if (lane >= d) inc += v;
+        }
+        sum = __shfl_sync(0xFFFFFFFFu, inc, 31);
+        return inc - own;
     };
-    int64_t sum = 0, mine = 0;  // mine: of request threadIdx.x
-    for (int b = threadIdx.x; b < a.B; b += kAttnThreads) {
-        const int64_t n = cost_of(b);
-        if (b < kAttnThreads) mine = n;
-        sum += n;
+    int64_t total = 0, head_start = 0;  // head_start: before this lane's, of the first kScan requests
+    for (int base = 0; base < a.B; base += kScan) {
+        int64_t sum;
+        const int64_t start = scan(base, sum);
+        if (base == 0) head_start = start;
+        total += sum;
     }
-#pragma unroll
-    for (int d = 16; d; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    if (lane == 0) scan_sum[warp] = sum;
-    __syncthreads();
-    int64_t total = 0;
-#pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) total += scan_sum[w];
     // requests without tokens
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         if (request_of(a, b, bad).tiles > 0) continue;
@@ -246,59 +255,47 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
         const int64_t big = extra * (share + 1);
         return static_cast<int>(u < big ? quotient(u, share + 1) : extra + quotient(u - big, share));
     };
-    // for each of n places: the request that holds it, and the costs before that
-    auto locate = [&](const int64_t* place, int n) {
-        int64_t before = 0, last = 0;
-        for (int i = 0; i < n; ++i) last = place[i] > last ? place[i] : last;
-        for (int base = 0; base < a.B; base += kAttnThreads) {
-            const int b = base + static_cast<int>(threadIdx.x);
-            const int64_t cost = base == 0 ? mine : (b < a.B ? cost_of(b) : 0);
-            int64_t inc = cost;
+    // the request that holds the place u < total, and the costs before it
+    auto locate = [&](int64_t u, int& found_b, int64_t& found_at) -> bool {
+        int64_t before = 0;
+        for (int base = 0; base < a.B; base += kScan) {
+            int64_t sum = 0, start = head_start;
+            if (a.B > kScan) start = scan(base, sum);
+            start += before;
+            int hit = -1;
 #pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
-                if (lane >= d) inc += v;
-            }
-            __syncthreads();
-            if (lane == 31) scan_sum[warp] = inc;
-            __syncthreads();
-            int64_t start = before, chunk = 0;
-#pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) {
-                if (w < warp) start += scan_sum[w];
-                chunk += scan_sum[w];
-            }
-            start += inc - cost;
-            for (int i = 0; i < n; ++i) {
-                if (place[i] >= start && place[i] < start + cost) {
-                    found_b[i] = b;
-                    found_at[i] = start;
+            for (int i = 0; i < kPer; ++i) {
+                if (u >= start && u < start + cost[i]) {
+                    hit = base + lane * kPer + i;
+                    found_at = start;
                 }
+                start += cost[i];
             }
-            before += chunk;
-            if (before > last) break;
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, hit >= 0);
+            if (who) {
+                found_b = __shfl_sync(0xFFFFFFFFu, hit, __ffs(who) - 1);
+                found_at = __shfl_sync(0xFFFFFFFFu, found_at, __ffs(who) - 1);
+                return true;
+            }
+            before += sum;
         }
-        __syncthreads();
+        return false;
     };
     int64_t begin = cta_begin(blockIdx.x), end = cta_begin(blockIdx.x + 1);
+    int first_b = 0;
+    int64_t first_at = 0;
     if (!jp.split) {
         // whole rows: from the first that begins in the share to the last that does
-        const int64_t ends[2] = {begin, end};
-        if (threadIdx.x < 2) found_b[threadIdx.x] = -1;
-        locate(ends, 2);
-        auto row_from = [&](int64_t u, int i) -> int64_t {
-            if (found_b[i] < 0) return u;  // past the last request
-            const int n = request_of(a, found_b[i], bad).tiles + kRowCost;
-            return found_at[i] + quotient(u - found_at[i] + n - 1, n) * n;
-        };
-        begin = row_from(begin, 0), end = row_from(end, 1);
-        __syncthreads();
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+            int64_t& u = i ? end : begin;
+            if (u >= total || !locate(u, first_b, first_at)) continue;
+            const int n = request_of(a, first_b, bad).tiles + kRowCost;
+            u = first_at + quotient(u - first_at + n - 1, n) * n;
+        }
     }
-    const int64_t places[kAttnWarps] = {begin, begin + (end - begin) / 4, begin + (end - begin) / 2,
-                                        begin + (end - begin) * 3 / 4};
     static_assert(kAttnWarps == 4, "shares of four warps");
-    locate(places, kAttnWarps);
-    const int64_t u0 = places[warp], u1 = warp + 1 < kAttnWarps ? places[(warp + 1) % kAttnWarps] : end;
+    const int64_t u0 = begin + ((end - begin) * warp >> 2), u1 = begin + ((end - begin) * (warp + 1) >> 2);
 
     // --- the rows of a share, in order ---------------------------------------
     auto open_segment = [&](Segment& s) {
@@ -312,7 +309,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
         if (++s.row == rows) {
             s.row = 0;
             do {
-                ++s.b;
+                if (++s.b >= a.B) return false;
                 s.q = request_of(a, s.b, bad);
             } while (s.q.tiles == 0);
         }
@@ -320,12 +317,12 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
         return true;
     };
     Segment seg{};
-    bool live = u1 > u0;
+    bool live = u1 > u0 && locate(u0, first_b, first_at);
     if (live) {
-        seg.b = found_b[warp];
+        seg.b = first_b;
         seg.q = request_of(a, seg.b, bad);
-        seg.row = static_cast<int>(quotient(u0 - found_at[warp], seg.q.tiles + kRowCost));
-        seg.at = found_at[warp] + static_cast<int64_t>(seg.row) * (seg.q.tiles + kRowCost);
+        seg.row = static_cast<int>(quotient(u0 - first_at, seg.q.tiles + kRowCost));
+        seg.at = first_at + static_cast<int64_t>(seg.row) * (seg.q.tiles + kRowCost);
         open_segment(seg);
         live = seg.t1 > seg.t0;
     }
@@ -711,13 +708,13 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
         if (part_b[i] < 0) continue;
         float top = -INFINITY, all = 0.f;
         uint32_t members = 0u;
-#pragma unroll
+#pragma unroll 1
         for (int j = 0; j < kAttnWarps * 2; ++j)
             if (part_b[j] == part_b[i] && part_row[j] == part_row[i]) {
                 members |= 1u << j;
                 top = fmaxf(top, part_m[j][h]);
             }
-#pragma unroll
+#pragma unroll 1
         for (int j = 0; j < kAttnWarps * 2; ++j)
             if ((members >> j) & 1u)
                 if (part_l[j][h] != 0.f) all += part_l[j][h] * (part_m[j][h] == top ? 1.f : exp2_fast(part_m[j][h] - top));
@@ -728,6 +725,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
     }
     if (jp.split && !jp.by_row && threadIdx.x == 0) jp.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
     __syncthreads();
+#pragma unroll 1
     for (int i = 0; i < kAttnWarps * 2; ++i) {
         if (part_b[i] < 0) continue;
         const uint32_t members = part_members[i];
@@ -739,13 +737,14 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
         const bool whole = flags == 3;
         const float vs = E4M3 ? a.cache.v_scale[hk_i] : 1.f;
         float* const to = jp.part + (static_cast<int64_t>(blockIdx.x) * 2 + (flags & 1)) * (HEADS * (DP + 2));
+#pragma unroll 1
         for (int item = threadIdx.x; item < n * (DP / 4); item += kAttnThreads) {
             const int h = item / (DP / 4), d = (item % (DP / 4)) * 4;
             if (d >= D) continue;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int j = 0; j < kAttnWarps * 2; ++j) {
-                if (!((members >> j) & 1u)) continue;
+#pragma unroll 1
+            for (uint32_t left = members; left; left &= left - 1u) {
+                const int j = __ffs(left) - 1;
                 const float f = part_f[j][h];
                 if (f == 0.f) continue;  // nothing there: the part may hold anything
                 const float4 x = *reinterpret_cast<const float4*>(part_of(j) + part_index<E4M3, DP>(h, d));
@@ -792,7 +791,7 @@ cudaError_t launch_attention_shape(const AttentionArgs& a, const DeviceInfo& dev
     ws.by_row = static_cast<int64_t>(a.B) * ws.rows <= ctas;
     ws.ctas = ctas;
     // rows of few tiles: not worth a second launch, so CTAs take them whole
-    ws.split = static_cast<int64_t>(a.columns) * a.cache.page > kWholeTiles * kTile;
+    ws.split = a.most > kWholeTiles * kTile;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kAttnThreads);
