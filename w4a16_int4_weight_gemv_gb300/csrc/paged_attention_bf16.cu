@@ -3,7 +3,7 @@
 
 namespace w4a16 {
 
-cudaError_t launch_attention_bf16(const AttentionArgs& a, const DeviceInfo& dev, JoinPlan& join, cudaStream_t s) {
+cudaError_t launch_attention_bf16(const AttentionArgs& a, const DeviceInfo& dev, JoinPlan join, cudaStream_t s) {
     return launch_attention_type<false>(a, dev, join, s);
 }
 

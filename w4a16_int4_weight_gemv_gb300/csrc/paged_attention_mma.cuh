@@ -1,30 +1,30 @@
 // Attention of one new token per request over a paged key/value cache
-// (w4a16_paged_attention): the kernel, for one cache type per translation unit.
+// (w4a16_paged_attention): the kernels, for one cache type per translation unit.
 //
 // A row is one request, one key/value head and up to 8 * NT of the query
 // heads that share it.  For the tokens j a row sees,
 //     s_j = c q . k_j (log2 units),  m = max s_j,  p_j = 2^(s_j - m),
 //     l = sum p_j,  o = sum p_j v_j,  out = o / l,
 // in one pass: a larger m scales the running l and o by 2^(m_old - m).
-// Partial (m, l, o) of disjoint token sets join the same way, in any grouping.
+// Parts (m, l, o) of disjoint token sets join the same way, in any grouping.
 //
 // Bound by HBM: each key and value is read once, for 2 * heads operations a
-// byte at most.  So the kernel is built around the copies:
-//   - Work is dealt in tiles of 16 tokens, rows one after another, and every
-//     warp takes an equal consecutive share of all tiles, whatever the lengths
-//     are (each CTA forms the sum of the tile counts itself; a row counts a
-//     tile more than it has, for its queries and its result).
-//   - A warp works alone, through a ring of its own of cp.async stages that
-//     runs on across rows; a row inside its share it finishes alone.  Only the
-//     two rows at the ends of its share may be others' too: their parts meet
-//     in shared memory once the CTA's warps are done, and what the CTA does
-//     not hold whole goes to the workspace, for a second launch to join
-//     (paged_attention.cu), always in the order of the tokens.
-//   - The products run on the warp MMA with the keys as the 16-row operand
-//     (tokens) and the heads as its 8 columns: one product covers 8 query
-//     heads, and the transposed second product (values^T times p^T) takes the
-//     probabilities from the accumulators by one 8x8 transpose in registers.
-//     (tcgen05 would want 64 or more query rows; here there are 1 to 16.)
+// byte at most.  So the kernels are built around the copies, tiles of 16
+// tokens through a ring of cp.async stages that each warp has for itself:
+//   - k_attention_shares: the tiles of all rows, one row after another, in
+//     equal consecutive shares for the warps of the whole GPU, whatever the
+//     lengths are.  A row inside a share its warp finishes alone; of the rows
+//     at the ends of a share it leaves parts in the workspace.  The ring runs
+//     on across rows, and no warp waits for another.
+//   - k_attention_join: a second launch joins those parts, always in the
+//     order of the tokens.
+//   - k_attention_rows: where there are few rows of few tiles, a CTA for each
+//     row, its warps joined in shared memory: no shares, no second launch.
+// The products run on the warp MMA with the keys as the 16-row operand
+// (tokens) and the heads as its 8 columns: one product covers 8 query heads,
+// and the transposed second product (values^T times p^T) takes the
+// probabilities from the accumulators by one 8x8 transpose in registers.
+// (tcgen05 would want 64 or more query rows; here there are 1 to 16.)
 #pragma once
 
 #include <cuda_fp16.h>
@@ -35,34 +35,13 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kTile = 16;  // tokens of a tile: the MMA's rows
-constexpr int kAttnWarps = 4;
-constexpr int kAttnThreads = kAttnWarps * 32;
-constexpr int kRowCost = 1;   // a row's queries and result, in tiles
-constexpr int kMinCost = 4;   // a warp's share at least
-constexpr int kWholeTiles = 32;  // rows that cannot be longer are not split over CTAs
-
-// Shared memory: a ring of kStages tiles per warp, and a place for the (o) of
-// the row a warp's share begins inside of (the row it ends inside of goes
-// where its ring was).
-template <bool E4M3, int DP, int NT>
-struct AttnShape {
-    static constexpr int kHeads = 8 * NT;
-    static constexpr int kRowBytes = DP * (E4M3 ? 1 : 2);
-    static constexpr int kChunks = kRowBytes / 16;             // 16-byte chunks of a row
-    static constexpr int kStageBytes = 2 * kTile * kRowBytes;  // keys, then values
-    static constexpr int kPartBytes = kHeads * DP * 4;
-    static constexpr int kJoinBytes = kAttnWarps * kPartBytes;
-    // two CTAs an SM with three or more stages where that fits, else one
-    static constexpr int kTwo = (112 * 1024 - kJoinBytes) / (kAttnWarps * kStageBytes);
-    static constexpr int kOne = (225 * 1024 - kJoinBytes) / (kAttnWarps * kStageBytes);
-    static constexpr int kPerSm = kTwo >= 3 ? 2 : 1;
-    static constexpr int kFit = kPerSm == 2 ? kTwo : kOne;
-    static constexpr int kStages = kFit > 6 ? 6 : kFit;
-    static constexpr int kRingBytes = kStages * kStageBytes;  // of a warp
-    static constexpr int kSmem = kAttnWarps * kRingBytes + kJoinBytes;
-    static_assert(kStages >= 2 && kRingBytes >= kPartBytes + 3 * 2 * kAttnWarps * kHeads * 4, "ring too short");
-};
+constexpr int kTile = 16;       // tokens of a tile: the MMA's rows
+constexpr int kShareWarps = 4;  // warps of a CTA
+constexpr int kRowWarps = 8;
+constexpr int kRowCost = 1;     // a row's queries and result, in tiles
+constexpr int kMinCost = 4;     // a warp's share at least
+constexpr int kWholeTiles = 8;  // rows that cannot be longer are not split over warps
+constexpr int kRowKernelTiles = 64;  // rows that cannot be longer may have a CTA each
 
 __device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void* src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
@@ -90,6 +69,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// 2^(m - top) of a part that is not empty (m may be infinite)
+__device__ __forceinline__ float part_factor(float m, float top) { return m == top ? 1.f : exp2_fast(m - top); }
 // two e4m3 codes (low and high byte) as an fp16 pair, exactly
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
     uint32_t d;
@@ -118,6 +99,31 @@ __device__ __forceinline__ uint32_t tile_offset(int r, int c) {
     return static_cast<uint32_t>((r * CH + (c ^ f)) * 16);
 }
 
+template <bool E4M3, int DP, int NT>
+struct AttnShape {
+    static constexpr int kHeads = 8 * NT;
+    static constexpr int kSteps = DP / 16;                     // 16-dim steps of a head
+    static constexpr int kRowBytes = DP * (E4M3 ? 1 : 2);
+    static constexpr int kChunks = kRowBytes / 16;             // 16-byte chunks of a row
+    static constexpr int kStageBytes = 2 * kTile * kRowBytes;  // keys, then values
+    static constexpr int kPartFloats = kHeads * (DP + 2);
+    // shares: as many CTAs an SM as registers allow (the accumulators' size decides) with
+    // rings of three stages or more
+    static constexpr int kPerSm = E4M3 ? (NT == 1 ? (DP == 64 ? 4 : DP == 128 ? 3 : 2) : (DP == 64 ? 3 : 2))
+                                       : (DP == 64 ? (NT == 1 ? 4 : 3) : DP == 128 ? 2 : 1);
+    static constexpr int kFit = (227 * 1024 / kPerSm - 1024 - 256) / (kShareWarps * kStageBytes);
+    static constexpr int kStages = kFit > 6 ? 6 : kFit;
+    static constexpr int kSmem = kShareWarps * kStages * kStageBytes;
+    // rows: one CTA an SM
+    static constexpr int kRowFit = 225 * 1024 / (kRowWarps * kStageBytes);
+    static constexpr int kRowStages = kRowFit > 4 ? 4 : kRowFit;
+    static constexpr bool kRowKernel = kRowStages >= 2;
+    static constexpr int kRowSmem = kRowWarps * kRowStages * kStageBytes;
+    static_assert(kStages >= 3, "ring too short");
+    static_assert(!kRowKernel || kRowStages * kStageBytes >= kHeads * DP * 4, "no room for a warp's part");
+    static_assert(kPerSm * 160 * kShareWarps <= most_workers(DP), "workspace");
+};
+
 // What one request looks like: its visible tokens [start, len), in tiles from
 // tile0 on.
 struct Request {
@@ -135,6 +141,374 @@ __device__ __forceinline__ Request request_of(const AttentionArgs& a, int b, boo
     return q;
 }
 
+// Which heads row `row` of a request stands for.
+struct Heads {
+    int hk, first, n;  // key/value head, first query head, how many
+};
+template <int HEADS>
+__device__ __forceinline__ Heads heads_of(const AttentionArgs& a, int row) {
+    const int G = a.q_heads / a.cache.heads, chunks = (G + HEADS - 1) / HEADS;
+    Heads h;
+    h.hk = row / chunks;
+    const int chunk = row - h.hk * chunks;
+    h.first = h.hk * G + chunk * HEADS;
+    h.n = min(HEADS, G - chunk * HEADS);
+    return h;
+}
+
+__device__ __forceinline__ void store_empty(const AttentionArgs& a, int b, int head, int heads, int thread, int threads) {
+    const int per = a.cache.dim / 8;
+    for (int i = thread; i < heads * per; i += threads) {
+        const int h = head + i / per, d = (i % per) * 8;
+        *reinterpret_cast<uint4*>(a.out + b * a.out_request + h * a.out_head + d) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (a.lse)
+        for (int h = thread; h < heads; h += threads) a.lse[static_cast<int64_t>(b) * a.q_heads + head + h] = -INFINITY;
+}
+
+// 16 dims of 8 heads from the accumulators (row r and r + 8 by columns 2c,
+// 2c + 1) times the heads' factors, transposed to dims along the lanes of a
+// head and stored; `out`: the row of head r's output, null for none.
+template <bool E4M3>
+__device__ __forceinline__ void store_dims(const float4& o, float f0, float f1, uint16_t* out, int c) {
+    const __nv_bfloat162 p0 = __floats2bfloat162_rn(o.x * f0, o.y * f1), p1 = __floats2bfloat162_rn(o.z * f0, o.w * f1);
+    const uint32_t v0 = transpose_8x8(*reinterpret_cast<const uint32_t*>(&p0));
+    const uint32_t v1 = transpose_8x8(*reinterpret_cast<const uint32_t*>(&p1));
+    if (!out) return;
+    if (E4M3) {  // rows of the product: even dims, then odd ones
+        *reinterpret_cast<uint2*>(out + 4 * c) = make_uint2(__byte_perm(v0, v1, 0x5410), __byte_perm(v0, v1, 0x7632));
+    } else {
+        *reinterpret_cast<uint32_t*>(out + 2 * c) = v0;
+        *reinterpret_cast<uint32_t*>(out + 8 + 2 * c) = v1;
+    }
+}
+template <bool E4M3>
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l != 0.f ? (m + (log2f(l) - (E4M3 ? kE4m3Bias : 0.f))) * 0.6931471805599453f : -INFINITY;
+}
+
+// The arithmetic of a warp on tiles of one row.  Lane 4 r + c.
+template <bool E4M3, int DP, int NT>
+struct RowMath {
+    using Sh = AttnShape<E4M3, DP, NT>;
+    static constexpr int CH = Sh::kChunks, KS = Sh::kSteps;
+    uint32_t qf[NT][KS][2];              // queries as B fragments (columns: heads)
+    float sl[NT][2];                     // score scale of columns 2c, 2c + 1
+    float m[NT][2], l[NT][2];            // of columns 2c, 2c + 1 (l: of this lane's tokens until reduced)
+    float4 o[NT][KS];                    // dims r, r + 8 (e4m3: 2r, 2r + 1) by columns 2c, 2c + 1
+
+    // requests the queries and clears the sums
+    __device__ __forceinline__ void begin(const AttentionArgs& a, int b, const Heads& hd, int lane) {
+        const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const uint16_t* qp = a.q + b * a.q_request + (hd.first + n * 8 + r) * a.q_head;
+            const bool have = n * 8 + r < hd.n;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                qf[n][k][0] = qf[n][k][1] = 0u;
+                if (have && k * 16 < a.cache.dim) {
+                    // bf16: dims 2c, 2c + 1 and 8 further; e4m3: the four dims whose codes one word holds
+                    const int d = k * 16 + (E4M3 ? 4 * c : 2 * c);
+                    qf[n][k][0] = *reinterpret_cast<const uint32_t*>(qp + d);
+                    qf[n][k][1] = *reinterpret_cast<const uint32_t*>(qp + d + (E4M3 ? 2 : 8));
+                }
+                o[n][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[n][e] = -INFINITY;
+                l[n][e] = 0.f;
+            }
+        }
+    }
+
+    // makes the queries that begin() requested into operands
+    __device__ __forceinline__ void ready(const AttentionArgs& a, int hk, int lane) {
+        const int c = lane & 3;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            sl[n][0] = sl[n][1] = a.scale * 1.4426950408889634f * (E4M3 ? a.cache.k_scale[hk] : 1.f);
+            if (E4M3) {
+                // to fp16, scaled by a power of two that takes the head's largest into [2^14, 2^15)
+                uint32_t big = 0u;
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+                    big = __vmaxu2(big, __vmaxu2(qf[n][k][0] & 0x7FFF7FFFu, qf[n][k][1] & 0x7FFF7FFFu));
+                big = max(big & 0xFFFFu, big >> 16);
+                big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+                big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+                const int sh = min(141 - min(static_cast<int>(big >> 7), 254), 126);
+                const float up = exp2i(sh), down = exp2i(-sh);
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t v = qf[n][k][e];
+                        const __half2 h = __floats2half2_rn(bf16_to_f32(v & 0xFFFFu) * up, bf16_to_f32(v >> 16) * up);
+                        qf[n][k][e] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                sl[n][0] *= __shfl_sync(0xFFFFFFFFu, down, 8 * c);
+                sl[n][1] *= __shfl_sync(0xFFFFFFFFu, down, 8 * c + 4);
+            }
+        }
+    }
+
+    // the tile at kt (shared address): keys, then values; mask: tokens that count
+    __device__ __forceinline__ void tile(uint32_t kt, uint32_t mask, int lane) {
+        constexpr float kBias = E4M3 ? kE4m3Bias : 0.f;
+        const uint32_t vt = kt + kTile * Sh::kRowBytes;
+        const int r = lane >> 2;
+        float s[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+        if (!E4M3) {
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                uint32_t f[4];
+                ldmatrix_x4(f, kt + tile_offset<CH>(lane & 15, 2 * k + (lane >> 4)));
+#pragma unroll
+                for (int n = 0; n < NT; ++n) attn_mma<E4M3>(s[n], f[0], f[1], f[2], f[3], qf[n][k][0], qf[n][k][1]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < KS; k += 2) {
+                uint32_t f[4];  // two chunks of 16 codes: rows r and r + 8 of each
+                ldmatrix_x4(f, kt + tile_offset<CH>(lane & 15, k + (lane >> 4)));
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t a0 = e4m3x2_to_f16x2(f[2 * j]), a2 = e4m3x2_to_f16x2(f[2 * j] >> 16);
+                    const uint32_t a1 = e4m3x2_to_f16x2(f[2 * j + 1]), a3 = e4m3x2_to_f16x2(f[2 * j + 1] >> 16);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        attn_mma<E4M3>(s[n], a0, a1, a2, a3, qf[n][k + j][0], qf[n][k + j][1]);
+                }
+            }
+        }
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][e] *= sl[n][e & 1];
+            if (mask != 0xFFFFu) {
+                if (!((mask >> r) & 1u)) s[n][0] = s[n][1] = -INFINITY;
+                if (!((mask >> (r + 8)) & 1u)) s[n][2] = s[n][3] = -INFINITY;
+            }
+            float top[2] = {fmaxf(s[n][0], s[n][2]), fmaxf(s[n][1], s[n][3])};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 4));
+                top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 8));
+                top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 16));
+                top[e] = fmaxf(top[e], m[n][e]);
+            }
+            if (__any_sync(0xFFFFFFFFu, top[0] > m[n][0] || top[1] > m[n][1])) {
+                float keep[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    keep[e] = part_factor(m[n][e], top[e]);  // from -infinity: 0
+                    m[n][e] = top[e];
+                    l[n][e] *= keep[e];
+                }
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    o[n][k].x *= keep[0], o[n][k].y *= keep[1];
+                    o[n][k].z *= keep[0], o[n][k].w *= keep[1];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float from = m[n][e & 1] == -INFINITY ? 0.f : m[n][e & 1] - kBias;
+                s[n][e] = exp2_fast(s[n][e] - from);
+                l[n][e & 1] += s[n][e];
+            }
+            // to 16 bits for the second product: fp16 rounds p by 2^-11, bf16 by 2^-8 of it
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                uint32_t v;
+                if (E4M3) {
+                    const __half2 h = __floats2half2_rn(s[n][2 * e], s[n][2 * e + 1]);
+                    v = *reinterpret_cast<const uint32_t*>(&h);
+                } else {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(s[n][2 * e], s[n][2 * e + 1]);
+                    v = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                pf[n][e] = transpose_8x8(v);
+            }
+        }
+        auto add = [&](int n, int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+            float d[4] = {o[n][k].x, o[n][k].y, o[n][k].z, o[n][k].w};
+            attn_mma<E4M3>(d, a0, a1, a2, a3, pf[n][0], pf[n][1]);
+            o[n][k] = make_float4(d[0], d[1], d[2], d[3]);
+        };
+        if (!E4M3) {
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                uint32_t f[4];
+                ldmatrix_x4_trans(f, vt + tile_offset<CH>((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+#pragma unroll
+                for (int n = 0; n < NT; ++n) add(n, k, f[0], f[1], f[2], f[3]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < KS; k += 2) {
+                uint32_t f[4];  // chunk k: tokens 0..7, 8..15, then chunk k + 1
+                ldmatrix_x4_trans(f, vt + tile_offset<CH>(lane & 15, k + (lane >> 4)));
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    // word: dims 2r, 2r + 1 of token 2c, then of token 2c + 1
+                    const uint32_t x0 = e4m3x2_to_f16x2(f[2 * j]), x1 = e4m3x2_to_f16x2(f[2 * j] >> 16);
+                    const uint32_t y0 = e4m3x2_to_f16x2(f[2 * j + 1]), y1 = e4m3x2_to_f16x2(f[2 * j + 1] >> 16);
+                    const uint32_t a0 = __byte_perm(x0, x1, 0x5410), a1 = __byte_perm(x0, x1, 0x7632);
+                    const uint32_t a2 = __byte_perm(y0, y1, 0x5410), a3 = __byte_perm(y0, y1, 0x7632);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) add(n, k + j, a0, a1, a2, a3);
+                }
+            }
+        }
+    }
+
+    __device__ __forceinline__ void reduce() {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 4);
+                l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 8);
+                l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 16);
+            }
+    }
+
+    // the row's result, all of its tokens seen (after reduce())
+    __device__ __forceinline__ void finish(const AttentionArgs& a, int b, const Heads& hd, int lane) {
+        const int r = lane >> 2, c = lane & 3;
+        const float vs = E4M3 ? a.cache.v_scale[hd.hk] : 1.f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float f[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                f[e] = l[n][e] != 0.f ? vs / l[n][e] : 0.f;
+                const int h = n * 8 + 2 * c + e;
+                if (a.lse && r == 0 && h < hd.n)
+                    a.lse[static_cast<int64_t>(b) * a.q_heads + hd.first + h] = lse_of<E4M3>(m[n][e], l[n][e]);
+            }
+            uint16_t* out = a.out + b * a.out_request + (hd.first + n * 8 + r) * a.out_head;
+            const bool have = n * 8 + r < hd.n;
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+                store_dims<E4M3>(o[n][k], f[0], f[1], have && k * 16 < a.cache.dim ? out + k * 16 : nullptr, c);
+        }
+    }
+
+    // the row's part (after reduce()): o, then m and l of every head
+    __device__ __forceinline__ void store_part(float* part, float* pm, float* pl, int lane) const {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int k = 0; k < KS; ++k) reinterpret_cast<float4*>(part)[(n * KS + k) * 32 + lane] = o[n][k];
+            if (lane < 4) {
+                reinterpret_cast<float2*>(pm)[n * 4 + lane] = make_float2(m[n][0], m[n][1]);
+                reinterpret_cast<float2*>(pl)[n * 4 + lane] = make_float2(l[n][0], l[n][1]);
+            }
+        }
+    }
+};
+
+// The block ids and the copies of consecutive tiles of a row.  Ids are loaded
+// early: where a tile lies in one block, those of 32 tiles at once (lane i:
+// tile base + i * step), else those of one tile's tokens (lanes i and i + 16:
+// token i).
+template <bool E4M3, int DP, int NT>
+struct TileCopy {
+    using Sh = AttnShape<E4M3, DP, NT>;
+    static constexpr int CH = Sh::kChunks, kBytes = E4M3 ? 1 : 2;
+    int base, id, place;
+
+    static __device__ __forceinline__ bool aligned(const AttentionArgs& a) { return a.cache.page % kTile == 0; }
+
+    // the ids for tile t (tiles of the row step apart, below t1)
+    __device__ __forceinline__ void look_up(const AttentionArgs& a, int b, const Request& q, int t, int t1, int step, int lane) {
+        base = t;
+        const bool whole = aligned(a);
+        const int tile = whole ? t + lane * step : t;
+        const int token = (q.tile0 + tile) * kTile + (whole ? 0 : lane & 15);
+        const int col = static_cast<int>(static_cast<unsigned>(token) / static_cast<unsigned>(a.cache.page));
+        place = token - col * a.cache.page;
+        id = -1;
+        if (whole ? tile < t1 : token >= q.start && token < q.len) {
+            id = a.block_table[b * a.table_stride + col];
+            if (id < 0) id = -2;
+        }
+    }
+    // whether look_up has to come before copy(t)
+    __device__ __forceinline__ bool wants(const AttentionArgs& a, int t, int step) const {
+        return aligned(a) ? t - base >= 32 * step : t != base;
+    }
+
+    // starts the copies of tile t into dst; returns the mask of the tokens the row sees
+    __device__ __forceinline__ uint32_t copy(const AttentionArgs& a, int hk, const Request& q, int t, int step, uint32_t dst, int lane,
+                                             bool& bad) const {
+        const int real_chunks = a.cache.dim * kBytes / 16;
+        const char* kp = static_cast<const char*>(a.cache.k) + hk * a.cache.k_head * kBytes;
+        const char* vp = static_cast<const char*>(a.cache.v) + hk * a.cache.v_head * kBytes;
+        uint32_t mask;
+        if (aligned(a)) {
+            const int from = (t - base) / step;
+            int64_t block = __shfl_sync(0xFFFFFFFFu, id, from);
+            const int first = __shfl_sync(0xFFFFFFFFu, place, from);
+            const int token = (q.tile0 + t) * kTile;
+            mask = q.len - token < kTile ? (1u << (q.len - token)) - 1u : 0xFFFFu;
+            if (q.start > token) mask &= 0xFFFFu << (q.start - token);
+            if (block < 0 || block >= a.cache.blocks) {
+                bad = true;
+                mask = 0u;
+                block = 0;
+            }
+            kp += (block * a.cache.k_block + first * a.cache.k_token) * kBytes;
+            vp += (block * a.cache.v_block + first * a.cache.v_token) * kBytes;
+            const int64_t ks = a.cache.k_token * kBytes, vs = a.cache.v_token * kBytes;
+#pragma unroll
+            for (int i = 0; i < kTile * CH / 32; ++i) {
+                const int row = (i * 32 + lane) / CH, ch = (i * 32 + lane) % CH;
+                const bool ok = (mask >> row) & 1u;
+                if (ch < real_chunks) {
+                    const uint32_t at = dst + tile_offset<CH>(row, ch);
+                    cp_async_16_zfill(at, kp + row * ks + ch * 16, ok);
+                    cp_async_16_zfill(at + kTile * Sh::kRowBytes, vp + row * vs + ch * 16, ok);
+                }
+            }
+        } else {
+            const bool valid = id >= 0 && id < a.cache.blocks;
+            bad |= id != -1 && !valid;
+            mask = __ballot_sync(0xFFFFFFFFu, valid) & 0xFFFFu;
+            const int64_t block = valid ? id : 0, first = valid ? place : 0;
+            const int64_t ko = (block * a.cache.k_block + first * a.cache.k_token) * kBytes;
+            const int64_t vo = (block * a.cache.v_block + first * a.cache.v_token) * kBytes;
+#pragma unroll
+            for (int i = 0; i < kTile * CH / 32; ++i) {
+                const int row = (i * 32 + lane) / CH, ch = (i * 32 + lane) % CH;
+                const int64_t kr = __shfl_sync(0xFFFFFFFFu, ko, row);
+                const int64_t vr = __shfl_sync(0xFFFFFFFFu, vo, row);
+                const bool ok = (mask >> row) & 1u;
+                if (ch < real_chunks) {
+                    const uint32_t at = dst + tile_offset<CH>(row, ch);
+                    cp_async_16_zfill(at, kp + kr + ch * 16, ok);
+                    cp_async_16_zfill(at + kTile * Sh::kRowBytes, vp + vr + ch * 16, ok);
+                }
+            }
+        }
+        return mask;
+    }
+};
+
+// Columns of a ring past dim are never copied: zeroed once.
+__device__ __forceinline__ void clear_ring(uint8_t* smem, int bytes, int thread, int threads) {
+    for (int i = thread; i < bytes / 16; i += threads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
 // n / d for n >= 0, d > 0: in 32 bits where both fit, as they do in all but
 // the largest calls (a 64-bit division takes about 200 ns here)
 __device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
@@ -149,55 +523,29 @@ struct Segment {
     Request q;
 };
 
-// float index of (head h, dim d) in a part in shared memory: swizzled so that a
-// fragment's 8 dims x 4 head pairs lie in different banks, four dims together
-template <bool E4M3, int DP>
-__device__ __forceinline__ int part_index(int h, int d) {
-    return h * DP + (d ^ (((h >> 1) & 3) * (E4M3 ? 16 : 8)));
-}
-
 template <bool E4M3, int DP, int NT>
-__global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const AttentionArgs a, const JoinPlan jp) {
+__global__ void __launch_bounds__(kShareWarps * 32, (AttnShape<E4M3, DP, NT>::kPerSm))
+    k_attention_shares(const AttentionArgs a, const JoinPlan jp) {
     using Sh = AttnShape<E4M3, DP, NT>;
-    constexpr int CH = Sh::kChunks, S = Sh::kStages, HEADS = Sh::kHeads, KS = DP / 16;
-    constexpr int kBytes = E4M3 ? 1 : 2;
-    constexpr float kBias = E4M3 ? kE4m3Bias : 0.f;
+    constexpr int S = Sh::kStages, HEADS = Sh::kHeads, KS = Sh::kSteps;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint32_t tile_mask[kAttnWarps][S];
-    // parts of a warp: 0 of the row its share begins inside of, 1 of the one it ends inside of
-    __shared__ int64_t part_at[kAttnWarps * 2];
-    __shared__ int part_b[kAttnWarps * 2], part_row[kAttnWarps * 2], part_ends[kAttnWarps * 2], part_tiles[kAttnWarps * 2];
-    __shared__ float part_m[kAttnWarps * 2][HEADS], part_l[kAttnWarps * 2][HEADS];
-    __shared__ uint32_t part_members[kAttnWarps * 2];
-    // once the rings are done, behind the first one's part: a part's factor, and the maximum and sum of its row
-    using PartFloats = float[HEADS];
-    PartFloats* const part_f = reinterpret_cast<PartFloats*>(smem + Sh::kPartBytes);
-    PartFloats *const part_top = part_f + kAttnWarps * 2, *const part_all = part_top + kAttnWarps * 2;
+    __shared__ uint32_t tile_mask[kShareWarps][S];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int r = lane >> 2, c = lane & 3;
-    const uint32_t ring = smem_addr(smem) + warp * Sh::kRingBytes;
-    auto part_of = [&](int i) -> float* {
-        return reinterpret_cast<float*>(smem + ((i & 1) ? (i >> 1) * Sh::kRingBytes
-                                                        : kAttnWarps * Sh::kRingBytes + (i >> 1) * Sh::kPartBytes));
-    };
-    const int D = a.cache.dim, G = a.q_heads / a.cache.heads;
-    const int chunks_of_group = (G + HEADS - 1) / HEADS;
-    const int rows = jp.rows;  // of a request
-    const int real_chunks = D * kBytes / 16;
+    const int worker = blockIdx.x * kShareWarps + warp;
+    const uint32_t ring = smem_addr(smem) + warp * S * Sh::kStageBytes;
+    const int rows = jp.rows;
     bool bad = false;
 
-    if (D != DP) {  // columns past dim are never copied: zero them once
-        for (int i = threadIdx.x; i < kAttnWarps * Sh::kRingBytes / 16; i += kAttnThreads)
-            reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (a.cache.dim != DP) {
+        clear_ring(smem, Sh::kSmem, threadIdx.x, kShareWarps * 32);
+        __syncthreads();
     }
-    if (threadIdx.x < kAttnWarps * 2) part_b[threadIdx.x] = -1;
-    __syncthreads();
     grid_dependency_wait();
     grid_dependents_launch();
 
-    // --- the share of each warp ---------------------------------------------
+    // --- the share of the warp ----------------------------------------------
     // Every warp forms the costs of all requests itself, kScan of them at a
-    // time (lane i: kPer in a row from kPer * i on): no barrier is needed.
+    // time (lane i: kPer in a row from kPer * i on).
     constexpr int kPer = 4, kScan = 32 * kPer;
     int64_t cost[kPer];  // of this lane's requests
     // the costs of requests base .. base + kScan - 1; returns those before this lane's, `sum`: all
@@ -229,29 +577,23 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
     // requests without tokens
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         if (request_of(a, b, bad).tiles > 0) continue;
-        for (int i = threadIdx.x; i < a.q_heads * (D / 8); i += kAttnThreads) {
-            const int h = i / (D / 8), d = (i - h * (D / 8)) * 8;
-            *reinterpret_cast<uint4*>(a.out + b * a.out_request + h * a.out_head + d) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        if (a.lse)
-            for (int h = threadIdx.x; h < a.q_heads; h += kAttnThreads)
-                a.lse[static_cast<int64_t>(b) * a.q_heads + h] = -INFINITY;
+        store_empty(a, b, 0, a.q_heads, threadIdx.x, kShareWarps * 32);
         if (jp.split && jp.by_row)
-            for (int i = threadIdx.x; i < rows; i += kAttnThreads) jp.joins[b * rows + i] = make_int4(-1, 0, 0, 0);
+            for (int i = threadIdx.x; i < rows; i += kShareWarps * 32) jp.joins[b * rows + i] = make_int4(-1, 0, 0, 0);
     }
-    const int64_t want = quotient(total + kMinCost * kAttnWarps - 1, kMinCost * kAttnWarps);
-    int ctas = want < gridDim.x ? static_cast<int>(want) : static_cast<int>(gridDim.x);
+    const int64_t want = quotient(total + kMinCost - 1, kMinCost);
+    int workers = want < jp.warps ? static_cast<int>(want) : jp.warps;
     // one request: rows of one length, so a multiple of them splits none unevenly
-    if (a.B == 1 && ctas > rows) ctas -= ctas % rows;
-    if (static_cast<int>(blockIdx.x) >= ctas) {
-        if (jp.split && !jp.by_row && threadIdx.x == 0) jp.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (a.B == 1 && workers > rows) workers -= workers % rows;
+    if (jp.split && !jp.by_row && lane == 0) jp.joins[worker] = make_int4(-1, 0, 0, 0);
+    if (worker >= workers) {
         if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
         return;
     }
-    // costs before CTA i: equal shares, the remainder to the first ones
-    const int64_t share = quotient(total, ctas), extra = total - share * ctas;
-    auto cta_begin = [&](int i) { return i * share + (i < extra ? i : extra); };
-    auto cta_of = [&](int64_t u) {
+    // costs before worker i: equal shares, the remainder to the first ones
+    const int64_t share = quotient(total, workers), extra = total - share * workers;
+    auto begin_of = [&](int i) { return i * share + (i < extra ? i : extra); };
+    auto worker_of = [&](int64_t u) {
         const int64_t big = extra * (share + 1);
         return static_cast<int>(u < big ? quotient(u, share + 1) : extra + quotient(u - big, share));
     };
@@ -281,21 +623,19 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
         }
         return false;
     };
-    int64_t begin = cta_begin(blockIdx.x), end = cta_begin(blockIdx.x + 1);
+    int64_t u0 = begin_of(worker), u1 = begin_of(worker + 1);
     int first_b = 0;
     int64_t first_at = 0;
     if (!jp.split) {
         // whole rows: from the first that begins in the share to the last that does
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
-            int64_t& u = i ? end : begin;
+            int64_t& u = i ? u1 : u0;
             if (u >= total || !locate(u, first_b, first_at)) continue;
             const int n = request_of(a, first_b, bad).tiles + kRowCost;
             u = first_at + quotient(u - first_at + n - 1, n) * n;
         }
     }
-    static_assert(kAttnWarps == 4, "shares of four warps");
-    const int64_t u0 = begin + ((end - begin) * warp >> 2), u1 = begin + ((end - begin) * (warp + 1) >> 2);
 
     // --- the rows of a share, in order ---------------------------------------
     auto open_segment = [&](Segment& s) {
@@ -328,493 +668,304 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attention_mma(const Atte
     }
 
     // The copies run ahead of the products: `ahead` is the segment of the next
-    // tile to copy, ahead_t the tile.  Block ids are loaded early: where a tile
-    // lies in one block, those of 32 tiles at once (lane i: tile win_t + i),
-    // else those of the next tile's tokens (lanes i and i + 16: token i).
+    // tile to copy, ahead_t the tile.
+    RowMath<E4M3, DP, NT> math;
+    TileCopy<E4M3, DP, NT> copy;
     Segment ahead = seg;
-    int ahead_t = seg.t0, win_t = seg.t0 - 32;
+    int ahead_t = seg.t0, ahead_hk = heads_of<HEADS>(a, seg.row).hk;
     bool more = live;
-    int ahead_id = -1, ahead_place = 0;
-    const bool aligned_pages = a.cache.page % kTile == 0;
-    auto settle = [&]() {
-        if (more && ahead_t >= ahead.t1) {
-            more = next_segment(ahead);
-            ahead_t = ahead.t0;
-            win_t = ahead_t - 32;
-        }
-        if (!more || (aligned_pages && ahead_t < win_t + 32)) return;
-        win_t = ahead_t;
-        const int token = aligned_pages ? (ahead.q.tile0 + ahead_t + lane) * kTile
-                                        : (ahead.q.tile0 + ahead_t) * kTile + (lane & 15);
-        const int col = static_cast<int>(static_cast<unsigned>(token) / static_cast<unsigned>(a.cache.page));
-        ahead_place = token - col * a.cache.page;
-        ahead_id = -1;
-        if (aligned_pages ? ahead_t + lane < ahead.t1 : token >= ahead.q.start && token < ahead.q.len) {
-            ahead_id = a.block_table[ahead.b * a.table_stride + col];
-            if (ahead_id < 0) ahead_id = -2;
-        }
-    };
-    auto copy_tile = [&](int slot) {
-        if (more) {
-            const int hk = ahead.row / chunks_of_group;
-            const char* kp = static_cast<const char*>(a.cache.k) + hk * a.cache.k_head * kBytes;
-            const char* vp = static_cast<const char*>(a.cache.v) + hk * a.cache.v_head * kBytes;
-            const uint32_t dst = ring + slot * Sh::kStageBytes;
-            uint32_t mask;  // the tokens of the tile that the row sees
-            if (aligned_pages) {
-                int64_t id = __shfl_sync(0xFFFFFFFFu, ahead_id, ahead_t - win_t);
-                const int place = __shfl_sync(0xFFFFFFFFu, ahead_place, ahead_t - win_t);
-                const int token = (ahead.q.tile0 + ahead_t) * kTile;
-                mask = ahead.q.len - token < kTile ? (1u << (ahead.q.len - token)) - 1u : 0xFFFFu;
-                if (ahead.q.start > token) mask &= 0xFFFFu << (ahead.q.start - token);
-                if (id < 0 || id >= a.cache.blocks) {
-                    bad = true;
-                    mask = 0u;
-                    id = 0;
-                }
-                kp += (id * a.cache.k_block + place * a.cache.k_token) * kBytes;
-                vp += (id * a.cache.v_block + place * a.cache.v_token) * kBytes;
-                const int64_t kt = a.cache.k_token * kBytes, vt = a.cache.v_token * kBytes;
-#pragma unroll
-                for (int i = 0; i < kTile * CH / 32; ++i) {
-                    const int row = (i * 32 + lane) / CH, ch = (i * 32 + lane) % CH;
-                    const bool ok = (mask >> row) & 1u;
-                    if (ch < real_chunks) {
-                        const uint32_t at = dst + tile_offset<CH>(row, ch);
-                        cp_async_16_zfill(at, kp + row * kt + ch * 16, ok);
-                        cp_async_16_zfill(at + kTile * Sh::kRowBytes, vp + row * vt + ch * 16, ok);
-                    }
-                }
-            } else {
-                const bool valid = ahead_id >= 0 && ahead_id < a.cache.blocks;
-                bad |= ahead_id != -1 && !valid;
-                mask = __ballot_sync(0xFFFFFFFFu, valid) & 0xFFFFu;
-                const int64_t id = valid ? ahead_id : 0, place = valid ? ahead_place : 0;
-                const int64_t ko = (id * a.cache.k_block + place * a.cache.k_token) * kBytes;
-                const int64_t vo = (id * a.cache.v_block + place * a.cache.v_token) * kBytes;
-#pragma unroll
-                for (int i = 0; i < kTile * CH / 32; ++i) {
-                    const int row = (i * 32 + lane) / CH, ch = (i * 32 + lane) % CH;
-                    const int64_t kr = __shfl_sync(0xFFFFFFFFu, ko, row);
-                    const int64_t vr = __shfl_sync(0xFFFFFFFFu, vo, row);
-                    const bool ok = (mask >> row) & 1u;
-                    if (ch < real_chunks) {
-                        const uint32_t at = dst + tile_offset<CH>(row, ch);
-                        cp_async_16_zfill(at, kp + kr + ch * 16, ok);
-                        cp_async_16_zfill(at + kTile * Sh::kRowBytes, vp + vr + ch * 16, ok);
-                    }
-                }
-            }
-            if (lane == 0) tile_mask[warp][slot] = mask;
-            ++ahead_t;
-            settle();
-        }
-        cp_async_commit();
-    };
-
-    settle();
+    if (more) copy.look_up(a, ahead.b, ahead.q, ahead_t, ahead.t1, 1, lane);
     // One step of the loop copies a tile and, once the ring is full, works on
     // the oldest one.
     int t = seg.t0, put = 0, slot = 0, primed = 0;
     bool fresh = true;  // the next tile is the first of its row here
-    int hk = 0, head0 = 0, heads = 0;  // key/value head, first query head and their number
-    uint32_t qf[NT][KS][2];            // queries as B fragments (columns: heads)
-    float sl[NT][2];                   // score scale of columns 2c, 2c + 1
-    float m[NT][2], l[NT][2], o[NT][KS][4];
+    Heads hd{};
     while (live) {
         if (fresh) {
             // the queries are requested before the tiles, which they would queue behind
             fresh = false;
-            hk = seg.row / chunks_of_group;
-            const int chunk = seg.row - hk * chunks_of_group;
-            head0 = hk * G + chunk * HEADS;
-            heads = min(HEADS, G - chunk * HEADS);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const uint16_t* qp = a.q + seg.b * a.q_request + (head0 + n * 8 + r) * a.q_head;
-                const bool have = n * 8 + r < heads;
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    qf[n][k][0] = qf[n][k][1] = 0u;
-                    if (have && k * 16 < D) {
-                        // bf16: dims 2c, 2c + 1 and 8 further; e4m3: the four dims whose codes one word holds
-                        const int d = k * 16 + (E4M3 ? 4 * c : 2 * c);
-                        qf[n][k][0] = *reinterpret_cast<const uint32_t*>(qp + d);
-                        qf[n][k][1] = *reinterpret_cast<const uint32_t*>(qp + d + (E4M3 ? 2 : 8));
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    m[n][e] = -INFINITY;
-                    l[n][e] = 0.f;
-                }
-#pragma unroll
-                for (int k = 0; k < KS; ++k)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[n][k][e] = 0.f;
-            }
+            hd = heads_of<HEADS>(a, seg.row);
+            math.begin(a, seg.b, hd, lane);
             // and those of the row after this one brought to L2
-            const int after_b = seg.row + 1 < rows ? seg.b : seg.b + 1, after_row = seg.row + 1 < rows ? seg.row + 1 : 0;
+            const int after_b = seg.row + 1 < rows ? seg.b : seg.b + 1;
             if (after_b < a.B) {
-                const int g = after_row / chunks_of_group, h = (after_row - g * chunks_of_group) * HEADS;
-                for (int i = lane; i < min(HEADS, G - h) * KS / 4; i += 32)
-                    if ((i % (KS / 4)) * 64 < D)
-                        prefetch_l2(a.q + after_b * a.q_request + (g * G + h + i / (KS / 4)) * a.q_head + (i % (KS / 4)) * 64);
+                const Heads h = heads_of<HEADS>(a, seg.row + 1 < rows ? seg.row + 1 : 0);
+                for (int i = lane; i < h.n * KS / 4; i += 32)
+                    if ((i % (KS / 4)) * 64 < a.cache.dim)
+                        prefetch_l2(a.q + after_b * a.q_request + (h.first + i / (KS / 4)) * a.q_head + (i % (KS / 4)) * 64);
             }
         }
         const bool full = primed == S - 1;
         if (full) cp_async_wait_group<S - 2>();
         __syncwarp();
-        copy_tile(put);
+        if (more) {
+            const uint32_t mask = copy.copy(a, ahead_hk, ahead.q, ahead_t, 1, ring + put * Sh::kStageBytes, lane, bad);
+            if (lane == 0) tile_mask[warp][put] = mask;
+            bool look = false;
+            if (++ahead_t >= ahead.t1) {
+                more = look = next_segment(ahead);
+                ahead_t = ahead.t0;
+                ahead_hk = heads_of<HEADS>(a, ahead.row).hk;
+            }
+            if (more && (look || copy.wants(a, ahead_t, 1))) copy.look_up(a, ahead.b, ahead.q, ahead_t, ahead.t1, 1, lane);
+        }
+        cp_async_commit();
         put = put + 1 == S ? 0 : put + 1;
         if (!full) {
             ++primed;
             continue;
         }
-        if (t == seg.t0) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                sl[n][0] = sl[n][1] = a.scale * 1.4426950408889634f * (E4M3 ? a.cache.k_scale[hk] : 1.f);
-                if (E4M3) {
-                    // to fp16, scaled by a power of two that takes the head's largest into [2^14, 2^15)
-                    uint32_t big = 0u;
-#pragma unroll
-                    for (int k = 0; k < KS; ++k)
-                        big = __vmaxu2(big, __vmaxu2(qf[n][k][0] & 0x7FFF7FFFu, qf[n][k][1] & 0x7FFF7FFFu));
-                    big = max(big & 0xFFFFu, big >> 16);
-                    big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
-                    big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
-                    const int eb = min(static_cast<int>(big >> 7), 254);
-                    const int sh = min(141 - eb, 126);
-                    const float up = exp2i(sh), down = exp2i(-sh);
-#pragma unroll
-                    for (int k = 0; k < KS; ++k)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t v = qf[n][k][e];
-                            const __half2 h = __floats2half2_rn(bf16_to_f32(v & 0xFFFFu) * up, bf16_to_f32(v >> 16) * up);
-                            qf[n][k][e] = *reinterpret_cast<const uint32_t*>(&h);
-                        }
-                    sl[n][0] *= __shfl_sync(0xFFFFFFFFu, down, 8 * c);
-                    sl[n][1] *= __shfl_sync(0xFFFFFFFFu, down, 8 * c + 4);
-                }
-            }
-        }
-        {
-            const uint32_t kt = ring + slot * Sh::kStageBytes, vt = kt + kTile * Sh::kRowBytes;
-            const uint32_t mask = tile_mask[warp][slot];
-            slot = slot + 1 == S ? 0 : slot + 1;
-
-            float s[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
-            if (!E4M3) {
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    uint32_t f[4];
-                    ldmatrix_x4(f, kt + tile_offset<CH>(lane & 15, 2 * k + (lane >> 4)));
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) attn_mma<E4M3>(s[n], f[0], f[1], f[2], f[3], qf[n][k][0], qf[n][k][1]);
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < KS; k += 2) {
-                    uint32_t f[4];  // two chunks of 16 codes: rows r and r + 8 of each
-                    ldmatrix_x4(f, kt + tile_offset<CH>(lane & 15, k + (lane >> 4)));
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t a0 = e4m3x2_to_f16x2(f[2 * j]), a2 = e4m3x2_to_f16x2(f[2 * j] >> 16);
-                        const uint32_t a1 = e4m3x2_to_f16x2(f[2 * j + 1]), a3 = e4m3x2_to_f16x2(f[2 * j + 1] >> 16);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            attn_mma<E4M3>(s[n], a0, a1, a2, a3, qf[n][k + j][0], qf[n][k + j][1]);
-                    }
-                }
-            }
-            uint32_t pf[NT][2];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] *= sl[n][e & 1];
-                if (mask != 0xFFFFu) {
-                    const bool lo = (mask >> r) & 1u, hi = (mask >> (r + 8)) & 1u;
-                    if (!lo) s[n][0] = s[n][1] = -INFINITY;
-                    if (!hi) s[n][2] = s[n][3] = -INFINITY;
-                }
-                float top[2] = {fmaxf(s[n][0], s[n][2]), fmaxf(s[n][1], s[n][3])};
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 4));
-                    top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 8));
-                    top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 16));
-                    top[e] = fmaxf(top[e], m[n][e]);
-                }
-                if (__any_sync(0xFFFFFFFFu, top[0] > m[n][0] || top[1] > m[n][1])) {
-                    float keep[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        keep[e] = m[n][e] == top[e] ? 1.f : exp2_fast(m[n][e] - top[e]);  // -inf: 0
-                        m[n][e] = top[e];
-                        l[n][e] *= keep[e];
-                    }
-#pragma unroll
-                    for (int k = 0; k < KS; ++k)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[n][k][e] *= keep[e & 1];
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float from = m[n][e & 1] == -INFINITY ? 0.f : m[n][e & 1] - kBias;
-                    s[n][e] = exp2_fast(s[n][e] - from);
-                    l[n][e & 1] += s[n][e];
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    uint32_t v;
-                    if (E4M3) {
-                        const __half2 h = __floats2half2_rn(s[n][2 * e], s[n][2 * e + 1]);
-                        v = *reinterpret_cast<const uint32_t*>(&h);
-                    } else {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(s[n][2 * e], s[n][2 * e + 1]);
-                        v = *reinterpret_cast<const uint32_t*>(&h);
-                    }
-                    pf[n][e] = transpose_8x8(v);
-                }
-            }
-            if (!E4M3) {
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    uint32_t f[4];
-                    ldmatrix_x4_trans(f, vt + tile_offset<CH>((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) attn_mma<E4M3>(o[n][k], f[0], f[1], f[2], f[3], pf[n][0], pf[n][1]);
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < KS; k += 2) {
-                    uint32_t f[4];  // chunk k: tokens 0..7, 8..15, then chunk k + 1
-                    ldmatrix_x4_trans(f, vt + tile_offset<CH>(lane & 15, k + (lane >> 4)));
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        // word: dims 2r, 2r + 1 of token 2c, then of token 2c + 1
-                        const uint32_t x0 = e4m3x2_to_f16x2(f[2 * j]), x1 = e4m3x2_to_f16x2(f[2 * j] >> 16);
-                        const uint32_t y0 = e4m3x2_to_f16x2(f[2 * j + 1]), y1 = e4m3x2_to_f16x2(f[2 * j + 1] >> 16);
-                        const uint32_t a0 = __byte_perm(x0, x1, 0x5410), a1 = __byte_perm(x0, x1, 0x7632);
-                        const uint32_t a2 = __byte_perm(y0, y1, 0x5410), a3 = __byte_perm(y0, y1, 0x7632);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            attn_mma<E4M3>(o[n][k + j], a0, a1, a2, a3, pf[n][0], pf[n][1]);
-                    }
-                }
-            }
-        }
-
+        if (t == seg.t0) math.ready(a, hd.hk, lane);
+        math.tile(ring + slot * Sh::kStageBytes, tile_mask[warp][slot], lane);
+        slot = slot + 1 == S ? 0 : slot + 1;
         if (++t < seg.t1) continue;
 
-        // --- the result of the segment ---------------------------------------
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 4);
-                l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 8);
-                l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 16);
-            }
+        math.reduce();
         const bool begins = seg.t0 == 0, ends = seg.t1 == seg.q.tiles;
         if (begins && ends) {
-            const float vs = E4M3 ? a.cache.v_scale[hk] : 1.f;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float f[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    f[e] = l[n][e] != 0.f ? vs / l[n][e] : 0.f;
-                    const int h = n * 8 + 2 * c + e;
-                    if (a.lse && r == 0 && h < heads)
-                        a.lse[static_cast<int64_t>(seg.b) * a.q_heads + head0 + h] =
-                            l[n][e] != 0.f ? (m[n][e] + (log2f(l[n][e]) - kBias)) * 0.6931471805599453f : -INFINITY;
-                }
-                // transposed to dims along the lanes of a head
-                uint16_t* out = a.out + seg.b * a.out_request + (head0 + n * 8 + r) * a.out_head;
-                const bool have = n * 8 + r < heads;
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    uint32_t v[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const __nv_bfloat162 p = __floats2bfloat162_rn(o[n][k][2 * e] * f[0], o[n][k][2 * e + 1] * f[1]);
-                        v[e] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&p));
-                    }
-                    if (have && k * 16 < D) {
-                        if (E4M3) {  // rows of the product: even dims, then odd ones
-                            *reinterpret_cast<uint2*>(out + k * 16 + 4 * c) =
-                                make_uint2(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[0], v[1], 0x7632));
-                        } else {
-                            *reinterpret_cast<uint32_t*>(out + k * 16 + 2 * c) = v[0];
-                            *reinterpret_cast<uint32_t*>(out + k * 16 + 8 + 2 * c) = v[1];
-                        }
-                    }
-                }
-            }
-            if (jp.split && jp.by_row && lane == 0) jp.joins[seg.b * rows + seg.row] = make_int4(-1, 0, 0, 0);
+            math.finish(a, seg.b, hd, lane);
         } else {
-            const int i = warp * 2 + (begins ? 1 : 0);
-            if (begins) {  // the last tiles of the share: the ring is free
-                cp_async_wait_group<0>();
-                __syncwarp();
-            }
-            float* part = part_of(i);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int h = n * 8 + 2 * c + e;
-                    if (r == 0) {
-                        part_m[i][h] = m[n][e];
-                        part_l[i][h] = l[n][e];
-                    }
-#pragma unroll
-                    for (int k = 0; k < KS; ++k) {
-                        if (E4M3) {
-                            *reinterpret_cast<float2*>(part + part_index<E4M3, DP>(h, k * 16 + 2 * r)) =
-                                make_float2(o[n][k][e], o[n][k][2 + e]);
-                        } else {
-                            part[part_index<E4M3, DP>(h, k * 16 + r)] = o[n][k][e];
-                            part[part_index<E4M3, DP>(h, k * 16 + r + 8)] = o[n][k][2 + e];
-                        }
-                    }
-                }
-            if (lane == 0) {
-                part_b[i] = seg.b;
-                part_row[i] = seg.row;
-                part_ends[i] = (begins ? 1 : 0) | (ends ? 2 : 0);
-                part_at[i] = seg.at + kRowCost;
-                part_tiles[i] = seg.q.tiles;
-            }
+            float* part = jp.part + (static_cast<int64_t>(worker) * 2 + (begins ? 1 : 0)) * Sh::kPartFloats;
+            math.store_part(part, part + HEADS * DP, part + HEADS * (DP + 1), lane);
         }
+        // a row that begins here: what the join launch has to do for it
+        if (jp.split && begins && lane == 0 && (jp.by_row || !ends))
+            jp.joins[jp.by_row ? seg.b * rows + seg.row : worker] =
+                ends ? make_int4(-1, 0, 0, 0) : make_int4(seg.b, seg.row, worker, worker_of(seg.at + kRowCost + seg.q.tiles - 1));
         live = next_segment(seg);
         t = seg.t0;
         fresh = true;
     }
     cp_async_wait_group<0>();
-    __syncthreads();
+    if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
+}
 
-    // --- parts of one row become one -----------------------------------------
-    // thread (i, h): the factor of part i's head h, and what part i leads
-    for (int x = threadIdx.x; x < kAttnWarps * 2 * HEADS; x += kAttnThreads) {
-        const int i = x / HEADS, h = x - i * HEADS;
-        if (part_b[i] < 0) continue;
-        float top = -INFINITY, all = 0.f;
-        uint32_t members = 0u;
+// Joins the parts of a row: grid (row, slice of its accumulators); threads
+// (x: accumulators, y: group, of which each takes every n-th part, so that
+// many parts are on their way at once).
+constexpr int kJoinThreads = 256;
+constexpr int kJoinDepth = 4;  // parts a thread requests together
+
+template <bool E4M3, int DP, int NT>
+__global__ void __launch_bounds__(kJoinThreads) k_attention_join(const AttentionArgs a, const JoinPlan jp) {
+    using Sh = AttnShape<E4M3, DP, NT>;
+    constexpr int HEADS = Sh::kHeads, KS = Sh::kSteps;
+    struct Sum {
+        float4 o;
+        float m[2], l[2];
+    };
+    __shared__ Sum sums[kJoinThreads];
+    grid_dependents_launch();
+    grid_dependency_wait();
+    const int4 d = __ldcg(jp.joins + blockIdx.x);
+    if (d.x < 0) return;
+    const int unit = blockIdx.y * blockDim.x + threadIdx.x;  // accumulator: (head block n, step k, lane)
+    const int lane = unit & 31, k = (unit >> 5) % KS, n = (unit >> 5) / KS, c = lane & 3, r = lane >> 2;
+    Sum s{make_float4(0.f, 0.f, 0.f, 0.f), {-INFINITY, -INFINITY}, {0.f, 0.f}};
+    auto add = [&](const float4& o, float2 m, float2 l) {
+        const float pm[2] = {m.x, m.y}, pl[2] = {l.x, l.y};
+        float f0[2], f1[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float top = pl[e] != 0.f ? fmaxf(s.m[e], pm[e]) : s.m[e];
+            f0[e] = part_factor(s.m[e], top);
+            f1[e] = pl[e] != 0.f ? part_factor(pm[e], top) : 0.f;
+            s.m[e] = top;
+            s.l[e] = s.l[e] * f0[e] + pl[e] * f1[e];
+        }
+        s.o.x = s.o.x * f0[0] + o.x * f1[0], s.o.y = s.o.y * f0[1] + o.y * f1[1];
+        s.o.z = s.o.z * f0[0] + o.z * f1[0], s.o.w = s.o.w * f0[1] + o.w * f1[1];
+    };
 #pragma unroll 1
-        for (int j = 0; j < kAttnWarps * 2; ++j)
-            if (part_b[j] == part_b[i] && part_row[j] == part_row[i]) {
-                members |= 1u << j;
-                top = fmaxf(top, part_m[j][h]);
-            }
-#pragma unroll 1
-        for (int j = 0; j < kAttnWarps * 2; ++j)
-            if ((members >> j) & 1u)
-                if (part_l[j][h] != 0.f) all += part_l[j][h] * (part_m[j][h] == top ? 1.f : exp2_fast(part_m[j][h] - top));
-        part_f[i][h] = part_l[i][h] != 0.f ? (part_m[i][h] == top ? 1.f : exp2_fast(part_m[i][h] - top)) : 0.f;
-        part_top[i][h] = top;
-        part_all[i][h] = all;
-        if (h == 0) part_members[i] = members;
-    }
-    if (jp.split && !jp.by_row && threadIdx.x == 0) jp.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    __syncthreads();
-#pragma unroll 1
-    for (int i = 0; i < kAttnWarps * 2; ++i) {
-        if (part_b[i] < 0) continue;
-        const uint32_t members = part_members[i];
-        if (members & ((1u << i) - 1u)) continue;  // an earlier part leads
-        const int b = part_b[i], row = part_row[i], final_part = 31 - __clz(members);
-        const int flags = part_ends[i] | part_ends[final_part];
-        const int hk_i = row / chunks_of_group, chunk = row - hk_i * chunks_of_group;
-        const int head_i = hk_i * G + chunk * HEADS, n = min(HEADS, G - chunk * HEADS);
-        const bool whole = flags == 3;
-        const float vs = E4M3 ? a.cache.v_scale[hk_i] : 1.f;
-        float* const to = jp.part + (static_cast<int64_t>(blockIdx.x) * 2 + (flags & 1)) * (HEADS * (DP + 2));
-#pragma unroll 1
-        for (int item = threadIdx.x; item < n * (DP / 4); item += kAttnThreads) {
-            const int h = item / (DP / 4), d = (item % (DP / 4)) * 4;
-            if (d >= D) continue;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-            for (uint32_t left = members; left; left &= left - 1u) {
-                const int j = __ffs(left) - 1;
-                const float f = part_f[j][h];
-                if (f == 0.f) continue;  // nothing there: the part may hold anything
-                const float4 x = *reinterpret_cast<const float4*>(part_of(j) + part_index<E4M3, DP>(h, d));
-                v.x = fmaf(x.x, f, v.x), v.y = fmaf(x.y, f, v.y);
-                v.z = fmaf(x.z, f, v.z), v.w = fmaf(x.w, f, v.w);
-            }
-            const float all = part_all[i][h];
-            if (whole) {
-                const float f = all != 0.f ? vs / all : 0.f;
-                const uint32_t lo = f32_to_bf16_rn(v.x * f) | (static_cast<uint32_t>(f32_to_bf16_rn(v.y * f)) << 16);
-                const uint32_t hi = f32_to_bf16_rn(v.z * f) | (static_cast<uint32_t>(f32_to_bf16_rn(v.w * f)) << 16);
-                *reinterpret_cast<uint2*>(a.out + b * a.out_request + (head_i + h) * a.out_head + d) = make_uint2(lo, hi);
-                if (d == 0 && a.lse)
-                    a.lse[static_cast<int64_t>(b) * a.q_heads + head_i + h] =
-                        all != 0.f ? (part_top[i][h] + (log2f(all) - kBias)) * 0.6931471805599453f : -INFINITY;
-            } else {
-                *reinterpret_cast<float4*>(to + h * DP + d) = v;
-                if (d == 0) {
-                    to[HEADS * DP + h] = part_top[i][h];
-                    to[HEADS * (DP + 1) + h] = all;
-                }
+    for (int q = d.z + static_cast<int>(threadIdx.y); q <= d.w; q += blockDim.y * kJoinDepth) {
+        float4 o[kJoinDepth];
+        float2 m[kJoinDepth], l[kJoinDepth];
+#pragma unroll
+        for (int i = 0; i < kJoinDepth; ++i) {
+            const int p = q + i * blockDim.y;
+            o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            m[i] = l[i] = make_float2(0.f, 0.f);
+            if (p <= d.w) {
+                const float* part = jp.part + (static_cast<int64_t>(p) * 2 + (p == d.z ? 1 : 0)) * Sh::kPartFloats;
+                o[i] = __ldcg(reinterpret_cast<const float4*>(part) + unit);
+                m[i] = __ldcg(reinterpret_cast<const float2*>(part + HEADS * DP) + n * 4 + c);
+                l[i] = __ldcg(reinterpret_cast<const float2*>(part + HEADS * (DP + 1)) + n * 4 + c);
             }
         }
-        // a row that begins here: what the join launch has to do for it
-        if (jp.split && threadIdx.x == 0 && (flags & 1) && (jp.by_row || !whole))
-            jp.joins[jp.by_row ? b * rows + row : static_cast<int>(blockIdx.x)] =
-                make_int4(whole ? -1 : b, row, static_cast<int>(blockIdx.x), cta_of(part_at[i] + part_tiles[i] - 1));
+#pragma unroll
+        for (int i = 0; i < kJoinDepth; ++i) add(o[i], m[i], l[i]);
+    }
+    if (blockDim.y > 1) {
+        sums[threadIdx.y * blockDim.x + threadIdx.x] = s;
+        __syncthreads();
+        if (threadIdx.y > 0) return;
+#pragma unroll 1
+        for (int g = 1; g < blockDim.y; ++g) {
+            const Sum& x = sums[g * blockDim.x + threadIdx.x];
+            add(x.o, make_float2(x.m[0], x.m[1]), make_float2(x.l[0], x.l[1]));
+        }
+    }
+    const Heads hd = heads_of<HEADS>(a, d.y);
+    const float vs = E4M3 ? a.cache.v_scale[hd.hk] : 1.f;
+    const float f0 = s.l[0] != 0.f ? vs / s.l[0] : 0.f, f1 = s.l[1] != 0.f ? vs / s.l[1] : 0.f;
+    const bool have = n * 8 + r < hd.n && k * 16 < a.cache.dim;
+    uint16_t* out = a.out + d.x * a.out_request + (hd.first + n * 8 + r) * a.out_head + k * 16;
+    store_dims<E4M3>(s.o, f0, f1, have ? out : nullptr, c);
+    if (a.lse && k == 0 && r == 0)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int h = n * 8 + 2 * c + e;
+            if (h < hd.n) a.lse[static_cast<int64_t>(d.x) * a.q_heads + hd.first + h] = lse_of<E4M3>(s.m[e], s.l[e]);
+        }
+}
+
+// One row per CTA.
+template <bool E4M3, int DP, int NT>
+__global__ void __launch_bounds__(kRowWarps * 32, 1) k_attention_rows(const AttentionArgs a, const int rows) {
+    using Sh = AttnShape<E4M3, DP, NT>;
+    constexpr int S = Sh::kRowStages, HEADS = Sh::kHeads, KS = Sh::kSteps;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint32_t tile_mask[kRowWarps][S];
+    __shared__ float part_m[kRowWarps][HEADS], part_l[kRowWarps][HEADS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t ring = smem_addr(smem) + warp * S * Sh::kStageBytes;
+    const int b = static_cast<int>(blockIdx.x) / rows, row = static_cast<int>(blockIdx.x) - b * rows;
+    const Heads hd = heads_of<HEADS>(a, row);
+    bool bad = false;
+    if (a.cache.dim != DP) {
+        clear_ring(smem, Sh::kRowSmem, threadIdx.x, kRowWarps * 32);
+        __syncthreads();
+    }
+    grid_dependency_wait();
+    grid_dependents_launch();
+    RowMath<E4M3, DP, NT> math;
+    math.begin(a, b, hd, lane);
+    const Request q = request_of(a, b, bad);
+    if (q.tiles == 0) {
+        store_empty(a, b, hd.first, hd.n, threadIdx.x, kRowWarps * 32);
+        if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
+        return;
+    }
+    TileCopy<E4M3, DP, NT> copy;
+    int ahead = warp, put = 0, slot = 0, primed = 0;
+    if (ahead < q.tiles) copy.look_up(a, b, q, ahead, q.tiles, kRowWarps, lane);
+    for (int t = warp; t < q.tiles;) {
+        const bool full = primed == S - 1;
+        if (full) cp_async_wait_group<S - 2>();
+        __syncwarp();
+        if (ahead < q.tiles) {
+            const uint32_t mask = copy.copy(a, hd.hk, q, ahead, kRowWarps, ring + put * Sh::kStageBytes, lane, bad);
+            if (lane == 0) tile_mask[warp][put] = mask;
+            ahead += kRowWarps;
+            if (ahead < q.tiles && copy.wants(a, ahead, kRowWarps)) copy.look_up(a, b, q, ahead, q.tiles, kRowWarps, lane);
+        }
+        cp_async_commit();
+        put = put + 1 == S ? 0 : put + 1;
+        if (!full) {
+            ++primed;
+            continue;
+        }
+        if (t == warp) math.ready(a, hd.hk, lane);
+        math.tile(ring + slot * Sh::kStageBytes, tile_mask[warp][slot], lane);
+        slot = slot + 1 == S ? 0 : slot + 1;
+        t += kRowWarps;
+    }
+    cp_async_wait_group<0>();
+    __syncwarp();
+    math.reduce();
+    math.store_part(reinterpret_cast<float*>(smem + warp * S * Sh::kStageBytes), part_m[warp], part_l[warp], lane);
+    __syncthreads();
+    const int used = min(q.tiles, kRowWarps);  // warps that had a tile
+    const int r = lane >> 2, c = lane & 3;
+    const float vs = E4M3 ? a.cache.v_scale[hd.hk] : 1.f;
+#pragma unroll 1
+    for (int u = warp; u < NT * KS; u += kRowWarps) {
+        const int n = u / KS, k = u % KS;
+        float top[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll 1
+        for (int w = 0; w < used; ++w)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) top[e] = fmaxf(top[e], part_m[w][n * 8 + 2 * c + e]);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int w = 0; w < used; ++w) {
+            float f[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float pl = part_l[w][n * 8 + 2 * c + e];
+                f[e] = pl != 0.f ? part_factor(part_m[w][n * 8 + 2 * c + e], top[e]) : 0.f;
+                l[e] += pl * f[e];
+            }
+            const float4 x = reinterpret_cast<const float4*>(smem + w * S * Sh::kStageBytes)[u * 32 + lane];
+            o.x += x.x * f[0], o.y += x.y * f[1], o.z += x.z * f[0], o.w += x.w * f[1];
+        }
+        const float f0 = l[0] != 0.f ? vs / l[0] : 0.f, f1 = l[1] != 0.f ? vs / l[1] : 0.f;
+        const bool have = n * 8 + r < hd.n && k * 16 < a.cache.dim;
+        uint16_t* out = a.out + b * a.out_request + (hd.first + n * 8 + r) * a.out_head + k * 16;
+        store_dims<E4M3>(o, f0, f1, have ? out : nullptr, c);
+        if (a.lse && k == 0 && r == 0)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (n * 8 + 2 * c + e < hd.n)
+                    a.lse[static_cast<int64_t>(b) * a.q_heads + hd.first + n * 8 + 2 * c + e] = lse_of<E4M3>(top[e], l[e]);
     }
     if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
 }
 
-template <bool E4M3, int DP, int NT>
-cudaError_t launch_attention_shape(const AttentionArgs& a, const DeviceInfo& dev, JoinPlan& ws,
-                                   cudaStream_t s) {
-    using Sh = AttnShape<E4M3, DP, NT>;
-    const void* kernel = reinterpret_cast<const void*>(k_paged_attention_mma<E4M3, DP, NT>);
-    cudaError_t e = ensure_dynamic_smem(kernel, Sh::kSmem);
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, int smem, cudaStream_t s, Args... args) {
+    cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
     if (e != cudaSuccess) return e;
-    int ctas = dev.sms * Sh::kPerSm;
-    if (ctas > kMostAttnCtas) ctas = kMostAttnCtas;
-    ws.heads = Sh::kHeads;
-    ws.padded = DP;
-    ws.rows = a.cache.heads * ((a.q_heads / a.cache.heads + Sh::kHeads - 1) / Sh::kHeads);
-    ws.by_row = static_cast<int64_t>(a.B) * ws.rows <= ctas;
-    ws.ctas = ctas;
-    // rows of few tiles: not worth a second launch, so CTAs take them whole
-    ws.split = a.most > kWholeTiles * kTile;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kAttnThreads);
-    cfg.dynamicSmemBytes = Sh::kSmem;
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_paged_attention_mma<E4M3, DP, NT>, a, ws);
+    e = cudaLaunchKernelEx(&cfg, kernel, args...);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+template <bool E4M3, int DP, int NT>
+cudaError_t launch_attention_shape(const AttentionArgs& a, const DeviceInfo& dev, JoinPlan jp, cudaStream_t s) {
+    using Sh = AttnShape<E4M3, DP, NT>;
+    const int G = a.q_heads / a.cache.heads;
+    jp.rows = a.cache.heads * ((G + Sh::kHeads - 1) / Sh::kHeads);
+    const int64_t all_rows = static_cast<int64_t>(a.B) * jp.rows;
+    const int most_tiles = (a.most + kTile - 1) / kTile + 1;  // of a row (a window may cut a tile at both ends)
+    // few short rows: a CTA each
+    if constexpr (Sh::kRowKernel) {
+        if (all_rows <= dev.sms && most_tiles <= kRowKernelTiles)
+            return launch_dependent(k_attention_rows<E4M3, DP, NT>, dim3(static_cast<unsigned>(all_rows)), dim3(kRowWarps * 32),
+                                    Sh::kRowSmem, s, a, jp.rows);
+    }
+    int ctas = dev.sms * Sh::kPerSm;
+    if (ctas > most_workers(DP) / kShareWarps) ctas = most_workers(DP) / kShareWarps;
+    jp.warps = ctas * kShareWarps;
+    jp.by_row = all_rows <= jp.warps;
+    jp.split = most_tiles > kWholeTiles;
+    cudaError_t e = launch_dependent(k_attention_shares<E4M3, DP, NT>, dim3(ctas), dim3(kShareWarps * 32), Sh::kSmem, s, a, jp);
+    if (e != cudaSuccess || !jp.split) return e;
+    // few rows: their accumulators over several CTAs, down to a warp's
+    const int places = jp.by_row ? static_cast<int>(all_rows) : jp.warps, units = Sh::kHeads * DP / 4;
+    int width = kJoinThreads;
+    while (width > units || (width > 32 && places * (units / width) < 2 * dev.sms)) width /= 2;
+    while (units % width) width /= 2;
+    return launch_dependent(k_attention_join<E4M3, DP, NT>, dim3(places, units / width), dim3(width, kJoinThreads / width), 0, s, a, jp);
+}
+
 template <bool E4M3>
-cudaError_t launch_attention_type(const AttentionArgs& a, const DeviceInfo& dev, JoinPlan& ws,
-                                  cudaStream_t s) {
+cudaError_t launch_attention_type(const AttentionArgs& a, const DeviceInfo& dev, const JoinPlan& jp, cudaStream_t s) {
     const bool wide = a.q_heads / a.cache.heads > 8;
     switch ((a.cache.dim + 63) / 64) {
-        case 1: return wide ? launch_attention_shape<E4M3, 64, 2>(a, dev, ws, s) : launch_attention_shape<E4M3, 64, 1>(a, dev, ws, s);
-        case 2: return wide ? launch_attention_shape<E4M3, 128, 2>(a, dev, ws, s) : launch_attention_shape<E4M3, 128, 1>(a, dev, ws, s);
-        case 3: return wide ? launch_attention_shape<E4M3, 192, 2>(a, dev, ws, s) : launch_attention_shape<E4M3, 192, 1>(a, dev, ws, s);
-        default: return wide ? launch_attention_shape<E4M3, 256, 2>(a, dev, ws, s) : launch_attention_shape<E4M3, 256, 1>(a, dev, ws, s);
+        case 1: return wide ? launch_attention_shape<E4M3, 64, 2>(a, dev, jp, s) : launch_attention_shape<E4M3, 64, 1>(a, dev, jp, s);
+        case 2: return wide ? launch_attention_shape<E4M3, 128, 2>(a, dev, jp, s) : launch_attention_shape<E4M3, 128, 1>(a, dev, jp, s);
+        case 3: return wide ? launch_attention_shape<E4M3, 192, 2>(a, dev, jp, s) : launch_attention_shape<E4M3, 192, 1>(a, dev, jp, s);
+        default: return wide ? launch_attention_shape<E4M3, 256, 2>(a, dev, jp, s) : launch_attention_shape<E4M3, 256, 1>(a, dev, jp, s);
     }
 }
 
