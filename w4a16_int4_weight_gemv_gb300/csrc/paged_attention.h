@@ -25,7 +25,6 @@ struct JoinPlan {
     // [warp][2][heads * (padded + 2)]; place 0: the row that the warp's share begins inside
     // of, 1: the row it ends inside of
     float* part;
-    int split;   // rows may span warps: the second launch is needed
     int by_row;
     int rows;    // of a request: key/value heads times chunks of the query heads sharing one
     int heads;   // query heads of a chunk: 8 or 16

@@ -18,8 +18,8 @@
 //     on across rows, and no warp waits for another.
 //   - k_attention_join: a second launch joins those parts, always in the
 //     order of the tokens.
-//   - k_attention_rows: where there are few rows of few tiles, a CTA for each
-//     row, its warps joined in shared memory: no shares, no second launch.
+//   - k_attention_rows: where no row can have many tiles, one to eight warps of
+//     a CTA for each row, joined in shared memory: no shares, no second launch.
 // The products run on the warp MMA with the keys as the 16-row operand
 // (tokens) and the heads as its 8 columns: one product covers 8 query heads,
 // and the transposed second product (values^T times p^T) takes the
@@ -40,8 +40,7 @@ constexpr int kShareWarps = 4;  // warps of a CTA
 constexpr int kRowWarps = 8;
 constexpr int kRowCost = 1;     // a row's queries and result, in tiles
 constexpr int kMinCost = 4;     // a warp's share at least
-constexpr int kWholeTiles = 8;  // rows that cannot be longer are not split over warps
-constexpr int kRowKernelTiles = 64;  // rows that cannot be longer may have a CTA each
+constexpr int kRowTiles = 8;    // rows kernel: tiles of a warp at most
 
 __device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void* src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
@@ -578,14 +577,14 @@ __global__ void __launch_bounds__(kShareWarps * 32, (AttnShape<E4M3, DP, NT>::kP
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         if (request_of(a, b, bad).tiles > 0) continue;
         store_empty(a, b, 0, a.q_heads, threadIdx.x, kShareWarps * 32);
-        if (jp.split && jp.by_row)
+        if (jp.by_row)
             for (int i = threadIdx.x; i < rows; i += kShareWarps * 32) jp.joins[b * rows + i] = make_int4(-1, 0, 0, 0);
     }
     const int64_t want = quotient(total + kMinCost - 1, kMinCost);
     int workers = want < jp.warps ? static_cast<int>(want) : jp.warps;
     // one request: rows of one length, so a multiple of them splits none unevenly
     if (a.B == 1 && workers > rows) workers -= workers % rows;
-    if (jp.split && !jp.by_row && lane == 0) jp.joins[worker] = make_int4(-1, 0, 0, 0);
+    if (!jp.by_row && lane == 0) jp.joins[worker] = make_int4(-1, 0, 0, 0);
     if (worker >= workers) {
         if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
         return;
@@ -623,19 +622,9 @@ __global__ void __launch_bounds__(kShareWarps * 32, (AttnShape<E4M3, DP, NT>::kP
         }
         return false;
     };
-    int64_t u0 = begin_of(worker), u1 = begin_of(worker + 1);
+    const int64_t u0 = begin_of(worker), u1 = begin_of(worker + 1);
     int first_b = 0;
     int64_t first_at = 0;
-    if (!jp.split) {
-        // whole rows: from the first that begins in the share to the last that does
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-            int64_t& u = i ? u1 : u0;
-            if (u >= total || !locate(u, first_b, first_at)) continue;
-            const int n = request_of(a, first_b, bad).tiles + kRowCost;
-            u = first_at + quotient(u - first_at + n - 1, n) * n;
-        }
-    }
 
     // --- the rows of a share, in order ---------------------------------------
     auto open_segment = [&](Segment& s) {
@@ -729,7 +718,7 @@ __global__ void __launch_bounds__(kShareWarps * 32, (AttnShape<E4M3, DP, NT>::kP
             math.store_part(part, part + HEADS * DP, part + HEADS * (DP + 1), lane);
         }
         // a row that begins here: what the join launch has to do for it
-        if (jp.split && begins && lane == 0 && (jp.by_row || !ends))
+        if (begins && lane == 0 && (jp.by_row || !ends))
             jp.joins[jp.by_row ? seg.b * rows + seg.row : worker] =
                 ends ? make_int4(-1, 0, 0, 0) : make_int4(seg.b, seg.row, worker, worker_of(seg.at + kRowCost + seg.q.tiles - 1));
         live = next_segment(seg);
@@ -819,18 +808,19 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Attention
         }
 }
 
-// One row per CTA.
+// 8 / wpr rows per CTA, wpr warps for each.
 template <bool E4M3, int DP, int NT>
-__global__ void __launch_bounds__(kRowWarps * 32, 1) k_attention_rows(const AttentionArgs a, const int rows) {
+__global__ void __launch_bounds__(kRowWarps * 32, 1) k_attention_rows(const AttentionArgs a, const int rows, const int wpr) {
     using Sh = AttnShape<E4M3, DP, NT>;
     constexpr int S = Sh::kRowStages, HEADS = Sh::kHeads, KS = Sh::kSteps;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t tile_mask[kRowWarps][S];
     __shared__ float part_m[kRowWarps][HEADS], part_l[kRowWarps][HEADS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int wir = warp & (wpr - 1), warp0 = warp - wir;  // warp in its row, and the row's first
     const uint32_t ring = smem_addr(smem) + warp * S * Sh::kStageBytes;
-    const int b = static_cast<int>(blockIdx.x) / rows, row = static_cast<int>(blockIdx.x) - b * rows;
-    const Heads hd = heads_of<HEADS>(a, row);
+    const unsigned id = (blockIdx.x * kRowWarps + warp) / static_cast<unsigned>(wpr);
+    const int b = static_cast<int>(id / static_cast<unsigned>(rows)), row = static_cast<int>(id - b * static_cast<unsigned>(rows));
     bool bad = false;
     if (a.cache.dim != DP) {
         clear_ring(smem, Sh::kRowSmem, threadIdx.x, kRowWarps * 32);
@@ -838,57 +828,67 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1) k_attention_rows(const Atte
     }
     grid_dependency_wait();
     grid_dependents_launch();
-    RowMath<E4M3, DP, NT> math;
-    math.begin(a, b, hd, lane);
-    const Request q = request_of(a, b, bad);
-    if (q.tiles == 0) {
-        store_empty(a, b, hd.first, hd.n, threadIdx.x, kRowWarps * 32);
-        if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
-        return;
+    Request q{};
+    Heads hd{};
+    if (b < a.B) {
+        hd = heads_of<HEADS>(a, row);
+        q = request_of(a, b, bad);
+        if (q.tiles == 0) store_empty(a, b, hd.first, hd.n, wir * 32 + lane, wpr * 32);
     }
-    TileCopy<E4M3, DP, NT> copy;
-    int ahead = warp, put = 0, slot = 0, primed = 0;
-    if (ahead < q.tiles) copy.look_up(a, b, q, ahead, q.tiles, kRowWarps, lane);
-    for (int t = warp; t < q.tiles;) {
-        const bool full = primed == S - 1;
-        if (full) cp_async_wait_group<S - 2>();
+    if (wir < q.tiles) {
+        RowMath<E4M3, DP, NT> math;
+        TileCopy<E4M3, DP, NT> copy;
+        int ahead = wir, put = 0, slot = 0, primed = 0;
+        copy.look_up(a, b, q, ahead, q.tiles, wpr, lane);
+        math.begin(a, b, hd, lane);
+        for (int t = wir; t < q.tiles;) {
+            const bool full = primed == S - 1;
+            if (full) cp_async_wait_group<S - 2>();
+            __syncwarp();
+            if (ahead < q.tiles) {
+                const uint32_t mask = copy.copy(a, hd.hk, q, ahead, wpr, ring + put * Sh::kStageBytes, lane, bad);
+                if (lane == 0) tile_mask[warp][put] = mask;
+                ahead += wpr;
+                if (ahead < q.tiles && copy.wants(a, ahead, wpr)) copy.look_up(a, b, q, ahead, q.tiles, wpr, lane);
+            }
+            cp_async_commit();
+            put = put + 1 == S ? 0 : put + 1;
+            if (!full) {
+                ++primed;
+                continue;
+            }
+            if (t == wir) math.ready(a, hd.hk, lane);
+            math.tile(ring + slot * Sh::kStageBytes, tile_mask[warp][slot], lane);
+            slot = slot + 1 == S ? 0 : slot + 1;
+            t += wpr;
+        }
+        cp_async_wait_group<0>();
         __syncwarp();
-        if (ahead < q.tiles) {
-            const uint32_t mask = copy.copy(a, hd.hk, q, ahead, kRowWarps, ring + put * Sh::kStageBytes, lane, bad);
-            if (lane == 0) tile_mask[warp][put] = mask;
-            ahead += kRowWarps;
-            if (ahead < q.tiles && copy.wants(a, ahead, kRowWarps)) copy.look_up(a, b, q, ahead, q.tiles, kRowWarps, lane);
+        math.reduce();
+        if (wpr == 1) {
+            math.finish(a, b, hd, lane);
+        } else {
+            math.store_part(reinterpret_cast<float*>(smem + warp * S * Sh::kStageBytes), part_m[warp], part_l[warp], lane);
         }
-        cp_async_commit();
-        put = put + 1 == S ? 0 : put + 1;
-        if (!full) {
-            ++primed;
-            continue;
-        }
-        if (t == warp) math.ready(a, hd.hk, lane);
-        math.tile(ring + slot * Sh::kStageBytes, tile_mask[warp][slot], lane);
-        slot = slot + 1 == S ? 0 : slot + 1;
-        t += kRowWarps;
     }
-    cp_async_wait_group<0>();
-    __syncwarp();
-    math.reduce();
-    math.store_part(reinterpret_cast<float*>(smem + warp * S * Sh::kStageBytes), part_m[warp], part_l[warp], lane);
+    if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
+    if (wpr == 1) return;
     __syncthreads();
-    const int used = min(q.tiles, kRowWarps);  // warps that had a tile
+    const int used = min(q.tiles, wpr);  // warps that had a tile
+    if (used == 0) return;
     const int r = lane >> 2, c = lane & 3;
     const float vs = E4M3 ? a.cache.v_scale[hd.hk] : 1.f;
 #pragma unroll 1
-    for (int u = warp; u < NT * KS; u += kRowWarps) {
+    for (int u = wir; u < NT * KS; u += wpr) {
         const int n = u / KS, k = u % KS;
         float top[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll 1
-        for (int w = 0; w < used; ++w)
+        for (int w = warp0; w < warp0 + used; ++w)
 #pragma unroll
             for (int e = 0; e < 2; ++e) top[e] = fmaxf(top[e], part_m[w][n * 8 + 2 * c + e]);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-        for (int w = 0; w < used; ++w) {
+        for (int w = warp0; w < warp0 + used; ++w) {
             float f[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -909,7 +909,6 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1) k_attention_rows(const Atte
                 if (n * 8 + 2 * c + e < hd.n)
                     a.lse[static_cast<int64_t>(b) * a.q_heads + hd.first + n * 8 + 2 * c + e] = lse_of<E4M3>(top[e], l[e]);
     }
-    if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
 }
 
 template <class... Params, class... Args>
@@ -936,20 +935,25 @@ cudaError_t launch_attention_shape(const AttentionArgs& a, const DeviceInfo& dev
     const int G = a.q_heads / a.cache.heads;
     jp.rows = a.cache.heads * ((G + Sh::kHeads - 1) / Sh::kHeads);
     const int64_t all_rows = static_cast<int64_t>(a.B) * jp.rows;
-    const int most_tiles = (a.most + kTile - 1) / kTile + 1;  // of a row (a window may cut a tile at both ends)
-    // few short rows: a CTA each
+    // of a row (a window may begin inside a tile)
+    const int visible = a.window > 0 && a.window < a.most ? a.window : a.most;
+    const int most_tiles = (visible + kTile - 1) / kTile + (visible < a.most);
+    // short rows: as many warps for each as one wave of CTAs has, if that leaves
+    // a warp few tiles
     if constexpr (Sh::kRowKernel) {
-        if (all_rows <= dev.sms && most_tiles <= kRowKernelTiles)
-            return launch_dependent(k_attention_rows<E4M3, DP, NT>, dim3(static_cast<unsigned>(all_rows)), dim3(kRowWarps * 32),
-                                    Sh::kRowSmem, s, a, jp.rows);
+        int wpr = kRowWarps;
+        while (wpr > 1 && all_rows * wpr > static_cast<int64_t>(dev.sms) * kRowWarps) wpr /= 2;
+        const int64_t grid = (all_rows * wpr + kRowWarps - 1) / kRowWarps;
+        if (most_tiles <= kRowTiles * wpr && grid < (int64_t(1) << 31))
+            return launch_dependent(k_attention_rows<E4M3, DP, NT>, dim3(static_cast<unsigned>(grid)), dim3(kRowWarps * 32),
+                                    Sh::kRowSmem, s, a, jp.rows, wpr);
     }
     int ctas = dev.sms * Sh::kPerSm;
     if (ctas > most_workers(DP) / kShareWarps) ctas = most_workers(DP) / kShareWarps;
     jp.warps = ctas * kShareWarps;
     jp.by_row = all_rows <= jp.warps;
-    jp.split = most_tiles > kWholeTiles;
     cudaError_t e = launch_dependent(k_attention_shares<E4M3, DP, NT>, dim3(ctas), dim3(kShareWarps * 32), Sh::kSmem, s, a, jp);
-    if (e != cudaSuccess || !jp.split) return e;
+    if (e != cudaSuccess) return e;
     // few rows: their accumulators over several CTAs, down to a warp's
     const int places = jp.by_row ? static_cast<int>(all_rows) : jp.warps, units = Sh::kHeads * DP / 4;
     int width = kJoinThreads;
