@@ -590,13 +590,48 @@ class PagedCache:
         self._ref = ctypes.addressof(self._struct)
 
 
-PagedMap = collections.namedtuple("PagedMap", "slots positions row_start kv_len free_head")
+class PagedMap(collections.namedtuple("PagedMap", "slots positions row_start kv_len free_head")):
+    """Outputs of w4a16_paged_map.  made_for: (requests, tokens) where
+    paged_map_buffers made them, so that they need no check."""
+    made_for = None
 
 
 def paged_map_buffers(requests: int, tokens: int, device) -> PagedMap:
     """Output buffers of w4a16_paged_map, to be kept from step to step."""
     new = lambda n: torch.empty(n, dtype=torch.int32, device=device)
-    return PagedMap(new(tokens), new(tokens), new(requests + 1), new(requests), new(1))
+    m = PagedMap(new(tokens), new(tokens), new(requests + 1), new(requests), new(1))
+    m.made_for = (requests, tokens)
+    return m
+
+
+# The paged calls run once per layer and step, next to kernels of a few
+# microseconds: what a valid argument has is checked in one expression, and
+# only where that fails is it looked into which one it was.
+_int32 = torch.int32
+_bf16 = torch.bfloat16
+
+
+def _vector(t, name: str, n: int) -> int:
+    """Address of an int32 vector of n entries."""
+    try:
+        if t.dtype is _int32 and t.is_cuda and t.shape == (n,) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, _I32, (n,))
+    return t.data_ptr()
+
+
+def _table(t, requests: int):
+    """Address, row stride and columns of a block table."""
+    try:
+        rows, columns = t.shape
+        stride, unit = t.stride()
+        if t.dtype is _int32 and t.is_cuda and rows == requests and (unit == 1 or columns == 1):
+            return t.data_ptr(), stride if rows > 1 else max(stride, columns), columns
+    except (AttributeError, ValueError):
+        pass
+    raise ValueError("block_table must be a CUDA int32 [%d, columns] with unit column stride" % requests)
 
 
 def w4a16_paged_map(ctx_len, new_len, block_table, free_blocks, free_head, page: int, num_blocks: int,
@@ -610,35 +645,51 @@ def w4a16_paged_map(ctx_len, new_len, block_table, free_blocks, free_head, page:
     slots and positions have (at least the new tokens; the rest gets -1).
     Returns PagedMap(slots [tokens], positions [tokens], row_start [B + 1],
     kv_len [B], free_head [1]), all int32."""
-    _need(ctx_len, "ctx_len", _I32)
-    B = ctx_len.shape[0]
-    _need(new_len, "new_len", _I32, (B,))
-    _need(free_blocks, "free_blocks", _I32)
-    _need(free_head, "free_head", _I32)
-    if (block_table.dim() != 2 or block_table.dtype != torch.int32 or not block_table.is_cuda
-            or block_table.stride(1) != 1 or block_table.shape[0] != B):
-        raise ValueError("block_table must be a CUDA int32 [%d, columns] with unit column stride" % B)
+    B = len(ctx_len)
+    ctx, new = _vector(ctx_len, "ctx_len", B), _vector(new_len, "new_len", B)
+    F = len(free_blocks)
+    free, head = _vector(free_blocks, "free_blocks", F), _vector(free_head, "free_head", 1)
+    table, stride, columns = _table(block_table, B)
     if out is None:
         out = paged_map_buffers(B, tokens, ctx_len.device)
-    else:
+    elif out.made_for != (B, tokens):
         for t, name, n in zip(out, PagedMap._fields, (tokens, tokens, B + 1, B, 1)):
             _need(t, name, _I32, (n,))
-    _check(load_library().w4a16_paged_map(
-        _ptr(ctx_len), _ptr(new_len), B, _ptr(block_table), block_table.stride(0), block_table.shape[1],
-        _ptr(free_blocks), free_blocks.numel(), _ptr(free_head), page, num_blocks, _ptr(out.slots),
-        _ptr(out.positions), tokens, _ptr(out.row_start), _ptr(out.kv_len), _ptr(out.free_head),
-        _stream(stream, ctx_len.get_device())), "w4a16_paged_map")
+    slots, positions, row_start, kv_len, head_out = out
+    rc = _lib.w4a16_paged_map(ctx, new, B, table, stride, columns, free, F, head, page, num_blocks,
+                              slots.data_ptr(), positions.data_ptr(), tokens, row_start.data_ptr(),
+                              kv_len.data_ptr(), head_out.data_ptr(), _stream(stream, ctx_len.get_device()))
+    if rc:
+        raise W4A16Error(rc, "w4a16_paged_map")
     return out
 
 
-def _need_rows(t, name: str, shape):
-    """bf16 heads [rows, heads, dim], dim contiguous."""
+def _rows(t, name: str, shape):
+    """Address, row and head strides of bf16 heads [rows, heads, dim], dim contiguous."""
+    try:
+        rows, heads, unit = t.stride()
+        if (t.dtype is _bf16 or t.dtype in _BF16) and t.is_cuda and unit == 1 and t.shape == shape:
+            return t.data_ptr(), rows, heads
+    except (AttributeError, ValueError):
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if not t.is_cuda or t.dtype not in _BF16 or t.dim() != 3 or t.stride(2) != 1:
         raise ValueError("%s must be a CUDA bf16 tensor [rows, heads, dim], dim contiguous" % name)
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+
+
+_section_arrays = {}  # the C arrays of the sections seen, by their values
+
+
+def _section_array(sections):
+    key = tuple(sections)
+    found = _section_arrays.get(key)
+    if found is None:
+        if len(_section_arrays) >= 64:
+            _section_arrays.clear()
+        found = _section_arrays[key] = (ctypes.c_int32 * len(key))(*key)
+    return found
 
 
 def w4a16_rope_append(q, k, v, positions, inv_freq, slots, cache: PagedCache, sections=None,
@@ -653,42 +704,48 @@ def w4a16_rope_append(q, k, v, positions, inv_freq, slots, cache: PagedCache, se
     turns back (the gradient).  q, or k, v, slots and cache together, may be
     None.  Returns the rotated queries (q_out, or a new tensor; q_out=q
     rotates in place)."""
-    ref = q if q is not None else k
-    T, _, dim = ref.shape
     if q is not None:
-        _need_rows(q, "q", q.shape)
+        shape = q.shape
+        T, heads, dim = shape if len(shape) == 3 else (0, 0, 0)
+        qa = _rows(q, "q", shape)
+        device = q.get_device()
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        else:
-            _need_rows(q_out, "q_out", q.shape)
-        qa = (_ptr(q), q.stride(0), q.stride(1), _ptr(q_out), q_out.stride(0), q_out.stride(1), q.shape[1])
+            q_out = torch.empty(shape, dtype=_bf16, device=q.device)
+        qo = _rows(q_out, "q_out", shape)
     else:
-        qa = (None, 0, 0, None, 0, 0, 0)
+        T, heads, dim = k.shape[0], 0, k.shape[2]
+        qa = qo = (None, 0, 0)
+        device = k.get_device()
     if cache is not None:
         shape = (T, cache.heads, cache.dim)
-        _need_rows(k, "k", shape)
-        _need_rows(v, "v", shape)
-        _need(slots, "slots", _I32, (T,))
-        ka = (_ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1))
-        slots_ptr, cache_ref = _ptr(slots), cache._ref
+        ka, va, slots_at, cache_at = _rows(k, "k", shape), _rows(v, "v", shape), _vector(slots, "slots", T), cache._ref
     else:
         if k is not None or v is not None or slots is not None:
             raise ValueError("k, v and slots go with a cache")
-        ka, slots_ptr, cache_ref = (None, 0, 0, None, 0, 0), None, None
-    _need(inv_freq, "inv_freq", _F32)
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
-    _need(positions, "positions", _I32, (T,) if positions.dim() == 1 else (axes, T))
+        ka, va, slots_at, cache_at = (None, 0, 0), (None, 0, 0), None, None
+    if not (inv_freq.dtype is torch.float32 and inv_freq.is_cuda and inv_freq.is_contiguous()):
+        _need(inv_freq, "inv_freq", _F32)
+    if positions.dim() == 1:
+        axes, axis_stride = 1, 0
+        positions_at = _vector(positions, "positions", T)
+    else:
+        axes, axis_stride = positions.shape[0], T
+        if not (positions.dtype is _int32 and positions.is_cuda and positions.is_contiguous() and positions.shape == (axes, T)):
+            _need(positions, "positions", _I32, (axes, T))
+        positions_at = positions.data_ptr()
     sec = None
     if sections is not None:
         if len(sections) != axes:
             raise ValueError("%d sections for %d axes" % (len(sections), axes))
-        sec = (ctypes.c_int32 * axes)(*sections)
+        sec = _section_array(sections)
     if T == 0:
         return q_out
-    _check(load_library().w4a16_rope_append(
-        *qa, *ka, _ptr(positions), T, _ptr(inv_freq), sec, axes, 2 * inv_freq.numel(), dim,
-        (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0), slots_ptr, cache_ref,
-        T, _stream(stream, ref.get_device())), "w4a16_rope_append")
+    rc = _lib.w4a16_rope_append(*qa, *qo, heads, *ka, *va, positions_at, axis_stride, inv_freq.data_ptr(), sec, axes,
+                                2 * inv_freq.numel(), dim,
+                                (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0),
+                                slots_at, cache_at, T, _stream(stream, device))
+    if rc:
+        raise W4A16Error(rc, "w4a16_rope_append")
     return q_out
 
 
@@ -710,28 +767,27 @@ def w4a16_paged_attention(q, cache: PagedCache, block_table, kv_len, scale: floa
     [B, q_heads]); a request of length 0 gets zeros and -infinity.
     workspace: from paged_attention_workspace, one per stream in use (None:
     a new one for this call)."""
-    B = q.shape[0]
-    H = q.shape[1]
-    _need_rows(q, "q", (B, H, cache.dim))
-    if (block_table.dim() != 2 or block_table.dtype != torch.int32 or not block_table.is_cuda
-            or block_table.stride(1) != 1 or block_table.shape[0] != B):
-        raise ValueError("block_table must be a CUDA int32 [%d, columns] with unit column stride" % B)
-    _need(kv_len, "kv_len", _I32, (B,))
+    shape = q.shape
+    B, H = shape[0], shape[1]
+    qa = _rows(q, "q", (B, H, cache.dim))
+    table, stride, columns = _table(block_table, B)
+    lengths = _vector(kv_len, "kv_len", B)
     if out is None:
-        out = torch.empty((B, H, cache.dim), dtype=torch.bfloat16, device=q.device)
-    else:
-        _need_rows(out, "out", q.shape)
+        out = torch.empty(shape, dtype=_bf16, device=q.device)
+    oa = _rows(out, "out", shape)
     if lse is None:
         lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-    else:
+    elif not (lse.dtype is torch.float32 and lse.is_cuda and lse.shape == (B, H) and lse.is_contiguous()):
         _need(lse, "lse", _F32, (B, H))
     if workspace is None:
         workspace = paged_attention_workspace(cache, H)
-    _check(load_library().w4a16_paged_attention(
-        _ptr(q), q.stride(0), q.stride(1), cache._ref, _ptr(block_table), block_table.stride(0),
-        block_table.shape[1], _ptr(kv_len), B, H, cache.dim ** -0.5 if scale is None else scale, window,
-        _ptr(out), out.stride(0), out.stride(1), _ptr(lse), _ptr(workspace), workspace.numel(),
-        _stream(stream, q.get_device())), "w4a16_paged_attention")
+    elif not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    rc = _lib.w4a16_paged_attention(*qa, cache._ref, table, stride, columns, lengths, B, H,
+                                    cache.dim ** -0.5 if scale is None else scale, window, *oa, lse.data_ptr(),
+                                    workspace.data_ptr(), workspace.nbytes, _stream(stream, q.get_device()))
+    if rc:
+        raise W4A16Error(rc, "w4a16_paged_attention")
     return out, lse
 
 
