@@ -794,7 +794,7 @@ w4a16_status w4a16_rope_append(const uint16_t* q, int64_t q_token, int64_t q_hea
     a.k = k, a.k_token = k_token, a.k_head = k_head;
     a.v = v, a.v_token = v_token, a.v_head = v_head;
     a.positions = positions, a.axis_stride = axis_stride, a.inv_freq = inv_freq;
-    a.slots = slots, a.rotary = rotary, a.dim = dim, a.T = T;
+    a.axes = axes, a.slots = slots, a.rotary = rotary, a.dim = dim, a.T = T;
     a.interleaved = (flags & W4A16_ROPE_INTERLEAVED) ? 1 : 0;
     a.inverse = (flags & W4A16_ROPE_INVERSE) ? 1 : 0;
     a.err = dev->err;

@@ -45,6 +45,7 @@ struct RopeArgs {
     const int32_t* positions;
     int64_t axis_stride;
     const float* inv_freq;
+    int axes;
     int axis_end[4];  // pairs below axis_end[a] (and not below axis_end[a - 1]) go by axis a
     const int32_t* slots;
     w4a16_kv_cache cache;  // heads 0 where there is none

@@ -9,11 +9,13 @@
 // 64 bits): the turn is good to about 2^-21 whatever the position, where the
 // rounded product pos * f alone is off by up to pos * f * 2^-24 radians.
 //
-// Bound by memory: every value is read once and written once.  A CTA serves
-// one token at a time: its first threads form the cosines and sines of all
-// pairs in shared memory, which every head of the token then reads.  A thread
-// moves units of 16 values (two 16-byte loads), loaded before the angles are
-// formed.
+// Bound by memory: every value is read once and written once.  A CTA takes
+// groups of tokens: it forms the cosines and sines of their pairs in shared
+// memory once, for all heads.  A thread has one unit of 16 values of a token
+// and takes it of TOKENS tokens of a group, all loads on their way while the
+// angles are formed; two buffers of angles leave one barrier a group.
+#include <algorithm>
+
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -22,8 +24,10 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kMaxPairs = 128;
+constexpr int kThreads = 256;  // at most
+constexpr int kAngles = 2048;  // of a group at most: tokens times pairs
+constexpr int kMany = 2;       // tokens of a thread and group where there are many
+constexpr int kPerSm = 4;      // CTAs of kThreads threads: 64 registers each
 
 // the high and low parts of 1 / pi
 constexpr float kInvPiHi = 0.31830987334251404f;
@@ -59,133 +63,188 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = f32_to_bf16_rn(x[2 * i]) | (static_cast<uint32_t>(f32_to_bf16_rn(x[2 * i + 1])) << 16);
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// eight values over the scale as e4m3, saturating (a NaN stays one)
+// Eight values over the scale as e4m3, saturating (a NaN stays one).  The
+// quotient: x times the reciprocal, corrected by its remainder, which rounds
+// as a division does.
 __device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], float scale) {
+    const float inv = 1.f / scale, most = 480.f * scale;  // 464 and more round to 448
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] / scale, x[2 * i + 1] / scale), __NV_SATFINITE,
-                                        __NV_E4M3);
+    for (int i = 0; i < 4; ++i) {
+        float v[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float t;
+            asm("min.NaN.f32 %0, %1, %2;" : "=f"(t) : "f"(x[2 * i + e]), "f"(most));
+            asm("max.NaN.f32 %0, %1, %2;" : "=f"(t) : "f"(t), "f"(-most));
+            const float q = t * inv;
+            v[e] = fmaf(fmaf(-q, scale, t), inv, q);
+        }
+        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
+    }
     return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
 // Units of a token: dim / 16 of each head, query heads first, then key heads,
 // then value heads.  Unit u of a head holds the values d0 .. d0 + 7 and
-// d1 .. d1 + 7; the first rotary / 16 units are turned.
-__global__ void __launch_bounds__(kThreads) k_rope_append(const RopeArgs a) {
-    __shared__ float2 cs[kMaxPairs];
-    const int per_head = a.dim / 16, half = a.rotary / 2;
+// d1 .. d1 + 7; the first rotary / 16 units are turned.  grid: (groups of
+// `group` tokens, ranges of `range` units of a token).
+// The angles of a unit's eight pairs lie in four float4 (cos, sin, cos, sin), the
+// i-th of all units of a token next to one another: no two lanes of a head meet
+// in a bank.
+template <int TOKENS>
+__global__ void __launch_bounds__(kThreads, kPerSm) k_rope_append(const RopeArgs a, const int group, const int range) {
+    extern __shared__ __align__(16) float4 angles[];  // [2][group * half / 2]
+    const int per_head = a.dim / 16, half = a.rotary / 2, turned = half / 8;  // turned: units of a head
+    const int step = group / TOKENS;  // tokens of a group that the threads take at once
     const int units = (a.q_heads + 2 * a.cache.heads) * per_head;
-    const int parts = gridDim.y;
-    uint32_t bad = 0u;
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        for (int i = threadIdx.x; i < half; i += kThreads) {
+    const int u_begin = blockIdx.y * range, u_count = min(range, units - u_begin);
+    // this thread's unit: of which token of the group, head and dims
+    const int my_token = static_cast<int>(threadIdx.x) / u_count;
+    int head, kind, d0, d1;
+    bool halves = false, neighbours = false;
+    {
+        const int u = u_begin + static_cast<int>(threadIdx.x) - my_token * u_count;
+        head = u / per_head;
+        const int at = u - head * per_head;
+        kind = head < a.q_heads ? 0 : head < a.q_heads + a.cache.heads ? 1 : 2;  // query, key, value
+        head -= kind == 0 ? 0 : kind == 1 ? a.q_heads : a.q_heads + a.cache.heads;
+        if (kind != 2 && at * 16 < a.rotary) (a.interleaved ? neighbours : halves) = true;
+        d0 = halves ? at * 8 : at * 16;
+        d1 = halves ? d0 + half : d0 + 8;
+    }
+    const uint16_t* src = kind == 0 ? a.q + head * a.q_head : kind == 1 ? a.k + head * a.k_head : a.v + head * a.v_head;
+    const int64_t src_token = kind == 0 ? a.q_token : kind == 1 ? a.k_token : a.v_token;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * group;
+    bool bad = false;
+    int buffer = 0;
+    grid_dependency_wait();
+    grid_dependents_launch();
+
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * group; t0 < a.T; t0 += stride) {
+        const int tokens = a.T - t0 < group ? static_cast<int>(a.T - t0) : group;
+        uint4 v0[TOKENS], v1[TOKENS];
+        int slot[TOKENS];
+#pragma unroll
+        for (int j = 0; j < TOKENS; ++j) {
+            const int token = my_token + j * step;
+            slot[j] = -1;
+            if (my_token >= step || token >= tokens) continue;
+            const uint16_t* x = src + (t0 + token) * src_token;
+            slot[j] = kind ? a.slots[t0 + token] : 0;
+            v0[j] = *reinterpret_cast<const uint4*>(x + d0);
+            v1[j] = *reinterpret_cast<const uint4*>(x + d1);
+        }
+        float4* const cs = angles + buffer * (group * half / 2);
+        buffer ^= 1;
+        for (int i = threadIdx.x; i < tokens * half; i += blockDim.x) {
+            const int token = i / half, pair = i - token * half;
             int axis = 0;
-            while (axis < 3 && i >= a.axis_end[axis]) ++axis;
-            float2 v = turn_of(a.positions[axis * a.axis_stride + t], a.inv_freq[i]);
-            if (a.inverse) v.y = -v.y;
-            cs[i] = v;
+            while (axis < 3 && pair >= a.axis_end[axis]) ++axis;
+            float2 c = turn_of(a.positions[axis * a.axis_stride + t0 + token], a.inv_freq[pair]);
+            if (a.inverse) c.y = -c.y;
+            reinterpret_cast<float2*>(cs + (token * 4 + (pair & 7) / 2) * turned + pair / 8)[pair & 1] = c;
         }
         __syncthreads();
-        int64_t slot = -1;
-        if (a.cache.heads) {
-            slot = a.slots[t];
-            if (slot != -1 && (slot < 0 || slot >= a.cache.blocks * a.cache.page)) {
-                bad = W4A16_DEVERR_SLOT;
-                slot = -1;
-            }
-        }
-        const int64_t block = slot < 0 ? 0 : slot / a.cache.page;
-        const int64_t place = slot < 0 ? 0 : slot - block * a.cache.page;
-        for (int u = blockIdx.y * kThreads + threadIdx.x; u < units; u += parts * kThreads) {
-            int head = u / per_head;
-            const int unit = u - head * per_head;
-            const bool turned = unit * 16 < a.rotary;
-            const bool halves = turned && !a.interleaved;
-            const int d0 = halves ? unit * 8 : unit * 16;
-            const int d1 = halves ? d0 + half : d0 + 8;
-            const uint16_t* src;
-            int kind = 0;  // query, key, value
-            if (head < a.q_heads) {
-                src = a.q + t * a.q_token + head * a.q_head;
-            } else {
-                if (slot < 0) continue;
-                head -= a.q_heads;
-                kind = head < a.cache.heads ? 1 : 2;
-                if (kind == 2) head -= a.cache.heads;
-                src = kind == 1 ? a.k + t * a.k_token + head * a.k_head
-                                : a.v + t * a.v_token + head * a.v_head;
-            }
-            const uint4 v0 = *reinterpret_cast<const uint4*>(src + d0);
-            const uint4 v1 = *reinterpret_cast<const uint4*>(src + d1);
-            float x[8], y[8];
-            unpack8(v0, x);
-            unpack8(v1, y);
-            if (turned && kind != 2) {
-                if (halves) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 c = cs[d0 + i];
-                        const float p = x[i] * c.x - y[i] * c.y, q = y[i] * c.x + x[i] * c.y;
-                        x[i] = p;
-                        y[i] = q;
-                    }
-                } else {
+        for (int j = 0; j < TOKENS; ++j) {
+            const int token = my_token + j * step, to = slot[j];
+            if (to == -1) continue;
+            if (kind && (to < 0 || to >= a.cache.blocks * a.cache.page)) {
+                bad = true;
+                continue;
+            }
+            float p[8], q[8];
+            unpack8(v0[j], p);
+            unpack8(v1[j], q);
+            if (halves || neighbours) {
+                const float4* c = cs + token * 4 * turned + (halves ? d0 / 8 : d0 / 16);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 c = cs[d0 / 2 + i], e = cs[d0 / 2 + 4 + i];
-                        const float p = x[2 * i] * c.x - x[2 * i + 1] * c.y;
-                        x[2 * i + 1] = x[2 * i + 1] * c.x + x[2 * i] * c.y;
-                        x[2 * i] = p;
-                        const float q = y[2 * i] * e.x - y[2 * i + 1] * e.y;
-                        y[2 * i + 1] = y[2 * i + 1] * e.x + y[2 * i] * e.y;
-                        y[2 * i] = q;
+                for (int i = 0; i < 4; ++i) {
+                    const float4 e = c[i * turned];
+                    if (halves) {
+                        const float y0 = p[2 * i] * e.x - q[2 * i] * e.y, y1 = p[2 * i + 1] * e.z - q[2 * i + 1] * e.w;
+                        q[2 * i] = q[2 * i] * e.x + p[2 * i] * e.y;
+                        q[2 * i + 1] = q[2 * i + 1] * e.z + p[2 * i + 1] * e.w;
+                        p[2 * i] = y0, p[2 * i + 1] = y1;
+                    } else {
+                        float* x = i < 2 ? p + 4 * i : q + 4 * (i - 2);
+                        const float y0 = x[0] * e.x - x[1] * e.y, y1 = x[2] * e.z - x[3] * e.w;
+                        x[1] = x[1] * e.x + x[0] * e.y;
+                        x[3] = x[3] * e.z + x[2] * e.w;
+                        x[0] = y0, x[2] = y1;
                     }
                 }
             }
             if (kind == 0) {
-                uint16_t* dst = a.q_out + t * a.qo_token + head * a.qo_head;
-                *reinterpret_cast<uint4*>(dst + d0) = pack8(x);
-                *reinterpret_cast<uint4*>(dst + d1) = pack8(y);
+                uint16_t* dst = a.q_out + (t0 + token) * a.qo_token + head * a.qo_head;
+                *reinterpret_cast<uint4*>(dst + d0) = pack8(p);
+                *reinterpret_cast<uint4*>(dst + d1) = pack8(q);
                 continue;
             }
-            const int64_t at = kind == 1 ? block * a.cache.k_block + place * a.cache.k_token + head * a.cache.k_head
-                                         : block * a.cache.v_block + place * a.cache.v_token + head * a.cache.v_head;
+            const int64_t block = static_cast<unsigned>(to) / static_cast<unsigned>(a.cache.page);
+            const int64_t place = to - block * a.cache.page;
+            const int64_t offset = kind == 1 ? block * a.cache.k_block + place * a.cache.k_token + head * a.cache.k_head
+                                             : block * a.cache.v_block + place * a.cache.v_token + head * a.cache.v_head;
             void* cache = kind == 1 ? a.cache.k : a.cache.v;
             if (a.cache.dtype == W4A16_CACHE_BF16) {
-                uint16_t* dst = static_cast<uint16_t*>(cache) + at;
-                *reinterpret_cast<uint4*>(dst + d0) = pack8(x);
-                *reinterpret_cast<uint4*>(dst + d1) = pack8(y);
+                uint16_t* dst = static_cast<uint16_t*>(cache) + offset;
+                *reinterpret_cast<uint4*>(dst + d0) = pack8(p);
+                *reinterpret_cast<uint4*>(dst + d1) = pack8(q);
             } else {
                 const float scale = kind == 1 ? a.cache.k_scale[head] : a.cache.v_scale[head];
-                uint8_t* dst = static_cast<uint8_t*>(cache) + at;
-                *reinterpret_cast<uint2*>(dst + d0) = pack8_e4m3(x, scale);
-                *reinterpret_cast<uint2*>(dst + d1) = pack8_e4m3(y, scale);
+                uint8_t* dst = static_cast<uint8_t*>(cache) + offset;
+                *reinterpret_cast<uint2*>(dst + d0) = pack8_e4m3(p, scale);
+                *reinterpret_cast<uint2*>(dst + d1) = pack8_e4m3(q, scale);
             }
         }
-        __syncthreads();
     }
-    if (bad) raise_device_error(a.err, bad);
+    if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
 }
 
 }  // namespace
 
 cudaError_t launch_rope_append(const RopeArgs& a, const DeviceInfo& dev, cudaStream_t s) {
-    const int units = (a.q_heads + 2 * a.cache.heads) * (a.dim / 16);
-    int64_t ctas = a.T;
-    const int64_t most = 16LL * dev.sms;
-    if (ctas > most) ctas = most;
-    // few tokens: a token's units over several CTAs, each forming the angles itself
-    int parts = 1;
-    const int want = (units + kThreads - 1) / kThreads;
-    while (parts < want && ctas * (parts + 1) <= most) ++parts;
-    k_rope_append<<<dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(parts)), kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    const int units = (a.q_heads + 2 * a.cache.heads) * (a.dim / 16), half = a.rotary / 2;
+    // a token's units over as few CTAs as hold them, over more where tokens are few
+    int parts = (units + kThreads - 1) / kThreads;
+    while (parts < 16 && units / parts > 64 && a.T * parts < dev.sms) parts *= 2;
+    const int range = (units + parts - 1) / parts;
+    parts = (units + range - 1) / range;
+    // tokens that the threads take at once: but a CTA for every SM at least
+    int64_t step = std::max(kThreads / range, 1);
+    if (half) step = std::min<int64_t>(step, kAngles / (kMany * half));
+    step = std::max<int64_t>(1, std::min<int64_t>(step, a.T * parts / dev.sms));
+    const int threads = static_cast<int>(step * range + 31) / 32 * 32;
+    // and how often: where every SM gets several groups all the same
+    const bool many = a.T * parts >= step * kMany * 4 * dev.sms;
+    const int group = static_cast<int>(step) * (many ? kMany : 1);
+    const int smem = group * half * 16;
+    auto* kernel = many ? k_rope_append<kMany> : k_rope_append<1>;
+    const cudaError_t rc = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
+    if (rc != cudaSuccess) return rc;
+    int64_t ctas = (a.T + group - 1) / group;
+    const int64_t wave = std::max<int64_t>(1, static_cast<int64_t>(kPerSm * kThreads / threads) * dev.sms / parts);
+    if (ctas > wave) ctas = wave;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(parts));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, group, range);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace w4a16
