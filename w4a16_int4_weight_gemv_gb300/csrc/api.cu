@@ -222,6 +222,25 @@ cudaError_t ensure_dynamic_smem(const void* kernel, int bytes) {
     return cudaSuccess;
 }
 
+cudaError_t ensure_shared_carveout(const void* kernel) {
+    struct Entry {
+        const void* kernel;
+        int device;
+    };
+    static std::mutex mu;
+    static Entry table[128];
+    static int used = 0;
+    int d = 0;
+    cudaError_t e = cudaGetDevice(&d);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < used; ++i)
+        if (table[i].kernel == kernel && table[i].device == d) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess && used < 128) table[used++] = Entry{kernel, d};
+    return e;
+}
+
 int max_active_clusters(const void* kernel, int threads, int smem, int S) {
     struct Entry {
         const void* kernel;

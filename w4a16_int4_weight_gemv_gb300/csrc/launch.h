@@ -280,6 +280,11 @@ HmmaChoice choose_hmma_plan(const DeviceInfo& dev, int M, int N, int K, int forc
 // spares the driver call -- about a microsecond -- on every launch).
 cudaError_t ensure_dynamic_smem(const void* kernel, int bytes);
 
+// Have `kernel` run with the largest shared-memory carve-out, once per device.
+// For small kernels that overlap a launch which needs it: an SM changes its
+// carve-out only when idle, so a small one keeps that launch's CTAs off it.
+cudaError_t ensure_shared_carveout(const void* kernel);
+
 // Number of clusters of S CTAs (threads each, smem bytes of dynamic shared
 // memory) of `kernel` the current device can run at once; cached.
 int max_active_clusters(const void* kernel, int threads, int smem, int S);

@@ -27,6 +27,8 @@
 // (tcgen05 would want 64 or more query rows; here there are 1 to 16.)
 #pragma once
 
+#include <algorithm>
+
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -39,7 +41,7 @@ constexpr int kTile = 16;       // tokens of a tile: the MMA's rows
 constexpr int kShareWarps = 4;  // warps of a CTA
 constexpr int kRowWarps = 8;
 constexpr int kRowCost = 1;     // a row's queries and result, in tiles
-constexpr int kMinCost = 4;     // a warp's share at least
+constexpr int kMinCost = 3;     // a warp's share at least
 constexpr int kRowTiles = 8;    // rows kernel: tiles of a warp at most
 
 __device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void* src, bool valid) {
@@ -508,17 +510,9 @@ __device__ __forceinline__ void clear_ring(uint8_t* smem, int bytes, int thread,
     for (int i = thread; i < bytes / 16; i += threads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// n / d for n >= 0, d > 0: in 32 bits where both fit, as they do in all but
-// the largest calls (a 64-bit division takes about 200 ns here)
-__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
-    if (((n | d) >> 32) == 0) return static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
-    return n / d;
-}
-
 // The tiles [t0, t1) of one row, and where the row begins among all costs.
 struct Segment {
-    int64_t at;
-    int b, row, t0, t1;
+    int at, b, row, t0, t1;
     Request q;
 };
 
@@ -544,32 +538,32 @@ __global__ void __launch_bounds__(kShareWarps * 32, (AttnShape<E4M3, DP, NT>::kP
 
     // --- the share of the warp ----------------------------------------------
     // Every warp forms the costs of all requests itself, kScan of them at a
-    // time (lane i: kPer in a row from kPer * i on).
+    // time (lane i: kPer in a row from kPer * i on).  They fit 32 bits.
     constexpr int kPer = 4, kScan = 32 * kPer;
-    int64_t cost[kPer];  // of this lane's requests
+    int cost[kPer];  // of this lane's requests
     // the costs of requests base .. base + kScan - 1; returns those before this lane's, `sum`: all
-    auto scan = [&](int base, int64_t& sum) -> int64_t {
-        int64_t own = 0;
+    auto scan = [&](int base, int& sum) -> int {
+        int own = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int b = base + lane * kPer + i;
             const int n = b < a.B ? request_of(a, b, bad).tiles : 0;
-            cost[i] = n ? static_cast<int64_t>(n + kRowCost) * rows : 0;
+            cost[i] = n ? (n + kRowCost) * rows : 0;
             own += cost[i];
         }
-        int64_t inc = own;
-#pragma unroll 1
+        int inc = own;
+#pragma unroll
         for (int d = 1; d < 32; d *= 2) {
-            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+            const int v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
             if (lane >= d) inc += v;
         }
         sum = __shfl_sync(0xFFFFFFFFu, inc, 31);
         return inc - own;
     };
-    int64_t total = 0, head_start = 0;  // head_start: before this lane's, of the first kScan requests
+    int total = 0, head_start = 0;  // head_start: before this lane's, of the first kScan requests
     for (int base = 0; base < a.B; base += kScan) {
-        int64_t sum;
-        const int64_t start = scan(base, sum);
+        int sum;
+        const int start = scan(base, sum);
         if (base == 0) head_start = start;
         total += sum;
     }
@@ -580,8 +574,7 @@ __global__ void __launch_bounds__(kShareWarps * 32, (AttnShape<E4M3, DP, NT>::kP
         if (jp.by_row)
             for (int i = threadIdx.x; i < rows; i += kShareWarps * 32) jp.joins[b * rows + i] = make_int4(-1, 0, 0, 0);
     }
-    const int64_t want = quotient(total + kMinCost - 1, kMinCost);
-    int workers = want < jp.warps ? static_cast<int>(want) : jp.warps;
+    int workers = min((total + kMinCost - 1) / kMinCost, jp.warps);
     // one request: rows of one length, so a multiple of them splits none unevenly
     if (a.B == 1 && workers > rows) workers -= workers % rows;
     if (!jp.by_row && lane == 0) jp.joins[worker] = make_int4(-1, 0, 0, 0);
@@ -590,17 +583,18 @@ __global__ void __launch_bounds__(kShareWarps * 32, (AttnShape<E4M3, DP, NT>::kP
         return;
     }
     // costs before worker i: equal shares, the remainder to the first ones
-    const int64_t share = quotient(total, workers), extra = total - share * workers;
-    auto begin_of = [&](int i) { return i * share + (i < extra ? i : extra); };
-    auto worker_of = [&](int64_t u) {
-        const int64_t big = extra * (share + 1);
-        return static_cast<int>(u < big ? quotient(u, share + 1) : extra + quotient(u - big, share));
+    const unsigned share = static_cast<unsigned>(total) / static_cast<unsigned>(workers), extra = total - share * workers;
+    const int u0 = worker * share + min(static_cast<unsigned>(worker), extra);
+    const int u1 = u0 + share + (worker < static_cast<int>(extra) ? 1 : 0);
+    auto worker_of = [&](int u) -> int {
+        const int big = extra * (share + 1);
+        return u < big ? static_cast<unsigned>(u) / (share + 1) : extra + static_cast<unsigned>(u - big) / share;
     };
     // the request that holds the place u < total, and the costs before it
-    auto locate = [&](int64_t u, int& found_b, int64_t& found_at) -> bool {
-        int64_t before = 0;
+    auto locate = [&](int u, int& found_b, int& found_at) -> bool {
+        int before = 0;
         for (int base = 0; base < a.B; base += kScan) {
-            int64_t sum = 0, start = head_start;
+            int sum = 0, start = head_start;
             if (a.B > kScan) start = scan(base, sum);
             start += before;
             int hit = -1;
@@ -622,15 +616,12 @@ __global__ void __launch_bounds__(kShareWarps * 32, (AttnShape<E4M3, DP, NT>::kP
         }
         return false;
     };
-    const int64_t u0 = begin_of(worker), u1 = begin_of(worker + 1);
-    int first_b = 0;
-    int64_t first_at = 0;
 
     // --- the rows of a share, in order ---------------------------------------
     auto open_segment = [&](Segment& s) {
-        const int64_t first = s.at + kRowCost;  // of the row's tiles
-        s.t0 = u0 > first ? static_cast<int>(u0 - first) : 0;
-        s.t1 = u1 - first < s.q.tiles ? static_cast<int>(u1 - first) : s.q.tiles;  // at most t0: nothing
+        const int first = s.at + kRowCost;  // of the row's tiles
+        s.t0 = max(u0 - first, 0);
+        s.t1 = min(u1 - first, s.q.tiles);  // at most t0: nothing
     };
     auto next_segment = [&](Segment& s) -> bool {
         s.at += s.q.tiles + kRowCost;
@@ -646,12 +637,11 @@ __global__ void __launch_bounds__(kShareWarps * 32, (AttnShape<E4M3, DP, NT>::kP
         return true;
     };
     Segment seg{};
-    bool live = u1 > u0 && locate(u0, first_b, first_at);
+    bool live = u1 > u0 && locate(u0, seg.b, seg.at);
     if (live) {
-        seg.b = first_b;
         seg.q = request_of(a, seg.b, bad);
-        seg.row = static_cast<int>(quotient(u0 - first_at, seg.q.tiles + kRowCost));
-        seg.at = first_at + static_cast<int64_t>(seg.row) * (seg.q.tiles + kRowCost);
+        seg.row = static_cast<unsigned>(u0 - seg.at) / static_cast<unsigned>(seg.q.tiles + kRowCost);
+        seg.at += seg.row * (seg.q.tiles + kRowCost);
         open_segment(seg);
         live = seg.t1 > seg.t0;
     }
@@ -732,7 +722,7 @@ __global__ void __launch_bounds__(kShareWarps * 32, (AttnShape<E4M3, DP, NT>::kP
 // Joins the parts of a row: grid (row, slice of its accumulators); threads
 // (x: accumulators, y: group, of which each takes every n-th part, so that
 // many parts are on their way at once).
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 512;  // at most
 constexpr int kJoinDepth = 4;  // parts a thread requests together
 
 template <bool E4M3, int DP, int NT>
@@ -911,9 +901,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1) k_attention_rows(const Atte
     }
 }
 
+// early: the grid's CTAs may start while the preceding one runs (they wait for its end themselves)
 template <class... Params, class... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, int smem, cudaStream_t s, Args... args) {
+cudaError_t launch_kernel(void (*kernel)(Params...), bool early, dim3 grid, dim3 block, int smem, cudaStream_t s, Args... args) {
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
+    if (e == cudaSuccess) e = ensure_shared_carveout(reinterpret_cast<const void*>(kernel));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
@@ -924,17 +916,18 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, i
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = early ? 1 : 0;
     e = cudaLaunchKernelEx(&cfg, kernel, args...);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <bool E4M3, int DP, int NT>
-cudaError_t launch_attention_shape(const AttentionArgs& a, const DeviceInfo& dev, JoinPlan jp, cudaStream_t s) {
+cudaError_t launch_attention_shape(const AttentionArgs& all, const DeviceInfo& dev, JoinPlan jp, cudaStream_t s) {
     using Sh = AttnShape<E4M3, DP, NT>;
+    AttentionArgs a = all;
     const int G = a.q_heads / a.cache.heads;
     jp.rows = a.cache.heads * ((G + Sh::kHeads - 1) / Sh::kHeads);
-    const int64_t all_rows = static_cast<int64_t>(a.B) * jp.rows;
+    int64_t all_rows = static_cast<int64_t>(a.B) * jp.rows;
     // of a row (a window may begin inside a tile)
     const int visible = a.window > 0 && a.window < a.most ? a.window : a.most;
     const int most_tiles = (visible + kTile - 1) / kTile + (visible < a.most);
@@ -944,22 +937,38 @@ cudaError_t launch_attention_shape(const AttentionArgs& a, const DeviceInfo& dev
         int wpr = kRowWarps;
         while (wpr > 1 && all_rows * wpr > static_cast<int64_t>(dev.sms) * kRowWarps) wpr /= 2;
         const int64_t grid = (all_rows * wpr + kRowWarps - 1) / kRowWarps;
-        if (most_tiles <= kRowTiles * wpr && grid < (int64_t(1) << 31))
-            return launch_dependent(k_attention_rows<E4M3, DP, NT>, dim3(static_cast<unsigned>(grid)), dim3(kRowWarps * 32),
-                                    Sh::kRowSmem, s, a, jp.rows, wpr);
+        if (most_tiles <= kRowTiles * wpr)
+            return launch_kernel(k_attention_rows<E4M3, DP, NT>, true, dim3(static_cast<unsigned>(grid)), dim3(kRowWarps * 32),
+                                 Sh::kRowSmem, s, a, jp.rows, wpr);
     }
-    int ctas = dev.sms * Sh::kPerSm;
-    if (ctas > most_workers(DP) / kShareWarps) ctas = most_workers(DP) / kShareWarps;
+    const int ctas = std::min(dev.sms * Sh::kPerSm, most_workers(DP) / kShareWarps);
     jp.warps = ctas * kShareWarps;
-    jp.by_row = all_rows <= jp.warps;
-    cudaError_t e = launch_dependent(k_attention_shares<E4M3, DP, NT>, dim3(ctas), dim3(kShareWarps * 32), Sh::kSmem, s, a, jp);
-    if (e != cudaSuccess) return e;
-    // few rows: their accumulators over several CTAs, down to a warp's
-    const int places = jp.by_row ? static_cast<int>(all_rows) : jp.warps, units = Sh::kHeads * DP / 4;
-    int width = kJoinThreads;
-    while (width > units || (width > 32 && places * (units / width) < 2 * dev.sms)) width /= 2;
-    while (units % width) width /= 2;
-    return launch_dependent(k_attention_join<E4M3, DP, NT>, dim3(places, units / width), dim3(width, kJoinThreads / width), 0, s, a, jp);
+    // as many requests at a time as have costs of 32 bits
+    const int64_t fit = std::max<int64_t>(1, 0x7FFFFFFF / (static_cast<int64_t>(most_tiles + kRowCost) * jp.rows));
+    for (int from = 0; from < all.B; from += a.B) {
+        a.B = static_cast<int>(std::min<int64_t>(all.B - from, fit));
+        a.q = all.q + from * a.q_request, a.out = all.out + from * a.out_request;
+        a.block_table = all.block_table + from * a.table_stride, a.kv_len = all.kv_len + from;
+        a.lse = all.lse ? all.lse + static_cast<int64_t>(from) * a.q_heads : nullptr;
+        all_rows = static_cast<int64_t>(a.B) * jp.rows;
+        jp.by_row = all_rows <= jp.warps;
+        // after the preceding launch, not into it: CTAs that are placed around others leave
+        // holes in the register file, and those that no longer fit run when the rest are done
+        // (20 key/value heads of 64 dims, 24 requests: 26.2 us launched early, 22.0 us so)
+        cudaError_t e = launch_kernel(k_attention_shares<E4M3, DP, NT>, false, dim3(ctas), dim3(kShareWarps * 32), Sh::kSmem, s, a, jp);
+        if (e != cudaSuccess) return e;
+        // few rows: their accumulators over several CTAs, down to a warp's; as many
+        // groups as a row has parts for, if rows are alike
+        const int places = jp.by_row ? static_cast<int>(all_rows) : jp.warps, units = Sh::kHeads * DP / 4;
+        int width = 256;
+        while (units % width || (width > 32 && places * (units / width) < dev.sms)) width /= 2;
+        const int parts = jp.warps / places + 2;
+        int groups = 1;
+        while (groups * width < kJoinThreads && groups * kJoinDepth < parts) groups *= 2;
+        e = launch_kernel(k_attention_join<E4M3, DP, NT>, true, dim3(places, units / width), dim3(width, groups), 0, s, a, jp);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 template <bool E4M3>
