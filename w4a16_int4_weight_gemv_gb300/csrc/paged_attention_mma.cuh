@@ -19,7 +19,8 @@
 //   - k_attention_join: a second launch joins those parts, always in the
 //     order of the tokens.
 //   - k_attention_rows: where no row can have many tiles, one to eight warps of
-//     a CTA for each row, joined in shared memory: no shares, no second launch.
+//     a CTA for each row, or, where rows are few, a cluster of up to eight such
+//     CTAs, joined through shared memory: no shares, no second launch.
 // The products run on the warp MMA with the keys as the 16-row operand
 // (tokens) and the heads as its 8 columns: one product covers 8 query heads,
 // and the transposed second product (values^T times p^T) takes the
@@ -39,10 +40,10 @@ namespace {
 
 constexpr int kTile = 16;       // tokens of a tile: the MMA's rows
 constexpr int kShareWarps = 4;  // warps of a CTA
-constexpr int kRowWarps = 8;
-constexpr int kRowCost = 1;     // a row's queries and result, in tiles
+constexpr int kRowCost = 2;     // a row's queries and result, in tiles (1: 128 requests over e4m3 132 us, 2: 125)
 constexpr int kMinCost = 3;     // a warp's share at least
 constexpr int kRowTiles = 8;    // rows kernel: tiles of a warp at most
+constexpr int kRowEnough = 3;   // and where a larger cluster no longer pays
 
 __device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void* src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
@@ -116,12 +117,15 @@ struct AttnShape {
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
     static constexpr int kSmem = kShareWarps * kStages * kStageBytes;
     // rows: one CTA an SM
+    static constexpr int kRowWarps = kStageBytes > 12288 ? 4 : 8;
     static constexpr int kRowFit = 225 * 1024 / (kRowWarps * kStageBytes);
     static constexpr int kRowStages = kRowFit > 4 ? 4 : kRowFit;
-    static constexpr bool kRowKernel = kRowStages >= 2;
-    static constexpr int kRowSmem = kRowWarps * kRowStages * kStageBytes;
+    static constexpr int kRowRing = kRowStages * kStageBytes;  // of a warp
+    static constexpr int kRowSmem = kRowWarps * kRowRing;
+    static constexpr int kPartBytes = kHeads * DP * 4;
+    static constexpr bool kClusters = kRowRing >= 2 * kPartBytes;  // room for the CTA's part behind a warp's
     static_assert(kStages >= 3, "ring too short");
-    static_assert(!kRowKernel || kRowStages * kStageBytes >= kHeads * DP * 4, "no room for a warp's part");
+    static_assert(kRowStages >= 2 && kRowRing >= kPartBytes, "no room for a warp's part");
     static_assert(kPerSm * 160 * kShareWarps <= most_workers(DP), "workspace");
 };
 
@@ -719,6 +723,65 @@ __global__ void __launch_bounds__(kShareWarps * 32, (AttnShape<E4M3, DP, NT>::kP
     if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
 }
 
+// A float4 and a float2 of the CTA `rank` of the cluster, at the place `local` has in this one.
+__device__ __forceinline__ uint32_t cluster_address(const void* local, uint32_t rank) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(local)), "r"(rank));
+    return remote;
+}
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t at) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    return v;
+}
+
+// A part's 16 dims of 8 heads, with what joining them takes: m and l of the
+// lane's two heads.
+struct DimPart {
+    float4 o;
+    float m[2], l[2];
+    __device__ __forceinline__ void clear() {
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+    }
+    __device__ __forceinline__ void add(const float4& x, float2 xm, float2 xl) {
+        const float pm[2] = {xm.x, xm.y}, pl[2] = {xl.x, xl.y};
+        float f0[2], f1[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float top = pl[e] != 0.f ? fmaxf(m[e], pm[e]) : m[e];
+            f0[e] = part_factor(m[e], top);
+            f1[e] = pl[e] != 0.f ? part_factor(pm[e], top) : 0.f;
+            m[e] = top;
+            l[e] = l[e] * f0[e] + pl[e] * f1[e];
+        }
+        o.x = o.x * f0[0] + x.x * f1[0], o.y = o.y * f0[1] + x.y * f1[1];
+        o.z = o.z * f0[0] + x.z * f1[0], o.w = o.w * f0[1] + x.w * f1[1];
+    }
+    // the result: dims of step k, heads of block n
+    template <bool E4M3>
+    __device__ __forceinline__ void finish(const AttentionArgs& a, int b, const Heads& hd, int n, int k, int lane) const {
+        const int r = lane >> 2, c = lane & 3;
+        const float vs = E4M3 ? a.cache.v_scale[hd.hk] : 1.f;
+        const float f0 = l[0] != 0.f ? vs / l[0] : 0.f, f1 = l[1] != 0.f ? vs / l[1] : 0.f;
+        const bool have = n * 8 + r < hd.n && k * 16 < a.cache.dim;
+        uint16_t* out = a.out + b * a.out_request + (hd.first + n * 8 + r) * a.out_head + k * 16;
+        store_dims<E4M3>(o, f0, f1, have ? out : nullptr, c);
+        if (a.lse && k == 0 && r == 0)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int h = n * 8 + 2 * c + e;
+                if (h < hd.n) a.lse[static_cast<int64_t>(b) * a.q_heads + hd.first + h] = lse_of<E4M3>(m[e], l[e]);
+            }
+    }
+};
+
 // Joins the parts of a row: grid (row, slice of its accumulators); threads
 // (x: accumulators, y: group, of which each takes every n-th part, so that
 // many parts are on their way at once).
@@ -729,32 +792,15 @@ template <bool E4M3, int DP, int NT>
 __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const AttentionArgs a, const JoinPlan jp) {
     using Sh = AttnShape<E4M3, DP, NT>;
     constexpr int HEADS = Sh::kHeads, KS = Sh::kSteps;
-    struct Sum {
-        float4 o;
-        float m[2], l[2];
-    };
-    __shared__ Sum sums[kJoinThreads];
+    __shared__ DimPart sums[kJoinThreads];
     grid_dependents_launch();
     grid_dependency_wait();
     const int4 d = __ldcg(jp.joins + blockIdx.x);
     if (d.x < 0) return;
     const int unit = blockIdx.y * blockDim.x + threadIdx.x;  // accumulator: (head block n, step k, lane)
-    const int lane = unit & 31, k = (unit >> 5) % KS, n = (unit >> 5) / KS, c = lane & 3, r = lane >> 2;
-    Sum s{make_float4(0.f, 0.f, 0.f, 0.f), {-INFINITY, -INFINITY}, {0.f, 0.f}};
-    auto add = [&](const float4& o, float2 m, float2 l) {
-        const float pm[2] = {m.x, m.y}, pl[2] = {l.x, l.y};
-        float f0[2], f1[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float top = pl[e] != 0.f ? fmaxf(s.m[e], pm[e]) : s.m[e];
-            f0[e] = part_factor(s.m[e], top);
-            f1[e] = pl[e] != 0.f ? part_factor(pm[e], top) : 0.f;
-            s.m[e] = top;
-            s.l[e] = s.l[e] * f0[e] + pl[e] * f1[e];
-        }
-        s.o.x = s.o.x * f0[0] + o.x * f1[0], s.o.y = s.o.y * f0[1] + o.y * f1[1];
-        s.o.z = s.o.z * f0[0] + o.z * f1[0], s.o.w = s.o.w * f0[1] + o.w * f1[1];
-    };
+    const int lane = unit & 31, k = (unit >> 5) % KS, n = (unit >> 5) / KS, c = lane & 3;
+    DimPart s;
+    s.clear();
 #pragma unroll 1
     for (int q = d.z + static_cast<int>(threadIdx.y); q <= d.w; q += blockDim.y * kJoinDepth) {
         float4 o[kJoinDepth];
@@ -772,7 +818,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Attention
             }
         }
 #pragma unroll
-        for (int i = 0; i < kJoinDepth; ++i) add(o[i], m[i], l[i]);
+        for (int i = 0; i < kJoinDepth; ++i) s.add(o[i], m[i], l[i]);
     }
     if (blockDim.y > 1) {
         sums[threadIdx.y * blockDim.x + threadIdx.x] = s;
@@ -780,40 +826,34 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Attention
         if (threadIdx.y > 0) return;
 #pragma unroll 1
         for (int g = 1; g < blockDim.y; ++g) {
-            const Sum& x = sums[g * blockDim.x + threadIdx.x];
-            add(x.o, make_float2(x.m[0], x.m[1]), make_float2(x.l[0], x.l[1]));
+            const DimPart& x = sums[g * blockDim.x + threadIdx.x];
+            s.add(x.o, make_float2(x.m[0], x.m[1]), make_float2(x.l[0], x.l[1]));
         }
     }
-    const Heads hd = heads_of<HEADS>(a, d.y);
-    const float vs = E4M3 ? a.cache.v_scale[hd.hk] : 1.f;
-    const float f0 = s.l[0] != 0.f ? vs / s.l[0] : 0.f, f1 = s.l[1] != 0.f ? vs / s.l[1] : 0.f;
-    const bool have = n * 8 + r < hd.n && k * 16 < a.cache.dim;
-    uint16_t* out = a.out + d.x * a.out_request + (hd.first + n * 8 + r) * a.out_head + k * 16;
-    store_dims<E4M3>(s.o, f0, f1, have ? out : nullptr, c);
-    if (a.lse && k == 0 && r == 0)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int h = n * 8 + 2 * c + e;
-            if (h < hd.n) a.lse[static_cast<int64_t>(d.x) * a.q_heads + hd.first + h] = lse_of<E4M3>(s.m[e], s.l[e]);
-        }
+    s.finish<E4M3>(a, d.x, heads_of<HEADS>(a, d.y), n, k, lane);
 }
 
-// 8 / wpr rows per CTA, wpr warps for each.
+// kRowWarps / wpr rows per CTA, wpr warps for each; or (cluster > 1, wpr =
+// kRowWarps) a row per cluster.  Tiles go round the CTAs of a row, then their
+// warps.
 template <bool E4M3, int DP, int NT>
-__global__ void __launch_bounds__(kRowWarps * 32, 1) k_attention_rows(const AttentionArgs a, const int rows, const int wpr) {
+__global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kRowWarps * 32), 1)
+    k_attention_rows(const AttentionArgs a, const int rows, const int wpr, const int cluster) {
     using Sh = AttnShape<E4M3, DP, NT>;
-    constexpr int S = Sh::kRowStages, HEADS = Sh::kHeads, KS = Sh::kSteps;
+    constexpr int S = Sh::kRowStages, HEADS = Sh::kHeads, KS = Sh::kSteps, W = Sh::kRowWarps;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint32_t tile_mask[kRowWarps][S];
-    __shared__ float part_m[kRowWarps][HEADS], part_l[kRowWarps][HEADS];
+    __shared__ uint32_t tile_mask[W][S];
+    __shared__ __align__(8) float part_m[W][HEADS], part_l[W][HEADS], cta_m[HEADS], cta_l[HEADS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int wir = warp & (wpr - 1), warp0 = warp - wir;  // warp in its row, and the row's first
-    const uint32_t ring = smem_addr(smem) + warp * S * Sh::kStageBytes;
-    const unsigned id = (blockIdx.x * kRowWarps + warp) / static_cast<unsigned>(wpr);
+    const int rank = cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int wir = warp & (wpr - 1), warp0 = warp - wir;  // warp in its row (of this CTA), and the row's first
+    const int first_tile = wir * cluster + rank, step = wpr * cluster;
+    const uint32_t ring = smem_addr(smem) + warp * Sh::kRowRing;
+    const unsigned id = cluster > 1 ? blockIdx.x / static_cast<unsigned>(cluster) : (blockIdx.x * W + warp) / static_cast<unsigned>(wpr);
     const int b = static_cast<int>(id / static_cast<unsigned>(rows)), row = static_cast<int>(id - b * static_cast<unsigned>(rows));
     bool bad = false;
     if (a.cache.dim != DP) {
-        clear_ring(smem, Sh::kRowSmem, threadIdx.x, kRowWarps * 32);
+        clear_ring(smem, Sh::kRowSmem, threadIdx.x, W * 32);
         __syncthreads();
     }
     grid_dependency_wait();
@@ -823,23 +863,23 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1) k_attention_rows(const Atte
     if (b < a.B) {
         hd = heads_of<HEADS>(a, row);
         q = request_of(a, b, bad);
-        if (q.tiles == 0) store_empty(a, b, hd.first, hd.n, wir * 32 + lane, wpr * 32);
+        if (q.tiles == 0 && rank == 0) store_empty(a, b, hd.first, hd.n, wir * 32 + lane, wpr * 32);
     }
-    if (wir < q.tiles) {
+    if (first_tile < q.tiles) {
         RowMath<E4M3, DP, NT> math;
         TileCopy<E4M3, DP, NT> copy;
-        int ahead = wir, put = 0, slot = 0, primed = 0;
-        copy.look_up(a, b, q, ahead, q.tiles, wpr, lane);
+        int ahead = first_tile, put = 0, slot = 0, primed = 0;
+        copy.look_up(a, b, q, ahead, q.tiles, step, lane);
         math.begin(a, b, hd, lane);
-        for (int t = wir; t < q.tiles;) {
+        for (int t = first_tile; t < q.tiles;) {
             const bool full = primed == S - 1;
             if (full) cp_async_wait_group<S - 2>();
             __syncwarp();
             if (ahead < q.tiles) {
-                const uint32_t mask = copy.copy(a, hd.hk, q, ahead, wpr, ring + put * Sh::kStageBytes, lane, bad);
+                const uint32_t mask = copy.copy(a, hd.hk, q, ahead, step, ring + put * Sh::kStageBytes, lane, bad);
                 if (lane == 0) tile_mask[warp][put] = mask;
-                ahead += wpr;
-                if (ahead < q.tiles && copy.wants(a, ahead, wpr)) copy.look_up(a, b, q, ahead, q.tiles, wpr, lane);
+                ahead += step;
+                if (ahead < q.tiles && copy.wants(a, ahead, step)) copy.look_up(a, b, q, ahead, q.tiles, step, lane);
             }
             cp_async_commit();
             put = put + 1 == S ? 0 : put + 1;
@@ -847,63 +887,66 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1) k_attention_rows(const Atte
                 ++primed;
                 continue;
             }
-            if (t == wir) math.ready(a, hd.hk, lane);
+            if (t == first_tile) math.ready(a, hd.hk, lane);
             math.tile(ring + slot * Sh::kStageBytes, tile_mask[warp][slot], lane);
             slot = slot + 1 == S ? 0 : slot + 1;
-            t += wpr;
+            t += step;
         }
         cp_async_wait_group<0>();
         __syncwarp();
         math.reduce();
-        if (wpr == 1) {
+        if (step == 1) {
             math.finish(a, b, hd, lane);
         } else {
-            math.store_part(reinterpret_cast<float*>(smem + warp * S * Sh::kStageBytes), part_m[warp], part_l[warp], lane);
+            math.store_part(reinterpret_cast<float*>(smem + warp * Sh::kRowRing), part_m[warp], part_l[warp], lane);
         }
     }
     if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
-    if (wpr == 1) return;
+    if (step == 1) return;
     __syncthreads();
-    const int used = min(q.tiles, wpr);  // warps that had a tile
-    if (used == 0) return;
+    if (q.tiles == 0) return;
+    const int used = min((q.tiles - rank + cluster - 1) / cluster, wpr);  // warps here that had a tile (at most 0: none)
     const int r = lane >> 2, c = lane & 3;
-    const float vs = E4M3 ? a.cache.v_scale[hd.hk] : 1.f;
+    float4* const cta_part = reinterpret_cast<float4*>(smem + Sh::kPartBytes);
 #pragma unroll 1
     for (int u = wir; u < NT * KS; u += wpr) {
-        const int n = u / KS, k = u % KS;
-        float top[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        const int n = u / KS, k = u % KS, h = n * 8 + 2 * c;
+        DimPart s;
+        s.clear();
 #pragma unroll 1
         for (int w = warp0; w < warp0 + used; ++w)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) top[e] = fmaxf(top[e], part_m[w][n * 8 + 2 * c + e]);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-        for (int w = warp0; w < warp0 + used; ++w) {
-            float f[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float pl = part_l[w][n * 8 + 2 * c + e];
-                f[e] = pl != 0.f ? part_factor(part_m[w][n * 8 + 2 * c + e], top[e]) : 0.f;
-                l[e] += pl * f[e];
+            s.add(reinterpret_cast<const float4*>(smem + w * Sh::kRowRing)[u * 32 + lane],
+                  *reinterpret_cast<const float2*>(&part_m[w][h]), *reinterpret_cast<const float2*>(&part_l[w][h]));
+        if (cluster == 1) {
+            s.finish<E4M3>(a, b, hd, n, k, lane);
+        } else {
+            cta_part[u * 32 + lane] = s.o;
+            if (k == 0 && r == 0) {
+                *reinterpret_cast<float2*>(&cta_m[h]) = make_float2(s.m[0], s.m[1]);
+                *reinterpret_cast<float2*>(&cta_l[h]) = make_float2(s.l[0], s.l[1]);
             }
-            const float4 x = reinterpret_cast<const float4*>(smem + w * S * Sh::kStageBytes)[u * 32 + lane];
-            o.x += x.x * f[0], o.y += x.y * f[1], o.z += x.z * f[0], o.w += x.w * f[1];
         }
-        const float f0 = l[0] != 0.f ? vs / l[0] : 0.f, f1 = l[1] != 0.f ? vs / l[1] : 0.f;
-        const bool have = n * 8 + r < hd.n && k * 16 < a.cache.dim;
-        uint16_t* out = a.out + b * a.out_request + (hd.first + n * 8 + r) * a.out_head + k * 16;
-        store_dims<E4M3>(o, f0, f1, have ? out : nullptr, c);
-        if (a.lse && k == 0 && r == 0)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if (n * 8 + 2 * c + e < hd.n)
-                    a.lse[static_cast<int64_t>(b) * a.q_heads + hd.first + n * 8 + 2 * c + e] = lse_of<E4M3>(top[e], l[e]);
     }
+    if (cluster == 1) return;
+    cluster_barrier();
+#pragma unroll 1
+    for (int u = warp * cluster + rank; u < NT * KS; u += W * cluster) {
+        const int n = u / KS, k = u % KS, h = n * 8 + 2 * c;
+        DimPart s;
+        s.clear();
+#pragma unroll 1
+        for (int x = 0; x < cluster; ++x)
+            s.add(ld_cluster_f32x4(cluster_address(cta_part + u * 32 + lane, x)), ld_cluster_f32x2(cluster_address(&cta_m[h], x)),
+                  ld_cluster_f32x2(cluster_address(&cta_l[h], x)));
+        s.finish<E4M3>(a, b, hd, n, k, lane);
+    }
+    cluster_barrier();  // nobody leaves while its part may be read
 }
 
 // early: the grid's CTAs may start while the preceding one runs (they wait for its end themselves)
 template <class... Params, class... Args>
-cudaError_t launch_kernel(void (*kernel)(Params...), bool early, dim3 grid, dim3 block, int smem, cudaStream_t s, Args... args) {
+cudaError_t launch_kernel(void (*kernel)(Params...), bool early, int cluster, dim3 grid, dim3 block, int smem, cudaStream_t s,
+                          Args... args) {
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
     if (e == cudaSuccess) e = ensure_shared_carveout(reinterpret_cast<const void*>(kernel));
     if (e != cudaSuccess) return e;
@@ -912,11 +955,20 @@ cudaError_t launch_kernel(void (*kernel)(Params...), bool early, dim3 grid, dim3
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (early) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = early ? 1 : 0;
+    cfg.numAttrs = n;
     e = cudaLaunchKernelEx(&cfg, kernel, args...);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -933,13 +985,19 @@ cudaError_t launch_attention_shape(const AttentionArgs& all, const DeviceInfo& d
     const int most_tiles = (visible + kTile - 1) / kTile + (visible < a.most);
     // short rows: as many warps for each as one wave of CTAs has, if that leaves
     // a warp few tiles
-    if constexpr (Sh::kRowKernel) {
-        int wpr = kRowWarps;
-        while (wpr > 1 && all_rows * wpr > static_cast<int64_t>(dev.sms) * kRowWarps) wpr /= 2;
-        const int64_t grid = (all_rows * wpr + kRowWarps - 1) / kRowWarps;
-        if (most_tiles <= kRowTiles * wpr)
-            return launch_kernel(k_attention_rows<E4M3, DP, NT>, true, dim3(static_cast<unsigned>(grid)), dim3(kRowWarps * 32),
-                                 Sh::kRowSmem, s, a, jp.rows, wpr);
+    {
+        constexpr int W = Sh::kRowWarps;
+        int wpr = W, cluster = 1;
+        while (wpr > 1 && all_rows * wpr > static_cast<int64_t>(dev.sms) * W) wpr /= 2;
+        if (Sh::kClusters && wpr == W)
+            while (cluster < 8 && most_tiles > kRowEnough * W * cluster && all_rows * cluster * 2 <= dev.sms) cluster *= 2;
+        while (cluster > 1 && max_active_clusters(reinterpret_cast<const void*>(k_attention_rows<E4M3, DP, NT>), W * 32,
+                                                  Sh::kRowSmem, cluster) < all_rows)
+            cluster /= 2;
+        const int64_t grid = cluster > 1 ? all_rows * cluster : (all_rows * wpr + W - 1) / W;
+        if (most_tiles <= kRowTiles * wpr * cluster)
+            return launch_kernel(k_attention_rows<E4M3, DP, NT>, true, cluster, dim3(static_cast<unsigned>(grid)), dim3(W * 32),
+                                 Sh::kRowSmem, s, a, jp.rows, wpr, cluster);
     }
     const int ctas = std::min(dev.sms * Sh::kPerSm, most_workers(DP) / kShareWarps);
     jp.warps = ctas * kShareWarps;
@@ -955,7 +1013,7 @@ cudaError_t launch_attention_shape(const AttentionArgs& all, const DeviceInfo& d
         // after the preceding launch, not into it: CTAs that are placed around others leave
         // holes in the register file, and those that no longer fit run when the rest are done
         // (20 key/value heads of 64 dims, 24 requests: 26.2 us launched early, 22.0 us so)
-        cudaError_t e = launch_kernel(k_attention_shares<E4M3, DP, NT>, false, dim3(ctas), dim3(kShareWarps * 32), Sh::kSmem, s, a, jp);
+        cudaError_t e = launch_kernel(k_attention_shares<E4M3, DP, NT>, false, 1, dim3(ctas), dim3(kShareWarps * 32), Sh::kSmem, s, a, jp);
         if (e != cudaSuccess) return e;
         // few rows: their accumulators over several CTAs, down to a warp's; as many
         // groups as a row has parts for, if rows are alike
@@ -965,7 +1023,7 @@ cudaError_t launch_attention_shape(const AttentionArgs& all, const DeviceInfo& d
         const int parts = jp.warps / places + 2;
         int groups = 1;
         while (groups * width < kJoinThreads && groups * kJoinDepth < parts) groups *= 2;
-        e = launch_kernel(k_attention_join<E4M3, DP, NT>, true, dim3(places, units / width), dim3(width, groups), 0, s, a, jp);
+        e = launch_kernel(k_attention_join<E4M3, DP, NT>, true, 1, dim3(places, units / width), dim3(width, groups), 0, s, a, jp);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
