@@ -4,7 +4,7 @@
 namespace w4a16 {
 
 size_t paged_attention_workspace(int q_heads, int kv_heads, int dim) {
-    const int heads = q_heads / kv_heads > 8 ? 16 : 8, padded = (dim + 63) / 64 * 64;
+    const int heads = q_heads / kv_heads > 8 ? 16 : 8, padded = padded_dim(dim);
     return static_cast<size_t>(most_workers(padded)) *
            (sizeof(int4) + 2 * static_cast<size_t>(heads) * (padded + 2) * sizeof(float));
 }
@@ -12,7 +12,7 @@ size_t paged_attention_workspace(int q_heads, int kv_heads, int dim) {
 cudaError_t launch_paged_attention(const AttentionArgs& a, const DeviceInfo& dev, cudaStream_t s) {
     JoinPlan join{};
     join.joins = static_cast<int4*>(a.workspace);
-    join.part = reinterpret_cast<float*>(join.joins + most_workers((a.cache.dim + 63) / 64 * 64));
+    join.part = reinterpret_cast<float*>(join.joins + most_workers(padded_dim(a.cache.dim)));
     return a.cache.dtype == W4A16_CACHE_BF16 ? launch_attention_bf16(a, dev, join, s)
                                              : launch_attention_e4m3(a, dev, join, s);
 }

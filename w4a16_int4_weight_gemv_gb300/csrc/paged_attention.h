@@ -10,9 +10,12 @@ namespace w4a16 {
 // the division by their sum.
 constexpr float kE4m3Bias = 15.f;
 
-// Most warps of the first launch, by the padded dim (64, 128, 192 or 256):
-// four, three or two CTAs of four warps on each of up to 160 SMs.
-constexpr int most_workers(int padded) { return padded == 64 ? 2560 : padded == 128 ? 1920 : 1280; }
+// The dims a kernel is built for: dim rounded up to one of them.
+constexpr int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 96 ? 96 : dim <= 128 ? 128 : dim <= 192 ? 192 : 256; }
+
+// Most warps of the first launch, by the padded dim: 16, 12 or 8 on each of up
+// to 160 SMs.
+constexpr int most_workers(int padded) { return padded == 64 ? 2560 : padded <= 128 ? 1920 : 1280; }
 
 // Rows that several warps of the first launch share, for the second to join.
 // A part is what a warp has of a row: o as the products' accumulators hold it
@@ -28,7 +31,7 @@ struct JoinPlan {
     int by_row;
     int rows;    // of a request: key/value heads times chunks of the query heads sharing one
     int heads;   // query heads of a chunk: 8 or 16
-    int padded;  // dim rounded up to 64
+    int padded;  // padded_dim
     int warps;   // of the first launch
 };
 

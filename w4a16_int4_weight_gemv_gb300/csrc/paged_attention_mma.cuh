@@ -39,7 +39,6 @@ namespace w4a16 {
 namespace {
 
 constexpr int kTile = 16;       // tokens of a tile: the MMA's rows
-constexpr int kShareWarps = 4;  // warps of a CTA
 constexpr int kRowCost = 2;     // a row's queries and result, in tiles (1: 128 requests over e4m3 132 us, 2: 125)
 constexpr int kMinCost = 3;     // a warp's share at least
 constexpr int kRowTiles = 8;    // rows kernel: tiles of a warp at most
@@ -105,15 +104,16 @@ template <bool E4M3, int DP, int NT>
 struct AttnShape {
     static constexpr int kHeads = 8 * NT;
     static constexpr int kSteps = DP / 16;                     // 16-dim steps of a head
-    static constexpr int kRowBytes = DP * (E4M3 ? 1 : 2);
-    static constexpr int kChunks = kRowBytes / 16;             // 16-byte chunks of a row
+    // 16-byte chunks of a row in shared memory (six would not swizzle: eight)
+    static constexpr int kChunks = E4M3 && DP == 96 ? 8 : DP * (E4M3 ? 1 : 2) / 16;
+    static constexpr int kRowBytes = kChunks * 16;
     static constexpr int kStageBytes = 2 * kTile * kRowBytes;  // keys, then values
     static constexpr int kPartFloats = kHeads * (DP + 2);
-    // shares: as many CTAs an SM as registers allow (the accumulators' size decides) with
-    // rings of three stages or more
-    static constexpr int kPerSm = E4M3 ? (NT == 1 ? (DP == 64 ? 4 : DP == 128 ? 3 : 2) : (DP == 64 ? 3 : 2))
-                                       : (DP == 64 ? (NT == 1 ? 4 : 3) : DP == 128 ? 2 : 1);
-    static constexpr int kFit = (227 * 1024 / kPerSm - 1024 - 256) / (kShareWarps * kStageBytes);
+    // shares: one CTA an SM, of as many warps as its registers allow (the accumulators'
+    // size decides) with rings of three stages or more
+    static constexpr int kShareWarps = 4 * (E4M3 ? (NT == 1 ? (DP == 64 ? 4 : DP <= 128 ? 3 : 2) : (DP == 64 ? 3 : 2))
+                                                 : (DP == 64 ? (NT == 1 ? 4 : 3) : DP <= 128 ? 2 : 1));
+    static constexpr int kFit = 226 * 1024 / (kShareWarps * kStageBytes);
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
     static constexpr int kSmem = kShareWarps * kStages * kStageBytes;
     // rows: one CTA an SM
@@ -126,7 +126,7 @@ struct AttnShape {
     static constexpr bool kClusters = kRowRing >= 2 * kPartBytes;  // room for the CTA's part behind a warp's
     static_assert(kStages >= 3, "ring too short");
     static_assert(kRowStages >= 2 && kRowRing >= kPartBytes, "no room for a warp's part");
-    static_assert(kPerSm * 160 * kShareWarps <= most_workers(DP), "workspace");
+    static_assert(160 * kShareWarps <= most_workers(DP), "workspace");
 };
 
 // What one request looks like: its visible tokens [start, len), in tiles from
@@ -521,20 +521,20 @@ struct Segment {
 };
 
 template <bool E4M3, int DP, int NT>
-__global__ void __launch_bounds__(kShareWarps * 32, (AttnShape<E4M3, DP, NT>::kPerSm))
+__global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kShareWarps * 32), 1)
     k_attention_shares(const AttentionArgs a, const JoinPlan jp) {
     using Sh = AttnShape<E4M3, DP, NT>;
-    constexpr int S = Sh::kStages, HEADS = Sh::kHeads, KS = Sh::kSteps;
+    constexpr int S = Sh::kStages, HEADS = Sh::kHeads, W = Sh::kShareWarps;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint32_t tile_mask[kShareWarps][S];
+    __shared__ uint32_t tile_mask[W][S];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int worker = blockIdx.x * kShareWarps + warp;
+    const int worker = blockIdx.x * W + warp;
     const uint32_t ring = smem_addr(smem) + warp * S * Sh::kStageBytes;
     const int rows = jp.rows;
     bool bad = false;
 
     if (a.cache.dim != DP) {
-        clear_ring(smem, Sh::kSmem, threadIdx.x, kShareWarps * 32);
+        clear_ring(smem, Sh::kSmem, threadIdx.x, W * 32);
         __syncthreads();
     }
     grid_dependency_wait();
@@ -574,9 +574,9 @@ __global__ void __launch_bounds__(kShareWarps * 32, (AttnShape<E4M3, DP, NT>::kP
     // requests without tokens
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         if (request_of(a, b, bad).tiles > 0) continue;
-        store_empty(a, b, 0, a.q_heads, threadIdx.x, kShareWarps * 32);
+        store_empty(a, b, 0, a.q_heads, threadIdx.x, W * 32);
         if (jp.by_row)
-            for (int i = threadIdx.x; i < rows; i += kShareWarps * 32) jp.joins[b * rows + i] = make_int4(-1, 0, 0, 0);
+            for (int i = threadIdx.x; i < rows; i += W * 32) jp.joins[b * rows + i] = make_int4(-1, 0, 0, 0);
     }
     int workers = min((total + kMinCost - 1) / kMinCost, jp.warps);
     // one request: rows of one length, so a multiple of them splits none unevenly
@@ -673,9 +673,10 @@ __global__ void __launch_bounds__(kShareWarps * 32, (AttnShape<E4M3, DP, NT>::kP
             const int after_b = seg.row + 1 < rows ? seg.b : seg.b + 1;
             if (after_b < a.B) {
                 const Heads h = heads_of<HEADS>(a, seg.row + 1 < rows ? seg.row + 1 : 0);
-                for (int i = lane; i < h.n * KS / 4; i += 32)
-                    if ((i % (KS / 4)) * 64 < a.cache.dim)
-                        prefetch_l2(a.q + after_b * a.q_request + (h.first + i / (KS / 4)) * a.q_head + (i % (KS / 4)) * 64);
+                constexpr int kLines = (DP + 63) / 64;
+                for (int i = lane; i < h.n * kLines; i += 32)
+                    if ((i % kLines) * 64 < a.cache.dim)
+                        prefetch_l2(a.q + after_b * a.q_request + (h.first + i / kLines) * a.q_head + (i % kLines) * 64);
             }
         }
         const bool full = primed == S - 1;
@@ -999,8 +1000,8 @@ cudaError_t launch_attention_shape(const AttentionArgs& all, const DeviceInfo& d
             return launch_kernel(k_attention_rows<E4M3, DP, NT>, true, cluster, dim3(static_cast<unsigned>(grid)), dim3(W * 32),
                                  Sh::kRowSmem, s, a, jp.rows, wpr, cluster);
     }
-    const int ctas = std::min(dev.sms * Sh::kPerSm, most_workers(DP) / kShareWarps);
-    jp.warps = ctas * kShareWarps;
+    const int ctas = std::min(dev.sms, most_workers(DP) / Sh::kShareWarps);
+    jp.warps = ctas * Sh::kShareWarps;
     // as many requests at a time as have costs of 32 bits
     const int64_t fit = std::max<int64_t>(1, 0x7FFFFFFF / (static_cast<int64_t>(most_tiles + kRowCost) * jp.rows));
     for (int from = 0; from < all.B; from += a.B) {
@@ -1010,10 +1011,11 @@ cudaError_t launch_attention_shape(const AttentionArgs& all, const DeviceInfo& d
         a.lse = all.lse ? all.lse + static_cast<int64_t>(from) * a.q_heads : nullptr;
         all_rows = static_cast<int64_t>(a.B) * jp.rows;
         jp.by_row = all_rows <= jp.warps;
-        // after the preceding launch, not into it: CTAs that are placed around others leave
-        // holes in the register file, and those that no longer fit run when the rest are done
-        // (20 key/value heads of 64 dims, 24 requests: 26.2 us launched early, 22.0 us so)
-        cudaError_t e = launch_kernel(k_attention_shares<E4M3, DP, NT>, false, 1, dim3(ctas), dim3(kShareWarps * 32), Sh::kSmem, s, a, jp);
+        // (early, because a CTA has an SM for itself: several smaller ones that are placed
+        // around others leave holes in the register file, and those that no longer fit then
+        // run when the rest are done -- 20 key/value heads of 64 dims, 24 requests: 26 us)
+        cudaError_t e = launch_kernel(k_attention_shares<E4M3, DP, NT>, true, 1, dim3(ctas), dim3(Sh::kShareWarps * 32), Sh::kSmem,
+                                      s, a, jp);
         if (e != cudaSuccess) return e;
         // few rows: their accumulators over several CTAs, down to a warp's; as many
         // groups as a row has parts for, if rows are alike
@@ -1032,10 +1034,11 @@ cudaError_t launch_attention_shape(const AttentionArgs& all, const DeviceInfo& d
 template <bool E4M3>
 cudaError_t launch_attention_type(const AttentionArgs& a, const DeviceInfo& dev, const JoinPlan& jp, cudaStream_t s) {
     const bool wide = a.q_heads / a.cache.heads > 8;
-    switch ((a.cache.dim + 63) / 64) {
-        case 1: return wide ? launch_attention_shape<E4M3, 64, 2>(a, dev, jp, s) : launch_attention_shape<E4M3, 64, 1>(a, dev, jp, s);
-        case 2: return wide ? launch_attention_shape<E4M3, 128, 2>(a, dev, jp, s) : launch_attention_shape<E4M3, 128, 1>(a, dev, jp, s);
-        case 3: return wide ? launch_attention_shape<E4M3, 192, 2>(a, dev, jp, s) : launch_attention_shape<E4M3, 192, 1>(a, dev, jp, s);
+    switch (padded_dim(a.cache.dim)) {
+        case 64: return wide ? launch_attention_shape<E4M3, 64, 2>(a, dev, jp, s) : launch_attention_shape<E4M3, 64, 1>(a, dev, jp, s);
+        case 96: return wide ? launch_attention_shape<E4M3, 96, 2>(a, dev, jp, s) : launch_attention_shape<E4M3, 96, 1>(a, dev, jp, s);
+        case 128: return wide ? launch_attention_shape<E4M3, 128, 2>(a, dev, jp, s) : launch_attention_shape<E4M3, 128, 1>(a, dev, jp, s);
+        case 192: return wide ? launch_attention_shape<E4M3, 192, 2>(a, dev, jp, s) : launch_attention_shape<E4M3, 192, 1>(a, dev, jp, s);
         default: return wide ? launch_attention_shape<E4M3, 256, 2>(a, dev, jp, s) : launch_attention_shape<E4M3, 256, 1>(a, dev, jp, s);
     }
 }
