@@ -537,6 +537,39 @@ def test_attention_nan_is_kept(w):
     assert torch.equal(lse.isnan().cpu(), nan.all(-1))
 
 
+def test_attention_of_tables_too_wide_for_one_launch(w):
+    # rows of 2^26 blocks: the costs of two requests would pass 32 bits, so each is launched by itself
+    lens = [70, 0, 700, 15]
+    q, cache, table = attention_problem(w, 77, lens, 16, 16, 64, 16, "bf16", "token")
+    wide = torch.empty(4, 1 << 26, dtype=torch.int32, device="cuda")
+    wide[:, :len(table[0])] = i32(table)
+    got = w.w4a16_paged_attention(q.cuda(), cache, wide, i32(lens))
+    check_attention(w, q, cache, table, lens, got=got)
+
+
+@pytest.mark.parametrize("lens", [[4000], [9, 7000, 0], [1500] * 6, [600] * 30], ids=str)
+@pytest.mark.parametrize("page", [16, 24])
+def test_attention_rows_over_clusters(w, lens, page):
+    # few rows: one to eight CTAs for each; with a window, and with a block that is not there
+    for dtype, dim, hq, hk in (("bf16", 128, 4, 2), ("fp8", 64, 3, 1), ("bf16", 256, 12, 1)):
+        q, cache, table = attention_problem(w, len(lens) + page, lens, hq, hk, dim, page, dtype, "token")
+        check_attention(w, q, cache, table, lens)
+        check_attention(w, q, cache, table, lens, window=333)
+    bad = [list(r) for r in table]
+    bad[lens.index(max(lens))][3] = -7
+    check_attention(w, q, cache, bad, lens, flags=w.DEVERR_SLOT)
+
+
+@pytest.mark.parametrize("B", [128, 129, 300])
+def test_attention_many_long_requests(w, B):
+    # more requests than one scan of the lengths holds, long enough to be dealt in shares
+    rng = random.Random(B)
+    lens = [rng.choice([0, 1, 160, rng.randrange(400)]) for _ in range(B)]
+    q, cache, table = attention_problem(w, B, lens, 8, 4, 64, 16, "bf16", "token")
+    check_attention(w, q, cache, table, lens)
+    check_attention(w, q, cache, table, [0] * (B - 1) + lens[-1:])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp8"])
 def test_attention_offsets_past_32_bits(w, dtype):
     # element offsets beyond 2^32: only the blocks in use are written

@@ -564,12 +564,17 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kShareWarps * 32), 1
         sum = __shfl_sync(0xFFFFFFFFu, inc, 31);
         return inc - own;
     };
-    int total = 0, head_start = 0;  // head_start: before this lane's, of the first kScan requests
-    for (int base = 0; base < a.B; base += kScan) {
-        int sum;
-        const int start = scan(base, sum);
-        if (base == 0) head_start = start;
-        total += sum;
+    int total = 0, head_start = 0;  // head_start: before this lane's requests, where one scan has all
+    if (a.B <= kScan) {
+        head_start = scan(0, total);
+    } else {
+#pragma unroll 8
+        for (int b = lane; b < a.B; b += 32) {
+            const int n = request_of(a, b, bad).tiles;
+            total += n ? (n + kRowCost) * rows : 0;
+        }
+#pragma unroll
+        for (int d = 16; d; d /= 2) total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
     }
     // requests without tokens
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
@@ -805,7 +810,7 @@ struct DimPart {
 // (x: accumulators, y: group, of which each takes every n-th part, so that
 // many parts are on their way at once).
 constexpr int kJoinThreads = 512;  // at most
-constexpr int kJoinDepth = 4;  // parts a thread requests together
+constexpr int kJoinDepth = 3;  // parts a thread requests together
 
 template <bool E4M3, int DP, int NT>
 __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const AttentionArgs a, const JoinPlan jp) {
@@ -1037,7 +1042,7 @@ cudaError_t launch_attention_shape(const AttentionArgs& all, const DeviceInfo& d
         // few rows: their accumulators over several CTAs, down to a warp's; as many
         // groups as a row has parts for, if rows are alike
         const int places = jp.by_row ? static_cast<int>(all_rows) : jp.warps, units = Sh::kHeads * DP / 4;
-        int width = 256;
+        int width = 128;
         while (units % width || (width > 32 && places * (units / width) < dev.sms)) width /= 2;
         const int parts = jp.warps / places + 2;
         int groups = 1;
