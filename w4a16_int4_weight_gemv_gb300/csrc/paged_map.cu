@@ -15,7 +15,7 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 
 struct Pair {
     int64_t tokens, blocks;
@@ -59,6 +59,8 @@ __global__ void __launch_bounds__(kThreads) k_paged_map(const PagedMapArgs a) {
     const bool first_cta = blockIdx.x == 0;
     uint32_t bad = 0u;
 
+    grid_dependency_wait();
+    grid_dependents_launch();
     Pair carry{0, 0};
     for (int base = 0; base < a.B; base += kThreads) {
         const int b = base + static_cast<int>(threadIdx.x);
@@ -173,8 +175,18 @@ cudaError_t launch_paged_map(const PagedMapArgs& a, const DeviceInfo& dev, cudaS
     int64_t ctas = (a.tokens + kThreads - 1) / kThreads;
     if (ctas > 2 * dev.sms) ctas = 2 * dev.sms;
     if (ctas < 1) ctas = 1;
-    k_paged_map<<<static_cast<int>(ctas), kThreads, smem, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t rc = cudaLaunchKernelEx(&cfg, k_paged_map, a);
+    return rc != cudaSuccess ? rc : cudaGetLastError();
 }
 
 }  // namespace w4a16
