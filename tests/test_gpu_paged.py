@@ -652,3 +652,34 @@ def test_attention_refusals(w):
     with pytest.raises(TypeError):
         w.PagedCache(cache.k.to(torch.float8_e4m3fn), cache.v.to(torch.float8_e4m3fn))
     assert w.w4a16_device_error(clear=True) == 0
+
+
+# --------------------------------------------------------------------------
+# the two ways of marshalling the arguments
+# --------------------------------------------------------------------------
+def test_both_marshallings_make_the_same_calls(w, monkeypatch):
+    if w._fast is None:
+        pytest.skip("the extension module was not built")
+    results = []
+    for fast in (w._fast, None):
+        monkeypatch.setattr(w, "_fast", fast)
+        ctx, new, table, free, head, blocks = map_problem(3, 9, 16, 60, 40)
+        t = i32(table)
+        m = w.w4a16_paged_map(i32(ctx), i32(new), t, i32(free), i32([head]), 16, blocks, sum(new) + 2,
+                              out=w.paged_map_buffers(9, sum(new) + 2, "cuda"))
+        case = (40, 6, 2, 64, 64, [20, 12], True, 16, "fp8", "head", 300)
+        qkv, pos, slots, cache = rope_problem(w, case, 5)
+        q, k, v = split_qkv(qkv.cuda(), 6, 2, 64)
+        out = torch.empty(40, 6, 64, dtype=torch.bfloat16, device="cuda")
+        assert w.w4a16_rope_append(q, k, v, pos.cuda(), freqs(64).cuda(), slots.cuda(), cache, sections=[20, 12], interleaved=True,
+                                   q_out=out) is out
+        lens = [30, 0, 77]
+        qa, ca, ta = attention_problem(w, 8, lens, 4, 2, 64, 16, "bf16", "token")
+        got = [torch.empty(3, 4, 64, dtype=torch.bfloat16, device="cuda"), torch.empty(3, 4, device="cuda")]
+        w.w4a16_paged_attention(qa.cuda(), ca, i32(ta), i32(lens), window=50, out=got[0], lse=got[1],
+                                workspace=w.paged_attention_workspace(ca, 4), stream=torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        results.append([t, *m, out, cache.k.float(), cache.v.float(), *got])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    assert w.w4a16_device_error(clear=True) == 0

@@ -14,6 +14,7 @@ from __future__ import annotations
 import collections
 import ctypes
 import enum
+import importlib.util
 import os
 
 import torch
@@ -590,23 +591,42 @@ class PagedCache:
         self._ref = ctypes.addressof(self._struct)
 
 
-class PagedMap(collections.namedtuple("PagedMap", "slots positions row_start kv_len free_head")):
-    """Outputs of w4a16_paged_map.  made_for: (requests, tokens) where
-    paged_map_buffers made them, so that they need no check."""
-    made_for = None
+PagedMap = collections.namedtuple("PagedMap", "slots positions row_start kv_len free_head")
 
 
 def paged_map_buffers(requests: int, tokens: int, device) -> PagedMap:
     """Output buffers of w4a16_paged_map, to be kept from step to step."""
     new = lambda n: torch.empty(n, dtype=torch.int32, device=device)
-    m = PagedMap(new(tokens), new(tokens), new(requests + 1), new(requests), new(1))
-    m.made_for = (requests, tokens)
-    return m
+    return PagedMap(new(tokens), new(tokens), new(requests + 1), new(requests), new(1))
 
 
 # The paged calls run once per layer and step, next to kernels of a few
-# microseconds: what a valid argument has is checked in one expression, and
-# only where that fails is it looked into which one it was.
+# microseconds.  So an extension module (fastcall.cpp) looks at the arguments
+# and makes the call; what it does not take -- arguments left out, bit patterns
+# for bf16, anything that is wrong -- goes through the functions here, which
+# check what a valid argument has in one expression, and only where that fails
+# look into which one it was.
+_fast = None
+
+
+def _load_fast():
+    import importlib.machinery
+    from . import build_ext
+    path = build_ext.fastcall_path()
+    if path is None or not os.path.exists(path) or _raw_current_stream is None:
+        return None
+    loader = importlib.machinery.ExtensionFileLoader("_fastcall", path)
+    try:
+        mod = importlib.util.module_from_spec(importlib.machinery.ModuleSpec("_fastcall", loader, origin=path))
+        loader.exec_module(mod)
+    except ImportError:
+        return None
+    address = lambda f: ctypes.cast(f, ctypes.c_void_p).value
+    mod.bind(address(_lib.w4a16_paged_map), address(_lib.w4a16_rope_append), address(_lib.w4a16_paged_attention),
+             _raw_current_stream)
+    return mod
+
+
 _int32 = torch.int32
 _bf16 = torch.bfloat16
 
@@ -645,6 +665,13 @@ def w4a16_paged_map(ctx_len, new_len, block_table, free_blocks, free_head, page:
     slots and positions have (at least the new tokens; the rest gets -1).
     Returns PagedMap(slots [tokens], positions [tokens], row_start [B + 1],
     kv_len [B], free_head [1]), all int32."""
+    if _fast is not None and out is not None:
+        rc = _fast.paged_map(ctx_len, new_len, block_table, free_blocks, free_head, page, num_blocks, tokens, out,
+                             None if stream is None else stream.cuda_stream)
+        if rc == 0:
+            return out
+        if rc is not None:
+            raise W4A16Error(rc, "w4a16_paged_map")
     B = len(ctx_len)
     ctx, new = _vector(ctx_len, "ctx_len", B), _vector(new_len, "new_len", B)
     F = len(free_blocks)
@@ -652,7 +679,7 @@ def w4a16_paged_map(ctx_len, new_len, block_table, free_blocks, free_head, page:
     table, stride, columns = _table(block_table, B)
     if out is None:
         out = paged_map_buffers(B, tokens, ctx_len.device)
-    elif out.made_for != (B, tokens):
+    else:
         for t, name, n in zip(out, PagedMap._fields, (tokens, tokens, B + 1, B, 1)):
             _need(t, name, _I32, (n,))
     slots, positions, row_start, kv_len, head_out = out
@@ -679,16 +706,17 @@ def _rows(t, name: str, shape):
     raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
 
 
-_section_arrays = {}  # the C arrays of the sections seen, by their values
+_section_arrays = {}  # C arrays and their addresses, by the sections' values
 
 
 def _section_array(sections):
     key = tuple(sections)
     found = _section_arrays.get(key)
     if found is None:
+        array = (ctypes.c_int32 * len(key))(*key)
         if len(_section_arrays) >= 64:
-            _section_arrays.clear()
-        found = _section_arrays[key] = (ctypes.c_int32 * len(key))(*key)
+            return array, ctypes.addressof(array)
+        found = _section_arrays[key] = array, ctypes.addressof(array)
     return found
 
 
@@ -704,6 +732,16 @@ def w4a16_rope_append(q, k, v, positions, inv_freq, slots, cache: PagedCache, se
     turns back (the gradient).  q, or k, v, slots and cache together, may be
     None.  Returns the rotated queries (q_out, or a new tensor; q_out=q
     rotates in place)."""
+    flags = (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0)
+    if _fast is not None and (q is None or q_out is not None) and (cache is not None or (k is None and v is None and slots is None)):
+        sec, sec_at = (None, 0) if sections is None else _section_array(sections)
+        rc = _fast.rope_append(q, k, v, positions, inv_freq, slots, None if cache is None else cache._ref,
+                               0 if cache is None else cache.heads, sec_at, 1 if sections is None else len(sections), flags,
+                               q_out, None if stream is None else stream.cuda_stream)
+        if rc == 0:
+            return q_out
+        if rc is not None:
+            raise W4A16Error(rc, "w4a16_rope_append")
     if q is not None:
         shape = q.shape
         T, heads, dim = shape if len(shape) == 3 else (0, 0, 0)
@@ -737,13 +775,11 @@ def w4a16_rope_append(q, k, v, positions, inv_freq, slots, cache: PagedCache, se
     if sections is not None:
         if len(sections) != axes:
             raise ValueError("%d sections for %d axes" % (len(sections), axes))
-        sec = _section_array(sections)
+        sec, _ = _section_array(sections)
     if T == 0:
         return q_out
     rc = _lib.w4a16_rope_append(*qa, *qo, heads, *ka, *va, positions_at, axis_stride, inv_freq.data_ptr(), sec, axes,
-                                2 * inv_freq.numel(), dim,
-                                (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0),
-                                slots_at, cache_at, T, _stream(stream, device))
+                                2 * inv_freq.numel(), dim, flags, slots_at, cache_at, T, _stream(stream, device))
     if rc:
         raise W4A16Error(rc, "w4a16_rope_append")
     return q_out
@@ -767,6 +803,15 @@ def w4a16_paged_attention(q, cache: PagedCache, block_table, kv_len, scale: floa
     [B, q_heads]); a request of length 0 gets zeros and -infinity.
     workspace: from paged_attention_workspace, one per stream in use (None:
     a new one for this call)."""
+    if scale is None:
+        scale = cache.dim ** -0.5
+    if _fast is not None and workspace is not None:
+        rc = _fast.paged_attention(q, cache._ref, cache.dim, block_table, kv_len, scale, window, out, lse, workspace,
+                                   None if stream is None else stream.cuda_stream)
+        if rc == 0:
+            return out, lse
+        if rc is not None:
+            raise W4A16Error(rc, "w4a16_paged_attention")
     shape = q.shape
     B, H = shape[0], shape[1]
     qa = _rows(q, "q", (B, H, cache.dim))
@@ -784,7 +829,7 @@ def w4a16_paged_attention(q, cache: PagedCache, block_table, kv_len, scale: floa
     elif not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor")
     rc = _lib.w4a16_paged_attention(*qa, cache._ref, table, stride, columns, lengths, B, H,
-                                    cache.dim ** -0.5 if scale is None else scale, window, *oa, lse.data_ptr(),
+                                    scale, window, *oa, lse.data_ptr(),
                                     workspace.data_ptr(), workspace.nbytes, _stream(stream, q.get_device()))
     if rc:
         raise W4A16Error(rc, "w4a16_paged_attention")
@@ -792,3 +837,4 @@ def w4a16_paged_attention(q, cache: PagedCache, block_table, kv_len, scale: floa
 
 
 load_library()
+_fast = _load_fast()

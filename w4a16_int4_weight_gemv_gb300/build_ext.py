@@ -1,7 +1,10 @@
 """Build libw4a16.so from csrc/ with nvcc for sm_103a (in-tree, no cmake).
 
 Each translation unit is compiled in parallel, then linked into one shared
-library in ``_build/``.  Host code is plain C++17 (portable between x86_64
+library in ``_build/``.  Next to it goes a small extension module
+(fastcall.cpp, host C++ against the installed torch's headers) that marshals
+the arguments of the paged-cache calls; where it cannot be built, binding.py
+does that itself, slower.  Host code is plain C++17 (portable between x86_64
 and aarch64 hosts).  Floating point is IEEE: no fast-math, no flush-to-zero
 (the CUDA-core kernel relies on subnormal FFMA operands).
 """
@@ -9,9 +12,12 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
+import re
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -50,8 +56,52 @@ def is_stale() -> bool:
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
+FASTCALL_SRC = os.path.join(HERE, "fastcall.cpp")
+
+
+def _torch_dir():
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
+
+
+def fastcall_path():
+    """The extension module's file, named after the torch it is built against (None without torch)."""
+    torch_dir = _torch_dir()
+    if torch_dir is None:
+        return None
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        found = re.search(r"^__version__ = ['\"]([^'\"]+)", f.read(), re.M)
+    return os.path.join(BUILD_DIR, "_fastcall.%s.so" % (found.group(1) if found else "unknown"))
+
+
+def build_fastcall(force: bool = False, verbose: bool = False):
+    """The extension module's path, or None where it cannot be built."""
+    path = fastcall_path()
+    if path is None:
+        return None
+    deps = [FASTCALL_SRC, os.path.join(INCLUDE, "w4a16.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path) for d in deps):
+        return path
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    torch_dir, tmp = _torch_dir(), path + ".%d.tmp" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O1", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"), "-I", INCLUDE, FASTCALL_SRC,
+           "-o", tmp, "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        r = subprocess.CompletedProcess(cmd, 1, "", str(e))
+    if r.returncode != 0:
+        if verbose:
+            print("fastcall.cpp not built:\n%s" % r.stderr)
+        return None
+    os.replace(tmp, path)
+    return path
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if not force and not is_stale():
+        build_fastcall(verbose=verbose)
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     objs = []
@@ -67,8 +117,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        fastcall = ex.submit(build_fastcall, force, verbose)
         objs = list(ex.map(compile_one, srcs))
+        fastcall.result()
     tmp = LIB_PATH + ".%d.tmp" % os.getpid()
     # static CUDA runtime (nvcc default): the library needs no libcudart at load time
     cmd = [nvcc(), ARCH, "-shared", "-Xcompiler", "-fPIC", "--cudart", "static", "-o", tmp] + objs

@@ -1,0 +1,239 @@
+// Argument marshalling of the paged-cache calls, for binding.py.
+//
+// Between kernels of a few microseconds the interpreter's share of a call
+// counts: looking at six tensors' types, shapes, strides and addresses in
+// Python and handing twenty arguments to ctypes takes about five microseconds
+// on a Grace core, here half of one.  Each function checks what it reads and
+// calls the C entry point; it returns the status, or None where an argument is
+// not of the form that it handles -- binding.py then takes its own way, which
+// names what is wrong or fills in what was left out.  No arithmetic, no
+// allocation, no state but the entry points.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "w4a16.h"
+
+namespace {
+
+decltype(&w4a16_paged_map) g_map;
+decltype(&w4a16_rope_append) g_append;
+decltype(&w4a16_paged_attention) g_attention;
+PyObject* g_current_stream;  // device index -> raw stream
+
+const at::Tensor* tensor_of(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
+
+// int32 vector of n entries on the GPU
+bool vector_of(PyObject* o, int64_t n, int32_t** p) {
+    const at::Tensor* t = tensor_of(o);
+    if (!t || t->scalar_type() != at::kInt || !t->is_cuda() || t->dim() != 1 || t->size(0) != n ||
+        (n > 1 && t->stride(0) != 1))
+        return false;
+    *p = static_cast<int32_t*>(t->data_ptr());
+    return true;
+}
+
+struct Table {
+    int32_t* p;
+    int64_t rows, columns, stride;
+};
+bool table_of(PyObject* o, Table* x) {
+    const at::Tensor* t = tensor_of(o);
+    if (!t || t->scalar_type() != at::kInt || !t->is_cuda() || t->dim() != 2) return false;
+    x->rows = t->size(0), x->columns = t->size(1), x->stride = t->stride(0);
+    if (x->columns > 1 && t->stride(1) != 1) return false;
+    if (x->rows <= 1 && x->stride < x->columns) x->stride = x->columns;
+    x->p = static_cast<int32_t*>(t->data_ptr());
+    return true;
+}
+
+// bf16 [rows, heads, dim], dim contiguous
+struct Rows {
+    uint16_t* p = nullptr;
+    int64_t n = 0, heads = 0, dim = 0, row = 0, head = 0;
+    int device = -1;
+};
+bool rows_of(PyObject* o, Rows* x) {
+    const at::Tensor* t = tensor_of(o);
+    if (!t || t->scalar_type() != at::kBFloat16 || !t->is_cuda() || t->dim() != 3 || t->stride(2) != 1) return false;
+    x->n = t->size(0), x->heads = t->size(1), x->dim = t->size(2);
+    x->row = t->stride(0), x->head = t->stride(1);
+    x->device = t->get_device();
+    x->p = static_cast<uint16_t*>(t->data_ptr());
+    return true;
+}
+
+// the raw stream given, or the current one of `device`
+bool stream_of(PyObject* o, int device, void** s) {
+    if (o != Py_None) {
+        *s = PyLong_AsVoidPtr(o);
+        return !PyErr_Occurred();
+    }
+    PyObject* index = PyLong_FromLong(device);
+    PyObject* raw = index ? PyObject_CallOneArg(g_current_stream, index) : nullptr;
+    Py_XDECREF(index);
+    if (!raw) return false;
+    *s = PyLong_AsVoidPtr(raw);
+    Py_DECREF(raw);
+    return !PyErr_Occurred();
+}
+
+bool integer(PyObject* o, int64_t* v) {
+    if (!PyLong_Check(o)) return false;
+    *v = PyLong_AsLongLong(o);
+    return !PyErr_Occurred();
+}
+
+PyObject* other_form() {  // not for here: no error is left behind
+    PyErr_Clear();
+    Py_RETURN_NONE;
+}
+
+template <class Call>
+PyObject* status_of(Call call) {
+    w4a16_status rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = call();
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+// (ctx_len, new_len, block_table, free_blocks, free_head, page, num_blocks, tokens, out, stream)
+PyObject* paged_map(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 10 || !g_map) return other_form();
+    try {
+        const at::Tensor* first = tensor_of(a[0]);
+        if (!first || first->dim() != 1 || !PyTuple_Check(a[8]) || PyTuple_GET_SIZE(a[8]) != 5) return other_form();
+        const int64_t B = first->size(0);
+        const at::Tensor* free_t = tensor_of(a[3]);
+        if (!free_t || free_t->dim() != 1) return other_form();
+        const int64_t F = free_t->size(0);
+        int32_t *ctx, *fresh, *free_blocks, *head, *slots, *positions, *row_start, *kv_len, *head_out;
+        Table t;
+        int64_t page, blocks, tokens;
+        void* stream;
+        if (!integer(a[5], &page) || !integer(a[6], &blocks) || !integer(a[7], &tokens) || !vector_of(a[0], B, &ctx) ||
+            !vector_of(a[1], B, &fresh) || !table_of(a[2], &t) || t.rows != B || !vector_of(a[3], F, &free_blocks) ||
+            !vector_of(a[4], 1, &head) || !vector_of(PyTuple_GET_ITEM(a[8], 0), tokens, &slots) ||
+            !vector_of(PyTuple_GET_ITEM(a[8], 1), tokens, &positions) ||
+            !vector_of(PyTuple_GET_ITEM(a[8], 2), B + 1, &row_start) || !vector_of(PyTuple_GET_ITEM(a[8], 3), B, &kv_len) ||
+            !vector_of(PyTuple_GET_ITEM(a[8], 4), 1, &head_out) || B > INT32_MAX || t.columns > INT32_MAX ||
+            page > INT32_MAX || page < INT32_MIN || !stream_of(a[9], first->get_device(), &stream))
+            return other_form();
+        return status_of([&] {
+            return g_map(ctx, fresh, static_cast<int>(B), t.p, t.stride, static_cast<int>(t.columns), free_blocks, F, head,
+                         static_cast<int>(page), blocks, slots, positions, tokens, row_start, kv_len, head_out, stream);
+        });
+    } catch (...) {
+        return other_form();
+    }
+}
+
+// (q, k, v, positions, inv_freq, slots, cache address, cache heads, sections address, axes, flags, q_out, stream)
+PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 13 || !g_append) return other_form();
+    try {
+        Rows q, out, k, v;
+        int32_t *slots = nullptr, *positions;
+        int64_t cache = 0, heads = 0, sections, axes, flags;
+        if (a[0] != Py_None) {
+            if (!rows_of(a[0], &q) || !rows_of(a[11], &out) || out.n != q.n || out.heads != q.heads || out.dim != q.dim)
+                return other_form();
+        }
+        if (a[6] != Py_None) {
+            if (!integer(a[6], &cache) || !integer(a[7], &heads) || !rows_of(a[1], &k) || !rows_of(a[2], &v) || k.heads != heads ||
+                v.heads != heads || v.n != k.n || v.dim != k.dim || (q.p && (q.n != k.n || q.dim != k.dim)) ||
+                !vector_of(a[5], k.n, &slots))
+                return other_form();
+        }
+        const Rows& any = q.p ? q : k;
+        const at::Tensor* pos = tensor_of(a[3]);
+        const at::Tensor* freq = tensor_of(a[4]);
+        void* stream;
+        if (!any.p || !pos || !freq || !integer(a[8], &sections) || !integer(a[9], &axes) || !integer(a[10], &flags) ||
+            freq->scalar_type() != at::kFloat || !freq->is_cuda() || freq->dim() != 1 || !freq->is_contiguous())
+            return other_form();
+        if (pos->dim() == 1) {
+            if (axes != 1 || !vector_of(a[3], any.n, &positions)) return other_form();
+        } else {
+            if (pos->dim() != 2 || pos->scalar_type() != at::kInt || !pos->is_cuda() || !pos->is_contiguous() || pos->size(0) != axes ||
+                pos->size(1) != any.n)
+                return other_form();
+            positions = static_cast<int32_t*>(pos->data_ptr());
+        }
+        if (any.n == 0 || q.heads > INT32_MAX || freq->size(0) > INT32_MAX / 2 || !stream_of(a[12], any.device, &stream))
+            return other_form();
+        const int rotary = 2 * static_cast<int>(freq->size(0));
+        const float* f = static_cast<const float*>(freq->data_ptr());
+        return status_of([&] {
+            return g_append(q.p, q.row, q.head, out.p, out.row, out.head, static_cast<int>(q.heads), k.p, k.row, k.head, v.p, v.row,
+                            v.head, positions, any.n, f, reinterpret_cast<const int32_t*>(sections), static_cast<int>(axes), rotary,
+                            static_cast<int>(any.dim), static_cast<unsigned>(flags), slots,
+                            reinterpret_cast<const w4a16_kv_cache*>(cache), any.n, stream);
+        });
+    } catch (...) {
+        return other_form();
+    }
+}
+
+// (q, cache address, cache dim, block_table, kv_len, scale, window, out, lse, workspace, stream)
+PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 11 || !g_attention) return other_form();
+    try {
+        Rows q, out;
+        Table t;
+        int32_t* lengths;
+        int64_t cache, dim, window;
+        if (!rows_of(a[0], &q) || !integer(a[1], &cache) || !integer(a[2], &dim) || q.dim != dim || !table_of(a[3], &t) ||
+            t.rows != q.n || !vector_of(a[4], q.n, &lengths) || !integer(a[6], &window) || !rows_of(a[7], &out) || out.n != q.n ||
+            out.heads != q.heads || out.dim != dim)
+            return other_form();
+        const at::Tensor *lse = tensor_of(a[8]), *ws = tensor_of(a[9]);
+        if (!lse || !ws || lse->scalar_type() != at::kFloat || !lse->is_cuda() || lse->dim() != 2 || lse->size(0) != q.n ||
+            lse->size(1) != q.heads || !lse->is_contiguous() || !ws->is_cuda() || !ws->is_contiguous())
+            return other_form();
+        const double scale = PyFloat_AsDouble(a[5]);
+        void* stream;
+        if (PyErr_Occurred() || q.n > INT32_MAX || q.heads > INT32_MAX || t.columns > INT32_MAX || window > INT32_MAX ||
+            window < INT32_MIN || !stream_of(a[10], q.device, &stream))
+            return other_form();
+        float* l = static_cast<float*>(lse->data_ptr());
+        void* w = ws->data_ptr();
+        const size_t bytes = ws->nbytes();
+        return status_of([&] {
+            return g_attention(q.p, q.row, q.head, reinterpret_cast<const w4a16_kv_cache*>(cache), t.p, t.stride,
+                               static_cast<int>(t.columns), lengths, static_cast<int>(q.n), static_cast<int>(q.heads),
+                               static_cast<float>(scale), static_cast<int>(window), out.p, out.row, out.head, l, w, bytes, stream);
+        });
+    } catch (...) {
+        return other_form();
+    }
+}
+
+// bind(map address, append address, attention address, current-stream function)
+PyObject* bind(PyObject*, PyObject* args) {
+    unsigned long long m, p, t;
+    PyObject* f;
+    if (!PyArg_ParseTuple(args, "KKKO", &m, &p, &t, &f)) return nullptr;
+    g_map = reinterpret_cast<decltype(g_map)>(m);
+    g_append = reinterpret_cast<decltype(g_append)>(p);
+    g_attention = reinterpret_cast<decltype(g_attention)>(t);
+    Py_INCREF(f);
+    Py_XDECREF(g_current_stream);
+    g_current_stream = f;
+    Py_RETURN_NONE;
+}
+
+PyMethodDef g_methods[] = {
+    {"bind", bind, METH_VARARGS, nullptr},
+    {"paged_map", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(paged_map)), METH_FASTCALL, nullptr},
+    {"rope_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(rope_append)), METH_FASTCALL, nullptr},
+    {"paged_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(paged_attention)), METH_FASTCALL, nullptr},
+    {nullptr, nullptr, 0, nullptr},
+};
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__fastcall() { return PyModule_Create(&g_module); }
