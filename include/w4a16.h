@@ -584,8 +584,8 @@ W4A16_API size_t w4a16_paged_attention_workspace_bytes(int q_heads, int kv_heads
  *   q, out: bf16, request b's head h at b * *_request + h * *_head; lse: fp32
  *   [B][q_heads] or NULL.
  *   block_table: int32, rows table_stride apart, `columns` entries; entries
- *   past a request's length are not read, nor is anything in the cache that
- *   no request sees.  A token whose block id is outside [0, cache->blocks) is
+ *   past a request's length may hold anything, and nothing in the cache that
+ *   no request sees is read.  A token whose block id is outside [0, cache->blocks) is
  *   left out and W4A16_DEVERR_SLOT set, as for a length above columns * page
  *   (a negative one counts as 0).
  *   workspace: >= w4a16_paged_attention_workspace_bytes(...) bytes, 16-byte

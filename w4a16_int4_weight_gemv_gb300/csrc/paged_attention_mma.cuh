@@ -729,7 +729,7 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kShareWarps * 32), 1
     if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
 }
 
-// A float4 and a float2 of the CTA `rank` of the cluster, at the place `local` has in this one.
+// Where the CTA `rank` of the cluster has what this one has at `local`.
 __device__ __forceinline__ uint32_t cluster_address(const void* local, uint32_t rank) {
     uint32_t remote;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(local)), "r"(rank));
@@ -740,10 +740,33 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t at) {
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
     return v;
 }
-__device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t at) {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+__device__ __forceinline__ float ld_cluster_f32(uint32_t at) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
     return v;
+}
+
+template <bool E4M3>
+__device__ __forceinline__ void store_lse(const AttentionArgs& a, int b, const Heads& hd, int h, float m, float l) {
+    if (a.lse && h < hd.n) a.lse[static_cast<int64_t>(b) * a.q_heads + hd.first + h] = lse_of<E4M3>(m, l);
+}
+
+// The factors of up to eight parts of a head, one lane each (lanes 8 h .. 8 h + 7
+// of a warp); m and l become those of all parts.
+__device__ __forceinline__ float join_factor(float& m, float& l) {
+    float top = m, all;
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));  // of an empty part: -infinity
+    const float f = l != 0.f ? part_factor(m, top) : 0.f;
+    all = l * f;
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2) all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
+    m = top, l = all;
+    return f;
+}
+__device__ __forceinline__ void add_scaled(float4& o, const float4& x, float2 f) {
+    o.x = fmaf(x.x, f.x, o.x), o.y = fmaf(x.y, f.y, o.y);
+    o.z = fmaf(x.z, f.x, o.z), o.w = fmaf(x.w, f.y, o.w);
 }
 
 // A part's 16 dims of 8 heads, with what joining them takes: m and l of the
@@ -770,24 +793,6 @@ struct DimPart {
         o.x = o.x * f0[0] + x.x * f1[0], o.y = o.y * f0[1] + x.y * f1[1];
         o.z = o.z * f0[0] + x.z * f1[0], o.w = o.w * f0[1] + x.w * f1[1];
     }
-    // `count` parts at once: their maximum first, so that no exponential waits for another
-    template <class M, class L, class Dims>
-    __device__ __forceinline__ void join(int count, M m_of, L l_of, Dims o_of) {
-        clear();
-#pragma unroll 4
-        for (int i = 0; i < count; ++i) {
-            const float2 xm = m_of(i);  // of an empty part: -infinity
-            m[0] = fmaxf(m[0], xm.x), m[1] = fmaxf(m[1], xm.y);
-        }
-#pragma unroll 4
-        for (int i = 0; i < count; ++i) {
-            const float2 xm = m_of(i), xl = l_of(i);
-            const float4 x = o_of(i);
-            const float f0 = xl.x != 0.f ? part_factor(xm.x, m[0]) : 0.f, f1 = xl.y != 0.f ? part_factor(xm.y, m[1]) : 0.f;
-            l[0] += xl.x * f0, l[1] += xl.y * f1;
-            o.x += x.x * f0, o.y += x.y * f1, o.z += x.z * f0, o.w += x.w * f1;
-        }
-    }
     // the result: dims of step k, heads of block n
     template <bool E4M3>
     __device__ __forceinline__ void finish(const AttentionArgs& a, int b, const Heads& hd, int n, int k, int lane) const {
@@ -797,12 +802,10 @@ struct DimPart {
         const bool have = n * 8 + r < hd.n && k * 16 < a.cache.dim;
         uint16_t* out = a.out + b * a.out_request + (hd.first + n * 8 + r) * a.out_head + k * 16;
         store_dims<E4M3>(o, f0, f1, have ? out : nullptr, c);
-        if (a.lse && k == 0 && r == 0)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int h = n * 8 + 2 * c + e;
-                if (h < hd.n) a.lse[static_cast<int64_t>(b) * a.q_heads + hd.first + h] = lse_of<E4M3>(m[e], l[e]);
-            }
+        if (k == 0 && r == 0) {
+            store_lse<E4M3>(a, b, hd, n * 8 + 2 * c, m[0], l[0]);
+            store_lse<E4M3>(a, b, hd, n * 8 + 2 * c + 1, m[1], l[1]);
+        }
     }
 };
 
@@ -870,7 +873,7 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kRowWarps * 32), 1)
     constexpr int S = Sh::kRowStages, HEADS = Sh::kHeads, KS = Sh::kSteps, W = Sh::kRowWarps;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t tile_mask[W][S];
-    __shared__ __align__(8) float part_m[W][HEADS], part_l[W][HEADS], cta_m[HEADS], cta_l[HEADS];
+    __shared__ __align__(8) float part_m[W][HEADS], part_l[W][HEADS], part_f[W][HEADS], cta_m[HEADS], cta_l[HEADS], cta_f[8][HEADS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
     const int wir = warp & (wpr - 1), warp0 = warp - wir;  // warp in its row (of this CTA), and the row's first
@@ -883,21 +886,24 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kRowWarps * 32), 1)
         clear_ring(smem, Sh::kRowSmem, threadIdx.x, W * 32);
         __syncthreads();
     }
+    const Heads hd = b < a.B ? heads_of<HEADS>(a, row) : Heads{};
     grid_dependency_wait();
     grid_dependents_launch();
+    // Queries, block ids (where they do not depend on the length) and length are
+    // requested together.
+    RowMath<E4M3, DP, NT> math;
+    TileCopy<E4M3, DP, NT> copy;
     Request q{};
-    Heads hd{};
     if (b < a.B) {
-        hd = heads_of<HEADS>(a, row);
+        const bool early = a.window == 0 && TileCopy<E4M3, DP, NT>::aligned(a);
+        if (early) copy.look_up(a, b, q, first_tile, (a.most + kTile - 1) / kTile, step, lane);
+        math.begin(a, b, hd, lane);
         q = request_of(a, b, bad);
+        if (!early) copy.look_up(a, b, q, first_tile, q.tiles, step, lane);
         if (q.tiles == 0 && rank == 0) store_empty(a, b, hd.first, hd.n, wir * 32 + lane, wpr * 32);
     }
     if (first_tile < q.tiles) {
-        RowMath<E4M3, DP, NT> math;
-        TileCopy<E4M3, DP, NT> copy;
         int ahead = first_tile, put = 0, slot = 0, primed = 0;
-        copy.look_up(a, b, q, ahead, q.tiles, step, lane);
-        math.begin(a, b, hd, lane);
         for (int t = first_tile; t < q.tiles;) {
             const bool full = primed == S - 1;
             if (full) cp_async_wait_group<S - 2>();
@@ -922,7 +928,7 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kRowWarps * 32), 1)
         cp_async_wait_group<0>();
         __syncwarp();
         math.reduce();
-        if (step == 1) {
+        if (step == 1 || q.tiles == 1) {  // nobody else has a part
             math.finish(a, b, hd, lane);
         } else {
             math.store_part(reinterpret_cast<float*>(smem + warp * Sh::kRowRing), part_m[warp], part_l[warp], lane);
@@ -931,37 +937,68 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kRowWarps * 32), 1)
     if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
     if (step == 1) return;
     __syncthreads();
-    if (q.tiles == 0) return;
+    const bool joins = q.tiles > 1;
     const int used = min((q.tiles - rank + cluster - 1) / cluster, wpr);  // warps here that had a tile (at most 0: none)
     const int r = lane >> 2, c = lane & 3;
+    const float vs = E4M3 && joins ? a.cache.v_scale[hd.hk] : 1.f;
     float4* const cta_part = reinterpret_cast<float4*>(smem + Sh::kPartBytes);
+    if (joins)
+        for (int x = wir * 32 + lane; x < HEADS * 8; x += wpr * 32) {
+            const int h = x >> 3, i = x & 7;
+            float m = -INFINITY, l = 0.f;
+            if (i < used) m = part_m[warp0 + i][h], l = part_l[warp0 + i][h];
+            const float f = join_factor(m, l);
+            if (i < wpr) part_f[warp0 + i][h] = f;
+            if (i == 0) {
+                if (cluster == 1) {
+                    store_lse<E4M3>(a, b, hd, h, m, l);
+                    part_l[warp0][h] = l != 0.f ? vs / l : 0.f;  // now the result's factor
+                } else {
+                    cta_m[h] = m, cta_l[h] = l;
+                }
+            }
+        }
+    __syncthreads();
+    if (!joins) return;
 #pragma unroll 1
     for (int u = wir; u < NT * KS; u += wpr) {
         const int n = u / KS, k = u % KS, h = n * 8 + 2 * c;
-        DimPart s;
-        s.join(used, [&](int i) { return *reinterpret_cast<const float2*>(&part_m[warp0 + i][h]); },
-               [&](int i) { return *reinterpret_cast<const float2*>(&part_l[warp0 + i][h]); },
-               [&](int i) { return reinterpret_cast<const float4*>(smem + (warp0 + i) * Sh::kRowRing)[u * 32 + lane]; });
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = 0; i < used; ++i)
+            add_scaled(o, reinterpret_cast<const float4*>(smem + (warp0 + i) * Sh::kRowRing)[u * 32 + lane],
+                       *reinterpret_cast<const float2*>(&part_f[warp0 + i][h]));
         if (cluster == 1) {
-            s.finish<E4M3>(a, b, hd, n, k, lane);
+            const float2 f = *reinterpret_cast<const float2*>(&part_l[warp0][h]);
+            uint16_t* out = a.out + b * a.out_request + (hd.first + n * 8 + r) * a.out_head + k * 16;
+            store_dims<E4M3>(o, f.x, f.y, n * 8 + r < hd.n && k * 16 < a.cache.dim ? out : nullptr, c);
         } else {
-            cta_part[u * 32 + lane] = s.o;
-            if (k == 0 && r == 0) {
-                *reinterpret_cast<float2*>(&cta_m[h]) = make_float2(s.m[0], s.m[1]);
-                *reinterpret_cast<float2*>(&cta_l[h]) = make_float2(s.l[0], s.l[1]);
-            }
+            cta_part[u * 32 + lane] = o;
         }
     }
     if (cluster == 1) return;
     cluster_barrier();
+    for (int x = threadIdx.x; x < HEADS * 8; x += W * 32) {
+        const int h = x >> 3, i = x & 7;
+        float m = -INFINITY, l = 0.f;
+        if (i < cluster) m = ld_cluster_f32(cluster_address(&cta_m[h], i)), l = ld_cluster_f32(cluster_address(&cta_l[h], i));
+        cta_f[i][h] = join_factor(m, l);
+        if (i == 0) {
+            if (rank == 0) store_lse<E4M3>(a, b, hd, h, m, l);
+            part_l[0][h] = l != 0.f ? vs / l : 0.f;
+        }
+    }
+    __syncthreads();
 #pragma unroll 1
     for (int u = warp * cluster + rank; u < NT * KS; u += W * cluster) {
         const int n = u / KS, k = u % KS, h = n * 8 + 2 * c;
-        DimPart s;
-        s.join(cluster, [&](int i) { return ld_cluster_f32x2(cluster_address(&cta_m[h], i)); },
-               [&](int i) { return ld_cluster_f32x2(cluster_address(&cta_l[h], i)); },
-               [&](int i) { return ld_cluster_f32x4(cluster_address(cta_part + u * 32 + lane, i)); });
-        s.finish<E4M3>(a, b, hd, n, k, lane);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = 0; i < cluster; ++i)
+            add_scaled(o, ld_cluster_f32x4(cluster_address(cta_part + u * 32 + lane, i)), *reinterpret_cast<const float2*>(&cta_f[i][h]));
+        const float2 f = *reinterpret_cast<const float2*>(&part_l[0][h]);
+        uint16_t* out = a.out + b * a.out_request + (hd.first + n * 8 + r) * a.out_head + k * 16;
+        store_dims<E4M3>(o, f.x, f.y, n * 8 + r < hd.n && k * 16 < a.cache.dim ? out : nullptr, c);
     }
     cluster_barrier();  // nobody leaves while its part may be read
 }
