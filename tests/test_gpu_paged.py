@@ -100,6 +100,30 @@ def test_map_long_prompts(w):
     check_map(w, ctx, new, table, free, head, 16, blocks, sum(new))
 
 
+@pytest.mark.parametrize("tokens", [90001, 400000])
+def test_map_buffers_off_16_bytes(w, tokens):
+    # many tokens (four a thread), outputs that begin anywhere, requests without new tokens between
+    rng = random.Random(tokens)
+    new = [rng.choice([0, 0, 1, 3, rng.randrange(2 * tokens // 40)]) for _ in range(40)]
+    ctx = [rng.randrange(50) for _ in new]
+    ctx, new, tokens = ctx, new, max(tokens, sum(new) + 2)
+    page, blocks = 24, sum(-(-(c + n) // 24) for c, n in zip(ctx, new)) + 5
+    ids = list(range(blocks))
+    rng.shuffle(ids)
+    columns = max(-(-(c + n) // page) for c, n in zip(ctx, new)) + 1
+    table = [[ids.pop() for _ in range(-(-c // page))] for c in ctx]
+    table = [r + [-1] * (columns - len(r)) for r in table]
+    want = ref.paged_map(ctx, new, table, ids, 0, page, blocks, tokens)
+    for shift in (1, 2, 4):
+        wide = [torch.full((tokens + 8,), 7, dtype=torch.int32, device="cuda") for _ in range(2)]
+        out = w.paged_map_buffers(40, tokens, "cuda")._replace(slots=wide[0][shift:shift + tokens], positions=wide[1][shift:shift + tokens])
+        m = w.w4a16_paged_map(i32(ctx), i32(new), i32(table), i32(ids), i32([0]), page, blocks, tokens, out=out)
+        assert m.slots.tolist() == want[1] and m.positions.tolist() == want[2]
+        for x in wide:
+            assert (x[:shift] == 7).all() and (x[shift + tokens:] == 7).all()
+    assert w.w4a16_device_error(clear=True) == 0
+
+
 def test_map_most_requests(w):
     ctx, new, table, free, head, blocks = map_problem(6, 16384, 16, 5, 3)
     check_map(w, ctx, new, table, free, head, 16, blocks, sum(new) + 1)
