@@ -14,6 +14,13 @@
 // memory once, for all heads.  A thread has one unit of 16 values of a token
 // and takes it of TOKENS tokens of a group, all loads on their way while the
 // angles are formed; two buffers of angles leave one barrier a group.
+//
+// Measured on one GB300 (copies run at 6.67 TB/s), 32 query and 8 key/value
+// heads of 128: 16384 tokens of three axes into bf16 66.7 us (6.04 TB/s), 4095
+// tokens into e4m3 20.2 us (4.56 TB/s; 57 % of the issue slots and the last
+// groups' tail), one token 2.0 us.  Two tokens a thread and four CTAs of 256
+// threads an SM: of one to four tokens and 256 to 512 threads the others took
+// 65 to 108 us for the first, 20 to 36 us for the second.
 #include <algorithm>
 
 #include <cuda_fp8.h>
