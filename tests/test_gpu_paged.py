@@ -272,6 +272,30 @@ def test_rope_append_matches_the_plain_form(w, case):
         assert torch.equal(stored.float().cpu()[i // page, i % page], before.float().cpu()[i // page, i % page])
 
 
+@pytest.mark.parametrize("case", [
+    # several groups of tokens a thread block, the last one ragged; one and two tokens a thread
+    (10007, 14, 1, 128, 128, [24, 20, 20], False, 16, "bf16", "token", 100000),
+    (10007, 14, 1, 128, 48, [24], True, 24, "bf16", "head", 1 << 25),
+    (10007, 14, 1, 128, 80, [40], True, 16, "fp8", "token", 100000),
+    (12001, 6, 5, 112, 64, [32], False, 7, "bf16", "token", 5000),
+    (9001, 1, 1, 48, 16, [8], False, 16, "fp8", "head", 5000),
+    (9001, 33, 2, 64, 64, [32], True, 16, "fp8", "token", 5000),
+    (7777, 5, 3, 80, 0, [0], False, 16, "bf16", "token", 10),
+], ids=lambda c: "T%d-q%d-kv%d-d%d-r%d-%s-%s" % (c[0], c[1], c[2], c[3], c[4], c[8], c[9]))
+def test_rope_append_of_many_tokens(w, case):
+    test_rope_append_matches_the_plain_form(w, case)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_rope_in_place_of_many_tokens(w, inter):
+    x = torch.randn(40011, 4, 64, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+    pos, f = torch.arange(40011).int().cuda(), freqs(64).cuda()
+    y = w.w4a16_rope_append(x, None, None, pos, f, None, None, interleaved=inter)
+    z = x.clone()
+    w.w4a16_rope_append(z, None, None, pos, f, None, None, q_out=z, interleaved=inter)
+    assert torch.equal(y, z)
+
+
 def test_rope_in_place_and_without_keys(w):
     gen = torch.Generator().manual_seed(3)
     x = torch.randn(9, 4, 64, generator=gen).bfloat16()

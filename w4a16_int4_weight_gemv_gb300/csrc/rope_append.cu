@@ -11,16 +11,17 @@
 //
 // Bound by memory: every value is read once and written once.  A CTA takes
 // groups of tokens: it forms the cosines and sines of their pairs in shared
-// memory once, for all heads.  A thread has one unit of 16 values of a token
-// and takes it of TOKENS tokens of a group, all loads on their way while the
-// angles are formed; two buffers of angles leave one barrier a group.
+// memory once, for all heads.  A thread has one unit of 16 values of a token,
+// two runs of eight so that the lanes of a head touch whole sectors, and takes
+// it of TOKENS tokens of a group.  The next group's values, slots and positions
+// are requested before this one's are turned and written: reads and writes
+// overlap within a CTA, and two buffers of angles leave one barrier a group.
 //
 // Measured on one GB300 (copies run at 6.67 TB/s), 32 query and 8 key/value
-// heads of 128: 16384 tokens of three axes into bf16 66.7 us (6.04 TB/s), 4095
-// tokens into e4m3 20.2 us (4.56 TB/s; 57 % of the issue slots and the last
-// groups' tail), one token 2.0 us.  Two tokens a thread and four CTAs of 256
-// threads an SM: of one to four tokens and 256 to 512 threads the others took
-// 65 to 108 us for the first, 20 to 36 us for the second.
+// heads of 128: 16384 tokens of three axes into bf16 63.3 us (6.36 TB/s), 4095
+// tokens into e4m3 18.9 us (4.88 TB/s), one token 1.75 us.  With a group's
+// requests after the last one's writes: 66.6, 20.2 and 1.93 us.  More CTAs an SM
+// leave too few registers: one token a thread and five CTAs 88 us for the first.
 #include <algorithm>
 
 #include <cuda_fp8.h>
@@ -33,8 +34,10 @@ namespace {
 
 constexpr int kThreads = 256;  // at most
 constexpr int kAngles = 2048;  // of a group at most: tokens times pairs
-constexpr int kMany = 2;       // tokens of a thread and group where there are many
-constexpr int kPerSm = 4;      // CTAs of kThreads threads: 64 registers each
+constexpr int kMany = 2;       // tokens of a thread and group where there are many:
+constexpr int kOften = 16;     // groups of an SM at least
+// CTAs of kThreads threads an SM: 64 registers each, 80 with several tokens on their way
+constexpr int per_sm(int tokens) { return tokens == 1 ? 4 : 3; }
 
 // the high and low parts of 1 / pi
 constexpr float kInvPiHi = 0.31830987334251404f;
@@ -99,6 +102,18 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], float scale) {
     return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
+// four neighbouring pairs; their angles: c[0] and c[step]
+__device__ __forceinline__ void turn_neighbours(float (&x)[8], const float4* c, int step) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float4 e = c[i * step];
+        const float y0 = x[4 * i] * e.x - x[4 * i + 1] * e.y, y1 = x[4 * i + 2] * e.z - x[4 * i + 3] * e.w;
+        x[4 * i + 1] = x[4 * i + 1] * e.x + x[4 * i] * e.y;
+        x[4 * i + 3] = x[4 * i + 3] * e.z + x[4 * i + 2] * e.w;
+        x[4 * i] = y0, x[4 * i + 2] = y1;
+    }
+}
+
 // Units of a token: dim / 16 of each head, query heads first, then key heads,
 // then value heads.  Unit u of a head holds the values d0 .. d0 + 7 and
 // d1 .. d1 + 7; the first rotary / 16 units are turned.  grid: (groups of
@@ -107,7 +122,7 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], float scale) {
 // i-th of all units of a token next to one another: no two lanes of a head meet
 // in a bank.
 template <int TOKENS>
-__global__ void __launch_bounds__(kThreads, kPerSm) k_rope_append(const RopeArgs a, const int group, const int range) {
+__global__ void __launch_bounds__(kThreads, per_sm(TOKENS)) k_rope_append(const RopeArgs a, const int group, const int range) {
     extern __shared__ __align__(16) float4 angles[];  // [2][group * half / 2]
     const int per_head = a.dim / 16, half = a.rotary / 2, turned = half / 8;  // turned: units of a head
     const int step = group / TOKENS;  // tokens of a group that the threads take at once
@@ -123,22 +138,38 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_rope_append(const RopeArgs
         const int at = u - head * per_head;
         kind = head < a.q_heads ? 0 : head < a.q_heads + a.cache.heads ? 1 : 2;  // query, key, value
         head -= kind == 0 ? 0 : kind == 1 ? a.q_heads : a.q_heads + a.cache.heads;
-        if (kind != 2 && at * 16 < a.rotary) (a.interleaved ? neighbours : halves) = true;
-        d0 = halves ? at * 8 : at * 16;
-        d1 = halves ? d0 + half : d0 + 8;
+        neighbours = kind != 2 && a.interleaved;
+        halves = kind != 2 && !a.interleaved && at < turned;
+        if (halves) {
+            d0 = at * 8;
+            d1 = d0 + half;
+        } else {  // the two halves of what is turned in place or not at all
+            const int from = kind != 2 && !a.interleaved ? a.rotary : 0;
+            d0 = from + (at - from / 16) * 8;
+            d1 = d0 + (a.dim - from) / 2;
+        }
     }
     const uint16_t* src = kind == 0 ? a.q + head * a.q_head : kind == 1 ? a.k + head * a.k_head : a.v + head * a.v_head;
     const int64_t src_token = kind == 0 ? a.q_token : kind == 1 ? a.k_token : a.v_token;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * group;
+    // the pair whose angle this thread forms first of every group (further ones: in `turns`)
+    const int first_token = half ? static_cast<int>(threadIdx.x) / half : 0;
+    const int first_pair = static_cast<int>(threadIdx.x) - first_token * half;
+    float first_freq = 0.f;
+    const int* first_pos = a.positions;
+    if (first_token < group && half) {
+        int axis = 0;
+        while (axis < 3 && first_pair >= a.axis_end[axis]) ++axis;
+        first_pos += axis * a.axis_stride + first_token;
+    }
     bool bad = false;
     int buffer = 0;
     grid_dependency_wait();
     grid_dependents_launch();
+    if (first_token < group && half) first_freq = a.inv_freq[first_pair];
 
-    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * group; t0 < a.T; t0 += stride) {
+    const auto load = [&](int64_t t0, uint4 (&v0)[TOKENS], uint4 (&v1)[TOKENS], int (&slot)[TOKENS], int& pos) {
         const int tokens = a.T - t0 < group ? static_cast<int>(a.T - t0) : group;
-        uint4 v0[TOKENS], v1[TOKENS];
-        int slot[TOKENS];
 #pragma unroll
         for (int j = 0; j < TOKENS; ++j) {
             const int token = my_token + j * step;
@@ -149,17 +180,39 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_rope_append(const RopeArgs
             v0[j] = *reinterpret_cast<const uint4*>(x + d0);
             v1[j] = *reinterpret_cast<const uint4*>(x + d1);
         }
+        if (half && first_token < tokens) pos = first_pos[t0];
+    };
+    const auto put = [&](float4* cs, int token, int pair, int pos, float f) {
+        float2 c = turn_of(pos, f);
+        if (a.inverse) c.y = -c.y;
+        cs += token * 4 * turned;
+        cs += a.interleaved ? (pair & 3) / 2 * 2 * turned + pair / 4 : (pair & 7) / 2 * turned + pair / 8;
+        reinterpret_cast<float2*>(cs)[pair & 1] = c;
+    };
+    const auto turns = [&](int64_t t0, int pos) {
         float4* const cs = angles + buffer * (group * half / 2);
-        buffer ^= 1;
-        for (int i = threadIdx.x; i < tokens * half; i += blockDim.x) {
+        const int tokens = a.T - t0 < group ? static_cast<int>(a.T - t0) : group;
+        if (half && first_token < tokens) put(cs, first_token, first_pair, pos, first_freq);
+        for (int i = threadIdx.x + blockDim.x; i < tokens * half; i += blockDim.x) {
             const int token = i / half, pair = i - token * half;
             int axis = 0;
             while (axis < 3 && pair >= a.axis_end[axis]) ++axis;
-            float2 c = turn_of(a.positions[axis * a.axis_stride + t0 + token], a.inv_freq[pair]);
-            if (a.inverse) c.y = -c.y;
-            reinterpret_cast<float2*>(cs + (token * 4 + (pair & 7) / 2) * turned + pair / 8)[pair & 1] = c;
+            put(cs, token, pair, a.positions[axis * a.axis_stride + t0 + token], a.inv_freq[pair]);
         }
-        __syncthreads();
+    };
+
+    int64_t t0 = static_cast<int64_t>(blockIdx.x) * group;
+    uint4 v0[TOKENS], v1[TOKENS];
+    int slot[TOKENS], pos = 0;
+    load(t0, v0, v1, slot, pos);
+    turns(t0, pos);
+    __syncthreads();
+    while (true) {
+        const bool more = a.T - t0 > stride;
+        uint4 n0[TOKENS], n1[TOKENS];
+        int nslot[TOKENS];
+        if (more) load(t0 + stride, n0, n1, nslot, pos);
+        const float4* const cs = angles + buffer * (group * half / 2);
 #pragma unroll
         for (int j = 0; j < TOKENS; ++j) {
             const int token = my_token + j * step, to = slot[j];
@@ -171,24 +224,19 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_rope_append(const RopeArgs
             float p[8], q[8];
             unpack8(v0[j], p);
             unpack8(v1[j], q);
-            if (halves || neighbours) {
-                const float4* c = cs + token * 4 * turned + (halves ? d0 / 8 : d0 / 16);
+            if (halves) {
+                const float4* c = cs + token * 4 * turned + d0 / 8;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float4 e = c[i * turned];
-                    if (halves) {
-                        const float y0 = p[2 * i] * e.x - q[2 * i] * e.y, y1 = p[2 * i + 1] * e.z - q[2 * i + 1] * e.w;
-                        q[2 * i] = q[2 * i] * e.x + p[2 * i] * e.y;
-                        q[2 * i + 1] = q[2 * i + 1] * e.z + p[2 * i + 1] * e.w;
-                        p[2 * i] = y0, p[2 * i + 1] = y1;
-                    } else {
-                        float* x = i < 2 ? p + 4 * i : q + 4 * (i - 2);
-                        const float y0 = x[0] * e.x - x[1] * e.y, y1 = x[2] * e.z - x[3] * e.w;
-                        x[1] = x[1] * e.x + x[0] * e.y;
-                        x[3] = x[3] * e.z + x[2] * e.w;
-                        x[0] = y0, x[2] = y1;
-                    }
+                    const float y0 = p[2 * i] * e.x - q[2 * i] * e.y, y1 = p[2 * i + 1] * e.z - q[2 * i + 1] * e.w;
+                    q[2 * i] = q[2 * i] * e.x + p[2 * i] * e.y;
+                    q[2 * i + 1] = q[2 * i + 1] * e.z + p[2 * i + 1] * e.w;
+                    p[2 * i] = y0, p[2 * i + 1] = y1;
                 }
+            } else if (neighbours) {
+                if (d0 < a.rotary) turn_neighbours(p, cs + token * 4 * turned + d0 / 8, 2 * turned);
+                if (d1 < a.rotary) turn_neighbours(q, cs + token * 4 * turned + d1 / 8, 2 * turned);
             }
             if (kind == 0) {
                 uint16_t* dst = a.q_out + (t0 + token) * a.qo_token + head * a.qo_head;
@@ -201,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_rope_append(const RopeArgs
             const int64_t offset = kind == 1 ? block * a.cache.k_block + place * a.cache.k_token + head * a.cache.k_head
                                              : block * a.cache.v_block + place * a.cache.v_token + head * a.cache.v_head;
             void* cache = kind == 1 ? a.cache.k : a.cache.v;
-            if (a.cache.dtype == W4A16_CACHE_BF16) {
+            if (TOKENS > 1 || a.cache.dtype == W4A16_CACHE_BF16) {  // several tokens: never over e4m3
                 uint16_t* dst = static_cast<uint16_t*>(cache) + offset;
                 *reinterpret_cast<uint4*>(dst + d0) = pack8(p);
                 *reinterpret_cast<uint4*>(dst + d1) = pack8(q);
@@ -212,6 +260,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_rope_append(const RopeArgs
                 *reinterpret_cast<uint2*>(dst + d1) = pack8_e4m3(q, scale);
             }
         }
+        if (!more) break;
+        t0 += stride;
+        buffer ^= 1;
+        turns(t0, pos);
+#pragma unroll
+        for (int j = 0; j < TOKENS; ++j) v0[j] = n0[j], v1[j] = n1[j], slot[j] = nslot[j];
+        __syncthreads();
     }
     if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
 }
@@ -230,15 +285,19 @@ cudaError_t launch_rope_append(const RopeArgs& a, const DeviceInfo& dev, cudaStr
     if (half) step = std::min<int64_t>(step, kAngles / (kMany * half));
     step = std::max<int64_t>(1, std::min<int64_t>(step, a.T * parts / dev.sms));
     const int threads = static_cast<int>(step * range + 31) / 32 * 32;
-    // and how often: where every SM gets several groups all the same
-    const bool many = a.T * parts >= step * kMany * 4 * dev.sms;
+    // and how often: several times over bf16 where that leaves enough groups for the SMs to
+    // end together (4095 tokens of 32 + 2 * 8 heads of 128: 18.3 us against 18.9, 16384 63
+    // against 67; 1500 tokens 8.6 against 7.8; over e4m3, where fewer registers are free, 4095
+    // tokens 20.0 against 18.8)
+    const bool bf16 = a.cache.heads == 0 || a.cache.dtype == W4A16_CACHE_BF16;
+    const bool many = bf16 && a.T * parts >= step * kMany * kOften * dev.sms;
     const int group = static_cast<int>(step) * (many ? kMany : 1);
     const int smem = group * half * 16;
     auto* kernel = many ? k_rope_append<kMany> : k_rope_append<1>;
     const cudaError_t rc = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
     if (rc != cudaSuccess) return rc;
     int64_t ctas = (a.T + group - 1) / group;
-    const int64_t wave = std::max<int64_t>(1, static_cast<int64_t>(kPerSm * kThreads / threads) * dev.sms / parts);
+    const int64_t wave = std::max<int64_t>(1, static_cast<int64_t>(per_sm(many ? kMany : 1) * kThreads / threads) * dev.sms / parts);
     if (ctas > wave) ctas = wave;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(parts));
