@@ -268,7 +268,6 @@ struct RowMath {
 
     // the tile at kt (shared address): keys, then values; mask: tokens that count
     __device__ __forceinline__ void tile(uint32_t kt, uint32_t mask, int lane) {
-        constexpr float kBias = E4M3 ? kE4m3Bias : 0.f;
         const uint32_t vt = kt + kTile * Sh::kRowBytes;
         const int r = lane >> 2;
         // two chains of products, where registers allow: the latency of one is a good part of a tile's
@@ -334,8 +333,10 @@ struct RowMath {
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float from = m[n][e & 1] == -INFINITY ? 0.f : m[n][e & 1] - kBias;
-                s[n][e] = exp2_fast(s[n][e] - from);
+                // the bias after the difference: m - 15 is not a float where m passes 2^24, and
+                // the largest p would then be 2^16, which no fp16 holds
+                s[n][e] -= m[n][e & 1] == -INFINITY ? 0.f : m[n][e & 1];
+                s[n][e] = exp2_fast(E4M3 ? s[n][e] + kE4m3Bias : s[n][e]);
                 l[n][e & 1] += s[n][e];
             }
             // to 16 bits for the second product: fp16 rounds p by 2^-11, bf16 by 2^-8 of it
