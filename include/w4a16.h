@@ -547,8 +547,9 @@ W4A16_API w4a16_status w4a16_paged_map(const int32_t* ctx_len, const int32_t* ne
  *   q: bf16, head h of token t at q + t * q_token + h * q_head; q_out the same
  *      with its own strides (may be q itself); both NULL: no queries.
  *   k, v: bf16 like q, cache->heads heads each; rotated k and plain v go to
- *      slot slots[t] of the cache, rounded once: to bf16, or to e4m3 of
- *      value / scale (beyond +-448: +-448).  slots[t] == -1: not stored; a
+ *      slot slots[t] of the cache, rounded once: to bf16, or to e4m3 of the
+ *      fp32 quotient value / scale (beyond +-448: +-448; a scale of 0 gives
+ *      +-448, and NaN for a value of 0).  slots[t] == -1: not stored; a
  *      slot outside the cache: not stored and W4A16_DEVERR_SLOT.  Slots are
  *      to be different from one another.  k, v, slots and cache NULL: no keys.
  *   positions: int32, axis a at positions + a * axis_stride.

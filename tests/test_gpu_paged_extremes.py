@@ -56,3 +56,31 @@ def test_attention_very_large_scores(w, dtype, top, sign, columns):
             assert ((got - want).abs() <= U * want.abs() + 2.0 ** -17 * size).all(), (b, h)
             exact = scores + torch.log(torch.tensor(float(len(mine)), dtype=torch.float64))
             assert abs(lse[b, h].double().cpu() - exact) <= 2.0 ** -21 * abs(exact), (b, h)
+
+
+SCALES = [0.0, -0.0, 2.0 ** -149, 2.0 ** -130, 1.5 * 2.0 ** -127, 2.0 ** -126, 1.1 * 2.0 ** -100, 2.0 ** -60, 0.037, -0.25, 2.0 ** 60, 1.3 * 2.0 ** 100,
+          1.7 * 2.0 ** 120, 2.0 ** 127, float("inf"), float("nan")]
+
+
+def test_append_of_any_scale(w):
+    # a head for every scale; codes equal to those of the fp32 quotient, not-a-numbers where that is none
+    heads, dim, tokens = len(SCALES), 64, 24
+    scale = torch.tensor(SCALES)
+    gen = torch.Generator().manual_seed(3)
+    x = torch.randn(tokens, heads, dim, generator=gen) * 2.0 ** torch.randint(-12, 9, (tokens, heads, dim), generator=gen)
+    near = torch.where(scale.isfinite() & (scale != 0), scale.abs(), 1.0)[:, None]
+    x[:16] *= near  # quotients of a size that the codes hold
+    x[16, :, 32:40] = torch.tensor([0.0, -0.0, float("inf"), -float("inf"), float("nan"), 3e38, -1e-40, 2.0 ** -133])
+    x = x.bfloat16()
+    kv = [torch.zeros(2, 16, heads, dim, dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2)]
+    cache = w.PagedCache(*kv, scale.cuda(), scale.cuda())
+    w.w4a16_rope_append(None, x.cuda(), x.cuda(), i32([0] * tokens), torch.ones(0, device="cuda"), i32(list(range(tokens))), cache)
+    assert w.w4a16_device_error(clear=True) == 0
+    quotient = x.float() / scale[:, None]
+    want = quotient.clamp(-448, 448).to(torch.float8_e4m3fn)
+    for c in kv:  # no pair is turned: keys are stored as values are
+        got = c.cpu().view(32, heads, dim)[:tokens]
+        nan = quotient.isnan()
+        assert torch.equal(got.float().isnan(), nan)
+        differ = (got.view(torch.uint8) != want.view(torch.uint8)) & ~nan
+        assert not differ.any(), differ.nonzero()[:8]
