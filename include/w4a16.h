@@ -592,7 +592,10 @@ W4A16_API size_t w4a16_paged_attention_workspace_bytes(int q_heads, int kv_heads
  *   workspace: >= w4a16_paged_attention_workspace_bytes(...) bytes, 16-byte
  *   aligned; its contents need no initialisation.  Calls that may overlap
  *   need one each.
- * Limits: q_heads a multiple of cache->heads, B * q_heads < 2^24.
+ * Limits: q_heads a multiple of cache->heads, B * q_heads < 2^24; and
+ * (ceil(V / 16) + 3) * R <= 2^31 - 256 with V = columns * page, or the window
+ * where that is smaller, and R = cache->heads times the chunks of the query heads
+ * of each (of 8, from nine on of 16), else W4A16_ERR_UNSUPPORTED.
  */
 W4A16_API w4a16_status w4a16_paged_attention(const uint16_t* q, int64_t q_request, int64_t q_head,
                                              const w4a16_kv_cache* cache,

@@ -99,6 +99,26 @@ def test_attention_checks(w):
         assert call() == S.ERR_CUDA
 
 
+def test_attention_refuses_tables_whose_tiles_pass_32_bits(w):
+    # the launch counts a request's tiles, and two more a row, in 32 bits
+    S, lib = w.Status, w.load_library()
+    def call(columns, page, kv, hq, window=0, B=1):
+        need = lib.w4a16_paged_attention_workspace_bytes(hq, kv, 64)
+        c = cache(w, heads=kv, dim=64, page=page, blocks=1000, k_head=64, v_head=64)
+        return lib.w4a16_paged_attention(A16, 64 * hq, 64, c, A16, columns, columns, A16, B, hq, 0.1, window, A16, 64 * hq, 64, None, A16, need, None)
+    allowed = S.ERR_CUDA if not torch.cuda.is_available() else None  # with a GPU: not launched on these addresses
+    #  tiles of a row, rows: 2^31 - 1024 tokens are 2^27 - 64 tiles
+    for args, fits in (((1 << 27, 16, 16, 16), True), ((1 << 27, 16, 17, 17), False), ((1 << 15, 1 << 16, 17, 17), False),
+                       ((1 << 27, 16, 2, 128), True), ((1 << 27, 16, 2, 2 * 129), False), ((1 << 27, 16, 8, 64), True), ((1 << 27, 16, 8, 72), True),
+                       ((1 << 27, 16, 8, 8 * 17), True), ((1 << 27, 16, 8, 8 * 33), False), ((1 << 27, 16, 17, 17, 1 << 30), True),
+                       ((1 << 27, 16, 64, 64, 1 << 30), False), ((1 << 26, 16, 31, 31), True), ((1 << 26, 16, 32, 32), False),
+                       ((1 << 26, 16, 32, 32, 0, 1000), False)):
+        if not fits:
+            assert call(*args) == S.ERR_UNSUPPORTED, args
+        elif allowed is not None:
+            assert call(*args) == allowed, args
+
+
 def test_binding_refuses_cpu_tensors(w):
     z = torch.zeros
     with pytest.raises(ValueError):

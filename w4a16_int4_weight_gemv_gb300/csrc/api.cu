@@ -836,7 +836,11 @@ w4a16_status w4a16_paged_attention(const uint16_t* q, int64_t q_request, int64_t
     if (st != W4A16_OK) return st;
     if (B < 1 || q_heads < 1 || q_heads % cache->heads != 0 || columns < 1 || table_stride < columns || window < 0)
         return W4A16_ERR_SHAPE;
-    if (static_cast<int64_t>(B) * q_heads >= (1 << 24)) return W4A16_ERR_UNSUPPORTED;
+    int64_t most = static_cast<int64_t>(columns) * cache->page;
+    if (most > 0x7FFFFFFF - 1024) most = 0x7FFFFFFF - 1024;  // token numbers stay in 32 bits
+    if (static_cast<int64_t>(B) * q_heads >= (1 << 24) ||
+        !attention_costs_fit(static_cast<int>(most), window, q_heads, cache->heads))
+        return W4A16_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(out) || !row_strides(q_request, q_head, 8) ||
         !row_strides(out_request, out_head, 8) || !aligned4(block_table) || !aligned4(kv_len) || !aligned4(lse))
         return W4A16_ERR_ALIGN;
@@ -846,8 +850,6 @@ w4a16_status w4a16_paged_attention(const uint16_t* q, int64_t q_request, int64_t
     DeviceCache* dev = nullptr;
     st = current_device(&dev);
     if (st != W4A16_OK) return st;
-    int64_t most = static_cast<int64_t>(columns) * cache->page;
-    if (most > 0x7FFFFFFF - 1024) most = 0x7FFFFFFF - 1024;  // token numbers stay in 32 bits
     AttentionArgs a{q, q_request, q_head, *cache, block_table, table_stride, kv_len, static_cast<int>(most), B, q_heads, window,
                     scale, out, out_request, out_head, lse, workspace, dev->err};
     return from_cuda(launch_paged_attention(a, dev->info, static_cast<cudaStream_t>(stream)));

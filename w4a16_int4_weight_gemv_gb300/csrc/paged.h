@@ -79,6 +79,10 @@ struct AttentionArgs {
     uint32_t* err;
 };
 
+// Whether the tiles that one request can have fit the 32 bits in which the launch
+// counts them.
+bool attention_costs_fit(int most, int window, int q_heads, int kv_heads);
+
 size_t paged_attention_workspace(int q_heads, int kv_heads, int dim);
 cudaError_t launch_paged_attention(const AttentionArgs& a, const DeviceInfo& dev, cudaStream_t s);
 

@@ -3,6 +3,12 @@
 
 namespace w4a16 {
 
+bool attention_costs_fit(int most, int window, int q_heads, int kv_heads) {
+    // (256 dims may take two rows of 8 for 16 heads, but over a short cache only)
+    const int heads = q_heads / kv_heads > 8 ? 16 : 8;
+    return (static_cast<int64_t>(most_tiles(most, window)) + kRowCost) * rows_of_request(q_heads, kv_heads, heads) <= kMostCost;
+}
+
 size_t paged_attention_workspace(int q_heads, int kv_heads, int dim) {
     const int heads = q_heads / kv_heads > 8 ? 16 : 8, padded = padded_dim(dim);
     return static_cast<size_t>(most_workers(padded)) *

@@ -17,6 +17,20 @@ constexpr int padded_dim(int dim) { return dim <= 64 ? 64 : dim <= 96 ? 96 : dim
 // to 160 SMs.
 constexpr int most_workers(int padded) { return padded == 64 ? 2560 : padded <= 128 ? 1920 : 1280; }
 
+constexpr int kTile = 16;    // tokens of a tile: the MMA's rows
+constexpr int kRowCost = 2;  // a row's queries and result, in tiles (1: 128 requests over e4m3 132 us, 2: 125)
+constexpr int kMostCost = 0x7FFFFF00;  // of all rows of a launch: sums a little above it still fit 32 bits
+
+// Tiles of a row at most (a window may begin inside one).
+constexpr int most_tiles(int most, int window) {
+    const int visible = window > 0 && window < most ? window : most;
+    return (visible + kTile - 1) / kTile + (visible < most);
+}
+// Rows of a request: `heads` query heads of a key/value head, or fewer, each.
+constexpr int rows_of_request(int q_heads, int kv_heads, int heads) {
+    return kv_heads * ((q_heads / kv_heads + heads - 1) / heads);
+}
+
 // Rows that several warps of the first launch share, for the second to join.
 // A part is what a warp has of a row: o as the products' accumulators hold it
 // (float4 per lane and 16 dims), then m (log2 units) and l of each head.

@@ -45,8 +45,6 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kTile = 16;       // tokens of a tile: the MMA's rows
-constexpr int kRowCost = 2;     // a row's queries and result, in tiles (1: 128 requests over e4m3 132 us, 2: 125)
 constexpr int kMinCost = 3;     // a warp's share at least
 constexpr int kRowTiles = 8;    // rows kernel: tiles of a warp at most
 constexpr int kRowEnough = 2;   // and where one CTA is enough
@@ -1047,12 +1045,9 @@ template <bool E4M3, int DP, int NT>
 cudaError_t launch_attention_shape(const AttentionArgs& all, const DeviceInfo& dev, JoinPlan jp, cudaStream_t s) {
     using Sh = AttnShape<E4M3, DP, NT>;
     AttentionArgs a = all;
-    const int G = a.q_heads / a.cache.heads;
-    jp.rows = a.cache.heads * ((G + Sh::kHeads - 1) / Sh::kHeads);
+    jp.rows = rows_of_request(a.q_heads, a.cache.heads, Sh::kHeads);
     int64_t all_rows = static_cast<int64_t>(a.B) * jp.rows;
-    // of a row (a window may begin inside a tile)
-    const int visible = a.window > 0 && a.window < a.most ? a.window : a.most;
-    const int most_tiles = (visible + kTile - 1) / kTile + (visible < a.most);
+    const int tiles = most_tiles(a.most, a.window);  // of a row
     // short rows: as many warps for each as one wave of CTAs has, if that leaves
     // a warp few tiles
     {
@@ -1060,20 +1055,20 @@ cudaError_t launch_attention_shape(const AttentionArgs& all, const DeviceInfo& d
         int wpr = W, cluster = 1;
         while (wpr > 1 && all_rows * wpr > static_cast<int64_t>(dev.sms) * W) wpr /= 2;
         // (19 tiles of 8 rows: 6.2 us with a CTA each, 6.9 with two, 5.9 with four)
-        if (Sh::kClusters && wpr == W && most_tiles > kRowEnough * W)
-            while (cluster < 8 && most_tiles > W * cluster && all_rows * cluster * 2 <= dev.sms) cluster *= 2;
+        if (Sh::kClusters && wpr == W && tiles > kRowEnough * W)
+            while (cluster < 8 && tiles > W * cluster && all_rows * cluster * 2 <= dev.sms) cluster *= 2;
         while (cluster > 1 && max_active_clusters(reinterpret_cast<const void*>(k_attention_rows<E4M3, DP, NT>), W * 32,
                                                   Sh::kRowSmem, cluster) < all_rows)
             cluster /= 2;
         const int64_t grid = cluster > 1 ? all_rows * cluster : (all_rows * wpr + W - 1) / W;
-        if (most_tiles <= kRowTiles * wpr * cluster)
+        if (tiles <= kRowTiles * wpr * cluster)
             return launch_kernel(k_attention_rows<E4M3, DP, NT>, true, cluster, dim3(static_cast<unsigned>(grid)), dim3(W * 32),
                                  Sh::kRowSmem, s, a, jp.rows, wpr, cluster);
     }
     const int ctas = std::min(dev.sms, most_workers(DP) / Sh::kShareWarps);
     jp.warps = ctas * Sh::kShareWarps;
-    // as many requests at a time as have costs of 32 bits
-    const int64_t fit = std::max<int64_t>(1, 0x7FFFFFFF / (static_cast<int64_t>(most_tiles + kRowCost) * jp.rows));
+    // as many requests at a time as have costs of 32 bits (one has: attention_costs_fit)
+    const int64_t fit = kMostCost / (static_cast<int64_t>(tiles + kRowCost) * jp.rows);
     for (int from = 0; from < all.B; from += a.B) {
         a.B = static_cast<int>(std::min<int64_t>(all.B - from, fit));
         a.q = all.q + from * a.q_request, a.out = all.out + from * a.out_request;
