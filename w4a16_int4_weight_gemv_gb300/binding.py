@@ -153,6 +153,24 @@ def _stream(stream, device: int = None):
     return torch.cuda.current_stream().cuda_stream
 
 
+def _empty(shape, dtype, device, stream, kept: bool = True) -> torch.Tensor:
+    """Memory that a call on `stream` makes itself.  Where that is not the
+    current stream, it is taken on `stream`: the allocator then hands it to
+    nobody else before the call's kernels are done with it.  What the caller
+    gets (kept) counts as used on the current stream too."""
+    if stream is not None:
+        here = torch.cuda.current_stream(device)
+        if stream.cuda_stream != here.cuda_stream:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+            with torch.cuda.stream(stream):
+                t = torch.empty(shape, dtype=dtype, device=device)
+            if kept:
+                t.record_stream(here)
+            return t
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _ptr(t: torch.Tensor):
     return t.data_ptr()
 
@@ -184,7 +202,7 @@ def int4_pack(codes: torch.Tensor, out: torch.Tensor = None, stream=None) -> tor
     _need(codes, "codes", _U8)
     N, K = codes.shape
     if out is None:
-        out = torch.empty((N, K // 8), dtype=torch.int32, device=codes.device)
+        out = _empty((N, K // 8), torch.int32, codes.device, stream)
     _need(out, "out", _U32, (N, K // 8))
     _check(load_library().int4_pack(_ptr(codes), _ptr(out), N, K, _stream(stream, codes.get_device())),
            "int4_pack")
@@ -199,7 +217,7 @@ def int4_dequant(wq, scale, zero, g: int, out_dtype=torch.bfloat16, out=None, st
     _need(scale, "scale", _BF16, (N, K // g))
     _need(zero, "zero", _U8, (N, K // g))
     if out is None:
-        out = torch.empty((N, K), dtype=out_dtype, device=wq.device)
+        out = _empty((N, K), out_dtype, wq.device, stream)
     _need(out, "out", (torch.bfloat16, torch.float32), (N, K))
     kind = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
     _check(load_library().int4_dequant(_ptr(wq), _ptr(scale), _ptr(zero), _ptr(out), kind,
@@ -213,7 +231,7 @@ def int3_pack(codes: torch.Tensor, out: torch.Tensor = None, stream=None) -> tor
     _need(codes, "codes", _U8)
     N, K = codes.shape
     if out is None:
-        out = torch.empty((N, 3 * K // 32), dtype=torch.int32, device=codes.device)
+        out = _empty((N, 3 * K // 32), torch.int32, codes.device, stream)
     _need(out, "out", _U32, (N, 3 * K // 32))
     _check(load_library().int3_pack(_ptr(codes), _ptr(out), N, K, _stream(stream, codes.get_device())),
            "int3_pack")
@@ -228,7 +246,7 @@ def int3_dequant(wq3, scale, zero, g: int, out_dtype=torch.bfloat16, out=None, s
     _need(scale, "scale", _BF16, (N, K // g))
     _need(zero, "zero", _U8, (N, K // g))
     if out is None:
-        out = torch.empty((N, K), dtype=out_dtype, device=wq3.device)
+        out = _empty((N, K), out_dtype, wq3.device, stream)
     _need(out, "out", (torch.bfloat16, torch.float32), (N, K))
     kind = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
     _check(load_library().int3_dequant(_ptr(wq3), _ptr(scale), _ptr(zero), _ptr(out), kind,
@@ -320,8 +338,7 @@ def w4a16_gemv(x, wq, scale, zero, g: int, out=None, out_dtype=torch.bfloat16,
         M = x.shape[0]
         NO = N // 2 if swiglu_output else N
         if out is None:
-            out = torch.empty((M, NO), dtype=torch.bfloat16 if swiglu_output else out_dtype,
-                              device=x.device)
+            out = _empty((M, NO), torch.bfloat16 if swiglu_output else out_dtype, x.device, stream)
         _need(out, "out", (torch.bfloat16, torch.float32), (M, NO))
         device = x.get_device()
     if x.dim() != 2 or x.shape[1] != K:
@@ -375,7 +392,7 @@ def w4a16_moe_gemv(x, expert_ids, wq, scale, zero, g: int, route_w=None, x_per_s
         shape = (M, N)
         need = w4a16_moe_workspace_bytes(M, topk, N, True) if kernel_id != 4 else 0
         if workspace is None and need > 0:
-            workspace = torch.empty(need // 4, dtype=torch.float32, device=x.device)
+            workspace = _empty(need // 4, torch.float32, x.device, stream, kept=False)
         if workspace is None:
             ws_ptr, ws_bytes = None, 0
         else:
@@ -385,7 +402,7 @@ def w4a16_moe_gemv(x, expert_ids, wq, scale, zero, g: int, route_w=None, x_per_s
         shape = (M, topk, N)
         ws_ptr, ws_bytes, rw = None, 0, None
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+        out = _empty(shape, torch.bfloat16, x.device, stream)
     _need(out, "out", _BF16, shape)
     if kernel_id == 0:
         _check(lib.w4a16_moe_gemv(_ptr(x), int(bool(x_per_slot)), _ptr(expert_ids), rw, _ptr(wq),
@@ -423,7 +440,7 @@ def w4a16_swiglu(gate, up, out=None, stream=None) -> torch.Tensor:
         raise ValueError("gate and up must have the same shape and row stride")
     rows, N = gate.shape
     if out is None:
-        out = torch.empty((rows, N), dtype=torch.bfloat16, device=gate.device)
+        out = _empty((rows, N), torch.bfloat16, gate.device, stream)
     if out.dim() != 2 or tuple(out.shape) != (rows, N) or out.stride(1) != 1:
         raise ValueError("out must be [rows, N] with unit column stride")
     _check(load_library().w4a16_swiglu(_ptr(gate), _ptr(up), gate.stride(0), _ptr(out),
@@ -465,10 +482,10 @@ def moe_ffn(x, expert_ids, route_w, gate, up, down, g: int, stream=None,
         (gw, gs, gz), (uw, us, uz), (dw, ds, dz) = gate, up, down
         E, F, H8 = gw.shape
         H = H8 * 8
-        y = torch.empty((M, H), dtype=torch.bfloat16, device=x.device)
+        y = _empty((M, H), torch.bfloat16, x.device, stream)
         lib = load_library()
         nbytes = int(lib.w4a16_moe_ffn_workspace_bytes(M, topk, H, F))
-        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
+        ws = _empty(max(nbytes, 16), torch.uint8, x.device, stream, kept=False)
         _check(lib.w4a16_moe_ffn(_ptr(x), _ptr(expert_ids), _ptr(route_w), _ptr(gw), _ptr(gs),
                                  _ptr(gz), _ptr(uw), _ptr(us), _ptr(uz), _ptr(dw), _ptr(ds),
                                  _ptr(dz), _ptr(y), M, topk, E, H, F, g, _ptr(ws), nbytes,
@@ -493,10 +510,10 @@ def w3a16_moe_ffn(x, expert_ids, route_w, gate, up, down, g: int, stream=None) -
     (gw, gs, gz), (uw, us, uz), (dw, ds, dz) = gate, up, down
     E, F, H3 = gw.shape
     H = H3 // 3 * 32
-    y = torch.empty((M, H), dtype=torch.bfloat16, device=x.device)
+    y = _empty((M, H), torch.bfloat16, x.device, stream)
     lib = load_library()
     nbytes = int(lib.w3a16_moe_ffn_workspace_bytes(M, topk, H, F))
-    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
+    ws = _empty(max(nbytes, 16), torch.uint8, x.device, stream, kept=False)
     _check(lib.w3a16_moe_ffn(_ptr(x), _ptr(expert_ids), _ptr(route_w), _ptr(gw), _ptr(gs),
                              _ptr(gz), _ptr(uw), _ptr(us), _ptr(uz), _ptr(dw), _ptr(ds),
                              _ptr(dz), _ptr(y), M, topk, E, H, F, g, _ptr(ws), nbytes,
@@ -526,7 +543,7 @@ def w3a16_moe_gemv(x, expert_ids, wq3, scale, zero, g: int, route_w=None, x_per_
     else:
         shape = (M, topk, N)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+        out = _empty(shape, torch.bfloat16, x.device, stream)
     _need(out, "out", _BF16, shape)
     _check(load_library().w3a16_moe_gemv(_ptr(x), int(bool(x_per_slot)), _ptr(expert_ids),
                                          None if route_w is None else _ptr(route_w), _ptr(wq3),
@@ -596,8 +613,11 @@ PagedMap = collections.namedtuple("PagedMap", "slots positions row_start kv_len 
 
 def paged_map_buffers(requests: int, tokens: int, device) -> PagedMap:
     """Output buffers of w4a16_paged_map, to be kept from step to step."""
-    new = lambda n: torch.empty(n, dtype=torch.int32, device=device)
-    return PagedMap(new(tokens), new(tokens), new(requests + 1), new(requests), new(1))
+    return _map_buffers(requests, tokens, device, None)
+
+
+def _map_buffers(requests: int, tokens: int, device, stream) -> PagedMap:
+    return PagedMap(*(_empty(n, torch.int32, device, stream) for n in (tokens, tokens, requests + 1, requests, 1)))
 
 
 # The paged calls run once per layer and step, next to kernels of a few
@@ -678,7 +698,7 @@ def w4a16_paged_map(ctx_len, new_len, block_table, free_blocks, free_head, page:
     free, head = _vector(free_blocks, "free_blocks", F), _vector(free_head, "free_head", 1)
     table, stride, columns = _table(block_table, B)
     if out is None:
-        out = paged_map_buffers(B, tokens, ctx_len.device)
+        out = _map_buffers(B, tokens, ctx_len.device, stream)
     else:
         for t, name, n in zip(out, PagedMap._fields, (tokens, tokens, B + 1, B, 1)):
             _need(t, name, _I32, (n,))
@@ -748,7 +768,7 @@ def w4a16_rope_append(q, k, v, positions, inv_freq, slots, cache: PagedCache, se
         qa = _rows(q, "q", shape)
         device = q.get_device()
         if q_out is None:
-            q_out = torch.empty(shape, dtype=_bf16, device=q.device)
+            q_out = _empty(shape, _bf16, q.device, stream)
         qo = _rows(q_out, "q_out", shape)
     else:
         T, heads, dim = k.shape[0], 0, k.shape[2]
@@ -788,8 +808,12 @@ def w4a16_rope_append(q, k, v, positions, inv_freq, slots, cache: PagedCache, se
 def paged_attention_workspace(cache: PagedCache, q_heads: int) -> torch.Tensor:
     """Workspace of w4a16_paged_attention for this cache and number of query
     heads (its contents need no initialisation)."""
+    return _attention_workspace(cache, q_heads, None)
+
+
+def _attention_workspace(cache: PagedCache, q_heads: int, stream) -> torch.Tensor:
     n = int(load_library().w4a16_paged_attention_workspace_bytes(q_heads, cache.heads, cache.dim))
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=cache.k.device)
+    return _empty(max(n, 16), torch.uint8, cache.k.device, stream, kept=False)
 
 
 def w4a16_paged_attention(q, cache: PagedCache, block_table, kv_len, scale: float = None, window: int = 0,
@@ -818,14 +842,14 @@ def w4a16_paged_attention(q, cache: PagedCache, block_table, kv_len, scale: floa
     table, stride, columns = _table(block_table, B)
     lengths = _vector(kv_len, "kv_len", B)
     if out is None:
-        out = torch.empty(shape, dtype=_bf16, device=q.device)
+        out = _empty(shape, _bf16, q.device, stream)
     oa = _rows(out, "out", shape)
     if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+        lse = _empty((B, H), torch.float32, q.device, stream)
     elif not (lse.dtype is torch.float32 and lse.is_cuda and lse.shape == (B, H) and lse.is_contiguous()):
         _need(lse, "lse", _F32, (B, H))
     if workspace is None:
-        workspace = paged_attention_workspace(cache, H)
+        workspace = _attention_workspace(cache, H, stream)
     elif not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor")
     rc = _lib.w4a16_paged_attention(*qa, cache._ref, table, stride, columns, lengths, B, H,
