@@ -159,3 +159,32 @@ def test_reference_attention_against_softmax():
     s = 0.25 * q[0] @ kk.t()
     assert torch.allclose(out[0], torch.softmax(s, 1) @ vv)
     assert torch.allclose(lse[0], torch.logsumexp(s, 1))
+
+
+def test_marshalling_module_is_of_these_sources_and_this_machine(w, monkeypatch, tmp_path):
+    # a file made for another Python, machine, torch or interface has another name: it is neither taken for
+    # fresh nor loaded, whatever its time stamp, also where no new one can be built
+    import shutil
+    import sysconfig
+
+    from w4a16_int4_weight_gemv_gb300 import build_ext
+    here = build_ext.fastcall_path()
+    assert torch.__version__ in here and here.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    include = tmp_path / "include"
+    shutil.copytree(build_ext.INCLUDE, include)
+    build = tmp_path / "_build"
+    build.mkdir()
+    monkeypatch.setattr(build_ext, "INCLUDE", str(include))
+    monkeypatch.setattr(build_ext, "BUILD_DIR", str(build))
+    monkeypatch.setenv("CXX", "/bin/false")
+    same = build_ext.fastcall_path()
+    assert same.rsplit("/", 1)[1] == here.rsplit("/", 1)[1]
+    open(same, "w").close()
+    assert build_ext.build_fastcall() == same  # of these sources: as it is
+    with open(include / "w4a16.h", "a") as f:
+        f.write("/* changed */\n")
+    changed = build_ext.fastcall_path()
+    assert changed != same
+    assert build_ext.build_fastcall() is None and w._load_fast() is None
+    monkeypatch.setattr(build_ext.sysconfig, "get_config_var", lambda name: ".cpython-399-other-linux-gnu.so")
+    assert build_ext.fastcall_path() not in (same, changed)

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import hashlib
 import importlib.util
 import os
 import re
@@ -64,14 +65,26 @@ def _torch_dir():
     return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
 
 
+def _fastcall_flags():
+    return ["-O1", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden"]
+
+
 def fastcall_path():
-    """The extension module's file, named after the torch it is built against (None without torch)."""
+    """The extension module's file (None without torch).  Its name holds what it
+    has to agree with: torch, Python and machine, and the sources it is made of
+    (their digest); so one made for something else, or before the C interface
+    changed, is not found, and is never loaded."""
     torch_dir = _torch_dir()
     if torch_dir is None:
         return None
     with open(os.path.join(torch_dir, "version.py")) as f:
         found = re.search(r"^__version__ = ['\"]([^'\"]+)", f.read(), re.M)
-    return os.path.join(BUILD_DIR, "_fastcall.%s.so" % (found.group(1) if found else "unknown"))
+    digest = hashlib.sha256(" ".join(_fastcall_flags()).encode())
+    for source in (FASTCALL_SRC, os.path.join(INCLUDE, "w4a16.h")):
+        with open(source, "rb") as f:
+            digest.update(f.read())
+    return os.path.join(BUILD_DIR, "_fastcall.%s.%s%s" % (found.group(1) if found else "unknown", digest.hexdigest()[:12],
+                                                          sysconfig.get_config_var("EXT_SUFFIX")))
 
 
 def build_fastcall(force: bool = False, verbose: bool = False):
@@ -79,12 +92,11 @@ def build_fastcall(force: bool = False, verbose: bool = False):
     path = fastcall_path()
     if path is None:
         return None
-    deps = [FASTCALL_SRC, os.path.join(INCLUDE, "w4a16.h"), os.path.abspath(__file__)]
-    if not force and os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path) for d in deps):
+    if not force and os.path.exists(path):
         return path
     os.makedirs(BUILD_DIR, exist_ok=True)
     torch_dir, tmp = _torch_dir(), path + ".%d.tmp" % os.getpid()
-    cmd = [os.environ.get("CXX", "g++"), "-O1", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+    cmd = [os.environ.get("CXX", "g++"), *_fastcall_flags(),
            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"), "-I", INCLUDE, FASTCALL_SRC,
            "-o", tmp, "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
     try:
