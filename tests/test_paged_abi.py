@@ -188,3 +188,48 @@ def test_marshalling_module_is_of_these_sources_and_this_machine(w, monkeypatch,
     assert build_ext.build_fastcall() is None and w._load_fast() is None
     monkeypatch.setattr(build_ext.sysconfig, "get_config_var", lambda name: ".cpython-399-other-linux-gnu.so")
     assert build_ext.fastcall_path() not in (same, changed)
+
+
+@pytest.mark.parametrize("fast", [True, False], ids=["marshalling module", "binding"])
+@pytest.mark.filterwarnings("ignore:Accessing the data pointer")
+def test_tensors_of_two_devices_are_refused(w, monkeypatch, fast):
+    # tensors without memory stand in for those of two GPUs
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    if not fast:
+        monkeypatch.setattr(w, "_fast", None)
+    with FakeTensorMode(allow_non_fake_inputs=True):
+        def make(dtype, *shape, gpu=0):
+            return torch.empty(shape, dtype=dtype, device="cuda:%d" % gpu)
+
+        def other(t):
+            return make(t.dtype, *t.shape, gpu=1)
+
+        i32, f32, bf16, e4m3 = torch.int32, torch.float32, torch.bfloat16, torch.float8_e4m3fn
+
+        def refused(call, args, names):
+            for name in names:
+                with pytest.raises(ValueError, match="device"):
+                    call(**{**args, name: other(args[name])})
+
+        kv = dict(k=make(e4m3, 8, 16, 2, 64), v=make(e4m3, 8, 16, 2, 64), k_scale=make(f32, 2), v_scale=make(f32, 2))
+        refused(w.PagedCache, kv, ["v", "k_scale", "v_scale"])
+        cache = w.PagedCache(make(bf16, 8, 16, 2, 64), make(bf16, 8, 16, 2, 64))
+
+        out = w.PagedMap(make(i32, 5), make(i32, 5), make(i32, 4), make(i32, 3), make(i32, 1))
+        args = dict(ctx_len=make(i32, 3), new_len=make(i32, 3), block_table=make(i32, 3, 4), free_blocks=make(i32, 6), free_head=make(i32, 1), page=16,
+                    num_blocks=8, tokens=5, out=out)
+        refused(w.w4a16_paged_map, args, ["new_len", "block_table", "free_blocks", "free_head"])
+        for name in out._fields:
+            with pytest.raises(ValueError, match="device"):
+                w.w4a16_paged_map(**{**args, "out": out._replace(**{name: other(getattr(out, name))})})
+
+        args = dict(q=make(bf16, 5, 4, 64), k=make(bf16, 5, 2, 64), v=make(bf16, 5, 2, 64), positions=make(i32, 5), inv_freq=make(f32, 32),
+                    slots=make(i32, 5), cache=cache, q_out=make(bf16, 5, 4, 64))
+        refused(w.w4a16_rope_append, args, ["q", "k", "v", "positions", "inv_freq", "slots", "q_out"])
+        refused(w.w4a16_rope_append, {**args, "q": None, "q_out": None, "positions": make(i32, 1, 5), "sections": [32]},
+                ["k", "v", "positions", "inv_freq", "slots"])
+        refused(w.w4a16_rope_append, {**args, "k": None, "v": None, "slots": None, "cache": None}, ["positions", "inv_freq", "q_out"])
+
+        args = dict(q=make(bf16, 3, 4, 64), cache=cache, block_table=make(i32, 3, 4), kv_len=make(i32, 3), out=make(bf16, 3, 4, 64),
+                    lse=make(f32, 3, 4), workspace=make(torch.uint8, 1 << 22))
+        refused(w.w4a16_paged_attention, args, ["q", "block_table", "kv_len", "out", "lse", "workspace"])

@@ -555,6 +555,13 @@ def w3a16_moe_gemv(x, expert_ids, wq3, scale, zero, g: int, route_w=None, x_per_
 # --------------------------------------------------------------------------
 # paged key/value cache: block map, rotary + append, one-token attention
 # --------------------------------------------------------------------------
+def _on_device(device: int, **tensors):
+    """A call's tensors are on one device: that of its first one, and of the cache."""
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != device:
+            raise ValueError("%s is on device %s, expected cuda:%d" % (name, t.device, device))
+
+
 class _KvCache(ctypes.Structure):
     """w4a16_kv_cache of include/w4a16.h."""
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
@@ -601,6 +608,9 @@ class PagedCache:
             _need(v_scale, "v_scale", _F32, (self.heads,))
         elif k_scale is not None or v_scale is not None:
             raise ValueError("a bfloat16 cache has no scales")
+        self.device = k.get_device()
+        if e4m3:
+            _on_device(self.device, k_scale=k_scale, v_scale=v_scale)
         self._struct = _KvCache(_ptr(k), _ptr(v), _ptr(k_scale) if e4m3 else None,
                                 _ptr(v_scale) if e4m3 else None, CACHE_E4M3 if e4m3 else CACHE_BF16,
                                 self.heads, self.dim, self.page, self.blocks,
@@ -703,9 +713,12 @@ def w4a16_paged_map(ctx_len, new_len, block_table, free_blocks, free_head, page:
         for t, name, n in zip(out, PagedMap._fields, (tokens, tokens, B + 1, B, 1)):
             _need(t, name, _I32, (n,))
     slots, positions, row_start, kv_len, head_out = out
+    device = ctx_len.get_device()
+    _on_device(device, new_len=new_len, block_table=block_table, free_blocks=free_blocks, free_head=free_head)
+    _on_device(device, **out._asdict())
     rc = _lib.w4a16_paged_map(ctx, new, B, table, stride, columns, free, F, head, page, num_blocks,
                               slots.data_ptr(), positions.data_ptr(), tokens, row_start.data_ptr(),
-                              kv_len.data_ptr(), head_out.data_ptr(), _stream(stream, ctx_len.get_device()))
+                              kv_len.data_ptr(), head_out.data_ptr(), _stream(stream, device))
     if rc:
         raise W4A16Error(rc, "w4a16_paged_map")
     return out
@@ -756,7 +769,7 @@ def w4a16_rope_append(q, k, v, positions, inv_freq, slots, cache: PagedCache, se
     if _fast is not None and (q is None or q_out is not None) and (cache is not None or (k is None and v is None and slots is None)):
         sec, sec_at = (None, 0) if sections is None else _section_array(sections)
         rc = _fast.rope_append(q, k, v, positions, inv_freq, slots, None if cache is None else cache._ref,
-                               0 if cache is None else cache.heads, sec_at, 1 if sections is None else len(sections), flags,
+                               0 if cache is None else cache.heads, 0 if cache is None else cache.device, sec_at, 1 if sections is None else len(sections), flags,
                                q_out, None if stream is None else stream.cuda_stream)
         if rc == 0:
             return q_out
@@ -796,6 +809,8 @@ def w4a16_rope_append(q, k, v, positions, inv_freq, slots, cache: PagedCache, se
         if len(sections) != axes:
             raise ValueError("%d sections for %d axes" % (len(sections), axes))
         sec, _ = _section_array(sections)
+    _on_device(device if cache is None else cache.device, q=q, q_out=q_out, k=k, v=v, positions=positions, inv_freq=inv_freq,
+               slots=slots)
     if T == 0:
         return q_out
     rc = _lib.w4a16_rope_append(*qa, *qo, heads, *ka, *va, positions_at, axis_stride, inv_freq.data_ptr(), sec, axes,
@@ -830,7 +845,7 @@ def w4a16_paged_attention(q, cache: PagedCache, block_table, kv_len, scale: floa
     if scale is None:
         scale = cache.dim ** -0.5
     if _fast is not None and workspace is not None:
-        rc = _fast.paged_attention(q, cache._ref, cache.dim, block_table, kv_len, scale, window, out, lse, workspace,
+        rc = _fast.paged_attention(q, cache._ref, cache.dim, cache.device, block_table, kv_len, scale, window, out, lse, workspace,
                                    None if stream is None else stream.cuda_stream)
         if rc == 0:
             return out, lse
@@ -852,6 +867,7 @@ def w4a16_paged_attention(q, cache: PagedCache, block_table, kv_len, scale: floa
         workspace = _attention_workspace(cache, H, stream)
     elif not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor")
+    _on_device(cache.device, q=q, block_table=block_table, kv_len=kv_len, out=out, lse=lse, workspace=workspace)
     rc = _lib.w4a16_paged_attention(*qa, cache._ref, table, stride, columns, lengths, B, H,
                                     scale, window, *oa, lse.data_ptr(),
                                     workspace.data_ptr(), workspace.nbytes, _stream(stream, q.get_device()))

@@ -24,10 +24,13 @@ PyObject* g_current_stream;  // device index -> raw stream
 
 const at::Tensor* tensor_of(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
 
-// int32 vector of n entries on the GPU
-bool vector_of(PyObject* o, int64_t n, int32_t** p) {
+// on the GPU `device`
+bool on(const at::Tensor* t, int64_t device) { return t->is_cuda() && t->get_device() == device; }
+
+// int32 vector of n entries
+bool vector_of(PyObject* o, int64_t n, int64_t device, int32_t** p) {
     const at::Tensor* t = tensor_of(o);
-    if (!t || t->scalar_type() != at::kInt || !t->is_cuda() || t->dim() != 1 || t->size(0) != n ||
+    if (!t || t->scalar_type() != at::kInt || !on(t, device) || t->dim() != 1 || t->size(0) != n ||
         (n > 1 && t->stride(0) != 1))
         return false;
     *p = static_cast<int32_t*>(t->data_ptr());
@@ -38,9 +41,9 @@ struct Table {
     int32_t* p;
     int64_t rows, columns, stride;
 };
-bool table_of(PyObject* o, Table* x) {
+bool table_of(PyObject* o, int64_t device, Table* x) {
     const at::Tensor* t = tensor_of(o);
-    if (!t || t->scalar_type() != at::kInt || !t->is_cuda() || t->dim() != 2) return false;
+    if (!t || t->scalar_type() != at::kInt || !on(t, device) || t->dim() != 2) return false;
     x->rows = t->size(0), x->columns = t->size(1), x->stride = t->stride(0);
     if (x->columns > 1 && t->stride(1) != 1) return false;
     if (x->rows <= 1 && x->stride < x->columns) x->stride = x->columns;
@@ -52,7 +55,7 @@ bool table_of(PyObject* o, Table* x) {
 struct Rows {
     uint16_t* p = nullptr;
     int64_t n = 0, heads = 0, dim = 0, row = 0, head = 0;
-    int device = -1;
+    int64_t device = -1;
 };
 bool rows_of(PyObject* o, Rows* x) {
     const at::Tensor* t = tensor_of(o);
@@ -65,12 +68,12 @@ bool rows_of(PyObject* o, Rows* x) {
 }
 
 // the raw stream given, or the current one of `device`
-bool stream_of(PyObject* o, int device, void** s) {
+bool stream_of(PyObject* o, int64_t device, void** s) {
     if (o != Py_None) {
         *s = PyLong_AsVoidPtr(o);
         return !PyErr_Occurred();
     }
-    PyObject* index = PyLong_FromLong(device);
+    PyObject* index = PyLong_FromLongLong(device);
     PyObject* raw = index ? PyObject_CallOneArg(g_current_stream, index) : nullptr;
     Py_XDECREF(index);
     if (!raw) return false;
@@ -105,7 +108,7 @@ PyObject* paged_map(PyObject*, PyObject* const* a, Py_ssize_t n) {
     try {
         const at::Tensor* first = tensor_of(a[0]);
         if (!first || first->dim() != 1 || !PyTuple_Check(a[8]) || PyTuple_GET_SIZE(a[8]) != 5) return other_form();
-        const int64_t B = first->size(0);
+        const int64_t B = first->size(0), dev = first->get_device();
         const at::Tensor* free_t = tensor_of(a[3]);
         if (!free_t || free_t->dim() != 1) return other_form();
         const int64_t F = free_t->size(0);
@@ -113,13 +116,14 @@ PyObject* paged_map(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Table t;
         int64_t page, blocks, tokens;
         void* stream;
-        if (!integer(a[5], &page) || !integer(a[6], &blocks) || !integer(a[7], &tokens) || !vector_of(a[0], B, &ctx) ||
-            !vector_of(a[1], B, &fresh) || !table_of(a[2], &t) || t.rows != B || !vector_of(a[3], F, &free_blocks) ||
-            !vector_of(a[4], 1, &head) || !vector_of(PyTuple_GET_ITEM(a[8], 0), tokens, &slots) ||
-            !vector_of(PyTuple_GET_ITEM(a[8], 1), tokens, &positions) ||
-            !vector_of(PyTuple_GET_ITEM(a[8], 2), B + 1, &row_start) || !vector_of(PyTuple_GET_ITEM(a[8], 3), B, &kv_len) ||
-            !vector_of(PyTuple_GET_ITEM(a[8], 4), 1, &head_out) || B > INT32_MAX || t.columns > INT32_MAX ||
-            page > INT32_MAX || page < INT32_MIN || !stream_of(a[9], first->get_device(), &stream))
+        if (!integer(a[5], &page) || !integer(a[6], &blocks) || !integer(a[7], &tokens) || !vector_of(a[0], B, dev, &ctx) ||
+            !vector_of(a[1], B, dev, &fresh) || !table_of(a[2], dev, &t) || t.rows != B || !vector_of(a[3], F, dev, &free_blocks) ||
+            !vector_of(a[4], 1, dev, &head) || !vector_of(PyTuple_GET_ITEM(a[8], 0), tokens, dev, &slots) ||
+            !vector_of(PyTuple_GET_ITEM(a[8], 1), tokens, dev, &positions) ||
+            !vector_of(PyTuple_GET_ITEM(a[8], 2), B + 1, dev, &row_start) ||
+            !vector_of(PyTuple_GET_ITEM(a[8], 3), B, dev, &kv_len) ||
+            !vector_of(PyTuple_GET_ITEM(a[8], 4), 1, dev, &head_out) || B > INT32_MAX || t.columns > INT32_MAX ||
+            page > INT32_MAX || page < INT32_MIN || !stream_of(a[9], dev, &stream))
             return other_form();
         return status_of([&] {
             return g_map(ctx, fresh, static_cast<int>(B), t.p, t.stride, static_cast<int>(t.columns), free_blocks, F, head,
@@ -130,39 +134,41 @@ PyObject* paged_map(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
 }
 
-// (q, k, v, positions, inv_freq, slots, cache address, cache heads, sections address, axes, flags, q_out, stream)
+// (q, k, v, positions, inv_freq, slots, cache address, cache heads, cache device, sections address, axes, flags, q_out, stream)
 PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != 13 || !g_append) return other_form();
+    if (n != 14 || !g_append) return other_form();
     try {
         Rows q, out, k, v;
         int32_t *slots = nullptr, *positions;
-        int64_t cache = 0, heads = 0, sections, axes, flags;
+        int64_t cache = 0, heads = 0, cache_device, sections, axes, flags;
         if (a[0] != Py_None) {
-            if (!rows_of(a[0], &q) || !rows_of(a[11], &out) || out.n != q.n || out.heads != q.heads || out.dim != q.dim)
+            if (!rows_of(a[0], &q) || !rows_of(a[12], &out) || out.n != q.n || out.heads != q.heads || out.dim != q.dim ||
+                out.device != q.device)
                 return other_form();
         }
         if (a[6] != Py_None) {
-            if (!integer(a[6], &cache) || !integer(a[7], &heads) || !rows_of(a[1], &k) || !rows_of(a[2], &v) || k.heads != heads ||
-                v.heads != heads || v.n != k.n || v.dim != k.dim || (q.p && (q.n != k.n || q.dim != k.dim)) ||
-                !vector_of(a[5], k.n, &slots))
+            if (!integer(a[6], &cache) || !integer(a[7], &heads) || !integer(a[8], &cache_device) || !rows_of(a[1], &k) || !rows_of(a[2], &v) ||
+                k.heads != heads || v.heads != heads || v.n != k.n || v.dim != k.dim || k.device != cache_device ||
+                v.device != cache_device || (q.p && (q.n != k.n || q.dim != k.dim || q.device != cache_device)) ||
+                !vector_of(a[5], k.n, cache_device, &slots))
                 return other_form();
         }
         const Rows& any = q.p ? q : k;
         const at::Tensor* pos = tensor_of(a[3]);
         const at::Tensor* freq = tensor_of(a[4]);
         void* stream;
-        if (!any.p || !pos || !freq || !integer(a[8], &sections) || !integer(a[9], &axes) || !integer(a[10], &flags) ||
-            freq->scalar_type() != at::kFloat || !freq->is_cuda() || freq->dim() != 1 || !freq->is_contiguous())
+        if (!any.p || !pos || !freq || !integer(a[9], &sections) || !integer(a[10], &axes) || !integer(a[11], &flags) ||
+            freq->scalar_type() != at::kFloat || !on(freq, any.device) || freq->dim() != 1 || !freq->is_contiguous())
             return other_form();
         if (pos->dim() == 1) {
-            if (axes != 1 || !vector_of(a[3], any.n, &positions)) return other_form();
+            if (axes != 1 || !vector_of(a[3], any.n, any.device, &positions)) return other_form();
         } else {
-            if (pos->dim() != 2 || pos->scalar_type() != at::kInt || !pos->is_cuda() || !pos->is_contiguous() || pos->size(0) != axes ||
+            if (pos->dim() != 2 || pos->scalar_type() != at::kInt || !on(pos, any.device) || !pos->is_contiguous() || pos->size(0) != axes ||
                 pos->size(1) != any.n)
                 return other_form();
             positions = static_cast<int32_t*>(pos->data_ptr());
         }
-        if (any.n == 0 || q.heads > INT32_MAX || freq->size(0) > INT32_MAX / 2 || !stream_of(a[12], any.device, &stream))
+        if (any.n == 0 || q.heads > INT32_MAX || freq->size(0) > INT32_MAX / 2 || !stream_of(a[13], any.device, &stream))
             return other_form();
         const int rotary = 2 * static_cast<int>(freq->size(0));
         const float* f = static_cast<const float*>(freq->data_ptr());
@@ -177,26 +183,27 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
 }
 
-// (q, cache address, cache dim, block_table, kv_len, scale, window, out, lse, workspace, stream)
+// (q, cache address, cache dim, cache device, block_table, kv_len, scale, window, out, lse, workspace, stream)
 PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != 11 || !g_attention) return other_form();
+    if (n != 12 || !g_attention) return other_form();
     try {
         Rows q, out;
         Table t;
         int32_t* lengths;
-        int64_t cache, dim, window;
-        if (!rows_of(a[0], &q) || !integer(a[1], &cache) || !integer(a[2], &dim) || q.dim != dim || !table_of(a[3], &t) ||
-            t.rows != q.n || !vector_of(a[4], q.n, &lengths) || !integer(a[6], &window) || !rows_of(a[7], &out) || out.n != q.n ||
-            out.heads != q.heads || out.dim != dim)
+        int64_t cache, dim, device, window;
+        if (!rows_of(a[0], &q) || !integer(a[1], &cache) || !integer(a[2], &dim) || q.dim != dim || !integer(a[3], &device) ||
+            q.device != device || !table_of(a[4], device, &t) || t.rows != q.n || !vector_of(a[5], q.n, device, &lengths) ||
+            !integer(a[7], &window) || !rows_of(a[8], &out) || out.n != q.n || out.heads != q.heads || out.dim != dim ||
+            out.device != device)
             return other_form();
-        const at::Tensor *lse = tensor_of(a[8]), *ws = tensor_of(a[9]);
-        if (!lse || !ws || lse->scalar_type() != at::kFloat || !lse->is_cuda() || lse->dim() != 2 || lse->size(0) != q.n ||
-            lse->size(1) != q.heads || !lse->is_contiguous() || !ws->is_cuda() || !ws->is_contiguous())
+        const at::Tensor *lse = tensor_of(a[9]), *ws = tensor_of(a[10]);
+        if (!lse || !ws || lse->scalar_type() != at::kFloat || !on(lse, device) || lse->dim() != 2 || lse->size(0) != q.n ||
+            lse->size(1) != q.heads || !lse->is_contiguous() || !on(ws, device) || !ws->is_contiguous())
             return other_form();
-        const double scale = PyFloat_AsDouble(a[5]);
+        const double scale = PyFloat_AsDouble(a[6]);
         void* stream;
         if (PyErr_Occurred() || q.n > INT32_MAX || q.heads > INT32_MAX || t.columns > INT32_MAX || window > INT32_MAX ||
-            window < INT32_MIN || !stream_of(a[10], q.device, &stream))
+            window < INT32_MIN || !stream_of(a[11], device, &stream))
             return other_form();
         float* l = static_cast<float*>(lse->data_ptr());
         void* w = ws->data_ptr();
