@@ -43,10 +43,8 @@ struct JoinPlan {
     // of, 1: the row it ends inside of
     float* part;
     int by_row;
-    int rows;    // of a request: key/value heads times chunks of the query heads sharing one
-    int heads;   // query heads of a chunk: 8 or 16
-    int padded;  // padded_dim
-    int warps;   // of the first launch
+    int rows;   // of a request: key/value heads times chunks of the query heads sharing one
+    int warps;  // of the first launch
 };
 
 // paged_attention_bf16.cu, paged_attention_e4m3.cu: all launches of a call; `join` has joins and part
