@@ -89,3 +89,47 @@ def test_a_captured_step_repeats_the_calls(ex):
     assert torch.equal(req.table, req2.table)
     assert torch.equal(req.cache.k, req2.cache.k) and torch.equal(req.cache.v, req2.cache.v)
     assert ex.w.w4a16_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_step_hands_the_right_things_on(ex, e4m3, monkeypatch):
+    """What the step itself gives its attention and takes from it: the call's own
+    queries, lengths and table, and the outputs that the rest of the step goes on with."""
+    layer, req = small(ex, e4m3)
+    w = ex.w
+    contexts = [5, 0, 130, 31]
+    calls = []
+    plain = w.w4a16_paged_attention
+
+    def recorded(q, cache, table, kv_len, **kw):
+        out, lse = plain(q, cache, table, kv_len, **kw)
+        calls.append((q.clone(), cache, table.clone(), kv_len.clone(), out.clone(), lse.clone()))
+        return out, lse
+
+    monkeypatch.setattr(w, "w4a16_paged_attention", recorded)
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    u = 2.0 ** -8
+    for s in range(3):
+        x = torch.randn(4, 512, generator=gen, device="cuda").bfloat16()
+        y = ex.step(layer, req, x)
+        q, cache, table, kv_len, out, lse = calls[s]
+        lens = [c + s + 1 for c in contexts]
+        assert len(calls) == s + 1 and cache is req.cache and kv_len.tolist() == lens and torch.equal(table, req.table)
+        # the queries: the projection's, turned in 64 bits, rounded once
+        rows = w.w4a16_gemv(x, *layer.qkv, ex.GROUP).double().cpu()[:, :512].view(4, 8, 64)
+        pos = torch.tensor([[n - 1 for n in lens]], dtype=torch.int32)
+        turned = ref.rope(rows, pos, layer.inv_freq.cpu(), [32], False)
+        size = rows.abs().amax(-1, keepdim=True)
+        assert ((q.double().cpu() - turned).abs() <= u * turned.abs() + 2.0 ** -18 * size).all()
+        # the outputs, over what is in the cache now
+        factor = 1 / 32 if e4m3 else 1
+        cached = [c.float().double().cpu() * factor for c in (req.cache.k, req.cache.v)]
+        want, want_lse, spread, reach = ref.attention(q.double().cpu(), *cached, table.tolist(), lens, layer.dim ** -0.5, 0)
+        score = (64 + 16) * 2.0 ** -24 * reach
+        assert ((out.double().cpu() - want).abs() <= u * want.abs() + (u + 2 * score[..., None]) * spread + 1e-30).all()
+        assert ((lse.double().cpu() - want_lse).abs() <= score + 2.0 ** -20 * (1 + want_lse.abs())).all()
+        # and the rest of the step from them: the same calls on the same rows give the same bits
+        h = x + w.w4a16_gemv(out.view(4, -1), *layer.out, ex.GROUP, weights_static=True)
+        top, ids = torch.topk(h.float() @ layer.router, layer.topk)
+        assert torch.equal(y, h + w.moe_ffn(h, ids.int(), torch.softmax(top, 1), layer.gate, layer.up, layer.down, ex.GROUP))
+    assert w.w4a16_device_error(clear=True) == 0
