@@ -3,6 +3,7 @@ launched (no GPU needed), and the plain forms the GPU tests compare with agree
 with hand-worked cases."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
@@ -233,3 +234,15 @@ def test_tensors_of_two_devices_are_refused(w, monkeypatch, fast):
         args = dict(q=make(bf16, 3, 4, 64), cache=cache, block_table=make(i32, 3, 4), kv_len=make(i32, 3), out=make(bf16, 3, 4, 64),
                     lse=make(f32, 3, 4), workspace=make(torch.uint8, 1 << 22))
         refused(w.w4a16_paged_attention, args, ["q", "block_table", "kv_len", "out", "lse", "workspace"])
+
+
+def test_sections_go_by_their_values(w):
+    # one list of whole numbers that change in place, as numpy and torch have them
+    for make in (lambda v: torch.tensor(v), lambda v: np.array(v)):
+        lengths = [make(20), make(12)]
+        assert list(w._section_array(lengths)[0]) == [20, 12]
+        for x in lengths:
+            x[()] = 16
+        assert list(w._section_array(lengths)[0]) == [16, 16]
+    with pytest.raises(TypeError):
+        w._section_array([16.0, 16.0])

@@ -15,6 +15,7 @@ import collections
 import ctypes
 import enum
 import importlib.util
+import operator
 import os
 
 import torch
@@ -743,7 +744,7 @@ _section_arrays = {}  # C arrays and their addresses, by the sections' values
 
 
 def _section_array(sections):
-    key = tuple(sections)
+    key = tuple(map(operator.index, sections))  # whole numbers, not the objects that hold them
     found = _section_arrays.get(key)
     if found is None:
         array = (ctypes.c_int32 * len(key))(*key)
