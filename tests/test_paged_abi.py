@@ -240,9 +240,9 @@ def test_sections_go_by_their_values(w):
     # one list of whole numbers that change in place, as numpy and torch have them
     for make in (lambda v: torch.tensor(v), lambda v: np.array(v)):
         lengths = [make(20), make(12)]
-        assert list(w._section_array(lengths)[0]) == [20, 12]
+        assert list(w._section_array(lengths)) == [20, 12]
         for x in lengths:
             x[()] = 16
-        assert list(w._section_array(lengths)[0]) == [16, 16]
+        assert list(w._section_array(lengths)) == [16, 16]
     with pytest.raises(TypeError):
         w._section_array([16.0, 16.0])

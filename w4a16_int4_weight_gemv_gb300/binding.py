@@ -740,18 +740,9 @@ def _rows(t, name: str, shape):
     raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
 
 
-_section_arrays = {}  # C arrays and their addresses, by the sections' values
-
-
 def _section_array(sections):
-    key = tuple(map(operator.index, sections))  # whole numbers, not the objects that hold them
-    found = _section_arrays.get(key)
-    if found is None:
-        array = (ctypes.c_int32 * len(key))(*key)
-        if len(_section_arrays) >= 64:
-            return array, ctypes.addressof(array)
-        found = _section_arrays[key] = array, ctypes.addressof(array)
-    return found
+    """The sections as a C array."""
+    return (ctypes.c_int32 * len(sections))(*map(operator.index, sections))
 
 
 def w4a16_rope_append(q, k, v, positions, inv_freq, slots, cache: PagedCache, sections=None,
@@ -768,9 +759,8 @@ def w4a16_rope_append(q, k, v, positions, inv_freq, slots, cache: PagedCache, se
     rotates in place)."""
     flags = (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_INVERSE if inverse else 0)
     if _fast is not None and (q is None or q_out is not None) and (cache is not None or (k is None and v is None and slots is None)):
-        sec, sec_at = (None, 0) if sections is None else _section_array(sections)
         rc = _fast.rope_append(q, k, v, positions, inv_freq, slots, None if cache is None else cache._ref,
-                               0 if cache is None else cache.heads, 0 if cache is None else cache.device, sec_at, 1 if sections is None else len(sections), flags,
+                               0 if cache is None else cache.heads, 0 if cache is None else cache.device, sections, flags,
                                q_out, None if stream is None else stream.cuda_stream)
         if rc == 0:
             return q_out
@@ -809,7 +799,7 @@ def w4a16_rope_append(q, k, v, positions, inv_freq, slots, cache: PagedCache, se
     if sections is not None:
         if len(sections) != axes:
             raise ValueError("%d sections for %d axes" % (len(sections), axes))
-        sec, _ = _section_array(sections)
+        sec = _section_array(sections)
     _on_device(device if cache is None else cache.device, q=q, q_out=q_out, k=k, v=v, positions=positions, inv_freq=inv_freq,
                slots=slots)
     if T == 0:

@@ -88,6 +88,27 @@ bool integer(PyObject* o, int64_t* v) {
     return !PyErr_Occurred();
 }
 
+// a list or tuple of at most four whole numbers; None: one axis, no array
+struct Sections {
+    int32_t n[4];
+    const int32_t* p = nullptr;
+    int axes = 1;
+};
+bool sections_of(PyObject* o, Sections* x) {
+    if (o == Py_None) return true;
+    if (!PyList_CheckExact(o) && !PyTuple_CheckExact(o)) return false;
+    const Py_ssize_t size = PySequence_Fast_GET_SIZE(o);
+    if (size < 1 || size > 4) return false;
+    for (Py_ssize_t i = 0; i < size; ++i) {
+        int64_t v;
+        if (!integer(PySequence_Fast_GET_ITEM(o, i), &v) || v < INT32_MIN || v > INT32_MAX) return false;
+        x->n[i] = static_cast<int32_t>(v);
+    }
+    x->p = x->n;
+    x->axes = static_cast<int>(size);
+    return true;
+}
+
 PyObject* other_form() {  // not for here: no error is left behind
     PyErr_Clear();
     Py_RETURN_NONE;
@@ -134,15 +155,16 @@ PyObject* paged_map(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
 }
 
-// (q, k, v, positions, inv_freq, slots, cache address, cache heads, cache device, sections address, axes, flags, q_out, stream)
+// (q, k, v, positions, inv_freq, slots, cache address, cache heads, cache device, sections, flags, q_out, stream)
 PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != 14 || !g_append) return other_form();
+    if (n != 13 || !g_append) return other_form();
     try {
         Rows q, out, k, v;
         int32_t *slots = nullptr, *positions;
-        int64_t cache = 0, heads = 0, cache_device, sections, axes, flags;
+        int64_t cache = 0, heads = 0, cache_device, flags;
+        Sections sections;
         if (a[0] != Py_None) {
-            if (!rows_of(a[0], &q) || !rows_of(a[12], &out) || out.n != q.n || out.heads != q.heads || out.dim != q.dim ||
+            if (!rows_of(a[0], &q) || !rows_of(a[11], &out) || out.n != q.n || out.heads != q.heads || out.dim != q.dim ||
                 out.device != q.device)
                 return other_form();
         }
@@ -157,24 +179,24 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor* pos = tensor_of(a[3]);
         const at::Tensor* freq = tensor_of(a[4]);
         void* stream;
-        if (!any.p || !pos || !freq || !integer(a[9], &sections) || !integer(a[10], &axes) || !integer(a[11], &flags) ||
+        if (!any.p || !pos || !freq || !sections_of(a[9], &sections) || !integer(a[10], &flags) ||
             freq->scalar_type() != at::kFloat || !on(freq, any.device) || freq->dim() != 1 || !freq->is_contiguous())
             return other_form();
         if (pos->dim() == 1) {
-            if (axes != 1 || !vector_of(a[3], any.n, any.device, &positions)) return other_form();
+            if (sections.axes != 1 || !vector_of(a[3], any.n, any.device, &positions)) return other_form();
         } else {
-            if (pos->dim() != 2 || pos->scalar_type() != at::kInt || !on(pos, any.device) || !pos->is_contiguous() || pos->size(0) != axes ||
+            if (pos->dim() != 2 || pos->scalar_type() != at::kInt || !on(pos, any.device) || !pos->is_contiguous() || pos->size(0) != sections.axes ||
                 pos->size(1) != any.n)
                 return other_form();
             positions = static_cast<int32_t*>(pos->data_ptr());
         }
-        if (any.n == 0 || q.heads > INT32_MAX || freq->size(0) > INT32_MAX / 2 || !stream_of(a[13], any.device, &stream))
+        if (any.n == 0 || q.heads > INT32_MAX || freq->size(0) > INT32_MAX / 2 || !stream_of(a[12], any.device, &stream))
             return other_form();
         const int rotary = 2 * static_cast<int>(freq->size(0));
         const float* f = static_cast<const float*>(freq->data_ptr());
         return status_of([&] {
             return g_append(q.p, q.row, q.head, out.p, out.row, out.head, static_cast<int>(q.heads), k.p, k.row, k.head, v.p, v.row,
-                            v.head, positions, any.n, f, reinterpret_cast<const int32_t*>(sections), static_cast<int>(axes), rotary,
+                            v.head, positions, any.n, f, sections.p, sections.axes, rotary,
                             static_cast<int>(any.dim), static_cast<unsigned>(flags), slots,
                             reinterpret_cast<const w4a16_kv_cache*>(cache), any.n, stream);
         });
