@@ -17,11 +17,14 @@
 // are requested before this one's are turned and written: reads and writes
 // overlap within a CTA, and two buffers of angles leave one barrier a group.
 //
-// Measured on one GB300 (copies run at 6.67 TB/s), 32 query and 8 key/value
-// heads of 128: 16384 tokens of three axes into bf16 62.7 us (6.43 TB/s), 4095
-// tokens into e4m3 18.2 us (5.07 TB/s; instruction issue), one token 1.6 us.  With
-// a group's requests after the last one's writes: 66.6, 20.2 and 1.9 us.  More CTAs
-// an SM leave too few registers: one token a thread and five CTAs 88 us for the first.
+// Measured on one GB300 (copies run at 6.67 TB/s) in a CUDA graph, 32 query and 8
+// key/value heads of 128: 16384 tokens of three axes into bf16 62.3 us (6.47 TB/s),
+// 4095 tokens into e4m3 18.1 us (5.09 TB/s; 65 % of the issue slots over the whole
+// call, with 39 % of the warps an SM could hold: what limits it is not shown), one
+// token 1.5 us.  With a group's requests after the last one's writes: 66.6, 20.2 and
+// 1.9 us.  More CTAs an SM leave too few registers: one token a thread and five CTAs
+// 88 us for the first.  (As it is, 16 bytes a thread are spilled with one token a
+// thread, 24 with two.)
 #include <algorithm>
 
 #include <cuda_fp8.h>
