@@ -12,8 +12,9 @@
 //
 // Bound by latency (length, sums, table entry, store): on one GB300, in a CUDA
 // graph, 2.9 us for 16 requests of one new token, 4.9 us for 262144 tokens of 96
-// requests, whose 2.3 MB would take 0.34 us (3.2 and 5.2 us a call).  (A launch for the sums and one for the rest would
-// cost a launch more; 512 threads a CTA, 7.7 us for the latter case.)
+// requests, whose 2.3 MB would take 0.34 us (3.2 and 5.2 us a call).  (A launch
+// for the sums and one for the rest would cost a launch more; 512 threads a CTA,
+// 7.7 us for the latter case.)
 #include "common.cuh"
 #include "paged.h"
 
