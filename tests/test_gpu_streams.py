@@ -147,3 +147,24 @@ def test_the_current_stream_by_name_changes_nothing(w):
         a, b = call(None), call(s)
     s.synchronize()
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("name", ["attention", "rope", "ffn"])
+def test_a_forked_stream_in_a_capture(w, name):
+    call = CALLS[name](w)
+    want = [bits(t) for t in tensors(call(None))]
+    torch.cuda.synchronize()
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.wait_stream(torch.cuda.current_stream())
+        got = tensors(call(s))
+        torch.cuda.current_stream().wait_stream(s)
+        read = [t.clone() for t in got]
+    for _ in range(3):
+        for t in got + read:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(read, want):
+            assert torch.equal(bits(a), b)
+    assert w.w4a16_device_error(clear=True) == 0
