@@ -478,7 +478,8 @@ W4A16_API w4a16_status w3a16_moe_gemv(const uint16_t* x, int x_per_slot,
  */
 typedef enum w4a16_cache_dtype {
     W4A16_CACHE_BF16 = 0,
-    W4A16_CACHE_E4M3 = 1 /* 8-bit floats: 4 exponent and 3 fraction bits, largest 448 */
+    W4A16_CACHE_E4M3 = 1, /* 8-bit floats: 4 exponent and 3 fraction bits, largest 448 */
+    W4A16_CACHE_INT8 = 2  /* -127..127; w4a16_scaled_cache only */
 } w4a16_cache_dtype;
 
 typedef struct w4a16_kv_cache {
@@ -613,6 +614,120 @@ W4A16_API w4a16_status w4a16_paged_attention(const uint16_t* q, int64_t q_reques
                                              int64_t out_request, int64_t out_head, float* lse,
                                              void* workspace, size_t workspace_bytes,
                                              void* stream);
+
+/*
+ * A paged cache in 8 bits whose scales are found as it is written: one fp32
+ * scale for each group of `group` neighbouring tokens of a block and each head,
+ * key = code * scale, value = code * scale.  Blocks, block tables and slots are
+ * those of w4a16_kv_cache (w4a16_paged_map serves both).
+ *   w4a16_scaled_append     rotary positions on q and k, k and v into the cache
+ *   w4a16_scaled_read       keys and values of requests back, in bf16 or fp32
+ *   w4a16_scaled_attention  one to sixteen new tokens of every request over it
+ * Alignment as above: codes in rows of 16 bytes (strides multiples of 16), scales
+ * 4 bytes.
+ */
+typedef struct w4a16_scaled_cache {
+    void* k;        /* k and v: device, code (block, token, head, d) at */
+    void* v;        /*   block * *_block + token * *_token + head * *_head + d */
+    float* k_scale; /* scale of (block, token, head) at block * ks_block + */
+    float* v_scale; /*   token / group * ks_group + head * ks_head (vs_* for the values) */
+    int32_t dtype;  /* W4A16_CACHE_E4M3 or W4A16_CACHE_INT8 */
+    int32_t heads;  /* key/value heads */
+    int32_t dim;    /* values of a head: a multiple of 16, 16..256 */
+    int32_t page;   /* tokens of a block, 1..65536 */
+    int32_t group;  /* tokens of a scale, 1..128, a divisor of page */
+    int64_t blocks; /* blocks * page < 2^31 */
+    int64_t k_block, k_token, k_head; /* strides in elements */
+    int64_t v_block, v_token, v_head;
+    int64_t ks_block, ks_group, ks_head;
+    int64_t vs_block, vs_group, vs_head;
+} w4a16_scaled_cache;
+
+/*
+ * w4a16_scaled_append -- w4a16_rope_append into a w4a16_scaled_cache, which finds the
+ * scales.  Arguments as there (flags: W4A16_ROPE_INTERLEAVED only).  With most = 448
+ * (E4M3) or 127 (INT8), for each group and head, keys and values apart:
+ *   The new tokens of a group are neighbours in the call, their slots ascending by
+ *   one; the first of them is place f of the group, whose earlier places a request
+ *   has filled before (f = 0 begins the group anew, whatever it held).
+ *   S = the smallest power of two that is >= 2^-126, >= need / most, and >= |the
+ *   scale so far| where f > 0.  need: the largest of the new tokens' magnitudes, of a
+ *   pair that is turned its length sqrt(x1^2 + x2^2) (the fp32 sum of the squares),
+ *   which no position changes.
+ *   New places: code = value / S, an exact quotient, rounded once to nearest even.
+ *   Places before f, where S is not the scale so far: code = code * (scale so far /
+ *   S), rounded likewise.  Between powers of two that shifts: an e4m3 code loses
+ *   nothing above 2^-6 S, an int8 one half a step each time, so that beside the
+ *   rotation's own error
+ *       E4M3: |code * S - value| <= 2^-4 |value| + 2^-9 S,   INT8: <= S
+ *   however often S grew (max(2^-4 |value|, 2^-10 S) and S / 2 where it did not).
+ *   A value that is not finite makes S NaN, and the group stands for NaN until it is
+ *   begun anew.  Places behind the new tokens keep their codes.
+ * slots[t] == -1: not stored; a slot outside the cache, or one in the group of the
+ * token before that does not follow that token's: not stored and W4A16_DEVERR_SLOT.
+ * The same group twice in a call with other tokens between: its contents are
+ * undefined.
+ */
+W4A16_API w4a16_status w4a16_scaled_append(const uint16_t* q, int64_t q_token, int64_t q_head,
+                                           uint16_t* q_out, int64_t q_out_token,
+                                           int64_t q_out_head, int q_heads, const uint16_t* k,
+                                           int64_t k_token, int64_t k_head, const uint16_t* v,
+                                           int64_t v_token, int64_t v_head,
+                                           const int32_t* positions, int64_t axis_stride,
+                                           const float* inv_freq, const int32_t* sections,
+                                           int axes, int rotary, int dim, unsigned flags,
+                                           const int32_t* slots, const w4a16_scaled_cache* cache,
+                                           int64_t T, void* stream);
+
+/*
+ * w4a16_scaled_read -- the keys and values of B >= 1 requests (at most 16384), one
+ * after another: row row_start[b] + i of k_out and v_out (row_start[b] <= row <
+ * row_start[b + 1]) is token first[b] + i of request b (first NULL: token i),
+ * code * scale rounded once to out_dtype (W4A16_OUT_BF16 or W4A16_OUT_F32).
+ *   k_out, v_out: head h of row r at r * *_row + h * *_head, rows of 16-byte
+ *   alignment; rows before row_start[0] and from row_start[B] on are left as they are.
+ *   rows: how many the outputs have; tokens past it are not read (W4A16_DEVERR_BLOCKS).
+ *   block_table as in w4a16_paged_attention; a token past columns * page, before 0 or in a
+ *   block outside the cache gives zeros and W4A16_DEVERR_SLOT.
+ *   row_start: int32 [B + 1], not descending (as w4a16_paged_map gives it; otherwise rows
+ *   are missing or undefined, but nothing outside the outputs is written).
+ */
+W4A16_API w4a16_status w4a16_scaled_read(const w4a16_scaled_cache* cache,
+                                         const int32_t* block_table, int64_t table_stride,
+                                         int columns, const int32_t* row_start,
+                                         const int32_t* first, int B, void* k_out, int64_t k_row,
+                                         int64_t k_out_head, void* v_out, int64_t v_row,
+                                         int64_t v_out_head, int out_dtype, int64_t rows,
+                                         void* stream);
+
+/*
+ * w4a16_scaled_attention_workspace_bytes -- device workspace of
+ * w4a16_scaled_attention for this head layout and number of new tokens.
+ */
+W4A16_API size_t w4a16_scaled_attention_workspace_bytes(int q_heads, int kv_heads, int dim,
+                                                        int new_tokens);
+
+/*
+ * w4a16_scaled_attention -- w4a16_paged_attention over a w4a16_scaled_cache, for the last
+ * `new_tokens` (N, 1..16) tokens of each request: new token i of request b, 0 <= i <
+ * N, sees the tokens below L = kv_len[b] - (N - 1 - i), of them the last `window` (0:
+ * all); where L <= 0 its out is 0 and its lse -infinity.  So drafts are verified
+ * together, each seeing those before it.
+ *   q, out: bf16, head h of new token i of request b at b * *_request + i * *_token +
+ *   h * *_head; lse: fp32 [B][N][q_heads] or NULL.
+ * fp32 scores, maxima and sums; two roundings: of out to bf16, and of the weights w_j =
+ * p_j * v_scale_j to fp16 before they multiply the codes c_j.  So, beside fp32's,
+ *     |error| <= 2^-8 |out| + 2^-11 sum_j p_j |v_j| + 2^-40 max_j w_j sum_j |c_j|.
+ * A key or value that is NaN reaches the new tokens that see it and no others.
+ * The other arguments, the workspace and the limits are those of w4a16_paged_attention,
+ * with N * q_heads in the place of q_heads.
+ */
+W4A16_API w4a16_status w4a16_scaled_attention(
+    const uint16_t* q, int64_t q_request, int64_t q_token, int64_t q_head,
+    const w4a16_scaled_cache* cache, const int32_t* block_table, int64_t table_stride, int columns,
+    const int32_t* kv_len, int B, int new_tokens, int q_heads, float scale, int window,
+    uint16_t* out, int64_t out_request, int64_t out_token, int64_t out_head, float* lse,
+    void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * w4a16_swiglu -- h[r][n] = bf16(silu(gate[r][n]) * up[r][n]), computed in

@@ -125,6 +125,15 @@ def load_library():
     lib.w4a16_paged_attention.restype = I32
     lib.w4a16_paged_attention.argtypes = [P, I64, I64, P, P, I64, I32, P, I32, I32, ctypes.c_float, I32, P,
                                           I64, I64, P, P, SZ, P]
+    lib.w4a16_scaled_append.restype = I32
+    lib.w4a16_scaled_append.argtypes = lib.w4a16_rope_append.argtypes
+    lib.w4a16_scaled_read.restype = I32
+    lib.w4a16_scaled_read.argtypes = [P, P, I64, I32, P, P, I32, P, I64, I64, P, I64, I64, I32, I64, P]
+    lib.w4a16_scaled_attention_workspace_bytes.restype = SZ
+    lib.w4a16_scaled_attention_workspace_bytes.argtypes = [I32, I32, I32, I32]
+    lib.w4a16_scaled_attention.restype = I32
+    lib.w4a16_scaled_attention.argtypes = [P, I64, I64, I64, P, P, I64, I32, P, I32, I32, I32, ctypes.c_float, I32, P,
+                                           I64, I64, I64, P, P, SZ, P]
     _lib = lib
     return lib
 
@@ -154,22 +163,23 @@ def _stream(stream, device: int = None):
     return torch.cuda.current_stream().cuda_stream
 
 
-def _empty(shape, dtype, device, stream, kept: bool = True) -> torch.Tensor:
+def _empty(shape, dtype, device, stream, kept: bool = True, zero: bool = False) -> torch.Tensor:
     """Memory that a call on `stream` makes itself.  Where that is not the
     current stream, it is taken on `stream`: the allocator then hands it to
     nobody else before the call's kernels are done with it.  What the caller
     gets (kept) counts as used on the current stream too."""
+    make = torch.zeros if zero else torch.empty
     if stream is not None:
         here = torch.cuda.current_stream(device)
         if stream.cuda_stream != here.cuda_stream:
             if not isinstance(stream, torch.cuda.Stream):
                 stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
             with torch.cuda.stream(stream):
-                t = torch.empty(shape, dtype=dtype, device=device)
+                t = make(shape, dtype=dtype, device=device)
             if kept:
                 t.record_stream(here)
             return t
-    return torch.empty(shape, dtype=dtype, device=device)
+    return make(shape, dtype=dtype, device=device)
 
 
 def _ptr(t: torch.Tensor):
@@ -644,7 +654,7 @@ def _load_fast():
     import importlib.machinery
     from . import build_ext
     path = build_ext.fastcall_path()
-    if path is None or not os.path.exists(path) or _raw_current_stream is None:
+    if path is None or not os.path.exists(path) or _raw_current_stream is None or not hasattr(torch._C, "_cuda_getDevice"):
         return None
     loader = importlib.machinery.ExtensionFileLoader("_fastcall", path)
     try:
@@ -654,7 +664,8 @@ def _load_fast():
         return None
     address = lambda f: ctypes.cast(f, ctypes.c_void_p).value
     mod.bind(address(_lib.w4a16_paged_map), address(_lib.w4a16_rope_append), address(_lib.w4a16_paged_attention),
-             _raw_current_stream)
+             address(_lib.w4a16_scaled_append), address(_lib.w4a16_scaled_read), address(_lib.w4a16_scaled_attention),
+             _raw_current_stream, torch._C._cuda_getDevice)
     return mod
 
 
@@ -865,6 +876,248 @@ def w4a16_paged_attention(q, cache: PagedCache, block_table, kv_len, scale: floa
     if rc:
         raise W4A16Error(rc, "w4a16_paged_attention")
     return out, lse
+
+
+# --------------------------------------------------------------------------
+# Paged cache in 8 bits, a scale for each group of tokens and head
+# --------------------------------------------------------------------------
+CACHE_INT8 = 2
+
+
+class _ScaledCache(ctypes.Structure):
+    """w4a16_scaled_cache of include/w4a16.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("dtype", ctypes.c_int32), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("group", ctypes.c_int32), ("blocks", ctypes.c_int64),
+                ("k_block", ctypes.c_int64), ("k_token", ctypes.c_int64), ("k_head", ctypes.c_int64),
+                ("v_block", ctypes.c_int64), ("v_token", ctypes.c_int64), ("v_head", ctypes.c_int64),
+                ("ks_block", ctypes.c_int64), ("ks_group", ctypes.c_int64), ("ks_head", ctypes.c_int64),
+                ("vs_block", ctypes.c_int64), ("vs_group", ctypes.c_int64), ("vs_head", ctypes.c_int64)]
+
+
+class ScaledCache:
+    """Handle of one layer's paged key/value cache in 8 bits with a scale for
+    each group of tokens and head.
+
+    k, v: CUDA tensors [blocks, page, heads, dim], int8 or float8_e4m3fn, dim
+    contiguous, the other strides free; k_scale, v_scale: float32 [blocks, page //
+    group, heads], any strides: key = code * k_scale of its group and head.
+    w4a16_scaled_append finds the scales and writes codes and scales; neither
+    needs initialisation.  The tensors stay the caller's; the handle holds
+    references to them, so the memory it points at lives as long as it does."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        for t, name in ((k, "k"), (v, "v"), (k_scale, "k_scale"), (v_scale, "v_scale")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError("%s must be a torch.Tensor" % name)
+            if not t.is_cuda:
+                raise ValueError("%s must be a CUDA tensor" % name)
+        for t, name in ((k, "k"), (v, "v")):
+            if t.dim() != 4 or t.stride(3) != 1:
+                raise ValueError("%s must be [blocks, page, heads, dim], dim contiguous" % name)
+        if k.dtype not in (torch.int8, torch.float8_e4m3fn) or v.dtype != k.dtype:
+            raise TypeError("k and v must both be int8 or both float8_e4m3fn")
+        if v.shape != k.shape:
+            raise ValueError("k and v must have the same shape")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.blocks, self.page, self.heads, self.dim = k.shape
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t.dtype is not torch.float32:
+                raise TypeError("%s has dtype %s, expected torch.float32" % (name, t.dtype))
+            if t.dim() != 3 or t.shape != k_scale.shape or t.shape[0] != self.blocks or t.shape[2] != self.heads or t.shape[1] < 1 or self.page % t.shape[1]:
+                raise ValueError("%s has shape %s, expected [%d, page // group, %d] for a page of %d"
+                                 % (name, tuple(t.shape), self.blocks, self.heads, self.page))
+        self.group = self.page // k_scale.shape[1]
+        self.device = k.get_device()
+        _on_device(self.device, v=v, k_scale=k_scale, v_scale=v_scale)
+        self._struct = _ScaledCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), CACHE_INT8 if k.dtype is torch.int8 else CACHE_E4M3,
+                                    self.heads, self.dim, self.page, self.group, self.blocks,
+                                    *k.stride()[:3], *v.stride()[:3], *k_scale.stride(), *v_scale.stride())
+        self._ref = ctypes.addressof(self._struct)
+
+
+def _scaled(cache) -> ScaledCache:
+    if not isinstance(cache, ScaledCache):
+        raise TypeError("cache must be a ScaledCache")
+    return cache
+
+
+def _launch(device: int, entry, *args) -> int:
+    """A C call whose tensors are on `device`, made with that as the current device."""
+    with torch.cuda.device(device):
+        return entry(*args)
+
+
+def w4a16_scaled_append(q, k, v, positions, inv_freq, slots, cache: ScaledCache, sections=None,
+                        interleaved: bool = False, q_out=None, stream=None):
+    """Rotary positions on q and k, and k and v into a cache whose scales are found
+    as it is written.
+
+    Arguments as in w4a16_rope_append; q may be None, k, v and slots may not.  A
+    group's scale is the smallest power of two whose codes hold its values, and
+    grows with them; a request fills its groups in order, and the tokens of one
+    group are neighbours in the call, their slots ascending (as w4a16_paged_map
+    gives them).  Returns the rotated queries (q_out, or a new tensor; q_out=q
+    rotates in place)."""
+    _scaled(cache)
+    flags = ROPE_INTERLEAVED if interleaved else 0
+    if _fast is not None and (q is None or q_out is not None):
+        rc = _fast.scaled_append(q, k, v, positions, inv_freq, slots, cache._ref, cache.heads, cache.device, sections, flags,
+                                 q_out, None if stream is None else stream.cuda_stream)
+        if rc == 0:
+            return q_out
+        if rc is not None:
+            raise W4A16Error(rc, "w4a16_scaled_append")
+    T = k.shape[0]
+    shape = (T, cache.heads, cache.dim)
+    ka, va, slots_at = _rows(k, "k", shape), _rows(v, "v", shape), _vector(slots, "slots", T)
+    heads, qa, qo = 0, (None, 0, 0), (None, 0, 0)
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != cache.dim:
+            raise ValueError("q has shape %s, expected [%d, q_heads, %d]" % (tuple(q.shape), T, cache.dim))
+        heads, qa = q.shape[1], _rows(q, "q", q.shape)
+        if q_out is None:
+            q_out = _empty(q.shape, _bf16, q.device, stream)
+        qo = _rows(q_out, "q_out", q.shape)
+    _need(inv_freq, "inv_freq", _F32)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must have one dimension")
+    if positions.dim() == 1:
+        axes, axis_stride, positions_at = 1, 0, _vector(positions, "positions", T)
+    else:
+        axes, axis_stride = positions.shape[0], T
+        _need(positions, "positions", _I32, (axes, T))
+        positions_at = positions.data_ptr()
+    sec = None
+    if sections is not None:
+        if len(sections) != axes:
+            raise ValueError("%d sections for %d axes" % (len(sections), axes))
+        sec = _section_array(sections)
+    _on_device(cache.device, q=q, q_out=q_out if q is not None else None, k=k, v=v, positions=positions, inv_freq=inv_freq, slots=slots)
+    if T == 0:
+        return q_out
+    rc = _launch(cache.device, _lib.w4a16_scaled_append, *qa, *qo, heads, *ka, *va, positions_at, axis_stride, inv_freq.data_ptr(), sec, axes,
+                 2 * inv_freq.numel(), cache.dim, flags, slots_at, cache._ref, T, _stream(stream, cache.device))
+    if rc:
+        raise W4A16Error(rc, "w4a16_scaled_append")
+    return q_out
+
+
+def w4a16_scaled_read(cache: ScaledCache, block_table, row_start, first=None, k_out=None, v_out=None, rows: int = None,
+                      dtype=torch.bfloat16, stream=None):
+    """The keys and values of requests, one request after another.
+
+    Row row_start[b] + i of k_out and v_out [rows, heads, dim] (bfloat16 or
+    float32, row and head strides allowed) is token first[b] + i of request b (first
+    None: token i), for rows below row_start[b + 1]; block_table int32 [B, columns],
+    row_start int32 [B + 1], first int32 [B].  Rows behind row_start[B] are left as
+    they are.  Without k_out and v_out: new tensors of `rows` rows and `dtype`,
+    zeros where no request has a row.  Returns (k_out, v_out)."""
+    _scaled(cache)
+    if _fast is not None and k_out is not None and first is None:
+        rc = _fast.scaled_read(cache._ref, cache.heads, cache.dim, cache.device, block_table, row_start, k_out, v_out,
+                               None if stream is None else stream.cuda_stream)
+        if rc == 0:
+            return k_out, v_out
+        if rc is not None:
+            raise W4A16Error(rc, "w4a16_scaled_read")
+    B = len(row_start) - 1
+    table, stride, columns = _table(block_table, B)
+    start = _vector(row_start, "row_start", B + 1)
+    first_at = None if first is None else _vector(first, "first", B)
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out go together")
+    if k_out is None:
+        if rows is None:
+            raise ValueError("rows is needed without k_out and v_out")
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError("dtype must be torch.bfloat16 or torch.float32")
+        k_out, v_out = (_empty((rows, cache.heads, cache.dim), dtype, cache.k.device, stream, zero=True) for _ in range(2))
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in (torch.bfloat16, torch.float32) or t.dtype != k_out.dtype:
+            raise TypeError("%s must be a CUDA tensor, both bfloat16 or both float32" % name)
+        if t.dim() != 3 or t.stride(2) != 1 or t.shape != k_out.shape or t.shape[1:] != (cache.heads, cache.dim):
+            raise ValueError("%s has shape %s, expected [rows, %d, %d], dim contiguous" % (name, tuple(t.shape), cache.heads, cache.dim))
+    if rows is not None and rows != k_out.shape[0]:
+        raise ValueError("rows is %d, k_out has %d" % (rows, k_out.shape[0]))
+    _on_device(cache.device, block_table=block_table, row_start=row_start, first=first, k_out=k_out, v_out=v_out)
+    rc = _launch(cache.device, _lib.w4a16_scaled_read, cache._ref, table, stride, columns, start, first_at, B, k_out.data_ptr(), *k_out.stride()[:2],
+                 v_out.data_ptr(), *v_out.stride()[:2], OUT_F32 if k_out.dtype is torch.float32 else OUT_BF16, k_out.shape[0],
+                 _stream(stream, cache.device))
+    if rc:
+        raise W4A16Error(rc, "w4a16_scaled_read")
+    return k_out, v_out
+
+
+def scaled_attention_workspace(cache: ScaledCache, q_heads: int, new_tokens: int = 1) -> torch.Tensor:
+    """Workspace of w4a16_scaled_attention for this cache, number of query heads
+    and most new tokens (its contents need no initialisation)."""
+    return _scaled_workspace(cache, q_heads, new_tokens, None)
+
+
+def _scaled_workspace(cache: ScaledCache, q_heads: int, new_tokens: int, stream) -> torch.Tensor:
+    n = int(load_library().w4a16_scaled_attention_workspace_bytes(q_heads, cache.heads, cache.dim, new_tokens))
+    return _empty(max(n, 16), torch.uint8, cache.k.device, stream, kept=False)
+
+
+def w4a16_scaled_attention(q, cache: ScaledCache, block_table, kv_len, scale: float = None, window: int = 0,
+                           out=None, lse=None, workspace=None, stream=None):
+    """Attention of the last one to sixteen tokens of each request over the cache.
+
+    q bf16 [B, q_heads, dim], or [B, N, q_heads, dim] for N new tokens of each
+    request (request, token and head strides allowed); block_table int32 [B, columns];
+    kv_len int32 [B], all tokens of a request, the new ones among them: new token i
+    sees kv_len - (N - 1 - i) of them, with window > 0 the last `window` of those.
+    scale defaults to dim ** -0.5.  Returns (out like q, lse float32 [B, q_heads] or
+    [B, N, q_heads]); a token that sees nothing gets zeros and -infinity.
+    workspace: from scaled_attention_workspace, one per stream in use (None: a new
+    one for this call)."""
+    _scaled(cache)
+    if scale is None:
+        scale = cache.dim ** -0.5
+    if _fast is not None and workspace is not None:
+        rc = _fast.scaled_attention(q, cache._ref, cache.dim, cache.device, block_table, kv_len, scale, window, out, lse, workspace,
+                                    None if stream is None else stream.cuda_stream)
+        if rc == 0:
+            return out, lse
+        if rc is not None:
+            raise W4A16Error(rc, "w4a16_scaled_attention")
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+        raise ValueError("q must be a tensor [B, q_heads, dim] or [B, new tokens, q_heads, dim]")
+    by_token = (lambda t: t) if q.dim() == 4 else (lambda t: t.unsqueeze(1))
+    B, N, H = by_token(q).shape[:3]
+    qa = _token_rows(by_token(q), "q", (B, N, H, cache.dim))
+    table, stride, columns = _table(block_table, B)
+    lengths = _vector(kv_len, "kv_len", B)
+    if out is None:
+        out = _empty(q.shape, _bf16, q.device, stream)
+    elif not isinstance(out, torch.Tensor) or out.dim() != q.dim():
+        raise ValueError("out must be a tensor of q's shape")
+    oa = _token_rows(by_token(out), "out", (B, N, H, cache.dim))
+    if lse is None:
+        lse = _empty(q.shape[:-1], torch.float32, q.device, stream)
+    else:
+        _need(lse, "lse", _F32, q.shape[:-1])
+    if workspace is None:
+        workspace = _scaled_workspace(cache, H, N, stream)
+    elif not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    _on_device(cache.device, q=q, block_table=block_table, kv_len=kv_len, out=out, lse=lse, workspace=workspace)
+    rc = _launch(cache.device, _lib.w4a16_scaled_attention, *qa, cache._ref, table, stride, columns, lengths, B, N, H, scale, window, *oa, lse.data_ptr(),
+                 workspace.data_ptr(), workspace.nbytes, _stream(stream, cache.device))
+    if rc:
+        raise W4A16Error(rc, "w4a16_scaled_attention")
+    return out, lse
+
+
+def _token_rows(t, name: str, shape):
+    """Address, request, token and head strides of bf16 heads [B, N, heads, dim], dim contiguous."""
+    if not t.is_cuda or t.dtype not in _BF16 or t.stride(3) != 1:
+        raise ValueError("%s must be a CUDA bf16 tensor, dim contiguous" % name)
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    return (t.data_ptr(), *t.stride()[:3])
 
 
 load_library()

@@ -16,6 +16,7 @@
 #include "launch.h"
 #include "moe_hmma_gemv.h"
 #include "paged.h"
+#include "scaled.h"
 #include "w4a16.h"
 
 namespace w4a16 {
@@ -853,6 +854,163 @@ w4a16_status w4a16_paged_attention(const uint16_t* q, int64_t q_request, int64_t
     AttentionArgs a{q, q_request, q_head, *cache, block_table, table_stride, kv_len, static_cast<int>(most), B, q_heads, window,
                     scale, out, out_request, out_head, lse, workspace, dev->err};
     return from_cuda(launch_paged_attention(a, dev->info, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+w4a16_status check_scaled_cache(const w4a16_scaled_cache& c) {
+    if (!c.k || !c.v || !c.k_scale || !c.v_scale) return W4A16_ERR_NULL;
+    if (c.dtype != W4A16_CACHE_E4M3 && c.dtype != W4A16_CACHE_INT8) return W4A16_ERR_UNSUPPORTED;
+    if (c.heads < 1 || c.page < 1 || c.blocks < 1 || c.dim < 16 || c.dim % 16 != 0 || c.group < 1) return W4A16_ERR_SHAPE;
+    if (c.dim > 256 || c.page > 65536 || c.heads > 65536 || c.group > kMostGroup) return W4A16_ERR_UNSUPPORTED;
+    if (c.page % c.group != 0) return W4A16_ERR_SHAPE;
+    if (c.blocks >= (int64_t(1) << 31) / c.page) return W4A16_ERR_UNSUPPORTED;
+    if (!aligned16(c.k) || !aligned16(c.v) || !aligned4(c.k_scale) || !aligned4(c.v_scale) ||
+        !row_strides(c.k_block, c.k_token, 16) || !row_strides(c.v_block, c.v_token, 16) ||
+        !row_strides(c.k_head, c.v_head, 16) || !row_strides(c.ks_block, c.ks_group, 1) ||
+        !row_strides(c.vs_block, c.vs_group, 1) || !row_strides(c.ks_head, c.vs_head, 1))
+        return W4A16_ERR_ALIGN;
+    return W4A16_OK;
+}
+
+// Whether two places of the cache are one (a stride of 0 over more than one): it can be
+// read, but not written.
+bool shares_places(const w4a16_scaled_cache& c) {
+    const int groups = c.page / c.group;
+    return (c.blocks > 1 && (!c.k_block || !c.v_block || !c.ks_block || !c.vs_block)) || (c.page > 1 && (!c.k_token || !c.v_token)) ||
+           (groups > 1 && (!c.ks_group || !c.vs_group)) || (c.heads > 1 && (!c.k_head || !c.v_head || !c.ks_head || !c.vs_head));
+}
+
+}  // namespace
+
+extern "C" {
+
+w4a16_status w4a16_scaled_append(const uint16_t* q, int64_t q_token, int64_t q_head, uint16_t* q_out,
+                                 int64_t q_out_token, int64_t q_out_head, int q_heads, const uint16_t* k,
+                                 int64_t k_token, int64_t k_head, const uint16_t* v, int64_t v_token,
+                                 int64_t v_head, const int32_t* positions, int64_t axis_stride,
+                                 const float* inv_freq, const int32_t* sections, int axes, int rotary, int dim,
+                                 unsigned flags, const int32_t* slots, const w4a16_scaled_cache* cache, int64_t T,
+                                 void* stream) {
+    if (flags & ~static_cast<unsigned>(W4A16_ROPE_INTERLEAVED)) return W4A16_ERR_UNSUPPORTED;
+    const bool has_q = q != nullptr;
+    if (has_q != (q_out != nullptr) || !cache || !k || !v || !slots) return W4A16_ERR_NULL;
+    if (rotary > 0 && (!positions || !inv_freq)) return W4A16_ERR_NULL;
+    if (T < 0 || axes < 1 || axis_stride < 0 || rotary < 0 || rotary % 16 != 0 || dim < 16 || dim % 16 != 0 ||
+        rotary > dim || (has_q && q_heads < 1))
+        return W4A16_ERR_SHAPE;
+    if (axes > 4 || dim > 256 || q_heads > 65536 || T >= (int64_t(1) << 31)) return W4A16_ERR_UNSUPPORTED;
+    w4a16_status st = check_scaled_cache(*cache);
+    if (st != W4A16_OK) return st;
+    if (cache->dim != dim) return W4A16_ERR_SHAPE;
+    if (shares_places(*cache)) return W4A16_ERR_UNSUPPORTED;
+    ScaledAppendArgs a{};
+    if (!sections && axes != 1) return W4A16_ERR_NULL;
+    int sum = 0;
+    for (int i = 0; i < 4; ++i) {
+        if (i < axes) {
+            const int n = sections ? sections[i] : rotary / 2;
+            if (n < 0 || n > rotary / 2) return W4A16_ERR_SHAPE;
+            sum += n;
+        }
+        a.axis_end[i] = sum;
+    }
+    if (sum != rotary / 2) return W4A16_ERR_SHAPE;
+    if ((has_q && (!aligned16(q) || !aligned16(q_out) || !row_strides(q_token, q_head, 8) ||
+                   !row_strides(q_out_token, q_out_head, 8))) ||
+        !aligned16(k) || !aligned16(v) || !row_strides(k_token, k_head, 8) || !row_strides(v_token, v_head, 8) ||
+        !aligned4(positions) || !aligned4(inv_freq) || !aligned4(slots))
+        return W4A16_ERR_ALIGN;
+    if (T == 0) return W4A16_OK;
+    DeviceCache* dev = nullptr;
+    st = current_device(&dev);
+    if (st != W4A16_OK) return st;
+    a.q = q, a.q_token = q_token, a.q_head = q_head;
+    a.q_out = q_out, a.qo_token = q_out_token, a.qo_head = q_out_head;
+    a.q_heads = has_q ? q_heads : 0;
+    a.k = k, a.k_token = k_token, a.k_head = k_head;
+    a.v = v, a.v_token = v_token, a.v_head = v_head;
+    a.positions = positions, a.axis_stride = axis_stride, a.inv_freq = inv_freq;
+    a.slots = slots, a.cache = *cache, a.rotary = rotary, a.dim = dim, a.T = T;
+    a.interleaved = (flags & W4A16_ROPE_INTERLEAVED) ? 1 : 0;
+    a.err = dev->err;
+    return from_cuda(launch_scaled_append(a, dev->info, static_cast<cudaStream_t>(stream)));
+}
+
+w4a16_status w4a16_scaled_read(const w4a16_scaled_cache* cache, const int32_t* block_table, int64_t table_stride,
+                               int columns, const int32_t* row_start, const int32_t* first, int B, void* k_out,
+                               int64_t k_row, int64_t k_out_head, void* v_out, int64_t v_row, int64_t v_out_head,
+                               int out_dtype, int64_t rows, void* stream) {
+    if (!cache || !block_table || !row_start || (rows > 0 && (!k_out || !v_out))) return W4A16_ERR_NULL;
+    w4a16_status st = check_scaled_cache(*cache);
+    if (st != W4A16_OK) return st;
+    if (B < 1 || columns < 1 || table_stride < columns || rows < 0) return W4A16_ERR_SHAPE;
+    if (B > kMaxMapRequests || rows >= (int64_t(1) << 31) || (out_dtype != W4A16_OUT_BF16 && out_dtype != W4A16_OUT_F32))
+        return W4A16_ERR_UNSUPPORTED;
+    const int row = out_dtype == W4A16_OUT_BF16 ? 8 : 4;
+    if (!aligned16(k_out) || !aligned16(v_out) || !row_strides(k_row, k_out_head, row) ||
+        !row_strides(v_row, v_out_head, row) || !aligned4(block_table) || !aligned4(row_start) || !aligned4(first))
+        return W4A16_ERR_ALIGN;
+    if (rows == 0) return W4A16_OK;
+    DeviceCache* dev = nullptr;
+    st = current_device(&dev);
+    if (st != W4A16_OK) return st;
+    ScaledReadArgs a{*cache, block_table, table_stride, row_start, first, k_out, v_out, k_row, k_out_head, v_row, v_out_head,
+                     rows, columns, B, out_dtype == W4A16_OUT_F32, dev->err};
+    return from_cuda(launch_scaled_read(a, dev->info, static_cast<cudaStream_t>(stream)));
+}
+
+size_t w4a16_scaled_attention_workspace_bytes(int q_heads, int kv_heads, int dim, int new_tokens) {
+    if (q_heads < 1 || q_heads >= (1 << 24) || kv_heads < 1 || q_heads % kv_heads != 0 || dim < 16 || dim > 256 ||
+        dim % 16 != 0 || new_tokens < 1 || new_tokens > kMostNew)
+        return 0;
+    return paged_attention_workspace(q_heads * new_tokens, kv_heads, dim);
+}
+
+w4a16_status w4a16_scaled_attention(const uint16_t* q, int64_t q_request, int64_t q_token, int64_t q_head,
+                                    const w4a16_scaled_cache* cache, const int32_t* block_table,
+                                    int64_t table_stride, int columns, const int32_t* kv_len, int B, int new_tokens,
+                                    int q_heads, float scale, int window, uint16_t* out, int64_t out_request,
+                                    int64_t out_token, int64_t out_head, float* lse, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+    if (!q || !cache || !block_table || !kv_len || !out) return W4A16_ERR_NULL;
+    w4a16_status st = check_scaled_cache(*cache);
+    if (st != W4A16_OK) return st;
+    if (B < 1 || q_heads < 1 || q_heads % cache->heads != 0 || columns < 1 || table_stride < columns || window < 0 ||
+        new_tokens < 1)
+        return W4A16_ERR_SHAPE;
+    if (new_tokens > kMostNew || static_cast<int64_t>(B) * q_heads >= (1 << 24) ||
+        static_cast<int64_t>(B) * q_heads * new_tokens >= (1 << 24))
+        return W4A16_ERR_UNSUPPORTED;
+    int64_t most = static_cast<int64_t>(columns) * cache->page;
+    if (most > 0x7FFFFFFF - 1024) most = 0x7FFFFFFF - 1024;  // token numbers stay in 32 bits
+    if (window >= most) window = 0;                          // all of them
+    if (!attention_costs_fit(static_cast<int>(most), window ? window + new_tokens - 1 : 0, q_heads * new_tokens, cache->heads))
+        return W4A16_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(out) || !row_strides(q_request, q_head, 8) || !row_strides(q_token, out_token, 8) ||
+        !row_strides(out_request, out_head, 8) || !aligned4(block_table) || !aligned4(kv_len) || !aligned4(lse))
+        return W4A16_ERR_ALIGN;
+    if (!workspace || workspace_bytes < paged_attention_workspace(q_heads * new_tokens, cache->heads, cache->dim))
+        return W4A16_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return W4A16_ERR_ALIGN;
+    DeviceCache* dev = nullptr;
+    st = current_device(&dev);
+    if (st != W4A16_OK) return st;
+    ScaledAttentionArgs a{};
+    a.q = q, a.q_request = q_request, a.q_token = q_token, a.q_head = q_head;
+    a.cache = w4a16_kv_cache{cache->k, cache->v, nullptr, nullptr, cache->dtype, cache->heads, cache->dim, cache->page, cache->blocks,
+                             cache->k_block, cache->k_token, cache->k_head, cache->v_block, cache->v_token, cache->v_head};
+    a.block_table = block_table, a.table_stride = table_stride, a.kv_len = kv_len;
+    a.most = static_cast<int>(most), a.B = B, a.q_heads = q_heads, a.window = window, a.scale = scale;
+    a.out = out, a.out_request = out_request, a.out_token = out_token, a.out_head = out_head;
+    a.lse = lse, a.workspace = workspace, a.err = dev->err;
+    a.tokens = new_tokens, a.k_scale = cache->k_scale, a.v_scale = cache->v_scale;
+    a.ks_block = cache->ks_block, a.ks_group = cache->ks_group, a.ks_head = cache->ks_head;
+    a.vs_block = cache->vs_block, a.vs_group = cache->vs_group, a.vs_head = cache->vs_head;
+    a.group = cache->group, a.magic = group_magic(cache->group);
+    return from_cuda(launch_scaled_attention(a, cache->dtype == W4A16_CACHE_INT8, dev->info, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -4,7 +4,7 @@
 namespace w4a16 {
 
 cudaError_t launch_attention_bf16(const AttentionArgs& a, const DeviceInfo& dev, JoinPlan join, cudaStream_t s) {
-    return launch_attention_type<false>(a, dev, join, s);
+    return launch_attention_type<kBf16>(a, dev, join, s);
 }
 
 }  // namespace w4a16

@@ -44,9 +44,32 @@
 
 #include "common.cuh"
 #include "paged_attention.h"
+#include "scaled.h"
 
 namespace w4a16 {
 namespace {
+
+// What a kernel is built for: the cache's type, and where its scales are.
+constexpr int kBf16 = 0;        // none
+constexpr int kE4m3 = 1;        // one a head
+constexpr int kE4m3Groups = 2;  // one a group of tokens and head, as for
+constexpr int kInt8Groups = 3;
+constexpr bool in_8_bits(int C) { return C != kBf16; }
+constexpr bool by_group(int C) { return C >= kE4m3Groups; }
+template <int C>
+struct ArgsOf {
+    using type = AttentionArgs;
+};
+template <>
+struct ArgsOf<kE4m3Groups> {
+    using type = ScaledAttentionArgs;
+};
+template <>
+struct ArgsOf<kInt8Groups> {
+    using type = ScaledAttentionArgs;
+};
+template <int C>
+using Args = typename ArgsOf<C>::type;
 
 constexpr int kMinCost = 3;     // a warp's share at least
 constexpr int kRowTiles = 8;    // rows kernel: tiles of a warp at most
@@ -86,13 +109,68 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<uint16_t>(v)));
     return d;
 }
+// A word of four codes as two fp16 pairs, exactly.
+template <int C>
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    if (C == kInt8Groups) {
+        // 1024 + (code + 128), the code's byte as the low one of an fp16
+        const uint32_t u = w ^ 0x80808080u;
+        const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+        uint32_t x = __byte_perm(u, 0x64646464u, 0x4140), y = __byte_perm(u, 0x64646464u, 0x4342);
+        const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&x), off), b = __hsub2(*reinterpret_cast<const __half2*>(&y), off);
+        lo = *reinterpret_cast<const uint32_t*>(&a), hi = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+        lo = e4m3x2_to_f16x2(w), hi = e4m3x2_to_f16x2(w >> 16);
+    }
+}
+// A word of four codes, two dims (even, odd) of one token, then of the next, as the fp16
+// pairs of the even and of the odd dim.
+template <int C>
+__device__ __forceinline__ void codes_to_f16_by_dim(uint32_t w, uint32_t& even, uint32_t& odd) {
+    if (C == kInt8Groups) {
+        const uint32_t u = w ^ 0x80808080u;
+        const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+        uint32_t x = __byte_perm(u, 0x64646464u, 0x4240), y = __byte_perm(u, 0x64646464u, 0x4341);
+        const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&x), off), b = __hsub2(*reinterpret_cast<const __half2*>(&y), off);
+        even = *reinterpret_cast<const uint32_t*>(&a), odd = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+        const uint32_t x0 = e4m3x2_to_f16x2(w), x1 = e4m3x2_to_f16x2(w >> 16);
+        even = __byte_perm(x0, x1, 0x5410), odd = __byte_perm(x0, x1, 0x7632);
+    }
+}
+// both halves, a NaN among them as a number
+__device__ __forceinline__ uint32_t as_numbers(uint32_t v) {
+    const __half2 low = __halves2half2(__ushort_as_half(0xDF00), __ushort_as_half(0xDF00));  // -448
+    const __half2 h = __hmax2(*reinterpret_cast<const __half2*>(&v), low);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void cp_async_4_zfill(uint32_t dst, const void* src, bool valid) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t at) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+// log2 of a scale's magnitude
+__device__ __forceinline__ float log2_fast(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(fabsf(x)));
+    return y;
+}
 __device__ __forceinline__ void prefetch_l2(const void* p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
-template <bool E4M3>
+template <int C>
 __device__ __forceinline__ void attn_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-    if (E4M3) {
+    if (in_8_bits(C)) {
         mma_f16_16816(d, a0, a1, a2, a3, b0, b1);
     } else {
         const uint32_t a[4] = {a0, a1, a2, a3};
@@ -108,18 +186,20 @@ __device__ __forceinline__ uint32_t tile_offset(int r, int c) {
     return static_cast<uint32_t>((r * CH + (c ^ f)) * 16);
 }
 
-template <bool E4M3, int DP, int NT>
+template <int C, int DP, int NT>
 struct AttnShape {
     static constexpr int kHeads = 8 * NT;
     static constexpr int kSteps = DP / 16;                     // 16-dim steps of a head
     // 16-byte chunks of a row in shared memory (six would not swizzle: eight)
-    static constexpr int kChunks = E4M3 && DP == 96 ? 8 : DP * (E4M3 ? 1 : 2) / 16;
+    static constexpr bool k8 = in_8_bits(C);
+    static constexpr int kChunks = k8 && DP == 96 ? 8 : DP * (k8 ? 1 : 2) / 16;
     static constexpr int kRowBytes = kChunks * 16;
-    static constexpr int kStageBytes = 2 * kTile * kRowBytes;  // keys, then values
+    static constexpr int kScales = 2 * kTile * kRowBytes;  // behind keys and values: the scales of the tile's tokens
+    static constexpr int kStageBytes = kScales + (by_group(C) ? 2 * kTile * 4 : 0);
     static constexpr int kPartFloats = kHeads * (DP + 2);
     // shares: one CTA an SM, of as many warps as its registers allow (the accumulators'
     // size decides) with rings of three stages or more
-    static constexpr int kShareWarps = 4 * (E4M3 ? (NT == 1 ? (DP == 64 ? 4 : DP <= 128 ? 3 : 2) : (DP == 64 ? 3 : 2))
+    static constexpr int kShareWarps = 4 * (k8 ? (NT == 1 ? (DP == 64 ? 4 : DP <= 128 ? 3 : 2) : (DP == 64 ? 3 : 2))
                                                  : (DP == 64 ? 3 : DP <= 128 ? 2 : 1));
     static constexpr int kFit = 226 * 1024 / (kShareWarps * kStageBytes);
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
@@ -137,94 +217,141 @@ struct AttnShape {
     static_assert(160 * kShareWarps <= most_workers(DP), "workspace");
 };
 
+// New tokens of a request.
+template <int C>
+__device__ __forceinline__ int new_tokens(const Args<C>& a) {
+    if constexpr (by_group(C)) return a.tokens;
+    else return 1;
+}
+
 // What one request looks like: its visible tokens [start, len), in tiles from
-// tile0 on.
+// tile0 on (visible to any of its new tokens).
 struct Request {
     int len, start, tile0, tiles;
 };
 
-__device__ __forceinline__ Request request_of(const AttentionArgs& a, int b, bool& bad) {
+template <int C>
+__device__ __forceinline__ Request request_of(const Args<C>& a, int b, bool& bad) {
     Request q;
     const int len = a.kv_len[b];
     bad |= len < 0 || len > a.most;
     q.len = min(max(len, 0), a.most);
-    q.start = a.window > 0 ? max(q.len - a.window, 0) : 0;
+    q.start = a.window > 0 ? max(q.len - (new_tokens<C>(a) - 1) - a.window, 0) : 0;
     q.tile0 = q.start / kTile;
     q.tiles = q.len > 0 ? (q.len - 1) / kTile + 1 - q.tile0 : 0;
     return q;
 }
 
-// Which heads row `row` of a request stands for.
+// Which heads row `row` of a request stands for.  With several new tokens these
+// are (token, query head) pairs, those of the first token first.
 struct Heads {
-    int hk, first, n;  // key/value head, first query head, how many
+    int hk, first, n;  // key/value head, first of the query heads that share it, how many
 };
-template <int HEADS>
-__device__ __forceinline__ Heads heads_of(const AttentionArgs& a, int row) {
-    const int G = a.q_heads / a.cache.heads, chunks = (G + HEADS - 1) / HEADS;
+template <int C, int HEADS>
+__device__ __forceinline__ Heads heads_of(const Args<C>& a, int row) {
+    const int G = a.q_heads / a.cache.heads * new_tokens<C>(a), chunks = (G + HEADS - 1) / HEADS;
     Heads h;
     h.hk = row / chunks;
     const int chunk = row - h.hk * chunks;
-    h.first = h.hk * G + chunk * HEADS;
+    h.first = chunk * HEADS;
     h.n = min(HEADS, G - chunk * HEADS);
     return h;
 }
-
-__device__ __forceinline__ void store_empty(const AttentionArgs& a, int b, int head, int heads, int thread, int threads) {
-    const int per = a.cache.dim / 8;
-    for (int i = thread; i < heads * per; i += threads) {
-        const int h = head + i / per, d = (i % per) * 8;
-        *reinterpret_cast<uint4*>(a.out + b * a.out_request + h * a.out_head + d) = make_uint4(0u, 0u, 0u, 0u);
+// The new token and the query head of a row's j-th.
+struct Column {
+    int token, head;
+};
+template <int C>
+__device__ __forceinline__ Column column_of(const Args<C>& a, const Heads& hd, int j) {
+    const int G = a.q_heads / a.cache.heads;
+    Column c{0, hd.first + j};
+    if constexpr (by_group(C)) {
+        c.token = c.head / G;
+        c.head -= c.token * G;
     }
+    c.head += hd.hk * G;
+    return c;
+}
+template <int C>
+__device__ __forceinline__ const uint16_t* query_of(const Args<C>& a, int b, const Heads& hd, int j) {
+    const Column c = column_of<C>(a, hd, j);
+    const uint16_t* q = a.q + b * a.q_request + c.head * a.q_head;
+    if constexpr (by_group(C)) q += c.token * a.q_token;
+    return q;
+}
+template <int C>
+__device__ __forceinline__ uint16_t* out_of(const Args<C>& a, int b, const Heads& hd, int j) {
+    const Column c = column_of<C>(a, hd, j);
+    uint16_t* out = a.out + b * a.out_request + c.head * a.out_head;
+    if constexpr (by_group(C)) out += c.token * a.out_token;
+    return out;
+}
+template <int C>
+__device__ __forceinline__ float* lse_at(const Args<C>& a, int b, const Heads& hd, int j) {
+    const Column c = column_of<C>(a, hd, j);
+    return a.lse + (static_cast<int64_t>(b) * new_tokens<C>(a) + c.token) * a.q_heads + c.head;
+}
+
+template <int C>
+__device__ __forceinline__ void store_empty(const Args<C>& a, int b, const Heads& hd, int thread, int threads) {
+    const int per = a.cache.dim / 8;
+    for (int i = thread; i < hd.n * per; i += threads)
+        *reinterpret_cast<uint4*>(out_of<C>(a, b, hd, i / per) + (i % per) * 8) = make_uint4(0u, 0u, 0u, 0u);
     if (a.lse)
-        for (int h = thread; h < heads; h += threads) a.lse[static_cast<int64_t>(b) * a.q_heads + head + h] = -INFINITY;
+        for (int j = thread; j < hd.n; j += threads) *lse_at<C>(a, b, hd, j) = -INFINITY;
 }
 
 // 16 dims of 8 heads from the accumulators (row r and r + 8 by columns 2c,
 // 2c + 1) times the heads' factors, transposed to dims along the lanes of a
 // head and stored; `out`: the row of head r's output, null for none.
-template <bool E4M3>
+template <int C>
 __device__ __forceinline__ void store_dims(const float4& o, float f0, float f1, uint16_t* out, int c) {
     const __nv_bfloat162 p0 = __floats2bfloat162_rn(o.x * f0, o.y * f1), p1 = __floats2bfloat162_rn(o.z * f0, o.w * f1);
     const uint32_t v0 = transpose_8x8(*reinterpret_cast<const uint32_t*>(&p0));
     const uint32_t v1 = transpose_8x8(*reinterpret_cast<const uint32_t*>(&p1));
     if (!out) return;
-    if (E4M3) {  // rows of the product: even dims, then odd ones
+    if (in_8_bits(C)) {  // rows of the product: even dims, then odd ones
         *reinterpret_cast<uint2*>(out + 4 * c) = make_uint2(__byte_perm(v0, v1, 0x5410), __byte_perm(v0, v1, 0x7632));
     } else {
         *reinterpret_cast<uint32_t*>(out + 2 * c) = v0;
         *reinterpret_cast<uint32_t*>(out + 8 + 2 * c) = v1;
     }
 }
-template <bool E4M3>
+template <int C>
 __device__ __forceinline__ float lse_of(float m, float l) {
-    return l != 0.f ? (m + (log2f(l) - (E4M3 ? kE4m3Bias : 0.f))) * 0.6931471805599453f : -INFINITY;
+    return l != 0.f ? (m + (log2f(l) - (C == kE4m3 ? kE4m3Bias : 0.f))) * 0.6931471805599453f : -INFINITY;
 }
 
 // The arithmetic of a warp on tiles of one row.  Lane 4 r + c.
-template <bool E4M3, int DP, int NT>
+template <int C, int DP, int NT>
 struct RowMath {
-    using Sh = AttnShape<E4M3, DP, NT>;
+    using Sh = AttnShape<C, DP, NT>;
     static constexpr int CH = Sh::kChunks, KS = Sh::kSteps;
     uint32_t qf[NT][KS][2];              // queries as B fragments (columns: heads)
     float sl[NT][2];                     // score scale of columns 2c, 2c + 1
     float m[NT][2], l[NT][2];            // of columns 2c, 2c + 1 (l: of this lane's tokens until reduced)
-    float4 o[NT][KS];                    // dims r, r + 8 (e4m3: 2r, 2r + 1) by columns 2c, 2c + 1
+    float4 o[NT][KS];                    // dims r, r + 8 (8 bits: 2r, 2r + 1) by columns 2c, 2c + 1
+    // with scales by group, where a value's weight is p times its scale: the largest weight
+    // (log2 units), by which o is scaled, and the tokens that the column sees, below
+    // upto, of them the last `window`
+    float big[NT][2];
+    int upto[NT][2];
 
     // requests the queries and clears the sums
-    __device__ __forceinline__ void begin(const AttentionArgs& a, int b, const Heads& hd, int lane) {
+    __device__ __forceinline__ void begin(const Args<C>& a, int b, const Heads& hd, int lane) {
         const int r = lane >> 2, c = lane & 3;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const uint16_t* qp = a.q + b * a.q_request + (hd.first + n * 8 + r) * a.q_head;
+            const uint16_t* qp = query_of<C>(a, b, hd, n * 8 + r);
             const bool have = n * 8 + r < hd.n;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 qf[n][k][0] = qf[n][k][1] = 0u;
                 if (have && k * 16 < a.cache.dim) {
-                    // bf16: dims 2c, 2c + 1 and 8 further; e4m3: the four dims whose codes one word holds
-                    const int d = k * 16 + (E4M3 ? 4 * c : 2 * c);
+                    // bf16: dims 2c, 2c + 1 and 8 further; 8 bits: the four dims whose codes one word holds
+                    const int d = k * 16 + (in_8_bits(C) ? 4 * c : 2 * c);
                     qf[n][k][0] = *reinterpret_cast<const uint32_t*>(qp + d);
-                    qf[n][k][1] = *reinterpret_cast<const uint32_t*>(qp + d + (E4M3 ? 2 : 8));
+                    qf[n][k][1] = *reinterpret_cast<const uint32_t*>(qp + d + (in_8_bits(C) ? 2 : 8));
                 }
                 o[n][k] = make_float4(0.f, 0.f, 0.f, 0.f);
             }
@@ -232,17 +359,22 @@ struct RowMath {
             for (int e = 0; e < 2; ++e) {
                 m[n][e] = -INFINITY;
                 l[n][e] = 0.f;
+                if constexpr (by_group(C)) {
+                    big[n][e] = -INFINITY;
+                    upto[n][e] = column_of<C>(a, hd, n * 8 + 2 * c + e).token + 1 - a.tokens;  // and its length: ready()
+                }
             }
         }
     }
 
     // makes the queries that begin() requested into operands
-    __device__ __forceinline__ void ready(const AttentionArgs& a, int hk, int lane) {
+    __device__ __forceinline__ void ready(const Args<C>& a, int hk, int len, int lane) {
         const int c = lane & 3;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            sl[n][0] = sl[n][1] = a.scale * 1.4426950408889634f * (E4M3 ? a.cache.k_scale[hk] : 1.f);
-            if (E4M3) {
+            sl[n][0] = sl[n][1] = a.scale * 1.4426950408889634f * (C == kE4m3 ? a.cache.k_scale[hk] : 1.f);
+            if (by_group(C)) upto[n][0] += len, upto[n][1] += len;
+            if (in_8_bits(C)) {
                 // to fp16, scaled by a power of two that takes the head's largest into [2^14, 2^15)
                 uint32_t big = 0u;
 #pragma unroll
@@ -267,8 +399,9 @@ struct RowMath {
         }
     }
 
-    // the tile at kt (shared address): keys, then values; mask: tokens that count
-    __device__ __forceinline__ void tile(uint32_t kt, uint32_t mask, int lane) {
+    // the tile at kt (shared address): keys, then values; mask: tokens that count; first:
+    // the number of its first token (scales by group only)
+    __device__ __forceinline__ void tile(const Args<C>& a, const Request& q, uint32_t kt, uint32_t mask, int first, int lane) {
         const uint32_t vt = kt + kTile * Sh::kRowBytes;
         const int r = lane >> 2;
         // two chains of products, where registers allow: the latency of one is a good part of a tile's
@@ -278,13 +411,13 @@ struct RowMath {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[n][e] = s1[n][e] = 0.f;
-        if (!E4M3) {
+        if (!in_8_bits(C)) {
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 uint32_t f[4];
                 ldmatrix_x4(f, kt + tile_offset<CH>(lane & 15, 2 * k + (lane >> 4)));
 #pragma unroll
-                for (int n = 0; n < NT; ++n) attn_mma<E4M3>(kTwo && (k & 1) ? s1[n] : s[n], f[0], f[1], f[2], f[3], qf[n][k][0], qf[n][k][1]);
+                for (int n = 0; n < NT; ++n) attn_mma<C>(kTwo && (k & 1) ? s1[n] : s[n], f[0], f[1], f[2], f[3], qf[n][k][0], qf[n][k][1]);
             }
         } else {
 #pragma unroll
@@ -293,22 +426,69 @@ struct RowMath {
                 ldmatrix_x4(f, kt + tile_offset<CH>(lane & 15, k + (lane >> 4)));
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const uint32_t a0 = e4m3x2_to_f16x2(f[2 * j]), a2 = e4m3x2_to_f16x2(f[2 * j] >> 16);
-                    const uint32_t a1 = e4m3x2_to_f16x2(f[2 * j + 1]), a3 = e4m3x2_to_f16x2(f[2 * j + 1] >> 16);
+                    uint32_t a0, a1, a2, a3;
+                    codes_to_f16<C>(f[2 * j], a0, a2);
+                    codes_to_f16<C>(f[2 * j + 1], a1, a3);
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
-                        attn_mma<E4M3>(kTwo && j ? s1[n] : s[n], a0, a1, a2, a3, qf[n][k + j][0], qf[n][k + j][1]);
+                        attn_mma<C>(kTwo && j ? s1[n] : s[n], a0, a1, a2, a3, qf[n][k + j][0], qf[n][k + j][1]);
                 }
+            }
+        }
+        // Scales by group: of keys r and r + 8, and of the values there in log2 units.
+        float ks[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
+        uint32_t sign[2] = {0u, 0u};
+        bool edge = false, one_scale = false, scrub = false;
+        if constexpr (by_group(C)) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                ks[i] = ld_shared_f32(kt + Sh::kScales + (r + 8 * i) * 4);
+                const float v = ld_shared_f32(kt + Sh::kScales + (kTile + r + 8 * i) * 4);
+                lv[i] = log2_fast(v);
+                sign[i] = __float_as_uint(v) & 0x80000000u;
+            }
+            one_scale = mask == 0xFFFFu && a.group % kTile == 0;
+            // tokens that some new ones see and others do not
+            edge = first + kTile > q.len - (a.tokens - 1) || (a.window > 0 && first < q.len - a.window);
+            if (C == kE4m3Groups && edge && a.tokens > 1) {
+                // a NaN among them stays with those that see it: their weight becomes NaN, and the
+                // code a number that the others' weight of 0 takes out
+                bool nan = false;
+#pragma unroll
+                for (int i = 0; i < KS / 2; ++i) {  // (the chunks that the products take: of 96 dims not all)
+                    const uint4 v = ld_shared_u4(vt + tile_offset<CH>(lane & 15, 2 * i + (lane >> 4)));
+                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) nan |= (((x[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u;
+                }
+                uint32_t who = __ballot_sync(0xFFFFFFFFu, nan);
+                who = (who | (who >> 16)) & 0xFFFFu;
+                scrub = who != 0u;
+                if ((who >> r) & 1u) lv[0] = NAN;
+                if ((who >> (r + 8)) & 1u) lv[1] = NAN;
+                one_scale = one_scale && !scrub;
             }
         }
         uint32_t pf[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][e] = (s[n][e] + s1[n][e]) * sl[n][e & 1];
+            for (int e = 0; e < 4; ++e) {
+                s[n][e] = (s[n][e] + s1[n][e]) * sl[n][e & 1];
+                if (by_group(C)) s[n][e] *= ks[e >> 1];
+            }
             if (mask != 0xFFFFu) {
                 if (!((mask >> r) & 1u)) s[n][0] = s[n][1] = -INFINITY;
                 if (!((mask >> (r + 8)) & 1u)) s[n][2] = s[n][3] = -INFINITY;
+            }
+            if constexpr (by_group(C)) {
+                if (edge) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int token = first + r + 8 * (e >> 1), end = upto[n][e & 1];
+                        if (token >= end || (a.window > 0 && token < end - a.window)) s[n][e] = -INFINITY;
+                    }
+                }
             }
             float top[2] = {fmaxf(s[n][0], s[n][2]), fmaxf(s[n][1], s[n][3])};
 #pragma unroll
@@ -316,15 +496,41 @@ struct RowMath {
                 top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 4));
                 top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 8));
                 top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 16));
-                top[e] = fmaxf(top[e], m[n][e]);
             }
-            if (__any_sync(0xFFFFFFFFu, top[0] > m[n][0] || top[1] > m[n][1])) {
+            // weights of the values: p times their scale, the largest of which o goes by.  (By the
+            // largest p instead, a token of large scale and small p would pass what fp16 holds.)
+            float w[4], heavy[2] = {-INFINITY, -INFINITY};
+            if constexpr (by_group(C)) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = s[n][e] == -INFINITY ? -INFINITY : s[n][e] + lv[e >> 1];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (one_scale) {
+                        heavy[e] = top[e] + lv[0];
+                    } else {
+                        heavy[e] = fmaxf(w[e], w[e + 2]);
+                        heavy[e] = fmaxf(heavy[e], __shfl_xor_sync(0xFFFFFFFFu, heavy[e], 4));
+                        heavy[e] = fmaxf(heavy[e], __shfl_xor_sync(0xFFFFFFFFu, heavy[e], 8));
+                        heavy[e] = fmaxf(heavy[e], __shfl_xor_sync(0xFFFFFFFFu, heavy[e], 16));
+                    }
+                    heavy[e] = fmaxf(heavy[e], big[n][e]);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) top[e] = fmaxf(top[e], m[n][e]);
+            bool grown = top[0] > m[n][0] || top[1] > m[n][1];
+            if (by_group(C)) grown |= heavy[0] > big[n][0] || heavy[1] > big[n][1];
+            if (__any_sync(0xFFFFFFFFu, grown)) {
                 float keep[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     keep[e] = part_factor(m[n][e], top[e]);  // from -infinity: 0
                     m[n][e] = top[e];
                     l[n][e] *= keep[e];
+                    if (by_group(C)) {
+                        keep[e] = part_factor(big[n][e], heavy[e]);
+                        big[n][e] = heavy[e];
+                    }
                 }
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
@@ -337,8 +543,12 @@ struct RowMath {
                 // the bias after the difference: m - 15 is not a float where m passes 2^24, and
                 // the largest p would then be 2^16, which no fp16 holds
                 s[n][e] -= m[n][e & 1] == -INFINITY ? 0.f : m[n][e & 1];
-                s[n][e] = exp2_fast(E4M3 ? s[n][e] + kE4m3Bias : s[n][e]);
+                s[n][e] = exp2_fast(C == kE4m3 ? s[n][e] + kE4m3Bias : s[n][e]);
                 l[n][e & 1] += s[n][e];
+                if (by_group(C)) {
+                    w[e] -= big[n][e & 1] == -INFINITY ? 0.f : big[n][e & 1];
+                    s[n][e] = __uint_as_float(__float_as_uint(exp2_fast(w[e] + kE4m3Bias)) ^ sign[e >> 1]);
+                }
             }
             // to 16 bits for the second product, whose operands are of one type: that of the
             // values.  fp16 rounds p by 2^-11 of it, bf16 by 2^-8, about as much as the result's
@@ -347,7 +557,7 @@ struct RowMath {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 uint32_t v;
-                if (E4M3) {
+                if (in_8_bits(C)) {
                     const __half2 h = __floats2half2_rn(s[n][2 * e], s[n][2 * e + 1]);
                     v = *reinterpret_cast<const uint32_t*>(&h);
                 } else {
@@ -359,10 +569,10 @@ struct RowMath {
         }
         auto add = [&](int n, int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
             float d[4] = {o[n][k].x, o[n][k].y, o[n][k].z, o[n][k].w};
-            attn_mma<E4M3>(d, a0, a1, a2, a3, pf[n][0], pf[n][1]);
+            attn_mma<C>(d, a0, a1, a2, a3, pf[n][0], pf[n][1]);
             o[n][k] = make_float4(d[0], d[1], d[2], d[3]);
         };
-        if (!E4M3) {
+        if (!in_8_bits(C)) {
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 uint32_t f[4];
@@ -378,10 +588,10 @@ struct RowMath {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     // word: dims 2r, 2r + 1 of token 2c, then of token 2c + 1
-                    const uint32_t x0 = e4m3x2_to_f16x2(f[2 * j]), x1 = e4m3x2_to_f16x2(f[2 * j] >> 16);
-                    const uint32_t y0 = e4m3x2_to_f16x2(f[2 * j + 1]), y1 = e4m3x2_to_f16x2(f[2 * j + 1] >> 16);
-                    const uint32_t a0 = __byte_perm(x0, x1, 0x5410), a1 = __byte_perm(x0, x1, 0x7632);
-                    const uint32_t a2 = __byte_perm(y0, y1, 0x5410), a3 = __byte_perm(y0, y1, 0x7632);
+                    uint32_t a0, a1, a2, a3;
+                    codes_to_f16_by_dim<C>(f[2 * j], a0, a1);
+                    codes_to_f16_by_dim<C>(f[2 * j + 1], a2, a3);
+                    if (C == kE4m3Groups && scrub) a0 = as_numbers(a0), a1 = as_numbers(a1), a2 = as_numbers(a2), a3 = as_numbers(a3);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) add(n, k + j, a0, a1, a2, a3);
                 }
@@ -398,12 +608,27 @@ struct RowMath {
                 l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 8);
                 l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 16);
             }
+        if constexpr (by_group(C)) {
+            // o by the largest p like l, in two steps: a float's range may not hold the factor
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float f[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    f[e] = big[n][e] == -INFINITY ? 0.f : exp2_fast(0.5f * (big[n][e] - kE4m3Bias - m[n][e]));
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    o[n][k].x = o[n][k].x * f[0] * f[0], o[n][k].y = o[n][k].y * f[1] * f[1];
+                    o[n][k].z = o[n][k].z * f[0] * f[0], o[n][k].w = o[n][k].w * f[1] * f[1];
+                }
+            }
+        }
     }
 
     // the row's result, all of its tokens seen (after reduce())
-    __device__ __forceinline__ void finish(const AttentionArgs& a, int b, const Heads& hd, int lane) {
+    __device__ __forceinline__ void finish(const Args<C>& a, int b, const Heads& hd, int lane) {
         const int r = lane >> 2, c = lane & 3;
-        const float vs = E4M3 ? a.cache.v_scale[hd.hk] : 1.f;
+        const float vs = C == kE4m3 ? a.cache.v_scale[hd.hk] : 1.f;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float f[2];
@@ -411,14 +636,13 @@ struct RowMath {
             for (int e = 0; e < 2; ++e) {
                 f[e] = l[n][e] != 0.f ? vs / l[n][e] : 0.f;
                 const int h = n * 8 + 2 * c + e;
-                if (a.lse && r == 0 && h < hd.n)
-                    a.lse[static_cast<int64_t>(b) * a.q_heads + hd.first + h] = lse_of<E4M3>(m[n][e], l[n][e]);
+                if (a.lse && r == 0 && h < hd.n) *lse_at<C>(a, b, hd, h) = lse_of<C>(m[n][e], l[n][e]);
             }
-            uint16_t* out = a.out + b * a.out_request + (hd.first + n * 8 + r) * a.out_head;
+            uint16_t* out = out_of<C>(a, b, hd, n * 8 + r);
             const bool have = n * 8 + r < hd.n;
 #pragma unroll
             for (int k = 0; k < KS; ++k)
-                store_dims<E4M3>(o[n][k], f[0], f[1], have && k * 16 < a.cache.dim ? out + k * 16 : nullptr, c);
+                store_dims<C>(o[n][k], f[0], f[1], have && k * 16 < a.cache.dim ? out + k * 16 : nullptr, c);
         }
     }
 
@@ -440,16 +664,16 @@ struct RowMath {
 // early: where a tile lies in one block, those of 32 tiles at once (lane i:
 // tile base + i * step), else those of one tile's tokens (lanes i and i + 16:
 // token i).
-template <bool E4M3, int DP, int NT>
+template <int C, int DP, int NT>
 struct TileCopy {
-    using Sh = AttnShape<E4M3, DP, NT>;
-    static constexpr int CH = Sh::kChunks, kBytes = E4M3 ? 1 : 2;
+    using Sh = AttnShape<C, DP, NT>;
+    static constexpr int CH = Sh::kChunks, kBytes = in_8_bits(C) ? 1 : 2;
     int base, id, place;
 
-    static __device__ __forceinline__ bool aligned(const AttentionArgs& a) { return a.cache.page % kTile == 0; }
+    static __device__ __forceinline__ bool aligned(const Args<C>& a) { return a.cache.page % kTile == 0; }
 
     // the ids for tile t (tiles of the row step apart, below t1)
-    __device__ __forceinline__ void look_up(const AttentionArgs& a, int b, const Request& q, int t, int t1, int step, int lane) {
+    __device__ __forceinline__ void look_up(const Args<C>& a, int b, const Request& q, int t, int t1, int step, int lane) {
         base = t;
         const bool whole = aligned(a);
         const int tile = whole ? t + lane * step : t;
@@ -463,12 +687,22 @@ struct TileCopy {
         }
     }
     // whether look_up has to come before copy(t)
-    __device__ __forceinline__ bool wants(const AttentionArgs& a, int t, int step) const {
+    __device__ __forceinline__ bool wants(const Args<C>& a, int t, int step) const {
         return aligned(a) ? t - base >= 32 * step : t != base;
     }
 
+    // the scales of this lane's token, of its key (lanes 0..15) or value
+    __device__ __forceinline__ void copy_scales(const Args<C>& a, int hk, int64_t block, int in, bool valid, uint32_t dst, int lane) const {
+        if constexpr (by_group(C)) {
+            const int64_t of = a.magic ? static_cast<int>(__umulhi(in, a.magic)) : in;
+            const float* at = lane < 16 ? a.k_scale + block * a.ks_block + of * a.ks_group + hk * a.ks_head
+                                        : a.v_scale + block * a.vs_block + of * a.vs_group + hk * a.vs_head;
+            cp_async_4_zfill(dst + Sh::kScales + lane * 4, at, valid);
+        }
+    }
+
     // starts the copies of tile t into dst; returns the mask of the tokens the row sees
-    __device__ __forceinline__ uint32_t copy(const AttentionArgs& a, int hk, const Request& q, int t, int step, uint32_t dst, int lane,
+    __device__ __forceinline__ uint32_t copy(const Args<C>& a, int hk, const Request& q, int t, int step, uint32_t dst, int lane,
                                              bool& bad) const {
         const int real_chunks = a.cache.dim * kBytes / 16;
         const char* kp = static_cast<const char*>(a.cache.k) + hk * a.cache.k_head * kBytes;
@@ -486,6 +720,7 @@ struct TileCopy {
                 mask = 0u;
                 block = 0;
             }
+            if constexpr (by_group(C)) copy_scales(a, hk, block, first + (lane & 15), (mask >> (lane & 15)) & 1u, dst, lane);
             kp += (block * a.cache.k_block + first * a.cache.k_token) * kBytes;
             vp += (block * a.cache.v_block + first * a.cache.v_token) * kBytes;
             const int64_t ks = a.cache.k_token * kBytes, vs = a.cache.v_token * kBytes;
@@ -504,6 +739,7 @@ struct TileCopy {
             bad |= id != -1 && !valid;
             mask = __ballot_sync(0xFFFFFFFFu, valid) & 0xFFFFu;
             const int64_t block = valid ? id : 0, first = valid ? place : 0;
+            if constexpr (by_group(C)) copy_scales(a, hk, block, static_cast<int>(first), valid, dst, lane);
             const int64_t ko = (block * a.cache.k_block + first * a.cache.k_token) * kBytes;
             const int64_t vo = (block * a.cache.v_block + first * a.cache.v_token) * kBytes;
 #pragma unroll
@@ -534,10 +770,10 @@ struct Segment {
     Request q;
 };
 
-template <bool E4M3, int DP, int NT>
-__global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kShareWarps * 32), 1)
-    k_attention_shares(const AttentionArgs a, const JoinPlan jp) {
-    using Sh = AttnShape<E4M3, DP, NT>;
+template <int C, int DP, int NT>
+__global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
+    k_attention_shares(const Args<C> a, const JoinPlan jp) {
+    using Sh = AttnShape<C, DP, NT>;
     constexpr int S = Sh::kStages, HEADS = Sh::kHeads, W = Sh::kShareWarps;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t tile_mask[W][S];
@@ -565,7 +801,7 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kShareWarps * 32), 1
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int b = base + lane * kPer + i;
-            const int n = b < a.B ? request_of(a, b, bad).tiles : 0;
+            const int n = b < a.B ? request_of<C>(a, b, bad).tiles : 0;
             cost[i] = n ? (n + kRowCost) * rows : 0;
             own += cost[i];
         }
@@ -584,7 +820,7 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kShareWarps * 32), 1
     } else {
 #pragma unroll 8
         for (int b = lane; b < a.B; b += 32) {
-            const int n = request_of(a, b, bad).tiles;
+            const int n = request_of<C>(a, b, bad).tiles;
             total += n ? (n + kRowCost) * rows : 0;
         }
 #pragma unroll
@@ -592,8 +828,12 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kShareWarps * 32), 1
     }
     // requests without tokens
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        if (request_of(a, b, bad).tiles > 0) continue;
-        store_empty(a, b, 0, a.q_heads, threadIdx.x, W * 32);
+        if (request_of<C>(a, b, bad).tiles > 0) continue;
+        if (by_group(C)) {
+            for (int row = 0; row < rows; ++row) store_empty<C>(a, b, heads_of<C, HEADS>(a, row), threadIdx.x, W * 32);
+        } else {
+            store_empty<C>(a, b, Heads{0, 0, a.q_heads}, threadIdx.x, W * 32);
+        }
         if (jp.by_row)
             for (int i = threadIdx.x; i < rows; i += W * 32) jp.joins[b * rows + i] = make_int4(-1, 0, 0, 0);
     }
@@ -653,7 +893,7 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kShareWarps * 32), 1
             s.row = 0;
             do {
                 if (++s.b >= a.B) return false;
-                s.q = request_of(a, s.b, bad);
+                s.q = request_of<C>(a, s.b, bad);
             } while (s.q.tiles == 0);
         }
         open_segment(s);
@@ -662,7 +902,7 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kShareWarps * 32), 1
     Segment seg{};
     bool live = u1 > u0 && locate(u0, seg.b, seg.at);
     if (live) {
-        seg.q = request_of(a, seg.b, bad);
+        seg.q = request_of<C>(a, seg.b, bad);
         seg.row = static_cast<unsigned>(u0 - seg.at) / static_cast<unsigned>(seg.q.tiles + kRowCost);
         seg.at += seg.row * (seg.q.tiles + kRowCost);
         open_segment(seg);
@@ -671,10 +911,10 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kShareWarps * 32), 1
 
     // The copies run ahead of the products: `ahead` is the segment of the next
     // tile to copy, ahead_t the tile.
-    RowMath<E4M3, DP, NT> math;
-    TileCopy<E4M3, DP, NT> copy;
+    RowMath<C, DP, NT> math;
+    TileCopy<C, DP, NT> copy;
     Segment ahead = seg;
-    int ahead_t = seg.t0, ahead_hk = heads_of<HEADS>(a, seg.row).hk;
+    int ahead_t = seg.t0, ahead_hk = heads_of<C, HEADS>(a, seg.row).hk;
     bool more = live;
     if (more) copy.look_up(a, ahead.b, ahead.q, ahead_t, ahead.t1, 1, lane);
     // One step of the loop copies a tile and, once the ring is full, works on
@@ -686,16 +926,16 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kShareWarps * 32), 1
         if (fresh) {
             // the queries are requested before the tiles, which they would queue behind
             fresh = false;
-            hd = heads_of<HEADS>(a, seg.row);
+            hd = heads_of<C, HEADS>(a, seg.row);
             math.begin(a, seg.b, hd, lane);
             // and those of the row after this one brought to L2
             const int after_b = seg.row + 1 < rows ? seg.b : seg.b + 1;
             if (after_b < a.B) {
-                const Heads h = heads_of<HEADS>(a, seg.row + 1 < rows ? seg.row + 1 : 0);
+                const Heads h = heads_of<C, HEADS>(a, seg.row + 1 < rows ? seg.row + 1 : 0);
                 constexpr int kLines = (DP + 63) / 64;
                 for (int i = lane; i < h.n * kLines; i += 32)
                     if ((i % kLines) * 64 < a.cache.dim)
-                        prefetch_l2(a.q + after_b * a.q_request + (h.first + i / kLines) * a.q_head + (i % kLines) * 64);
+                        prefetch_l2(query_of<C>(a, after_b, h, i / kLines) + (i % kLines) * 64);
             }
         }
         const bool full = primed == S - 1;
@@ -708,7 +948,7 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kShareWarps * 32), 1
             if (++ahead_t >= ahead.t1) {
                 more = look = next_segment(ahead);
                 ahead_t = ahead.t0;
-                ahead_hk = heads_of<HEADS>(a, ahead.row).hk;
+                ahead_hk = heads_of<C, HEADS>(a, ahead.row).hk;
             }
             if (more && (look || copy.wants(a, ahead_t, 1))) copy.look_up(a, ahead.b, ahead.q, ahead_t, ahead.t1, 1, lane);
         }
@@ -718,8 +958,8 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kShareWarps * 32), 1
             ++primed;
             continue;
         }
-        if (t == seg.t0) math.ready(a, hd.hk, lane);
-        math.tile(ring + slot * Sh::kStageBytes, tile_mask[warp][slot], lane);
+        if (t == seg.t0) math.ready(a, hd.hk, seg.q.len, lane);
+        math.tile(a, seg.q, ring + slot * Sh::kStageBytes, tile_mask[warp][slot], (seg.q.tile0 + t) * kTile, lane);
         slot = slot + 1 == S ? 0 : slot + 1;
         if (++t < seg.t1) continue;
 
@@ -760,9 +1000,9 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t at) {
     return v;
 }
 
-template <bool E4M3>
-__device__ __forceinline__ void store_lse(const AttentionArgs& a, int b, const Heads& hd, int h, float m, float l) {
-    if (a.lse && h < hd.n) a.lse[static_cast<int64_t>(b) * a.q_heads + hd.first + h] = lse_of<E4M3>(m, l);
+template <int C>
+__device__ __forceinline__ void store_lse(const Args<C>& a, int b, const Heads& hd, int h, float m, float l) {
+    if (a.lse && h < hd.n) *lse_at<C>(a, b, hd, h) = lse_of<C>(m, l);
 }
 
 // The factors of up to eight parts of a head, one lane each (lanes 8 h .. 8 h + 7
@@ -808,17 +1048,16 @@ struct DimPart {
         o.z = o.z * f0[0] + x.z * f1[0], o.w = o.w * f0[1] + x.w * f1[1];
     }
     // the result: dims of step k, heads of block n
-    template <bool E4M3>
-    __device__ __forceinline__ void finish(const AttentionArgs& a, int b, const Heads& hd, int n, int k, int lane) const {
+    template <int C>
+    __device__ __forceinline__ void finish(const Args<C>& a, int b, const Heads& hd, int n, int k, int lane) const {
         const int r = lane >> 2, c = lane & 3;
-        const float vs = E4M3 ? a.cache.v_scale[hd.hk] : 1.f;
+        const float vs = C == kE4m3 ? a.cache.v_scale[hd.hk] : 1.f;
         const float f0 = l[0] != 0.f ? vs / l[0] : 0.f, f1 = l[1] != 0.f ? vs / l[1] : 0.f;
         const bool have = n * 8 + r < hd.n && k * 16 < a.cache.dim;
-        uint16_t* out = a.out + b * a.out_request + (hd.first + n * 8 + r) * a.out_head + k * 16;
-        store_dims<E4M3>(o, f0, f1, have ? out : nullptr, c);
+        store_dims<C>(o, f0, f1, have ? out_of<C>(a, b, hd, n * 8 + r) + k * 16 : nullptr, c);
         if (k == 0 && r == 0) {
-            store_lse<E4M3>(a, b, hd, n * 8 + 2 * c, m[0], l[0]);
-            store_lse<E4M3>(a, b, hd, n * 8 + 2 * c + 1, m[1], l[1]);
+            store_lse<C>(a, b, hd, n * 8 + 2 * c, m[0], l[0]);
+            store_lse<C>(a, b, hd, n * 8 + 2 * c + 1, m[1], l[1]);
         }
     }
 };
@@ -829,9 +1068,9 @@ struct DimPart {
 constexpr int kJoinThreads = 512;  // at most
 constexpr int kJoinDepth = 3;  // parts a thread requests together
 
-template <bool E4M3, int DP, int NT>
-__global__ void __launch_bounds__(kJoinThreads) k_attention_join(const AttentionArgs a, const JoinPlan jp) {
-    using Sh = AttnShape<E4M3, DP, NT>;
+template <int C, int DP, int NT>
+__global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Args<C> a, const JoinPlan jp) {
+    using Sh = AttnShape<C, DP, NT>;
     constexpr int HEADS = Sh::kHeads, KS = Sh::kSteps;
     __shared__ DimPart sums[kJoinThreads / 2];
     grid_dependents_launch();
@@ -874,16 +1113,16 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Attention
         __syncthreads();
     }
     if (threadIdx.y > 0) return;
-    s.finish<E4M3>(a, d.x, heads_of<HEADS>(a, d.y), n, k, lane);
+    s.finish<C>(a, d.x, heads_of<C, HEADS>(a, d.y), n, k, lane);
 }
 
 // kRowWarps / wpr rows per CTA, wpr warps for each; or (cluster > 1, wpr =
 // kRowWarps) a row per cluster.  Tiles go round the CTAs of a row, then their
 // warps.
-template <bool E4M3, int DP, int NT>
-__global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kRowWarps * 32), 1)
-    k_attention_rows(const AttentionArgs a, const int rows, const int wpr, const int cluster) {
-    using Sh = AttnShape<E4M3, DP, NT>;
+template <int C, int DP, int NT>
+__global__ void __launch_bounds__((AttnShape<C, DP, NT>::kRowWarps * 32), 1)
+    k_attention_rows(const Args<C> a, const int rows, const int wpr, const int cluster) {
+    using Sh = AttnShape<C, DP, NT>;
     constexpr int S = Sh::kRowStages, HEADS = Sh::kHeads, KS = Sh::kSteps, W = Sh::kRowWarps;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint32_t tile_mask[W][S];
@@ -900,21 +1139,21 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kRowWarps * 32), 1)
         clear_ring(smem, Sh::kRowSmem, threadIdx.x, W * 32);
         __syncthreads();
     }
-    const Heads hd = b < a.B ? heads_of<HEADS>(a, row) : Heads{};
+    const Heads hd = b < a.B ? heads_of<C, HEADS>(a, row) : Heads{};
     grid_dependency_wait();
     grid_dependents_launch();
     // Queries, block ids (where they do not depend on the length) and length are
     // requested together.
-    RowMath<E4M3, DP, NT> math;
-    TileCopy<E4M3, DP, NT> copy;
+    RowMath<C, DP, NT> math;
+    TileCopy<C, DP, NT> copy;
     Request q{};
     if (b < a.B) {
-        const bool early = a.window == 0 && TileCopy<E4M3, DP, NT>::aligned(a);
+        const bool early = a.window == 0 && TileCopy<C, DP, NT>::aligned(a);
         if (early) copy.look_up(a, b, q, first_tile, (a.most + kTile - 1) / kTile, step, lane);
         math.begin(a, b, hd, lane);
-        q = request_of(a, b, bad);
+        q = request_of<C>(a, b, bad);
         if (!early) copy.look_up(a, b, q, first_tile, q.tiles, step, lane);
-        if (q.tiles == 0 && rank == 0) store_empty(a, b, hd.first, hd.n, wir * 32 + lane, wpr * 32);
+        if (q.tiles == 0 && rank == 0) store_empty<C>(a, b, hd, wir * 32 + lane, wpr * 32);
     }
     if (first_tile < q.tiles) {
         int ahead = first_tile, put = 0, slot = 0, primed = 0;
@@ -934,8 +1173,8 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kRowWarps * 32), 1)
                 ++primed;
                 continue;
             }
-            if (t == first_tile) math.ready(a, hd.hk, lane);
-            math.tile(ring + slot * Sh::kStageBytes, tile_mask[warp][slot], lane);
+            if (t == first_tile) math.ready(a, hd.hk, q.len, lane);
+            math.tile(a, q, ring + slot * Sh::kStageBytes, tile_mask[warp][slot], (q.tile0 + t) * kTile, lane);
             slot = slot + 1 == S ? 0 : slot + 1;
             t += step;
         }
@@ -954,7 +1193,7 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kRowWarps * 32), 1)
     const bool joins = q.tiles > 1;
     const int used = min((q.tiles - rank + cluster - 1) / cluster, wpr);  // warps here that had a tile (at most 0: none)
     const int r = lane >> 2, c = lane & 3;
-    const float vs = E4M3 && joins ? a.cache.v_scale[hd.hk] : 1.f;
+    const float vs = C == kE4m3 && joins ? a.cache.v_scale[hd.hk] : 1.f;
     float4* const cta_part = reinterpret_cast<float4*>(smem + Sh::kPartBytes);
     if (joins)
         for (int x = wir * 32 + lane; x < HEADS * 8; x += wpr * 32) {
@@ -965,7 +1204,7 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kRowWarps * 32), 1)
             if (i < wpr) part_f[warp0 + i][h] = f;
             if (i == 0) {
                 if (cluster == 1) {
-                    store_lse<E4M3>(a, b, hd, h, m, l);
+                    store_lse<C>(a, b, hd, h, m, l);
                     part_l[warp0][h] = l != 0.f ? vs / l : 0.f;  // now the result's factor
                 } else {
                     cta_m[h] = m, cta_l[h] = l;
@@ -984,8 +1223,7 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kRowWarps * 32), 1)
                        *reinterpret_cast<const float2*>(&part_f[warp0 + i][h]));
         if (cluster == 1) {
             const float2 f = *reinterpret_cast<const float2*>(&part_l[warp0][h]);
-            uint16_t* out = a.out + b * a.out_request + (hd.first + n * 8 + r) * a.out_head + k * 16;
-            store_dims<E4M3>(o, f.x, f.y, n * 8 + r < hd.n && k * 16 < a.cache.dim ? out : nullptr, c);
+            store_dims<C>(o, f.x, f.y, n * 8 + r < hd.n && k * 16 < a.cache.dim ? out_of<C>(a, b, hd, n * 8 + r) + k * 16 : nullptr, c);
         } else {
             cta_part[u * 32 + lane] = o;
         }
@@ -998,7 +1236,7 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kRowWarps * 32), 1)
         if (i < cluster) m = ld_cluster_f32(cluster_address(&cta_m[h], i)), l = ld_cluster_f32(cluster_address(&cta_l[h], i));
         cta_f[i][h] = join_factor(m, l);
         if (i == 0) {
-            if (rank == 0) store_lse<E4M3>(a, b, hd, h, m, l);
+            if (rank == 0) store_lse<C>(a, b, hd, h, m, l);
             part_l[0][h] = l != 0.f ? vs / l : 0.f;
         }
     }
@@ -1011,8 +1249,7 @@ __global__ void __launch_bounds__((AttnShape<E4M3, DP, NT>::kRowWarps * 32), 1)
         for (int i = 0; i < cluster; ++i)
             add_scaled(o, ld_cluster_f32x4(cluster_address(cta_part + u * 32 + lane, i)), *reinterpret_cast<const float2*>(&cta_f[i][h]));
         const float2 f = *reinterpret_cast<const float2*>(&part_l[0][h]);
-        uint16_t* out = a.out + b * a.out_request + (hd.first + n * 8 + r) * a.out_head + k * 16;
-        store_dims<E4M3>(o, f.x, f.y, n * 8 + r < hd.n && k * 16 < a.cache.dim ? out : nullptr, c);
+        store_dims<C>(o, f.x, f.y, n * 8 + r < hd.n && k * 16 < a.cache.dim ? out_of<C>(a, b, hd, n * 8 + r) + k * 16 : nullptr, c);
     }
     cluster_barrier();  // nobody leaves while its part may be read
 }
@@ -1047,13 +1284,15 @@ cudaError_t launch_kernel(void (*kernel)(Params...), bool early, int cluster, di
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <bool E4M3, int DP, int NT>
-cudaError_t launch_attention_shape(const AttentionArgs& all, const DeviceInfo& dev, JoinPlan jp, cudaStream_t s) {
-    using Sh = AttnShape<E4M3, DP, NT>;
-    AttentionArgs a = all;
-    jp.rows = rows_of_request(a.q_heads, a.cache.heads, Sh::kHeads);
+template <int C, int DP, int NT>
+cudaError_t launch_attention_shape(const Args<C>& all, const DeviceInfo& dev, JoinPlan jp, cudaStream_t s) {
+    using Sh = AttnShape<C, DP, NT>;
+    Args<C> a = all;
+    int tokens = 1;
+    if constexpr (by_group(C)) tokens = a.tokens;
+    jp.rows = rows_of_request(a.q_heads * tokens, a.cache.heads, Sh::kHeads);
     int64_t all_rows = static_cast<int64_t>(a.B) * jp.rows;
-    const int tiles = most_tiles(a.most, a.window);  // of a row
+    const int tiles = most_tiles(a.most, a.window > 0 ? a.window + tokens - 1 : 0);  // of a row
     // short rows: as many warps for each as one wave of CTAs has, if that leaves
     // a warp few tiles
     {
@@ -1063,12 +1302,12 @@ cudaError_t launch_attention_shape(const AttentionArgs& all, const DeviceInfo& d
         // (19 tiles of 8 rows: 6.2 us with a CTA each, 6.9 with two, 5.9 with four)
         if (Sh::kClusters && wpr == W && tiles > kRowEnough * W)
             while (cluster < 8 && tiles > W * cluster && all_rows * cluster * 2 <= dev.sms) cluster *= 2;
-        while (cluster > 1 && max_active_clusters(reinterpret_cast<const void*>(k_attention_rows<E4M3, DP, NT>), W * 32,
+        while (cluster > 1 && max_active_clusters(reinterpret_cast<const void*>(k_attention_rows<C, DP, NT>), W * 32,
                                                   Sh::kRowSmem, cluster) < all_rows)
             cluster /= 2;
         const int64_t grid = cluster > 1 ? all_rows * cluster : (all_rows * wpr + W - 1) / W;
         if (tiles <= kRowTiles * wpr * cluster)
-            return launch_kernel(k_attention_rows<E4M3, DP, NT>, true, cluster, dim3(static_cast<unsigned>(grid)), dim3(W * 32),
+            return launch_kernel(k_attention_rows<C, DP, NT>, true, cluster, dim3(static_cast<unsigned>(grid)), dim3(W * 32),
                                  Sh::kRowSmem, s, a, jp.rows, wpr, cluster);
     }
     const int ctas = std::min(dev.sms, most_workers(DP) / Sh::kShareWarps);
@@ -1079,13 +1318,13 @@ cudaError_t launch_attention_shape(const AttentionArgs& all, const DeviceInfo& d
         a.B = static_cast<int>(std::min<int64_t>(all.B - from, fit));
         a.q = all.q + from * a.q_request, a.out = all.out + from * a.out_request;
         a.block_table = all.block_table + from * a.table_stride, a.kv_len = all.kv_len + from;
-        a.lse = all.lse ? all.lse + static_cast<int64_t>(from) * a.q_heads : nullptr;
+        a.lse = all.lse ? all.lse + static_cast<int64_t>(from) * tokens * a.q_heads : nullptr;
         all_rows = static_cast<int64_t>(a.B) * jp.rows;
         jp.by_row = all_rows <= jp.warps;
         // (early, because a CTA has an SM for itself: several smaller ones that are placed
         // around others leave holes in the register file, and those that no longer fit then
         // run when the rest are done -- 20 key/value heads of 64 dims, 24 requests: 26 us)
-        cudaError_t e = launch_kernel(k_attention_shares<E4M3, DP, NT>, true, 1, dim3(ctas), dim3(Sh::kShareWarps * 32), Sh::kSmem,
+        cudaError_t e = launch_kernel(k_attention_shares<C, DP, NT>, true, 1, dim3(ctas), dim3(Sh::kShareWarps * 32), Sh::kSmem,
                                       s, a, jp);
         if (e != cudaSuccess) return e;
         // few rows: their accumulators over several CTAs, down to a warp's; as many
@@ -1096,26 +1335,28 @@ cudaError_t launch_attention_shape(const AttentionArgs& all, const DeviceInfo& d
         const int parts = jp.warps / places + 2;
         int groups = 1;
         while (groups * width < kJoinThreads && groups * kJoinDepth < parts) groups *= 2;
-        e = launch_kernel(k_attention_join<E4M3, DP, NT>, true, 1, dim3(places, units / width), dim3(width, groups), 0, s, a, jp);
+        e = launch_kernel(k_attention_join<C, DP, NT>, true, 1, dim3(places, units / width), dim3(width, groups), 0, s, a, jp);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
 
-template <bool E4M3>
-cudaError_t launch_attention_type(const AttentionArgs& a, const DeviceInfo& dev, const JoinPlan& jp, cudaStream_t s) {
-    const bool wide = a.q_heads / a.cache.heads > 8;
+template <int C>
+cudaError_t launch_attention_type(const Args<C>& a, const DeviceInfo& dev, const JoinPlan& jp, cudaStream_t s) {
+    int tokens = 1;
+    if constexpr (by_group(C)) tokens = a.tokens;
+    const bool wide = a.q_heads / a.cache.heads * tokens > 8;
     // 16 heads of 256 dims fill a warp's registers: two rows of 8 are faster while the second
     // finds the cache in L2 (8 requests, windows of 4096: 15.4 us against 18.0; 134 MB over
     // e4m3 50 against 58; but 1.07 GB of bf16 328 against 216)
     const int64_t visible = a.window > 0 && a.window < a.most ? a.window : a.most;
-    const bool in_l2 = static_cast<double>(a.B) * visible * a.cache.heads * a.cache.dim * (E4M3 ? 2 : 4) <= (1 << 27);
+    const bool in_l2 = static_cast<double>(a.B) * visible * a.cache.heads * a.cache.dim * (in_8_bits(C) ? 2 : 4) <= (1 << 27);
     switch (padded_dim(a.cache.dim)) {
-        case 64: return wide ? launch_attention_shape<E4M3, 64, 2>(a, dev, jp, s) : launch_attention_shape<E4M3, 64, 1>(a, dev, jp, s);
-        case 96: return wide ? launch_attention_shape<E4M3, 96, 2>(a, dev, jp, s) : launch_attention_shape<E4M3, 96, 1>(a, dev, jp, s);
-        case 128: return wide ? launch_attention_shape<E4M3, 128, 2>(a, dev, jp, s) : launch_attention_shape<E4M3, 128, 1>(a, dev, jp, s);
-        case 192: return wide ? launch_attention_shape<E4M3, 192, 2>(a, dev, jp, s) : launch_attention_shape<E4M3, 192, 1>(a, dev, jp, s);
-        default: return wide && !in_l2 ? launch_attention_shape<E4M3, 256, 2>(a, dev, jp, s) : launch_attention_shape<E4M3, 256, 1>(a, dev, jp, s);
+        case 64: return wide ? launch_attention_shape<C, 64, 2>(a, dev, jp, s) : launch_attention_shape<C, 64, 1>(a, dev, jp, s);
+        case 96: return wide ? launch_attention_shape<C, 96, 2>(a, dev, jp, s) : launch_attention_shape<C, 96, 1>(a, dev, jp, s);
+        case 128: return wide ? launch_attention_shape<C, 128, 2>(a, dev, jp, s) : launch_attention_shape<C, 128, 1>(a, dev, jp, s);
+        case 192: return wide ? launch_attention_shape<C, 192, 2>(a, dev, jp, s) : launch_attention_shape<C, 192, 1>(a, dev, jp, s);
+        default: return wide && !in_l2 ? launch_attention_shape<C, 256, 2>(a, dev, jp, s) : launch_attention_shape<C, 256, 1>(a, dev, jp, s);
     }
 }
 

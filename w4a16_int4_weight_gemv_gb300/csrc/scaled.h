@@ -1,0 +1,72 @@
+// Host-side launcher interface of the operators over a w4a16_scaled_cache
+// (append that finds the scales, read, attention).  Internal to the library.
+#pragma once
+
+#include "paged.h"
+
+namespace w4a16 {
+
+constexpr int kMostGroup = 128;  // tokens of a scale
+constexpr int kMostNew = 16;     // new tokens of a request
+
+// place / group for places of a page (below 2^16) by one multiplication: the high
+// half of place * ceil(2^32 / group).  (0 stands for a group of one.)
+inline uint32_t group_magic(int group) {
+    return group == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + group - 1) / group);
+}
+
+struct ScaledAppendArgs {
+    const uint16_t* q;
+    uint16_t* q_out;
+    const uint16_t* k;
+    const uint16_t* v;
+    int64_t q_token, q_head, qo_token, qo_head, k_token, k_head, v_token, v_head;
+    const int32_t* positions;
+    int64_t axis_stride;
+    const float* inv_freq;
+    int axis_end[4];  // pairs below axis_end[a] (and not below axis_end[a - 1]) go by axis a
+    const int32_t* slots;
+    w4a16_scaled_cache cache;  // heads 0 where there is none
+    int q_heads;
+    int rotary;
+    int dim;
+    int interleaved;
+    int64_t T;
+    uint32_t* err;
+};
+
+cudaError_t launch_scaled_append(const ScaledAppendArgs& a, const DeviceInfo& dev, cudaStream_t s);
+
+struct ScaledReadArgs {
+    w4a16_scaled_cache cache;
+    const int32_t* block_table;
+    int64_t table_stride;
+    const int32_t* row_start;
+    const int32_t* first;  // NULL: 0
+    void* k_out;
+    void* v_out;
+    int64_t k_row, k_out_head, v_row, v_out_head;
+    int64_t rows;
+    int columns;
+    int B;
+    int out_f32;
+    uint32_t* err;
+};
+
+cudaError_t launch_scaled_read(const ScaledReadArgs& a, const DeviceInfo& dev, cudaStream_t s);
+
+// The one-token launch's arguments (its cache without scales; q_heads: those of a
+// token), and what several tokens and scales by group need.
+struct ScaledAttentionArgs : AttentionArgs {
+    int tokens;  // new ones of a request
+    int64_t q_token, out_token;
+    const float* k_scale;
+    const float* v_scale;
+    int64_t ks_block, ks_group, ks_head, vs_block, vs_group, vs_head;
+    int group;
+    uint32_t magic;  // of group
+};
+
+cudaError_t launch_scaled_attention(const ScaledAttentionArgs& a, int int8, const DeviceInfo& dev, cudaStream_t s);
+
+}  // namespace w4a16

@@ -20,7 +20,11 @@ namespace {
 decltype(&w4a16_paged_map) g_map;
 decltype(&w4a16_rope_append) g_append;
 decltype(&w4a16_paged_attention) g_attention;
+decltype(&w4a16_scaled_append) g_scaled_append;
+decltype(&w4a16_scaled_read) g_scaled_read;
+decltype(&w4a16_scaled_attention) g_scaled_attention;
 PyObject* g_current_stream;  // device index -> raw stream
+PyObject* g_current_device;  // -> device index
 
 const at::Tensor* tensor_of(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
 
@@ -86,6 +90,15 @@ bool integer(PyObject* o, int64_t* v) {
     if (!PyLong_Check(o)) return false;
     *v = PyLong_AsLongLong(o);
     return !PyErr_Occurred();
+}
+
+// whether `device` is the current one: the stream 0 is that one's
+bool current(int64_t device) {
+    PyObject* now = PyObject_CallNoArgs(g_current_device);
+    if (!now) return false;
+    const int64_t is = PyLong_AsLongLong(now);
+    Py_DECREF(now);
+    return !PyErr_Occurred() && is == device;
 }
 
 // a list or tuple of at most four whole numbers; None: one axis, no array
@@ -155,9 +168,11 @@ PyObject* paged_map(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
 }
 
+// The two appends take the same arguments, their caches apart.
 // (q, k, v, positions, inv_freq, slots, cache address, cache heads, cache device, sections, flags, q_out, stream)
-PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != 13 || !g_append) return other_form();
+template <class Cache, class Entry>
+PyObject* append_to(Entry entry, PyObject* const* a, Py_ssize_t n) {
+    if (n != 13 || !entry) return other_form();
     try {
         Rows q, out, k, v;
         int32_t *slots = nullptr, *positions;
@@ -195,14 +210,21 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int rotary = 2 * static_cast<int>(freq->size(0));
         const float* f = static_cast<const float*>(freq->data_ptr());
         return status_of([&] {
-            return g_append(q.p, q.row, q.head, out.p, out.row, out.head, static_cast<int>(q.heads), k.p, k.row, k.head, v.p, v.row,
+            return entry(q.p, q.row, q.head, out.p, out.row, out.head, static_cast<int>(q.heads), k.p, k.row, k.head, v.p, v.row,
                             v.head, positions, any.n, f, sections.p, sections.axes, rotary,
                             static_cast<int>(any.dim), static_cast<unsigned>(flags), slots,
-                            reinterpret_cast<const w4a16_kv_cache*>(cache), any.n, stream);
+                            reinterpret_cast<const Cache*>(cache), any.n, stream);
         });
     } catch (...) {
         return other_form();
     }
+}
+
+PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) { return append_to<w4a16_kv_cache>(g_append, a, n); }
+PyObject* scaled_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    int64_t device;
+    if (n != 13 || !integer(a[8], &device) || !current(device)) return other_form();
+    return append_to<w4a16_scaled_cache>(g_scaled_append, a, n);
 }
 
 // (q, cache address, cache dim, cache device, block_table, kv_len, scale, window, out, lse, workspace, stream)
@@ -240,17 +262,114 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
 }
 
-// bind(map address, append address, attention address, current-stream function)
+// [rows, heads, dim] in bf16 or fp32, dim contiguous
+struct Output {
+    void* p;
+    int64_t rows, row, head;
+    bool f32;
+};
+bool output_of(PyObject* o, int64_t heads, int64_t dim, int64_t device, Output* x) {
+    const at::Tensor* t = tensor_of(o);
+    if (!t || (t->scalar_type() != at::kBFloat16 && t->scalar_type() != at::kFloat) || !on(t, device) || t->dim() != 3 || t->stride(2) != 1 ||
+        t->size(1) != heads || t->size(2) != dim)
+        return false;
+    *x = Output{t->data_ptr(), t->size(0), t->stride(0), t->stride(1), t->scalar_type() == at::kFloat};
+    return true;
+}
+
+// (cache address, cache heads, cache dim, cache device, block_table, row_start, k_out, v_out, stream)
+PyObject* scaled_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 9 || !g_scaled_read) return other_form();
+    try {
+        int64_t cache, heads, dim, device;
+        Table t;
+        int32_t* start;
+        Output k, v;
+        void* stream;
+        if (!integer(a[0], &cache) || !integer(a[1], &heads) || !integer(a[2], &dim) || !integer(a[3], &device) || !table_of(a[4], device, &t) ||
+            t.rows >= INT32_MAX || t.columns > INT32_MAX || !vector_of(a[5], t.rows + 1, device, &start) || !output_of(a[6], heads, dim, device, &k) ||
+            !output_of(a[7], heads, dim, device, &v) || !current(device) || k.rows != v.rows || k.f32 != v.f32 || !stream_of(a[8], device, &stream))
+            return other_form();
+        return status_of([&] {
+            return g_scaled_read(reinterpret_cast<const w4a16_scaled_cache*>(cache), t.p, t.stride, static_cast<int>(t.columns), start, nullptr,
+                                 static_cast<int>(t.rows), k.p, k.row, k.head, v.p, v.row, v.head, k.f32 ? W4A16_OUT_F32 : W4A16_OUT_BF16, k.rows,
+                                 stream);
+        });
+    } catch (...) {
+        return other_form();
+    }
+}
+
+// bf16 [B, heads, dim] or [B, tokens, heads, dim], dim contiguous
+struct TokenRows {
+    uint16_t* p;
+    int64_t n, tokens, heads, dim, request, token, head, device;
+    bool several;
+};
+bool token_rows_of(PyObject* o, TokenRows* x) {
+    const at::Tensor* t = tensor_of(o);
+    if (!t || t->scalar_type() != at::kBFloat16 || !t->is_cuda() || (t->dim() != 3 && t->dim() != 4) || t->stride(-1) != 1) return false;
+    x->several = t->dim() == 4;
+    x->n = t->size(0), x->tokens = x->several ? t->size(1) : 1, x->heads = t->size(-2), x->dim = t->size(-1);
+    x->request = t->stride(0), x->token = x->several ? t->stride(1) : 0, x->head = t->stride(-2);
+    x->device = t->get_device();
+    x->p = static_cast<uint16_t*>(t->data_ptr());
+    return true;
+}
+
+// (q, cache address, cache dim, cache device, block_table, kv_len, scale, window, out, lse, workspace, stream)
+PyObject* scaled_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 12 || !g_scaled_attention) return other_form();
+    try {
+        TokenRows q, out;
+        Table t;
+        int32_t* lengths;
+        int64_t cache, dim, device, window;
+        if (!token_rows_of(a[0], &q) || !integer(a[1], &cache) || !integer(a[2], &dim) || q.dim != dim || !integer(a[3], &device) ||
+            q.device != device || !table_of(a[4], device, &t) || t.rows != q.n || !vector_of(a[5], q.n, device, &lengths) ||
+            !integer(a[7], &window) || !token_rows_of(a[8], &out) || out.several != q.several || out.n != q.n || out.tokens != q.tokens ||
+            out.heads != q.heads || out.dim != dim || out.device != device)
+            return other_form();
+        const at::Tensor *lse = tensor_of(a[9]), *ws = tensor_of(a[10]);
+        if (!lse || !ws || lse->scalar_type() != at::kFloat || !on(lse, device) || lse->dim() != (q.several ? 3 : 2) || lse->size(0) != q.n ||
+            lse->size(-1) != q.heads || (q.several && lse->size(1) != q.tokens) || !lse->is_contiguous() || !on(ws, device) || !ws->is_contiguous())
+            return other_form();
+        const double scale = PyFloat_AsDouble(a[6]);
+        void* stream;
+        if (PyErr_Occurred() || !current(device) || q.n > INT32_MAX || q.heads > INT32_MAX || q.tokens > INT32_MAX || t.columns > INT32_MAX || window > INT32_MAX ||
+            window < INT32_MIN || !stream_of(a[11], device, &stream))
+            return other_form();
+        float* l = static_cast<float*>(lse->data_ptr());
+        void* w = ws->data_ptr();
+        const size_t bytes = ws->nbytes();
+        return status_of([&] {
+            return g_scaled_attention(q.p, q.request, q.token, q.head, reinterpret_cast<const w4a16_scaled_cache*>(cache), t.p, t.stride,
+                                      static_cast<int>(t.columns), lengths, static_cast<int>(q.n), static_cast<int>(q.tokens),
+                                      static_cast<int>(q.heads), static_cast<float>(scale), static_cast<int>(window), out.p, out.request,
+                                      out.token, out.head, l, w, bytes, stream);
+        });
+    } catch (...) {
+        return other_form();
+    }
+}
+
+// bind(map, append, attention, scaled append, scaled read, scaled attention: addresses; current-stream and current-device functions)
 PyObject* bind(PyObject*, PyObject* args) {
-    unsigned long long m, p, t;
-    PyObject* f;
-    if (!PyArg_ParseTuple(args, "KKKO", &m, &p, &t, &f)) return nullptr;
+    unsigned long long m, p, t, sp, sr, st;
+    PyObject *f, *d;
+    if (!PyArg_ParseTuple(args, "KKKKKKOO", &m, &p, &t, &sp, &sr, &st, &f, &d)) return nullptr;
     g_map = reinterpret_cast<decltype(g_map)>(m);
     g_append = reinterpret_cast<decltype(g_append)>(p);
     g_attention = reinterpret_cast<decltype(g_attention)>(t);
+    g_scaled_append = reinterpret_cast<decltype(g_scaled_append)>(sp);
+    g_scaled_read = reinterpret_cast<decltype(g_scaled_read)>(sr);
+    g_scaled_attention = reinterpret_cast<decltype(g_scaled_attention)>(st);
     Py_INCREF(f);
     Py_XDECREF(g_current_stream);
     g_current_stream = f;
+    Py_INCREF(d);
+    Py_XDECREF(g_current_device);
+    g_current_device = d;
     Py_RETURN_NONE;
 }
 
@@ -259,6 +378,9 @@ PyMethodDef g_methods[] = {
     {"paged_map", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(paged_map)), METH_FASTCALL, nullptr},
     {"rope_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(rope_append)), METH_FASTCALL, nullptr},
     {"paged_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(paged_attention)), METH_FASTCALL, nullptr},
+    {"scaled_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(scaled_append)), METH_FASTCALL, nullptr},
+    {"scaled_read", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(scaled_read)), METH_FASTCALL, nullptr},
+    {"scaled_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(scaled_attention)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
