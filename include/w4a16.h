@@ -717,7 +717,7 @@ W4A16_API size_t w4a16_scaled_attention_workspace_bytes(int q_heads, int kv_head
  *   h * *_head; lse: fp32 [B][N][q_heads] or NULL.
  * fp32 scores, maxima and sums; two roundings: of out to bf16, and of the weights w_j =
  * p_j * v_scale_j to fp16 before they multiply the codes c_j.  So, beside fp32's,
- *     |error| <= 2^-8 |out| + 2^-11 sum_j p_j |v_j| + 2^-40 max_j w_j sum_j |c_j|.
+ *     |error| <= 2^-8 |out| + 2^-11 sum_j p_j |v_j| + 2^-33 max_j w_j sum_j |c_j|.
  * A key or value that is NaN reaches the new tokens that see it and no others.
  * The other arguments, the workspace and the limits are those of w4a16_paged_attention,
  * with N * q_heads in the place of q_heads.

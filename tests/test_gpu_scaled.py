@@ -9,7 +9,7 @@ product, one rounding).  Tolerances of the rest:
       code's magnitude, at least 2^-10) + 2^-20 (|x1| + |x2|) / S, the rotation's
       error: cosine and sine to about 2^-21 each with the fp32 products;
   queries: 2^-8 |y| + 2^-20 (|x1| + |x2|);
-  attention, out: 2^-8 |y| + 2^-11 sum p|v| + 2^-40 max_j(p_j |s_j|) sum |c_j| (the
+  attention, out: 2^-8 |y| + 2^-11 sum p|v| + 2^-33 max_j(p_j |s_j|) sum |c_j| (the
       rounding of the result and of the weights in fp16, normal and below), and as a
       relative error of each weight the fp32 scores' error, (dim + 16) 2^-24 of scale
       sum |q||k| (twice: in the maximum's row and in the token's own), and 2^-22 (8 +
@@ -401,7 +401,7 @@ def check_attention(w, q, cache, table, lens, scale=None, window=0, flags=0, got
     want, want_lse, spread, reach, low = ref.attention(q.double(), code_values(cache.k), code_values(cache.v), ks, vs, table, lens, scale, window, cache.group)
     score = (dim + 16) * 2.0 ** -24 * reach
     logs = torch.log2(torch.where(vs.isfinite() & (vs != 0), vs, 1.0).abs()).abs().max()
-    tol = U * want.abs() + (2.0 ** -11 + 2 * score[..., None] + 2.0 ** -22 * (8 + logs)) * spread + 2.0 ** -40 * low + 1e-37
+    tol = U * want.abs() + (2.0 ** -11 + 2 * score[..., None] + 2.0 ** -22 * (8 + logs)) * spread + 2.0 ** -33 * low + 1e-37
     assert not out.isnan().any()
     assert ((out - want).abs() <= tol).all(), float(((out - want).abs() / tol).max())
     empty = want_lse == -float("inf")

@@ -1010,6 +1010,12 @@ w4a16_status w4a16_scaled_attention(const uint16_t* q, int64_t q_request, int64_
     a.ks_block = cache->ks_block, a.ks_group = cache->ks_group, a.ks_head = cache->ks_head;
     a.vs_block = cache->vs_block, a.vs_group = cache->vs_group, a.vs_head = cache->vs_head;
     a.group = cache->group, a.magic = group_magic(cache->group);
+    const int box = cache->page % 16 == 0 ? 16 : cache->page % 8 == 0 ? 8 : 0, inner = cache->dim <= 64 ? 64 : 128;
+    a.tensor_copies = box && encode_cache_map(&a.k_map, cache->k, *cache, cache->k_block, cache->k_token, cache->k_head, inner, box) &&
+                      encode_cache_map(&a.v_map, cache->v, *cache, cache->v_block, cache->v_token, cache->v_head, inner, box);
+    a.boxes_log2 = !a.tensor_copies ? 4 : box == 16 ? 0 : 1;
+    a.boxes = 1 << a.boxes_log2;
+    a.one_scale = a.boxes == 1 && cache->group % 16 == 0;
     return from_cuda(launch_scaled_attention(a, cache->dtype == W4A16_CACHE_INT8, dev->info, static_cast<cudaStream_t>(stream)));
 }
 

@@ -71,6 +71,10 @@ struct ArgsOf<kInt8Groups> {
 template <int C>
 using Args = typename ArgsOf<C>::type;
 
+// Scales by group: weights go into fp16 products as 2^kWeightBias of the largest,
+// which may grow by 2^kSlack before o is scaled again: 2^15 at most.
+constexpr float kWeightBias = 8.f, kSlack = 7.f;
+
 constexpr int kMinCost = 3;     // a warp's share at least
 constexpr int kRowTiles = 8;    // rows kernel: tiles of a warp at most
 constexpr int kRowEnough = 2;   // and where one CTA is enough
@@ -109,14 +113,14 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<uint16_t>(v)));
     return d;
 }
-// A word of four codes as two fp16 pairs, exactly.
+// A word of four codes as two fp16 pairs, exactly: e4m3 the first two and the last
+// two, int8 the first and third and the second and fourth.
 template <int C>
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
     if (C == kInt8Groups) {
-        // 1024 + (code + 128), the code's byte as the low one of an fp16
-        const uint32_t u = w ^ 0x80808080u;
+        // 1024 + (code + 128), the code's byte (its top bit turned) as the low one of an fp16
         const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
-        uint32_t x = __byte_perm(u, 0x64646464u, 0x4140), y = __byte_perm(u, 0x64646464u, 0x4342);
+        const uint32_t x = (w & 0x00FF00FFu) ^ 0x64806480u, y = ((w >> 8) & 0x00FF00FFu) ^ 0x64806480u;
         const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&x), off), b = __hsub2(*reinterpret_cast<const __half2*>(&y), off);
         lo = *reinterpret_cast<const uint32_t*>(&a), hi = *reinterpret_cast<const uint32_t*>(&b);
     } else {
@@ -127,16 +131,7 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
 // pairs of the even and of the odd dim.
 template <int C>
 __device__ __forceinline__ void codes_to_f16_by_dim(uint32_t w, uint32_t& even, uint32_t& odd) {
-    if (C == kInt8Groups) {
-        const uint32_t u = w ^ 0x80808080u;
-        const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-        uint32_t x = __byte_perm(u, 0x64646464u, 0x4240), y = __byte_perm(u, 0x64646464u, 0x4341);
-        const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&x), off), b = __hsub2(*reinterpret_cast<const __half2*>(&y), off);
-        even = *reinterpret_cast<const uint32_t*>(&a), odd = *reinterpret_cast<const uint32_t*>(&b);
-    } else {
-        const uint32_t x0 = e4m3x2_to_f16x2(w), x1 = e4m3x2_to_f16x2(w >> 16);
-        even = __byte_perm(x0, x1, 0x5410), odd = __byte_perm(x0, x1, 0x7632);
-    }
+    codes_to_f16<C>(C == kInt8Groups ? w : __byte_perm(w, 0u, 0x3120), even, odd);
 }
 // both halves, a NaN among them as a number
 __device__ __forceinline__ uint32_t as_numbers(uint32_t v) {
@@ -186,33 +181,46 @@ __device__ __forceinline__ uint32_t tile_offset(int r, int c) {
     return static_cast<uint32_t>((r * CH + (c ^ f)) * 16);
 }
 
+// The same where scales go by group: as a tensor copy lays boxes of 64 or 128 bytes by
+// tokens out, of 256-byte rows the first halves of all tokens and then the second.
+template <int CH>
+__device__ __forceinline__ uint32_t group_offset(int r, int c) {
+    if (CH == 4) return static_cast<uint32_t>((r * 4 + (c ^ ((r >> 1) & 3))) * 16);
+    return static_cast<uint32_t>((c >> 3) * (kTile * 128) + (r * 8 + ((c & 7) ^ (r & 7))) * 16);
+}
+
 template <int C, int DP, int NT>
 struct AttnShape {
     static constexpr int kHeads = 8 * NT;
     static constexpr int kSteps = DP / 16;                     // 16-dim steps of a head
     // 16-byte chunks of a row in shared memory (six would not swizzle: eight)
+    // (scales by group: as the tensor copies lay rows out, 64 bytes or one or two times 128)
     static constexpr bool k8 = in_8_bits(C);
-    static constexpr int kChunks = k8 && DP == 96 ? 8 : DP * (k8 ? 1 : 2) / 16;
+    static constexpr int kChunks = by_group(C) ? (DP == 64 ? 4 : DP <= 128 ? 8 : 16) : k8 && DP == 96 ? 8 : DP * (k8 ? 1 : 2) / 16;
     static constexpr int kRowBytes = kChunks * 16;
-    static constexpr int kScales = 2 * kTile * kRowBytes;  // behind keys and values: the scales of the tile's tokens
-    static constexpr int kStageBytes = kScales + (by_group(C) ? 2 * kTile * 4 : 0);
+    static constexpr int kStageBytes = 2 * kTile * kRowBytes;  // keys, then values
+    // scales by group: beside a stage what is known of it (16 bytes), the scales of its 16
+    // keys and values and a barrier; and what aligns the first stage
+    static constexpr int kBeside = by_group(C) ? 16 + 2 * kTile * 4 + 8 : 0, kAlign = by_group(C) ? 1024 : 0;
     static constexpr int kPartFloats = kHeads * (DP + 2);
     // shares: one CTA an SM, of as many warps as its registers allow (the accumulators'
     // size decides) with rings of three stages or more
     static constexpr int kShareWarps = 4 * (k8 ? (NT == 1 ? (DP == 64 ? 4 : DP <= 128 ? 3 : 2) : (DP == 64 ? 3 : 2))
                                                  : (DP == 64 ? 3 : DP <= 128 ? 2 : 1));
-    static constexpr int kFit = 226 * 1024 / (kShareWarps * kStageBytes);
+    static constexpr int kFit = (226 * 1024 - kAlign) / (kShareWarps * (kStageBytes + kBeside));
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
-    static constexpr int kSmem = kShareWarps * kStages * kStageBytes;
+    static constexpr int kSmem = kShareWarps * kStages * (kStageBytes + kBeside) + kAlign;
     // rows: one CTA an SM
     static constexpr int kRowWarps = kStageBytes > 12288 ? 4 : 8;
-    static constexpr int kRowFit = 225 * 1024 / (kRowWarps * kStageBytes);
+    static constexpr int kRowFit = (225 * 1024 - kAlign) / (kRowWarps * (kStageBytes + kBeside));
     static constexpr int kRowStages = kRowFit > 4 ? 4 : kRowFit;
     static constexpr int kRowRing = kRowStages * kStageBytes;  // of a warp
-    static constexpr int kRowSmem = kRowWarps * kRowRing;
+    static constexpr int kRowSmem = kRowWarps * (kRowRing + kRowStages * kBeside) + kAlign;
+    // scales by group: tiles of a step of the loop, two where registers hold them
+    static constexpr int kPair = DP <= 128 && NT == 1 ? 2 : 1;
     static constexpr int kPartBytes = kHeads * DP * 4;
     static constexpr bool kClusters = kRowRing >= 2 * kPartBytes;  // room for the CTA's part behind a warp's
-    static_assert(kStages >= 3, "ring too short");
+    static_assert(kStages >= 3 && kStages > kPair && kRowStages >= kPair, "ring too short");
     static_assert(kRowStages >= 2 && kRowRing >= kPartBytes, "no room for a warp's part");
     static_assert(160 * kShareWarps <= most_workers(DP), "workspace");
 };
@@ -393,15 +401,35 @@ struct RowMath {
                         const __half2 h = __floats2half2_rn(bf16_to_f32(v & 0xFFFFu) * up, bf16_to_f32(v >> 16) * up);
                         qf[n][k][e] = *reinterpret_cast<const uint32_t*>(&h);
                     }
+                if (C == kInt8Groups) {  // the pairs that codes_to_f16 makes
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) {
+                        const uint32_t v0 = qf[n][k][0], v1 = qf[n][k][1];
+                        qf[n][k][0] = __byte_perm(v0, v1, 0x5410), qf[n][k][1] = __byte_perm(v0, v1, 0x7632);
+                    }
+                }
                 sl[n][0] *= __shfl_sync(0xFFFFFFFFu, down, 8 * c);
                 sl[n][1] *= __shfl_sync(0xFFFFFFFFu, down, 8 * c + 4);
             }
         }
     }
 
-    // the tile at kt (shared address): keys, then values; mask: tokens that count; first:
-    // the number of its first token (scales by group only)
-    __device__ __forceinline__ void tile(const Args<C>& a, const Request& q, uint32_t kt, uint32_t mask, int first, int lane) {
+    // the largest of a column's tokens
+    static __device__ __forceinline__ float over_tokens(float x) {
+        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+        return fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+    }
+    __device__ __forceinline__ void scale_o(int n, const float (&f)[2]) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            o[n][k].x *= f[0], o[n][k].y *= f[1];
+            o[n][k].z *= f[0], o[n][k].w *= f[1];
+        }
+    }
+
+    // the tile at kt (shared address): keys, then values; mask: tokens that count
+    __device__ __forceinline__ void tile(uint32_t kt, uint32_t mask, int lane) {
         const uint32_t vt = kt + kTile * Sh::kRowBytes;
         const int r = lane >> 2;
         // two chains of products, where registers allow: the latency of one is a good part of a tile's
@@ -426,117 +454,35 @@ struct RowMath {
                 ldmatrix_x4(f, kt + tile_offset<CH>(lane & 15, k + (lane >> 4)));
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    uint32_t a0, a1, a2, a3;
-                    codes_to_f16<C>(f[2 * j], a0, a2);
-                    codes_to_f16<C>(f[2 * j + 1], a1, a3);
+                    const uint32_t a0 = e4m3x2_to_f16x2(f[2 * j]), a2 = e4m3x2_to_f16x2(f[2 * j] >> 16);
+                    const uint32_t a1 = e4m3x2_to_f16x2(f[2 * j + 1]), a3 = e4m3x2_to_f16x2(f[2 * j + 1] >> 16);
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
                         attn_mma<C>(kTwo && j ? s1[n] : s[n], a0, a1, a2, a3, qf[n][k + j][0], qf[n][k + j][1]);
                 }
             }
         }
-        // Scales by group: of keys r and r + 8, and of the values there in log2 units.
-        float ks[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
-        uint32_t sign[2] = {0u, 0u};
-        bool edge = false, one_scale = false, scrub = false;
-        if constexpr (by_group(C)) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                ks[i] = ld_shared_f32(kt + Sh::kScales + (r + 8 * i) * 4);
-                const float v = ld_shared_f32(kt + Sh::kScales + (kTile + r + 8 * i) * 4);
-                lv[i] = log2_fast(v);
-                sign[i] = __float_as_uint(v) & 0x80000000u;
-            }
-            one_scale = mask == 0xFFFFu && a.group % kTile == 0;
-            // tokens that some new ones see and others do not
-            edge = first + kTile > q.len - (a.tokens - 1) || (a.window > 0 && first < q.len - a.window);
-            if (C == kE4m3Groups && edge && a.tokens > 1) {
-                // a NaN among them stays with those that see it: their weight becomes NaN, and the
-                // code a number that the others' weight of 0 takes out
-                bool nan = false;
-#pragma unroll
-                for (int i = 0; i < KS / 2; ++i) {  // (the chunks that the products take: of 96 dims not all)
-                    const uint4 v = ld_shared_u4(vt + tile_offset<CH>(lane & 15, 2 * i + (lane >> 4)));
-                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) nan |= (((x[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u;
-                }
-                uint32_t who = __ballot_sync(0xFFFFFFFFu, nan);
-                who = (who | (who >> 16)) & 0xFFFFu;
-                scrub = who != 0u;
-                if ((who >> r) & 1u) lv[0] = NAN;
-                if ((who >> (r + 8)) & 1u) lv[1] = NAN;
-                one_scale = one_scale && !scrub;
-            }
-        }
         uint32_t pf[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[n][e] = (s[n][e] + s1[n][e]) * sl[n][e & 1];
-                if (by_group(C)) s[n][e] *= ks[e >> 1];
-            }
+            for (int e = 0; e < 4; ++e) s[n][e] = (s[n][e] + s1[n][e]) * sl[n][e & 1];
             if (mask != 0xFFFFu) {
                 if (!((mask >> r) & 1u)) s[n][0] = s[n][1] = -INFINITY;
                 if (!((mask >> (r + 8)) & 1u)) s[n][2] = s[n][3] = -INFINITY;
             }
-            if constexpr (by_group(C)) {
-                if (edge) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int token = first + r + 8 * (e >> 1), end = upto[n][e & 1];
-                        if (token >= end || (a.window > 0 && token < end - a.window)) s[n][e] = -INFINITY;
-                    }
-                }
-            }
             float top[2] = {fmaxf(s[n][0], s[n][2]), fmaxf(s[n][1], s[n][3])};
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 4));
-                top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 8));
-                top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 16));
-            }
-            // weights of the values: p times their scale, the largest of which o goes by.  (By the
-            // largest p instead, a token of large scale and small p would pass what fp16 holds.)
-            float w[4], heavy[2] = {-INFINITY, -INFINITY};
-            if constexpr (by_group(C)) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = s[n][e] == -INFINITY ? -INFINITY : s[n][e] + lv[e >> 1];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (one_scale) {
-                        heavy[e] = top[e] + lv[0];
-                    } else {
-                        heavy[e] = fmaxf(w[e], w[e + 2]);
-                        heavy[e] = fmaxf(heavy[e], __shfl_xor_sync(0xFFFFFFFFu, heavy[e], 4));
-                        heavy[e] = fmaxf(heavy[e], __shfl_xor_sync(0xFFFFFFFFu, heavy[e], 8));
-                        heavy[e] = fmaxf(heavy[e], __shfl_xor_sync(0xFFFFFFFFu, heavy[e], 16));
-                    }
-                    heavy[e] = fmaxf(heavy[e], big[n][e]);
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) top[e] = fmaxf(top[e], m[n][e]);
-            bool grown = top[0] > m[n][0] || top[1] > m[n][1];
-            if (by_group(C)) grown |= heavy[0] > big[n][0] || heavy[1] > big[n][1];
-            if (__any_sync(0xFFFFFFFFu, grown)) {
+            for (int e = 0; e < 2; ++e) top[e] = fmaxf(over_tokens(top[e]), m[n][e]);
+            if (__any_sync(0xFFFFFFFFu, top[0] > m[n][0] || top[1] > m[n][1])) {
                 float keep[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     keep[e] = part_factor(m[n][e], top[e]);  // from -infinity: 0
                     m[n][e] = top[e];
                     l[n][e] *= keep[e];
-                    if (by_group(C)) {
-                        keep[e] = part_factor(big[n][e], heavy[e]);
-                        big[n][e] = heavy[e];
-                    }
                 }
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    o[n][k].x *= keep[0], o[n][k].y *= keep[1];
-                    o[n][k].z *= keep[0], o[n][k].w *= keep[1];
-                }
+                scale_o(n, keep);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -545,10 +491,6 @@ struct RowMath {
                 s[n][e] -= m[n][e & 1] == -INFINITY ? 0.f : m[n][e & 1];
                 s[n][e] = exp2_fast(C == kE4m3 ? s[n][e] + kE4m3Bias : s[n][e]);
                 l[n][e & 1] += s[n][e];
-                if (by_group(C)) {
-                    w[e] -= big[n][e & 1] == -INFINITY ? 0.f : big[n][e & 1];
-                    s[n][e] = __uint_as_float(__float_as_uint(exp2_fast(w[e] + kE4m3Bias)) ^ sign[e >> 1]);
-                }
             }
             // to 16 bits for the second product, whose operands are of one type: that of the
             // values.  fp16 rounds p by 2^-11 of it, bf16 by 2^-8, about as much as the result's
@@ -588,15 +530,215 @@ struct RowMath {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     // word: dims 2r, 2r + 1 of token 2c, then of token 2c + 1
-                    uint32_t a0, a1, a2, a3;
-                    codes_to_f16_by_dim<C>(f[2 * j], a0, a1);
-                    codes_to_f16_by_dim<C>(f[2 * j + 1], a2, a3);
-                    if (C == kE4m3Groups && scrub) a0 = as_numbers(a0), a1 = as_numbers(a1), a2 = as_numbers(a2), a3 = as_numbers(a3);
+                    const uint32_t x0 = e4m3x2_to_f16x2(f[2 * j]), x1 = e4m3x2_to_f16x2(f[2 * j] >> 16);
+                    const uint32_t y0 = e4m3x2_to_f16x2(f[2 * j + 1]), y1 = e4m3x2_to_f16x2(f[2 * j + 1] >> 16);
+                    const uint32_t a0 = __byte_perm(x0, x1, 0x5410), a1 = __byte_perm(x0, x1, 0x7632);
+                    const uint32_t a2 = __byte_perm(y0, y1, 0x5410), a3 = __byte_perm(y0, y1, 0x7632);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) add(n, k + j, a0, a1, a2, a3);
                 }
             }
         }
+    }
+
+    // --- scales by group ------------------------------------------------------
+    // Scores s of P tiles (log2 units; rows r, r + 8 by columns 2c, 2c + 1) to the weights of
+    // the values, p times the scale, 2^lv.  o goes by the largest weight: by the largest p instead,
+    // a token of large scale and small p would pass what fp16 holds.  m and the largest weight
+    // need not be the largest there are, only near them (kSlack), so that most tiles take a vote
+    // here and no exchange.  ALIKE: a tile's tokens have one scale.  HIDDEN: some scores are
+    // -infinity for tokens that a column does not see, whose scale may be anything.
+    template <int P, bool ALIKE, bool HIDDEN>
+    __device__ __forceinline__ void weigh(int n, float (&s)[P][NT][4], const float (&lv)[P][2], const uint32_t (&sign)[P][2]) {
+        float top[2], heavy[2];
+        const auto weight = [&](int p, int e) { return HIDDEN && s[p][n][e] == -INFINITY ? -INFINITY : s[p][n][e] + lv[p][e >> 1]; };
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            top[e] = heavy[e] = -INFINITY;
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const float most = fmaxf(s[p][n][e], s[p][n][e + 2]);
+                top[e] = fmaxf(top[e], most);
+                heavy[e] = fmaxf(heavy[e], ALIKE && !HIDDEN ? most + lv[p][0] : fmaxf(weight(p, e), weight(p, e + 2)));
+            }
+        }
+        bool over = false;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) over |= top[e] > m[n][e] + kSlack || heavy[e] > big[n][e] + kSlack;
+        if (__any_sync(0xFFFFFFFFu, over)) {
+            float keep[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                top[e] = fmaxf(over_tokens(top[e]), m[n][e]);
+                heavy[e] = fmaxf(over_tokens(heavy[e]), big[n][e]);
+                l[n][e] *= part_factor(m[n][e], top[e]);  // from -infinity: 0
+                keep[e] = part_factor(big[n][e], heavy[e]);
+                m[n][e] = top[e], big[n][e] = heavy[e];
+            }
+            scale_o(n, keep);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float base = m[n][e] == -INFINITY ? 0.f : m[n][e], heavy = big[n][e] == -INFINITY ? 0.f : big[n][e];
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float& x = s[p][n][2 * i + e];
+                    // (the bias after the difference, which is a float's whatever the maximum's size)
+                    const float w = weight(p, 2 * i + e) - heavy + kWeightBias;
+                    l[n][e] += exp2_fast(x - base);
+                    x = __uint_as_float(__float_as_uint(exp2_fast(w)) ^ sign[p][i]);
+                }
+        }
+    }
+
+    // P tiles of a row: codes at kt (shared addresses: keys, then values), what is known of them
+    // and the scales of their tokens at info; first: the numbers of their first tokens
+    template <int P>
+    __device__ __forceinline__ void tiles(const Args<C>& a, const Request& q, const uint32_t (&kt)[P], const uint32_t (&info)[P],
+                                          const int (&first)[P], int lane) {
+        constexpr int kValues = kTile * Sh::kRowBytes;  // from a key's place to its value's
+        constexpr bool kTwo = P == 1 && NT * KS <= 16;  // two chains of products, as above
+        const int r = lane >> 2;
+        uint32_t at[P];  // chunk lane / 16 of row lane % 16; chunk k + lane / 16 (k even): its address xor 16 k
+#pragma unroll
+        for (int p = 0; p < P; ++p) at[p] = kt[p] + group_offset<CH>(lane & 15, lane >> 4);
+        float s[P][NT][4], s1[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s1[n][e] = 0.f;
+#pragma unroll
+                for (int p = 0; p < P; ++p) s[p][n][e] = 0.f;
+            }
+#pragma unroll
+        for (int k = 0; k < KS; k += 2)
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                uint32_t f[4];  // two chunks of 16 codes: rows r and r + 8 of each
+                ldmatrix_x4(f, (at[p] ^ ((k & 7) * 16)) + (k >> 3) * (kTile * 128));
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t a0, a1, a2, a3;
+                    codes_to_f16<C>(f[2 * j], a0, a2);
+                    codes_to_f16<C>(f[2 * j + 1], a1, a3);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) attn_mma<C>(kTwo && j ? s1[n] : s[p][n], a0, a1, a2, a3, qf[n][k + j][0], qf[n][k + j][1]);
+                }
+            }
+        uint32_t mask[P], pf[P][NT][2];
+        float ks[P][2], lv[P][2];
+        uint32_t sign[P][2];
+        bool hidden = false;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const uint4 x = ld_shared_u4(info[p]);
+            mask[p] = x.x;
+            ks[p][0] = ks[p][1] = __uint_as_float(x.y);
+            lv[p][0] = lv[p][1] = log2_fast(__uint_as_float(x.z));
+            sign[p][0] = sign[p][1] = x.z & 0x80000000u;
+            hidden |= x.x != 0xFFFFu;
+        }
+        // tokens that some new ones see and others do not (the last tile reaches furthest)
+        const bool edge = first[P - 1] + kTile > q.len - (a.tokens - 1) || (a.window > 0 && first[0] < q.len - a.window);
+        hidden |= edge;
+        const auto scores = [&](int n) {
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[p][n][e] = (kTwo ? s[p][n][e] + s1[n][e] : s[p][n][e]) * (sl[n][e & 1] * ks[p][e >> 1]);
+        };
+        const auto to_f16 = [&](int n) {  // for the second product: 2^-11 of each weight, l takes the unrounded p
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const __half2 h = __floats2half2_rn(s[p][n][2 * e], s[p][n][2 * e + 1]);
+                    pf[p][n][e] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&h));
+                }
+        };
+        if (a.one_scale && !hidden) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                scores(n);
+                weigh<P, true, false>(n, s, lv, sign);
+                to_f16(n);
+            }
+        } else {
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                if (!a.one_scale) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        ks[p][i] = ld_shared_f32(info[p] + 16 + (r + 8 * i) * 4);
+                        const float v = ld_shared_f32(info[p] + 16 + (kTile + r + 8 * i) * 4);
+                        lv[p][i] = log2_fast(v);
+                        sign[p][i] = __float_as_uint(v) & 0x80000000u;
+                    }
+                }
+                if (C == kE4m3Groups && edge && a.tokens > 1) {
+                    // A NaN that some new tokens see stays with them: its weight becomes NaN there, and
+                    // the code a number.
+                    bool nan = false;
+#pragma unroll
+                    for (int k = 0; k < KS; k += 2) {  // (the chunks that the products take: of 96 dims not all)
+                        const uint4 v = ld_shared_u4((at[p] ^ ((k & 7) * 16)) + (k >> 3) * (kTile * 128) + kValues);
+                        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) nan |= (((x[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u;
+                    }
+                    uint32_t who = __ballot_sync(0xFFFFFFFFu, nan);
+                    who |= who >> 16;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if ((who >> (r + 8 * i)) & 1u) lv[p][i] = NAN;
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                scores(n);
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    if (!((mask[p] >> r) & 1u)) s[p][n][0] = s[p][n][1] = -INFINITY;
+                    if (!((mask[p] >> (r + 8)) & 1u)) s[p][n][2] = s[p][n][3] = -INFINITY;
+                    if (edge) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int token = first[p] + r + 8 * (e >> 1), end = upto[n][e & 1];
+                            if (token >= end || (a.window > 0 && token < end - a.window)) s[p][n][e] = -INFINITY;
+                        }
+                    }
+                }
+                weigh<P, false, true>(n, s, lv, sign);
+                to_f16(n);
+            }
+        }
+        // an e4m3 NaN would reach every column, those of weight 0 too; and in places that nobody
+        // sees codes may be anything
+        const bool scrub = C == kE4m3Groups && hidden;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int k = 0; k < KS; k += 2) {
+                uint32_t f[4];  // chunk k: tokens 0..7, 8..15, then chunk k + 1
+                ldmatrix_x4_trans(f, (at[p] ^ ((k & 7) * 16)) + (k >> 3) * (kTile * 128) + kValues);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    // word: dims 2r, 2r + 1 of token 2c, then of token 2c + 1
+                    uint32_t a0, a1, a2, a3;
+                    codes_to_f16_by_dim<C>(f[2 * j], a0, a1);
+                    codes_to_f16_by_dim<C>(f[2 * j + 1], a2, a3);
+                    if (scrub) a0 = as_numbers(a0), a1 = as_numbers(a1), a2 = as_numbers(a2), a3 = as_numbers(a3);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float d[4] = {o[n][k + j].x, o[n][k + j].y, o[n][k + j].z, o[n][k + j].w};
+                        attn_mma<C>(d, a0, a1, a2, a3, pf[p][n][0], pf[p][n][1]);
+                        o[n][k + j] = make_float4(d[0], d[1], d[2], d[3]);
+                    }
+                }
+            }
     }
 
     __device__ __forceinline__ void reduce() {
@@ -615,7 +757,7 @@ struct RowMath {
                 float f[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    f[e] = big[n][e] == -INFINITY ? 0.f : exp2_fast(0.5f * (big[n][e] - kE4m3Bias - m[n][e]));
+                    f[e] = big[n][e] == -INFINITY ? 0.f : exp2_fast(0.5f * (big[n][e] - kWeightBias - m[n][e]));
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
                     o[n][k].x = o[n][k].x * f[0] * f[0], o[n][k].y = o[n][k].y * f[1] * f[1];
@@ -691,16 +833,6 @@ struct TileCopy {
         return aligned(a) ? t - base >= 32 * step : t != base;
     }
 
-    // the scales of this lane's token, of its key (lanes 0..15) or value
-    __device__ __forceinline__ void copy_scales(const Args<C>& a, int hk, int64_t block, int in, bool valid, uint32_t dst, int lane) const {
-        if constexpr (by_group(C)) {
-            const int64_t of = a.magic ? static_cast<int>(__umulhi(in, a.magic)) : in;
-            const float* at = lane < 16 ? a.k_scale + block * a.ks_block + of * a.ks_group + hk * a.ks_head
-                                        : a.v_scale + block * a.vs_block + of * a.vs_group + hk * a.vs_head;
-            cp_async_4_zfill(dst + Sh::kScales + lane * 4, at, valid);
-        }
-    }
-
     // starts the copies of tile t into dst; returns the mask of the tokens the row sees
     __device__ __forceinline__ uint32_t copy(const Args<C>& a, int hk, const Request& q, int t, int step, uint32_t dst, int lane,
                                              bool& bad) const {
@@ -720,7 +852,6 @@ struct TileCopy {
                 mask = 0u;
                 block = 0;
             }
-            if constexpr (by_group(C)) copy_scales(a, hk, block, first + (lane & 15), (mask >> (lane & 15)) & 1u, dst, lane);
             kp += (block * a.cache.k_block + first * a.cache.k_token) * kBytes;
             vp += (block * a.cache.v_block + first * a.cache.v_token) * kBytes;
             const int64_t ks = a.cache.k_token * kBytes, vs = a.cache.v_token * kBytes;
@@ -739,7 +870,6 @@ struct TileCopy {
             bad |= id != -1 && !valid;
             mask = __ballot_sync(0xFFFFFFFFu, valid) & 0xFFFFu;
             const int64_t block = valid ? id : 0, first = valid ? place : 0;
-            if constexpr (by_group(C)) copy_scales(a, hk, block, static_cast<int>(first), valid, dst, lane);
             const int64_t ko = (block * a.cache.k_block + first * a.cache.k_token) * kBytes;
             const int64_t vo = (block * a.cache.v_block + first * a.cache.v_token) * kBytes;
 #pragma unroll
@@ -759,6 +889,147 @@ struct TileCopy {
     }
 };
 
+// A tensor copy of a box (64 or 128 bytes of one head by box tokens of a block).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+
+// Scales by group: the ring of a warp, and what fills it.  The codes of a tile come as
+// tensor copies of boxes of 16 or 8 tokens, which take next to no instructions (with
+// cp.async these were a third of all); blocks whose pages no box divides, by cp.async.
+// Block ids are loaded early, those of 32 boxes at once (lane i: box i % boxes of the
+// i / boxes-th tile).  Where a tile lies in one group its two scales come with them,
+// else those of its tokens by cp.async.
+template <int C, int DP, int NT>
+struct GroupRing {
+    using Sh = AttnShape<C, DP, NT>;
+    static constexpr int CH = Sh::kChunks, kInner = CH == 4 ? 64 : 128, kHalves = CH == 16 ? 2 : 1;
+    uint32_t codes, beside, bars;  // shared addresses: of stage 0 its codes; what is known of it; its barrier
+    int known, id, place;          // how many tiles' ids are left; this lane's
+    float ks, vs;
+    bool late;  // a copy did not arrive
+
+    __device__ __forceinline__ void open(uint32_t smem, int warp, int warps, int stages, int lane) {
+        smem = (smem + 1023u) & ~1023u;
+        codes = smem + warp * stages * Sh::kStageBytes;
+        beside = smem + warps * stages * Sh::kStageBytes + warp * stages * 144;
+        bars = smem + warps * stages * (Sh::kStageBytes + 144) + warp * stages * 8;
+        late = false;
+        if (lane < stages) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + lane * 8) : "memory");
+        mbar_init_fence();
+        fence_proxy_async_smem();
+        __syncwarp();
+    }
+
+    // the ids of the boxes from tile t on (tiles step apart, below t1) that hold tokens of [low, high)
+    __device__ __forceinline__ void look_up(const Args<C>& a, int b, int hk, int tile0, int low, int high, int t, int t1, int step, int lane) {
+        const int tile = t + (lane >> a.boxes_log2) * step;
+        const int token = (tile0 + tile) * kTile + (lane & (a.boxes - 1)) * (kTile >> a.boxes_log2);
+        const int col = static_cast<int>(static_cast<unsigned>(token) / static_cast<unsigned>(a.cache.page));
+        place = token - col * a.cache.page;
+        id = -1;
+        known = 32 >> a.boxes_log2;
+        if (tile < t1 && token < high && token + (kTile >> a.boxes_log2) > low) id = a.block_table[b * a.table_stride + col];
+        if (a.one_scale) {
+            ks = vs = 0.f;
+            if (id >= 0 && id < a.cache.blocks) {
+                const int64_t of = __umulhi(place, a.magic);  // (a group of 16 tokens at least)
+                ks = a.k_scale[id * a.ks_block + of * a.ks_group + hk * a.ks_head];
+                vs = a.v_scale[id * a.vs_block + of * a.vs_group + hk * a.vs_head];
+            }
+        }
+    }
+
+    // starts the copies of the next tile, the row's t-th, into a stage
+    __device__ __forceinline__ void copy(const Args<C>& a, int hk, const Request& q, int t, int stage, int lane, bool& bad) {
+        const uint32_t dst = codes + stage * Sh::kStageBytes, bar = bars + stage * 8, info = beside + stage * 144;
+        const int from = 32 - (known << a.boxes_log2);
+        --known;
+        const int first = (q.tile0 + t) * kTile;
+        uint32_t mask = q.len - first < kTile ? (1u << (q.len - first)) - 1u : 0xFFFFu;
+        if (q.start > first) mask &= 0xFFFFu << (q.start - first);
+        if (a.one_scale) {  // and one box
+            const int block = __shfl_sync(0xFFFFFFFFu, id, from), in = __shfl_sync(0xFFFFFFFFu, place, from);
+            const float k = __shfl_sync(0xFFFFFFFFu, ks, from), v = __shfl_sync(0xFFFFFFFFu, vs, from);
+            const bool valid = block >= 0 && block < a.cache.blocks;
+            if (!valid) mask = 0u, bad = true;
+            if (lane == 0) {
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %1};" ::"r"(info), "r"(mask), "r"(__float_as_uint(k)), "r"(__float_as_uint(v)) : "memory");
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(valid ? kTile * 2 * kHalves * kInner : 0) : "memory");
+                if (valid) {
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h) {
+                        tma_load_4d(dst + h * (kTile * 128), &a.k_map, h * 128, hk, in, block, bar);
+                        tma_load_4d(dst + h * (kTile * 128) + kTile * Sh::kRowBytes, &a.v_map, h * 128, hk, in, block, bar);
+                    }
+                }
+            }
+            return;
+        }
+        const int u = kTile >> a.boxes_log2, mine = lane & 15, box = from + mine / u;
+        const int block = __shfl_sync(0xFFFFFFFFu, id, box), in = __shfl_sync(0xFFFFFFFFu, place, box) + (mine & (u - 1));
+        const bool seen = (mask >> mine) & 1u, valid = seen && block >= 0 && block < a.cache.blocks;
+        bad |= seen && !valid;
+        mask = __ballot_sync(0xFFFFFFFFu, valid) & 0xFFFFu;
+        {
+            const int64_t of = a.magic ? static_cast<int>(__umulhi(in, a.magic)) : in, at = valid ? block : 0;
+            const float* src = lane < 16 ? a.k_scale + at * a.ks_block + of * a.ks_group + hk * a.ks_head
+                                         : a.v_scale + at * a.vs_block + of * a.vs_group + hk * a.vs_head;
+            cp_async_4_zfill(info + 16 + lane * 4, valid ? src : a.k_scale, valid);
+        }
+        if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(info), "r"(mask) : "memory");
+        if (a.tensor_copies) {
+            // lane i: of box i / (2 kHalves) the key's or the value's, first or second half
+            const uint32_t here = (1u << u) - 1u;
+            if (lane == 0) {
+                const int n = ((mask & here) != 0u) + ((mask >> u) != 0u);
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n * u * 2 * kHalves * kInner) : "memory");
+            }
+            __syncwarp();
+            const int mybox = lane / (2 * kHalves), h = lane / 2 % kHalves;
+            const int b = __shfl_sync(0xFFFFFFFFu, id, (from + mybox) & 31), p = __shfl_sync(0xFFFFFFFFu, place, (from + mybox) & 31);
+            if (mybox < a.boxes && ((mask >> (mybox * u)) & here)) {
+                const uint32_t to = dst + h * (kTile * 128) + mybox * u * kInner;
+                if (lane & 1) tma_load_4d(to + kTile * Sh::kRowBytes, &a.v_map, h * 128, hk, p, b, bar);
+                else tma_load_4d(to, &a.k_map, h * 128, hk, p, b, bar);
+            }
+        } else {
+            const int64_t at = valid ? block : 0, row = valid ? in : 0;
+            const int64_t ko = at * a.cache.k_block + row * a.cache.k_token, vo = at * a.cache.v_block + row * a.cache.v_token;
+            const char* kp = static_cast<const char*>(a.cache.k) + hk * a.cache.k_head;
+            const char* vp = static_cast<const char*>(a.cache.v) + hk * a.cache.v_head;
+            const int chunks = a.cache.dim / 16;
+#pragma unroll
+            for (int i = 0; i < kTile * CH / 32; ++i) {
+                const int r = (i * 32 + lane) / CH, ch = (i * 32 + lane) % CH;
+                const int64_t kr = __shfl_sync(0xFFFFFFFFu, ko, r), vr = __shfl_sync(0xFFFFFFFFu, vo, r);
+                const bool ok = ((mask >> r) & 1u) && ch < chunks;  // (past dim: zeros)
+                const uint32_t to = dst + group_offset<CH>(r, ch);
+                cp_async_16_zfill(to, ok ? kp + kr + ch * 16 : kp, ok);
+                cp_async_16_zfill(to + kTile * Sh::kRowBytes, ok ? vp + vr + ch * 16 : vp, ok);
+            }
+            if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+        }
+    }
+
+    // waits for the codes of a stage (scales of tokens: cp.async groups)
+    __device__ __forceinline__ void wait(int stage, uint32_t parity) {
+        const uint32_t bar = bars + stage * 8;
+        for (int i = 0; !late; ++i) {
+            uint32_t done;
+            asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                         : "=r"(done)
+                         : "r"(bar), "r"(parity), "r"(100000u)
+                         : "memory");
+            if (done) return;
+            late = i >= 8192;
+        }
+    }
+};
+
 // Columns of a ring past dim are never copied: zeroed once.
 __device__ __forceinline__ void clear_ring(uint8_t* smem, int bytes, int thread, int threads) {
     for (int i = thread; i < bytes / 16; i += threads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -772,10 +1043,10 @@ struct Segment {
 
 template <int C, int DP, int NT>
 __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
-    k_attention_shares(const Args<C> a, const JoinPlan jp) {
+    k_attention_shares(const __grid_constant__ Args<C> a, const JoinPlan jp) {
     using Sh = AttnShape<C, DP, NT>;
     constexpr int S = Sh::kStages, HEADS = Sh::kHeads, W = Sh::kShareWarps;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint32_t tile_mask[W][S];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int worker = blockIdx.x * W + warp;
@@ -783,7 +1054,11 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
     const int rows = jp.rows;
     bool bad = false;
 
-    if (a.cache.dim != DP) {
+    GroupRing<C, DP, NT> groups;
+    if constexpr (by_group(C)) {
+        groups.open(smem_addr(smem), warp, W, S, lane);
+        if (a.tensor_copies && threadIdx.x == 0) prefetch_tensor_map(&a.k_map), prefetch_tensor_map(&a.v_map);
+    } else if (a.cache.dim != DP) {
         clear_ring(smem, Sh::kSmem, threadIdx.x, W * 32);
         __syncthreads();
     }
@@ -916,53 +1191,52 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
     Segment ahead = seg;
     int ahead_t = seg.t0, ahead_hk = heads_of<C, HEADS>(a, seg.row).hk;
     bool more = live;
-    if (more) copy.look_up(a, ahead.b, ahead.q, ahead_t, ahead.t1, 1, lane);
-    // One step of the loop copies a tile and, once the ring is full, works on
-    // the oldest one.
+    auto look_up = [&] {
+        if constexpr (by_group(C)) groups.look_up(a, ahead.b, ahead_hk, ahead.q.tile0, ahead.q.start, ahead.q.len, ahead_t, ahead.t1, 1, lane);
+        else copy.look_up(a, ahead.b, ahead.q, ahead_t, ahead.t1, 1, lane);
+    };
+    if (more) look_up();
     int t = seg.t0, put = 0, slot = 0, primed = 0;
     bool fresh = true;  // the next tile is the first of its row here
     Heads hd{};
-    while (live) {
-        if (fresh) {
-            // the queries are requested before the tiles, which they would queue behind
-            fresh = false;
-            hd = heads_of<C, HEADS>(a, seg.row);
-            math.begin(a, seg.b, hd, lane);
-            // and those of the row after this one brought to L2
-            const int after_b = seg.row + 1 < rows ? seg.b : seg.b + 1;
-            if (after_b < a.B) {
-                const Heads h = heads_of<C, HEADS>(a, seg.row + 1 < rows ? seg.row + 1 : 0);
-                constexpr int kLines = (DP + 63) / 64;
-                for (int i = lane; i < h.n * kLines; i += 32)
-                    if ((i % kLines) * 64 < a.cache.dim)
-                        prefetch_l2(query_of<C>(a, after_b, h, i / kLines) + (i % kLines) * 64);
-            }
+    auto begin_row = [&] {
+        // the queries are requested before the tiles, which they would queue behind
+        fresh = false;
+        hd = heads_of<C, HEADS>(a, seg.row);
+        math.begin(a, seg.b, hd, lane);
+        // and those of the row after this one brought to L2
+        const int after_b = seg.row + 1 < rows ? seg.b : seg.b + 1;
+        if (after_b < a.B) {
+            const Heads h = heads_of<C, HEADS>(a, seg.row + 1 < rows ? seg.row + 1 : 0);
+            constexpr int kLines = (DP + 63) / 64;
+            for (int i = lane; i < h.n * kLines; i += 32)
+                if ((i % kLines) * 64 < a.cache.dim) prefetch_l2(query_of<C>(a, after_b, h, i / kLines) + (i % kLines) * 64);
         }
-        const bool full = primed == S - 1;
-        if (full) cp_async_wait_group<S - 2>();
-        __syncwarp();
+    };
+    // starts the copies of the next tile, if there is one
+    auto copy_next = [&] {
         if (more) {
-            const uint32_t mask = copy.copy(a, ahead_hk, ahead.q, ahead_t, 1, ring + put * Sh::kStageBytes, lane, bad);
-            if (lane == 0) tile_mask[warp][put] = mask;
+            if constexpr (by_group(C)) {
+                groups.copy(a, ahead_hk, ahead.q, ahead_t, put, lane, bad);
+            } else {
+                const uint32_t mask = copy.copy(a, ahead_hk, ahead.q, ahead_t, 1, ring + put * Sh::kStageBytes, lane, bad);
+                if (lane == 0) tile_mask[warp][put] = mask;
+            }
             bool look = false;
             if (++ahead_t >= ahead.t1) {
                 more = look = next_segment(ahead);
                 ahead_t = ahead.t0;
                 ahead_hk = heads_of<C, HEADS>(a, ahead.row).hk;
             }
-            if (more && (look || copy.wants(a, ahead_t, 1))) copy.look_up(a, ahead.b, ahead.q, ahead_t, ahead.t1, 1, lane);
+            if constexpr (by_group(C)) look |= groups.known == 0;
+            else look |= copy.wants(a, ahead_t, 1);
+            if (more && look) look_up();
         }
         cp_async_commit();
         put = put + 1 == S ? 0 : put + 1;
-        if (!full) {
-            ++primed;
-            continue;
-        }
-        if (t == seg.t0) math.ready(a, hd.hk, seg.q.len, lane);
-        math.tile(a, seg.q, ring + slot * Sh::kStageBytes, tile_mask[warp][slot], (seg.q.tile0 + t) * kTile, lane);
-        slot = slot + 1 == S ? 0 : slot + 1;
-        if (++t < seg.t1) continue;
-
+    };
+    // the row's tiles here are done: its result or its part
+    auto end_row = [&] {
         math.reduce();
         const bool begins = seg.t0 == 0, ends = seg.t1 == seg.q.tiles;
         if (begins && ends) {
@@ -978,6 +1252,60 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
         live = next_segment(seg);
         t = seg.t0;
         fresh = true;
+    };
+    if constexpr (by_group(C)) {
+        // A step works on the oldest tiles, one or two of a row, and copies as many into their
+        // places.  S groups of copies are on their way before it, empty ones among them.
+        constexpr int P = Sh::kPair;
+        uint32_t parity = 0u;
+        while (live) {
+            if (fresh) begin_row();
+            for (; primed < S; ++primed) copy_next();
+            const bool pair = P == 2 && seg.t1 - t >= 2;
+            const int next = slot + 1 == S ? 0 : slot + 1;
+            if (pair) cp_async_wait_group<S - 2>();
+            else cp_async_wait_group<S - 1>();
+            groups.wait(slot, parity);
+            if (pair) groups.wait(next, parity ^ (next == 0 ? 1u : 0u));
+            __syncwarp();
+            if (t == seg.t0) math.ready(a, hd.hk, seg.q.len, lane);
+            const int first = (seg.q.tile0 + t) * kTile;
+            const uint32_t kt = groups.codes + slot * Sh::kStageBytes, info = groups.beside + slot * 144;
+            bool both = false;
+            if constexpr (P == 2) {
+                both = pair;
+                if (pair)
+                    math.template tiles<2>(a, seg.q, {kt, groups.codes + next * Sh::kStageBytes}, {info, groups.beside + next * 144},
+                                           {first, first + kTile}, lane);
+            }
+            if (!both) math.template tiles<1>(a, seg.q, {kt}, {info}, {first}, lane);
+            __syncwarp();
+            for (int i = 0; i < (pair ? 2 : 1); ++i) {
+                copy_next();
+                if (++slot == S) slot = 0, parity ^= 1u;
+                ++t;
+            }
+            if (t >= seg.t1) end_row();
+        }
+        if (groups.late) raise_device_error(a.err, W4A16_DEVERR_TIMEOUT);
+    } else {
+        // One step of the loop copies a tile and, once the ring is full, works on
+        // the oldest one.
+        while (live) {
+            if (fresh) begin_row();
+            const bool full = primed == S - 1;
+            if (full) cp_async_wait_group<S - 2>();
+            __syncwarp();
+            copy_next();
+            if (!full) {
+                ++primed;
+                continue;
+            }
+            if (t == seg.t0) math.ready(a, hd.hk, seg.q.len, lane);
+            math.tile(ring + slot * Sh::kStageBytes, tile_mask[warp][slot], lane);
+            slot = slot + 1 == S ? 0 : slot + 1;
+            if (++t >= seg.t1) end_row();
+        }
     }
     cp_async_wait_group<0>();
     if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
@@ -1121,10 +1449,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Args<C> a
 // warps.
 template <int C, int DP, int NT>
 __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kRowWarps * 32), 1)
-    k_attention_rows(const Args<C> a, const int rows, const int wpr, const int cluster) {
+    k_attention_rows(const __grid_constant__ Args<C> a, const int rows, const int wpr, const int cluster) {
     using Sh = AttnShape<C, DP, NT>;
     constexpr int S = Sh::kRowStages, HEADS = Sh::kHeads, KS = Sh::kSteps, W = Sh::kRowWarps;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem_all[];
+    uint8_t* const smem = smem_all + (by_group(C) ? (0u - smem_addr(smem_all)) & 1023u : 0u);
     __shared__ uint32_t tile_mask[W][S];
     __shared__ __align__(8) float part_m[W][HEADS], part_l[W][HEADS], part_f[W][HEADS], cta_m[HEADS], cta_l[HEADS], cta_f[8][HEADS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1135,7 +1464,11 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kRowWarps * 32), 1)
     const unsigned id = cluster > 1 ? blockIdx.x / static_cast<unsigned>(cluster) : (blockIdx.x * W + warp) / static_cast<unsigned>(wpr);
     const int b = static_cast<int>(id / static_cast<unsigned>(rows)), row = static_cast<int>(id - b * static_cast<unsigned>(rows));
     bool bad = false;
-    if (a.cache.dim != DP) {
+    GroupRing<C, DP, NT> groups;
+    if constexpr (by_group(C)) {
+        groups.open(smem_addr(smem), warp, W, S, lane);
+        if (a.tensor_copies && threadIdx.x == 0) prefetch_tensor_map(&a.k_map), prefetch_tensor_map(&a.v_map);
+    } else if (a.cache.dim != DP) {
         clear_ring(smem, Sh::kRowSmem, threadIdx.x, W * 32);
         __syncthreads();
     }
@@ -1148,35 +1481,88 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kRowWarps * 32), 1)
     TileCopy<C, DP, NT> copy;
     Request q{};
     if (b < a.B) {
-        const bool early = a.window == 0 && TileCopy<C, DP, NT>::aligned(a);
-        if (early) copy.look_up(a, b, q, first_tile, (a.most + kTile - 1) / kTile, step, lane);
+        const bool early = a.window == 0 && (by_group(C) || TileCopy<C, DP, NT>::aligned(a));
+        const int most_tiles = (a.most + kTile - 1) / kTile;
+        if constexpr (by_group(C)) {
+            if (early) groups.look_up(a, b, hd.hk, 0, 0, a.most, first_tile, most_tiles, step, lane);
+        } else {
+            if (early) copy.look_up(a, b, q, first_tile, most_tiles, step, lane);
+        }
         math.begin(a, b, hd, lane);
         q = request_of<C>(a, b, bad);
-        if (!early) copy.look_up(a, b, q, first_tile, q.tiles, step, lane);
+        if constexpr (by_group(C)) {
+            if (!early) groups.look_up(a, b, hd.hk, q.tile0, q.start, q.len, first_tile, q.tiles, step, lane);
+        } else {
+            if (!early) copy.look_up(a, b, q, first_tile, q.tiles, step, lane);
+        }
         if (q.tiles == 0 && rank == 0) store_empty<C>(a, b, hd, wir * 32 + lane, wpr * 32);
     }
     if (first_tile < q.tiles) {
         int ahead = first_tile, put = 0, slot = 0, primed = 0;
-        for (int t = first_tile; t < q.tiles;) {
-            const bool full = primed == S - 1;
-            if (full) cp_async_wait_group<S - 2>();
-            __syncwarp();
+        auto copy_next = [&] {
             if (ahead < q.tiles) {
-                const uint32_t mask = copy.copy(a, hd.hk, q, ahead, step, ring + put * Sh::kStageBytes, lane, bad);
-                if (lane == 0) tile_mask[warp][put] = mask;
+                if constexpr (by_group(C)) {
+                    groups.copy(a, hd.hk, q, ahead, put, lane, bad);
+                } else {
+                    const uint32_t mask = copy.copy(a, hd.hk, q, ahead, step, ring + put * Sh::kStageBytes, lane, bad);
+                    if (lane == 0) tile_mask[warp][put] = mask;
+                }
                 ahead += step;
-                if (ahead < q.tiles && copy.wants(a, ahead, step)) copy.look_up(a, b, q, ahead, q.tiles, step, lane);
+                if constexpr (by_group(C)) {
+                    if (ahead < q.tiles && groups.known == 0) groups.look_up(a, b, hd.hk, q.tile0, q.start, q.len, ahead, q.tiles, step, lane);
+                } else {
+                    if (ahead < q.tiles && copy.wants(a, ahead, step)) copy.look_up(a, b, q, ahead, q.tiles, step, lane);
+                }
             }
             cp_async_commit();
             put = put + 1 == S ? 0 : put + 1;
-            if (!full) {
-                ++primed;
-                continue;
+        };
+        if constexpr (by_group(C)) {
+            constexpr int P = Sh::kPair;
+            uint32_t parity = 0u;
+            for (; primed < S; ++primed) copy_next();
+            for (int t = first_tile; t < q.tiles;) {
+                const bool pair = P == 2 && t + step < q.tiles;
+                const int next = slot + 1 == S ? 0 : slot + 1;
+                if (pair) cp_async_wait_group<S - 2>();
+                else cp_async_wait_group<S - 1>();
+                groups.wait(slot, parity);
+                if (pair) groups.wait(next, parity ^ (next == 0 ? 1u : 0u));
+                __syncwarp();
+                if (t == first_tile) math.ready(a, hd.hk, q.len, lane);
+                const int first = (q.tile0 + t) * kTile;
+                const uint32_t kt = groups.codes + slot * Sh::kStageBytes, info = groups.beside + slot * 144;
+                bool both = false;
+                if constexpr (P == 2) {
+                    both = pair;
+                    if (pair)
+                        math.template tiles<2>(a, q, {kt, groups.codes + next * Sh::kStageBytes}, {info, groups.beside + next * 144},
+                                               {first, first + step * kTile}, lane);
+                }
+                if (!both) math.template tiles<1>(a, q, {kt}, {info}, {first}, lane);
+                __syncwarp();
+                for (int i = 0; i < (pair ? 2 : 1); ++i) {
+                    copy_next();
+                    if (++slot == S) slot = 0, parity ^= 1u;
+                    t += step;
+                }
             }
-            if (t == first_tile) math.ready(a, hd.hk, q.len, lane);
-            math.tile(a, q, ring + slot * Sh::kStageBytes, tile_mask[warp][slot], (q.tile0 + t) * kTile, lane);
-            slot = slot + 1 == S ? 0 : slot + 1;
-            t += step;
+            if (groups.late) raise_device_error(a.err, W4A16_DEVERR_TIMEOUT);
+        } else {
+            for (int t = first_tile; t < q.tiles;) {
+                const bool full = primed == S - 1;
+                if (full) cp_async_wait_group<S - 2>();
+                __syncwarp();
+                copy_next();
+                if (!full) {
+                    ++primed;
+                    continue;
+                }
+                if (t == first_tile) math.ready(a, hd.hk, q.len, lane);
+                math.tile(ring + slot * Sh::kStageBytes, tile_mask[warp][slot], lane);
+                slot = slot + 1 == S ? 0 : slot + 1;
+                t += step;
+            }
         }
         cp_async_wait_group<0>();
         __syncwarp();

@@ -2,6 +2,8 @@
 // (append that finds the scales, read, attention).  Internal to the library.
 #pragma once
 
+#include <cuda.h>  // CUtensorMap
+
 #include "paged.h"
 
 namespace w4a16 {
@@ -65,7 +67,19 @@ struct ScaledAttentionArgs : AttentionArgs {
     int64_t ks_block, ks_group, ks_head, vs_block, vs_group, vs_head;
     int group;
     uint32_t magic;  // of group
+    // A tile of 16 tokens is one box, or 2^boxes_log2 = boxes of them, that lies in one block;
+    // tensor_copies: its codes come by tensor copies (boxes of 16 or 8 tokens); one_scale: it is one
+    // box and lies in one group.
+    int boxes, boxes_log2, tensor_copies, one_scale;
+    CUtensorMap k_map;  // boxes of one head's values by `box` tokens of a block
+    CUtensorMap v_map;
 };
+
+// The tensor map of keys or values: boxes of `inner` codes (64 or 128, their swizzle) of a
+// head by `box` tokens of a block; codes past dim read as zeros.  False where there is none
+// for these strides.
+bool encode_cache_map(CUtensorMap* map, const void* codes, const w4a16_scaled_cache& c, int64_t block, int64_t token, int64_t head, int inner,
+                      int box);
 
 cudaError_t launch_scaled_attention(const ScaledAttentionArgs& a, int int8, const DeviceInfo& dev, cudaStream_t s);
 

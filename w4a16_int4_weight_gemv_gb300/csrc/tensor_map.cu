@@ -16,6 +16,7 @@
 #include <cuda_runtime.h>
 
 #include "launch.h"
+#include "scaled.h"
 
 namespace w4a16 {
 namespace {
@@ -53,6 +54,23 @@ bool encode_weight_map(CUtensorMap* map, const void* wq, int N, int K, unsigned 
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(wq), dims, strides, box,
               elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_cache_map(CUtensorMap* map, const void* codes, const w4a16_scaled_cache& c, int64_t block, int64_t token, int64_t head, int inner,
+                      int box) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.dim), static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.page),
+                                static_cast<cuuint64_t>(c.blocks)};
+    // bytes from one head, token and block to the next; of a single one any
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.heads > 1 ? head : c.dim), static_cast<cuuint64_t>(c.page > 1 ? token : c.dim),
+                                   static_cast<cuuint64_t>(c.blocks > 1 ? block : c.dim)};
+    for (cuuint64_t s : strides)
+        if (s == 0 || s >= (cuuint64_t(1) << 40)) return false;
+    const cuuint32_t boxes[4] = {static_cast<cuuint32_t>(inner), 1, static_cast<cuuint32_t>(box), 1}, ones[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(codes), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              inner == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace w4a16
