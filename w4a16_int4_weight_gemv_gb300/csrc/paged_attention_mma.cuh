@@ -232,6 +232,13 @@ __device__ __forceinline__ int new_tokens(const Args<C>& a) {
     else return 1;
 }
 
+// Whether a tile lies in one group.
+template <int C>
+__device__ __forceinline__ bool one_scale(const Args<C>& a) {
+    if constexpr (by_group(C)) return a.one_scale;
+    else return false;
+}
+
 // What one request looks like: its visible tokens [start, len), in tiles from
 // tile0 on (visible to any of its new tokens).
 struct Request {
@@ -943,7 +950,33 @@ struct GroupRing {
         }
     }
 
-    // starts the copies of the next tile, the row's t-th, into a stage
+    // one_scale: starts the copies of the next n tiles, the row's t-th and n - 1 more step
+    // apart, into stages from `stage` of S on.  Each by the lane that holds its id.
+    __device__ __forceinline__ void copy_whole(const Args<C>& a, int hk, const Request& q, int t, int step, int n, int stage, int S, int lane, bool& bad) {
+        const int j = lane - (32 - known);
+        known -= n;
+        if (static_cast<unsigned>(j) < static_cast<unsigned>(n)) {
+            const int left = q.len - (q.tile0 + t + j * step) * kTile, before = q.start + left - q.len;  // tokens from the tile's first on; not seen
+            uint32_t mask = left < kTile ? (1u << left) - 1u : 0xFFFFu;
+            if (before > 0) mask &= 0xFFFFu << before;
+            const bool valid = id >= 0 && id < a.cache.blocks;
+            if (!valid) mask = 0u, bad = true;
+            int at = stage + j;
+            if (at >= S) at -= S;
+            const uint32_t dst = codes + at * Sh::kStageBytes, bar = bars + at * 8;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %1};" ::"r"(beside + at * 144), "r"(mask), "r"(__float_as_uint(ks)), "r"(__float_as_uint(vs)) : "memory");
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(valid ? kTile * 2 * kHalves * kInner : 0) : "memory");
+            if (valid) {
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) {
+                    tma_load_4d(dst + h * (kTile * 128), &a.k_map, h * 128, hk, place, id, bar);
+                    tma_load_4d(dst + h * (kTile * 128) + kTile * Sh::kRowBytes, &a.v_map, h * 128, hk, place, id, bar);
+                }
+            }
+        }
+    }
+
+    // else: those of the next tile, the row's t-th, into a stage
     __device__ __forceinline__ void copy(const Args<C>& a, int hk, const Request& q, int t, int stage, int lane, bool& bad) {
         const uint32_t dst = codes + stage * Sh::kStageBytes, bar = bars + stage * 8, info = beside + stage * 144;
         const int from = 32 - (known << a.boxes_log2);
@@ -951,24 +984,6 @@ struct GroupRing {
         const int first = (q.tile0 + t) * kTile;
         uint32_t mask = q.len - first < kTile ? (1u << (q.len - first)) - 1u : 0xFFFFu;
         if (q.start > first) mask &= 0xFFFFu << (q.start - first);
-        if (a.one_scale) {  // and one box
-            const int block = __shfl_sync(0xFFFFFFFFu, id, from), in = __shfl_sync(0xFFFFFFFFu, place, from);
-            const float k = __shfl_sync(0xFFFFFFFFu, ks, from), v = __shfl_sync(0xFFFFFFFFu, vs, from);
-            const bool valid = block >= 0 && block < a.cache.blocks;
-            if (!valid) mask = 0u, bad = true;
-            if (lane == 0) {
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %1};" ::"r"(info), "r"(mask), "r"(__float_as_uint(k)), "r"(__float_as_uint(v)) : "memory");
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(valid ? kTile * 2 * kHalves * kInner : 0) : "memory");
-                if (valid) {
-#pragma unroll
-                    for (int h = 0; h < kHalves; ++h) {
-                        tma_load_4d(dst + h * (kTile * 128), &a.k_map, h * 128, hk, in, block, bar);
-                        tma_load_4d(dst + h * (kTile * 128) + kTile * Sh::kRowBytes, &a.v_map, h * 128, hk, in, block, bar);
-                    }
-                }
-            }
-            return;
-        }
         const int u = kTile >> a.boxes_log2, mine = lane & 15, box = from + mine / u;
         const int block = __shfl_sync(0xFFFFFFFFu, id, box), in = __shfl_sync(0xFFFFFFFFu, place, box) + (mine & (u - 1));
         const bool seen = (mask >> mine) & 1u, valid = seen && block >= 0 && block < a.cache.blocks;
@@ -1015,18 +1030,18 @@ struct GroupRing {
         }
     }
 
-    // waits for the codes of a stage (scales of tokens: cp.async groups)
+    __device__ __forceinline__ bool arrived(int stage, uint32_t parity) const {
+        uint32_t done;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(done)
+                     : "r"(bars + stage * 8), "r"(parity), "r"(100000u)
+                     : "memory");
+        return done != 0u;
+    }
+    // waits for the codes of a stage (scales of tokens: cp.async groups), 0.8 s at most
     __device__ __forceinline__ void wait(int stage, uint32_t parity) {
-        const uint32_t bar = bars + stage * 8;
-        for (int i = 0; !late; ++i) {
-            uint32_t done;
-            asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                         : "=r"(done)
-                         : "r"(bar), "r"(parity), "r"(100000u)
-                         : "memory");
-            if (done) return;
-            late = i >= 8192;
-        }
+        if (arrived(stage, parity)) return;
+        for (int i = 0; !late && !arrived(stage, parity); ++i) late = i >= 8192;
     }
 };
 
@@ -1213,17 +1228,29 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
                 if ((i % kLines) * 64 < a.cache.dim) prefetch_l2(query_of<C>(a, after_b, h, i / kLines) + (i % kLines) * 64);
         }
     };
-    // starts the copies of the next tile, if there is one
-    auto copy_next = [&] {
-        if (more) {
+    // starts the copies of the next `n` tiles, as far as there are any
+    auto copy_next = [&](int n) {
+        while (n > 0 && more) {
+            int now = 1;
             if constexpr (by_group(C)) {
-                groups.copy(a, ahead_hk, ahead.q, ahead_t, put, lane, bad);
+                if (a.one_scale) {
+                    now = min(min(n, ahead.t1 - ahead_t), groups.known);
+                    groups.copy_whole(a, ahead_hk, ahead.q, ahead_t, 1, now, put, S, lane, bad);
+                } else {
+                    groups.copy(a, ahead_hk, ahead.q, ahead_t, put, lane, bad);
+                    cp_async_commit();
+                }
             } else {
                 const uint32_t mask = copy.copy(a, ahead_hk, ahead.q, ahead_t, 1, ring + put * Sh::kStageBytes, lane, bad);
                 if (lane == 0) tile_mask[warp][put] = mask;
+                cp_async_commit();
             }
+            n -= now;
+            put += now;
+            if (put >= S) put -= S;
             bool look = false;
-            if (++ahead_t >= ahead.t1) {
+            ahead_t += now;
+            if (ahead_t >= ahead.t1) {
                 more = look = next_segment(ahead);
                 ahead_t = ahead.t0;
                 ahead_hk = heads_of<C, HEADS>(a, ahead.row).hk;
@@ -1232,8 +1259,9 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
             else look |= copy.wants(a, ahead_t, 1);
             if (more && look) look_up();
         }
-        cp_async_commit();
-        put = put + 1 == S ? 0 : put + 1;
+        // (groups of copies are counted, so empty ones in place of those that are not there)
+        if (!by_group(C) || !one_scale<C>(a))
+            for (; n > 0; --n) cp_async_commit();
     };
     // the row's tiles here are done: its result or its part
     auto end_row = [&] {
@@ -1260,11 +1288,13 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
         uint32_t parity = 0u;
         while (live) {
             if (fresh) begin_row();
-            for (; primed < S; ++primed) copy_next();
+            if (!primed) copy_next(S), primed = 1;
             const bool pair = P == 2 && seg.t1 - t >= 2;
             const int next = slot + 1 == S ? 0 : slot + 1;
-            if (pair) cp_async_wait_group<S - 2>();
-            else cp_async_wait_group<S - 1>();
+            if (!one_scale<C>(a)) {
+                if (pair) cp_async_wait_group<S - 2>();
+                else cp_async_wait_group<S - 1>();
+            }
             groups.wait(slot, parity);
             if (pair) groups.wait(next, parity ^ (next == 0 ? 1u : 0u));
             __syncwarp();
@@ -1280,11 +1310,11 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
             }
             if (!both) math.template tiles<1>(a, seg.q, {kt}, {info}, {first}, lane);
             __syncwarp();
-            for (int i = 0; i < (pair ? 2 : 1); ++i) {
-                copy_next();
-                if (++slot == S) slot = 0, parity ^= 1u;
-                ++t;
-            }
+            const int done = pair ? 2 : 1;
+            copy_next(done);
+            t += done;
+            slot += done;
+            if (slot >= S) slot -= S, parity ^= 1u;
             if (t >= seg.t1) end_row();
         }
         if (groups.late) raise_device_error(a.err, W4A16_DEVERR_TIMEOUT);
@@ -1296,7 +1326,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
             const bool full = primed == S - 1;
             if (full) cp_async_wait_group<S - 2>();
             __syncwarp();
-            copy_next();
+            copy_next(1);
             if (!full) {
                 ++primed;
                 continue;
@@ -1499,33 +1529,46 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kRowWarps * 32), 1)
     }
     if (first_tile < q.tiles) {
         int ahead = first_tile, put = 0, slot = 0, primed = 0;
-        auto copy_next = [&] {
-            if (ahead < q.tiles) {
+        auto copy_next = [&](int n) {
+            while (n > 0 && ahead < q.tiles) {
+                int now = 1;
                 if constexpr (by_group(C)) {
-                    groups.copy(a, hd.hk, q, ahead, put, lane, bad);
+                    if (a.one_scale) {
+                        now = min(min(n, (q.tiles - ahead + step - 1) / step), groups.known);
+                        groups.copy_whole(a, hd.hk, q, ahead, step, now, put, S, lane, bad);
+                    } else {
+                        groups.copy(a, hd.hk, q, ahead, put, lane, bad);
+                        cp_async_commit();
+                    }
                 } else {
                     const uint32_t mask = copy.copy(a, hd.hk, q, ahead, step, ring + put * Sh::kStageBytes, lane, bad);
                     if (lane == 0) tile_mask[warp][put] = mask;
+                    cp_async_commit();
                 }
-                ahead += step;
+                n -= now;
+                put += now;
+                if (put >= S) put -= S;
+                ahead += now * step;
                 if constexpr (by_group(C)) {
                     if (ahead < q.tiles && groups.known == 0) groups.look_up(a, b, hd.hk, q.tile0, q.start, q.len, ahead, q.tiles, step, lane);
                 } else {
                     if (ahead < q.tiles && copy.wants(a, ahead, step)) copy.look_up(a, b, q, ahead, q.tiles, step, lane);
                 }
             }
-            cp_async_commit();
-            put = put + 1 == S ? 0 : put + 1;
+            if (!by_group(C) || !one_scale<C>(a))
+                for (; n > 0; --n) cp_async_commit();
         };
         if constexpr (by_group(C)) {
             constexpr int P = Sh::kPair;
             uint32_t parity = 0u;
-            for (; primed < S; ++primed) copy_next();
+            copy_next(S);
             for (int t = first_tile; t < q.tiles;) {
                 const bool pair = P == 2 && t + step < q.tiles;
                 const int next = slot + 1 == S ? 0 : slot + 1;
-                if (pair) cp_async_wait_group<S - 2>();
-                else cp_async_wait_group<S - 1>();
+                if (!one_scale<C>(a)) {
+                    if (pair) cp_async_wait_group<S - 2>();
+                    else cp_async_wait_group<S - 1>();
+                }
                 groups.wait(slot, parity);
                 if (pair) groups.wait(next, parity ^ (next == 0 ? 1u : 0u));
                 __syncwarp();
@@ -1541,11 +1584,11 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kRowWarps * 32), 1)
                 }
                 if (!both) math.template tiles<1>(a, q, {kt}, {info}, {first}, lane);
                 __syncwarp();
-                for (int i = 0; i < (pair ? 2 : 1); ++i) {
-                    copy_next();
-                    if (++slot == S) slot = 0, parity ^= 1u;
-                    t += step;
-                }
+                const int done = pair ? 2 : 1;
+                copy_next(done);
+                t += done * step;
+                slot += done;
+                if (slot >= S) slot -= S, parity ^= 1u;
             }
             if (groups.late) raise_device_error(a.err, W4A16_DEVERR_TIMEOUT);
         } else {
@@ -1553,7 +1596,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kRowWarps * 32), 1)
                 const bool full = primed == S - 1;
                 if (full) cp_async_wait_group<S - 2>();
                 __syncwarp();
-                copy_next();
+                copy_next(1);
                 if (!full) {
                     ++primed;
                     continue;
