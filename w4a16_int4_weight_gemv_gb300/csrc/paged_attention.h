@@ -42,6 +42,9 @@ struct JoinPlan {
     // [warp][2][heads * (padded + 2)]; place 0: the row that the warp's share begins inside
     // of, 1: the row it ends inside of
     float* part;
+    // Scales by group: the parts of a CTA's warps are joined in it, to parts [CTA][2]; joins name
+    // CTAs, one entry per row or CTA; part: [warp], those that a warp has besides its last one.
+    float* cta_part;
     int by_row;
     int rows;   // of a request: key/value heads times chunks of the query heads sharing one
     int warps;  // of the first launch

@@ -1050,6 +1050,68 @@ __device__ __forceinline__ void clear_ring(uint8_t* smem, int bytes, int thread,
     for (int i = thread; i < bytes / 16; i += threads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
+template <int C>
+__device__ __forceinline__ void store_lse(const Args<C>& a, int b, const Heads& hd, int h, float m, float l) {
+    if (a.lse && h < hd.n) *lse_at<C>(a, b, hd, h) = lse_of<C>(m, l);
+}
+
+// The factors of up to eight parts of a head, one lane each (lanes 8 h .. 8 h + 7
+// of a warp); m and l become those of all parts.
+__device__ __forceinline__ float join_factor(float& m, float& l) {
+    float top = m, all;
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));  // of an empty part: -infinity
+    const float f = l != 0.f ? part_factor(m, top) : 0.f;
+    all = l * f;
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2) all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
+    m = top, l = all;
+    return f;
+}
+__device__ __forceinline__ void add_scaled(float4& o, const float4& x, float2 f) {
+    o.x = fmaf(x.x, f.x, o.x), o.y = fmaf(x.y, f.y, o.y);
+    o.z = fmaf(x.z, f.x, o.z), o.w = fmaf(x.w, f.y, o.w);
+}
+
+// A part's 16 dims of 8 heads, with what joining them takes: m and l of the
+// lane's two heads.
+struct DimPart {
+    float4 o;
+    float m[2], l[2];
+    __device__ __forceinline__ void clear() {
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+    }
+    __device__ __forceinline__ void add(const float4& x, float2 xm, float2 xl) {
+        const float pm[2] = {xm.x, xm.y}, pl[2] = {xl.x, xl.y};
+        float f0[2], f1[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float top = pl[e] != 0.f ? fmaxf(m[e], pm[e]) : m[e];
+            f0[e] = part_factor(m[e], top);
+            f1[e] = pl[e] != 0.f ? part_factor(pm[e], top) : 0.f;
+            m[e] = top;
+            l[e] = l[e] * f0[e] + pl[e] * f1[e];
+        }
+        o.x = o.x * f0[0] + x.x * f1[0], o.y = o.y * f0[1] + x.y * f1[1];
+        o.z = o.z * f0[0] + x.z * f1[0], o.w = o.w * f0[1] + x.w * f1[1];
+    }
+    // the result: dims of step k, heads of block n
+    template <int C>
+    __device__ __forceinline__ void finish(const Args<C>& a, int b, const Heads& hd, int n, int k, int lane) const {
+        const int r = lane >> 2, c = lane & 3;
+        const float vs = C == kE4m3 ? a.cache.v_scale[hd.hk] : 1.f;
+        const float f0 = l[0] != 0.f ? vs / l[0] : 0.f, f1 = l[1] != 0.f ? vs / l[1] : 0.f;
+        const bool have = n * 8 + r < hd.n && k * 16 < a.cache.dim;
+        store_dims<C>(o, f0, f1, have ? out_of<C>(a, b, hd, n * 8 + r) + k * 16 : nullptr, c);
+        if (k == 0 && r == 0) {
+            store_lse<C>(a, b, hd, n * 8 + 2 * c, m[0], l[0]);
+            store_lse<C>(a, b, hd, n * 8 + 2 * c + 1, m[1], l[1]);
+        }
+    }
+};
+
 // The tiles [t0, t1) of one row, and where the row begins among all costs.
 struct Segment {
     int at, b, row, t0, t1;
@@ -1130,10 +1192,23 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
     int workers = min((total + kMinCost - 1) / kMinCost, jp.warps);
     // one request: rows of one length, so a multiple of them splits none unevenly
     if (a.B == 1 && workers > rows) workers -= workers % rows;
-    if (!jp.by_row && lane == 0) jp.joins[worker] = make_int4(-1, 0, 0, 0);
-    if (worker >= workers) {
-        if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
-        return;
+    // Scales by group: the parts of a CTA's warps are joined here, so that few are left for the
+    // join launch.  A warp's: of the row that its share begins inside of, and of the row it ends
+    // inside of ({request or -1: none, row, whether the row ends here, whether the part is in the
+    // ring}); `spill`: for the join launch, the row that begins here and goes on in another CTA.
+    __shared__ int4 notes[by_group(C) ? W : 1][2];
+    __shared__ int4 spill;
+    if constexpr (by_group(C)) {
+        if (lane < 2) notes[warp][lane] = make_int4(-1, 0, 0, 0);
+        if (threadIdx.x == 0) spill = make_int4(-1, 0, 0, 0);
+        __syncthreads();
+        if (workers == 0) workers = 1;  // (nothing to do: no row is found)
+    } else {
+        if (!jp.by_row && lane == 0) jp.joins[worker] = make_int4(-1, 0, 0, 0);
+        if (worker >= workers) {
+            if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
+            return;
+        }
     }
     // costs before worker i: equal shares, the remainder to the first ones
     const unsigned share = static_cast<unsigned>(total) / static_cast<unsigned>(workers), extra = total - share * workers;
@@ -1190,7 +1265,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
         return true;
     };
     Segment seg{};
-    bool live = u1 > u0 && locate(u0, seg.b, seg.at);
+    bool live = u1 > u0 && (!by_group(C) || worker < workers) && locate(u0, seg.b, seg.at);
     if (live) {
         seg.q = request_of<C>(a, seg.b, bad);
         seg.row = static_cast<unsigned>(u0 - seg.at) / static_cast<unsigned>(seg.q.tiles + kRowCost);
@@ -1264,20 +1339,42 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
             for (; n > 0; --n) cp_async_commit();
     };
     // the row's tiles here are done: its result or its part
+    uint8_t* const rings = smem + (by_group(C) ? (0u - smem_addr(smem)) & 1023u : 0u);
     auto end_row = [&] {
         math.reduce();
         const bool begins = seg.t0 == 0, ends = seg.t1 == seg.q.tiles;
-        if (begins && ends) {
-            math.finish(a, seg.b, hd, lane);
+        if constexpr (by_group(C)) {
+            const int b = seg.b, row = seg.row;
+            // a row that begins here: what the join launch has to do for it
+            if (begins && lane == 0) {
+                const int last = (ends ? worker : worker_of(seg.at + kRowCost + seg.q.tiles - 1)) / W;
+                int4 join = make_int4(-1, 0, 0, 0);
+                if (last != static_cast<int>(blockIdx.x)) spill = join = make_int4(b, row, blockIdx.x, last);
+                if (jp.by_row) jp.joins[b * rows + row] = join;
+            }
+            live = next_segment(seg);
+            if (begins && ends) {
+                math.finish(a, b, hd, lane);
+            } else {
+                // (the ring is empty once nothing follows)
+                float* part = live ? jp.part + static_cast<int64_t>(worker) * Sh::kPartFloats
+                                   : reinterpret_cast<float*>(rings + warp * S * Sh::kStageBytes);
+                math.store_part(part, part + HEADS * DP, part + HEADS * (DP + 1), lane);
+                if (lane == 0) notes[warp][begins] = make_int4(b, row, ends, !live);
+            }
         } else {
-            float* part = jp.part + (static_cast<int64_t>(worker) * 2 + (begins ? 1 : 0)) * Sh::kPartFloats;
-            math.store_part(part, part + HEADS * DP, part + HEADS * (DP + 1), lane);
+            if (begins && ends) {
+                math.finish(a, seg.b, hd, lane);
+            } else {
+                float* part = jp.part + (static_cast<int64_t>(worker) * 2 + (begins ? 1 : 0)) * Sh::kPartFloats;
+                math.store_part(part, part + HEADS * DP, part + HEADS * (DP + 1), lane);
+            }
+            // a row that begins here: what the join launch has to do for it
+            if (begins && lane == 0 && (jp.by_row || !ends))
+                jp.joins[jp.by_row ? seg.b * rows + seg.row : worker] =
+                    ends ? make_int4(-1, 0, 0, 0) : make_int4(seg.b, seg.row, worker, worker_of(seg.at + kRowCost + seg.q.tiles - 1));
+            live = next_segment(seg);
         }
-        // a row that begins here: what the join launch has to do for it
-        if (begins && lane == 0 && (jp.by_row || !ends))
-            jp.joins[jp.by_row ? seg.b * rows + seg.row : worker] =
-                ends ? make_int4(-1, 0, 0, 0) : make_int4(seg.b, seg.row, worker, worker_of(seg.at + kRowCost + seg.q.tiles - 1));
-        live = next_segment(seg);
         t = seg.t0;
         fresh = true;
     };
@@ -1318,6 +1415,42 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
             if (t >= seg.t1) end_row();
         }
         if (groups.late) raise_device_error(a.err, W4A16_DEVERR_TIMEOUT);
+        if (!a.one_scale) cp_async_wait_group<0>();
+        __syncthreads();
+        if (!jp.by_row && threadIdx.x == 0) jp.joins[blockIdx.x] = spill;
+        // the row that comes from the preceding CTA, then those that begin in a warp's share and go on
+        for (int i = -1; i < W; ++i) {
+            const int from = i < 0 ? 0 : i, place = i < 0 ? 0 : 1;
+            const int4 head = notes[from][place];
+            if (head.x < 0) continue;
+            int to = from;
+            bool ends = head.z;
+            while (!ends && to + 1 < W && notes[to + 1][0].x >= 0) ends = notes[++to][0].z;
+            const bool whole = place == 1 && ends;
+            float* const out = jp.cta_part + (static_cast<int64_t>(blockIdx.x) * 2 + place) * Sh::kPartFloats;
+            for (int unit = threadIdx.x; unit < HEADS * DP / 4; unit += W * 32) {  // accumulator: (head block n, step k, lane)
+                const int k = (unit >> 5) % Sh::kSteps, n = (unit >> 5) / Sh::kSteps, c = lane & 3;
+                DimPart sum;
+                sum.clear();
+                for (int w = from; w <= to; ++w) {
+                    const bool near = notes[w][w == from ? place : 0].w;
+                    const float* part = near ? reinterpret_cast<const float*>(rings + w * S * Sh::kStageBytes)
+                                             : jp.part + (static_cast<int64_t>(blockIdx.x) * W + w) * Sh::kPartFloats;
+                    const float2* ml = reinterpret_cast<const float2*>(part + HEADS * DP) + n * 4 + c;
+                    if (near) sum.add(reinterpret_cast<const float4*>(part)[unit], ml[0], ml[HEADS / 2]);
+                    else sum.add(__ldcg(reinterpret_cast<const float4*>(part) + unit), __ldcg(ml), __ldcg(ml + HEADS / 2));
+                }
+                if (whole) {
+                    sum.template finish<C>(a, head.x, heads_of<C, HEADS>(a, head.y), n, k, lane);
+                } else {
+                    reinterpret_cast<float4*>(out)[unit] = sum.o;
+                    if (k == 0 && lane < 4) {
+                        float2* ml = reinterpret_cast<float2*>(out + HEADS * DP) + n * 4 + c;
+                        ml[0] = make_float2(sum.m[0], sum.m[1]), ml[HEADS / 2] = make_float2(sum.l[0], sum.l[1]);
+                    }
+                }
+            }
+        }
     } else {
         // One step of the loop copies a tile and, once the ring is full, works on
         // the oldest one.
@@ -1358,68 +1491,6 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t at) {
     return v;
 }
 
-template <int C>
-__device__ __forceinline__ void store_lse(const Args<C>& a, int b, const Heads& hd, int h, float m, float l) {
-    if (a.lse && h < hd.n) *lse_at<C>(a, b, hd, h) = lse_of<C>(m, l);
-}
-
-// The factors of up to eight parts of a head, one lane each (lanes 8 h .. 8 h + 7
-// of a warp); m and l become those of all parts.
-__device__ __forceinline__ float join_factor(float& m, float& l) {
-    float top = m, all;
-#pragma unroll
-    for (int d = 1; d < 8; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));  // of an empty part: -infinity
-    const float f = l != 0.f ? part_factor(m, top) : 0.f;
-    all = l * f;
-#pragma unroll
-    for (int d = 1; d < 8; d *= 2) all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
-    m = top, l = all;
-    return f;
-}
-__device__ __forceinline__ void add_scaled(float4& o, const float4& x, float2 f) {
-    o.x = fmaf(x.x, f.x, o.x), o.y = fmaf(x.y, f.y, o.y);
-    o.z = fmaf(x.z, f.x, o.z), o.w = fmaf(x.w, f.y, o.w);
-}
-
-// A part's 16 dims of 8 heads, with what joining them takes: m and l of the
-// lane's two heads.
-struct DimPart {
-    float4 o;
-    float m[2], l[2];
-    __device__ __forceinline__ void clear() {
-        o = make_float4(0.f, 0.f, 0.f, 0.f);
-        m[0] = m[1] = -INFINITY;
-        l[0] = l[1] = 0.f;
-    }
-    __device__ __forceinline__ void add(const float4& x, float2 xm, float2 xl) {
-        const float pm[2] = {xm.x, xm.y}, pl[2] = {xl.x, xl.y};
-        float f0[2], f1[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float top = pl[e] != 0.f ? fmaxf(m[e], pm[e]) : m[e];
-            f0[e] = part_factor(m[e], top);
-            f1[e] = pl[e] != 0.f ? part_factor(pm[e], top) : 0.f;
-            m[e] = top;
-            l[e] = l[e] * f0[e] + pl[e] * f1[e];
-        }
-        o.x = o.x * f0[0] + x.x * f1[0], o.y = o.y * f0[1] + x.y * f1[1];
-        o.z = o.z * f0[0] + x.z * f1[0], o.w = o.w * f0[1] + x.w * f1[1];
-    }
-    // the result: dims of step k, heads of block n
-    template <int C>
-    __device__ __forceinline__ void finish(const Args<C>& a, int b, const Heads& hd, int n, int k, int lane) const {
-        const int r = lane >> 2, c = lane & 3;
-        const float vs = C == kE4m3 ? a.cache.v_scale[hd.hk] : 1.f;
-        const float f0 = l[0] != 0.f ? vs / l[0] : 0.f, f1 = l[1] != 0.f ? vs / l[1] : 0.f;
-        const bool have = n * 8 + r < hd.n && k * 16 < a.cache.dim;
-        store_dims<C>(o, f0, f1, have ? out_of<C>(a, b, hd, n * 8 + r) + k * 16 : nullptr, c);
-        if (k == 0 && r == 0) {
-            store_lse<C>(a, b, hd, n * 8 + 2 * c, m[0], l[0]);
-            store_lse<C>(a, b, hd, n * 8 + 2 * c + 1, m[1], l[1]);
-        }
-    }
-};
-
 // Joins the parts of a row: grid (row, slice of its accumulators); threads
 // (x: accumulators, y: group, of which each takes every n-th part, so that
 // many parts are on their way at once).
@@ -1449,7 +1520,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Args<C> a
             o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             m[i] = l[i] = make_float2(0.f, 0.f);
             if (p <= d.w) {
-                const float* part = jp.part + (static_cast<int64_t>(p) * 2 + (p == d.z ? 1 : 0)) * Sh::kPartFloats;
+                const float* part = (by_group(C) ? jp.cta_part : jp.part) + (static_cast<int64_t>(p) * 2 + (p == d.z ? 1 : 0)) * Sh::kPartFloats;
                 o[i] = __ldcg(reinterpret_cast<const float4*>(part) + unit);
                 m[i] = __ldcg(reinterpret_cast<const float2*>(part + HEADS * DP) + n * 4 + c);
                 l[i] = __ldcg(reinterpret_cast<const float2*>(part + HEADS * (DP + 1)) + n * 4 + c);
@@ -1749,7 +1820,8 @@ cudaError_t launch_attention_shape(const Args<C>& all, const DeviceInfo& dev, Jo
         a.block_table = all.block_table + from * a.table_stride, a.kv_len = all.kv_len + from;
         a.lse = all.lse ? all.lse + static_cast<int64_t>(from) * tokens * a.q_heads : nullptr;
         all_rows = static_cast<int64_t>(a.B) * jp.rows;
-        jp.by_row = all_rows <= jp.warps;
+        const int sharers = by_group(C) ? ctas : jp.warps;  // whose parts the join launch joins
+        jp.by_row = all_rows <= sharers;
         // (early, because a CTA has an SM for itself: several smaller ones that are placed
         // around others leave holes in the register file, and those that no longer fit then
         // run when the rest are done -- 20 key/value heads of 64 dims, 24 requests: 26 us)
@@ -1758,10 +1830,10 @@ cudaError_t launch_attention_shape(const Args<C>& all, const DeviceInfo& dev, Jo
         if (e != cudaSuccess) return e;
         // few rows: their accumulators over several CTAs, down to a warp's; as many
         // groups as a row has parts for, if rows are alike
-        const int places = jp.by_row ? static_cast<int>(all_rows) : jp.warps, units = Sh::kHeads * DP / 4;
+        const int places = jp.by_row ? static_cast<int>(all_rows) : sharers, units = Sh::kHeads * DP / 4;
         int width = 128;
         while (units % width || (width > 32 && places * (units / width) < dev.sms)) width /= 2;
-        const int parts = jp.warps / places + 2;
+        const int parts = sharers / places + 2;
         int groups = 1;
         while (groups * width < kJoinThreads && groups * kJoinDepth < parts) groups *= 2;
         e = launch_kernel(k_attention_join<C, DP, NT>, true, 1, dim3(places, units / width), dim3(width, groups), 0, s, a, jp);
