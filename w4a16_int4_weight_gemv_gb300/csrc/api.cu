@@ -1010,12 +1010,23 @@ w4a16_status w4a16_scaled_attention(const uint16_t* q, int64_t q_request, int64_
     a.ks_block = cache->ks_block, a.ks_group = cache->ks_group, a.ks_head = cache->ks_head;
     a.vs_block = cache->vs_block, a.vs_group = cache->vs_group, a.vs_head = cache->vs_head;
     a.group = cache->group, a.magic = group_magic(cache->group);
-    const int box = cache->page % 16 == 0 ? 16 : cache->page % 8 == 0 ? 8 : 0, inner = cache->dim <= 64 ? 64 : 128;
-    a.tensor_copies = box && encode_cache_map(&a.k_map, cache->k, *cache, cache->k_block, cache->k_token, cache->k_head, inner, box) &&
-                      encode_cache_map(&a.v_map, cache->v, *cache, cache->v_block, cache->v_token, cache->v_head, inner, box);
-    a.boxes_log2 = !a.tensor_copies ? 4 : box == 16 ? 0 : 1;
-    a.boxes = 1 << a.boxes_log2;
-    a.one_scale = a.boxes == 1 && cache->group % 16 == 0;
+    const w4a16_scaled_cache& c = *cache;
+    // the largest boxes that blocks are made of, and groups if that can be
+    int box = c.dim <= 128 ? 32 : 16;
+    while (box > 8 && (c.page % box != 0 || (c.group % 8 == 0 && c.group % box != 0))) box /= 2;
+    if (c.page % box != 0) box = 0;
+    const int inner = c.dim <= 64 ? 64 : 128;
+    a.tensor_copies = box && encode_cache_map(&a.k_map, c.k, c, c.k_block, c.k_token, c.k_head, inner, box) &&
+                      encode_cache_map(&a.v_map, c.v, c, c.v_block, c.v_token, c.v_head, inner, box);
+    a.box_log2 = !a.tensor_copies ? 0 : box == 32 ? 5 : box == 16 ? 4 : 3;
+    a.scales = kTokenScales;
+    if (a.tensor_copies && c.group % box == 0) {
+        a.scales = kBoxScales;
+    } else if (a.tensor_copies && c.group <= 4 && box % (4 * c.group) == 0) {
+        const bool together = c.ks_group == 1 && c.vs_group == 1 && c.ks_block % 4 == 0 && c.ks_head % 4 == 0 && c.vs_block % 4 == 0 &&
+                              c.vs_head % 4 == 0 && aligned16(c.k_scale) && aligned16(c.v_scale);
+        if (together) a.scales = kRowScales, a.group_log2 = c.group == 4 ? 2 : c.group - 1;
+    }
     return from_cuda(launch_scaled_attention(a, cache->dtype == W4A16_CACHE_INT8, dev->info, static_cast<cudaStream_t>(stream)));
 }
 

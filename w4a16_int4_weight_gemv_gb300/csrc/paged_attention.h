@@ -22,9 +22,9 @@ constexpr int kRowCost = 2;  // a row's queries and result, in tiles (1: 128 req
 constexpr int kMostCost = 0x7FFFFF00;  // of all rows of a launch: sums a little above it still fit 32 bits
 
 // Tiles of a row at most (a window may begin inside one).
-constexpr int most_tiles(int most, int window) {
+constexpr int most_tiles(int most, int window, int tokens = kTile) {
     const int visible = window > 0 && window < most ? window : most;
-    return (visible + kTile - 1) / kTile + (visible < most);
+    return (visible + tokens - 1) / tokens + (visible < most);
 }
 // Rows of a request: `heads` query heads of a key/value head, or fewer, each.
 constexpr int rows_of_request(int q_heads, int kv_heads, int heads) {
@@ -42,9 +42,6 @@ struct JoinPlan {
     // [warp][2][heads * (padded + 2)]; place 0: the row that the warp's share begins inside
     // of, 1: the row it ends inside of
     float* part;
-    // Scales by group: the parts of a CTA's warps are joined in it, to parts [CTA][2]; joins name
-    // CTAs, one entry per row or CTA; part: [warp], those that a warp has besides its last one.
-    float* cta_part;
     int by_row;
     int rows;   // of a request: key/value heads times chunks of the query heads sharing one
     int warps;  // of the first launch

@@ -75,6 +75,10 @@ using Args = typename ArgsOf<C>::type;
 // which may grow by 2^kSlack before o is scaled again: 2^15 at most.
 constexpr float kWeightBias = 8.f, kSlack = 7.f;
 
+// Tokens of a tile: the MMA's rows; with scales by group twice as many, whose control then
+// weighs half as much a token, where a ring of those fits.
+constexpr int tile_tokens(int C, int DP) { return by_group(C) && DP <= 128 ? 32 : kTile; }
+
 constexpr int kMinCost = 3;     // a warp's share at least
 constexpr int kRowTiles = 8;    // rows kernel: tiles of a warp at most
 constexpr int kRowEnough = 2;   // and where one CTA is enough
@@ -186,7 +190,7 @@ __device__ __forceinline__ uint32_t tile_offset(int r, int c) {
 template <int CH>
 __device__ __forceinline__ uint32_t group_offset(int r, int c) {
     if (CH == 4) return static_cast<uint32_t>((r * 4 + (c ^ ((r >> 1) & 3))) * 16);
-    return static_cast<uint32_t>((c >> 3) * (kTile * 128) + (r * 8 + ((c & 7) ^ (r & 7))) * 16);
+    return static_cast<uint32_t>((c >> 3) * (kTile * 128) + (r * 8 + ((c & 7) ^ (r & 7))) * 16);  // (two halves: tiles of kTile)
 }
 
 template <int C, int DP, int NT>
@@ -198,10 +202,14 @@ struct AttnShape {
     static constexpr bool k8 = in_8_bits(C);
     static constexpr int kChunks = by_group(C) ? (DP == 64 ? 4 : DP <= 128 ? 8 : 16) : k8 && DP == 96 ? 8 : DP * (k8 ? 1 : 2) / 16;
     static constexpr int kRowBytes = kChunks * 16;
-    static constexpr int kStageBytes = 2 * kTile * kRowBytes;  // keys, then values
-    // scales by group: beside a stage what is known of it (16 bytes), the scales of its 16
-    // keys and values and a barrier; and what aligns the first stage
-    static constexpr int kBeside = by_group(C) ? 16 + 2 * kTile * 4 + 8 : 0, kAlign = by_group(C) ? 1024 : 0;
+    static constexpr int kTokens = tile_tokens(C, DP);
+    static constexpr int kStageBytes = 2 * kTokens * kRowBytes;  // keys, then values
+    // Scales by group: what is known of a tile in shared memory.  For every eight of its tokens 16
+    // bytes: the mask of those that the row sees, their keys' and their values' scale
+    // (kBoxScales); then the scales of its tokens' keys and of their values, one by one.
+    static constexpr int kInfoKeys = kTokens * 2, kInfoValues = kTokens * 6, kInfo = kTokens * 10;
+    // that and a barrier are beside a stage; and what aligns the first one
+    static constexpr int kBeside = by_group(C) ? kInfo + 8 : 0, kAlign = by_group(C) ? 1024 : 0;
     static constexpr int kPartFloats = kHeads * (DP + 2);
     // shares: one CTA an SM, of as many warps as its registers allow (the accumulators'
     // size decides) with rings of three stages or more
@@ -216,11 +224,11 @@ struct AttnShape {
     static constexpr int kRowStages = kRowFit > 4 ? 4 : kRowFit;
     static constexpr int kRowRing = kRowStages * kStageBytes;  // of a warp
     static constexpr int kRowSmem = kRowWarps * (kRowRing + kRowStages * kBeside) + kAlign;
-    // scales by group: tiles of a step of the loop, two where registers hold them
-    static constexpr int kPair = DP <= 128 && NT == 1 ? 2 : 1;
+    // scales by group: how many 16 tokens are worked on together, where registers allow
+    static constexpr int kTogether = kTokens == 32 && NT == 1 ? 2 : 1;
     static constexpr int kPartBytes = kHeads * DP * 4;
     static constexpr bool kClusters = kRowRing >= 2 * kPartBytes;  // room for the CTA's part behind a warp's
-    static_assert(kStages >= 3 && kStages > kPair && kRowStages >= kPair, "ring too short");
+    static_assert(kStages >= (kTokens == 32 ? 2 : 3), "ring too short");
     static_assert(kRowStages >= 2 && kRowRing >= kPartBytes, "no room for a warp's part");
     static_assert(160 * kShareWarps <= most_workers(DP), "workspace");
 };
@@ -232,11 +240,11 @@ __device__ __forceinline__ int new_tokens(const Args<C>& a) {
     else return 1;
 }
 
-// Whether a tile lies in one group.
+// Whether tiles come as groups of cp.async.
 template <int C>
-__device__ __forceinline__ bool one_scale(const Args<C>& a) {
-    if constexpr (by_group(C)) return a.one_scale;
-    else return false;
+__device__ __forceinline__ bool counts_groups(const Args<C>& a) {
+    if constexpr (by_group(C)) return a.scales == kTokenScales;
+    else return true;
 }
 
 // What one request looks like: its visible tokens [start, len), in tiles from
@@ -245,15 +253,15 @@ struct Request {
     int len, start, tile0, tiles;
 };
 
-template <int C>
+template <int C, int TOKENS>
 __device__ __forceinline__ Request request_of(const Args<C>& a, int b, bool& bad) {
     Request q;
     const int len = a.kv_len[b];
     bad |= len < 0 || len > a.most;
     q.len = min(max(len, 0), a.most);
     q.start = a.window > 0 ? max(q.len - (new_tokens<C>(a) - 1) - a.window, 0) : 0;
-    q.tile0 = q.start / kTile;
-    q.tiles = q.len > 0 ? (q.len - 1) / kTile + 1 - q.tile0 : 0;
+    q.tile0 = q.start / TOKENS;
+    q.tiles = q.len > 0 ? (q.len - 1) / TOKENS + 1 - q.tile0 : 0;
     return q;
 }
 
@@ -553,9 +561,9 @@ struct RowMath {
     // the values, p times the scale, 2^lv.  o goes by the largest weight: by the largest p instead,
     // a token of large scale and small p would pass what fp16 holds.  m and the largest weight
     // need not be the largest there are, only near them (kSlack), so that most tiles take a vote
-    // here and no exchange.  ALIKE: a tile's tokens have one scale.  HIDDEN: some scores are
-    // -infinity for tokens that a column does not see, whose scale may be anything.
-    template <int P, bool ALIKE, bool HIDDEN>
+    // here and no exchange.  HIDDEN: some scores are -infinity for tokens that a column does not
+    // see, whose scale may be anything.
+    template <int P, bool HIDDEN>
     __device__ __forceinline__ void weigh(int n, float (&s)[P][NT][4], const float (&lv)[P][2], const uint32_t (&sign)[P][2]) {
         float top[2], heavy[2];
         const auto weight = [&](int p, int e) { return HIDDEN && s[p][n][e] == -INFINITY ? -INFINITY : s[p][n][e] + lv[p][e >> 1]; };
@@ -564,9 +572,8 @@ struct RowMath {
             top[e] = heavy[e] = -INFINITY;
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                const float most = fmaxf(s[p][n][e], s[p][n][e + 2]);
-                top[e] = fmaxf(top[e], most);
-                heavy[e] = fmaxf(heavy[e], ALIKE && !HIDDEN ? most + lv[p][0] : fmaxf(weight(p, e), weight(p, e + 2)));
+                top[e] = fmaxf(top[e], fmaxf(s[p][n][e], s[p][n][e + 2]));
+                heavy[e] = fmaxf(heavy[e], fmaxf(weight(p, e), weight(p, e + 2)));
             }
         }
         bool over = false;
@@ -600,17 +607,17 @@ struct RowMath {
         }
     }
 
-    // P tiles of a row: codes at kt (shared addresses: keys, then values), what is known of them
-    // and the scales of their tokens at info; first: the numbers of their first tokens
+    // P times 16 tokens of a tile from its `from`-th on: codes at kt (shared address: keys, then
+    // values), what is known of them at info; first: the number of its first token
     template <int P>
-    __device__ __forceinline__ void tiles(const Args<C>& a, const Request& q, const uint32_t (&kt)[P], const uint32_t (&info)[P],
-                                          const int (&first)[P], int lane) {
-        constexpr int kValues = kTile * Sh::kRowBytes;  // from a key's place to its value's
+    __device__ __forceinline__ void tokens(const Args<C>& a, const Request& q, uint32_t kt, uint32_t info, int first, int from, int lane) {
+        constexpr int kValues = Sh::kTokens * Sh::kRowBytes;  // from a key's place to its value's
         constexpr bool kTwo = P == 1 && NT * KS <= 16;  // two chains of products, as above
         const int r = lane >> 2;
         uint32_t at[P];  // chunk lane / 16 of row lane % 16; chunk k + lane / 16 (k even): its address xor 16 k
 #pragma unroll
-        for (int p = 0; p < P; ++p) at[p] = kt[p] + group_offset<CH>(lane & 15, lane >> 4);
+        for (int p = 0; p < P; ++p) at[p] = kt + (from + 16 * p) * Sh::kRowBytes + group_offset<CH>(lane & 15, lane >> 4);
+        first += from;
         float s[P][NT][4], s1[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -641,15 +648,28 @@ struct RowMath {
         bool hidden = false;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const uint4 x = ld_shared_u4(info[p]);
-            mask[p] = x.x;
-            ks[p][0] = ks[p][1] = __uint_as_float(x.y);
-            lv[p][0] = lv[p][1] = log2_fast(__uint_as_float(x.z));
-            sign[p][0] = sign[p][1] = x.z & 0x80000000u;
-            hidden |= x.x != 0xFFFFu;
+            const uint32_t known = info + (from + 16 * p) * 2;
+            const uint4 x = ld_shared_u4(known), y = ld_shared_u4(known + 16);  // rows r, rows r + 8
+            mask[p] = x.x | (y.x << 8);
+            hidden |= mask[p] != 0xFFFFu;
+            float v[2] = {__uint_as_float(x.z), __uint_as_float(y.z)};
+            ks[p][0] = __uint_as_float(x.y), ks[p][1] = __uint_as_float(y.y);
+            if (a.scales != kBoxScales) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t of = info + ((from + 16 * p + r + 8 * i) >> a.group_log2) * 4;
+                    ks[p][i] = ld_shared_f32(of + Sh::kInfoKeys);
+                    v[i] = ld_shared_f32(of + Sh::kInfoValues);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                lv[p][i] = log2_fast(v[i]);
+                sign[p][i] = __float_as_uint(v[i]) & 0x80000000u;
+            }
         }
-        // tokens that some new ones see and others do not (the last tile reaches furthest)
-        const bool edge = first[P - 1] + kTile > q.len - (a.tokens - 1) || (a.window > 0 && first[0] < q.len - a.window);
+        // tokens that some new ones see and others do not
+        const bool edge = first + 16 * P > q.len - (a.tokens - 1) || (a.window > 0 && first < q.len - a.window);
         hidden |= edge;
         const auto scores = [&](int n) {
 #pragma unroll
@@ -666,25 +686,16 @@ struct RowMath {
                     pf[p][n][e] = transpose_8x8(*reinterpret_cast<const uint32_t*>(&h));
                 }
         };
-        if (a.one_scale && !hidden) {
+        if (!hidden) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 scores(n);
-                weigh<P, true, false>(n, s, lv, sign);
+                weigh<P, false>(n, s, lv, sign);
                 to_f16(n);
             }
         } else {
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                if (!a.one_scale) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        ks[p][i] = ld_shared_f32(info[p] + 16 + (r + 8 * i) * 4);
-                        const float v = ld_shared_f32(info[p] + 16 + (kTile + r + 8 * i) * 4);
-                        lv[p][i] = log2_fast(v);
-                        sign[p][i] = __float_as_uint(v) & 0x80000000u;
-                    }
-                }
                 if (C == kE4m3Groups && edge && a.tokens > 1) {
                     // A NaN that some new tokens see stays with them: its weight becomes NaN there, and
                     // the code a number.
@@ -713,12 +724,12 @@ struct RowMath {
                     if (edge) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int token = first[p] + r + 8 * (e >> 1), end = upto[n][e & 1];
+                            const int token = first + 16 * p + r + 8 * (e >> 1), end = upto[n][e & 1];
                             if (token >= end || (a.window > 0 && token < end - a.window)) s[p][n][e] = -INFINITY;
                         }
                     }
                 }
-                weigh<P, false, true>(n, s, lv, sign);
+                weigh<P, true>(n, s, lv, sign);
                 to_f16(n);
             }
         }
@@ -746,6 +757,13 @@ struct RowMath {
                     }
                 }
             }
+    }
+
+    // a tile
+    __device__ __forceinline__ void tile(const Args<C>& a, const Request& q, uint32_t kt, uint32_t info, int first, int lane) {
+        constexpr int P = Sh::kTogether;
+#pragma unroll 1
+        for (int from = 0; from < Sh::kTokens; from += 16 * P) tokens<P>(a, q, kt, info, first, from, lane);
     }
 
     __device__ __forceinline__ void reduce() {
@@ -904,129 +922,154 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// Scales by group: the ring of a warp, and what fills it.  The codes of a tile come as
-// tensor copies of boxes of 16 or 8 tokens, which take next to no instructions (with
-// cp.async these were a third of all); blocks whose pages no box divides, by cp.async.
-// Block ids are loaded early, those of 32 boxes at once (lane i: box i % boxes of the
-// i / boxes-th tile).  Where a tile lies in one group its two scales come with them,
-// else those of its tokens by cp.async.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// Scales by group: the ring of a warp, and what fills it.  Block ids are loaded early, those
+// of 32 boxes at once (lane i: box i % boxes of the i / boxes-th tile).  The lane that has a
+// box's id starts its copies: of the codes as tensor copies, which take next to no
+// instructions (with cp.async these were a third of all); its scale comes with the id
+// (kBoxScales), or those of its tokens as another copy (kRowScales).  Blocks and scales that
+// do not allow that: by cp.async (kTokenScales), their codes too where no box divides a page.
 template <int C, int DP, int NT>
 struct GroupRing {
     using Sh = AttnShape<C, DP, NT>;
-    static constexpr int CH = Sh::kChunks, kInner = CH == 4 ? 64 : 128, kHalves = CH == 16 ? 2 : 1;
-    uint32_t codes, beside, bars;  // shared addresses: of stage 0 its codes; what is known of it; its barrier
-    int known, id, place;          // how many tiles' ids are left; this lane's
+    static constexpr int CH = Sh::kChunks, kInner = CH == 4 ? 64 : 128, kHalves = CH == 16 ? 2 : 1, TT = Sh::kTokens;
+    uint32_t codes, info, bars;  // shared addresses: of stage 0 its codes; what is known of it; its barrier
+    int known, id, place;        // how many tiles' ids are left; this lane's
     float ks, vs;
     bool late;  // a copy did not arrive
 
-    __device__ __forceinline__ void open(uint32_t smem, int warp, int warps, int stages, int lane) {
+    __device__ __forceinline__ void open(const Args<C>& a, uint32_t smem, int warp, int warps, int stages, int lane) {
         smem = (smem + 1023u) & ~1023u;
         codes = smem + warp * stages * Sh::kStageBytes;
-        beside = smem + warps * stages * Sh::kStageBytes + warp * stages * 144;
-        bars = smem + warps * stages * (Sh::kStageBytes + 144) + warp * stages * 8;
+        info = smem + warps * stages * Sh::kStageBytes + warp * stages * Sh::kInfo;
+        bars = smem + warps * stages * (Sh::kStageBytes + Sh::kInfo) + warp * stages * 8;
         late = false;
-        if (lane < stages) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + lane * 8) : "memory");
+        if (lane < stages)
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bars + lane * 8), "r"(a.scales == kTokenScales ? 1 : boxes(a)) : "memory");
         mbar_init_fence();
         fence_proxy_async_smem();
         __syncwarp();
     }
+    static __device__ __forceinline__ int boxes_log2(const Args<C>& a) { return (TT == 32 ? 5 : 4) - a.box_log2; }
+    static __device__ __forceinline__ int boxes(const Args<C>& a) { return TT >> a.box_log2; }
 
     // the ids of the boxes from tile t on (tiles step apart, below t1) that hold tokens of [low, high)
     __device__ __forceinline__ void look_up(const Args<C>& a, int b, int hk, int tile0, int low, int high, int t, int t1, int step, int lane) {
-        const int tile = t + (lane >> a.boxes_log2) * step;
-        const int token = (tile0 + tile) * kTile + (lane & (a.boxes - 1)) * (kTile >> a.boxes_log2);
+        const int shift = boxes_log2(a), tile = t + (lane >> shift) * step;
+        const int token = (tile0 + tile) * TT + ((lane & (boxes(a) - 1)) << a.box_log2);
         const int col = static_cast<int>(static_cast<unsigned>(token) / static_cast<unsigned>(a.cache.page));
         place = token - col * a.cache.page;
         id = -1;
-        known = 32 >> a.boxes_log2;
-        if (tile < t1 && token < high && token + (kTile >> a.boxes_log2) > low) id = a.block_table[b * a.table_stride + col];
-        if (a.one_scale) {
+        known = 32 >> shift;
+        if (tile < t1 && token < high && token + (1 << a.box_log2) > low) id = a.block_table[b * a.table_stride + col];
+        if (a.scales == kBoxScales) {
             ks = vs = 0.f;
             if (id >= 0 && id < a.cache.blocks) {
-                const int64_t of = __umulhi(place, a.magic);  // (a group of 16 tokens at least)
+                const int64_t of = __umulhi(place, a.magic);  // (a group of 8 tokens at least)
                 ks = a.k_scale[id * a.ks_block + of * a.ks_group + hk * a.ks_head];
                 vs = a.v_scale[id * a.vs_block + of * a.vs_group + hk * a.vs_head];
             }
         }
     }
 
-    // one_scale: starts the copies of the next n tiles, the row's t-th and n - 1 more step
-    // apart, into stages from `stage` of S on.  Each by the lane that holds its id.
-    __device__ __forceinline__ void copy_whole(const Args<C>& a, int hk, const Request& q, int t, int step, int n, int stage, int S, int lane, bool& bad) {
-        const int j = lane - (32 - known);
-        known -= n;
-        if (static_cast<unsigned>(j) < static_cast<unsigned>(n)) {
-            const int left = q.len - (q.tile0 + t + j * step) * kTile, before = q.start + left - q.len;  // tokens from the tile's first on; not seen
-            uint32_t mask = left < kTile ? (1u << left) - 1u : 0xFFFFu;
-            if (before > 0) mask &= 0xFFFFu << before;
-            const bool valid = id >= 0 && id < a.cache.blocks;
-            if (!valid) mask = 0u, bad = true;
-            int at = stage + j;
-            if (at >= S) at -= S;
-            const uint32_t dst = codes + at * Sh::kStageBytes, bar = bars + at * 8;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %1};" ::"r"(beside + at * 144), "r"(mask), "r"(__float_as_uint(ks)), "r"(__float_as_uint(vs)) : "memory");
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(valid ? kTile * 2 * kHalves * kInner : 0) : "memory");
-            if (valid) {
+    // kBoxScales, kRowScales: starts the copies of the row's t-th tile, the next of those looked
+    // up, into a stage
+    __device__ __forceinline__ void copy_boxes(const Args<C>& a, int hk, const Request& q, int t, int stage, int lane, bool& bad) {
+        const int box = lane - 32 + (known << boxes_log2(a));
+        --known;
+        if (static_cast<unsigned>(box) < static_cast<unsigned>(boxes(a))) {
+            const int u = 1 << a.box_log2, first = (q.tile0 + t) * TT + box * u;
+            // the tokens from `start` on, below `len`
+            const int begin = min(max(q.start - first, 0), u), end = min(max(q.len - first, 0), u);
+            uint32_t mask = end > begin ? (0xFFFFFFFFu >> (32 - end)) & (0xFFFFFFFFu << begin) : 0u;
+            if (id < 0 || id >= a.cache.blocks) {
+                bad |= mask != 0u;
+                mask = 0u;
+            }
+            const uint32_t dst = codes + stage * Sh::kStageBytes + box * u * kInner, bar = bars + stage * 8, to = info + stage * Sh::kInfo;
+            const bool rows = a.scales == kRowScales;
+            const uint32_t more = rows ? static_cast<uint32_t>(u >> a.group_log2) * 4u : 0u;  // bytes of the tokens' scales
+            if (mask) {
+                expect_bytes(bar, u * 2 * kHalves * kInner + 2 * more);
 #pragma unroll
                 for (int h = 0; h < kHalves; ++h) {
                     tma_load_4d(dst + h * (kTile * 128), &a.k_map, h * 128, hk, place, id, bar);
-                    tma_load_4d(dst + h * (kTile * 128) + kTile * Sh::kRowBytes, &a.v_map, h * 128, hk, place, id, bar);
+                    tma_load_4d(dst + h * (kTile * 128) + TT * Sh::kRowBytes, &a.v_map, h * 128, hk, place, id, bar);
                 }
+                if (rows) {
+                    const int64_t of = place >> a.group_log2;
+                    bulk_load(to + Sh::kInfoKeys + box * more, a.k_scale + id * a.ks_block + of + hk * a.ks_head, more, bar);
+                    bulk_load(to + Sh::kInfoValues + box * more, a.v_scale + id * a.vs_block + of + hk * a.vs_head, more, bar);
+                }
+            } else {
+                expect_bytes(bar, 0);
             }
+#pragma unroll
+            for (int i = 0; i < TT / 8; ++i)
+                if (i < u / 8)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %1};" ::"r"(to + (box * (u / 8) + i) * 16), "r"((mask >> (8 * i)) & 0xFFu),
+                                 "r"(__float_as_uint(ks)), "r"(__float_as_uint(vs))
+                                 : "memory");
         }
     }
 
-    // else: those of the next tile, the row's t-th, into a stage
+    // kTokenScales: those of the next tile, the row's t-th, into a stage
     __device__ __forceinline__ void copy(const Args<C>& a, int hk, const Request& q, int t, int stage, int lane, bool& bad) {
-        const uint32_t dst = codes + stage * Sh::kStageBytes, bar = bars + stage * 8, info = beside + stage * 144;
-        const int from = 32 - (known << a.boxes_log2);
+        const uint32_t dst = codes + stage * Sh::kStageBytes, bar = bars + stage * 8, to = info + stage * Sh::kInfo;
+        const int from = 32 - (known << boxes_log2(a)), u = 1 << a.box_log2;
         --known;
-        const int first = (q.tile0 + t) * kTile;
-        uint32_t mask = q.len - first < kTile ? (1u << (q.len - first)) - 1u : 0xFFFFu;
-        if (q.start > first) mask &= 0xFFFFu << (q.start - first);
-        const int u = kTile >> a.boxes_log2, mine = lane & 15, box = from + mine / u;
+        const int mine = lane & (TT - 1), token = (q.tile0 + t) * TT + mine, box = from + (mine >> a.box_log2);
         const int block = __shfl_sync(0xFFFFFFFFu, id, box), in = __shfl_sync(0xFFFFFFFFu, place, box) + (mine & (u - 1));
-        const bool seen = (mask >> mine) & 1u, valid = seen && block >= 0 && block < a.cache.blocks;
+        const bool seen = token >= q.start && token < q.len, valid = seen && block >= 0 && block < a.cache.blocks;
         bad |= seen && !valid;
-        mask = __ballot_sync(0xFFFFFFFFu, valid) & 0xFFFFu;
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, valid) & (0xFFFFFFFFu >> (32 - TT));
+        const int64_t at = valid ? block : 0, row = valid ? in : 0;
         {
-            const int64_t of = a.magic ? static_cast<int>(__umulhi(in, a.magic)) : in, at = valid ? block : 0;
-            const float* src = lane < 16 ? a.k_scale + at * a.ks_block + of * a.ks_group + hk * a.ks_head
-                                         : a.v_scale + at * a.vs_block + of * a.vs_group + hk * a.vs_head;
-            cp_async_4_zfill(info + 16 + lane * 4, valid ? src : a.k_scale, valid);
+            const int64_t of = a.magic ? static_cast<int>(__umulhi(in, a.magic)) : in;
+            const float* k = a.k_scale + at * a.ks_block + of * a.ks_group + hk * a.ks_head;
+            const float* v = a.v_scale + at * a.vs_block + of * a.vs_group + hk * a.vs_head;
+            if (lane < TT) {
+                cp_async_4_zfill(to + Sh::kInfoKeys + mine * 4, valid ? k : a.k_scale, valid);
+                cp_async_4_zfill(to + Sh::kInfoValues + mine * 4, valid ? v : a.v_scale, valid);
+            }
         }
-        if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(info), "r"(mask) : "memory");
+        if (lane < TT / 8) asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + lane * 16), "r"((mask >> (8 * lane)) & 0xFFu) : "memory");
         if (a.tensor_copies) {
             // lane i: of box i / (2 kHalves) the key's or the value's, first or second half
-            const uint32_t here = (1u << u) - 1u;
-            if (lane == 0) {
-                const int n = ((mask & here) != 0u) + ((mask >> u) != 0u);
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n * u * 2 * kHalves * kInner) : "memory");
-            }
-            __syncwarp();
+            const uint32_t here = 0xFFFFFFFFu >> (32 - u);
             const int mybox = lane / (2 * kHalves), h = lane / 2 % kHalves;
+            const bool mybox_seen = mybox < boxes(a) && ((mask >> ((mybox * u) & 31)) & here);
+            const int copies = __popc(__ballot_sync(0xFFFFFFFFu, mybox_seen));
+            if (lane == 0) expect_bytes(bar, copies * u * kInner);
+            __syncwarp();
             const int b = __shfl_sync(0xFFFFFFFFu, id, (from + mybox) & 31), p = __shfl_sync(0xFFFFFFFFu, place, (from + mybox) & 31);
-            if (mybox < a.boxes && ((mask >> (mybox * u)) & here)) {
-                const uint32_t to = dst + h * (kTile * 128) + mybox * u * kInner;
-                if (lane & 1) tma_load_4d(to + kTile * Sh::kRowBytes, &a.v_map, h * 128, hk, p, b, bar);
-                else tma_load_4d(to, &a.k_map, h * 128, hk, p, b, bar);
+            if (mybox_seen) {
+                const uint32_t there = dst + h * (kTile * 128) + mybox * u * kInner;
+                if (lane & 1) tma_load_4d(there + TT * Sh::kRowBytes, &a.v_map, h * 128, hk, p, b, bar);
+                else tma_load_4d(there, &a.k_map, h * 128, hk, p, b, bar);
             }
         } else {
-            const int64_t at = valid ? block : 0, row = valid ? in : 0;
             const int64_t ko = at * a.cache.k_block + row * a.cache.k_token, vo = at * a.cache.v_block + row * a.cache.v_token;
             const char* kp = static_cast<const char*>(a.cache.k) + hk * a.cache.k_head;
             const char* vp = static_cast<const char*>(a.cache.v) + hk * a.cache.v_head;
             const int chunks = a.cache.dim / 16;
-#pragma unroll
-            for (int i = 0; i < kTile * CH / 32; ++i) {
+#pragma unroll 4
+            for (int i = 0; i < TT * CH / 32; ++i) {
                 const int r = (i * 32 + lane) / CH, ch = (i * 32 + lane) % CH;
                 const int64_t kr = __shfl_sync(0xFFFFFFFFu, ko, r), vr = __shfl_sync(0xFFFFFFFFu, vo, r);
                 const bool ok = ((mask >> r) & 1u) && ch < chunks;  // (past dim: zeros)
-                const uint32_t to = dst + group_offset<CH>(r, ch);
-                cp_async_16_zfill(to, ok ? kp + kr + ch * 16 : kp, ok);
-                cp_async_16_zfill(to + kTile * Sh::kRowBytes, ok ? vp + vr + ch * 16 : vp, ok);
+                const uint32_t there = dst + group_offset<CH>(r, ch);
+                cp_async_16_zfill(there, ok ? kp + kr + ch * 16 : kp, ok);
+                cp_async_16_zfill(there + TT * Sh::kRowBytes, ok ? vp + vr + ch * 16 : vp, ok);
             }
-            if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+            if (lane == 0) expect_bytes(bar, 0);
         }
     }
 
@@ -1038,7 +1081,7 @@ struct GroupRing {
                      : "memory");
         return done != 0u;
     }
-    // waits for the codes of a stage (scales of tokens: cp.async groups), 0.8 s at most
+    // waits for a stage's tensor copies (cp.async: their groups), 0.8 s at most
     __device__ __forceinline__ void wait(int stage, uint32_t parity) {
         if (arrived(stage, parity)) return;
         for (int i = 0; !late && !arrived(stage, parity); ++i) late = i >= 8192;
@@ -1118,6 +1161,13 @@ struct Segment {
     Request q;
 };
 
+// Whether all of a CTA's W warps come after the one in which a row begins and before the one
+// in which it ends.
+template <int W>
+__device__ __forceinline__ bool inside_of_row(int cta, int first, int last) {
+    return first < cta * W && last >= (cta + 1) * W;
+}
+
 template <int C, int DP, int NT>
 __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
     k_attention_shares(const __grid_constant__ Args<C> a, const JoinPlan jp) {
@@ -1133,7 +1183,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
 
     GroupRing<C, DP, NT> groups;
     if constexpr (by_group(C)) {
-        groups.open(smem_addr(smem), warp, W, S, lane);
+        groups.open(a, smem_addr(smem), warp, W, S, lane);
         if (a.tensor_copies && threadIdx.x == 0) prefetch_tensor_map(&a.k_map), prefetch_tensor_map(&a.v_map);
     } else if (a.cache.dim != DP) {
         clear_ring(smem, Sh::kSmem, threadIdx.x, W * 32);
@@ -1153,7 +1203,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int b = base + lane * kPer + i;
-            const int n = b < a.B ? request_of<C>(a, b, bad).tiles : 0;
+            const int n = b < a.B ? request_of<C, Sh::kTokens>(a, b, bad).tiles : 0;
             cost[i] = n ? (n + kRowCost) * rows : 0;
             own += cost[i];
         }
@@ -1172,7 +1222,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
     } else {
 #pragma unroll 8
         for (int b = lane; b < a.B; b += 32) {
-            const int n = request_of<C>(a, b, bad).tiles;
+            const int n = request_of<C, Sh::kTokens>(a, b, bad).tiles;
             total += n ? (n + kRowCost) * rows : 0;
         }
 #pragma unroll
@@ -1180,7 +1230,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
     }
     // requests without tokens
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        if (request_of<C>(a, b, bad).tiles > 0) continue;
+        if (request_of<C, Sh::kTokens>(a, b, bad).tiles > 0) continue;
         if (by_group(C)) {
             for (int row = 0; row < rows; ++row) store_empty<C>(a, b, heads_of<C, HEADS>(a, row), threadIdx.x, W * 32);
         } else {
@@ -1192,23 +1242,10 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
     int workers = min((total + kMinCost - 1) / kMinCost, jp.warps);
     // one request: rows of one length, so a multiple of them splits none unevenly
     if (a.B == 1 && workers > rows) workers -= workers % rows;
-    // Scales by group: the parts of a CTA's warps are joined here, so that few are left for the
-    // join launch.  A warp's: of the row that its share begins inside of, and of the row it ends
-    // inside of ({request or -1: none, row, whether the row ends here, whether the part is in the
-    // ring}); `spill`: for the join launch, the row that begins here and goes on in another CTA.
-    __shared__ int4 notes[by_group(C) ? W : 1][2];
-    __shared__ int4 spill;
-    if constexpr (by_group(C)) {
-        if (lane < 2) notes[warp][lane] = make_int4(-1, 0, 0, 0);
-        if (threadIdx.x == 0) spill = make_int4(-1, 0, 0, 0);
-        __syncthreads();
-        if (workers == 0) workers = 1;  // (nothing to do: no row is found)
-    } else {
-        if (!jp.by_row && lane == 0) jp.joins[worker] = make_int4(-1, 0, 0, 0);
-        if (worker >= workers) {
-            if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
-            return;
-        }
+    if (!jp.by_row && lane == 0) jp.joins[worker] = make_int4(-1, 0, 0, 0);
+    if (worker >= workers) {
+        if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
+        return;
     }
     // costs before worker i: equal shares, the remainder to the first ones
     const unsigned share = static_cast<unsigned>(total) / static_cast<unsigned>(workers), extra = total - share * workers;
@@ -1258,21 +1295,28 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
             s.row = 0;
             do {
                 if (++s.b >= a.B) return false;
-                s.q = request_of<C>(a, s.b, bad);
+                s.q = request_of<C, Sh::kTokens>(a, s.b, bad);
             } while (s.q.tiles == 0);
         }
         open_segment(s);
         return true;
     };
     Segment seg{};
-    bool live = u1 > u0 && (!by_group(C) || worker < workers) && locate(u0, seg.b, seg.at);
+    bool live = u1 > u0 && locate(u0, seg.b, seg.at);
     if (live) {
-        seg.q = request_of<C>(a, seg.b, bad);
+        seg.q = request_of<C, Sh::kTokens>(a, seg.b, bad);
         seg.row = static_cast<unsigned>(u0 - seg.at) / static_cast<unsigned>(seg.q.tiles + kRowCost);
         seg.at += seg.row * (seg.q.tiles + kRowCost);
         open_segment(seg);
         live = seg.t1 > seg.t0;
     }
+
+    // Scales by group: a CTA all of whose warps lie inside of one row joins their parts itself, to
+    // that of its first one, so that a long row leaves few to the join launch.
+    bool inside = false;
+    uint8_t* const rings = smem + (by_group(C) ? (0u - smem_addr(smem)) & 1023u : 0u);
+    if constexpr (by_group(C))
+        inside = live && inside_of_row<W>(blockIdx.x, worker_of(seg.at + kRowCost), worker_of(seg.at + kRowCost + seg.q.tiles - 1));
 
     // The copies run ahead of the products: `ahead` is the segment of the next
     // tile to copy, ahead_t the tile.
@@ -1303,29 +1347,18 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
                 if ((i % kLines) * 64 < a.cache.dim) prefetch_l2(query_of<C>(a, after_b, h, i / kLines) + (i % kLines) * 64);
         }
     };
-    // starts the copies of the next `n` tiles, as far as there are any
-    auto copy_next = [&](int n) {
-        while (n > 0 && more) {
-            int now = 1;
+    // starts the copies of the next tile, if there is one
+    auto copy_next = [&] {
+        if (more) {
             if constexpr (by_group(C)) {
-                if (a.one_scale) {
-                    now = min(min(n, ahead.t1 - ahead_t), groups.known);
-                    groups.copy_whole(a, ahead_hk, ahead.q, ahead_t, 1, now, put, S, lane, bad);
-                } else {
-                    groups.copy(a, ahead_hk, ahead.q, ahead_t, put, lane, bad);
-                    cp_async_commit();
-                }
+                if (a.scales != kTokenScales) groups.copy_boxes(a, ahead_hk, ahead.q, ahead_t, put, lane, bad);
+                else groups.copy(a, ahead_hk, ahead.q, ahead_t, put, lane, bad);
             } else {
                 const uint32_t mask = copy.copy(a, ahead_hk, ahead.q, ahead_t, 1, ring + put * Sh::kStageBytes, lane, bad);
                 if (lane == 0) tile_mask[warp][put] = mask;
-                cp_async_commit();
             }
-            n -= now;
-            put += now;
-            if (put >= S) put -= S;
             bool look = false;
-            ahead_t += now;
-            if (ahead_t >= ahead.t1) {
+            if (++ahead_t >= ahead.t1) {
                 more = look = next_segment(ahead);
                 ahead_t = ahead.t0;
                 ahead_hk = heads_of<C, HEADS>(a, ahead.row).hk;
@@ -1334,120 +1367,64 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
             else look |= copy.wants(a, ahead_t, 1);
             if (more && look) look_up();
         }
-        // (groups of copies are counted, so empty ones in place of those that are not there)
-        if (!by_group(C) || !one_scale<C>(a))
-            for (; n > 0; --n) cp_async_commit();
+        if (counts_groups<C>(a)) cp_async_commit();
+        put = put + 1 == S ? 0 : put + 1;
     };
     // the row's tiles here are done: its result or its part
-    uint8_t* const rings = smem + (by_group(C) ? (0u - smem_addr(smem)) & 1023u : 0u);
     auto end_row = [&] {
         math.reduce();
         const bool begins = seg.t0 == 0, ends = seg.t1 == seg.q.tiles;
-        if constexpr (by_group(C)) {
-            const int b = seg.b, row = seg.row;
-            // a row that begins here: what the join launch has to do for it
-            if (begins && lane == 0) {
-                const int last = (ends ? worker : worker_of(seg.at + kRowCost + seg.q.tiles - 1)) / W;
-                int4 join = make_int4(-1, 0, 0, 0);
-                if (last != static_cast<int>(blockIdx.x)) spill = join = make_int4(b, row, blockIdx.x, last);
-                if (jp.by_row) jp.joins[b * rows + row] = join;
-            }
-            live = next_segment(seg);
-            if (begins && ends) {
-                math.finish(a, b, hd, lane);
-            } else {
-                // (the ring is empty once nothing follows)
-                float* part = live ? jp.part + static_cast<int64_t>(worker) * Sh::kPartFloats
-                                   : reinterpret_cast<float*>(rings + warp * S * Sh::kStageBytes);
-                math.store_part(part, part + HEADS * DP, part + HEADS * (DP + 1), lane);
-                if (lane == 0) notes[warp][begins] = make_int4(b, row, ends, !live);
-            }
+        if (begins && ends) {
+            math.finish(a, seg.b, hd, lane);
         } else {
-            if (begins && ends) {
-                math.finish(a, seg.b, hd, lane);
-            } else {
-                float* part = jp.part + (static_cast<int64_t>(worker) * 2 + (begins ? 1 : 0)) * Sh::kPartFloats;
-                math.store_part(part, part + HEADS * DP, part + HEADS * (DP + 1), lane);
-            }
-            // a row that begins here: what the join launch has to do for it
-            if (begins && lane == 0 && (jp.by_row || !ends))
-                jp.joins[jp.by_row ? seg.b * rows + seg.row : worker] =
-                    ends ? make_int4(-1, 0, 0, 0) : make_int4(seg.b, seg.row, worker, worker_of(seg.at + kRowCost + seg.q.tiles - 1));
-            live = next_segment(seg);
+            // (inside: into the ring, which is empty then)
+            float* part = inside ? reinterpret_cast<float*>(rings + warp * S * Sh::kStageBytes)
+                                 : jp.part + (static_cast<int64_t>(worker) * 2 + (begins ? 1 : 0)) * Sh::kPartFloats;
+            math.store_part(part, part + HEADS * DP, part + HEADS * (DP + 1), lane);
         }
+        // a row that begins here: what the join launch has to do for it
+        if (begins && lane == 0 && (jp.by_row || !ends))
+            jp.joins[jp.by_row ? seg.b * rows + seg.row : worker] =
+                ends ? make_int4(-1, 0, 0, 0) : make_int4(seg.b, seg.row, worker, worker_of(seg.at + kRowCost + seg.q.tiles - 1));
+        live = next_segment(seg);
         t = seg.t0;
         fresh = true;
     };
     if constexpr (by_group(C)) {
-        // A step works on the oldest tiles, one or two of a row, and copies as many into their
-        // places.  S groups of copies are on their way before it, empty ones among them.
-        constexpr int P = Sh::kPair;
+        // A step works on the oldest tile and copies another into its place.  (S groups of
+        // cp.async are on their way before it, empty ones among them.)
         uint32_t parity = 0u;
         while (live) {
             if (fresh) begin_row();
-            if (!primed) copy_next(S), primed = 1;
-            const bool pair = P == 2 && seg.t1 - t >= 2;
-            const int next = slot + 1 == S ? 0 : slot + 1;
-            if (!one_scale<C>(a)) {
-                if (pair) cp_async_wait_group<S - 2>();
-                else cp_async_wait_group<S - 1>();
-            }
+            for (; primed < S; ++primed) copy_next();
+            if (counts_groups<C>(a)) cp_async_wait_group<S - 1>();
             groups.wait(slot, parity);
-            if (pair) groups.wait(next, parity ^ (next == 0 ? 1u : 0u));
             __syncwarp();
             if (t == seg.t0) math.ready(a, hd.hk, seg.q.len, lane);
-            const int first = (seg.q.tile0 + t) * kTile;
-            const uint32_t kt = groups.codes + slot * Sh::kStageBytes, info = groups.beside + slot * 144;
-            bool both = false;
-            if constexpr (P == 2) {
-                both = pair;
-                if (pair)
-                    math.template tiles<2>(a, seg.q, {kt, groups.codes + next * Sh::kStageBytes}, {info, groups.beside + next * 144},
-                                           {first, first + kTile}, lane);
-            }
-            if (!both) math.template tiles<1>(a, seg.q, {kt}, {info}, {first}, lane);
+            math.tile(a, seg.q, groups.codes + slot * Sh::kStageBytes, groups.info + slot * Sh::kInfo, (seg.q.tile0 + t) * Sh::kTokens, lane);
             __syncwarp();
-            const int done = pair ? 2 : 1;
-            copy_next(done);
-            t += done;
-            slot += done;
-            if (slot >= S) slot -= S, parity ^= 1u;
-            if (t >= seg.t1) end_row();
+            copy_next();
+            if (++slot == S) slot = 0, parity ^= 1u;
+            if (++t >= seg.t1) end_row();
         }
         if (groups.late) raise_device_error(a.err, W4A16_DEVERR_TIMEOUT);
-        if (!a.one_scale) cp_async_wait_group<0>();
-        __syncthreads();
-        if (!jp.by_row && threadIdx.x == 0) jp.joins[blockIdx.x] = spill;
-        // the row that comes from the preceding CTA, then those that begin in a warp's share and go on
-        for (int i = -1; i < W; ++i) {
-            const int from = i < 0 ? 0 : i, place = i < 0 ? 0 : 1;
-            const int4 head = notes[from][place];
-            if (head.x < 0) continue;
-            int to = from;
-            bool ends = head.z;
-            while (!ends && to + 1 < W && notes[to + 1][0].x >= 0) ends = notes[++to][0].z;
-            const bool whole = place == 1 && ends;
-            float* const out = jp.cta_part + (static_cast<int64_t>(blockIdx.x) * 2 + place) * Sh::kPartFloats;
+        if (inside) {
+            __syncthreads();
+            float* const out = jp.part + static_cast<int64_t>(blockIdx.x) * W * 2 * Sh::kPartFloats;
             for (int unit = threadIdx.x; unit < HEADS * DP / 4; unit += W * 32) {  // accumulator: (head block n, step k, lane)
                 const int k = (unit >> 5) % Sh::kSteps, n = (unit >> 5) / Sh::kSteps, c = lane & 3;
                 DimPart sum;
                 sum.clear();
-                for (int w = from; w <= to; ++w) {
-                    const bool near = notes[w][w == from ? place : 0].w;
-                    const float* part = near ? reinterpret_cast<const float*>(rings + w * S * Sh::kStageBytes)
-                                             : jp.part + (static_cast<int64_t>(blockIdx.x) * W + w) * Sh::kPartFloats;
+#pragma unroll 4
+                for (int w = 0; w < W; ++w) {
+                    const float* part = reinterpret_cast<const float*>(rings + w * S * Sh::kStageBytes);
                     const float2* ml = reinterpret_cast<const float2*>(part + HEADS * DP) + n * 4 + c;
-                    if (near) sum.add(reinterpret_cast<const float4*>(part)[unit], ml[0], ml[HEADS / 2]);
-                    else sum.add(__ldcg(reinterpret_cast<const float4*>(part) + unit), __ldcg(ml), __ldcg(ml + HEADS / 2));
+                    sum.add(reinterpret_cast<const float4*>(part)[unit], ml[0], ml[HEADS / 2]);
                 }
-                if (whole) {
-                    sum.template finish<C>(a, head.x, heads_of<C, HEADS>(a, head.y), n, k, lane);
-                } else {
-                    reinterpret_cast<float4*>(out)[unit] = sum.o;
-                    if (k == 0 && lane < 4) {
-                        float2* ml = reinterpret_cast<float2*>(out + HEADS * DP) + n * 4 + c;
-                        ml[0] = make_float2(sum.m[0], sum.m[1]), ml[HEADS / 2] = make_float2(sum.l[0], sum.l[1]);
-                    }
+                reinterpret_cast<float4*>(out)[unit] = sum.o;
+                if (k == 0 && lane < 4) {
+                    float2* ml = reinterpret_cast<float2*>(out + HEADS * DP) + n * 4 + c;
+                    ml[0] = make_float2(sum.m[0], sum.m[1]), ml[HEADS / 2] = make_float2(sum.l[0], sum.l[1]);
                 }
             }
         }
@@ -1459,7 +1436,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
             const bool full = primed == S - 1;
             if (full) cp_async_wait_group<S - 2>();
             __syncwarp();
-            copy_next(1);
+            copy_next();
             if (!full) {
                 ++primed;
                 continue;
@@ -1510,8 +1487,20 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Args<C> a
     const int lane = unit & 31, k = (unit >> 5) % KS, n = (unit >> 5) / KS, c = lane & 3;
     DimPart s;
     s.clear();
+    // the i-th part: of warp first + i, where every CTA inside of the row has but one
+    int parts = d.w - d.z + 1, lead = parts, inner = 0;  // warps before the CTAs inside; those CTAs
+    if constexpr (by_group(C)) {
+        constexpr int W = Sh::kShareWarps;
+        const int from = d.z / W + 1;
+        inner = max(d.w / W - from, 0);
+        if (inner) {
+            lead = from * W - d.z;
+            parts -= inner * (W - 1);
+        }
+    }
+    const auto warp_of = [&](int i) { return d.z + i + (i < lead ? 0 : min(i - lead, inner) * (Sh::kShareWarps - 1)); };
 #pragma unroll 1
-    for (int q = d.z + static_cast<int>(threadIdx.y); q <= d.w; q += blockDim.y * kJoinDepth) {
+    for (int q = threadIdx.y; q < parts; q += blockDim.y * kJoinDepth) {
         float4 o[kJoinDepth];
         float2 m[kJoinDepth], l[kJoinDepth];
 #pragma unroll
@@ -1519,8 +1508,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Args<C> a
             const int p = q + i * blockDim.y;
             o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             m[i] = l[i] = make_float2(0.f, 0.f);
-            if (p <= d.w) {
-                const float* part = (by_group(C) ? jp.cta_part : jp.part) + (static_cast<int64_t>(p) * 2 + (p == d.z ? 1 : 0)) * Sh::kPartFloats;
+            if (p < parts) {
+                const float* part = jp.part + (static_cast<int64_t>(by_group(C) ? warp_of(p) : d.z + p) * 2 + (p == 0 ? 1 : 0)) * Sh::kPartFloats;
                 o[i] = __ldcg(reinterpret_cast<const float4*>(part) + unit);
                 m[i] = __ldcg(reinterpret_cast<const float2*>(part + HEADS * DP) + n * 4 + c);
                 l[i] = __ldcg(reinterpret_cast<const float2*>(part + HEADS * (DP + 1)) + n * 4 + c);
@@ -1567,7 +1556,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kRowWarps * 32), 1)
     bool bad = false;
     GroupRing<C, DP, NT> groups;
     if constexpr (by_group(C)) {
-        groups.open(smem_addr(smem), warp, W, S, lane);
+        groups.open(a, smem_addr(smem), warp, W, S, lane);
         if (a.tensor_copies && threadIdx.x == 0) prefetch_tensor_map(&a.k_map), prefetch_tensor_map(&a.v_map);
     } else if (a.cache.dim != DP) {
         clear_ring(smem, Sh::kRowSmem, threadIdx.x, W * 32);
@@ -1583,14 +1572,14 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kRowWarps * 32), 1)
     Request q{};
     if (b < a.B) {
         const bool early = a.window == 0 && (by_group(C) || TileCopy<C, DP, NT>::aligned(a));
-        const int most_tiles = (a.most + kTile - 1) / kTile;
+        const int most_tiles = (a.most + Sh::kTokens - 1) / Sh::kTokens;
         if constexpr (by_group(C)) {
             if (early) groups.look_up(a, b, hd.hk, 0, 0, a.most, first_tile, most_tiles, step, lane);
         } else {
             if (early) copy.look_up(a, b, q, first_tile, most_tiles, step, lane);
         }
         math.begin(a, b, hd, lane);
-        q = request_of<C>(a, b, bad);
+        q = request_of<C, Sh::kTokens>(a, b, bad);
         if constexpr (by_group(C)) {
             if (!early) groups.look_up(a, b, hd.hk, q.tile0, q.start, q.len, first_tile, q.tiles, step, lane);
         } else {
@@ -1600,66 +1589,37 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kRowWarps * 32), 1)
     }
     if (first_tile < q.tiles) {
         int ahead = first_tile, put = 0, slot = 0, primed = 0;
-        auto copy_next = [&](int n) {
-            while (n > 0 && ahead < q.tiles) {
-                int now = 1;
+        auto copy_next = [&] {
+            if (ahead < q.tiles) {
                 if constexpr (by_group(C)) {
-                    if (a.one_scale) {
-                        now = min(min(n, (q.tiles - ahead + step - 1) / step), groups.known);
-                        groups.copy_whole(a, hd.hk, q, ahead, step, now, put, S, lane, bad);
-                    } else {
-                        groups.copy(a, hd.hk, q, ahead, put, lane, bad);
-                        cp_async_commit();
-                    }
+                    if (a.scales != kTokenScales) groups.copy_boxes(a, hd.hk, q, ahead, put, lane, bad);
+                    else groups.copy(a, hd.hk, q, ahead, put, lane, bad);
                 } else {
                     const uint32_t mask = copy.copy(a, hd.hk, q, ahead, step, ring + put * Sh::kStageBytes, lane, bad);
                     if (lane == 0) tile_mask[warp][put] = mask;
-                    cp_async_commit();
                 }
-                n -= now;
-                put += now;
-                if (put >= S) put -= S;
-                ahead += now * step;
+                ahead += step;
                 if constexpr (by_group(C)) {
                     if (ahead < q.tiles && groups.known == 0) groups.look_up(a, b, hd.hk, q.tile0, q.start, q.len, ahead, q.tiles, step, lane);
                 } else {
                     if (ahead < q.tiles && copy.wants(a, ahead, step)) copy.look_up(a, b, q, ahead, q.tiles, step, lane);
                 }
             }
-            if (!by_group(C) || !one_scale<C>(a))
-                for (; n > 0; --n) cp_async_commit();
+            if (counts_groups<C>(a)) cp_async_commit();
+            put = put + 1 == S ? 0 : put + 1;
         };
         if constexpr (by_group(C)) {
-            constexpr int P = Sh::kPair;
             uint32_t parity = 0u;
-            copy_next(S);
-            for (int t = first_tile; t < q.tiles;) {
-                const bool pair = P == 2 && t + step < q.tiles;
-                const int next = slot + 1 == S ? 0 : slot + 1;
-                if (!one_scale<C>(a)) {
-                    if (pair) cp_async_wait_group<S - 2>();
-                    else cp_async_wait_group<S - 1>();
-                }
+            for (; primed < S; ++primed) copy_next();
+            for (int t = first_tile; t < q.tiles; t += step) {
+                if (counts_groups<C>(a)) cp_async_wait_group<S - 1>();
                 groups.wait(slot, parity);
-                if (pair) groups.wait(next, parity ^ (next == 0 ? 1u : 0u));
                 __syncwarp();
                 if (t == first_tile) math.ready(a, hd.hk, q.len, lane);
-                const int first = (q.tile0 + t) * kTile;
-                const uint32_t kt = groups.codes + slot * Sh::kStageBytes, info = groups.beside + slot * 144;
-                bool both = false;
-                if constexpr (P == 2) {
-                    both = pair;
-                    if (pair)
-                        math.template tiles<2>(a, q, {kt, groups.codes + next * Sh::kStageBytes}, {info, groups.beside + next * 144},
-                                               {first, first + step * kTile}, lane);
-                }
-                if (!both) math.template tiles<1>(a, q, {kt}, {info}, {first}, lane);
+                math.tile(a, q, groups.codes + slot * Sh::kStageBytes, groups.info + slot * Sh::kInfo, (q.tile0 + t) * Sh::kTokens, lane);
                 __syncwarp();
-                const int done = pair ? 2 : 1;
-                copy_next(done);
-                t += done * step;
-                slot += done;
-                if (slot >= S) slot -= S, parity ^= 1u;
+                copy_next();
+                if (++slot == S) slot = 0, parity ^= 1u;
             }
             if (groups.late) raise_device_error(a.err, W4A16_DEVERR_TIMEOUT);
         } else {
@@ -1667,7 +1627,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kRowWarps * 32), 1)
                 const bool full = primed == S - 1;
                 if (full) cp_async_wait_group<S - 2>();
                 __syncwarp();
-                copy_next(1);
+                copy_next();
                 if (!full) {
                     ++primed;
                     continue;
@@ -1792,7 +1752,7 @@ cudaError_t launch_attention_shape(const Args<C>& all, const DeviceInfo& dev, Jo
     if constexpr (by_group(C)) tokens = a.tokens;
     jp.rows = rows_of_request(a.q_heads * tokens, a.cache.heads, Sh::kHeads);
     int64_t all_rows = static_cast<int64_t>(a.B) * jp.rows;
-    const int tiles = most_tiles(a.most, a.window > 0 ? a.window + tokens - 1 : 0);  // of a row
+    const int tiles = most_tiles(a.most, a.window > 0 ? a.window + tokens - 1 : 0, Sh::kTokens);  // of a row
     // short rows: as many warps for each as one wave of CTAs has, if that leaves
     // a warp few tiles
     {
@@ -1820,8 +1780,7 @@ cudaError_t launch_attention_shape(const Args<C>& all, const DeviceInfo& dev, Jo
         a.block_table = all.block_table + from * a.table_stride, a.kv_len = all.kv_len + from;
         a.lse = all.lse ? all.lse + static_cast<int64_t>(from) * tokens * a.q_heads : nullptr;
         all_rows = static_cast<int64_t>(a.B) * jp.rows;
-        const int sharers = by_group(C) ? ctas : jp.warps;  // whose parts the join launch joins
-        jp.by_row = all_rows <= sharers;
+        jp.by_row = all_rows <= jp.warps;
         // (early, because a CTA has an SM for itself: several smaller ones that are placed
         // around others leave holes in the register file, and those that no longer fit then
         // run when the rest are done -- 20 key/value heads of 64 dims, 24 requests: 26 us)
@@ -1830,10 +1789,11 @@ cudaError_t launch_attention_shape(const Args<C>& all, const DeviceInfo& dev, Jo
         if (e != cudaSuccess) return e;
         // few rows: their accumulators over several CTAs, down to a warp's; as many
         // groups as a row has parts for, if rows are alike
-        const int places = jp.by_row ? static_cast<int>(all_rows) : sharers, units = Sh::kHeads * DP / 4;
+        const int places = jp.by_row ? static_cast<int>(all_rows) : jp.warps, units = Sh::kHeads * DP / 4;
         int width = 128;
         while (units % width || (width > 32 && places * (units / width) < dev.sms)) width /= 2;
-        const int parts = sharers / places + 2;
+        int parts = jp.warps / places + 2;
+        if (by_group(C)) parts = std::min(parts, 2 * Sh::kShareWarps + ctas / places);  // (a part a CTA inside of a row)
         int groups = 1;
         while (groups * width < kJoinThreads && groups * kJoinDepth < parts) groups *= 2;
         e = launch_kernel(k_attention_join<C, DP, NT>, true, 1, dim3(places, units / width), dim3(width, groups), 0, s, a, jp);

@@ -57,6 +57,10 @@ struct ScaledReadArgs {
 
 cudaError_t launch_scaled_read(const ScaledReadArgs& a, const DeviceInfo& dev, cudaStream_t s);
 
+constexpr int kBoxScales = 0;    // a box lies in one group, whose scales come with its block id
+constexpr int kRowScales = 1;    // groups of 1, 2 or 4 tokens, four or more in a box, their scales one after another in memory
+constexpr int kTokenScales = 2;  // one by one
+
 // The one-token launch's arguments (its cache without scales; q_heads: those of a
 // token), and what several tokens and scales by group need.
 struct ScaledAttentionArgs : AttentionArgs {
@@ -67,10 +71,11 @@ struct ScaledAttentionArgs : AttentionArgs {
     int64_t ks_block, ks_group, ks_head, vs_block, vs_group, vs_head;
     int group;
     uint32_t magic;  // of group
-    // A tile of 16 tokens is one box, or 2^boxes_log2 = boxes of them, that lies in one block;
-    // tensor_copies: its codes come by tensor copies (boxes of 16 or 8 tokens); one_scale: it is one
-    // box and lies in one group.
-    int boxes, boxes_log2, tensor_copies, one_scale;
+    // A tile's tokens are boxes of 2^box_log2, each in one block; tensor_copies: their codes come by
+    // tensor copies (boxes of 8, 16 or 32 tokens).
+    int box_log2, tensor_copies;
+    int scales;      // where those of a tile come from:
+    int group_log2;  //   kRowScales: of group; else 0
     CUtensorMap k_map;  // boxes of one head's values by `box` tokens of a block
     CUtensorMap v_map;
 };
