@@ -966,7 +966,7 @@ size_t w4a16_scaled_attention_workspace_bytes(int q_heads, int kv_heads, int dim
     if (q_heads < 1 || q_heads >= (1 << 24) || kv_heads < 1 || q_heads % kv_heads != 0 || dim < 16 || dim > 256 ||
         dim % 16 != 0 || new_tokens < 1 || new_tokens > kMostNew)
         return 0;
-    return paged_attention_workspace(q_heads * new_tokens, kv_heads, dim);
+    return scaled_attention_workspace(q_heads, kv_heads, dim, new_tokens);
 }
 
 w4a16_status w4a16_scaled_attention(const uint16_t* q, int64_t q_request, int64_t q_token, int64_t q_head,
@@ -992,7 +992,7 @@ w4a16_status w4a16_scaled_attention(const uint16_t* q, int64_t q_request, int64_
     if (!aligned16(q) || !aligned16(out) || !row_strides(q_request, q_head, 8) || !row_strides(q_token, out_token, 8) ||
         !row_strides(out_request, out_head, 8) || !aligned4(block_table) || !aligned4(kv_len) || !aligned4(lse))
         return W4A16_ERR_ALIGN;
-    if (!workspace || workspace_bytes < paged_attention_workspace(q_heads * new_tokens, cache->heads, cache->dim))
+    if (!workspace || workspace_bytes < scaled_attention_workspace(q_heads, cache->heads, cache->dim, new_tokens))
         return W4A16_ERR_WORKSPACE;
     if (!aligned16(workspace)) return W4A16_ERR_ALIGN;
     DeviceCache* dev = nullptr;

@@ -210,20 +210,22 @@ struct AttnShape {
     static constexpr int kInfoKeys = kTokens * 2, kInfoValues = kTokens * 6, kInfo = kTokens * 10;
     // that and a barrier are beside a stage; and what aligns the first one
     static constexpr int kBeside = by_group(C) ? kInfo + 8 : 0, kAlign = by_group(C) ? 1024 : 0;
+    // more than 16 heads: their queries, which registers do not hold beside the sums, of each warp
+    static constexpr int kQueries = NT > 2 ? NT * kSteps * 256 : 0;
     static constexpr int kPartFloats = kHeads * (DP + 2);
     // shares: one CTA an SM, of as many warps as its registers allow (the accumulators'
     // size decides) with rings of three stages or more
-    static constexpr int kShareWarps = 4 * (k8 ? (NT == 1 ? (DP == 64 ? 4 : DP <= 128 ? 3 : 2) : (DP == 64 ? 3 : 2))
+    static constexpr int kShareWarps = 4 * (k8 ? (NT == 1 ? (DP == 64 ? 4 : DP <= 128 ? 3 : 2) : (DP == 64 && NT == 2 ? 3 : 2))
                                                  : (DP == 64 ? 3 : DP <= 128 ? 2 : 1));
-    static constexpr int kFit = (226 * 1024 - kAlign) / (kShareWarps * (kStageBytes + kBeside));
+    static constexpr int kFit = (226 * 1024 - kAlign - kShareWarps * kQueries) / (kShareWarps * (kStageBytes + kBeside));
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
-    static constexpr int kSmem = kShareWarps * kStages * (kStageBytes + kBeside) + kAlign;
+    static constexpr int kSmem = kShareWarps * (kStages * (kStageBytes + kBeside) + kQueries) + kAlign;
     // rows: one CTA an SM
     static constexpr int kRowWarps = kStageBytes > 12288 ? 4 : 8;
-    static constexpr int kRowFit = (225 * 1024 - kAlign) / (kRowWarps * (kStageBytes + kBeside));
+    static constexpr int kRowFit = (225 * 1024 - kAlign - kRowWarps * kQueries) / (kRowWarps * (kStageBytes + kBeside));
     static constexpr int kRowStages = kRowFit > 4 ? 4 : kRowFit;
     static constexpr int kRowRing = kRowStages * kStageBytes;  // of a warp
-    static constexpr int kRowSmem = kRowWarps * (kRowRing + kRowStages * kBeside) + kAlign;
+    static constexpr int kRowSmem = kRowWarps * (kRowRing + kRowStages * kBeside + kQueries) + kAlign;
     // scales by group: how many 16 tokens are worked on together, where registers allow
     static constexpr int kTogether = kTokens == 32 && NT == 1 ? 2 : 1;
     static constexpr int kPartBytes = kHeads * DP * 4;
@@ -231,6 +233,7 @@ struct AttnShape {
     static_assert(kStages >= (kTokens == 32 ? 2 : 3), "ring too short");
     static_assert(kRowStages >= 2 && kRowRing >= kPartBytes, "no room for a warp's part");
     static_assert(160 * kShareWarps <= most_workers(DP), "workspace");
+    static_assert(!by_group(C) || kStages * kStageBytes >= kPartBytes, "no room for a warp's part");
 };
 
 // New tokens of a request.
@@ -350,7 +353,9 @@ template <int C, int DP, int NT>
 struct RowMath {
     using Sh = AttnShape<C, DP, NT>;
     static constexpr int CH = Sh::kChunks, KS = Sh::kSteps;
-    uint32_t qf[NT][KS][2];              // queries as B fragments (columns: heads)
+    static constexpr bool kQueriesNear = NT > 2;  // in shared memory: [step][head block][lane] pairs of words
+    uint32_t qf[kQueriesNear ? 1 : NT][KS][2];    // queries as B fragments (columns: heads)
+    uint32_t queries;                             // or where those are
     float sl[NT][2];                     // score scale of columns 2c, 2c + 1
     float m[NT][2], l[NT][2];            // of columns 2c, 2c + 1 (l: of this lane's tokens until reduced)
     float4 o[NT][KS];                    // dims r, r + 8 (8 bits: 2r, 2r + 1) by columns 2c, 2c + 1
@@ -360,24 +365,31 @@ struct RowMath {
     float big[NT][2];
     int upto[NT][2];
 
+    // the queries of head block n
+    __device__ __forceinline__ void request(const Args<C>& a, int b, const Heads& hd, int n, uint32_t (&q)[KS][2], int lane) const {
+        const int r = lane >> 2, c = lane & 3;
+        const uint16_t* qp = query_of<C>(a, b, hd, n * 8 + r);
+        const bool have = n * 8 + r < hd.n;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            q[k][0] = q[k][1] = 0u;
+            if (have && k * 16 < a.cache.dim) {
+                // bf16: dims 2c, 2c + 1 and 8 further; 8 bits: the four dims whose codes one word holds
+                const int d = k * 16 + (in_8_bits(C) ? 4 * c : 2 * c);
+                q[k][0] = *reinterpret_cast<const uint32_t*>(qp + d);
+                q[k][1] = *reinterpret_cast<const uint32_t*>(qp + d + (in_8_bits(C) ? 2 : 8));
+            }
+        }
+    }
+
     // requests the queries and clears the sums
     __device__ __forceinline__ void begin(const Args<C>& a, int b, const Heads& hd, int lane) {
-        const int r = lane >> 2, c = lane & 3;
+        const int c = lane & 3;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const uint16_t* qp = query_of<C>(a, b, hd, n * 8 + r);
-            const bool have = n * 8 + r < hd.n;
+            if (!kQueriesNear) request(a, b, hd, n, qf[kQueriesNear ? 0 : n], lane);
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                qf[n][k][0] = qf[n][k][1] = 0u;
-                if (have && k * 16 < a.cache.dim) {
-                    // bf16: dims 2c, 2c + 1 and 8 further; 8 bits: the four dims whose codes one word holds
-                    const int d = k * 16 + (in_8_bits(C) ? 4 * c : 2 * c);
-                    qf[n][k][0] = *reinterpret_cast<const uint32_t*>(qp + d);
-                    qf[n][k][1] = *reinterpret_cast<const uint32_t*>(qp + d + (in_8_bits(C) ? 2 : 8));
-                }
-                o[n][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
+            for (int k = 0; k < KS; ++k) o[n][k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 m[n][e] = -INFINITY;
@@ -391,37 +403,39 @@ struct RowMath {
     }
 
     // makes the queries that begin() requested into operands
-    __device__ __forceinline__ void ready(const Args<C>& a, int hk, int len, int lane) {
+    __device__ __forceinline__ void ready(const Args<C>& a, int b, const Heads& hd, int len, int lane) {
         const int c = lane & 3;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            sl[n][0] = sl[n][1] = a.scale * 1.4426950408889634f * (C == kE4m3 ? a.cache.k_scale[hk] : 1.f);
+            sl[n][0] = sl[n][1] = a.scale * 1.4426950408889634f * (C == kE4m3 ? a.cache.k_scale[hd.hk] : 1.f);
             if (by_group(C)) upto[n][0] += len, upto[n][1] += len;
             if (in_8_bits(C)) {
+                if (kQueriesNear) request(a, b, hd, n, qf[0], lane);
+                uint32_t(&q)[KS][2] = qf[kQueriesNear ? 0 : n];
                 // to fp16, scaled by a power of two that takes the head's largest into [2^14, 2^15)
                 uint32_t big = 0u;
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
-                    big = __vmaxu2(big, __vmaxu2(qf[n][k][0] & 0x7FFF7FFFu, qf[n][k][1] & 0x7FFF7FFFu));
+                    big = __vmaxu2(big, __vmaxu2(q[k][0] & 0x7FFF7FFFu, q[k][1] & 0x7FFF7FFFu));
                 big = max(big & 0xFFFFu, big >> 16);
                 big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
                 big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
                 const int sh = min(141 - min(static_cast<int>(big >> 7), 254), 126);
                 const float up = exp2i(sh), down = exp2i(-sh);
 #pragma unroll
-                for (int k = 0; k < KS; ++k)
+                for (int k = 0; k < KS; ++k) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint32_t v = qf[n][k][e];
+                        const uint32_t v = q[k][e];
                         const __half2 h = __floats2half2_rn(bf16_to_f32(v & 0xFFFFu) * up, bf16_to_f32(v >> 16) * up);
-                        qf[n][k][e] = *reinterpret_cast<const uint32_t*>(&h);
+                        q[k][e] = *reinterpret_cast<const uint32_t*>(&h);
                     }
-                if (C == kInt8Groups) {  // the pairs that codes_to_f16 makes
-#pragma unroll
-                    for (int k = 0; k < KS; ++k) {
-                        const uint32_t v0 = qf[n][k][0], v1 = qf[n][k][1];
-                        qf[n][k][0] = __byte_perm(v0, v1, 0x5410), qf[n][k][1] = __byte_perm(v0, v1, 0x7632);
+                    if (C == kInt8Groups) {  // the pairs that codes_to_f16 makes
+                        const uint32_t v0 = q[k][0], v1 = q[k][1];
+                        q[k][0] = __byte_perm(v0, v1, 0x5410), q[k][1] = __byte_perm(v0, v1, 0x7632);
                     }
+                    if (kQueriesNear)
+                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(queries + ((k * NT + n) * 32 + lane) * 8), "r"(q[k][0]), "r"(q[k][1]) : "memory");
                 }
                 sl[n][0] *= __shfl_sync(0xFFFFFFFFu, down, 8 * c);
                 sl[n][1] *= __shfl_sync(0xFFFFFFFFu, down, 8 * c + 4);
@@ -639,7 +653,15 @@ struct RowMath {
                     codes_to_f16<C>(f[2 * j], a0, a2);
                     codes_to_f16<C>(f[2 * j + 1], a1, a3);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) attn_mma<C>(kTwo && j ? s1[n] : s[p][n], a0, a1, a2, a3, qf[n][k + j][0], qf[n][k + j][1]);
+                    for (int n = 0; n < NT; ++n) {
+                        uint32_t q0, q1;
+                        if constexpr (kQueriesNear) {
+                            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(q0), "=r"(q1) : "r"(queries + (((k + j) * NT + n) * 32 + lane) * 8) : "memory");
+                        } else {
+                            q0 = qf[n][k + j][0], q1 = qf[n][k + j][1];
+                        }
+                        attn_mma<C>(kTwo && j ? s1[n] : s[p][n], a0, a1, a2, a3, q0, q1);
+                    }
                 }
             }
         uint32_t mask[P], pf[P][NT][2];
@@ -1231,8 +1253,16 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
     // requests without tokens
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         if (request_of<C, Sh::kTokens>(a, b, bad).tiles > 0) continue;
-        if (by_group(C)) {
-            for (int row = 0; row < rows; ++row) store_empty<C>(a, b, heads_of<C, HEADS>(a, row), threadIdx.x, W * 32);
+        if constexpr (by_group(C)) {
+            const int per = a.cache.dim / 8;
+            for (int i = threadIdx.x; i < a.tokens * a.q_heads * per; i += W * 32) {
+                const int j = i / per, token = j / a.q_heads;
+                *reinterpret_cast<uint4*>(a.out + b * a.out_request + token * a.out_token + (j - token * a.q_heads) * a.out_head + (i - j * per) * 8) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (a.lse)
+                for (int j = threadIdx.x; j < a.tokens * a.q_heads; j += W * 32)
+                    a.lse[static_cast<int64_t>(b) * a.tokens * a.q_heads + j] = -INFINITY;
         } else {
             store_empty<C>(a, b, Heads{0, 0, a.q_heads}, threadIdx.x, W * 32);
         }
@@ -1313,6 +1343,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
 
     // Scales by group: a CTA all of whose warps lie inside of one row joins their parts itself, to
     // that of its first one, so that a long row leaves few to the join launch.
+    __shared__ __align__(8) float near_ml[by_group(C) ? W : 1][2 * HEADS];
     bool inside = false;
     uint8_t* const rings = smem + (by_group(C) ? (0u - smem_addr(smem)) & 1023u : 0u);
     if constexpr (by_group(C))
@@ -1321,6 +1352,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
     // The copies run ahead of the products: `ahead` is the segment of the next
     // tile to copy, ahead_t the tile.
     RowMath<C, DP, NT> math;
+    if (Sh::kQueries) math.queries = smem_addr(rings) + W * S * (Sh::kStageBytes + Sh::kBeside) + warp * Sh::kQueries;
     TileCopy<C, DP, NT> copy;
     Segment ahead = seg;
     int ahead_t = seg.t0, ahead_hk = heads_of<C, HEADS>(a, seg.row).hk;
@@ -1380,7 +1412,8 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
             // (inside: into the ring, which is empty then)
             float* part = inside ? reinterpret_cast<float*>(rings + warp * S * Sh::kStageBytes)
                                  : jp.part + (static_cast<int64_t>(worker) * 2 + (begins ? 1 : 0)) * Sh::kPartFloats;
-            math.store_part(part, part + HEADS * DP, part + HEADS * (DP + 1), lane);
+            float* const ml = inside ? near_ml[warp] : part + HEADS * DP;
+            math.store_part(part, ml, ml + HEADS, lane);
         }
         // a row that begins here: what the join launch has to do for it
         if (begins && lane == 0 && (jp.by_row || !ends))
@@ -1400,7 +1433,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
             if (counts_groups<C>(a)) cp_async_wait_group<S - 1>();
             groups.wait(slot, parity);
             __syncwarp();
-            if (t == seg.t0) math.ready(a, hd.hk, seg.q.len, lane);
+            if (t == seg.t0) math.ready(a, seg.b, hd, seg.q.len, lane);
             math.tile(a, seg.q, groups.codes + slot * Sh::kStageBytes, groups.info + slot * Sh::kInfo, (seg.q.tile0 + t) * Sh::kTokens, lane);
             __syncwarp();
             copy_next();
@@ -1418,7 +1451,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
 #pragma unroll 4
                 for (int w = 0; w < W; ++w) {
                     const float* part = reinterpret_cast<const float*>(rings + w * S * Sh::kStageBytes);
-                    const float2* ml = reinterpret_cast<const float2*>(part + HEADS * DP) + n * 4 + c;
+                    const float2* ml = reinterpret_cast<const float2*>(near_ml[w]) + n * 4 + c;
                     sum.add(reinterpret_cast<const float4*>(part)[unit], ml[0], ml[HEADS / 2]);
                 }
                 reinterpret_cast<float4*>(out)[unit] = sum.o;
@@ -1441,7 +1474,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
                 ++primed;
                 continue;
             }
-            if (t == seg.t0) math.ready(a, hd.hk, seg.q.len, lane);
+            if (t == seg.t0) math.ready(a, seg.b, hd, seg.q.len, lane);
             math.tile(ring + slot * Sh::kStageBytes, tile_mask[warp][slot], lane);
             slot = slot + 1 == S ? 0 : slot + 1;
             if (++t >= seg.t1) end_row();
@@ -1568,6 +1601,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kRowWarps * 32), 1)
     // Queries, block ids (where they do not depend on the length) and length are
     // requested together.
     RowMath<C, DP, NT> math;
+    if (Sh::kQueries) math.queries = smem_addr(smem) + W * S * (Sh::kStageBytes + Sh::kBeside) + warp * Sh::kQueries;
     TileCopy<C, DP, NT> copy;
     Request q{};
     if (b < a.B) {
@@ -1615,7 +1649,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kRowWarps * 32), 1)
                 if (counts_groups<C>(a)) cp_async_wait_group<S - 1>();
                 groups.wait(slot, parity);
                 __syncwarp();
-                if (t == first_tile) math.ready(a, hd.hk, q.len, lane);
+                if (t == first_tile) math.ready(a, b, hd, q.len, lane);
                 math.tile(a, q, groups.codes + slot * Sh::kStageBytes, groups.info + slot * Sh::kInfo, (q.tile0 + t) * Sh::kTokens, lane);
                 __syncwarp();
                 copy_next();
@@ -1632,7 +1666,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kRowWarps * 32), 1)
                     ++primed;
                     continue;
                 }
-                if (t == first_tile) math.ready(a, hd.hk, q.len, lane);
+                if (t == first_tile) math.ready(a, b, hd, q.len, lane);
                 math.tile(ring + slot * Sh::kStageBytes, tile_mask[warp][slot], lane);
                 slot = slot + 1 == S ? 0 : slot + 1;
                 t += step;
@@ -1800,6 +1834,18 @@ cudaError_t launch_attention_shape(const Args<C>& all, const DeviceInfo& dev, Jo
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
+}
+
+// Scales by group: more than 16 columns, which share what it takes to bring a tile and make
+// it operands, as 24 or 32 together (five new tokens of 4 heads as 16 and 4: 96 us, as 24: MEASURE).
+template <int C>
+cudaError_t launch_attention_wide(const Args<C>& a, const DeviceInfo& dev, const JoinPlan& jp, cudaStream_t s) {
+    const bool three = columns_together(a.q_heads / a.cache.heads * a.tokens, a.cache.dim) == 24;
+    switch (padded_dim(a.cache.dim)) {
+        case 64: return three ? launch_attention_shape<C, 64, 3>(a, dev, jp, s) : launch_attention_shape<C, 64, 4>(a, dev, jp, s);
+        case 96: return three ? launch_attention_shape<C, 96, 3>(a, dev, jp, s) : launch_attention_shape<C, 96, 4>(a, dev, jp, s);
+        default: return three ? launch_attention_shape<C, 128, 3>(a, dev, jp, s) : launch_attention_shape<C, 128, 4>(a, dev, jp, s);
+    }
 }
 
 template <int C>

@@ -86,6 +86,13 @@ struct ScaledAttentionArgs : AttentionArgs {
 bool encode_cache_map(CUtensorMap* map, const void* codes, const w4a16_scaled_cache& c, int64_t block, int64_t token, int64_t head, int inner,
                       int box);
 
+// Columns (new tokens times the query heads of a key/value head) that are worked on together:
+// 8, 16, and up to 128 dims 24 or 32, of as equal rows as there are.
+constexpr int columns_together(int columns, int dim) {
+    const int most = dim <= 128 ? 32 : 16, rows = (columns + most - 1) / most;
+    return (columns + 8 * rows - 1) / (8 * rows) * 8;
+}
+size_t scaled_attention_workspace(int q_heads, int kv_heads, int dim, int new_tokens);
 cudaError_t launch_scaled_attention(const ScaledAttentionArgs& a, int int8, const DeviceInfo& dev, cudaStream_t s);
 
 }  // namespace w4a16
