@@ -2,10 +2,12 @@
 INT4 fused QKV projection, rotary positions and cache append, attention over
 the paged cache, INT4 output projection, routed SwiGLU experts.
 
-    python examples/decode_step.py [--requests 4] [--steps 8] [--cache e4m3] [--graph]
+    python examples/decode_step.py [--requests 4] [--steps 8] [--cache int8] [--graph]
 
 Weights and requests are random; the requests begin with contexts of different
-lengths, whose keys and values are put into the cache as a prompt's would be.
+lengths, whose keys and values are put into the cache as a prompt's would be.  The
+cache is bf16, e4m3 with a fixed scale a head, or int8 or e4m3 with scales by groups
+of 16 tokens that are found as it is written (int8, e4m3-groups).
 With --graph a step is captured once in a CUDA graph and replayed: lengths,
 block tables and slots are all made on the GPU, so nothing of a step depends
 on the host.  Needs the library built and a GB300.
@@ -54,28 +56,43 @@ class Layer:
 class Requests:
     """The running requests: their lengths, block table and share of the cache."""
 
-    def __init__(self, layer: Layer, contexts, room, page=16, e4m3=False, seed=0):
+    def __init__(self, layer: Layer, contexts, room, page=16, e4m3=False, seed=0, groups=None):
         n = len(contexts)
         columns = -(-(max(contexts) + room) // page)
         self.blocks, self.page = n * columns, page
         shape = (self.blocks, page, layer.kv_heads, layer.dim)
-        dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
-        scales = [torch.full((layer.kv_heads,), 1 / 32, device="cuda") for _ in range(2)] if e4m3 else [None, None]
-        self.cache = w.PagedCache(torch.zeros(shape, dtype=dtype, device="cuda"), torch.zeros(shape, dtype=dtype, device="cuda"), *scales)
+        if groups is not None:  # the codes' type: scales by groups of 16 tokens; nothing needs initialisation
+            codes = [torch.empty(shape, dtype=groups, device="cuda") for _ in range(2)]
+            scales = [torch.empty(self.blocks, layer.kv_heads, page // 16, device="cuda").transpose(1, 2) for _ in range(2)]
+            self.cache = w.ScaledCache(*codes, *scales)
+            self.workspace = w.scaled_attention_workspace(self.cache, layer.q_heads)
+        else:
+            dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+            scales = [torch.full((layer.kv_heads,), 1 / 32, device="cuda") for _ in range(2)] if e4m3 else [None, None]
+            self.cache = w.PagedCache(torch.zeros(shape, dtype=dtype, device="cuda"), torch.zeros(shape, dtype=dtype, device="cuda"), *scales)
+            self.workspace = w.paged_attention_workspace(self.cache, layer.q_heads)
         self.table = torch.full((n, columns), -1, dtype=torch.int32, device="cuda")
         order = torch.randperm(self.blocks, generator=torch.Generator().manual_seed(seed))
         self.free = order.int().cuda()
         self.free_head = torch.zeros(1, dtype=torch.int32, device="cuda")
         self.lengths = torch.zeros(n, dtype=torch.int32, device="cuda")
         self.one = torch.ones(n, dtype=torch.int32, device="cuda")
-        self.workspace = w.paged_attention_workspace(self.cache, layer.q_heads)
         # the contexts: keys and values as a prompt's projection would give them
         gen = torch.Generator(device="cuda").manual_seed(seed + 1)
         total = sum(contexts)
         self.advance(w.w4a16_paged_map(self.lengths, torch.tensor(contexts, dtype=torch.int32, device="cuda"), self.table, self.free,
                                        self.free_head, page, self.blocks, total))
         self.prompt = [torch.randn(total, layer.kv_heads, layer.dim, generator=gen, device="cuda").bfloat16() for _ in range(2)]
-        w.w4a16_rope_append(None, *self.prompt, self.map.positions, layer.inv_freq, self.map.slots, self.cache)
+        self.append(None, *self.prompt, self.map, layer.inv_freq)
+
+    def append(self, q, k, v, m, inv_freq):
+        """Rotary positions on q (in place) and k, k and v into the cache."""
+        call = w.w4a16_scaled_append if isinstance(self.cache, w.ScaledCache) else w.w4a16_rope_append
+        call(q, k, v, m.positions, inv_freq, m.slots, self.cache, q_out=q)
+
+    def attend(self, q, m):
+        call = w.w4a16_scaled_attention if isinstance(self.cache, w.ScaledCache) else w.w4a16_paged_attention
+        return call(q, self.cache, self.table, m.kv_len, workspace=self.workspace)[0]
 
     def advance(self, m):
         self.map = m
@@ -90,8 +107,8 @@ def step(layer: Layer, req: Requests, x):
     qkv = w.w4a16_gemv(x, *layer.qkv, GROUP, weights_static=True)
     q, k, v = (t.view(n, -1, layer.dim) for t in
                qkv.split([layer.q_heads * layer.dim, layer.kv_heads * layer.dim, layer.kv_heads * layer.dim], 1))
-    w.w4a16_rope_append(q, k, v, m.positions, layer.inv_freq, m.slots, req.cache, q_out=q)
-    a, _ = w.w4a16_paged_attention(q, req.cache, req.table, m.kv_len, workspace=req.workspace)
+    req.append(q, k, v, m, layer.inv_freq)
+    a = req.attend(q, m)
     x = x + w.w4a16_gemv(a.view(n, -1), *layer.out, GROUP, weights_static=True)
     top, ids = torch.topk(x.float() @ layer.router, layer.topk)
     y = x + w.moe_ffn(x, ids.int(), torch.softmax(top, 1), layer.gate, layer.up, layer.down, GROUP)
@@ -103,12 +120,13 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--requests", type=int, default=4, help="1 to 16")
     ap.add_argument("--steps", type=int, default=8)
-    ap.add_argument("--cache", choices=("bf16", "e4m3"), default="bf16")
+    ap.add_argument("--cache", choices=("bf16", "e4m3", "int8", "e4m3-groups"), default="bf16")
     ap.add_argument("--graph", action="store_true")
     a = ap.parse_args()
     layer = Layer()
     contexts = [37 + 911 * i for i in range(a.requests)]
-    req = Requests(layer, contexts, room=a.steps + 8, e4m3=a.cache == "e4m3")
+    groups = {"int8": torch.int8, "e4m3-groups": torch.float8_e4m3fn}.get(a.cache)
+    req = Requests(layer, contexts, room=a.steps + 8, e4m3=a.cache == "e4m3", groups=groups)
     x = torch.randn(a.requests, 4096, device="cuda").bfloat16()
     step(layer, req, x)  # everything loaded before the capture and the clock
     if a.graph:
