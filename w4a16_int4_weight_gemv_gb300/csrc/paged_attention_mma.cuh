@@ -226,8 +226,10 @@ struct AttnShape {
     static constexpr int kRowStages = kRowFit > 4 ? 4 : kRowFit;
     static constexpr int kRowRing = kRowStages * kStageBytes;  // of a warp
     static constexpr int kRowSmem = kRowWarps * (kRowRing + kRowStages * kBeside + kQueries) + kAlign;
-    // scales by group: how many 16 tokens are worked on together, where registers allow
-    static constexpr int kTogether = kTokens == 32 && NT == 1 ? 2 : 1;
+    // scales by group: how many 16 tokens are worked on together.  Two for up to 24 columns
+    // (drafts of 4 tokens of 4 heads, 16 x 8192 tokens of int8 77 -> 70 us; of 5 tokens 96 ->
+    // 91), one for 32, whose registers then spill twice as much (121 -> 131).
+    static constexpr int kTogether = kTokens == 32 && NT <= 3 ? 2 : 1;
     static constexpr int kPartBytes = kHeads * DP * 4;
     static constexpr bool kClusters = kRowRing >= 2 * kPartBytes;  // room for the CTA's part behind a warp's
     static_assert(kStages >= (kTokens == 32 ? 2 : 3), "ring too short");
