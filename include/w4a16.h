@@ -702,7 +702,7 @@ W4A16_API w4a16_status w4a16_scaled_read(const w4a16_scaled_cache* cache,
 
 /*
  * w4a16_scaled_attention_workspace_bytes -- device workspace of
- * w4a16_scaled_attention for this head layout and number of new tokens.
+ * w4a16_scaled_attention for this head layout and as many new tokens, or fewer.
  */
 W4A16_API size_t w4a16_scaled_attention_workspace_bytes(int q_heads, int kv_heads, int dim,
                                                         int new_tokens);

@@ -117,6 +117,13 @@ def test_attention_checks(w):
         assert call() == S.ERR_CUDA and call(window=2 ** 31 - 1) == S.ERR_CUDA
 
 
+@pytest.mark.parametrize("dim", [16, 64, 128, 144, 256])
+@pytest.mark.parametrize("hq", [1, 3, 4, 5, 7, 9, 16, 40])
+def test_workspace_serves_fewer_new_tokens(w, hq, dim):
+    size = [w.load_library().w4a16_scaled_attention_workspace_bytes(hq, 1, dim, n) for n in range(1, 17)]
+    assert size == sorted(size)
+
+
 def test_attention_refuses_tables_whose_tiles_pass_32_bits(w):
     S, lib = w.Status, w.load_library()
     def call(columns, page, kv, hq, new, window=0):

@@ -88,8 +88,9 @@ bool encode_cache_map(CUtensorMap* map, const void* codes, const w4a16_scaled_ca
 
 // Columns (new tokens times the query heads of a key/value head) that are worked on together:
 // 8, 16, and up to 128 dims 24 or 32, of as equal rows as there are.
+constexpr int most_together(int dim) { return dim <= 128 ? 32 : 16; }
 constexpr int columns_together(int columns, int dim) {
-    const int most = dim <= 128 ? 32 : 16, rows = (columns + most - 1) / most;
+    const int most = most_together(dim), rows = (columns + most - 1) / most;
     return (columns + 8 * rows - 1) / (8 * rows) * 8;
 }
 size_t scaled_attention_workspace(int q_heads, int kv_heads, int dim, int new_tokens);

@@ -13,7 +13,8 @@ cudaError_t launch_attention_e4m3_groups_wide(const ScaledAttentionArgs& a, cons
 cudaError_t launch_attention_int8_groups_wide(const ScaledAttentionArgs& a, const DeviceInfo& dev, JoinPlan join, cudaStream_t s);
 
 size_t scaled_attention_workspace(int q_heads, int kv_heads, int dim, int new_tokens) {
-    const int padded = padded_dim(dim), columns = columns_together(q_heads / kv_heads * new_tokens, dim);
+    // (fewer new tokens may be worked on in larger rows: 36 columns as 24 twice, 32 as they are)
+    const int padded = padded_dim(dim), columns = std::min((q_heads / kv_heads * new_tokens + 7) / 8 * 8, most_together(dim));
     return static_cast<size_t>(most_workers(padded)) * (sizeof(int4) + 2 * static_cast<size_t>(columns) * (padded + 2) * sizeof(float));
 }
 
