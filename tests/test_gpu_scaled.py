@@ -739,7 +739,7 @@ def test_refusals(w):
             (w.w4a16_scaled_append, dict(slots=i32(range(5)).long())), (w.w4a16_scaled_append, dict(v=x.float())), (w.w4a16_scaled_append, dict(q_out=x[:2])),
             (w.w4a16_scaled_read, dict(rows=None)), (w.w4a16_scaled_read, dict(dtype=torch.float16)), (w.w4a16_scaled_read, dict(row_start=i32([0, 40]))),
             (w.w4a16_scaled_read, dict(k_out=z(43, 2, 64))), (w.w4a16_scaled_read, dict(k_out=z(43, 2, 64), v_out=z(43, 2, 64, dtype=torch.float32))),
-            (w.w4a16_scaled_read, dict(k_out=z(43, 2, 32), v_out=z(43, 2, 32)))):
+            (w.w4a16_scaled_read, dict(k_out=z(43, 2, 32), v_out=z(43, 2, 32))), (w.w4a16_scaled_read, dict(k_out=z(44, 2, 64), v_out=z(44, 2, 64)))):
         with pytest.raises((ValueError, TypeError)):
             call(**{**bases[call], **bad})
     other = w.PagedCache(z(2, 16, 2, 64), z(2, 16, 2, 64))

@@ -1015,7 +1015,7 @@ def w4a16_scaled_read(cache: ScaledCache, block_table, row_start, first=None, k_
     they are.  Without k_out and v_out: new tensors of `rows` rows and `dtype`,
     zeros where no request has a row.  Returns (k_out, v_out)."""
     _scaled(cache)
-    if _fast is not None and k_out is not None and first is None:
+    if _fast is not None and k_out is not None and first is None and rows is None:
         rc = _fast.scaled_read(cache._ref, cache.heads, cache.dim, cache.device, block_table, row_start, k_out, v_out,
                                None if stream is None else stream.cuda_stream)
         if rc == 0:

@@ -463,6 +463,7 @@ cudaError_t launch_scaled_append(const ScaledAppendArgs& a, const DeviceInfo& de
     plan.turns = plan.chunk == kChunk && plan.q_chunk == kChunk;
     plan.kv_ctas = static_cast<unsigned>(chunks(plan.chunk) * plan.kv_parts);
     const int64_t ctas = plan.kv_ctas + chunks(plan.q_chunk) * plan.q_parts;
+    if (ctas >= int64_t(1) << 31) return cudaErrorInvalidConfiguration;  // (2^31 tokens of 65536 heads, all one by strides of 0)
     const bool many = ctas > 2 * dev.sms;
     const int tokens = std::max(plan.chunk + a.cache.group - 1, plan.q_chunk);
     const int smem = std::max(tokens * half * 8, 16);
