@@ -474,6 +474,22 @@ def test_attention_shares_inside_a_window(w, dim, group, new, dtype):
     check_attention(w, q, cache, table, lens, window=8999)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("group,new", [(4, 6), (8, 3), (4, 8), (2, 16)])
+def test_attention_24_and_32_columns_together(w, group, new, dim, dtype):
+    # long rows: a CTA's warps join inside of one; short ones: in their CTA
+    lens = [20011, 5, 0, 1999]
+    q, cache, table = attention_problem(w, dim + group, lens, new, group, 1, dim, 32, 8, TYPES[dtype])
+    check_attention(w, q, cache, table, lens)
+    check_attention(w, q, cache, table, lens, window=1000)
+    # the workspace of more new tokens serves fewer
+    ws = w.scaled_attention_workspace(cache, group, 16)
+    got = w.w4a16_scaled_attention(q.cuda(), cache, i32(table), i32(lens), workspace=ws, out=torch.empty_like(q, device="cuda"),
+                                   lse=torch.empty(q.shape[:3], device="cuda"))
+    check_attention(w, q, cache, table, lens, got=got)
+
+
 def test_attention_many_requests(w):
     rng = random.Random(4)
     lens = [rng.choice([0, 1, 5, rng.randrange(120)]) for _ in range(700)]
