@@ -490,6 +490,19 @@ def test_attention_24_and_32_columns_together(w, group, new, dim, dtype):
     check_attention(w, q, cache, table, lens, got=got)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("dim,hq,hk,requests", [(128, 16, 8, 5), (64, 20, 20, 3), (192, 7, 7, 4), (128, 6, 3, 9), (256, 9, 9, 200), (64, 4, 2, 130), (128, 8, 8, 320), (16, 17, 17, 2)])
+def test_attention_teams(w, dim, hq, hk, requests, dtype):
+    # a token's heads next to one another, wide tables: the warps of an SM take the same shares of a
+    # request's heads; warps are left over where the heads do not divide them
+    rng = random.Random(dim + hk)
+    some = [0, 1, 700, 33, 0, 1500, 64, 2100, 31, 32]
+    lens = [some[i] if i < 10 else rng.choice([0, 3, 17, 40, 90]) for i in range(requests)]
+    q, cache, table = attention_problem(w, dim + hq, lens, 1, hq, hk, dim, 16, 16, TYPES[dtype], columns=4096)
+    check_attention(w, q, cache, table, lens)
+    check_attention(w, q, cache, table, lens, window=32769)
+
+
 def test_attention_many_requests(w):
     rng = random.Random(4)
     lens = [rng.choice([0, 1, 5, rng.randrange(120)]) for _ in range(700)]

@@ -35,7 +35,8 @@ constexpr int rows_of_request(int q_heads, int kv_heads, int heads) {
 // A part is what a warp has of a row: o as the products' accumulators hold it
 // (float4 per lane and 16 dims), then m (log2 units) and l of each head.
 struct JoinPlan {
-    // {request or -1: nothing to join, row of the request, first warp, last warp}: one per
+    // {request or -1: nothing to join, row of the request (with a mark where every warp left a
+    // part, see kTeamRow), first warp, last warp}: one per
     // row (by_row: no more rows than warps), else one per warp, for the row that begins
     // in it and goes on in the next
     int4* joins;
@@ -45,6 +46,7 @@ struct JoinPlan {
     int by_row;
     int rows;   // of a request: key/value heads times chunks of the query heads sharing one
     int warps;  // of the first launch
+    int teams;  // by group: 0, or how many warps share each row of a request, the same shares for all of its rows
 };
 
 // paged_attention_bf16.cu, paged_attention_e4m3.cu: all launches of a call; `join` has joins and part

@@ -80,6 +80,8 @@ constexpr float kWeightBias = 8.f, kSlack = 7.f;
 constexpr int tile_tokens(int C, int DP) { return by_group(C) && DP <= 128 ? 32 : kTile; }
 
 constexpr int kMinCost = 3;     // a warp's share at least
+constexpr int kTeamTiles = 5;   // and where it takes the same tokens of its request's heads as its neighbours
+constexpr int kTeamRow = 1 << 30;  // a row (below 2^24) to join of which each warp has a part
 constexpr int kRowTiles = 8;    // rows kernel: tiles of a warp at most
 constexpr int kRowEnough = 2;   // and where one CTA is enough
 
@@ -1215,7 +1217,6 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint32_t tile_mask[W][S];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int worker = blockIdx.x * W + warp;
     const uint32_t ring = smem_addr(smem) + warp * S * Sh::kStageBytes;
     const int rows = jp.rows;
     bool bad = false;
@@ -1236,6 +1237,8 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
     // time (lane i: kPer in a row from kPer * i on).  They fit 32 bits.
     constexpr int kPer = 4, kScan = 32 * kPer;
     int cost[kPer];  // of this lane's requests
+    const bool may_team = by_group(C) && NT == 1 && jp.teams > 0;
+    int count = may_team ? 1 : rows;  // rows that are counted of a request
     // the costs of requests base .. base + kScan - 1; returns those before this lane's, `sum`: all
     auto scan = [&](int base, int& sum) -> int {
         int own = 0;
@@ -1243,7 +1246,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
         for (int i = 0; i < kPer; ++i) {
             const int b = base + lane * kPer + i;
             const int n = b < a.B ? request_of<C, Sh::kTokens>(a, b, bad).tiles : 0;
-            cost[i] = n ? (n + kRowCost) * rows : 0;
+            cost[i] = n ? (n + kRowCost) * count : 0;
             own += cost[i];
         }
         int inc = own;
@@ -1262,11 +1265,26 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
 #pragma unroll 8
         for (int b = lane; b < a.B; b += 32) {
             const int n = request_of<C, Sh::kTokens>(a, b, bad).tiles;
-            total += n ? (n + kRowCost) * rows : 0;
+            total += n ? (n + kRowCost) * count : 0;
         }
 #pragma unroll
         for (int d = 16; d; d /= 2) total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
     }
+    // teams: warps one after another have the same share of a request's rows, each of its own row,
+    // so that `worker` counts along one row's warps, where that gives every warp kTeamTiles tiles
+    // (16 requests of 1400 tokens, 3 tiles a warp: 24.5 us, without 23.0)
+    const int place = blockIdx.x * W + warp;
+    const bool teams = may_team && static_cast<int64_t>(total) * rows >= static_cast<int64_t>(kTeamTiles) * jp.warps;
+    if (may_team && !teams) {
+        count = rows;
+        total *= rows, head_start *= rows;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) cost[i] *= rows;
+    }
+    const bool spare = teams && place >= jp.teams * rows;
+    const int my_row = teams ? static_cast<unsigned>(place) % static_cast<unsigned>(rows) : 0;
+    const int worker = teams && !spare ? my_row * jp.teams + place / rows : place;
+    const int turn = teams ? (spare ? 0x7FFFFFFF : place / rows) : place;  // of the shares
     // requests without tokens
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         if (request_of<C, Sh::kTokens>(a, b, bad).tiles > 0) continue;
@@ -1286,18 +1304,18 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
         if (jp.by_row)
             for (int i = threadIdx.x; i < rows; i += W * 32) jp.joins[b * rows + i] = make_int4(-1, 0, 0, 0);
     }
-    int workers = min((total + kMinCost - 1) / kMinCost, jp.warps);
+    int workers = min((total + kMinCost - 1) / kMinCost, teams ? jp.teams : jp.warps);
     // one request: rows of one length, so a multiple of them splits none unevenly
-    if (a.B == 1 && workers > rows) workers -= workers % rows;
+    if (!teams && a.B == 1 && workers > rows) workers -= workers % rows;
     if (!jp.by_row && lane == 0) jp.joins[worker] = make_int4(-1, 0, 0, 0);
-    if (worker >= workers) {
+    if (turn >= workers) {
         if (bad) raise_device_error(a.err, W4A16_DEVERR_SLOT);
         return;
     }
-    // costs before worker i: equal shares, the remainder to the first ones
+    // costs before the i-th share: equal ones, the remainder to the first
     const unsigned share = static_cast<unsigned>(total) / static_cast<unsigned>(workers), extra = total - share * workers;
-    const int u0 = worker * share + min(static_cast<unsigned>(worker), extra);
-    const int u1 = u0 + share + (worker < static_cast<int>(extra) ? 1 : 0);
+    const int u0 = turn * share + min(static_cast<unsigned>(turn), extra);
+    const int u1 = u0 + share + (turn < static_cast<int>(extra) ? 1 : 0);
     auto worker_of = [&](int u) -> int {
         const int big = extra * (share + 1);
         return u < big ? static_cast<unsigned>(u) / (share + 1) : extra + static_cast<unsigned>(u - big) / share;
@@ -1338,8 +1356,8 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
     auto next_segment = [&](Segment& s) -> bool {
         s.at += s.q.tiles + kRowCost;
         if (s.at + kRowCost >= u1) return false;
-        if (++s.row == rows) {
-            s.row = 0;
+        if (teams || ++s.row == rows) {
+            s.row = my_row;
             do {
                 if (++s.b >= a.B) return false;
                 s.q = request_of<C, Sh::kTokens>(a, s.b, bad);
@@ -1352,8 +1370,12 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
     bool live = u1 > u0 && locate(u0, seg.b, seg.at);
     if (live) {
         seg.q = request_of<C, Sh::kTokens>(a, seg.b, bad);
-        seg.row = static_cast<unsigned>(u0 - seg.at) / static_cast<unsigned>(seg.q.tiles + kRowCost);
-        seg.at += seg.row * (seg.q.tiles + kRowCost);
+        if (teams) {
+            seg.row = my_row;
+        } else {
+            seg.row = static_cast<unsigned>(u0 - seg.at) / static_cast<unsigned>(seg.q.tiles + kRowCost);
+            seg.at += seg.row * (seg.q.tiles + kRowCost);
+        }
         open_segment(seg);
         live = seg.t1 > seg.t0;
     }
@@ -1364,7 +1386,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
     bool inside = false;
     uint8_t* const rings = smem + (by_group(C) ? (0u - smem_addr(smem)) & 1023u : 0u);
     if constexpr (by_group(C))
-        inside = live && inside_of_row<W>(blockIdx.x, worker_of(seg.at + kRowCost), worker_of(seg.at + kRowCost + seg.q.tiles - 1));
+        inside = live && !teams && inside_of_row<W>(blockIdx.x, worker_of(seg.at + kRowCost), worker_of(seg.at + kRowCost + seg.q.tiles - 1));
 
     // The copies run ahead of the products: `ahead` is the segment of the next
     // tile to copy, ahead_t the tile.
@@ -1388,9 +1410,10 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
         hd = heads_of<C, HEADS>(a, seg.row);
         math.begin(a, seg.b, hd, lane);
         // and those of the row after this one brought to L2
-        const int after_b = seg.row + 1 < rows ? seg.b : seg.b + 1;
+        const bool same = !teams && seg.row + 1 < rows;
+        const int after_b = same ? seg.b : seg.b + 1;
         if (after_b < a.B) {
-            const Heads h = heads_of<C, HEADS>(a, seg.row + 1 < rows ? seg.row + 1 : 0);
+            const Heads h = heads_of<C, HEADS>(a, same ? seg.row + 1 : my_row);
             constexpr int kLines = (DP + 63) / 64;
             for (int i = lane; i < h.n * kLines; i += 32)
                 if ((i % kLines) * 64 < a.cache.dim) prefetch_l2(query_of<C>(a, after_b, h, i / kLines) + (i % kLines) * 64);
@@ -1435,7 +1458,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
         // a row that begins here: what the join launch has to do for it
         if (begins && lane == 0 && (jp.by_row || !ends))
             jp.joins[jp.by_row ? seg.b * rows + seg.row : worker] =
-                ends ? make_int4(-1, 0, 0, 0) : make_int4(seg.b, seg.row, worker, worker_of(seg.at + kRowCost + seg.q.tiles - 1));
+                ends ? make_int4(-1, 0, 0, 0) : make_int4(seg.b, seg.row | (teams ? kTeamRow : 0), worker, worker - turn + worker_of(seg.at + kRowCost + seg.q.tiles - 1));
         live = next_segment(seg);
         t = seg.t0;
         fresh = true;
@@ -1522,12 +1545,14 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t at) {
 // (x: accumulators, y: group, of which each takes every n-th part, so that
 // many parts are on their way at once).
 constexpr int kJoinThreads = 512;  // at most
-constexpr int kJoinDepth = 3;  // parts a thread requests together
+// parts a thread requests together (by group four: 24 requests, 20 heads of 64 dims 27.6 us with
+// three or eight, 26.6)
+constexpr int join_depth(int C, int NT) { return by_group(C) && NT == 1 ? 4 : 3; }
 
 template <int C, int DP, int NT>
 __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Args<C> a, const JoinPlan jp) {
     using Sh = AttnShape<C, DP, NT>;
-    constexpr int HEADS = Sh::kHeads, KS = Sh::kSteps;
+    constexpr int HEADS = Sh::kHeads, KS = Sh::kSteps, kJoinDepth = join_depth(C, NT);
     __shared__ DimPart sums[kJoinThreads / 2];
     grid_dependents_launch();
     grid_dependency_wait();
@@ -1542,7 +1567,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Args<C> a
     if constexpr (by_group(C)) {
         constexpr int W = Sh::kShareWarps;
         const int from = d.z / W + 1;
-        inner = max(d.w / W - from, 0);
+        inner = d.y & kTeamRow ? 0 : max(d.w / W - from, 0);
         if (inner) {
             lead = from * W - d.z;
             parts -= inner * (W - 1);
@@ -1581,7 +1606,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Args<C> a
         __syncthreads();
     }
     if (threadIdx.y > 0) return;
-    s.finish<C>(a, d.x, heads_of<C, HEADS>(a, d.y), n, k, lane);
+    s.finish<C>(a, d.x, heads_of<C, HEADS>(a, d.y & (kTeamRow - 1)), n, k, lane);
 }
 
 // kRowWarps / wpr rows per CTA, wpr warps for each; or (cluster > 1, wpr =
@@ -1823,6 +1848,21 @@ cudaError_t launch_attention_shape(const Args<C>& all, const DeviceInfo& dev, Jo
     }
     const int ctas = std::min(dev.sms, most_workers(DP) / Sh::kShareWarps);
     jp.warps = ctas * Sh::kShareWarps;
+    // Where a token's heads lie next to one another, the warps of an SM take the same tokens of all
+    // of them at the same time.  One head after another would find the DRAM's pages closed again, at
+    // a cost that differs between GPUs (64 requests of 8192 tokens of int8: 212 or 179 us, so 175 on
+    // either; 24 of 12000 with 20 heads of 64 dims 215 or 190, so 155; where a block keeps each
+    // head's tokens together 175 both ways).  Not where a row has so many warps that a CTA can join
+    // theirs (one request of 131072 tokens: 60 or 54 us, so 58 or 57; of 32768 22, so 23), products
+    // bound it (16 columns 72, 74), there is little for each warp, or many had nothing to do;
+    // the kernel looks at what the lengths give.
+    if constexpr (by_group(C) && NT == 1) {
+        const int teams = jp.warps / jp.rows;
+        const bool next_to = a.cache.k_head < a.cache.k_token && a.cache.v_head < a.cache.v_token;
+        if (next_to && jp.rows > 1 && (jp.warps - teams * jp.rows) * 16 <= jp.warps && jp.warps < 128 * all_rows &&
+            all_rows * (tiles + kRowCost) >= kTeamTiles * static_cast<int64_t>(jp.warps))
+            jp.teams = teams;
+    }
     // as many requests at a time as have costs of 32 bits (one has: attention_costs_fit)
     const int64_t fit = kMostCost / (static_cast<int64_t>(tiles + kRowCost) * jp.rows);
     for (int from = 0; from < all.B; from += a.B) {
@@ -1844,9 +1884,9 @@ cudaError_t launch_attention_shape(const Args<C>& all, const DeviceInfo& dev, Jo
         int width = 128;
         while (units % width || (width > 32 && places * (units / width) < dev.sms)) width /= 2;
         int parts = jp.warps / places + 2;
-        if (by_group(C)) parts = std::min(parts, 2 * Sh::kShareWarps + ctas / places);  // (a part a CTA inside of a row)
+        if (by_group(C) && !jp.teams) parts = std::min(parts, 2 * Sh::kShareWarps + ctas / places);  // (a part a CTA inside of a row)
         int groups = 1;
-        while (groups * width < kJoinThreads && groups * kJoinDepth < parts) groups *= 2;
+        while (groups * width < kJoinThreads && groups * join_depth(C, NT) < parts) groups *= 2;
         e = launch_kernel(k_attention_join<C, DP, NT>, true, 1, dim3(places, units / width), dim3(width, groups), 0, s, a, jp);
         if (e != cudaSuccess) return e;
     }
