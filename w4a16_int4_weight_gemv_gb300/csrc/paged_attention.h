@@ -35,10 +35,9 @@ constexpr int rows_of_request(int q_heads, int kv_heads, int heads) {
 // A part is what a warp has of a row: o as the products' accumulators hold it
 // (float4 per lane and 16 dims), then m (log2 units) and l of each head.
 struct JoinPlan {
-    // {request or -1: nothing to join, row of the request (with a mark where every warp left a
-    // part, see kTeamRow), first warp, last warp}: one per
-    // row (by_row: no more rows than warps), else one per warp, for the row that begins
-    // in it and goes on in the next
+    // {request or -1: nothing to join, row of the request (marked by kTeamRow where every warp
+    // left a part), first warp, last warp}: one per row (by_row: no more rows than warps), else
+    // one per warp, for the row that begins in it and goes on in the next
     int4* joins;
     // [warp][2][heads * (padded + 2)]; place 0: the row that the warp's share begins inside
     // of, 1: the row it ends inside of

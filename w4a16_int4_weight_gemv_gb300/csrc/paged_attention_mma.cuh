@@ -1,5 +1,7 @@
-// Attention of one new token per request over a paged key/value cache
-// (w4a16_paged_attention): the kernels, for one cache type per translation unit.
+// Attention over a paged key/value cache, of one new token per request over bf16 or
+// e4m3 with a scale a head (w4a16_paged_attention), of one to sixteen over 8 bits with a
+// scale for each group of tokens and head (w4a16_scaled_attention): the kernels, for one
+// cache type per translation unit.
 //
 // A row is one request, one key/value head and up to 8 * NT of the query
 // heads that share it.  For the tokens j a row sees,
@@ -36,6 +38,32 @@
 // Registers: all instances but those of 16 heads of 256 dims (24 bytes spilled
 // by the shares over bf16, 104 over e4m3) and 16 of 192 over e4m3 (32) hold what
 // they need.
+//
+// Scales by group.  A row's columns are (new token, query head) pairs.  With codes c and
+// scales a (keys) and b (values),
+//     s_j = c a_j q . k_j,  m = max s_j,  l = sum 2^(s_j - m),
+//     w_j = s_j + log2 b_j,  M = max w_j,  o = sum 2^(w_j - M) v_j,  out = o 2^(M - m) / l:
+// the value's scale goes into the weight, which is what the second product needs in fp16
+// anyway, and o by a maximum of its own, since scales of neighbouring groups may be any
+// powers of two apart.  m and M move only when a score passes them by 2^kSlack.
+//   - A tile (32 tokens up to 128 dims) is boxes of 8, 16 or 32 tokens of a block and head,
+//     each a tensor copy to the warp's ring, which its mbarrier counts: with cp.async the
+//     copies were a third of all instructions.  A box's scale comes with its block id, those
+//     of groups of 1, 2 or 4 tokens as small copies of their own; what fits neither comes by
+//     cp.async.
+//   - A CTA whose warps all lie inside of one row joins their parts itself (131072 tokens of
+//     one request, heads apart: 58 us without, 53 with).
+//   - Up to 32 columns take one row: the codes' conversion and the copies, of which there are
+//     as many for one column as for 32, are what a tile costs.
+// Bound, on a GB300 whose copies run at 6.77 TB/s (32 heads over 8 of 128 dims, int8): with
+// one new token by HBM while there is enough to read (64 requests of 8192 tokens 175 us, 6.1
+// TB/s; 128 of 0 to 8192 127 us, 5.7 TB/s; of 32 of 8192, 97 us, DRAM is 70 % busy over the
+// whole launch, issue 56 %, the ALU pipe 55 %, the tensor pipe 15 %); from 16 columns on by the issue of what a column adds, softmax and products
+// (16 requests of 8192, 268 MB: 58 us with 4 columns, 70 with 16, 91 with 20, 121 with 32);
+// below 50 MB by two launches and their dependent reads (16 requests of 1400 tokens 23 us, 7.5
+// us of it at the rate of HBM), or by one (300 tokens 6.7 us in a graph).
+// Registers: spills are 346 to 378 bytes in 16 columns of 256 dims, 76 to 98 in 32 of 128,
+// 8 in 16 of 64 over int8; no others.
 #pragma once
 
 #include <algorithm>
@@ -1894,8 +1922,8 @@ cudaError_t launch_attention_shape(const Args<C>& all, const DeviceInfo& dev, Jo
 }
 
 // Scales by group: more than 16 columns, which share what it takes to bring a tile and make
-// it operands, as 24 or 32 together (16 requests of 16384 tokens at
-// most, five new tokens of 4 heads as 16 and 4: 96 us, as 24: 77).
+// it operands, as 24 or 32 together (16 requests of 16384 tokens at most, five new tokens of 4
+// heads: as 16 and 4 96 us, as 24 77).
 template <int C>
 cudaError_t launch_attention_wide(const Args<C>& a, const DeviceInfo& dev, const JoinPlan& jp, cudaStream_t s) {
     const bool three = columns_together(a.q_heads / a.cache.heads * a.tokens, a.cache.dim) == 24;

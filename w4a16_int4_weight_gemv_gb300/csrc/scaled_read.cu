@@ -9,6 +9,10 @@
 // time, all their codes and scales requested before the first is used.  (CTAs that go on
 // to further chunks, whose places they look up meanwhile, took 175 us for the case below:
 // four CTAs an SM that come and go overlap as well, and need fewer registers.)
+//
+// Measured on one GB300 (copies run at 6.77 TB/s), 8 heads of 128 dims to bf16: 64 requests
+// of 0 to 8192 tokens 167.5 us, 1.10 GB at 6.56 TB/s (0.97 of the copy rate); 300 tokens 3.7
+// us (2.6 in a graph): launch, row, block id, codes, one after another.
 #include <algorithm>
 
 #include "common.cuh"
