@@ -58,8 +58,8 @@
 // Bound, on a GB300 whose copies run at 6.77 TB/s (32 heads over 8 of 128 dims, int8): with
 // one new token by HBM while there is enough to read (64 requests of 8192 tokens 175 us, 6.1
 // TB/s; 128 of 0 to 8192 127 us, 5.7 TB/s; of 32 of 8192, 97 us, DRAM is 70 % busy over the
-// whole launch, issue 56 %, the ALU pipe 55 %, the tensor pipe 15 %); from 16 columns on by the issue of what a column adds, softmax and products
-// (16 requests of 8192, 268 MB: 58 us with 4 columns, 70 with 16, 91 with 20, 121 with 32);
+// whole launch, issue 56 %, the ALU pipe 55 %, the tensor pipe 15 %); from 16 columns on by what eight warps an SM, all that registers hold, do one after
+// another (issue 40 to 45 %, tensor pipe 21 to 28 %; 16 requests of 8192, 268 MB: 58 us with 4 columns, 70 with 16, 91 with 20, 121 with 32);
 // below 50 MB by two launches and their dependent reads (16 requests of 1400 tokens 23 us, 7.5
 // us of it at the rate of HBM), or by one (300 tokens 6.7 us in a graph).
 // Registers: spills are 346 to 378 bytes in 16 columns of 256 dims, 76 to 98 in 32 of 128,
