@@ -721,8 +721,8 @@ W4A16_API size_t w4a16_scaled_attention_workspace_bytes(int q_heads, int kv_head
  * A key or value that is NaN reaches the new tokens that see it and no others.
  * The other arguments, the workspace and the limits are those of w4a16_paged_attention,
  * with N * q_heads in the place of q_heads.  Where a request sees a token, codes and scales of
- * up to 31 tokens around it in the same block and head may be read too; what they hold
- * changes nothing.
+ * up to 31 tokens around it in the same block and head may be read too, and scales of blocks
+ * that its table names past its length; what they hold changes nothing.
  */
 W4A16_API w4a16_status w4a16_scaled_attention(
     const uint16_t* q, int64_t q_request, int64_t q_token, int64_t q_head,

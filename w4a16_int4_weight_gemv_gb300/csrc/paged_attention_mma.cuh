@@ -55,15 +55,17 @@
 //     one request, heads apart: 58 us without, 53 with).
 //   - Up to 32 columns take one row: the codes' conversion and the copies, of which there are
 //     as many for one column as for 32, are what a tile costs.
-// Bound, on a GB300 whose copies run at 6.77 TB/s (32 heads over 8 of 128 dims, int8): with
-// one new token by HBM while there is enough to read (64 requests of 8192 tokens 175 us, 6.1
-// TB/s; 128 of 0 to 8192 127 us, 5.7 TB/s; of 32 of 8192, 97 us, DRAM is 70 % busy over the
-// whole launch, issue 56 %, the ALU pipe 55 %, the tensor pipe 15 %); from 16 columns on by what eight warps an SM, all that registers hold, do one after
-// another (issue 40 to 45 %, tensor pipe 21 to 28 %; 16 requests of 8192, 268 MB: 58 us with 4 columns, 70 with 16, 91 with 20, 121 with 32);
-// below 50 MB by two launches and their dependent reads (16 requests of 1400 tokens 23 us, 7.5
-// us of it at the rate of HBM), or by one (300 tokens 6.7 us in a graph).
-// Registers: spills are 346 to 378 bytes in 16 columns of 256 dims, 76 to 98 in 32 of 128,
-// 8 in 16 of 64 over int8; no others.
+// Bound, on a GB300 whose copies run at 6.77 TB/s (32 heads over 8 of 128 dims, int8):
+//   - with one new token by HBM while there is enough to read: 64 requests of 8192 tokens 175
+//     us, 6.1 TB/s; 128 of 0 to 8192 127 us, 5.7 TB/s; 32 of 8192 97 us, over the whole of which
+//     DRAM is 70 % busy, issue 56 %, the ALU pipe 55 %, the tensor pipe 15 %;
+//   - from 16 columns on by what eight warps an SM, all that registers hold, do one after another
+//     (issue 40 to 45 %, tensor pipe 21 to 28 %): 16 requests of 8192 tokens, 268 MB, 58 us with
+//     4 columns, 70 with 16, 91 with 20, 121 with 32;
+//   - below 50 MB by two launches and their dependent reads (16 requests of 1400 tokens 23 us,
+//     7.5 of it at the rate of HBM), or by one (300 tokens 6.7 us in a graph).
+// Registers: the shares spill 346 to 378 bytes in 16 columns of 256 dims, 76 to 98 in 32 of
+// 128, 8 in 16 of 64 over int8, single launches 122 to 130 and 4 in the first two; no others.
 #pragma once
 
 #include <algorithm>
@@ -1501,6 +1503,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
             if (counts_groups<C>(a)) cp_async_wait_group<S - 1>();
             groups.wait(slot, parity);
             if (groups.gave_up(slot, parity, S)) more = false;
+            __syncwarp();  // (what the lanes themselves put into the stage)
             if (t == seg.t0) math.ready(a, seg.b, hd, seg.q.len, lane);
             math.tile(a, seg.q, groups.codes + slot * Sh::kStageBytes, groups.info + slot * Sh::kInfo, (seg.q.tile0 + t) * Sh::kTokens, lane);
             __syncwarp();
@@ -1719,6 +1722,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kRowWarps * 32), 1)
                 if (counts_groups<C>(a)) cp_async_wait_group<S - 1>();
                 groups.wait(slot, parity);
                 if (groups.gave_up(slot, parity, S)) ahead = q.tiles;
+                __syncwarp();  // (what the lanes themselves put into the stage)
                 if (t == first_tile) math.ready(a, b, hd, q.len, lane);
                 math.tile(a, q, groups.codes + slot * Sh::kStageBytes, groups.info + slot * Sh::kInfo, (q.tile0 + t) * Sh::kTokens, lane);
                 __syncwarp();
