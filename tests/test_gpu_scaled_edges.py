@@ -1,0 +1,67 @@
+"""Calls over an 8-bit paged cache with scales by group whose inputs lie at the edge of
+what the interface allows."""
+import pytest
+import torch
+
+from .test_gpu_paged import i32, w  # noqa: F401  (w: the fixture)
+from .test_gpu_scaled import E4M3, U, attention_problem, raw
+
+pytestmark = pytest.mark.gpu
+
+
+# --------------------------------------------------------------------------
+# attention: value codes that are no number
+# --------------------------------------------------------------------------
+def with_code(w, q, cache, table, lens, window, where, code):
+    """Attention with one value code (token `where` of request 0, head 0, dim 7) set to `code`, and that code put back."""
+    at = raw(cache.v)[table[0][where // cache.page], where % cache.page, 0, 7:8]
+    before = at.clone()
+    at.fill_(code)
+    got = w.w4a16_scaled_attention(q.cuda(), cache, i32(table), i32(lens), window=window)
+    at.copy_(before)
+    return got
+
+
+# (dim, page, group): a scale a box, a scale or two tokens, one by one beside tensor copies, no boxes; rows of 64, 128 and 256 bytes
+@pytest.mark.parametrize("columns", [None, 4096], ids=["one launch", "shares"])
+@pytest.mark.parametrize("dim,page,group", [(64, 16, 16), (128, 32, 32), (96, 16, 1), (128, 32, 2), (64, 24, 12), (80, 7, 7), (256, 16, 16), (192, 64, 4)])
+def test_a_nan_value_reaches_the_one_new_token_that_sees_it(w, dim, page, group, columns):
+    # 150 tokens: the last step partly filled from 128 or 144 on; window 45 begins at 105, inside a step
+    lens = [150, 20]
+    q, cache, table = attention_problem(w, dim + page, lens, 1, 4, 2, dim, page, group, E4M3, columns=columns)
+    for window, seen, unseen in ((0, (0, 10, 127, 128, 144, 149), ()), (45, (105, 111, 130, 149), (104, 96, 3))):
+        for where in seen + unseen:
+            want = with_code(w, q, cache, table, lens, window, where, 0x00)
+            for code in (0x7F, 0xFF):
+                out, lse = with_code(w, q, cache, table, lens, window, where, code)
+                nan = torch.zeros_like(out, dtype=torch.bool)
+                nan[0, 0, :2, 7] = where in seen
+                assert torch.equal(out.isnan(), nan), (where, window)
+                # the rest is what it is with a code of 0, bit for bit
+                assert torch.equal(out.masked_fill(nan, 0.0), want[0].masked_fill(nan, 0.0)) and torch.equal(lse, want[1])
+    assert w.w4a16_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("columns", [None, 4096], ids=["one launch", "shares"])
+@pytest.mark.parametrize("dim,page,group", [(64, 16, 16), (128, 32, 2), (80, 7, 7), (256, 16, 16)])
+@pytest.mark.parametrize("new,hq", [(4, 4), (8, 8), (7, 8)])
+def test_a_nan_value_reaches_all_new_tokens_that_see_it(w, new, hq, dim, page, group, columns):
+    # new token i of N sees 150 - (N - 1 - i) tokens
+    lens = [150, 20]
+    q, cache, table = attention_problem(w, dim + page, lens, new, hq, 2, dim, page, group, E4M3, columns=columns)
+    most = 448 * float(cache.v_scale.nan_to_num(0.0).abs().max())
+    for window in (0, 45):
+        for where in (10, 128, 150 - new, 149, 105, 102, 96):
+            want = with_code(w, q, cache, table, lens, window, where, 0x00)[0]
+            out = with_code(w, q, cache, table, lens, window, where, 0x7F)[0]
+            ends = [150 - (new - 1 - i) for i in range(new)]
+            hit = torch.tensor([where < end and (not window or where >= end - window) for end in ends]).cuda()
+            half = hq // 2  # query heads of head 0
+            assert out[0, hit, :half, 7].isnan().all()
+            assert not out[1].isnan().any() and not out[0, ~hit].isnan().any() and not out[0, :, half:].isnan().any()
+            if where < 150 - new and (not window or where >= 150 - window):  # all of them see it: nothing but its dim
+                assert int(out.isnan().sum()) == new * half
+            # whoever does not see it: twice the error of one call, 2^-8 of the result and 2^-10 of a value at most
+            for a, b in ((out[1], want[1]), (out[0, ~hit], want[0, ~hit]), (out[0, :, half:], want[0, :, half:])):
+                assert ((a - b).abs().double() <= 2 * (U * b.abs().double() + 2.0 ** -10 * most)).all()
+    assert w.w4a16_device_error(clear=True) == 0

@@ -169,12 +169,6 @@ template <int C>
 __device__ __forceinline__ void codes_to_f16_by_dim(uint32_t w, uint32_t& even, uint32_t& odd) {
     codes_to_f16<C>(C == kInt8Groups ? w : __byte_perm(w, 0u, 0x3120), even, odd);
 }
-// both halves, a NaN among them as a number
-__device__ __forceinline__ uint32_t as_numbers(uint32_t v) {
-    const __half2 low = __halves2half2(__ushort_as_half(0xDF00), __ushort_as_half(0xDF00));  // -448
-    const __half2 h = __hmax2(*reinterpret_cast<const __half2*>(&v), low);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ void cp_async_4_zfill(uint32_t dst, const void* src, bool valid) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0)
                  : "memory");
@@ -188,6 +182,9 @@ __device__ __forceinline__ uint4 ld_shared_u4(uint32_t at) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
     return v;
+}
+__device__ __forceinline__ void st_shared_u4(uint32_t at, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 // log2 of a scale's magnitude
 __device__ __forceinline__ float log2_fast(float x) {
@@ -752,22 +749,37 @@ struct RowMath {
         } else {
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                if (C == kE4m3Groups && edge && a.tokens > 1) {
-                    // A NaN that some new tokens see stays with them: its weight becomes NaN there, and
-                    // the code a number.
+                if (C == kE4m3Groups) {
+                    // A weight of 0 does not stop a NaN: codes that no new token sees, which may be
+                    // anything, become 0 where they are.  So do NaN codes that some see and others do
+                    // not; the token's weight becomes NaN instead, for those that do.
+                    const int row = lane & 15, token = first + 16 * p + row;
+                    const bool none = !((mask[p] >> row) & 1u);
+                    const bool some = !none && edge && a.tokens > 1 && (token >= q.len - (a.tokens - 1) || (a.window > 0 && token < q.len - a.window));
                     bool nan = false;
+                    if (none || some) {
+#pragma unroll 1
+                        for (int k = 0; k < KS; k += 2) {  // (the chunks that the products take: of 96 dims not all)
+                            const uint32_t chunk = (at[p] ^ ((k & 7) * 16)) + (k >> 3) * (kTile * 128) + kValues;
+                            const uint4 v = none ? make_uint4(0u, 0u, 0u, 0u) : ld_shared_u4(chunk);
+                            uint32_t x[4] = {v.x, v.y, v.z, v.w}, found = 0u;
 #pragma unroll
-                    for (int k = 0; k < KS; k += 2) {  // (the chunks that the products take: of 96 dims not all)
-                        const uint4 v = ld_shared_u4((at[p] ^ ((k & 7) * 16)) + (k >> 3) * (kTile * 128) + kValues);
-                        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) nan |= (((x[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u;
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t top = ((x[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // of bytes 0x7F, 0xFF
+                                found |= top;
+                                x[j] &= ~((top >> 7) * 0xFFu);
+                            }
+                            nan |= found != 0u;
+                            if (none || found) st_shared_u4(chunk, make_uint4(x[0], x[1], x[2], x[3]));
+                        }
                     }
+                    fence_proxy_async_smem();  // before the next tensor copy into this stage
                     uint32_t who = __ballot_sync(0xFFFFFFFFu, nan);
                     who |= who >> 16;
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                         if ((who >> (r + 8 * i)) & 1u) lv[p][i] = NAN;
+                    __syncwarp();
                 }
             }
 #pragma unroll
@@ -789,9 +801,6 @@ struct RowMath {
                 to_f16(n);
             }
         }
-        // an e4m3 NaN would reach every column, those of weight 0 too; and in places that nobody
-        // sees codes may be anything
-        const bool scrub = C == kE4m3Groups && hidden;
 #pragma unroll
         for (int p = 0; p < P; ++p)
 #pragma unroll
@@ -804,7 +813,6 @@ struct RowMath {
                     uint32_t a0, a1, a2, a3;
                     codes_to_f16_by_dim<C>(f[2 * j], a0, a1);
                     codes_to_f16_by_dim<C>(f[2 * j + 1], a2, a3);
-                    if (scrub) a0 = as_numbers(a0), a1 = as_numbers(a1), a2 = as_numbers(a2), a3 = as_numbers(a3);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         float d[4] = {o[n][k + j].x, o[n][k + j].y, o[n][k + j].z, o[n][k + j].w};
