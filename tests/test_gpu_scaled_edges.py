@@ -3,8 +3,8 @@ what the interface allows."""
 import pytest
 import torch
 
-from .test_gpu_paged import i32, w  # noqa: F401  (w: the fixture)
-from .test_gpu_scaled import E4M3, U, attention_problem, raw
+from .test_gpu_paged import freqs, i32, w  # noqa: F401  (w: the fixture)
+from .test_gpu_scaled import E4M3, TYPES, U, attention_problem, check_append, make_cache, raw
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +65,20 @@ def test_a_nan_value_reaches_all_new_tokens_that_see_it(w, new, hq, dim, page, g
             for a, b in ((out[1], want[1]), (out[0, ~hit], want[0, ~hit]), (out[0, :, half:], want[0, :, half:])):
                 assert ((a - b).abs().double() <= 2 * (U * b.abs().double() + 2.0 ** -10 * most)).all()
     assert w.w4a16_device_error(clear=True) == 0
+
+
+# --------------------------------------------------------------------------
+# append: pairs longer than the largest float
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("inter", [False, True], ids=["halves", "neighbours"])
+@pytest.mark.parametrize("rotary", [32, 64])
+def test_keys_longer_than_a_float_holds_are_turned(w, rotary, inter, dtype):
+    gen = torch.Generator().manual_seed(rotary)
+    T, hk, dim = 40, 2, 64
+    x = torch.randn(T, 2 * hk, dim, generator=gen).sign() * 3.3e38
+    x[5:9] *= torch.rand(4, 2 * hk, dim, generator=gen)
+    x[20] = 1.0  # beside values of ordinary size, in one group and alone
+    x[24:28] = torch.randn(4, 2 * hk, dim, generator=gen)
+    cache = make_cache(w, gen, 4, 16, 4, hk, dim, TYPES[dtype])
+    check_append(w, cache, x.bfloat16().view(T, -1), 0, torch.arange(T).int() * 997, freqs(rotary), None, inter, list(range(16, 16 + T)))

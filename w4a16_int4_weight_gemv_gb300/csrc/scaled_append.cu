@@ -179,13 +179,15 @@ __device__ __forceinline__ bool longer(const uint4& v0, const uint4& v1, const P
     return top > most2;
 }
 
-template <bool INT8>
-__device__ __forceinline__ uint2 codes_of(float (&x)[8], float inv) {
+__device__ __forceinline__ void scale8(float (&x)[8], float f) {
 #pragma unroll
     for (int i = 0; i < 8; i += 2)
         asm("{.reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;}"
             : "+f"(x[i]), "+f"(x[i + 1])
-            : "f"(inv));
+            : "f"(f));
+}
+template <bool INT8>
+__device__ __forceinline__ uint2 codes_of(const float (&x)[8]) {
     return make_uint2(f32_to_codes<INT8>(x[0], x[1], x[2], x[3]), f32_to_codes<INT8>(x[4], x[5], x[6], x[7]));
 }
 
@@ -419,9 +421,10 @@ __global__ void __launch_bounds__(kThreads, PER_SM) k_scaled_append(const Scaled
             float p[8], q[8];
             unpack8(x0, p);
             unpack8(x1, q);
+            scale8(p, inv), scale8(q, inv);  // first: a pair of large values turns past what a float holds
             if (turns) turn(p, q, at, cs, a.rotary);
-            *reinterpret_cast<uint2*>(dst + at.d0) = codes_of<INT8>(p, inv);
-            *reinterpret_cast<uint2*>(dst + at.d1) = codes_of<INT8>(q, inv);
+            *reinterpret_cast<uint2*>(dst + at.d0) = codes_of<INT8>(p);
+            *reinterpret_cast<uint2*>(dst + at.d1) = codes_of<INT8>(q);
             dst += dst_step, cs += tps * 4 * turned;
         };
 #pragma unroll
