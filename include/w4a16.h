@@ -664,9 +664,10 @@ typedef struct w4a16_scaled_cache {
  *   A value that is not finite makes S NaN, and the group stands for NaN until it is
  *   begun anew.  Places behind the new tokens keep their codes.
  * slots[t] == -1: not stored; a slot outside the cache, or one in the group of the
- * token before that does not follow that token's: not stored and W4A16_DEVERR_SLOT.
- * The same group twice in a call with other tokens between: its contents are
- * undefined.
+ * token before that does not follow that token's (the same slot again, an earlier or a
+ * later one): not stored, nor are the tokens that go on from it within that group, and
+ * W4A16_DEVERR_SLOT.  The same group twice in a call with other tokens between: its
+ * contents are undefined.
  */
 W4A16_API w4a16_status w4a16_scaled_append(const uint16_t* q, int64_t q_token, int64_t q_head,
                                            uint16_t* q_out, int64_t q_out_token,

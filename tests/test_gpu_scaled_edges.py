@@ -3,8 +3,9 @@ what the interface allows."""
 import pytest
 import torch
 
-from .test_gpu_paged import freqs, i32, w  # noqa: F401  (w: the fixture)
-from .test_gpu_scaled import E4M3, TYPES, U, attention_problem, check_append, make_cache, raw
+from .scaled_slots import stored
+from .test_gpu_paged import freqs, i32, split_qkv, w  # noqa: F401  (w: the fixture)
+from .test_gpu_scaled import E4M3, TYPES, U, attention_problem, check_append, make_cache, raw, same_bits, state_of
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +83,44 @@ def test_keys_longer_than_a_float_holds_are_turned(w, rotary, inter, dtype):
     x[24:28] = torch.randn(4, 2 * hk, dim, generator=gen)
     cache = make_cache(w, gen, 4, 16, 4, hk, dim, TYPES[dtype])
     check_append(w, cache, x.bfloat16().view(T, -1), 0, torch.arange(T).int() * 997, freqs(rotary), None, inter, list(range(16, 16 + T)))
+
+
+# --------------------------------------------------------------------------
+# append: slots that do not follow one another
+# --------------------------------------------------------------------------
+def check_slots(w, page, group, hk, dim, slots, blocks, seed, dtype):
+    """What the tokens that are stored give, and nothing of the others: the same cache, bit for bit, as
+    with -1 in their places, which is compared with the plain form."""
+    kept, bad = stored(slots, group, blocks * page)
+    T = len(slots)
+    qkv = torch.randn(T, 2 * hk * dim, generator=torch.Generator().manual_seed(seed)).bfloat16()
+    pos, f = torch.arange(T).int(), freqs(dim)
+    clean, cache = (make_cache(w, torch.Generator().manual_seed(seed), blocks, page, group, hk, dim, dtype) for _ in range(2))
+    assert same_bits(state_of(clean), state_of(cache))
+    check_append(w, clean, qkv, 0, pos, f, None, False, kept)
+    _, k, v = split_qkv(qkv.cuda(), 0, hk, dim)
+    for _ in range(3):
+        again = make_cache(w, torch.Generator().manual_seed(seed), blocks, page, group, hk, dim, dtype)
+        w.w4a16_scaled_append(None, k, v, pos.cuda(), f.cuda(), i32(slots), again)
+        assert w.w4a16_device_error(clear=True) == (w.DEVERR_SLOT if bad else 0)
+        assert same_bits(state_of(clean), state_of(again))
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("group,slots", [(4, [17, 16]), (4, [16, 16]), (4, [19, 16, 17, 18, 19, 20, 21]), (4, [16, 17, 16, 17, 18]), (4, [18, 17, 16]),
+                                         (4, [16, 18, 19, 20]), (16, [31, 16]), (16, [16, 16, 17]), (1, [16, 16]), (1, [17, 17, 18, 18, 18, 17 + 16]),
+                                         (8, [24, 16, 24 + 8, 24 + 8]), (2, [3, 2, 1, 0])], ids=str)
+def test_a_slot_in_the_group_of_the_token_before_has_to_follow_it(w, group, slots, dtype):
+    check_slots(w, 16, group, 3, 64, slots, 4, 5, TYPES[dtype])
+
+
+@pytest.mark.parametrize("T", [40, 700, 6000])
+@pytest.mark.parametrize("group", [1, 4, 16])
+def test_slots_out_of_order_in_calls_of_many_tokens(w, group, T):
+    # such pairs between the tokens of neighbouring groups, in blocks of their own: inside of what a CTA
+    # takes (a power of two of tokens, 32 at most) and across two CTAs
+    slots, spare = list(range(16, 16 + T)), (T // 16 + 4) * 16
+    for t in range(15, T - 1, 16):
+        slots[t], slots[t + 1] = spare + group - 1, spare  # a group's last place, then its first (group 1: the same again)
+        spare += 16
+    check_slots(w, 16, group, 2, 32, slots, spare // 16, T + group, TYPES["int8"])

@@ -310,8 +310,9 @@ __global__ void __launch_bounds__(kThreads, PER_SM) k_scaled_append(const Scaled
             const bool valid = s >= 0 && s < a.cache.blocks * a.cache.page;
             const int place = valid ? s % group : 0;
             const bool begins = valid && (place == 0 || before != s - 1);
-            // not the first token of its group here, and not the next one either
-            const bool apart = begins && place > 0 && before >= 0 && before / group == s / group;
+            // in the group of the token before it, whose warp has that group, but not behind it: not
+            // stored, nor what goes on from it (which begins nothing)
+            const bool apart = begins && before >= 0 && before / group == s / group;
             int n = 0;
             if (begins && !apart) {
                 n = 1;
