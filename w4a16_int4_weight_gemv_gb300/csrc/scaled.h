@@ -28,8 +28,8 @@ struct ScaledAppendArgs {
     const float* inv_freq;
     int axis_end[4];  // pairs below axis_end[a] (and not below axis_end[a - 1]) go by axis a
     const int32_t* slots;
-    w4a16_scaled_cache cache;  // heads 0 where there is none
-    int q_heads;
+    w4a16_scaled_cache cache;
+    int q_heads;  // 0 where there are no queries
     int rotary;
     int dim;
     int interleaved;
