@@ -299,10 +299,10 @@ __device__ __forceinline__ Request request_of(const Args<C>& a, int b, bool& bad
     return q;
 }
 
-// Which heads row `row` of a request stands for.  With several new tokens these
-// are (token, query head) pairs, those of the first token first.
+// Which heads row `row` of a request stands for.  With scales by group these are (new
+// token, query head) pairs, those of the first token first.
 struct Heads {
-    int hk, first, n;  // key/value head, first of the query heads that share it, how many
+    int hk, first, n;  // key/value head, first query head (by group: first pair of those that share hk), how many
 };
 template <int C, int HEADS>
 __device__ __forceinline__ Heads heads_of(const Args<C>& a, int row) {
@@ -310,7 +310,7 @@ __device__ __forceinline__ Heads heads_of(const Args<C>& a, int row) {
     Heads h;
     h.hk = row / chunks;
     const int chunk = row - h.hk * chunks;
-    h.first = chunk * HEADS;
+    h.first = chunk * HEADS + (by_group(C) ? 0 : h.hk * G);
     h.n = min(HEADS, G - chunk * HEADS);
     return h;
 }
@@ -320,13 +320,12 @@ struct Column {
 };
 template <int C>
 __device__ __forceinline__ Column column_of(const Args<C>& a, const Heads& hd, int j) {
-    const int G = a.q_heads / a.cache.heads;
     Column c{0, hd.first + j};
     if constexpr (by_group(C)) {
+        const int G = a.q_heads / a.cache.heads;
         c.token = c.head / G;
-        c.head -= c.token * G;
+        c.head += hd.hk * G - c.token * G;
     }
-    c.head += hd.hk * G;
     return c;
 }
 template <int C>
