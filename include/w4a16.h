@@ -663,6 +663,10 @@ typedef struct w4a16_scaled_cache {
  *   however often S grew (max(2^-4 |value|, 2^-10 S) and S / 2 where it did not).
  *   A value that is not finite makes S NaN, and the group stands for NaN until it is
  *   begun anew.  Places behind the new tokens keep their codes.
+ *   S goes by all tokens that were written since the group was begun.  So tokens that
+ *   are taken back, their places then given to others (drafts that are not accepted),
+ *   leave the scale that they asked for, its coarser step or its NaN, to the tokens of
+ *   their group; writing the group from f = 0 on again takes it back too.
  * slots[t] == -1: not stored; a slot outside the cache, or one in the group of the
  * token before that does not follow that token's (the same slot again, an earlier or a
  * later one): not stored, nor are the tokens that go on from it within that group, and

@@ -5,7 +5,7 @@ import torch
 
 from .scaled_slots import stored
 from .test_gpu_paged import freqs, i32, split_qkv, w  # noqa: F401  (w: the fixture)
-from .test_gpu_scaled import E4M3, TYPES, U, attention_problem, check_append, make_cache, raw, same_bits, state_of
+from .test_gpu_scaled import E4M3, TYPES, U, attention_problem, check_append, code_values, make_cache, raw, same_bits, state_of
 
 pytestmark = pytest.mark.gpu
 
@@ -124,3 +124,45 @@ def test_slots_out_of_order_in_calls_of_many_tokens(w, group, T):
         slots[t], slots[t + 1] = spare + group - 1, spare  # a group's last place, then its first (group 1: the same again)
         spare += 16
     check_slots(w, 16, group, 2, 32, slots, spare // 16, T + group, TYPES["int8"])
+
+
+# --------------------------------------------------------------------------
+# append: tokens that are taken back
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_drafts_taken_back_leave_their_scale(w, dtype):
+    gen = torch.Generator().manual_seed(9)
+    cache = make_cache(w, gen, 2, 16, 8, 1, 32, TYPES[dtype])
+    x = torch.randn(16, 2, 32, generator=gen).bfloat16()
+
+    def write(values, at):
+        n = len(values)
+        check_append(w, cache, values.reshape(n, -1), 0, torch.arange(n).int(), freqs(32), None, False, list(range(at, at + n)))
+        return [s[0, :, 0].cpu() for s in (cache.k_scale, cache.v_scale)]
+
+    def off():  # the accepted values, by the header's bound; e4m3: 2^-4 of the value besides
+        have = (code_values(cache.v)[0] * cache.v_scale[0].double().cpu().repeat_interleave(8, 0)[..., None])[:, 0]
+        want, S = x[:, 1].double(), cache.v_scale[0].double().cpu().repeat_interleave(8, 0)
+        return (have - want).abs(), S if dtype == "int8" else 2.0 ** -9 * S + 2.0 ** -4 * want.abs()
+
+    first = write(x[:3], 0)
+    grown = write(64 * x[3:5], 3)  # drafts, 64 times as large
+    assert all(g[0] >= 16 * f[0] for f, g in zip(first, grown))
+    kept = write(x[3:16], 3)  # others take their places, and go on into the next group
+    assert all(k[0] == g[0] for k, g in zip(kept, grown))  # as far as it grew
+    assert all(k[1] <= 4 * f[0] for k, f in zip(kept, first))  # the group that began since then has its own
+    e, bound = off()
+    assert (e <= bound).all()
+    # written from its first place on, the group has a scale of its own tokens again
+    again = write(x[:8], 0)
+    assert all(a[0] < g[0] / 8 and a[1] == k[1] for a, g, k in zip(again, grown, kept))
+    e, bound = off()
+    assert (e <= bound).all()
+    # a draft that is not finite
+    bad = x[5:6].clone()
+    bad[0, :, 7] = float("inf")
+    assert all(s[0].isnan() and not s[1].isnan() for s in write(bad, 5))
+    assert all(s[0].isnan() for s in write(x[5:8], 5))
+    assert all(s[0] == a[0] for s, a in zip(write(x[:8], 0), again))
+    e, bound = off()
+    assert (e <= bound).all()

@@ -958,8 +958,9 @@ def w4a16_scaled_append(q, k, v, positions, inv_freq, slots, cache: ScaledCache,
     group's scale is the smallest power of two whose codes hold its values, and
     grows with them; a request fills its groups in order, and the tokens of one
     group are neighbours in the call, their slots ascending (as w4a16_paged_map
-    gives them).  Returns the rotated queries (q_out, or a new tensor; q_out=q
-    rotates in place)."""
+    gives them).  Tokens that are taken back (drafts) leave the scale as far as it
+    grew until the group is written from its first token on again.  Returns the
+    rotated queries (q_out, or a new tensor; q_out=q rotates in place)."""
     _scaled(cache)
     flags = ROPE_INTERLEAVED if interleaved else 0
     if _fast is not None and (q is None or q_out is not None):
