@@ -324,7 +324,8 @@ __device__ __forceinline__ Column column_of(const Args<C>& a, const Heads& hd, i
     if constexpr (by_group(C)) {
         const int G = a.q_heads / a.cache.heads;
         c.token = c.head / G;
-        c.head += hd.hk * G - c.token * G;
+        c.head -= c.token * G;
+        c.head += hd.hk * G;
     }
     return c;
 }
