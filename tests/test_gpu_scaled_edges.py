@@ -166,3 +166,15 @@ def test_drafts_taken_back_leave_their_scale(w, dtype):
     assert all(s[0] == a[0] for s, a in zip(write(x[:8], 0), again))
     e, bound = off()
     assert (e <= bound).all()
+
+
+def test_an_append_without_keys_values_or_slots_is_refused(w):
+    cache = make_cache(w, torch.Generator().manual_seed(1), 2, 16, 8, 2, 64, TYPES["int8"])
+    before = state_of(cache)
+    x = torch.randn(5, 2, 64, device="cuda").bfloat16()
+    args = dict(q=x, k=x, v=x, positions=i32(range(5)), inv_freq=freqs(64).cuda(), slots=i32(range(5)), cache=cache)
+    for name in ("k", "v", "slots"):
+        for q_out in (None, torch.empty_like(x)):
+            with pytest.raises(TypeError):
+                w.w4a16_scaled_append(**{**args, name: None, "q_out": q_out})
+    assert same_bits(before, state_of(cache)) and w.w4a16_device_error(clear=True) == 0

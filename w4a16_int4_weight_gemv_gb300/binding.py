@@ -970,6 +970,8 @@ def w4a16_scaled_append(q, k, v, positions, inv_freq, slots, cache: ScaledCache,
             return q_out
         if rc is not None:
             raise W4A16Error(rc, "w4a16_scaled_append")
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise TypeError("k must be a torch.Tensor [T, heads, dim]")
     T = k.shape[0]
     shape = (T, cache.heads, cache.dim)
     ka, va, slots_at = _rows(k, "k", shape), _rows(v, "v", shape), _vector(slots, "slots", T)
