@@ -691,7 +691,8 @@ W4A16_API w4a16_status w4a16_scaled_append(const uint16_t* q, int64_t q_token, i
  * code * scale rounded once to out_dtype (W4A16_OUT_BF16 or W4A16_OUT_F32).
  *   k_out, v_out: head h of row r at r * *_row + h * *_head, rows of 16-byte
  *   alignment; rows before row_start[0] and from row_start[B] on are left as they are.
- *   rows: how many the outputs have; tokens past it are not read (W4A16_DEVERR_BLOCKS).
+ *   rows: how many the outputs have; tokens past it are not read (W4A16_DEVERR_BLOCKS; with
+ *   0 nothing is looked at).
  *   block_table as in w4a16_paged_attention; a token past columns * page, before 0 or in a
  *   block outside the cache gives zeros and W4A16_DEVERR_SLOT.
  *   row_start: int32 [B + 1], not descending (as w4a16_paged_map gives it; otherwise rows
@@ -723,7 +724,8 @@ W4A16_API size_t w4a16_scaled_attention_workspace_bytes(int q_heads, int kv_head
  * fp32 scores, maxima and sums; two roundings: of out to bf16, and of the weights w_j =
  * p_j * v_scale_j to fp16 before they multiply the codes c_j.  So, beside fp32's,
  *     |error| <= 2^-8 |out| + 2^-11 sum_j p_j |v_j| + 2^-33 max_j w_j sum_j |c_j|.
- * A key or value that is NaN reaches the new tokens that see it and no others.
+ * A key or value that is NaN reaches the new tokens that see it and no others (a value of
+ * e4m3 code NaN its own dim, or all dims of the head where other new tokens do not see it).
  * The other arguments, the workspace and the limits are those of w4a16_paged_attention,
  * with N * q_heads in the place of q_heads.  Where a request sees a token, codes and scales of
  * up to 31 tokens around it in the same block and head may be read too, and scales of blocks

@@ -27,17 +27,17 @@
 // (tokens) and the heads as its 8 columns: one product covers 8 query heads,
 // and the transposed second product (values^T times p^T) takes the
 // probabilities from the accumulators by one 8x8 transpose in registers.
-// (tcgen05 would want 64 or more query rows; here there are 1 to 16.)
+// (tcgen05 could take 128 tokens as its rows and the heads as its columns; it was not tried.)
 //
 // Measured on one GB300 (copies run at 6.67 TB/s) in a CUDA graph, 32 query
 // heads over 8 of 128 dims: one request of 131072 tokens in bf16 92 us (5.85
-// TB/s), 128 requests of 0 to 8192 tokens over e4m3 125 us (5.82 TB/s; 58 % of
+// TB/s), 128 requests of 0 to 8192 tokens over e4m3 124 us (5.88 TB/s; 58 % of
 // the issue slots, 18 % of the tensor pipe), 16 requests of 0 to 4096 tokens
 // 26 us (15 us of it at the rate of HBM, the rest the two launches), one request
-// of 300 tokens 4.9 us.
-// Registers: all instances but those of 16 heads of 256 dims (24 bytes spilled
-// by the shares over bf16, 104 over e4m3) and 16 of 192 over e4m3 (32) hold what
-// they need.
+// of 300 tokens 5.0 us.
+// Registers: all instances but those of 16 heads of 256 dims (16 bytes spilled by
+// the shares over bf16, 96 over e4m3, 102 in one launch) and 16 of 192 over e4m3 (32,
+// in one launch 12) hold what they need.
 //
 // Scales by group.  A row's columns are (new token, query head) pairs.  With codes c and
 // scales a (keys) and b (values),
@@ -56,16 +56,17 @@
 //   - Up to 32 columns take one row: the codes' conversion and the copies, of which there are
 //     as many for one column as for 32, are what a tile costs.
 // Bound, on a GB300 whose copies run at 6.77 TB/s (32 heads over 8 of 128 dims, int8):
-//   - with one new token by HBM while there is enough to read: 64 requests of 8192 tokens 175
-//     us, 6.1 TB/s; 128 of 0 to 8192 127 us, 5.7 TB/s; 32 of 8192 97 us, over the whole of which
-//     DRAM is 70 % busy, issue 56 %, the ALU pipe 55 %, the tensor pipe 15 %;
+//   - with one new token by HBM while there is enough to read: 64 requests of 8192 tokens 175 to
+//     178 us, 6.1 TB/s; 128 of 0 to 8192 127 us, 5.7 TB/s; 32 of 8192 97 us, over the whole of
+//     which DRAM is 70 % busy, issue 57 %, the ALU pipe 55 %, the tensor pipe 15 %;
 //   - from 16 columns on by what eight warps an SM, all that registers hold, do one after another
-//     (issue 40 to 45 %, tensor pipe 21 to 28 %): 16 requests of 8192 tokens, 268 MB, 58 us with
-//     4 columns, 70 with 16, 91 with 20, 121 with 32;
-//   - below 50 MB by two launches and their dependent reads (16 requests of 1400 tokens 23 us,
-//     7.5 of it at the rate of HBM), or by one (300 tokens 6.7 us in a graph).
-// Registers: the shares spill 346 to 378 bytes in 16 columns of 256 dims, 76 to 98 in 32 of
-// 128, 8 in 16 of 64 over int8, single launches 122 to 130 and 4 in the first two; no others.
+//     (issue 40 to 45 %, tensor pipe 21 to 28 %): 16 requests of 8192 tokens, 268 MB, 56 us with
+//     4 columns, 72 with 16, 91 with 20, 123 with 32, over e4m3 56, 64, 83 and 113;
+//   - below 50 MB by two launches and their dependent reads (16 requests of 0 to 4096 tokens, a
+//     scale a token, 22 us, 7.5 of it at the rate of HBM), or by one (300 tokens 6.7 us in a graph).
+// Registers: the shares spill (over int8, over e4m3) 386 and 326 bytes in 16 columns of 256
+// dims, 90 and 26 in 32 of 128, 8 and none in 32 of 96 and in 16 of 64, single launches 158 and
+// 90, 14 and 4 in the first two; no others.
 #pragma once
 
 #include <algorithm>
@@ -752,7 +753,9 @@ struct RowMath {
                 if (C == kE4m3Groups) {
                     // A weight of 0 does not stop a NaN: codes that no new token sees, which may be
                     // anything, become 0 where they are.  So do NaN codes that some see and others do
-                    // not; the token's weight becomes NaN instead, for those that do.
+                    // not; the token's weight becomes NaN instead, for those that do.  (As numbers in
+                    // the products' loop instead, which has no room for it: 32 columns of 128 dims 118
+                    // us, so 113, 16 of 256 198, so 148; eight requests of 301 tokens 6.8, so 7.0.)
                     const int row = lane & 15, token = first + 16 * p + row;
                     const bool none = !((mask[p] >> row) & 1u);
                     const bool some = !none && edge && a.tokens > 1 && (token >= q.len - (a.tokens - 1) || (a.window > 0 && token < q.len - a.window));
@@ -1310,7 +1313,7 @@ __global__ void __launch_bounds__((AttnShape<C, DP, NT>::kShareWarps * 32), 1)
     }
     // teams: warps one after another have the same share of a request's rows, each of its own row,
     // so that `worker` counts along one row's warps, where that gives every warp kTeamTiles tiles
-    // (16 requests of 1400 tokens, 3 tiles a warp: 24.5 us, without 23.0)
+    // (16 requests of 0 to 4096 tokens, 3 tiles a warp: 24.5 us, without 23.0)
     const int place = blockIdx.x * W + warp;
     const bool teams = may_team && static_cast<int64_t>(total) * rows >= static_cast<int64_t>(kTeamTiles) * jp.warps;
     if (may_team && !teams) {

@@ -19,13 +19,13 @@
 // turned by CTAs of their own in the same launch.
 //
 // Measured on one GB300 (copies run at 6.77 TB/s), 32 query heads over 8 of 128 dims: 17002
-// tokens of ragged prompts 72.7 us, 383 MB at 5.3 TB/s (0.78 of the copy rate); of them keys
+// tokens of ragged prompts 71.9 us, 383 MB at 5.3 TB/s (0.79 of the copy rate); of them keys
 // and values alone 37 us for 209 MB: every run is read, searched, and written by one warp, whose
 // long reads have 24 warps an SM to hide behind (of 10 cycles between a
-// warp's issues 3.2 wait for memory; the issue slots are half busy).  One token 4.0 us (3.7 in a graph): launch, slots and positions,
+// warp's issues 3.2 wait for memory; the issue slots are half busy).  One token 4.2 us (3.8 in a graph): launch, slots and positions,
 // then values, one after another.  Slower for the prompts: chunks of 16 tokens 74.9 us, four
 // CTAs an SM, which spill 306 bytes, 83; CTAs that stay and bring the next chunk to L2 94 to
-// 167; the next run's values in registers 73.  (Three spill 84 to 96 bytes.)
+// 167; the next run's values in registers 73.  (Three spill 84 to 88 bytes.)
 #include <algorithm>
 
 #include "common.cuh"
